@@ -329,6 +329,126 @@ int polar_memory_step(float* state, const void* q, const void* k, const void* v,
                       const float* alpha, const float* beta, void* mem, int B,
                       int H, int T, int d, int dtype, float eps, void* stream);
 
+/*
+ * Decayed linear attention: a memory stream with one decay per head.
+ * (No counterpart on the pages, whose memory channel is the gated-delta rule
+ * of polar_memory_step: this is the plain additive memory without erasure,
+ * whose prompts need not be walked token by token and which trains.)  For
+ * each (b, h), with gamma = exp(log_decay[h]):
+ *   S_t = gamma S_{t-1} + v_t k_t^T        (S maps keys to values: row i is
+ *   mem_t = scale * S_t q_t                 value dimension i)
+ * S_{-1} is state_in, or zero.
+ *   q, k, v, mem : [B, H, T, d] of dtype
+ *   log_decay    : [H] fp32, natural logarithm of the decay per token,
+ *                  expected <= 0 (0: no decay; below -200 reads as -200,
+ *                  whose first power already vanishes in fp32)
+ *   lengths      : [B] int32, device, or NULL (all T): tokens of sequence b
+ *                  in a padded batch, in [0, T].  Tokens past it are not
+ *                  read into any result, whatever they hold.
+ *   state_in     : [B, H, d, d] fp32 or NULL (zero)
+ *   state_out    : [B, H, d, d] fp32 or NULL: S after each sequence's last
+ *                  token (after lengths[b] = 0 tokens: state_in).  May be
+ *                  state_in itself; other overlaps are not allowed.
+ * Rows of mem at or past lengths[b] are written as zeros.  A length outside
+ * [0, T] is clamped and records status 3 in polar_attn_device_status.
+ * polar_linear_fwd takes a prompt by chunks of tokens; polar_linear_step is
+ * the same recurrence for one token, q, k, v, mem [B, H, d], with the state
+ * updated in place.  bf16 prompts run on the tensor cores: the state is
+ * carried in fp32 and rounded to bf16 only as an operand of the product that
+ * reads it; fp32 runs on the FP32 pipes.
+ * workspace: polar_linear_workspace_bytes(B, H, T, d, dtype) bytes, device,
+ * 16-byte aligned; its contents on entry do not affect the results.
+ */
+int polar_linear_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                     const int* lengths, const float* state_in, void* mem, float* state_out,
+                     int B, int H, int T, int d, int dtype, float scale, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int polar_linear_step(float* state, const void* q, const void* k, const void* v,
+                      const float* log_decay, void* mem, int B, int H, int d, int dtype,
+                      float scale, void* stream);
+
+/*
+ * Backward of polar_linear_fwd.  With R_t the gradient of S_t:
+ *   R_t = scale dmem_t q_t^T + gamma R_{t+1},   R_last += dstate_out
+ *   dq_t = scale S_t^T dmem_t,  dk_t = R_t^T v_t,  dv_t = R_t k_t
+ *   dstate_in = gamma R_0
+ *   dmem       : [B, H, T, d] of dtype (rows past lengths[b] are not read
+ *                into any result)
+ *   dstate_out : [B, H, d, d] fp32 or NULL (zero): gradient of state_out
+ *   dq, dk, dv : [B, H, T, d] of dtype (written; rows past lengths[b] zero)
+ *   dstate_in  : [B, H, d, d] fp32 or NULL (may be dstate_out itself)
+ * The other arguments are the forward's.  The decay is a constant of the
+ * layer, as the temperature's and the gate's constants are: it carries no
+ * gradient.  workspace: polar_linear_bwd_workspace_bytes(...) bytes.
+ */
+int polar_linear_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                     const int* lengths, const float* state_in, const void* dmem,
+                     const float* dstate_out, void* dq, void* dk, void* dv, float* dstate_in,
+                     int B, int H, int T, int d, int dtype, float scale, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the two calls above (0 for invalid sizes). */
+size_t polar_linear_workspace_bytes(int B, int H, int T, int d, int dtype);
+size_t polar_linear_bwd_workspace_bytes(int B, int H, int T, int d, int dtype);
+
+/*
+ * polar_attn_decode_paged that also accumulates every cache row's attention
+ * weight (what polar_cache_evict selects by):
+ *   weights : [B, Hkv, weights_stride] fp32, device, weights_stride >=
+ *             max_seq_len: weights[b][hkv][j] += sum of p_j over the query
+ *             heads of the group, for the rows j < seq_lens[b] (p_j: the
+ *             softmax weights of the decode; rows on page indices outside
+ *             the pool get none).  The caller zeroes a row's entry when it
+ *             appends the row.
+ * Other arguments and results as polar_attn_decode_paged; every entry is
+ * added to by one thread, so results do not depend on timing.  workspace: at
+ * least polar_attn_decode_paged_weights_workspace_bytes(...) bytes (the
+ * split records and one fp32 logit per query head and cache row).
+ */
+int polar_attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_pages,
+                                    const int* block_table, const int* seq_lens,
+                                    const void* mem, const float* w_count, void* out,
+                                    float* n_eff, float* conf, float* weights,
+                                    int weights_stride, int B, int Hq, int Hkv, int d,
+                                    int page_size, int num_pages, int max_pages,
+                                    int max_seq_len, int dtype, const polar_consts_t* c,
+                                    int num_splits, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+size_t polar_attn_decode_paged_weights_workspace_bytes(int B, int Hq, int Hkv, int max_seq_len,
+                                                       int d, int num_splits);
+
+/*
+ * Eviction from a paged cache by accumulated attention weight, in place.
+ * (No counterpart on the pages.)  For every sequence with n = seq_lens[b] >
+ * keep rows, each KV head keeps `keep` of its rows: first the rows of its
+ * newest `recent` tokens (position > newest position - recent), then those
+ * of larger weight; equal weights prefer the lower row, NaN counts below
+ * every number.  Kept rows j >= keep move, in ascending order, into the
+ * evicted rows below keep, in ascending order; the other kept rows stay, so
+ * no more rows are copied than must be.  The order of rows does not matter
+ * to the decode.
+ *   k_pages, v_pages, block_table, seq_lens, page_size, num_pages,
+ *   max_pages, max_seq_len : as in polar_attn_decode_paged (a length of 0 is
+ *             allowed).  A page must belong to one sequence of the call.
+ *   weights   : [B, Hkv, stride] fp32, moved with the rows; the entries of
+ *               rows keep .. n - 1 become 0 (ready for appended rows)
+ *   positions : [B, Hkv, stride] int32, the token each row holds, moved with
+ *               the rows (entries past the kept rows are left as they are)
+ *   new_lens  : [B] int32 (written): min(seq_lens[b], keep); may be seq_lens
+ *   keep >= 1, 0 <= recent <= keep, stride >= max_seq_len
+ * Sequences of at most `keep` rows are left untouched.  Pages that hold no
+ * row below new_lens[b] are free afterwards.  A length outside [0,
+ * max_seq_len] is clamped and a page index outside the pool is not touched;
+ * either records status 3 in polar_attn_device_status.
+ * workspace: polar_cache_evict_workspace_bytes(...) bytes, 16-byte aligned.
+ */
+int polar_cache_evict(void* k_pages, void* v_pages, const int* block_table,
+                      const int* seq_lens, float* weights, int* positions, int* new_lens,
+                      int B, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                      int max_seq_len, int stride, int dtype, int keep, int recent,
+                      void* workspace, size_t workspace_bytes, void* stream);
+size_t polar_cache_evict_workspace_bytes(int B, int Hkv, int max_seq_len, int keep);
+
 /* Size of the library-owned device array used by
  * polar_attn_decode_static_scratch (8 MiB per GPU that loads the library). */
 #define POLAR_ATTN_STATIC_SCRATCH_BYTES (8u * 1024u * 1024u)
@@ -375,8 +495,8 @@ const char* polar_attn_strerror(int status);
 /* Kernel-side status of the current device: every wait inside the kernels
  * has a time limit; a kernel whose wait runs out stops early and records a
  * non-zero code here (1 = a pipeline wait timed out, 2 = the self-test wait
- * timed out as intended, 3 = the paged decode met a page index or sequence
- * length outside its bounds).  Synchronises the device.  reset != 0 clears it.
+ * timed out as intended, 3 = a call met a page index or sequence length
+ * outside its bounds).  Synchronises the device.  reset != 0 clears it.
  * Returns the code, or -1 if the device could not be queried. */
 int polar_attn_device_status(int reset);
 

@@ -9,10 +9,14 @@ from .polar import (  # noqa: F401
     bwd_stats,
     bwd_workspace_bytes,
     PolarError,
+    cache_evict,
+    cache_evict_workspace_bytes,
     combine,
     decode,
     decode_paged,
     decode_static_scratch,
+    decode_paged_weights,
+    decode_paged_weights_workspace_bytes,
     decode_paged_workspace_bytes,
     decode_num_splits,
     decode_workspace_bytes,
@@ -23,6 +27,11 @@ from .polar import (  # noqa: F401
     fwd_host_workspace_bytes,
     fwd_stats,
     lib,
+    linear_bwd,
+    linear_bwd_workspace_bytes,
+    linear_fwd,
+    linear_step,
+    linear_workspace_bytes,
     memory_step,
     selftest_wait_timeout,
     strerror,

@@ -35,6 +35,8 @@ void note(const char* what, int code, const char* detail) {
                 detail ? detail : "");
 }
 
+}  // namespace
+
 int cuda_status(const char* what, cudaError_t e) {
   if (e == cudaSuccess) return POLAR_OK;
   note(what, (int)e, cudaGetErrorString(e));
@@ -46,8 +48,6 @@ int* status_word() {
   if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
   return static_cast<int*>(p);
 }
-
-}  // namespace
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -97,9 +97,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 3-D map over a [BH, T, d] bf16 tensor with a {64, rows, 1} box and 128-byte
-// swizzle; out-of-range rows read as zeros.
-bool make_map(CUtensorMap* map, const void* base, int BH, int T, int d, int rows = 128) {
+}  // namespace
+
+bool make_map(CUtensorMap* map, const void* base, int BH, int T, int d, int rows) {
   auto fn = encode_fn();
   if (!fn) {
     note("cudaGetDriverEntryPointByVersion(cuTensorMapEncodeTiled)", -1, "");
@@ -116,6 +116,8 @@ bool make_map(CUtensorMap* map, const void* base, int BH, int T, int d, int rows
   if (r != CUDA_SUCCESS) note("cuTensorMapEncodeTiled", (int)r, "");
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 // 2-D map over a [rows, d] bf16 tensor with a {64, box_rows} box and
 // 128-byte swizzle; rows past the end read as zeros.
@@ -378,12 +380,14 @@ size_t polar_attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int max_s
   return (size_t)B * Hq * s * (d + 4) * sizeof(float);
 }
 
-int polar_attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
-                            const int* block_table, const int* seq_lens, const void* mem,
-                            const float* w_count, void* out, float* n_eff, float* conf, int B,
-                            int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
-                            int max_seq_len, int dtype, const polar_consts_t* c, int num_splits,
-                            void* workspace, size_t workspace_bytes, void* stream) {
+// Both paged calls; weights is null in polar_attn_decode_paged.
+static int decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                        const int* block_table, const int* seq_lens, const void* mem,
+                        const float* w_count, void* out, float* n_eff, float* conf,
+                        float* weights, int weights_stride, int B, int Hq, int Hkv, int d,
+                        int page_size, int num_pages, int max_pages, int max_seq_len, int dtype,
+                        const polar_consts_t* c, int num_splits, void* workspace,
+                        size_t workspace_bytes, void* stream) {
   if (B < 0 || Hq < 1 || Hkv < 1 || num_splits < 0 || num_pages < 1 || max_pages < 1 ||
       max_seq_len < 1)
     return POLAR_ERR_INVALID;
@@ -408,7 +412,9 @@ int polar_attn_decode_paged(const void* q, const void* k_pages, const void* v_pa
   int st = check_device(&sms);
   if (st != POLAR_OK) return st;
   const int splits = num_splits > 0 ? num_splits : auto_splits_paged(B * Hkv, max_seq_len, d, sms);
-  const size_t need = (size_t)B * Hq * splits * (d + 4) * sizeof(float);
+  const size_t records = (size_t)B * Hq * splits * (d + 4) * sizeof(float);
+  const size_t need =
+      records + (weights ? (size_t)B * Hq * max_seq_len * sizeof(float) : (size_t)0);
   if (!workspace || workspace_bytes < need) return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
   int* status = status_word();
@@ -429,6 +435,7 @@ int polar_attn_decode_paged(const void* q, const void* k_pages, const void* v_pa
   a.num_pages = num_pages;
   a.max_pages = max_pages;
   a.status = status;
+  if (weights) a.logits = a.base.partials + records / sizeof(float);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const long long rows = (long long)num_pages * Hkv * page_size;
   if (dtype == POLAR_BF16 && rows < INT_MAX) {
@@ -442,8 +449,51 @@ int polar_attn_decode_paged(const void* q, const void* k_pages, const void* v_pa
     st = cuda_status("paged decode split launch", launch_decode_paged_split(a, dtype, s));
   }
   if (st != POLAR_OK) return st;
-  return cuda_status("paged decode combine launch", launch_decode_combine(a.base, dtype, s));
+  st = cuda_status("paged decode combine launch", launch_decode_combine(a.base, dtype, s));
+  if (st != POLAR_OK || !weights) return st;
+  const WeightsArgs w{a.logits, a.base.partials, seq_lens, weights,     B,
+                      Hq,       Hkv,             d,        splits,      max_seq_len,
+                      weights_stride};
+  return cuda_status("decode weights launch", launch_decode_weights(w, s));
 }
+
+int polar_attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                            const int* block_table, const int* seq_lens, const void* mem,
+                            const float* w_count, void* out, float* n_eff, float* conf, int B,
+                            int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                            int max_seq_len, int dtype, const polar_consts_t* c, int num_splits,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_paged(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, out, n_eff, conf,
+                      nullptr, 0, B, Hq, Hkv, d, page_size, num_pages, max_pages, max_seq_len,
+                      dtype, c, num_splits, workspace, workspace_bytes, stream);
+}
+
+size_t polar_attn_decode_paged_weights_workspace_bytes(int B, int Hq, int Hkv, int max_seq_len,
+                                                       int d, int num_splits) {
+  const size_t records =
+      polar_attn_decode_paged_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits);
+  return records ? records + (size_t)B * Hq * max_seq_len * sizeof(float) : 0;
+}
+
+int polar_attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_pages,
+                                    const int* block_table, const int* seq_lens,
+                                    const void* mem, const float* w_count, void* out,
+                                    float* n_eff, float* conf, float* weights,
+                                    int weights_stride, int B, int Hq, int Hkv, int d,
+                                    int page_size, int num_pages, int max_pages,
+                                    int max_seq_len, int dtype, const polar_consts_t* c,
+                                    int num_splits, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  if (weights_stride < max_seq_len) return POLAR_ERR_INVALID;
+  if (!weights && B > 0) return POLAR_ERR_INVALID;
+  if (B > 0 && Hkv > 0 && (((long long)max_seq_len + 1023) / 1024) * B * Hkv > INT_MAX)
+    return POLAR_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(weights) & 3u) return POLAR_ERR_MISALIGNED;
+  return decode_paged(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, out, n_eff, conf,
+                      weights, weights_stride, B, Hq, Hkv, d, page_size, num_pages, max_pages,
+                      max_seq_len, dtype, c, num_splits, workspace, workspace_bytes, stream);
+}
+
 
 int polar_memory_step(float* state, const void* q, const void* k, const void* v,
                       const float* alpha, const float* beta, void* mem, int B, int H, int T,

@@ -1,0 +1,388 @@
+// Accumulated attention weights of cache rows, and eviction by them.
+//
+// Weights: p_j = exp(s_j - lse) needs the logsumexp over all of a sequence's
+// rows, which is known only after every split has run.  The split kernels
+// therefore store their logits (4 bytes per query head and row beside the
+// 4 d or more bytes of K and V that the row costs), and the kernel here turns
+// them into weights once the split records are there.
+//
+// Eviction: one CTA per (sequence, KV head) finds the keep-th largest
+// (protected, weight, lower row) key by four radix passes over 8 bits, lists
+// the evicted rows below `keep` and the kept rows past it, both ascending,
+// and moves weights and positions; a second kernel copies the K and V rows.
+#include <climits>
+#include <cstdint>
+
+#include "polar_device.cuh"
+#include "polar_internal.h"
+
+namespace polar {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kWThreads = 256;
+constexpr int kWRows = 1024;  // cache rows per CTA
+
+// One CTA per kWRows rows of a (sequence, KV head).
+template <int G>
+__global__ void __launch_bounds__(kWThreads) polar_decode_weights_kernel(const WeightsArgs a) {
+  __shared__ float s_lse[G];
+  const int parts = (a.max_seq_len + kWRows - 1) / kWRows;
+  const int bh = blockIdx.x / parts, b = bh / a.Hkv, hkv = bh % a.Hkv;
+  const int n = min(max(a.seq_lens[b], 0), a.max_seq_len);
+  const int j0 = (int)(blockIdx.x % parts) * kWRows;
+  if (j0 >= n) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t head0 = (size_t)b * a.Hq + (size_t)hkv * G;
+  if (warp < G) {
+    // logsumexp of the head over its splits, log2 units
+    const float* rec = a.partials + (head0 + warp) * a.splits * (a.d + 4);
+    float m = -INFINITY, l = 0.f;
+    for (int s = lane; s < a.splits; s += 32) {
+      const float ms = rec[(size_t)s * (a.d + 4)], ls = rec[(size_t)s * (a.d + 4) + 1];
+      if (ms == -INFINITY) continue;
+      const float mx = fmaxf(m, ms);
+      l = l * expf(m - mx) + ls * expf(ms - mx);
+      m = mx;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m, o);
+      const float lo = __shfl_xor_sync(0xffffffffu, l, o);
+      const float mx = fmaxf(m, mo);
+      if (mx != -INFINITY) {
+        l = l * expf(m - mx) + lo * expf(mo - mx);
+        m = mx;
+      }
+    }
+    if (lane == 0) s_lse[warp] = m == -INFINITY ? INFINITY : m * kLog2e + log2f(l);
+  }
+  __syncthreads();
+  float lse[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) lse[g] = s_lse[g];
+  const float* x = a.logits + head0 * a.max_seq_len;
+  float* w = a.weights + (size_t)bh * a.stride;
+  const int j1 = min(j0 + kWRows, n);
+  for (int j = j0 + threadIdx.x; j < j1; j += kWThreads) {
+    float p = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) p += exp2f(x[(size_t)g * a.max_seq_len + j] - lse[g]);
+    w[j] += p;
+  }
+}
+
+// ------------------------------------------------------------- eviction --
+
+constexpr int kEThreads = 1024;
+constexpr int kEWarps = kEThreads / 32;
+constexpr int kCopies = 8;  // copies of the histogram (fewer collisions)
+
+// Weight -> unsigned order: NaN below everything, -0 equal to 0.
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+struct SelectSmem {
+  uint32_t hist[kCopies][256];
+  uint32_t warp_a[kEWarps], warp_b[kEWarps];
+  uint32_t prefix, need;
+  int newest;
+};
+
+// Exclusive sums over the warps of two per-warp counts (in place).
+__device__ __forceinline__ void scan_warps(SelectSmem& sm) {
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    uint32_t a = sm.warp_a[threadIdx.x], b = sm.warp_b[threadIdx.x];
+    const uint32_t a0 = a, b0 = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t ta = __shfl_up_sync(0xffffffffu, a, o);
+      const uint32_t tb = __shfl_up_sync(0xffffffffu, b, o);
+      if ((int)threadIdx.x >= o) {
+        a += ta;
+        b += tb;
+      }
+    }
+    sm.warp_a[threadIdx.x] = a - a0;
+    sm.warp_b[threadIdx.x] = b - b0;
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const EvictArgs a) {
+  __shared__ SelectSmem sm;
+  const int bh = blockIdx.x, b = bh / a.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int n = a.seq_lens[b];
+  if (n < 0 || n > a.max_seq_len) {
+    if (tid == 0) atomicExch(a.status, 3);
+    n = min(max(n, 0), a.max_seq_len);
+  }
+  if (n <= a.keep) {
+    if (tid == 0) {
+      a.counts[bh] = 0;
+      a.counts[gridDim.x + bh] = n;
+    }
+    return;
+  }
+  float* w = a.weights + (size_t)bh * a.stride;
+  int* pos = a.positions + (size_t)bh * a.stride;
+  if (tid == 0) sm.newest = INT_MIN;
+  __syncthreads();
+  int newest = INT_MIN;
+  for (int j = tid; j < n; j += kEThreads) newest = max(newest, pos[j]);
+  newest = __reduce_max_sync(0xffffffffu, newest);
+  if (lane == 0) atomicMax(&sm.newest, newest);
+  __syncthreads();
+  const long long guard = (long long)sm.newest - a.recent;  // positions above stay
+  auto key_of = [&](int j) -> uint32_t {
+    return pos[j] > guard ? 0xFFFFFFFFu : order_key(w[j]);
+  };
+  // key of the keep-th largest row, 8 bits a pass from the top
+  uint32_t prefix = 0, need = (uint32_t)a.keep;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < kCopies * 256; i += kEThreads) (&sm.hist[0][0])[i] = 0;
+    __syncthreads();
+    for (int j = tid; j < n; j += kEThreads) {
+      const uint32_t key = key_of(j);
+      if (shift == 24 || (key >> (shift + 8)) == prefix)
+        atomicAdd(&sm.hist[warp % kCopies][(key >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // bin that holds the need-th largest, from the top: 8 bins a lane
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = 0;
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) c[i] += sm.hist[k][255 - (lane * 8 + i)];
+        sum += c[i];
+      }
+      uint32_t before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += t;
+      }
+      before -= sum;  // rows in larger bins
+      if (before < need && need <= before + sum) {
+        uint32_t acc = before;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (acc < need && need <= acc + c[i]) {
+            sm.prefix = (prefix << 8) | (uint32_t)(255 - (lane * 8 + i));
+            sm.need = need - acc;
+          }
+          acc += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix = sm.prefix;
+    need = sm.need;
+  }
+  // rows above the threshold stay, and the first `need` equal to it.  Each
+  // warp owns a run of rows: ranks come from ballots and a scan over warps.
+  const int span = (n + kEThreads - 1) / kEThreads * 32;
+  const int w0 = warp * span, w1 = min(w0 + span, n);
+  uint32_t eq = 0;
+  for (int j0 = w0; j0 < w1; j0 += 32) {
+    const int j = j0 + lane;
+    eq += __popc(__ballot_sync(0xffffffffu, j < w1 && key_of(j) == prefix));
+  }
+  if (lane == 0) {
+    sm.warp_a[warp] = eq;
+    sm.warp_b[warp] = 0;
+  }
+  scan_warps(sm);
+  const uint32_t eq0 = sm.warp_a[warp];
+  __syncthreads();
+  const uint32_t below = (1u << lane) - 1u;
+  uint32_t holes = 0, movers = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t rank = eq0;
+    uint32_t hole_at = 0, mover_at = 0;
+    if (pass == 1) {
+      hole_at = sm.warp_a[warp];
+      mover_at = sm.warp_b[warp];
+    }
+    int2* mv = a.moves + (size_t)bh * a.max_moves;
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+      const int j = j0 + lane;
+      const uint32_t key = j < w1 ? key_of(j) : 0u;
+      const bool is_eq = j < w1 && key == prefix;
+      const uint32_t m_eq = __ballot_sync(0xffffffffu, is_eq);
+      const bool kept =
+          j < w1 && (key > prefix || (is_eq && rank + __popc(m_eq & below) < need));
+      rank += __popc(m_eq);
+      const bool hole = j < w1 && !kept && j < a.keep, mover = kept && j >= a.keep;
+      const uint32_t m_h = __ballot_sync(0xffffffffu, hole);
+      const uint32_t m_m = __ballot_sync(0xffffffffu, mover);
+      if (pass == 0) {
+        holes += __popc(m_h);
+        movers += __popc(m_m);
+      } else {
+        if (hole) mv[hole_at + __popc(m_h & below)].y = j;
+        if (mover) mv[mover_at + __popc(m_m & below)].x = j;
+        hole_at += __popc(m_h);
+        mover_at += __popc(m_m);
+      }
+    }
+    if (pass == 0) {
+      if (lane == 0) {
+        sm.warp_a[warp] = holes;
+        sm.warp_b[warp] = movers;
+      }
+      scan_warps(sm);
+      if (warp == kEWarps - 1 && lane == 0) {
+        a.counts[bh] = (int)(sm.warp_a[warp] + holes);
+        a.counts[gridDim.x + bh] = n;
+        sm.need = sm.warp_a[warp] + holes;
+      }
+    }
+  }
+  __syncthreads();
+  const int total = (int)sm.need;
+  const int2* mv = a.moves + (size_t)bh * a.max_moves;
+  for (int i = tid; i < total; i += kEThreads) {
+    const int2 m = mv[i];
+    w[m.y] = w[m.x];
+    pos[m.y] = pos[m.x];
+  }
+  __syncthreads();
+  for (int j = a.keep + tid; j < n; j += kEThreads) w[j] = 0.f;
+}
+
+// Grid (parts, B * Hkv): the listed rows of K and V, 16 bytes a thread.
+__global__ void __launch_bounds__(256) polar_evict_move_kernel(const EvictArgs a) {
+  const int bh = blockIdx.y, b = bh / a.Hkv, h = bh % a.Hkv;
+  const int total = a.counts[bh], n = a.counts[gridDim.y + bh];
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = min(n, a.keep);
+  const int vecs = a.row_bytes >> 4;  // 16-byte pieces of a row
+  const int per = 2 * vecs;           // of a K and a V row
+  const int* table = a.block_table + (size_t)b * a.max_pages;
+  const int2* mv = a.moves + (size_t)bh * a.max_moves;
+  const int page = 1 << a.page_shift;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)total * per;
+       i += (long long)gridDim.x * 256) {
+    const int2 m = mv[i / per];
+    const int piece = (int)(i % per);
+    const int p_from = table[m.x >> a.page_shift], p_to = table[m.y >> a.page_shift];
+    if (p_from < 0 || p_from >= a.num_pages || p_to < 0 || p_to >= a.num_pages) {
+      atomicExch(a.status, 3);
+      continue;
+    }
+    const size_t from = ((size_t)p_from * a.Hkv + h) * page + (m.x & (page - 1));
+    const size_t to = ((size_t)p_to * a.Hkv + h) * page + (m.y & (page - 1));
+    uint8_t* pool = static_cast<uint8_t*>(piece < vecs ? a.k_pages : a.v_pages);
+    const size_t off = (size_t)(piece < vecs ? piece : piece - vecs) * 16;
+    *reinterpret_cast<uint4*>(pool + to * a.row_bytes + off) =
+        *reinterpret_cast<const uint4*>(pool + from * a.row_bytes + off);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_weights(const WeightsArgs& a, cudaStream_t s) {
+  const unsigned grid = (unsigned)((a.max_seq_len + kWRows - 1) / kWRows) * a.B * a.Hkv;
+  switch (a.Hq / a.Hkv) {
+    case 1: polar_decode_weights_kernel<1><<<grid, kWThreads, 0, s>>>(a); break;
+    case 2: polar_decode_weights_kernel<2><<<grid, kWThreads, 0, s>>>(a); break;
+    case 4: polar_decode_weights_kernel<4><<<grid, kWThreads, 0, s>>>(a); break;
+    default: polar_decode_weights_kernel<8><<<grid, kWThreads, 0, s>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
+  const int heads = a.B * a.Hkv;
+  polar_evict_select_kernel<<<heads, kEThreads, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const long long pieces = (long long)a.max_moves * 2 * (a.row_bytes >> 4);
+  long long parts = (pieces + 1023) / 1024;
+  parts = parts < 1 ? 1 : (parts > 64 ? 64 : parts);
+  polar_evict_move_kernel<<<dim3((unsigned)parts, heads), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace polar
+
+using namespace polar;
+
+// Rows one head may have to move: as many as both sides of the cut hold.
+static int evict_max_moves(int max_seq_len, int keep) {
+  const int past = max_seq_len > keep ? max_seq_len - keep : 0;
+  return past < keep ? past : keep;
+}
+
+extern "C" {
+
+size_t polar_cache_evict_workspace_bytes(int B, int Hkv, int max_seq_len, int keep) {
+  if (B < 0 || Hkv < 1 || max_seq_len < 1 || keep < 1 || (long long)B * Hkv > 65535) return 0;
+  const size_t heads = (size_t)B * Hkv;
+  return heads * evict_max_moves(max_seq_len, keep) * sizeof(int2) + heads * 2 * sizeof(int);
+}
+
+int polar_cache_evict(void* k_pages, void* v_pages, const int* block_table,
+                      const int* seq_lens, float* weights, int* positions, int* new_lens,
+                      int B, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                      int max_seq_len, int stride, int dtype, int keep, int recent,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || Hkv < 1 || num_pages < 1 || max_pages < 1 || max_seq_len < 1 || keep < 1 ||
+      recent < 0 || recent > keep || stride < max_seq_len)
+    return POLAR_ERR_INVALID;
+  if (dtype != POLAR_F32 && dtype != POLAR_BF16) return POLAR_ERR_UNSUPPORTED;
+  if ((d != 64 && d != 128) || max_seq_len > (1 << 30) || (long long)B * Hkv > 65535)
+    return POLAR_ERR_UNSUPPORTED;
+  if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+    return POLAR_ERR_UNSUPPORTED;
+  if ((long long)max_pages * page_size < max_seq_len) return POLAR_ERR_INVALID;
+  if (B == 0) return POLAR_OK;
+  if (!k_pages || !v_pages || !block_table || !seq_lens || !weights || !positions || !new_lens)
+    return POLAR_ERR_INVALID;
+  const void* words[] = {block_table, seq_lens, weights, positions, new_lens};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return POLAR_ERR_MISALIGNED;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return POLAR_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < polar_cache_evict_workspace_bytes(B, Hkv, max_seq_len, keep))
+    return POLAR_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
+  int st = check_device(nullptr);
+  if (st != POLAR_OK) return st;
+  int* status = status_word();
+  if (!status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
+  EvictArgs a{};
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.weights = weights;
+  a.positions = positions;
+  a.new_lens = new_lens;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.d = d;
+  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.max_seq_len = max_seq_len;
+  a.stride = stride;
+  a.row_bytes = d * (dtype == POLAR_BF16 ? 2 : 4);
+  a.keep = keep;
+  a.recent = recent;
+  a.max_moves = evict_max_moves(max_seq_len, keep);
+  a.moves = static_cast<int2*>(workspace);
+  a.counts = reinterpret_cast<int*>(a.moves + (size_t)B * Hkv * a.max_moves);
+  a.status = status;
+  return cuda_status("cache eviction launch",
+                     launch_cache_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -372,14 +372,14 @@ struct PagedSmem {
   int abort_flag;
 };
 
-template <int D, typename T, int G>
+template <int D, typename T, int G, bool kLogits>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     polar_decode_paged_split_kernel(const T* __restrict__ q, const T* __restrict__ kp,
                                     const T* __restrict__ vp, const int* __restrict__ table,
                                     const int* __restrict__ lens, float* __restrict__ partials,
                                     int Hq, int Hkv, int max_pages, int num_pages,
                                     int page_shift, int splits, int chunk, polar_consts_t c,
-                                    int* status) {
+                                    int* status, float* __restrict__ logits, int logit_stride) {
   using S = PagedSmem<D, T, G>;
   constexpr int EPL = Elem<T>::kPerVec;  // elements per lane per row
   constexpr int LPK = D / EPL;           // lanes per key row
@@ -565,6 +565,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             }
           }
           const float sc = my_valid ? v[0] : -INFINITY;
+          if constexpr (kLogits) {
+            const int key = key0 + (u0 + my_u) * NG + g;
+            if (key < k1 && key < logit_stride)
+              logits[((size_t)b * Hq + hkv * G + my_g) * logit_stride + key] = sc;
+          }
           float bm = sc;
 #pragma unroll
           for (int o = 1; o < UB; o <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
@@ -646,6 +651,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 #pragma unroll
               for (int o = LPK / 2; o > 0; o >>= 1) d0 += __shfl_xor_sync(0xffffffffu, d0, o);
               sc[gi][u] = valid ? d0 : -INFINITY;
+              if constexpr (kLogits) {
+                if (sub == 0 && key0 + kk < k1 && key0 + kk < logit_stride)
+                  logits[((size_t)b * Hq + hkv * G + gi) * logit_stride + key0 + kk] = sc[gi][u];
+              }
             }
           }
 #pragma unroll
@@ -754,20 +763,25 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   }
 }
 
-template <int D, typename T, int G>
-cudaError_t paged_split_d(const PagedArgs& a, cudaStream_t s) {
+template <int D, typename T, int G, bool kLogits>
+cudaError_t paged_split_l(const PagedArgs& a, cudaStream_t s) {
   using S = PagedSmem<D, T, G>;
   const DecodeArgs& d = a.base;
   const int smem = (int)sizeof(S);
-  cudaError_t e = cudaFuncSetAttribute(polar_decode_paged_split_kernel<D, T, G>,
+  cudaError_t e = cudaFuncSetAttribute(polar_decode_paged_split_kernel<D, T, G, kLogits>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   dim3 grid(d.B * a.Hkv, d.splits);
-  polar_decode_paged_split_kernel<D, T, G><<<grid, kPagedThreads, smem, s>>>(
+  polar_decode_paged_split_kernel<D, T, G, kLogits><<<grid, kPagedThreads, smem, s>>>(
       static_cast<const T*>(d.q), static_cast<const T*>(a.k_pages),
       static_cast<const T*>(a.v_pages), a.block_table, d.seq_lens, d.partials, d.H, a.Hkv,
-      a.max_pages, a.num_pages, a.page_shift, d.splits, d.chunk, d.c, a.status);
+      a.max_pages, a.num_pages, a.page_shift, d.splits, d.chunk, d.c, a.status, a.logits, d.Tkv);
   return cudaGetLastError();
+}
+
+template <int D, typename T, int G>
+cudaError_t paged_split_d(const PagedArgs& a, cudaStream_t s) {
+  return a.logits ? paged_split_l<D, T, G, true>(a, s) : paged_split_l<D, T, G, false>(a, s);
 }
 
 template <int D, typename T>

@@ -162,9 +162,11 @@ struct PagedTcParams {
   int splits, chunk;
   polar_consts_t c;
   int* status;
+  float* logits;  // kLogits: [B, Hq, logit_stride], every row's logit (log2 units)
+  int logit_stride;
 };
 
-template <int D, int G>
+template <int D, int G, bool kLogits>
 __global__ void __launch_bounds__(kPThreads, 2)
     polar_decode_paged_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                                  const __grid_constant__ CUtensorMap map_v,
@@ -431,6 +433,14 @@ __global__ void __launch_bounds__(kPThreads, 2)
         x[g] = valid ? __uint_as_float(r[g]) * scale2 : -INFINITY;
         up = up || x[g] > m_ref[g] + kPRescale;
       }
+      if constexpr (kLogits) {
+        // consecutive threads hold consecutive keys: coalesced per head
+        if (w && mine && key < k1 && key < p.logit_stride) {
+          float* lg = p.logits + ((size_t)b * p.Hq + (size_t)hkv * G) * p.logit_stride + key;
+#pragma unroll
+          for (int g = 0; g < G; ++g) lg[(size_t)g * p.logit_stride] = x[g];
+        }
+      }
       const bool wup = __any_sync(0xffffffffu, up);
       if (lane == 0) ms.up[j & 1][warp] = wup ? 1u : 0u;
       if (!softmax_bar_and(w)) {
@@ -567,8 +577,8 @@ __global__ void __launch_bounds__(kPThreads, 2)
   }
 }
 
-template <int D, int G>
-cudaError_t paged_tc_d(const PagedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+template <int D, int G, bool kLogits>
+cudaError_t paged_tc_l(const PagedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
                        cudaStream_t s) {
   using L = PLayout<D>;
   PagedTcParams p;
@@ -588,13 +598,21 @@ cudaError_t paged_tc_d(const PagedArgs& a, const CUtensorMap& mk, const CUtensor
   p.chunk = a.base.chunk;
   p.c = a.base.c;
   p.status = a.status;
-  cudaError_t e = cudaFuncSetAttribute(polar_decode_paged_tc_kernel<D, G>,
+  p.logits = a.logits;
+  p.logit_stride = a.base.Tkv;
+  cudaError_t e = cudaFuncSetAttribute(polar_decode_paged_tc_kernel<D, G, kLogits>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kSmemBytes);
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)(a.base.B * a.Hkv), (unsigned)a.base.splits);
-  polar_decode_paged_tc_kernel<D, G><<<grid, kPThreads, L::kSmemBytes, s>>>(mk, mv, p);
+  polar_decode_paged_tc_kernel<D, G, kLogits><<<grid, kPThreads, L::kSmemBytes, s>>>(mk, mv, p);
   return cudaGetLastError();
+}
+
+template <int D, int G>
+cudaError_t paged_tc_d(const PagedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                       cudaStream_t s) {
+  return a.logits ? paged_tc_l<D, G, true>(a, mk, mv, s) : paged_tc_l<D, G, false>(a, mk, mv, s);
 }
 
 template <int D>

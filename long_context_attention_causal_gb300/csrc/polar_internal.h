@@ -48,7 +48,83 @@ struct PagedArgs {
   const int* block_table;         // [B, max_pages]
   int Hkv, page_shift, num_pages, max_pages;
   int* status;
+  float* logits = nullptr;  // optional [B, Hq, Tkv]: every row's logit, log2 units
 };
+
+// weights[b][hkv][j] += sum over the group's heads of exp2(logit) / l, from the
+// logits and the split records that a paged split kernel wrote.
+struct WeightsArgs {
+  const float *logits, *partials;
+  const int* seq_lens;
+  float* weights;
+  int B, Hq, Hkv, d, splits, max_seq_len, stride;
+};
+
+struct EvictArgs {
+  void *k_pages, *v_pages;
+  const int *block_table, *seq_lens;
+  float* weights;
+  int *positions, *new_lens;
+  int B, Hkv, d, page_shift, num_pages, max_pages, max_seq_len, stride, row_bytes;
+  int keep, recent;
+  int* counts;   // [B * Hkv] rows to move, then [B * Hkv] lengths
+  int2* moves;   // [B * Hkv][max_moves] (from, to)
+  int max_moves;
+  int* status;
+};
+
+// One application of the decayed linear recurrence over all (b, h):
+//   forward: out_t = s * (sum_{u <= t} g^(t-u) (x_t . y_u) z_u + g^(t+1) M x_t)
+//   reverse: out_t = s * sum_{u >= t} g^(u-t) (x_t . y_u) z_u + g^(L-1-t) M x_t
+// with M the state at the sequence's start (forward) or end (reverse).  The
+// stored state is [z dim][y dim], transposed if state_t.
+struct LinearArgs {
+  const void *x, *y, *z;  // [B, H, T, d]
+  void* out;              // [B, H, T, d]
+  const float* log_decay;
+  const int* lengths;     // may be null
+  int B, H, T, d;
+  float scale;
+  bool reverse, state_t;
+  int nseg, seg_tokens;   // segments of whole tiles of kLinearTile tokens
+  const float* init;      // state at the start, or null (zero)
+  const float* seg_states;  // [BH][nseg][d][d] state before each segment, or null: one
+                            // segment that starts from init
+  int* status;
+};
+constexpr int kLinearTile = 128;
+
+// State of each segment alone, then (scan) the states before each segment in
+// place and the final state.
+struct LinearStateArgs {
+  const void *y, *z;
+  const float* log_decay;
+  const int* lengths;
+  int B, H, T, d;
+  float scale;  // factor of the state's products
+  bool reverse;
+  int nseg, seg_tokens;
+  const float* init;   // may be null
+  float* seg_states;   // [BH][nseg][d][d]
+  float* final_state;  // may be null
+  int* status;
+};
+cudaError_t launch_linear_states(const LinearStateArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s);
+cudaError_t launch_linear_out(const LinearArgs& a, int dtype, cudaStream_t s);
+
+struct LinearStepArgs {
+  float* state;
+  const void *q, *k, *v;
+  const float* log_decay;
+  void* mem;
+  int B, H, d;
+  float scale;
+};
+cudaError_t launch_linear_step(const LinearStepArgs& a, int dtype, cudaStream_t s);
+
+cudaError_t launch_decode_weights(const WeightsArgs& a, cudaStream_t s);
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 
 struct MemoryArgs {
   float* state;                   // [B, H, d, d] fp32, updated in place
@@ -136,6 +212,11 @@ int check_device(int* num_sms);
 int auto_splits(int BH, int Tkv, int num_sms);
 bool decode_sizes_ok(int B, int H, int Tkv, int d);
 void set_last_error(const char* msg);
+int cuda_status(const char* what, cudaError_t e);
+int* status_word();  // device address of the current device's status word, or null
+// 3-D map over a [BH, T, d] bf16 tensor with a {64, rows, 1} box and 128-byte
+// swizzle; out-of-range rows read as zeros.
+bool make_map(CUtensorMap* map, const void* base, int BH, int T, int d, int rows = 128);
 
 // Bounded-wait self test (one thread, a barrier nothing completes).
 cudaError_t launch_selftest_wait(long long limit_cycles, int* status, cudaStream_t s);

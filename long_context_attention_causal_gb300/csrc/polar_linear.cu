@@ -1,0 +1,441 @@
+// Decayed linear attention on the FP32 pipes: the single-token step, the
+// segment states, their scan, and the chunked outputs for fp32 tensors.
+//
+// Per head, S_t = g S_{t-1} + v_t k_t^T and mem_t = c S_t q_t.  Over a chunk
+// of tokens with local index i and the state M before it,
+//   mem_i = c [ sum_{j <= i} g^(i-j) (q_i . k_j) v_j + g^(i+1) M q_i ]
+//   M'    = g^n M + sum_j g^(n-1-j) v_j k_j^T            (n tokens)
+// Every power of g has an exponent >= 0, so nothing overflows for g <= 1.
+// The gradients are the same sums: dq is the forward over (dmem, v, k) with
+// the state transposed; dk and dv run from the last token over (v, dmem, q)
+// and (k, q, dmem).  The kernels therefore take three tensors x, y, z
+// (out_t sums (x_t . y_u) z_u) and a direction.  From the end, with M the
+// gradient of the state after the chunk,
+//   out_i = c sum_{j >= i} g^(j-i) (x_i . y_j) z_j + g^(n-1-i) M x_i
+//   M'    = g^n M + c sum_j g^(j+1) z_j y_j^T
+//
+// A sequence is cut into segments of whole 128-token tiles, so that few
+// heads still fill the GPU: one kernel sums each segment's state alone, a
+// scan turns them into the states before each segment, and the output kernel
+// walks the segments in parallel.
+#include "polar_device.cuh"
+#include "polar_internal.h"
+#include "polar_linear.cuh"
+
+namespace polar {
+
+namespace {
+
+constexpr int kC = 64;        // tokens per chunk
+constexpr int kZ = 32;        // z columns (rows of the state) per CTA
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store2(float* p, float a, float b) {
+  *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+// Rows [t0, t0 + kC) x D of a tensor into shared memory (row stride D + 4),
+// zeros from token `end` on: what lies past a sequence may be anything.
+template <int D, typename T>
+__device__ __forceinline__ void load_rows(float (*dst)[D + 4], const T* src, int t0, int end) {
+  constexpr int kV = D / 4;
+  for (int i = threadIdx.x; i < kC * kV; i += kThreads) {
+    const int r = i / kV, c = (i % kV) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t0 + r < end) x = load4<T>(src + (size_t)(t0 + r) * D + c);
+    *reinterpret_cast<float4*>(&dst[r][c]) = x;
+  }
+}
+
+// Columns [z0, z0 + kZ) of the same rows.
+template <int D, typename T>
+__device__ __forceinline__ void load_cols(float (*dst)[kZ], const T* src, int t0, int end,
+                                          int z0) {
+  constexpr int kV = kZ / 4;
+  for (int i = threadIdx.x; i < kC * kV; i += kThreads) {
+    const int r = i / kV, c = (i % kV) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t0 + r < end) x = load4<T>(src + (size_t)(t0 + r) * D + z0 + c);
+    *reinterpret_cast<float4*>(&dst[r][c]) = x;
+  }
+}
+
+// The thread's share of a 32 x D state: rows r0 .. r0 + kR - 1, four columns.
+template <int D>
+struct StateTile {
+  static constexpr int kLanes = D / 4;
+  static constexpr int kR = kZ * kLanes / kThreads;
+  static __device__ __forceinline__ int row0() { return (int)(threadIdx.x / kLanes) * kR; }
+  static __device__ __forceinline__ int col0() { return (int)(threadIdx.x % kLanes) * 4; }
+};
+
+// acc += sum_j w_j z_j y_j^T over the rows of a chunk (zw holds w_j z_j).
+template <int D>
+__device__ __forceinline__ void state_products(float4 (&acc)[StateTile<D>::kR],
+                                               const float (*y)[D + 4], const float (*zw)[kZ]) {
+  using S = StateTile<D>;
+  const int r0 = S::row0(), c0 = S::col0();
+#pragma unroll 4
+  for (int j = 0; j < kC; ++j) {
+    const float4 yv = *reinterpret_cast<const float4*>(&y[j][c0]);
+#pragma unroll
+    for (int r = 0; r < S::kR; ++r) {
+      const float zv = zw[j][r0 + r];
+      acc[r].x = fmaf(zv, yv.x, acc[r].x);
+      acc[r].y = fmaf(zv, yv.y, acc[r].y);
+      acc[r].z = fmaf(zv, yv.z, acc[r].z);
+      acc[r].w = fmaf(zv, yv.w, acc[r].w);
+    }
+  }
+}
+
+// ------------------------------------------------------ segment states --
+
+template <int D>
+struct StateSmem {
+  float y[kC][D + 4];
+  float zw[kC][kZ];
+};
+
+// Grid (BH * nseg, D / kZ).  Weights are taken from the segment's end, so the
+// accumulators never need rescaling.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads)
+    polar_linear_state_kernel(const LinearStateArgs a) {
+  using S = StateTile<D>;
+  __shared__ __align__(16) StateSmem<D> sm;
+  const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
+  const int z0 = blockIdx.y * kZ;
+  const int len = linear_length(a.lengths, bh / a.H, a.T, a.status);
+  const int t0 = seg * a.seg_tokens, t1 = min(t0 + a.seg_tokens, len);
+  const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
+  const T* y = static_cast<const T*>(a.y) + (size_t)bh * a.T * D;
+  const T* z = static_cast<const T*>(a.z) + (size_t)bh * a.T * D;
+  float4 acc[S::kR];
+#pragma unroll
+  for (int r = 0; r < S::kR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = t0; c0 < t1; c0 += kC) {
+    __syncthreads();
+    load_rows<D, T>(sm.y, y, c0, t1);
+    for (int i = threadIdx.x; i < kC * (kZ / 4); i += kThreads) {
+      const int r = i / (kZ / 4), c = (i % (kZ / 4)) * 4, t = c0 + r;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < t1) {
+        v = load4<T>(z + (size_t)t * D + z0 + c);
+        const float w = a.reverse ? a.scale * linear_power(l2, t - t0 + 1)
+                                  : a.scale * linear_power(l2, t1 - 1 - t);
+        v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+      }
+      *reinterpret_cast<float4*>(&sm.zw[r][c]) = v;
+    }
+    __syncthreads();
+    state_products<D>(acc, sm.y, sm.zw);
+  }
+  float* dst = a.seg_states + ((size_t)blockIdx.x * D + z0) * D;
+#pragma unroll
+  for (int r = 0; r < S::kR; ++r)
+    *reinterpret_cast<float4*>(dst + (size_t)(S::row0() + r) * D + S::col0()) = acc[r];
+}
+
+// Grid (BH, d * d / 256): one state element per thread through the segments
+// in order; the segment's own sum is replaced by the state before it.
+__global__ void __launch_bounds__(256) polar_linear_scan_kernel(const LinearStateArgs a) {
+  const int bh = blockIdx.x, dd = a.d * a.d;
+  const int e = blockIdx.y * 256 + threadIdx.x;
+  const int len = linear_length(a.lengths, bh / a.H, a.T, nullptr);
+  const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
+  float m = a.init ? a.init[(size_t)bh * dd + e] : 0.f;
+  float* seg = a.seg_states + (size_t)bh * a.nseg * dd + e;
+  const float whole = linear_power(l2, a.seg_tokens);
+  constexpr int kU = 8;
+  for (int s0 = 0; s0 < a.nseg; s0 += kU) {
+    float own[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int s = a.reverse ? a.nseg - 1 - (s0 + u) : s0 + u;
+      own[u] = s0 + u < a.nseg ? seg[(size_t)s * dd] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (s0 + u >= a.nseg) break;
+      const int s = a.reverse ? a.nseg - 1 - (s0 + u) : s0 + u;
+      const int n = min(max(len - s * a.seg_tokens, 0), a.seg_tokens);
+      seg[(size_t)s * dd] = m;
+      const float g = n == a.seg_tokens ? whole : linear_power(l2, n);
+      m = fmaf(g, m, own[u]);
+    }
+  }
+  if (a.final_state) a.final_state[(size_t)bh * dd + e] = m;
+}
+
+// -------------------------------------------------------------- outputs --
+
+template <int D>
+struct OutSmem {
+  float x[kC][D + 4];
+  float y[kC][D + 4];
+  float m[kZ][D + 4];  // rows z0 .. of the state
+  float z[kC][kZ];
+  float zw[kC][kZ];
+  float p[kC][kC + 4];  // decayed scores
+  float pw[kC + 1];     // powers of g
+};
+
+// Grid (BH * nseg, D / kZ): the CTA walks its segment's chunks with its 32
+// rows of the state in shared memory.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads)
+    polar_linear_out_kernel(const LinearArgs a) {
+  using S = StateTile<D>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  OutSmem<D>& sm = *reinterpret_cast<OutSmem<D>*>(smem_raw);
+  const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
+  const int z0 = blockIdx.y * kZ, tid = threadIdx.x;
+  const int len = linear_length(a.lengths, bh / a.H, a.T, a.status);
+  const int t0 = seg * a.seg_tokens, t1 = min(t0 + a.seg_tokens, a.T);
+  const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
+  const T* x = static_cast<const T*>(a.x) + (size_t)bh * a.T * D;
+  const T* y = static_cast<const T*>(a.y) + (size_t)bh * a.T * D;
+  const T* z = static_cast<const T*>(a.z) + (size_t)bh * a.T * D;
+  T* out = static_cast<T*>(a.out) + (size_t)bh * a.T * D;
+
+  const float* st = a.seg_states ? a.seg_states + (size_t)blockIdx.x * D * D
+                                 : (a.init ? a.init + (size_t)bh * D * D : nullptr);
+  for (int i = tid; i < kZ * D; i += kThreads) {
+    const int r = a.state_t ? i % kZ : i / D, c = a.state_t ? i / kZ : i % D;
+    float v = 0.f;
+    if (st) v = a.state_t ? st[(size_t)c * D + z0 + r] : st[(size_t)(z0 + r) * D + c];
+    sm.m[r][c] = v;
+  }
+  for (int i = tid; i <= kC; i += kThreads) sm.pw[i] = linear_power(l2, i);
+  // forward: the output scale applies to the state's part too; reverse: the
+  // state already carries it
+  const float s_in = a.reverse ? 1.f : a.scale, s_z = a.reverse ? a.scale : 1.f;
+  const int tx = tid & 15, ty = tid >> 4;
+  const int n_ch = (t1 - t0 + kC - 1) / kC;
+  for (int ci = 0; ci < n_ch; ++ci) {
+    const int c0 = t0 + (a.reverse ? n_ch - 1 - ci : ci) * kC;
+    const int n = min(max(len - c0, 0), min(kC, t1 - c0));  // tokens of the chunk
+    __syncthreads();
+    if (n > 0) {
+      load_rows<D, T>(sm.x, x, c0, c0 + n);
+      load_rows<D, T>(sm.y, y, c0, c0 + n);
+      load_cols<D, T>(sm.z, z, c0, c0 + n, z0);
+    }
+    __syncthreads();
+    float o[4][2];
+#pragma unroll
+    for (int ii = 0; ii < 4; ++ii) o[ii][0] = o[ii][1] = 0.f;
+    if (n > 0) {
+      // scores: rows 4 ty .., keys tx + 16 jj
+      float sc[4][4];
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = 0.f;
+#pragma unroll 2
+      for (int k = 0; k < D; k += 4) {
+        float4 xv[4], yv[4];
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii)
+          xv[ii] = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+          yv[jj] = *reinterpret_cast<const float4*>(&sm.y[tx + 16 * jj][k]);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = dot4(xv[ii], yv[jj], sc[ii][jj]);
+      }
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const int i = 4 * ty + ii, j = tx + 16 * jj;
+          const int dist = a.reverse ? j - i : i - j;
+          sm.p[i][j] = dist >= 0 ? sc[ii][jj] * sm.pw[dist] : 0.f;
+        }
+      for (int i = tid; i < kC * kZ; i += kThreads) {
+        const int r = i / kZ;
+        const float w = r < n ? s_z * sm.pw[a.reverse ? r + 1 : n - 1 - r] : 0.f;
+        sm.zw[r][i % kZ] = sm.z[r][i % kZ] * w;
+      }
+      __syncthreads();
+      // the state's part: rows 4 ty .., state rows 2 tx, 2 tx + 1
+#pragma unroll 2
+      for (int k = 0; k < D; k += 4) {
+        const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[2 * tx][k]);
+        const float4 m1 = *reinterpret_cast<const float4*>(&sm.m[2 * tx + 1][k]);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const float4 xv = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
+          o[ii][0] = dot4(xv, m0, o[ii][0]);
+          o[ii][1] = dot4(xv, m1, o[ii][1]);
+        }
+      }
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        const int i = 4 * ty + ii;
+        const float w = i < n ? s_in * sm.pw[a.reverse ? n - 1 - i : i + 1] : 0.f;
+        o[ii][0] *= w;
+        o[ii][1] *= w;
+      }
+      // the chunk's own part
+      float q[4][2];
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) q[ii][0] = q[ii][1] = 0.f;
+#pragma unroll 2
+      for (int j = 0; j < kC; j += 4) {
+        float2 zv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          zv[e] = *reinterpret_cast<const float2*>(&sm.z[j + e][2 * tx]);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const float4 pv = *reinterpret_cast<const float4*>(&sm.p[4 * ty + ii][j]);
+          q[ii][0] = dot4(pv, make_float4(zv[0].x, zv[1].x, zv[2].x, zv[3].x), q[ii][0]);
+          q[ii][1] = dot4(pv, make_float4(zv[0].y, zv[1].y, zv[2].y, zv[3].y), q[ii][1]);
+        }
+      }
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        o[ii][0] = fmaf(a.scale, q[ii][0], o[ii][0]);
+        o[ii][1] = fmaf(a.scale, q[ii][1], o[ii][1]);
+      }
+    }
+#pragma unroll
+    for (int ii = 0; ii < 4; ++ii) {
+      const int i = 4 * ty + ii;
+      if (c0 + i < t1)
+        store2(out + (size_t)(c0 + i) * D + z0 + 2 * tx, i < n ? o[ii][0] : 0.f,
+               i < n ? o[ii][1] : 0.f);
+    }
+    if (n > 0 && ci + 1 < n_ch) {
+      __syncthreads();  // every read of the state is done
+      float4 acc[S::kR];
+      const float g = sm.pw[n];
+#pragma unroll
+      for (int r = 0; r < S::kR; ++r) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.m[S::row0() + r][S::col0()]);
+        acc[r] = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
+      }
+      state_products<D>(acc, sm.y, sm.zw);
+#pragma unroll
+      for (int r = 0; r < S::kR; ++r)
+        *reinterpret_cast<float4*>(&sm.m[S::row0() + r][S::col0()]) = acc[r];
+    }
+  }
+}
+
+// ----------------------------------------------------------------- step --
+
+constexpr int kStepRows = 8;   // state rows per warp
+constexpr int kStepWarps = 4;
+
+// One token: the state is read and written once, which is all of the time.
+// Rows are independent, so a head's rows are spread over d / 32 CTAs: the
+// smallest calls then use several SMs a head.
+template <int D, typename T>
+__global__ void __launch_bounds__(kStepWarps * 32)
+    polar_linear_step_kernel(const LinearStepArgs a) {
+  constexpr int kL = D / 4;      // lanes per row
+  constexpr int kRW = 32 / kL;   // rows a warp holds at once
+  constexpr int kN = kStepRows / kRW;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t bh = blockIdx.x / (D / (kStepRows * kStepWarps));
+  const int part = blockIdx.x % (D / (kStepRows * kStepWarps));
+  const int row0 = (part * kStepWarps + warp) * kStepRows + lane / kL, c0 = (lane % kL) * 4;
+  float* S = a.state + bh * D * D;
+  float4 s[kN];
+#pragma unroll
+  for (int r = 0; r < kN; ++r)
+    s[r] = *reinterpret_cast<const float4*>(S + (size_t)(row0 + r * kRW) * D + c0);
+  const float4 k = load4<T>(static_cast<const T*>(a.k) + bh * D + c0);
+  const float4 q = load4<T>(static_cast<const T*>(a.q) + bh * D + c0);
+  const float g = linear_power(linear_log2_decay(a.log_decay, (int)(bh % a.H)), 1);
+  const T* v = static_cast<const T*>(a.v) + bh * D;
+  T* mem = static_cast<T*>(a.mem) + bh * D;
+#pragma unroll
+  for (int r = 0; r < kN; ++r) {
+    const int row = row0 + r * kRW;
+    const float vr = linear_load(v + row);
+    s[r].x = fmaf(g, s[r].x, vr * k.x);
+    s[r].y = fmaf(g, s[r].y, vr * k.y);
+    s[r].z = fmaf(g, s[r].z, vr * k.z);
+    s[r].w = fmaf(g, s[r].w, vr * k.w);
+    *reinterpret_cast<float4*>(S + (size_t)row * D + c0) = s[r];
+    float o = dot4(s[r], q, 0.f);
+#pragma unroll
+    for (int w = kL / 2; w > 0; w >>= 1) o += __shfl_xor_sync(0xffffffffu, o, w);
+    if (lane % kL == 0) linear_store(mem + row, a.scale * o);
+  }
+}
+
+template <int D, typename T>
+cudaError_t step_d(const LinearStepArgs& a, cudaStream_t s) {
+  polar_linear_step_kernel<D, T>
+      <<<(unsigned)a.B * a.H * (D / (kStepRows * kStepWarps)), kStepWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, typename T>
+cudaError_t states_d(const LinearStateArgs& a, cudaStream_t s) {
+  polar_linear_state_kernel<D, T><<<dim3((unsigned)a.B * a.H * a.nseg, D / kZ), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D, typename T>
+cudaError_t out_d(const LinearArgs& a, cudaStream_t s) {
+  const int smem = (int)sizeof(OutSmem<D>);
+  cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D, T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  polar_linear_out_kernel<D, T>
+      <<<dim3((unsigned)a.B * a.H * a.nseg, D / kZ), kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_states(const LinearStateArgs& a, int dtype, cudaStream_t s) {
+  if (dtype == POLAR_BF16)
+    return a.d == 64 ? states_d<64, __nv_bfloat16>(a, s) : states_d<128, __nv_bfloat16>(a, s);
+  return a.d == 64 ? states_d<64, float>(a, s) : states_d<128, float>(a, s);
+}
+
+cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s) {
+  polar_linear_scan_kernel<<<dim3((unsigned)a.B * a.H, a.d * a.d / 256), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_out(const LinearArgs& a, int dtype, cudaStream_t s) {
+  if (dtype == POLAR_BF16)
+    return a.d == 64 ? out_d<64, __nv_bfloat16>(a, s) : out_d<128, __nv_bfloat16>(a, s);
+  return a.d == 64 ? out_d<64, float>(a, s) : out_d<128, float>(a, s);
+}
+
+cudaError_t launch_linear_step(const LinearStepArgs& a, int dtype, cudaStream_t s) {
+  if (dtype == POLAR_BF16)
+    return a.d == 64 ? step_d<64, __nv_bfloat16>(a, s) : step_d<128, __nv_bfloat16>(a, s);
+  return a.d == 64 ? step_d<64, float>(a, s) : step_d<128, float>(a, s);
+}
+
+}  // namespace polar

@@ -1,0 +1,38 @@
+// Device helpers of the decayed linear attention kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace polar {
+
+// Tokens of sequence b: lengths[b] clamped to [0, T] (all T without lengths);
+// a length outside records status 3.
+__device__ __forceinline__ int linear_length(const int* lengths, int b, int T, int* status) {
+  if (!lengths) return T;
+  const int n = lengths[b];
+  if ((n < 0 || n > T) && status && threadIdx.x == 0) atomicExch(status, 3);
+  return min(max(n, 0), T);
+}
+
+// log2 of a head's decay.  Below -200 the first power is 0 in fp32 already;
+// the clamp keeps -inf * 0 = NaN out of the zeroth power.  NaN passes.
+__device__ __forceinline__ float linear_log2_decay(const float* log_decay, int h) {
+  const float x = log_decay[h];
+  return (x < -200.f ? -200.f : x) * 1.4426950408889634f;
+}
+
+// g^n for n >= 0.  The product's rounding moves the result by 2^-24 |n l2|
+// relative: a power that still weighs (above 2^-24) is right to 1e-6.
+__device__ __forceinline__ float linear_power(float l2, int n) { return exp2f(l2 * (float)n); }
+
+__device__ __forceinline__ float linear_load(const float* p) { return *p; }
+__device__ __forceinline__ float linear_load(const __nv_bfloat16* p) {
+  return __bfloat162float(*p);
+}
+__device__ __forceinline__ void linear_store(float* p, float x) { *p = x; }
+__device__ __forceinline__ void linear_store(__nv_bfloat16* p, float x) {
+  *p = __float2bfloat16_rn(x);
+}
+
+}  // namespace polar

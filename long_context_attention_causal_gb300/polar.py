@@ -104,12 +104,32 @@ def lib() -> ctypes.CDLL:
             L.polar_attn_fwd_host.restype = ci
             L.polar_attn_fwd_host_workspace_bytes.argtypes = [ci, ci, ci, ci, ci]
             L.polar_attn_fwd_host_workspace_bytes.restype = cs
+            cf = ctypes.c_float
+            L.polar_linear_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci,
+                                           cf, vp, cs, vp]
+            L.polar_linear_step.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, cf, vp]
+            L.polar_linear_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci,
+                                           ci, ci, ci, ci, cf, vp, cs, vp]
+            for f in ("polar_linear_workspace_bytes", "polar_linear_bwd_workspace_bytes"):
+                getattr(L, f).argtypes = [ci, ci, ci, ci, ci]
+                getattr(L, f).restype = cs
+            L.polar_attn_decode_paged_weights.argtypes = [
+                vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, ci, ci,
+                ci, cp, ci, vp, cs, vp]
+            L.polar_attn_decode_paged_weights_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci]
+            L.polar_attn_decode_paged_weights_workspace_bytes.restype = cs
+            L.polar_cache_evict.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci,
+                                            ci, ci, ci, ci, ci, vp, cs, vp]
+            L.polar_cache_evict_workspace_bytes.argtypes = [ci, ci, ci, ci]
+            L.polar_cache_evict_workspace_bytes.restype = cs
             L.polar_attn_last_error.argtypes = []
             L.polar_attn_last_error.restype = ctypes.c_char_p
             for f in ("polar_attn_fwd", "polar_attn_decode", "polar_attn_combine",
                       "polar_attn_decode_num_splits", "polar_attn_device_status",
                       "polar_attn_selftest_wait_timeout", "polar_attn_version",
-                      "polar_attn_default_consts"):
+                      "polar_attn_default_consts", "polar_linear_fwd", "polar_linear_step",
+                      "polar_linear_bwd", "polar_attn_decode_paged_weights",
+                      "polar_cache_evict"):
                 getattr(L, f).restype = ci
             _lib = L
     return _lib
@@ -457,6 +477,246 @@ def memory_step(state, q, k, v, alpha, beta, mem=None, eps=1e-6, stream=None):
                                  float(eps), _stream(stream))
     _check(st, "polar_memory_step")
     return mem
+
+
+def linear_workspace_bytes(B, H, T, d, dtype=torch.bfloat16) -> int:
+    code = 1 if dtype == torch.bfloat16 else 0
+    return int(lib().polar_linear_workspace_bytes(B, H, T, d, code))
+
+
+def linear_bwd_workspace_bytes(B, H, T, d, dtype=torch.bfloat16) -> int:
+    code = 1 if dtype == torch.bfloat16 else 0
+    return int(lib().polar_linear_bwd_workspace_bytes(B, H, T, d, code))
+
+
+def _same_device(q, *tensors):
+    for t in tensors:
+        if t is not None and t.device != q.device:
+            raise ValueError(f"all tensors must be on {q.device}, got one on {t.device}")
+
+
+def _linear_args(q, k, v, log_decay, state, lengths, scale):
+    """Checks shared by linear_fwd and linear_bwd; returns (B, H, T, d, scale)."""
+    _dev(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, d]")
+    B, H, T, d = q.shape
+    for name, t in (("k", k), ("v", v)):
+        _dev(t, name, q.dtype)
+        _shape(t, name, q.shape)
+    _dev(log_decay, "log_decay", torch.float32)
+    _shape(log_decay, "log_decay", (H,))
+    _dev(state, "state", torch.float32)
+    _shape(state, "state", (B, H, d, d))
+    _dev(lengths, "lengths", torch.int32)
+    _shape(lengths, "lengths", (B,))
+    _same_device(q, k, v, log_decay, state, lengths)
+    return B, H, T, d, (d ** -0.5 if scale is None else float(scale))
+
+
+def _workspace(workspace, need, q):
+    if workspace is None:
+        return torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+    _dev(workspace, "workspace")
+    _same_device(q, workspace)
+    return workspace
+
+
+def linear_fwd(q, k, v, log_decay, state=None, lengths=None, scale=None, mem=None,
+               state_out=None, want_state=False, workspace=None, stream=None):
+    """Decayed linear attention over a prompt (a memory stream whose decay is
+    one number per head): q, k, v [B, H, T, d] (bf16 or fp32); log_decay [H]
+    fp32, <= 0; state [B, H, d, d] fp32 or None (zero); lengths [B] int32 or
+    None (all T): tokens of a padded batch.  scale defaults to d ** -0.5.
+    Returns (mem [B, H, T, d], state after the last token or None); rows of
+    mem past a length are zero.  state_out may be state."""
+    B, H, T, d, scale = _linear_args(q, k, v, log_decay, state, lengths, scale)
+    if mem is None:
+        mem = torch.empty_like(q)
+    if state_out is None and want_state:
+        state_out = torch.empty((B, H, d, d), device=q.device, dtype=torch.float32)
+    _dev(mem, "mem", q.dtype)
+    _shape(mem, "mem", q.shape)
+    _dev(state_out, "state_out", torch.float32)
+    _shape(state_out, "state_out", (B, H, d, d))
+    _same_device(q, mem, state_out)
+    code = _dtype_code(q)
+    with torch.cuda.device(q.device):
+        need = int(lib().polar_linear_workspace_bytes(B, H, T, d, code))
+        workspace = _workspace(workspace, need, q)
+        st = lib().polar_linear_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(mem),
+            _ptr(state_out), B, H, T, d, code, scale, _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "polar_linear_fwd")
+    return mem, state_out
+
+
+def linear_step(state, q, k, v, log_decay, scale=None, mem=None, stream=None):
+    """One token of the decayed linear attention, the state updated in place:
+    state [B, H, d, d] fp32; q, k, v [B, H, d] (bf16 or fp32); log_decay [H]
+    fp32.  Returns mem [B, H, d]."""
+    _dev(state, "state", torch.float32)
+    _dev(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H, d]")
+    B, H, d = q.shape
+    for name, t in (("k", k), ("v", v)):
+        _dev(t, name, q.dtype)
+        _shape(t, name, q.shape)
+    _shape(state, "state", (B, H, d, d))
+    _dev(log_decay, "log_decay", torch.float32)
+    _shape(log_decay, "log_decay", (H,))
+    if mem is None:
+        mem = torch.empty_like(q)
+    _dev(mem, "mem", q.dtype)
+    _shape(mem, "mem", q.shape)
+    _same_device(q, state, k, v, log_decay, mem)
+    with torch.cuda.device(q.device):
+        st = lib().polar_linear_step(
+            _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(mem), B, H, d,
+            _dtype_code(q), d ** -0.5 if scale is None else float(scale), _stream(stream))
+    _check(st, "polar_linear_step")
+    return mem
+
+
+def linear_bwd(q, k, v, log_decay, dmem, state=None, dstate_out=None, lengths=None, scale=None,
+               dq=None, dk=None, dv=None, dstate=None, want_dstate=False, workspace=None,
+               stream=None):
+    """Gradients of linear_fwd: dmem [B, H, T, d] in q's type and dstate_out
+    [B, H, d, d] fp32 (None: zero) are the gradients of its two results.
+    Returns (dq, dk, dv in q's type, dstate fp32 or None).  The decay is a
+    constant and gets none."""
+    B, H, T, d, scale = _linear_args(q, k, v, log_decay, state, lengths, scale)
+    _dev(dmem, "dmem", q.dtype)
+    _shape(dmem, "dmem", q.shape)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(q) if dk is None else dk
+    dv = torch.empty_like(q) if dv is None else dv
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        _dev(t, name, q.dtype)
+        _shape(t, name, q.shape)
+    if dstate is None and want_dstate:
+        dstate = torch.empty((B, H, d, d), device=q.device, dtype=torch.float32)
+    for name, t in (("dstate_out", dstate_out), ("dstate", dstate)):
+        _dev(t, name, torch.float32)
+        _shape(t, name, (B, H, d, d))
+    _same_device(q, dmem, dq, dk, dv, dstate_out, dstate)
+    code = _dtype_code(q)
+    with torch.cuda.device(q.device):
+        need = int(lib().polar_linear_bwd_workspace_bytes(B, H, T, d, code))
+        workspace = _workspace(workspace, need, q)
+        st = lib().polar_linear_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(dmem),
+            _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate), B, H, T, d, code, scale,
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "polar_linear_bwd")
+    return dq, dk, dv, dstate
+
+
+def decode_paged_weights_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits=0) -> int:
+    return int(lib().polar_attn_decode_paged_weights_workspace_bytes(B, Hq, Hkv, max_seq_len, d,
+                                                                     num_splits))
+
+
+def decode_paged_weights(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, weights,
+                         max_seq_len=None, num_splits=0, workspace=None, out=None, n_eff=None,
+                         conf=None, consts=None, want_conf=False, stream=None):
+    """decode_paged that also adds every cache row's attention weight, summed
+    over the query heads of its group, to weights [B, Hkv, stride] fp32
+    (stride >= max_seq_len).  max_seq_len defaults to the smaller of the
+    table's capacity and the stride.  Returns (out, n_eff, conf)."""
+    _dev(q, "q")
+    dt = q.dtype
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("mem", mem)):
+        _dev(t, name, dt)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(w_count, "w_count", torch.float32)
+    _dev(weights, "weights", torch.float32)
+    B, Hq, d = q.shape
+    num_pages, Hkv, page, d2 = k_pages.shape
+    if d2 != d or v_pages.shape != k_pages.shape or tuple(mem.shape) != (B, Hq, d):
+        raise ValueError("shape mismatch between q, mem and the pages")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    _shape(seq_lens, "seq_lens", (B,))
+    _shape(w_count, "w_count", (Hq, d))
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv):
+        raise ValueError("weights must be [B, Hkv, stride]")
+    max_pages, stride = block_table.shape[1], weights.shape[2]
+    if max_seq_len is None:
+        max_seq_len = min(max_pages * page, stride)
+    if out is None:
+        out = torch.empty_like(q)
+    if n_eff is None:
+        n_eff = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+    if conf is None and want_conf:
+        conf = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+    _dec_outputs(q, out, n_eff, conf, (B, Hq))
+    _same_device(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, weights, out, n_eff,
+                 conf)
+    c = consts or default_consts()
+    with torch.cuda.device(q.device):
+        need = decode_paged_weights_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits)
+        workspace = _workspace(workspace, need, q)
+        st = lib().polar_attn_decode_paged_weights(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(mem),
+            _ptr(w_count), _ptr(out), _ptr(n_eff), _ptr(conf), _ptr(weights), stride, B, Hq, Hkv,
+            d, page, num_pages, max_pages, int(max_seq_len), _dtype_code(q), ctypes.byref(c),
+            int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream(stream))
+    _check(st, "polar_attn_decode_paged_weights")
+    return out, n_eff, conf
+
+
+def cache_evict_workspace_bytes(B, Hkv, max_seq_len, keep) -> int:
+    return int(lib().polar_cache_evict_workspace_bytes(B, Hkv, max_seq_len, keep))
+
+
+def cache_evict(k_pages, v_pages, block_table, seq_lens, weights, positions, keep, recent=0,
+                max_seq_len=None, new_lens=None, workspace=None, stream=None):
+    """Cuts every sequence of more than `keep` rows to `keep`, per KV head and
+    in place: the rows of the newest `recent` tokens stay, then those of
+    largest accumulated weight.
+
+    k_pages, v_pages [num_pages, Hkv, page, d]; block_table [B, max_pages]
+    and seq_lens [B] int32; weights [B, Hkv, stride] fp32 and positions [B,
+    Hkv, stride] int32 move with the rows.  Returns the new lengths [B] int32
+    (written into new_lens when given, which may be seq_lens)."""
+    _dev(k_pages, "k_pages")
+    _dev(v_pages, "v_pages", k_pages.dtype)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(weights, "weights", torch.float32)
+    _dev(positions, "positions", torch.int32)
+    num_pages, Hkv, page, d = k_pages.shape
+    _shape(v_pages, "v_pages", k_pages.shape)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    _shape(seq_lens, "seq_lens", (B,))
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv):
+        raise ValueError("weights must be [B, Hkv, stride]")
+    _shape(positions, "positions", weights.shape)
+    stride = weights.shape[2]
+    if max_seq_len is None:
+        max_seq_len = min(max_pages * page, stride)
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+    _dev(new_lens, "new_lens", torch.int32)
+    _shape(new_lens, "new_lens", (B,))
+    _same_device(k_pages, v_pages, block_table, seq_lens, weights, positions, new_lens)
+    with torch.cuda.device(k_pages.device):
+        need = cache_evict_workspace_bytes(B, Hkv, max_seq_len, int(keep))
+        workspace = _workspace(workspace, need, k_pages)
+        st = lib().polar_cache_evict(
+            _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(weights),
+            _ptr(positions), _ptr(new_lens), B, Hkv, d, page, num_pages, max_pages,
+            int(max_seq_len), stride, _dtype_code(k_pages), int(keep), int(recent),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "polar_cache_evict")
+    return new_lens
 
 
 def bwd_workspace_bytes(B, H, T, d) -> int:
