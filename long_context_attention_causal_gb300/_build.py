@@ -20,8 +20,8 @@ LIB = os.path.join(PKG, "libpolarattn.so")
 SOURCES = ["polar_api.cu", "polar_prefill_tc.cu", "polar_prefill_f32.cu",
            "polar_decode.cu", "polar_decode_static.cu", "polar_memory.cu",
            "polar_backward.cu", "polar_backward_tc.cu", "polar_host.cu",
-           "polar_decode_paged_tc.cu", "polar_linear.cu", "polar_linear_api.cu",
-           "polar_cache.cu"]
+           "polar_decode_paged_tc.cu", "polar_linear.cu", "polar_linear_tc.cu",
+           "polar_linear_api.cu", "polar_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -91,6 +91,7 @@ struct LinearArgs {
   const float* seg_states;  // [BH][nseg][d][d] state before each segment, or null: one
                             // segment that starts from init
   int* status;
+  float* final_state = nullptr;  // tensor-core kernel, one segment: the state after all
 };
 constexpr int kLinearTile = 128;
 
@@ -109,9 +110,14 @@ struct LinearStateArgs {
   float* final_state;  // may be null
   int* status;
 };
-cudaError_t launch_linear_states(const LinearStateArgs& a, int dtype, cudaStream_t s);
+// fp32 on the FP32 pipes.
+cudaError_t launch_linear_states(const LinearStateArgs& a, cudaStream_t s);
 cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s);
-cudaError_t launch_linear_out(const LinearArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_linear_out(const LinearArgs& a, cudaStream_t s);
+// bf16 on the tensor cores.  maps: x, y, z, out / y, z (128-row boxes).
+cudaError_t launch_linear_out_tc(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s);
+cudaError_t launch_linear_states_tc(const LinearStateArgs& a, const CUtensorMap* maps,
+                                    cudaStream_t s);
 
 struct LinearStepArgs {
   float* state;

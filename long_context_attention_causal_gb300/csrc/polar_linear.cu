@@ -415,9 +415,7 @@ cudaError_t out_d(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_linear_states(const LinearStateArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == POLAR_BF16)
-    return a.d == 64 ? states_d<64, __nv_bfloat16>(a, s) : states_d<128, __nv_bfloat16>(a, s);
+cudaError_t launch_linear_states(const LinearStateArgs& a, cudaStream_t s) {
   return a.d == 64 ? states_d<64, float>(a, s) : states_d<128, float>(a, s);
 }
 
@@ -426,9 +424,7 @@ cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_linear_out(const LinearArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == POLAR_BF16)
-    return a.d == 64 ? out_d<64, __nv_bfloat16>(a, s) : out_d<128, __nv_bfloat16>(a, s);
+cudaError_t launch_linear_out(const LinearArgs& a, cudaStream_t s) {
   return a.d == 64 ? out_d<64, float>(a, s) : out_d<128, float>(a, s);
 }
 

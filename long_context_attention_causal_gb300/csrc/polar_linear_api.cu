@@ -62,6 +62,31 @@ size_t state_bytes(int B, int H, int T, int d, int dtype) {
   return (size_t)B * H * g.nseg * d * d * sizeof(float);
 }
 
+// bf16 runs on the tensor cores, fp32 on the FP32 pipes.
+int run_states(const LinearStateArgs& a, int dtype, cudaStream_t s) {
+  int st;
+  if (dtype == POLAR_BF16) {
+    CUtensorMap maps[2];
+    if (!make_map(&maps[0], a.y, a.B * a.H, a.T, a.d) ||
+        !make_map(&maps[1], a.z, a.B * a.H, a.T, a.d))
+      return POLAR_ERR_CUDA;
+    st = cuda_status("linear state launch", launch_linear_states_tc(a, maps, s));
+  } else {
+    st = cuda_status("linear state launch", launch_linear_states(a, s));
+  }
+  if (st != POLAR_OK) return st;
+  return cuda_status("linear scan launch", launch_linear_scan(a, s));
+}
+
+int run_out(const LinearArgs& a, int dtype, cudaStream_t s) {
+  if (dtype != POLAR_BF16) return cuda_status("linear output launch", launch_linear_out(a, s));
+  CUtensorMap maps[4];
+  const void* bases[4] = {a.x, a.y, a.z, a.out};
+  for (int i = 0; i < 4; ++i)
+    if (!make_map(&maps[i], bases[i], a.B * a.H, a.T, a.d)) return POLAR_ERR_CUDA;
+  return cuda_status("linear output launch", launch_linear_out_tc(a, maps, s));
+}
+
 }  // namespace
 
 }  // namespace polar
@@ -102,21 +127,20 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   if (!status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* seg = static_cast<float*>(workspace);
-  const bool walked = g.nseg > 1 || state_out;
+  // The tensor-core kernel writes the state of a whole sequence itself.
+  const bool tc = dtype == POLAR_BF16;
+  const bool walked = g.nseg > 1 || (state_out && !(tc && g.nseg == 1));
   if (walked) {
     const LinearStateArgs a{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
                             g.nseg, g.seg_tokens, state_in, seg, state_out, status};
-    if (g.nseg > 0) {
-      st = cuda_status("linear state launch", launch_linear_states(a, dtype, s));
-      if (st != POLAR_OK) return st;
-    }
-    st = cuda_status("linear scan launch", launch_linear_scan(a, s));
+    st = T > 0 ? run_states(a, dtype, s) : cuda_status("linear scan launch", launch_linear_scan(a, s));
     if (st != POLAR_OK) return st;
   }
   if (T == 0) return POLAR_OK;
   const LinearArgs a{q, k, v, mem, log_decay, lengths, B, H, T, d, scale, false, false,
-                     g.nseg, g.seg_tokens, state_in, walked ? seg : nullptr, status};
-  return cuda_status("linear output launch", launch_linear_out(a, dtype, s));
+                     g.nseg, g.seg_tokens, state_in, walked ? seg : nullptr, status,
+                     walked ? nullptr : state_out};
+  return run_out(a, dtype, s);
 }
 
 int polar_linear_step(float* state, const void* q, const void* k, const void* v,
@@ -163,33 +187,32 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* seg_s = static_cast<float*>(workspace);
   float* seg_r = seg_s + one;
+  const bool tc = dtype == POLAR_BF16;
   if (g.nseg > 1) {
     const LinearStateArgs a{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
                             g.nseg, g.seg_tokens, state_in, seg_s, nullptr, status};
-    st = cuda_status("linear state launch", launch_linear_states(a, dtype, s));
-    if (st == POLAR_OK) st = cuda_status("linear scan launch", launch_linear_scan(a, s));
+    st = run_states(a, dtype, s);
     if (st != POLAR_OK) return st;
   }
-  const bool walked = g.nseg > 1 || dstate_in;
+  const bool walked = g.nseg > 1 || (dstate_in && !(tc && g.nseg == 1));
   if (walked) {
     const LinearStateArgs a{q, dmem, log_decay, lengths, B, H, T, d, scale, true,
                             g.nseg, g.seg_tokens, dstate_out, seg_r, dstate_in, status};
-    if (g.nseg > 0) {
-      st = cuda_status("linear state launch", launch_linear_states(a, dtype, s));
-      if (st != POLAR_OK) return st;
-    }
-    st = cuda_status("linear scan launch", launch_linear_scan(a, s));
+    st = T > 0 ? run_states(a, dtype, s) : cuda_status("linear scan launch", launch_linear_scan(a, s));
     if (st != POLAR_OK) return st;
   }
   if (T == 0) return POLAR_OK;
+  const float* before_r = walked ? seg_r : nullptr;
   const LinearArgs aq{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
                       g.nseg, g.seg_tokens, state_in, g.nseg > 1 ? seg_s : nullptr, status};
   const LinearArgs ak{v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
-                      g.nseg, g.seg_tokens, dstate_out, walked ? seg_r : nullptr, status};
+                      g.nseg, g.seg_tokens, dstate_out, before_r, status};
+  // last: it may write dstate_in over dstate_out, which dk's kernel reads
   const LinearArgs av{k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
-                      g.nseg, g.seg_tokens, dstate_out, walked ? seg_r : nullptr, status};
+                      g.nseg, g.seg_tokens, dstate_out, before_r, status,
+                      walked ? nullptr : dstate_in};
   for (const LinearArgs* a : {&aq, &ak, &av}) {
-    st = cuda_status("linear gradient launch", launch_linear_out(*a, dtype, s));
+    st = run_out(*a, dtype, s);
     if (st != POLAR_OK) return st;
   }
   return POLAR_OK;

@@ -1,0 +1,782 @@
+// Decayed linear attention of bf16 tensors on the tensor cores.
+//
+// The mathematics (chunks, the state before them, the two directions, the
+// segments) is in polar_linear.cu; a chunk here is a tile of 128 tokens.
+// Per tile, with x, y, z its rows, M the state before it (z dim x y dim) and
+// w_j the powers of the decay:
+//   S  = x y^T                 scores            A, B in shared memory
+//   P  = S * decay, bf16                         over S in TMEM
+//   O1 = P z                                     A in TMEM
+//   O2 = x M^T                 M as a bf16 operand in shared memory
+//   out_i = O1_i + g^(i+1) O2_i
+//   M' = g^n M + z^T (w y)
+// The state lives in fp32 registers (a row of TMEM's lanes a thread pair);
+// its products leave TMEM once a tile.  w y is not exact in bf16, so it
+// enters as two bf16 terms, hi + lo (2^-16 relative), both products in fp32:
+// the state is as good as fp32 inputs allow, and what it rounds to bf16 for
+// O2 is rounded once.  hi, then lo, are written over y in place, which only
+// the scores read unscaled: no second copy of a tile is needed, and two whole
+// stages of x, y, z fit beside the state operand (7 x 32 KB at d = 128).
+//
+// Bound: HBM.  A tile moves 4 x 32 KB at d = 128 against 6 products of
+// 2 * 128^3 flop: at the measured rates 3.0 us of an SM's share of the copy
+// bandwidth to about 2.0 us of its tensor rate.
+//
+// Roles (448 threads, one CTA per SM): warps 0-3 P and the outputs (thread =
+// row = TMEM lane), warps 4-11 the state and the scaling of y (two groups,
+// half of the columns each), warp 12 TMA, warp 13 MMA and TMEM.
+#include "polar_device.cuh"
+#include "polar_internal.h"
+#include "polar_linear.cuh"
+
+namespace polar {
+
+namespace {
+
+constexpr int kTok = kLinearTile;  // tokens per tile
+constexpr int kThreads = 448;
+constexpr int kStateThreads = 256;
+constexpr int kWarpTMA = 12, kWarpMMA = 13;
+constexpr int kStateWarps = 8;
+constexpr uint32_t kColS = 0, kColO1 = 128, kColO2 = 256, kColDS = 384;
+
+struct OutBars {
+  uint64_t full_xy[2], full_z[2], empty_x[2], empty_yz[2];
+  uint64_t s_full, p_full, o_full, o_free;      // one phase a tile
+  uint64_t y_hi, y_lo, hi_done, ds_full, m_op;  // m_op: one phase a tile, the first before it
+  uint64_t fixed;                               // once: rows past the sequence are zeroed
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  float full_pw[32];   // g^31 .. g^0 (forward), g^0 .. g^31 (reverse)
+  float diag_pw[64];   // 31 zeros, then g^0 .. g^31
+};
+
+template <int D>
+struct OutLayout {
+  static constexpr int kTile = kTok * D * 2;
+  static constexpr int kAtom = kTok * 128;  // 64 columns of a tile
+  static constexpr int kStage = 3 * kTile;  // x, y, z
+  static constexpr int kMOff = 2 * kStage;  // state operand, D rows
+  static constexpr int kMAtom = D * 128;
+  static constexpr int kBarOff = kMOff + D * D * 2;
+  static constexpr int kSmemBytes = kBarOff + (int)sizeof(OutBars) + 1024;
+  // more than half of the SM's, so one CTA holds the 512 TMEM columns
+  static constexpr int kAsked = kSmemBytes > 120000 ? kSmemBytes : 120000;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+struct OutParams {
+  const float* log_decay;
+  const int* lengths;
+  const float* init;        // state at the sequence's start or end, or null
+  const float* seg_states;  // per segment, or null
+  float* final_state;       // or null (one segment per sequence only)
+  __nv_bfloat16* out;
+  int H, T, nseg, seg_tokens, state_t;
+  float scale;
+  int* status;
+};
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x,
+                                             int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_commit_wait_read() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// Generic-proxy shared-memory writes made visible to TMA and the tensor core.
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Named barrier of the 128 output threads that also ANDs a predicate: after a
+// failed wait all of them leave together.
+__device__ __forceinline__ bool out_bar_and(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+// The pair (f0, f1) as bf16 hi and the rest as bf16 lo.
+__device__ __forceinline__ void split_pair(float f0, float f1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(f0, f1);
+  lo = pack_bf16x2(f0 - __uint_as_float(hi << 16), f1 - __uint_as_float(hi & 0xFFFF0000u));
+}
+__device__ __forceinline__ void split_vec(uint4 y, float w, uint4& hi, uint4& lo) {
+  const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    split_pair(w * __uint_as_float(in[e] << 16), w * __uint_as_float(in[e] & 0xFFFF0000u), h[e],
+               l[e]);
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Zero rows [n, 128) of a tile in shared memory (state threads).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int n, int tid) {
+  for (int i = tid; i < kTok * D / 8; i += kStateThreads)
+    if (((i >> 3) & (kTok - 1)) >= n) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// One (b, h) segment a CTA.  kRev: from the last tile back.
+template <int D, bool kRev>
+__global__ void __launch_bounds__(kThreads, 1)
+    polar_linear_out_tc_kernel(const __grid_constant__ CUtensorMap map_x,
+                               const __grid_constant__ CUtensorMap map_y,
+                               const __grid_constant__ CUtensorMap map_z,
+                               const __grid_constant__ CUtensorMap map_o, const OutParams p) {
+  using L = OutLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  OutBars& br = *reinterpret_cast<OutBars*>(smem + L::kBarOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
+  const int len = linear_length(p.lengths, bh / p.H, p.T, p.status);
+  const int t0 = seg * p.seg_tokens, t1 = min(t0 + p.seg_tokens, p.T);
+  const int tokens = min(max(len - t0, 0), t1 - t0);  // of this segment
+  const int nt = (tokens + kTok - 1) / kTok;          // tiles that hold any
+  const float l2 = linear_log2_decay(p.log_decay, bh % p.H);
+  const bool final = p.final_state != nullptr;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&br.full_xy[i], 1);
+      mbar_init(&br.full_z[i], 1);
+      mbar_init(&br.empty_x[i], 1);
+      mbar_init(&br.empty_yz[i], 1);
+    }
+    mbar_init(&br.s_full, 1);
+    mbar_init(&br.p_full, 4);
+    mbar_init(&br.o_full, 1);
+    mbar_init(&br.o_free, 4);
+    mbar_init(&br.y_hi, kStateWarps);
+    mbar_init(&br.y_lo, kStateWarps);
+    mbar_init(&br.hi_done, 1);
+    mbar_init(&br.ds_full, 1);
+    mbar_init(&br.m_op, kStateWarps);
+    mbar_init(&br.fixed, kStateWarps);
+    mbar_init(&br.drain, 1);
+    br.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (threadIdx.x < 32) br.full_pw[threadIdx.x] = linear_power(l2, kRev ? lane : 31 - lane);
+  if (threadIdx.x < 64)
+    br.diag_pw[threadIdx.x] = threadIdx.x < 31 ? 0.f : linear_power(l2, (int)threadIdx.x - 31);
+  if (warp == kWarpMMA) tmem_alloc(&br.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = br.tmem_base;
+  volatile int* abort_flag = &br.abort_flag;
+  // tile of step c, its first token, and the tokens it holds
+  auto tile_row = [&](int c) { return t0 + (kRev ? nt - 1 - c : c) * kTok; };
+  auto tile_n = [&](int c) { return min(kTok, t0 + tokens - tile_row(c)); };
+  // rows past the sequence, but inside the tensor, must be zeroed
+  auto ragged = [&](int c) { return tile_n(c) < kTok && tile_row(c) + tile_n(c) < p.T; };
+  // the state after step c is read by step c + 1, or is the final one
+  auto updates = [&](int c) { return c + 1 < nt || final; };
+
+  if (warp == kWarpTMA) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      tma_prefetch_desc(&map_x);
+      tma_prefetch_desc(&map_y);
+      tma_prefetch_desc(&map_z);
+    }
+    __syncwarp();
+    int issued = 0;
+    bool ok = true;
+    for (int c = 0; c < nt && ok; ++c) {
+      const int st = c & 1;
+      if (c >= 2) {
+        ok = mbar_wait_warp(&br.empty_yz[st], (uint32_t)(c / 2 - 1) & 1, abort_flag, p.status);
+        if (ok)
+          ok = mbar_wait_warp(&br.empty_x[st], (uint32_t)(c / 2 - 1) & 1, abort_flag, p.status);
+      }
+      if (!ok) break;
+      uint8_t* sx = smem + st * L::kStage;
+      mbar_arrive_expect_tx_warp(&br.full_xy[st], 2 * L::kTile);
+      for (int h = 0; h < D / 64; ++h) {
+        tma_load_3d_warp(sx + h * L::kAtom, &map_x, &br.full_xy[st], 64 * h, tile_row(c), bh);
+        tma_load_3d_warp(sx + L::kTile + h * L::kAtom, &map_y, &br.full_xy[st], 64 * h,
+                         tile_row(c), bh);
+      }
+      mbar_arrive_expect_tx_warp(&br.full_z[st], L::kTile);
+      for (int h = 0; h < D / 64; ++h)
+        tma_load_3d_warp(sx + 2 * L::kTile + h * L::kAtom, &map_z, &br.full_z[st], 64 * h,
+                         tile_row(c), bh);
+      issued = c + 1;
+    }
+    if (!ok) {
+      // aborted: let the copies already issued land before the CTA exits
+      volatile int never = 0;
+      const long long lim = kWaitLimitCycles / 4;
+      for (int c = issued - 1; c >= 0 && c >= issued - 2; --c) {
+        mbar_wait(&br.full_xy[c & 1], (uint32_t)(c / 2) & 1, &never, p.status, lim);
+        mbar_wait(&br.full_z[c & 1], (uint32_t)(c / 2) & 1, &never, p.status, lim);
+      }
+      __syncwarp();
+    }
+  } else if (warp == kWarpMMA) {
+    // ------------------------------------------------------- MMA issuer --
+    // whole warp: uniform waits and descriptors, one elected lane issues
+    constexpr uint32_t kIdS = idesc_bf16_f32(kTok, kTok, 0, 0);
+    constexpr uint32_t kIdO1 = idesc_bf16_f32(kTok, D, 0, 1);
+    constexpr uint32_t kIdO2 = idesc_bf16_f32(kTok, D, 0, 0);
+    constexpr uint32_t kIdDS = idesc_bf16_f32(128, D, 1, 1);
+    const uint32_t lbo = D == 128 ? L::kAtom : 0;
+    const uint32_t base = smem_u32(smem);
+    // K-major (rows of 64 columns) and MN-major (tokens as the K dim) views
+    const uint64_t km = smem_desc_sw128(base, 16, 1024);
+    const uint64_t mn = smem_desc_sw128(base, lbo, 1024);
+    const uint64_t m_desc = smem_desc_sw128(base + L::kMOff, 16, 1024);
+    bool any = false;
+    auto at = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
+    auto kstep = [&](int kk, uint32_t atom) { return at((kk >> 2) * atom) + (uint64_t)(kk & 3) * 2; };
+    auto issue_s = [&](int c) -> bool {
+      if (!mbar_wait_warp(&br.full_xy[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status))
+        return false;
+      if (ragged(c) && !mbar_wait_warp(&br.fixed, 0, abort_flag, p.status)) return false;
+      tc_fence_after();
+      const uint64_t x0 = km + at((c & 1) * L::kStage), y0 = x0 + at(L::kTile);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_ss_warp(tmem + kColS, x0 + kstep(kk, L::kAtom), y0 + kstep(kk, L::kAtom), kIdS,
+                     kk > 0);
+      umma_commit_warp(&br.s_full);
+      any = true;
+      return true;
+    };
+    auto issue_o2 = [&](int c) -> bool {
+      if (!mbar_wait_warp(&br.m_op, (uint32_t)c & 1, abort_flag, p.status)) return false;
+      if (c > 0 && !mbar_wait_warp(&br.o_free, (uint32_t)(c - 1) & 1, abort_flag, p.status))
+        return false;
+      tc_fence_after();
+      const uint64_t x0 = km + at((c & 1) * L::kStage);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_ss_warp(tmem + kColO2, x0 + kstep(kk, L::kAtom), m_desc + kstep(kk, L::kMAtom), kIdO2,
+                     kk > 0);
+      return true;
+    };
+    auto issue_ds = [&](int c, bool add) {
+      const uint64_t y0 = mn + at((c & 1) * L::kStage + L::kTile), z0 = y0 + at(L::kTile);
+#pragma unroll
+      for (int kk = 0; kk < kTok / 16; ++kk)
+        umma_ss_warp(tmem + kColDS, z0 + at(kk * 2048), y0 + at(kk * 2048), kIdDS,
+                     (add || kk > 0) ? 1u : 0u);
+    };
+    bool ok = nt == 0 || (issue_s(0) && issue_o2(0));
+    for (int c = 0; c < nt && ok; ++c) {
+      ok = mbar_wait_warp(&br.full_z[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status) &&
+           mbar_wait_warp(&br.p_full, (uint32_t)c & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t z0 = mn + at((c & 1) * L::kStage + 2 * L::kTile);
+#pragma unroll
+      for (int kk = 0; kk < kTok / 16; ++kk)
+        umma_ts_warp(tmem + kColO1, tmem + kColS + kk * 8, z0 + at(kk * 2048), kIdO1, kk > 0);
+      umma_commit_warp(&br.o_full);  // O2 of this tile was issued before
+      if (updates(c)) {
+        ok = mbar_wait_warp(&br.y_hi, (uint32_t)c & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        issue_ds(c, false);
+        umma_commit_warp(&br.hi_done);
+        ok = mbar_wait_warp(&br.y_lo, (uint32_t)c & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        issue_ds(c, true);
+        umma_commit_warp(&br.ds_full);
+      }
+      umma_commit_warp(&br.empty_yz[c & 1]);
+      if (c + 1 < nt) ok = issue_s(c + 1) && issue_o2(c + 1);
+    }
+    if (!ok && any) {
+      // aborted: wait for the products in flight before TMEM is released
+      volatile int never = 0;
+      umma_commit_warp(&br.drain);
+      __syncwarp();
+      mbar_wait(&br.drain, 0, &never, p.status, kWaitLimitCycles / 4);
+      __syncwarp();
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------- P and the outputs --
+    const int r = threadIdx.x;  // row of the tile
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + kColS;
+    for (int c = 0; c < nt; ++c) {
+      const int n = tile_n(c);
+      bool ok = __all_sync(0xffffffffu,
+                           mbar_wait(&br.s_full, (uint32_t)c & 1, abort_flag, p.status));
+      if (ok) {
+        tc_fence_after();
+        // 32-column blocks of this warp's rows: whole before the diagonal one
+        // (after it in reverse), zero beyond it
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          uint32_t pk[16];
+          if (b == warp) {
+            uint32_t v[32];
+            tmem_ld32(s_tm + 32 * b, v);
+            tmem_ld_wait();
+            reg_fence32(v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float f[2];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int dist = kRev ? e + u - lane : lane - e - u;
+                const float w = p.scale * br.diag_pw[31 + dist];
+                f[u] = dist >= 0 ? __uint_as_float(v[e + u]) * w : 0.f;
+              }
+              pk[e / 2] = pack_bf16x2(f[0], f[1]);
+            }
+          } else if (kRev ? b > warp : b < warp) {
+            uint32_t v[32];
+            tmem_ld32(s_tm + 32 * b, v);
+            const float rf = p.scale * linear_power(l2, kRev ? 32 * b - r : r - 32 * b - 31);
+            tmem_ld_wait();
+            reg_fence32(v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(&br.full_pw[e]);
+              pk[e / 2] = pack_bf16x2(__uint_as_float(v[e]) * (w.x * rf),
+                                      __uint_as_float(v[e + 1]) * (w.y * rf));
+              pk[e / 2 + 1] = pack_bf16x2(__uint_as_float(v[e + 2]) * (w.z * rf),
+                                          __uint_as_float(v[e + 3]) * (w.w * rf));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          }
+          // P block b lies over S columns 16 b .. 16 b + 15, read already
+          tmem_st16(s_tm + 16 * b, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br.p_full);
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&br.o_full, (uint32_t)c & 1, abort_flag, p.status));
+      }
+      uint8_t* stage = smem + (c & 1) * L::kStage;  // x's tile: its readers are done
+      if (ok) {
+        tc_fence_after();
+        const bool live = r < n;
+        const float w2 = live ? (kRev ? linear_power(l2, n - 1 - r)
+                                      : p.scale * linear_power(l2, r + 1))
+                              : 0.f;
+#pragma unroll 1
+        for (int b = 0; b < D / 32; ++b) {
+          uint32_t o1[32], o2[32];
+          tmem_ld32(tmem + lane_base + kColO1 + 32 * b, o1);
+          tmem_ld32(tmem + lane_base + kColO2 + 32 * b, o2);
+          tmem_ld_wait();
+          reg_fence32(o1);
+          reg_fence32(o2);
+          if (b == D / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&br.o_free);
+          }
+          uint8_t* line = stage + (b >> 1) * L::kAtom + r * 128;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t o4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = 8 * g + 2 * e;
+              const float a0 = fmaf(w2, __uint_as_float(o2[i]), __uint_as_float(o1[i]));
+              const float a1 = fmaf(w2, __uint_as_float(o2[i + 1]), __uint_as_float(o1[i + 1]));
+              o4[e] = live ? pack_bf16x2(a0, a1) : 0u;
+            }
+            const int ch = (b & 1) * 4 + g;
+            *reinterpret_cast<uint4*>(line + ((ch ^ (r & 7)) << 4)) =
+                make_uint4(o4[0], o4[1], o4[2], o4[3]);
+          }
+        }
+        fence_async_smem();
+      }
+      if (!out_bar_and(ok)) break;
+      if (r == 0) {
+        for (int h = 0; h < D / 64; ++h)
+          tma_store_3d(&map_o, stage + h * L::kAtom, 64 * h, tile_row(c), bh);
+        tma_store_commit_wait_read();
+        mbar_arrive(&br.empty_x[c & 1]);
+      }
+    }
+    // tiles past the sequence
+    uint4* tail = reinterpret_cast<uint4*>(p.out + ((size_t)bh * p.T + t0 + (size_t)nt * kTok) * D);
+    const long long vecs = (long long)(t1 - t0 - nt * kTok) * (D / 8);
+    for (long long i = r; i < vecs; i += 128) tail[i] = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    // ------------------------------------------------ state, scaling of y --
+    const int tid = threadIdx.x - 128;
+    const int half = (warp - 4) >> 2;  // which half of the columns
+    const int r = threadIdx.x & 127;   // state row (z dim) = TMEM lane
+    constexpr int kCols = D / 2;
+    const bool mine = r < D;           // at d = 64 lanes 64.. repeat the rows
+    const uint32_t ds_tm =
+        tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColDS + half * kCols;
+    float m[kCols];
+    const float* src = p.seg_states ? p.seg_states + (size_t)blockIdx.x * D * D
+                                    : (p.init ? p.init + (size_t)bh * D * D : nullptr);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int col = half * kCols + i;
+      m[i] = src && mine ? (p.state_t ? src[(size_t)col * D + r] : src[(size_t)r * D + col]) : 0.f;
+    }
+    // the state as the bf16 operand of O2: row r, this half's columns
+    auto write_operand = [&]() {
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < kCols; i += 8) {
+          const int col = half * kCols + i;
+          uint8_t* line = smem + L::kMOff + (col >> 6) * L::kMAtom + r * 128;
+          const int ch = (col & 63) >> 3;
+          *reinterpret_cast<uint4*>(line + ((ch ^ (r & 7)) << 4)) =
+              make_uint4(pack_bf16x2(m[i], m[i + 1]), pack_bf16x2(m[i + 2], m[i + 3]),
+                         pack_bf16x2(m[i + 4], m[i + 5]), pack_bf16x2(m[i + 6], m[i + 7]));
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br.m_op);
+    };
+    write_operand();
+    constexpr int kVecs = kTok * D / 8 / kStateThreads;  // 16-byte pieces of y a thread
+    const float g_full = linear_power(l2, kTok);
+    float w_full[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = (tid >> 3) + 32 * k;
+      w_full[k] = kRev ? p.scale * linear_power(l2, j + 1) : linear_power(l2, kTok - 1 - j);
+    }
+    bool ok = true;
+    for (int c = 0; c < nt && ok; ++c) {
+      const int n = tile_n(c);
+      uint8_t* ty = smem + (c & 1) * L::kStage + L::kTile;
+      ok = mbar_wait_warp(&br.full_xy[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status);
+      if (ok && ragged(c)) {
+        ok = mbar_wait_warp(&br.full_z[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status);
+        if (!ok) break;
+        zero_rows<D>(ty, n, tid);
+        zero_rows<D>(ty + L::kTile, n, tid);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br.fixed);
+      }
+      if (!ok || !updates(c)) break;
+      ok = mbar_wait_warp(&br.s_full, (uint32_t)c & 1, abort_flag, p.status);
+      if (!ok) break;
+      uint4 lo[kVecs];
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        float w = w_full[k & 3];
+        if (n < kTok) {
+          const int j = (tid >> 3) + 32 * (k & 3);
+          w = j >= n ? 0.f : (kRev ? w : linear_power(l2, n - 1 - j));
+        }
+        uint4* at = reinterpret_cast<uint4*>(ty) + tid + kStateThreads * k;
+        uint4 hi;
+        split_vec(*at, w, hi, lo[k]);
+        *at = hi;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br.y_hi);
+      ok = mbar_wait_warp(&br.hi_done, (uint32_t)c & 1, abort_flag, p.status);
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k)
+        reinterpret_cast<uint4*>(ty)[tid + kStateThreads * k] = lo[k];
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br.y_lo);
+      ok = mbar_wait_warp(&br.ds_full, (uint32_t)c & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const float g = n == kTok ? g_full : linear_power(l2, n);
+#pragma unroll
+      for (int b = 0; b < kCols / 32; ++b) {
+        uint32_t v[32];
+        tmem_ld32(ds_tm + 32 * b, v);
+        tmem_ld_wait();
+        reg_fence32(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          m[32 * b + e] = fmaf(g, m[32 * b + e], __uint_as_float(v[e]));
+      }
+      // ds_full also says that O2 of this tile has read the operand
+      if (c + 1 < nt) write_operand();
+    }
+    if (ok && final && mine) {
+      float* dst = p.final_state + ((size_t)bh * D + r) * D + half * kCols;
+#pragma unroll
+      for (int i = 0; i < kCols; i += 4)
+        *reinterpret_cast<float4*>(dst + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------ segment states --
+
+// The state of each segment alone: one accumulator in TMEM over all of its
+// tiles, y weighted by the distance to the segment's end (start in reverse),
+// hi and lo, so nothing is ever rescaled.
+constexpr int kSThreads = 320;  // 8 scaling warps, TMA, MMA
+constexpr int kSWarpTMA = 8, kSWarpMMA = 9;
+
+template <int D>
+struct StateLayout {
+  static constexpr int kNS = D == 128 ? 2 : 4;
+  static constexpr int kTile = kTok * D * 2;
+  static constexpr int kAtom = kTok * 128;
+  static constexpr int kStage = 3 * kTile;  // y (then hi), z, lo
+  static constexpr int kBarOff = kNS * kStage;
+  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+};
+
+struct StateBars {
+  uint64_t full[4], empty[4], scaled[4], done, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+struct StateParams {
+  const float* log_decay;
+  const int* lengths;
+  float* seg_states;
+  int H, T, nseg, seg_tokens, reverse;
+  float scale;
+  int* status;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kSThreads, 1)
+    polar_linear_state_tc_kernel(const __grid_constant__ CUtensorMap map_y,
+                                 const __grid_constant__ CUtensorMap map_z, const StateParams p) {
+  using L = StateLayout<D>;
+  constexpr int NS = L::kNS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  StateBars& br = *reinterpret_cast<StateBars*>(smem + L::kBarOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
+  const int len = linear_length(p.lengths, bh / p.H, p.T, p.status);
+  const int t0 = seg * p.seg_tokens, t1 = max(t0, min(t0 + p.seg_tokens, len));
+  const int nt = (t1 - t0 + kTok - 1) / kTok;
+  const float l2 = linear_log2_decay(p.log_decay, bh % p.H);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&br.full[i], 1);
+      mbar_init(&br.empty[i], 1);
+      mbar_init(&br.scaled[i], kStateWarps);
+    }
+    mbar_init(&br.done, 1);
+    mbar_init(&br.drain, 1);
+    br.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kSWarpMMA) tmem_alloc(&br.tmem_base, 128);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = br.tmem_base;
+  volatile int* abort_flag = &br.abort_flag;
+
+  if (warp == kSWarpTMA) {
+    if (lane == 0) {
+      tma_prefetch_desc(&map_y);
+      tma_prefetch_desc(&map_z);
+    }
+    __syncwarp();
+    int issued = 0;
+    bool ok = true;
+    for (int c = 0; c < nt && ok; ++c) {
+      const int st = c % NS;
+      if (c >= NS)
+        ok = mbar_wait_warp(&br.empty[st], (uint32_t)(c / NS - 1) & 1, abort_flag, p.status);
+      if (!ok) break;
+      uint8_t* sy = smem + st * L::kStage;
+      mbar_arrive_expect_tx_warp(&br.full[st], 2 * L::kTile);
+      for (int h = 0; h < D / 64; ++h) {
+        tma_load_3d_warp(sy + h * L::kAtom, &map_y, &br.full[st], 64 * h, t0 + c * kTok, bh);
+        tma_load_3d_warp(sy + L::kTile + h * L::kAtom, &map_z, &br.full[st], 64 * h,
+                         t0 + c * kTok, bh);
+      }
+      issued = c + 1;
+    }
+    if (!ok) {
+      volatile int never = 0;
+      for (int c = issued - 1; c >= 0 && c >= issued - NS; --c)
+        mbar_wait(&br.full[c % NS], (uint32_t)(c / NS) & 1, &never, p.status,
+                  kWaitLimitCycles / 4);
+      __syncwarp();
+    }
+  } else if (warp == kSWarpMMA) {
+    constexpr uint32_t kId = idesc_bf16_f32(128, D, 1, 1);
+    const uint64_t mn = smem_desc_sw128(smem_u32(smem), D == 128 ? L::kAtom : 0, 1024);
+    auto at = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
+    bool ok = true, any = false;
+    for (int c = 0; c < nt; ++c) {
+      const int st = c % NS;
+      ok = mbar_wait_warp(&br.scaled[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t y0 = mn + at(st * L::kStage), z0 = y0 + at(L::kTile), l0 = z0 + at(L::kTile);
+#pragma unroll
+      for (int kk = 0; kk < kTok / 16; ++kk)
+        umma_ss_warp(tmem, z0 + at(kk * 2048), y0 + at(kk * 2048), kId,
+                     (c > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+      for (int kk = 0; kk < kTok / 16; ++kk)
+        umma_ss_warp(tmem, z0 + at(kk * 2048), l0 + at(kk * 2048), kId, 1u);
+      umma_commit_warp(&br.empty[st]);
+      any = true;
+    }
+    if (ok && any) umma_commit_warp(&br.done);
+    if (!ok && any) {
+      volatile int never = 0;
+      umma_commit_warp(&br.drain);
+      __syncwarp();
+      mbar_wait(&br.drain, 0, &never, p.status, kWaitLimitCycles / 4);
+      __syncwarp();
+    }
+  } else {
+    const int tid = threadIdx.x;
+    bool ok = true;
+    for (int c = 0; c < nt; ++c) {
+      const int st = c % NS, row = t0 + c * kTok, n = min(kTok, t1 - row);
+      ok = mbar_wait_warp(&br.full[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
+      if (!ok) break;
+      uint8_t* ty = smem + st * L::kStage;
+      if (n < kTok) zero_rows<D>(ty + L::kTile, n, tid);
+      constexpr int kVecs = kTok * D / 8 / kStateThreads;
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = row + (tid >> 3) + 32 * k;
+        w[k] = p.scale * linear_power(l2, p.reverse ? t - t0 + 1 : max(t1 - 1 - t, 0));
+      }
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        const bool live = (tid >> 3) + 32 * (k & 3) < n;
+        uint4* at = reinterpret_cast<uint4*>(ty) + tid + kStateThreads * k;
+        uint4 hi, lo;
+        split_vec(*at, w[k & 3], hi, lo);
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        *at = live ? hi : zero;
+        *(reinterpret_cast<uint4*>(ty + 2 * L::kTile) + tid + kStateThreads * k) =
+            live ? lo : zero;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br.scaled[st]);
+    }
+    const int half = warp >> 2, r = threadIdx.x & 127;
+    constexpr int kCols = D / 2;
+    float* dst = p.seg_states + ((size_t)blockIdx.x * D + r) * D + half * kCols;
+    ok = ok && (nt == 0 || mbar_wait(&br.done, 0, abort_flag, p.status));
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < kCols / 32; ++b) {
+        uint32_t v[32];
+        if (nt > 0) {
+          tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * kCols + 32 * b, v);
+          tmem_ld_wait();
+          reg_fence32(v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0u;
+        }
+        if (r < D) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(dst + 32 * b + e) =
+                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSWarpMMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
+template <int D, bool kRev>
+cudaError_t out_tc_d(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s) {
+  using L = OutLayout<D>;
+  const OutParams p{a.log_decay, a.lengths, a.init, a.seg_states, a.final_state,
+                    static_cast<__nv_bfloat16*>(a.out), a.H, a.T, a.nseg, a.seg_tokens,
+                    a.state_t ? 1 : 0, a.scale, a.status};
+  auto kern = polar_linear_out_tc_kernel<D, kRev>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAsked);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)a.B * a.H * a.nseg, kThreads, L::kAsked, s>>>(maps[0], maps[1], maps[2],
+                                                                 maps[3], p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t state_tc_d(const LinearStateArgs& a, const CUtensorMap* maps, cudaStream_t s) {
+  using L = StateLayout<D>;
+  const StateParams p{a.log_decay, a.lengths, a.seg_states, a.H, a.T, a.nseg, a.seg_tokens,
+                      a.reverse ? 1 : 0, a.scale, a.status};
+  cudaError_t e = cudaFuncSetAttribute(polar_linear_state_tc_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       L::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  polar_linear_state_tc_kernel<D>
+      <<<(unsigned)a.B * a.H * a.nseg, kSThreads, L::kSmemBytes, s>>>(maps[0], maps[1], p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_out_tc(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s) {
+  if (a.d == 64)
+    return a.reverse ? out_tc_d<64, true>(a, maps, s) : out_tc_d<64, false>(a, maps, s);
+  return a.reverse ? out_tc_d<128, true>(a, maps, s) : out_tc_d<128, false>(a, maps, s);
+}
+
+cudaError_t launch_linear_states_tc(const LinearStateArgs& a, const CUtensorMap* maps,
+                                    cudaStream_t s) {
+  return a.d == 64 ? state_tc_d<64>(a, maps, s) : state_tc_d<128>(a, maps, s);
+}
+
+}  // namespace polar
