@@ -73,11 +73,21 @@ struct EvictArgs {
   int* status;
 };
 
-// One application of the decayed linear recurrence over all (b, h):
+// How the decayed linear recurrence is spread over CTAs: the tiles of all
+// (b, h), head by head, in `parts` runs of `per` tiles.  A head that a run
+// boundary cuts is continued from a state handed over (LinearStateArgs).
+constexpr int kLinearTile = 128;
+struct LinearSplit {
+  int tiles;  // of one head
+  int per, parts;
+  bool cut;   // some boundary lies inside a head
+};
+
+// One application of the recurrence over all (b, h):
 //   forward: out_t = s * (sum_{u <= t} g^(t-u) (x_t . y_u) z_u + g^(t+1) M x_t)
 //   reverse: out_t = s * sum_{u >= t} g^(u-t) (x_t . y_u) z_u + g^(L-1-t) M x_t
 // with M the state at the sequence's start (forward) or end (reverse).  The
-// stored state is [z dim][y dim], transposed if state_t.
+// stored states are [z dim][y dim], transposed if state_t.
 struct LinearArgs {
   const void *x, *y, *z;  // [B, H, T, d]
   void* out;              // [B, H, T, d]
@@ -86,17 +96,16 @@ struct LinearArgs {
   int B, H, T, d;
   float scale;
   bool reverse, state_t;
-  int nseg, seg_tokens;   // segments of whole tiles of kLinearTile tokens
-  const float* init;      // state at the start, or null (zero)
-  const float* seg_states;  // [BH][nseg][d][d] state before each segment, or null: one
-                            // segment that starts from init
+  LinearSplit split;
+  const float* init;      // [B, H, d, d] state at the start (end), or null (zero)
+  const float* cuts;      // states at the cuts (LinearStateArgs), null without cuts
+  float* final_state;     // [B, H, d, d] state at the other end, or null (not with state_t)
   int* status;
-  float* final_state = nullptr;  // tensor-core kernel, one segment: the state after all
 };
-constexpr int kLinearTile = 128;
 
-// State of each segment alone, then (scan) the states before each segment in
-// place and the final state.
+// States at the cuts.  Forward: slot i is the state at the end of run i,
+// reverse: at its start.  The state kernels sum each run's own part of the
+// cut head; the scan joins them in place, from init.
 struct LinearStateArgs {
   const void *y, *z;
   const float* log_decay;
@@ -104,11 +113,11 @@ struct LinearStateArgs {
   int B, H, T, d;
   float scale;  // factor of the state's products
   bool reverse;
-  int nseg, seg_tokens;
-  const float* init;   // may be null
-  float* seg_states;   // [BH][nseg][d][d]
-  float* final_state;  // may be null
+  LinearSplit split;
+  const float* init;  // may be null
+  float* cuts;        // [parts][d][d]
   int* status;
+  float* init_copy;   // [B, H, d, d]: where the scan copies init, or null
 };
 // fp32 on the FP32 pipes.
 cudaError_t launch_linear_states(const LinearStateArgs& a, cudaStream_t s);
@@ -118,6 +127,9 @@ cudaError_t launch_linear_out(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_out_tc(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s);
 cudaError_t launch_linear_states_tc(const LinearStateArgs& a, const CUtensorMap* maps,
                                     cudaStream_t s);
+// final = init (or zero) for prompts without tokens.
+cudaError_t launch_linear_copy_state(const float* init, float* final_state, size_t n,
+                                     cudaStream_t s);
 
 struct LinearStepArgs {
   float* state;

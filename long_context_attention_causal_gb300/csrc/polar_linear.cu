@@ -1,5 +1,5 @@
 // Decayed linear attention on the FP32 pipes: the single-token step, the
-// segment states, their scan, and the chunked outputs for fp32 tensors.
+// states at the cuts, their scan, and the chunked outputs for fp32 tensors.
 //
 // Per head, S_t = g S_{t-1} + v_t k_t^T and mem_t = c S_t q_t.  Over a chunk
 // of tokens with local index i and the state M before it,
@@ -14,10 +14,10 @@
 //   out_i = c sum_{j >= i} g^(j-i) (x_i . y_j) z_j + g^(n-1-i) M x_i
 //   M'    = g^n M + c sum_j g^(j+1) z_j y_j^T
 //
-// A sequence is cut into segments of whole 128-token tiles, so that few
-// heads still fill the GPU: one kernel sums each segment's state alone, a
-// scan turns them into the states before each segment, and the output kernel
-// walks the segments in parallel.
+// The 128-token tiles of all heads are dealt out to the CTAs in equal runs, so
+// that few heads still fill the GPU.  A head that a run boundary cuts needs
+// its state there first: one kernel sums each run's own part of the cut head,
+// a scan joins the parts, and the output kernel walks all runs in parallel.
 #include "polar_device.cuh"
 #include "polar_internal.h"
 #include "polar_linear.cuh"
@@ -107,7 +107,7 @@ __device__ __forceinline__ void state_products(float4 (&acc)[StateTile<D>::kR],
   }
 }
 
-// ------------------------------------------------------ segment states --
+// ------------------------------------------------------ states at cuts --
 
 template <int D>
 struct StateSmem {
@@ -115,20 +115,22 @@ struct StateSmem {
   float zw[kC][kZ];
 };
 
-// Grid (BH * nseg, D / kZ).  Weights are taken from the segment's end, so the
-// accumulators never need rescaling.
+// Grid (parts, D / kZ): the part of the run that reaches its cut.  Weights are
+// taken from the cut, so the accumulators never need rescaling.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads)
     polar_linear_state_kernel(const LinearStateArgs a) {
   using S = StateTile<D>;
   __shared__ __align__(16) StateSmem<D> sm;
-  const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
-  const int z0 = blockIdx.y * kZ;
-  const int len = linear_length(a.lengths, bh / a.H, a.T, a.status);
-  const int t0 = seg * a.seg_tokens, t1 = min(t0 + a.seg_tokens, len);
-  const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
-  const T* y = static_cast<const T*>(a.y) + (size_t)bh * a.T * D;
-  const T* z = static_cast<const T*>(a.z) + (size_t)bh * a.T * D;
+  const int BH = a.B * a.H, part = blockIdx.x, z0 = blockIdx.y * kZ;
+  const int i = a.reverse ? 0 : linear_portions(a.split, BH, part) - 1;
+  const LinearPortion po =
+      linear_portion(a.split, BH, a.H, a.T, a.lengths, a.status, part, i);
+  if (!(a.reverse ? po.cut_left : po.cut_right)) return;
+  const int t0 = po.row(po.first), t1 = max(t0, min(po.row(po.last), po.len));
+  const float l2 = linear_log2_decay(a.log_decay, po.bh % a.H);
+  const T* y = static_cast<const T*>(a.y) + (size_t)po.bh * a.T * D;
+  const T* z = static_cast<const T*>(a.z) + (size_t)po.bh * a.T * D;
   float4 acc[S::kR];
 #pragma unroll
   for (int r = 0; r < S::kR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -140,8 +142,7 @@ __global__ void __launch_bounds__(kThreads)
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < t1) {
         v = load4<T>(z + (size_t)t * D + z0 + c);
-        const float w = a.reverse ? a.scale * linear_power(l2, t - t0 + 1)
-                                  : a.scale * linear_power(l2, t1 - 1 - t);
+        const float w = a.scale * linear_power(l2, a.reverse ? t - t0 + 1 : t1 - 1 - t);
         v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
       }
       *reinterpret_cast<float4*>(&sm.zw[r][c]) = v;
@@ -149,41 +150,61 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     state_products<D>(acc, sm.y, sm.zw);
   }
-  float* dst = a.seg_states + ((size_t)blockIdx.x * D + z0) * D;
+  float* dst = a.cuts + ((size_t)part * D + z0) * D;
 #pragma unroll
   for (int r = 0; r < S::kR; ++r)
     *reinterpret_cast<float4*>(dst + (size_t)(S::row0() + r) * D + S::col0()) = acc[r];
 }
 
-// Grid (BH, d * d / 256): one state element per thread through the segments
-// in order; the segment's own sum is replaced by the state before it.
-__global__ void __launch_bounds__(256) polar_linear_scan_kernel(const LinearStateArgs a) {
-  const int bh = blockIdx.x, dd = a.d * a.d;
-  const int e = blockIdx.y * 256 + threadIdx.x;
+// Grid (BH, d * d / 512): four state elements a thread through the cuts of
+// the head in order; a run's own sum is replaced by the state at its cut.
+constexpr int kScanThreads = 128;
+__global__ void __launch_bounds__(kScanThreads) polar_linear_scan_kernel(const LinearStateArgs a) {
+  const int bh = blockIdx.x, dd = a.d * a.d, per = a.split.per;
+  const long long h0 = (long long)bh * a.split.tiles, h1 = h0 + a.split.tiles;
+  // boundaries k * per strictly inside the head
+  const long long k0 = h0 / per + 1, k1 = (h1 - 1) / per;
+  const int cuts = (int)(k1 - k0 + 1);
+  const int e = (blockIdx.y * kScanThreads + threadIdx.x) * 4;
+  if (a.init_copy)
+    *reinterpret_cast<float4*>(a.init_copy + (size_t)bh * dd + e) =
+        *reinterpret_cast<const float4*>(a.init + (size_t)bh * dd + e);
+  if (cuts < 1) return;
   const int len = linear_length(a.lengths, bh / a.H, a.T, nullptr);
   const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
-  float m = a.init ? a.init[(size_t)bh * dd + e] : 0.f;
-  float* seg = a.seg_states + (size_t)bh * a.nseg * dd + e;
-  const float whole = linear_power(l2, a.seg_tokens);
+  float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.init) m = *reinterpret_cast<const float4*>(a.init + (size_t)bh * dd + e);
+  // forward: boundary k closes run k - 1; reverse: it opens run k
+  auto slot = [&](int i) {
+    const long long run = a.reverse ? k1 - i : k0 + i - 1;
+    return reinterpret_cast<float4*>(a.cuts + (size_t)run * dd + e);
+  };
   constexpr int kU = 8;
-  for (int s0 = 0; s0 < a.nseg; s0 += kU) {
-    float own[kU];
+  for (int i0 = 0; i0 < cuts; i0 += kU) {
+    float4 own[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      own[u] = i0 + u < cuts ? __ldcg(slot(i0 + u)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int s = a.reverse ? a.nseg - 1 - (s0 + u) : s0 + u;
-      own[u] = s0 + u < a.nseg ? seg[(size_t)s * dd] : 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      if (s0 + u >= a.nseg) break;
-      const int s = a.reverse ? a.nseg - 1 - (s0 + u) : s0 + u;
-      const int n = min(max(len - s * a.seg_tokens, 0), a.seg_tokens);
-      seg[(size_t)s * dd] = m;
-      const float g = n == a.seg_tokens ? whole : linear_power(l2, n);
-      m = fmaf(g, m, own[u]);
+      if (i0 + u < cuts) {
+        const long long k = a.reverse ? k1 - (i0 + u) : k0 + i0 + u;  // the boundary
+        const long long lo = a.reverse ? k * per : max(h0, (k - 1) * per);
+        const long long hi = a.reverse ? min(h1, (k + 1) * per) : k * per;
+        const int ta = (int)(lo - h0) * kLinearTile, tb = (int)(hi - h0) * kLinearTile;
+        const float g = linear_power(l2, max(min(len, tb) - ta, 0));
+        m = make_float4(fmaf(g, m.x, own[u].x), fmaf(g, m.y, own[u].y), fmaf(g, m.z, own[u].z),
+                        fmaf(g, m.w, own[u].w));
+        *slot(i0 + u) = m;
+      }
     }
   }
-  if (a.final_state) a.final_state[(size_t)bh * dd + e] = m;
+}
+
+__global__ void __launch_bounds__(256) polar_linear_copy_kernel(const float* init, float* dst,
+                                                                size_t n) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) dst[i] = init ? init[i] : 0.f;
 }
 
 // -------------------------------------------------------------- outputs --
@@ -199,26 +220,36 @@ struct OutSmem {
   float pw[kC + 1];     // powers of g
 };
 
-// Grid (BH * nseg, D / kZ): the CTA walks its segment's chunks with its 32
-// rows of the state in shared memory.
+// Grid (parts, D / kZ): the CTA walks its run's chunks with its 32 rows of the
+// state in shared memory.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads)
     polar_linear_out_kernel(const LinearArgs a) {
   using S = StateTile<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   OutSmem<D>& sm = *reinterpret_cast<OutSmem<D>*>(smem_raw);
-  const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg;
+  const int BH = a.B * a.H, part = blockIdx.x;
   const int z0 = blockIdx.y * kZ, tid = threadIdx.x;
-  const int len = linear_length(a.lengths, bh / a.H, a.T, a.status);
-  const int t0 = seg * a.seg_tokens, t1 = min(t0 + a.seg_tokens, a.T);
+  const int tx = tid & 15, ty = tid >> 4;
+  const int n_po = linear_portions(a.split, BH, part);
+  for (int ip = 0; ip < n_po; ++ip) {
+  const LinearPortion po = linear_portion(a.split, BH, a.H, a.T, a.lengths, a.status, part,
+                                          a.reverse ? n_po - 1 - ip : ip);
+  const int bh = po.bh, len = po.len;
+  const int t0 = po.row(po.first), t1 = min(po.row(po.last), a.T);
   const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
   const T* x = static_cast<const T*>(a.x) + (size_t)bh * a.T * D;
   const T* y = static_cast<const T*>(a.y) + (size_t)bh * a.T * D;
   const T* z = static_cast<const T*>(a.z) + (size_t)bh * a.T * D;
   T* out = static_cast<T*>(a.out) + (size_t)bh * a.T * D;
+  float* fin = a.final_state && !(a.reverse ? po.cut_left : po.cut_right)
+                   ? a.final_state + (size_t)bh * D * D
+                   : nullptr;
 
-  const float* st = a.seg_states ? a.seg_states + (size_t)blockIdx.x * D * D
-                                 : (a.init ? a.init + (size_t)bh * D * D : nullptr);
+  const float* st = (a.reverse ? po.cut_right : po.cut_left)
+                        ? a.cuts + (size_t)(a.reverse ? part + 1 : part - 1) * D * D
+                        : (a.init ? a.init + (size_t)bh * D * D : nullptr);
+  __syncthreads();  // the last portion's reads are done
   for (int i = tid; i < kZ * D; i += kThreads) {
     const int r = a.state_t ? i % kZ : i / D, c = a.state_t ? i / kZ : i % D;
     float v = 0.f;
@@ -229,7 +260,6 @@ __global__ void __launch_bounds__(kThreads)
   // forward: the output scale applies to the state's part too; reverse: the
   // state already carries it
   const float s_in = a.reverse ? 1.f : a.scale, s_z = a.reverse ? a.scale : 1.f;
-  const int tx = tid & 15, ty = tid >> 4;
   const int n_ch = (t1 - t0 + kC - 1) / kC;
   for (int ci = 0; ci < n_ch; ++ci) {
     const int c0 = t0 + (a.reverse ? n_ch - 1 - ci : ci) * kC;
@@ -328,7 +358,7 @@ __global__ void __launch_bounds__(kThreads)
         store2(out + (size_t)(c0 + i) * D + z0 + 2 * tx, i < n ? o[ii][0] : 0.f,
                i < n ? o[ii][1] : 0.f);
     }
-    if (n > 0 && ci + 1 < n_ch) {
+    if (n > 0 && (ci + 1 < n_ch || fin)) {
       __syncthreads();  // every read of the state is done
       float4 acc[S::kR];
       const float g = sm.pw[n];
@@ -342,6 +372,12 @@ __global__ void __launch_bounds__(kThreads)
       for (int r = 0; r < S::kR; ++r)
         *reinterpret_cast<float4*>(&sm.m[S::row0() + r][S::col0()]) = acc[r];
     }
+  }
+  if (fin) {
+    __syncthreads();
+    for (int i = tid; i < kZ * D; i += kThreads)
+      fin[(size_t)(z0 + i / D) * D + i % D] = sm.m[i / D][i % D];
+  }
   }
 }
 
@@ -398,7 +434,8 @@ cudaError_t step_d(const LinearStepArgs& a, cudaStream_t s) {
 
 template <int D, typename T>
 cudaError_t states_d(const LinearStateArgs& a, cudaStream_t s) {
-  polar_linear_state_kernel<D, T><<<dim3((unsigned)a.B * a.H * a.nseg, D / kZ), kThreads, 0, s>>>(a);
+  polar_linear_state_kernel<D, T>
+      <<<dim3((unsigned)a.split.parts, D / kZ), kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -409,7 +446,7 @@ cudaError_t out_d(const LinearArgs& a, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   polar_linear_out_kernel<D, T>
-      <<<dim3((unsigned)a.B * a.H * a.nseg, D / kZ), kThreads, smem, s>>>(a);
+      <<<dim3((unsigned)a.split.parts, D / kZ), kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -420,7 +457,14 @@ cudaError_t launch_linear_states(const LinearStateArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s) {
-  polar_linear_scan_kernel<<<dim3((unsigned)a.B * a.H, a.d * a.d / 256), 256, 0, s>>>(a);
+  polar_linear_scan_kernel<<<dim3((unsigned)a.B * a.H, a.d * a.d / (4 * kScanThreads)),
+                             kScanThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_copy_state(const float* init, float* final_state, size_t n,
+                                     cudaStream_t s) {
+  polar_linear_copy_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(init, final_state, n);
   return cudaGetLastError();
 }
 

@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "polar_internal.h"
+
 namespace polar {
 
 // Tokens of sequence b: lengths[b] clamped to [0, T] (all T without lengths);
@@ -25,6 +27,43 @@ __device__ __forceinline__ float linear_log2_decay(const float* log_decay, int h
 // g^n for n >= 0.  The product's rounding moves the result by 2^-24 |n l2|
 // relative: a power that still weighs (above 2^-24) is right to 1e-6.
 __device__ __forceinline__ float linear_power(float l2, int n) { return exp2f(l2 * (float)n); }
+
+// The tiles of one head that one run holds.
+struct LinearPortion {
+  int bh;
+  int first, last;  // tiles [first, last) of the head
+  int len;          // tokens of the sequence
+  int live;         // tiles of the portion that hold tokens: [first, first + live)
+  bool cut_left, cut_right;  // the run's boundary cuts the head there
+  __device__ __forceinline__ int row(int tile) const { return tile * kLinearTile; }
+  __device__ __forceinline__ int tokens(int tile) const {
+    return min(kLinearTile, len - tile * kLinearTile);
+  }
+};
+
+// Number of heads that run `part` touches, and the i-th of them in order.
+__device__ __forceinline__ int linear_portions(const LinearSplit& s, int BH, int part) {
+  const long long i0 = (long long)part * s.per;
+  const long long i1 = min(i0 + s.per, (long long)BH * s.tiles);
+  return (int)((i1 - 1) / s.tiles - i0 / s.tiles) + 1;
+}
+__device__ __forceinline__ LinearPortion linear_portion(const LinearSplit& s, int BH, int H, int T,
+                                                        const int* lengths, int* status, int part,
+                                                        int i) {
+  const long long i0 = (long long)part * s.per;
+  const long long i1 = min(i0 + s.per, (long long)BH * s.tiles);
+  LinearPortion p;
+  p.bh = (int)(i0 / s.tiles) + i;
+  const long long h0 = (long long)p.bh * s.tiles;
+  p.first = (int)(i0 > h0 ? i0 - h0 : 0);
+  p.last = (int)(i1 < h0 + s.tiles ? i1 - h0 : s.tiles);
+  p.cut_left = p.first > 0;
+  p.cut_right = p.last < s.tiles;
+  p.len = linear_length(lengths, p.bh / H, T, status);
+  const int end = min(p.last, (p.len + kLinearTile - 1) / kLinearTile);
+  p.live = max(end - p.first, 0);
+  return p;
+}
 
 __device__ __forceinline__ float linear_load(const float* p) { return *p; }
 __device__ __forceinline__ float linear_load(const __nv_bfloat16* p) {

@@ -1,6 +1,7 @@
 // C ABI of the decayed linear attention: argument validation, the split of a
 // sequence into segments, and the launches.  The contract of every entry
 // point is in include/polar_attn.h, the mathematics in polar_linear.cu.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -12,34 +13,24 @@ namespace polar {
 
 namespace {
 
-struct Segments {
-  int nseg, seg_tokens;
-};
-
-// Segments per sequence.  One segment per head needs no state pass but leaves
-// SMs idle when heads are few; with n > 1 every CTA walks 1/n of the tiles at
-// one and a half times the cost a tile (the state pass reads y and z once
-// more), plus a tile's time for the start and about four for the two extra
-// launches.  The count with the least cost over whole waves is taken.
-Segments segments(int BH, int T, int d, int dtype, int sms) {
-  const int tiles = (T + kLinearTile - 1) / kLinearTile;
-  if (tiles < 1) return {0, kLinearTile};
-  const long long per_seg = dtype == POLAR_BF16 ? 1 : d / 32;  // CTAs per segment
-  const long long slots = dtype == POLAR_BF16 ? sms : 2ll * sms;
-  long long best = 1;
-  double best_cost = 1e300;
-  for (long long n = 1; n <= tiles && n <= 1024; ++n) {
-    const long long per = (tiles + n - 1) / n;
-    const long long real = (tiles + per - 1) / per;
-    const double waves = (double)((BH * real * per_seg + slots - 1) / slots);
-    const double cost = n == 1 ? waves * (per + 1) : waves * 1.5 * (per + 1) + 4;
-    if (cost < best_cost - 1e-9) {
-      best_cost = cost;
-      best = n;
-    }
-  }
-  const int per = (int)((tiles + best - 1) / best);
-  return {(tiles + per - 1) / per, per * kLinearTile};
+// Runs of tiles.  Whole heads to a CTA need one launch and read every row
+// once, but leave SMs idle when heads are few.  Equal runs over all slots
+// cut heads: y and z of what lies before a cut are read a second time (about
+// 0.45 of a tile's time), and the state and scan launches cost about four
+// tiles' time.  The cheaper of the two is taken.
+LinearSplit split(int BH, int T, int d, int dtype, int sms) {
+  LinearSplit r;
+  r.tiles = (T + kLinearTile - 1) / kLinearTile;
+  const long long n = (long long)BH * r.tiles;
+  // CTAs at once: one a SM on the tensor cores; fp32 two, d / 32 to a run
+  const long long slots = dtype == POLAR_BF16 ? sms : std::max(1, 2 * sms / (d / 32));
+  const long long whole = r.tiles * ((BH + slots - 1) / slots);
+  const long long even = (n + slots - 1) / slots;
+  r.per = (int)((double)whole <= 1.45 * (double)even + 4.0 ? whole : even);
+  if (r.per < 1) r.per = 1;
+  r.parts = (int)((n + r.per - 1) / r.per);
+  r.cut = r.per % std::max(r.tiles, 1) != 0;
+  return r;
 }
 
 bool sizes_ok(int B, int H, int T, int d, int dtype) {
@@ -55,11 +46,18 @@ int check_sizes(int B, int H, int T, int d, int dtype, float scale) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-size_t state_bytes(int B, int H, int T, int d, int dtype) {
+// A state a cut, and one a head for a copy of the incoming states: the CTA
+// that ends a cut head may write state_out over the state_in that the CTA of
+// its start has yet to read.
+size_t cut_floats(const LinearSplit& g, int d) { return (size_t)g.parts * d * d; }
+size_t cut_bytes(const LinearSplit& g, int BH, int d) {
+  return g.cut ? (cut_floats(g, d) + (size_t)BH * d * d) * sizeof(float) : 0;
+}
+
+size_t workspace_bytes_of(int B, int H, int T, int d, int dtype) {
   int sms = 0;
   if (check_device(&sms) != POLAR_OK) sms = 148;
-  const Segments g = segments(B * H, T, d, dtype, sms);
-  return (size_t)B * H * g.nseg * d * d * sizeof(float);
+  return B * H > 0 && T > 0 ? cut_bytes(split(B * H, T, d, dtype, sms), B * H, d) : 0;
 }
 
 // bf16 runs on the tensor cores, fp32 on the FP32 pipes.
@@ -97,12 +95,12 @@ extern "C" {
 
 size_t polar_linear_workspace_bytes(int B, int H, int T, int d, int dtype) {
   if (!sizes_ok(B, H, T, d, dtype)) return 0;
-  return state_bytes(B, H, T, d, dtype);
+  return workspace_bytes_of(B, H, T, d, dtype);
 }
 
 size_t polar_linear_bwd_workspace_bytes(int B, int H, int T, int d, int dtype) {
   if (!sizes_ok(B, H, T, d, dtype)) return 0;
-  return 2 * state_bytes(B, H, T, d, dtype);
+  return 2 * workspace_bytes_of(B, H, T, d, dtype);
 }
 
 int polar_linear_fwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -119,27 +117,26 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   int sms = 0;
   st = check_device(&sms);
   if (st != POLAR_OK) return st;
-  const Segments g = segments(B * H, T, d, dtype, sms);
-  const size_t need = (size_t)B * H * g.nseg * d * d * sizeof(float);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cuda_status("linear state copy", launch_linear_copy_state(
+                                                state_in, state_out, (size_t)B * H * d * d, s));
+  const LinearSplit g = split(B * H, T, d, dtype, sms);
+  const size_t need = cut_bytes(g, B * H, d);
   if (need && (!workspace || workspace_bytes < need)) return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
   int* status = status_word();
   if (!status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* seg = static_cast<float*>(workspace);
-  // The tensor-core kernel writes the state of a whole sequence itself.
-  const bool tc = dtype == POLAR_BF16;
-  const bool walked = g.nseg > 1 || (state_out && !(tc && g.nseg == 1));
-  if (walked) {
+  float* cuts = static_cast<float*>(workspace);
+  float* copy = g.cut && state_in && state_in == state_out ? cuts + cut_floats(g, d) : nullptr;
+  if (g.cut) {
     const LinearStateArgs a{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
-                            g.nseg, g.seg_tokens, state_in, seg, state_out, status};
-    st = T > 0 ? run_states(a, dtype, s) : cuda_status("linear scan launch", launch_linear_scan(a, s));
+                            g, state_in, cuts, status, copy};
+    st = run_states(a, dtype, s);
     if (st != POLAR_OK) return st;
   }
-  if (T == 0) return POLAR_OK;
   const LinearArgs a{q, k, v, mem, log_decay, lengths, B, H, T, d, scale, false, false,
-                     g.nseg, g.seg_tokens, state_in, walked ? seg : nullptr, status,
-                     walked ? nullptr : state_out};
+                     g, copy ? copy : state_in, cuts, state_out, status};
   return run_out(a, dtype, s);
 }
 
@@ -177,40 +174,36 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   int sms = 0;
   st = check_device(&sms);
   if (st != POLAR_OK) return st;
-  const Segments g = segments(B * H, T, d, dtype, sms);
-  const size_t one = (size_t)B * H * g.nseg * d * d;
-  const size_t need = 2 * one * sizeof(float);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cuda_status("linear state copy",
+                       launch_linear_copy_state(dstate_out, dstate_in, (size_t)B * H * d * d, s));
+  const LinearSplit g = split(B * H, T, d, dtype, sms);
+  const size_t one = cut_bytes(g, B * H, d), need = 2 * one;
   if (need && (!workspace || workspace_bytes < need)) return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
   int* status = status_word();
   if (!status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* seg_s = static_cast<float*>(workspace);
-  float* seg_r = seg_s + one;
-  const bool tc = dtype == POLAR_BF16;
-  if (g.nseg > 1) {
-    const LinearStateArgs a{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
-                            g.nseg, g.seg_tokens, state_in, seg_s, nullptr, status};
-    st = run_states(a, dtype, s);
+  float* cuts_s = static_cast<float*>(workspace);
+  float* cuts_r = cuts_s + one / sizeof(float);
+  float* copy =
+      g.cut && dstate_out && dstate_out == dstate_in ? cuts_r + cut_floats(g, d) : nullptr;
+  if (g.cut) {
+    const LinearStateArgs as{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
+                             g, state_in, cuts_s, status, nullptr};
+    const LinearStateArgs ar{q, dmem, log_decay, lengths, B, H, T, d, scale, true,
+                             g, dstate_out, cuts_r, status, copy};
+    st = run_states(as, dtype, s);
+    if (st == POLAR_OK) st = run_states(ar, dtype, s);
     if (st != POLAR_OK) return st;
   }
-  const bool walked = g.nseg > 1 || (dstate_in && !(tc && g.nseg == 1));
-  if (walked) {
-    const LinearStateArgs a{q, dmem, log_decay, lengths, B, H, T, d, scale, true,
-                            g.nseg, g.seg_tokens, dstate_out, seg_r, dstate_in, status};
-    st = T > 0 ? run_states(a, dtype, s) : cuda_status("linear scan launch", launch_linear_scan(a, s));
-    if (st != POLAR_OK) return st;
-  }
-  if (T == 0) return POLAR_OK;
-  const float* before_r = walked ? seg_r : nullptr;
   const LinearArgs aq{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
-                      g.nseg, g.seg_tokens, state_in, g.nseg > 1 ? seg_s : nullptr, status};
+                      g, state_in, cuts_s, nullptr, status};
   const LinearArgs ak{v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
-                      g.nseg, g.seg_tokens, dstate_out, before_r, status};
+                      g, dstate_out, cuts_r, nullptr, status};
   // last: it may write dstate_in over dstate_out, which dk's kernel reads
   const LinearArgs av{k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
-                      g.nseg, g.seg_tokens, dstate_out, before_r, status,
-                      walked ? nullptr : dstate_in};
+                      g, copy ? copy : dstate_out, cuts_r, dstate_in, status};
   for (const LinearArgs* a : {&aq, &ak, &av}) {
     st = run_out(*a, dtype, s);
     if (st != POLAR_OK) return st;

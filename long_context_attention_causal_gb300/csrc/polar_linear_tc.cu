@@ -1,7 +1,7 @@
 // Decayed linear attention of bf16 tensors on the tensor cores.
 //
 // The mathematics (chunks, the state before them, the two directions, the
-// segments) is in polar_linear.cu; a chunk here is a tile of 128 tokens.
+// runs and cuts) is in polar_linear.cu; a chunk here is a tile of 128 tokens.
 // Per tile, with x, y, z its rows, M the state before it (z dim x y dim) and
 // w_j the powers of the decay:
 //   S  = x y^T                 scores            A, B in shared memory
@@ -42,14 +42,14 @@ constexpr uint32_t kColS = 0, kColO1 = 128, kColO2 = 256, kColDS = 384;
 
 struct OutBars {
   uint64_t full_xy[2], full_z[2], empty_x[2], empty_yz[2];
-  uint64_t s_full, p_full, o_full, o_free;      // one phase a tile
-  uint64_t y_hi, y_lo, hi_done, ds_full, m_op;  // m_op: one phase a tile, the first before it
-  uint64_t fixed;                               // once: rows past the sequence are zeroed
+  uint64_t s_full, p_full, o_full, o_free, m_op;  // one phase a tile (m_op before it)
+  uint64_t y_hi, y_lo, hi_done, ds_full;          // one phase a state update
+  uint64_t fixed;  // one phase a tile with rows past the sequence: they are zeroed
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  float full_pw[32];   // g^31 .. g^0 (forward), g^0 .. g^31 (reverse)
-  float diag_pw[64];   // 31 zeros, then g^0 .. g^31
+  float full_pw[2][32];  // g^31 .. g^0 (forward), g^0 .. g^31 (reverse); by portion parity
+  float diag_pw[2][64];  // 31 zeros, then g^0 .. g^31
 };
 
 template <int D>
@@ -69,11 +69,11 @@ struct OutLayout {
 struct OutParams {
   const float* log_decay;
   const int* lengths;
-  const float* init;        // state at the sequence's start or end, or null
-  const float* seg_states;  // per segment, or null
-  float* final_state;       // or null (one segment per sequence only)
+  const float *init, *cuts;  // see LinearArgs
+  float* final_state;
   __nv_bfloat16* out;
-  int H, T, nseg, seg_tokens, state_t;
+  int BH, H, T, state_t;
+  LinearSplit split;
   float scale;
   int* status;
 };
@@ -133,7 +133,9 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int n, int tid) {
     if (((i >> 3) & (kTok - 1)) >= n) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
 }
 
-// One (b, h) segment a CTA.  kRev: from the last tile back.
+// One run of tiles a CTA.  kRev: from the last tile back.  Every role walks
+// the same portions and tiles; it counts tiles (k), state updates (ku) and
+// tiles with rows to zero (kf) for the phases of the barriers.
 template <int D, bool kRev>
 __global__ void __launch_bounds__(kThreads, 1)
     polar_linear_out_tc_kernel(const __grid_constant__ CUtensorMap map_x,
@@ -146,13 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   OutBars& br = *reinterpret_cast<OutBars*>(smem + L::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
-  const int len = linear_length(p.lengths, bh / p.H, p.T, p.status);
-  const int t0 = seg * p.seg_tokens, t1 = min(t0 + p.seg_tokens, p.T);
-  const int tokens = min(max(len - t0, 0), t1 - t0);  // of this segment
-  const int nt = (tokens + kTok - 1) / kTok;          // tiles that hold any
-  const float l2 = linear_log2_decay(p.log_decay, bh % p.H);
-  const bool final = p.final_state != nullptr;
+  const int n_po = linear_portions(p.split, p.BH, blockIdx.x);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -165,32 +161,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&br.p_full, 4);
     mbar_init(&br.o_full, 1);
     mbar_init(&br.o_free, 4);
+    mbar_init(&br.m_op, kStateWarps);
     mbar_init(&br.y_hi, kStateWarps);
     mbar_init(&br.y_lo, kStateWarps);
     mbar_init(&br.hi_done, 1);
     mbar_init(&br.ds_full, 1);
-    mbar_init(&br.m_op, kStateWarps);
     mbar_init(&br.fixed, kStateWarps);
     mbar_init(&br.drain, 1);
     br.abort_flag = 0;
     fence_barrier_init();
   }
-  if (threadIdx.x < 32) br.full_pw[threadIdx.x] = linear_power(l2, kRev ? lane : 31 - lane);
-  if (threadIdx.x < 64)
-    br.diag_pw[threadIdx.x] = threadIdx.x < 31 ? 0.f : linear_power(l2, (int)threadIdx.x - 31);
   if (warp == kWarpMMA) tmem_alloc(&br.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = br.tmem_base;
   volatile int* abort_flag = &br.abort_flag;
-  // tile of step c, its first token, and the tokens it holds
-  auto tile_row = [&](int c) { return t0 + (kRev ? nt - 1 - c : c) * kTok; };
-  auto tile_n = [&](int c) { return min(kTok, t0 + tokens - tile_row(c)); };
+  auto portion = [&](int i) {
+    return linear_portion(p.split, p.BH, p.H, p.T, p.lengths, p.status, blockIdx.x,
+                          kRev ? n_po - 1 - i : i);
+  };
+  // the c-th live tile of a portion
+  auto tile_of = [](const LinearPortion& po, int c) {
+    return po.first + (kRev ? po.live - 1 - c : c);
+  };
   // rows past the sequence, but inside the tensor, must be zeroed
-  auto ragged = [&](int c) { return tile_n(c) < kTok && tile_row(c) + tile_n(c) < p.T; };
-  // the state after step c is read by step c + 1, or is the final one
-  auto updates = [&](int c) { return c + 1 < nt || final; };
+  auto ragged = [&](int tile, int n) { return n < kTok && tile * kTok + n < p.T; };
+  // the portion holds the head's last tile in walking order
+  auto is_final = [&](const LinearPortion& po) {
+    return p.final_state != nullptr && !(kRev ? po.cut_left : po.cut_right);
+  };
+  // the state after tile c is read by tile c + 1, or is the final one
+  auto updates = [&](const LinearPortion& po, int c) { return c + 1 < po.live || is_final(po); };
 
   if (warp == kWarpTMA) {
     // ------------------------------------------------------ TMA producer --
@@ -200,34 +202,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map_z);
     }
     __syncwarp();
-    int issued = 0;
+    int k = 0;
     bool ok = true;
-    for (int c = 0; c < nt && ok; ++c) {
-      const int st = c & 1;
-      if (c >= 2) {
-        ok = mbar_wait_warp(&br.empty_yz[st], (uint32_t)(c / 2 - 1) & 1, abort_flag, p.status);
-        if (ok)
-          ok = mbar_wait_warp(&br.empty_x[st], (uint32_t)(c / 2 - 1) & 1, abort_flag, p.status);
+    for (int ip = 0; ip < n_po && ok; ++ip) {
+      const LinearPortion po = portion(ip);
+      for (int c = 0; c < po.live; ++c, ++k) {
+        const int st = k & 1, row = po.row(tile_of(po, c));
+        if (k >= 2) {
+          const uint32_t ph = (uint32_t)(k / 2 - 1) & 1;
+          ok = mbar_wait_warp(&br.empty_yz[st], ph, abort_flag, p.status) &&
+               mbar_wait_warp(&br.empty_x[st], ph, abort_flag, p.status);
+          if (!ok) break;
+        }
+        uint8_t* sx = smem + st * L::kStage;
+        mbar_arrive_expect_tx_warp(&br.full_xy[st], 2 * L::kTile);
+        for (int h = 0; h < D / 64; ++h) {
+          tma_load_3d_warp(sx + h * L::kAtom, &map_x, &br.full_xy[st], 64 * h, row, po.bh);
+          tma_load_3d_warp(sx + L::kTile + h * L::kAtom, &map_y, &br.full_xy[st], 64 * h, row,
+                           po.bh);
+        }
+        mbar_arrive_expect_tx_warp(&br.full_z[st], L::kTile);
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_3d_warp(sx + 2 * L::kTile + h * L::kAtom, &map_z, &br.full_z[st], 64 * h, row,
+                           po.bh);
       }
-      if (!ok) break;
-      uint8_t* sx = smem + st * L::kStage;
-      mbar_arrive_expect_tx_warp(&br.full_xy[st], 2 * L::kTile);
-      for (int h = 0; h < D / 64; ++h) {
-        tma_load_3d_warp(sx + h * L::kAtom, &map_x, &br.full_xy[st], 64 * h, tile_row(c), bh);
-        tma_load_3d_warp(sx + L::kTile + h * L::kAtom, &map_y, &br.full_xy[st], 64 * h,
-                         tile_row(c), bh);
-      }
-      mbar_arrive_expect_tx_warp(&br.full_z[st], L::kTile);
-      for (int h = 0; h < D / 64; ++h)
-        tma_load_3d_warp(sx + 2 * L::kTile + h * L::kAtom, &map_z, &br.full_z[st], 64 * h,
-                         tile_row(c), bh);
-      issued = c + 1;
     }
     if (!ok) {
       // aborted: let the copies already issued land before the CTA exits
       volatile int never = 0;
       const long long lim = kWaitLimitCycles / 4;
-      for (int c = issued - 1; c >= 0 && c >= issued - 2; --c) {
+      for (int c = k - 1; c >= 0 && c >= k - 2; --c) {
         mbar_wait(&br.full_xy[c & 1], (uint32_t)(c / 2) & 1, &never, p.status, lim);
         mbar_wait(&br.full_z[c & 1], (uint32_t)(c / 2) & 1, &never, p.status, lim);
       }
@@ -246,67 +250,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t km = smem_desc_sw128(base, 16, 1024);
     const uint64_t mn = smem_desc_sw128(base, lbo, 1024);
     const uint64_t m_desc = smem_desc_sw128(base + L::kMOff, 16, 1024);
-    bool any = false;
     auto at = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
     auto kstep = [&](int kk, uint32_t atom) { return at((kk >> 2) * atom) + (uint64_t)(kk & 3) * 2; };
-    auto issue_s = [&](int c) -> bool {
-      if (!mbar_wait_warp(&br.full_xy[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status))
-        return false;
-      if (ragged(c) && !mbar_wait_warp(&br.fixed, 0, abort_flag, p.status)) return false;
-      tc_fence_after();
-      const uint64_t x0 = km + at((c & 1) * L::kStage), y0 = x0 + at(L::kTile);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        umma_ss_warp(tmem + kColS, x0 + kstep(kk, L::kAtom), y0 + kstep(kk, L::kAtom), kIdS,
-                     kk > 0);
-      umma_commit_warp(&br.s_full);
-      any = true;
-      return true;
-    };
-    auto issue_o2 = [&](int c) -> bool {
-      if (!mbar_wait_warp(&br.m_op, (uint32_t)c & 1, abort_flag, p.status)) return false;
-      if (c > 0 && !mbar_wait_warp(&br.o_free, (uint32_t)(c - 1) & 1, abort_flag, p.status))
-        return false;
-      tc_fence_after();
-      const uint64_t x0 = km + at((c & 1) * L::kStage);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        umma_ss_warp(tmem + kColO2, x0 + kstep(kk, L::kAtom), m_desc + kstep(kk, L::kMAtom), kIdO2,
-                     kk > 0);
-      return true;
-    };
-    auto issue_ds = [&](int c, bool add) {
-      const uint64_t y0 = mn + at((c & 1) * L::kStage + L::kTile), z0 = y0 + at(L::kTile);
+    auto issue_ds = [&](int st, bool add) {
+      const uint64_t y0 = mn + at(st * L::kStage + L::kTile), z0 = y0 + at(L::kTile);
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
         umma_ss_warp(tmem + kColDS, z0 + at(kk * 2048), y0 + at(kk * 2048), kIdDS,
                      (add || kk > 0) ? 1u : 0u);
     };
-    bool ok = nt == 0 || (issue_s(0) && issue_o2(0));
-    for (int c = 0; c < nt && ok; ++c) {
-      ok = mbar_wait_warp(&br.full_z[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status) &&
-           mbar_wait_warp(&br.p_full, (uint32_t)c & 1, abort_flag, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t z0 = mn + at((c & 1) * L::kStage + 2 * L::kTile);
+    int k = 0, ku = 0, kf = 0;
+    bool ok = true, any = false;
+    for (int ip = 0; ip < n_po && ok; ++ip) {
+      const LinearPortion po = portion(ip);
+      for (int c = 0; c < po.live; ++c, ++k) {
+        const int st = k & 1, tile = tile_of(po, c);
+        const uint32_t ph = (uint32_t)k & 1, ph2 = (uint32_t)(k / 2) & 1;
+        // scores: over P of the tile before, whose product is issued already
+        ok = mbar_wait_warp(&br.full_xy[st], ph2, abort_flag, p.status);
+        if (ok && ragged(tile, po.tokens(tile)))
+          ok = mbar_wait_warp(&br.fixed, (uint32_t)(kf++) & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t x0 = km + at(st * L::kStage), y0 = x0 + at(L::kTile);
 #pragma unroll
-      for (int kk = 0; kk < kTok / 16; ++kk)
-        umma_ts_warp(tmem + kColO1, tmem + kColS + kk * 8, z0 + at(kk * 2048), kIdO1, kk > 0);
-      umma_commit_warp(&br.o_full);  // O2 of this tile was issued before
-      if (updates(c)) {
-        ok = mbar_wait_warp(&br.y_hi, (uint32_t)c & 1, abort_flag, p.status);
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss_warp(tmem + kColS, x0 + kstep(kk, L::kAtom), y0 + kstep(kk, L::kAtom), kIdS,
+                       kk > 0);
+        umma_commit_warp(&br.s_full);
+        any = true;
+        // O2, once the state is written and the last outputs are read
+        ok = mbar_wait_warp(&br.m_op, ph, abort_flag, p.status);
+        if (ok && k > 0) ok = mbar_wait_warp(&br.o_free, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        issue_ds(c, false);
-        umma_commit_warp(&br.hi_done);
-        ok = mbar_wait_warp(&br.y_lo, (uint32_t)c & 1, abort_flag, p.status);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss_warp(tmem + kColO2, x0 + kstep(kk, L::kAtom), m_desc + kstep(kk, L::kMAtom),
+                       kIdO2, kk > 0);
+        // O1
+        ok = mbar_wait_warp(&br.full_z[st], ph2, abort_flag, p.status) &&
+             mbar_wait_warp(&br.p_full, ph, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        issue_ds(c, true);
-        umma_commit_warp(&br.ds_full);
+        const uint64_t z0 = mn + at(st * L::kStage + 2 * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk)
+          umma_ts_warp(tmem + kColO1, tmem + kColS + kk * 8, z0 + at(kk * 2048), kIdO1, kk > 0);
+        umma_commit_warp(&br.o_full);
+        if (updates(po, c)) {
+          const uint32_t pu = (uint32_t)(ku++) & 1;
+          ok = mbar_wait_warp(&br.y_hi, pu, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_ds(st, false);
+          umma_commit_warp(&br.hi_done);
+          ok = mbar_wait_warp(&br.y_lo, pu, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_ds(st, true);
+          umma_commit_warp(&br.ds_full);
+        }
+        umma_commit_warp(&br.empty_yz[st]);
       }
-      umma_commit_warp(&br.empty_yz[c & 1]);
-      if (c + 1 < nt) ok = issue_s(c + 1) && issue_o2(c + 1);
     }
     if (!ok && any) {
       // aborted: wait for the products in flight before TMEM is released
@@ -321,128 +327,138 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x;  // row of the tile
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + kColS;
-    for (int c = 0; c < nt; ++c) {
-      const int n = tile_n(c);
-      bool ok = __all_sync(0xffffffffu,
-                           mbar_wait(&br.s_full, (uint32_t)c & 1, abort_flag, p.status));
-      if (ok) {
-        tc_fence_after();
-        // 32-column blocks of this warp's rows: whole before the diagonal one
-        // (after it in reverse), zero beyond it
+    int k = 0;
+    bool go = true;
+    for (int ip = 0; ip < n_po && go; ++ip) {
+      const LinearPortion po = portion(ip);
+      const float l2 = linear_log2_decay(p.log_decay, po.bh % p.H);
+      // powers of the head's decay; two sets, so that a warp still in the last
+      // portion keeps its own (every tile ends in a barrier of these warps)
+      float* full_pw = br.full_pw[ip & 1];
+      float* diag_pw = br.diag_pw[ip & 1];
+      if (r < 32) full_pw[r] = linear_power(l2, kRev ? r : 31 - r);
+      if (r < 64) diag_pw[r] = r < 31 ? 0.f : linear_power(l2, r - 31);
+      go = out_bar_and(true);
+      for (int c = 0; c < po.live; ++c, ++k) {
+        const int st = k & 1, tile = tile_of(po, c), n = po.tokens(tile);
+        const uint32_t ph = (uint32_t)k & 1;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(&br.s_full, ph, abort_flag, p.status));
+        if (ok) {
+          tc_fence_after();
+          // 32-column blocks of this warp's rows: whole before the diagonal
+          // one (after it in reverse), zero beyond it
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          uint32_t pk[16];
-          if (b == warp) {
-            uint32_t v[32];
-            tmem_ld32(s_tm + 32 * b, v);
-            tmem_ld_wait();
-            reg_fence32(v);
+          for (int b = 0; b < 4; ++b) {
+            uint32_t pk[16];
+            if (b == warp) {
+              uint32_t v[32];
+              tmem_ld32(s_tm + 32 * b, v);
+              tmem_ld_wait();
+              reg_fence32(v);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float f[2];
+              for (int e = 0; e < 32; e += 2) {
+                float f[2];
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int dist = kRev ? e + u - lane : lane - e - u;
-                const float w = p.scale * br.diag_pw[31 + dist];
-                f[u] = dist >= 0 ? __uint_as_float(v[e + u]) * w : 0.f;
+                for (int u = 0; u < 2; ++u) {
+                  const int dist = kRev ? e + u - lane : lane - e - u;
+                  const float w = p.scale * diag_pw[31 + dist];
+                  f[u] = dist >= 0 ? __uint_as_float(v[e + u]) * w : 0.f;
+                }
+                pk[e / 2] = pack_bf16x2(f[0], f[1]);
               }
-              pk[e / 2] = pack_bf16x2(f[0], f[1]);
-            }
-          } else if (kRev ? b > warp : b < warp) {
-            uint32_t v[32];
-            tmem_ld32(s_tm + 32 * b, v);
-            const float rf = p.scale * linear_power(l2, kRev ? 32 * b - r : r - 32 * b - 31);
-            tmem_ld_wait();
-            reg_fence32(v);
+            } else if (kRev ? b > warp : b < warp) {
+              uint32_t v[32];
+              tmem_ld32(s_tm + 32 * b, v);
+              const float rf = p.scale * linear_power(l2, kRev ? 32 * b - r : r - 32 * b - 31);
+              tmem_ld_wait();
+              reg_fence32(v);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 w = *reinterpret_cast<const float4*>(&br.full_pw[e]);
-              pk[e / 2] = pack_bf16x2(__uint_as_float(v[e]) * (w.x * rf),
-                                      __uint_as_float(v[e + 1]) * (w.y * rf));
-              pk[e / 2 + 1] = pack_bf16x2(__uint_as_float(v[e + 2]) * (w.z * rf),
-                                          __uint_as_float(v[e + 3]) * (w.w * rf));
-            }
-          } else {
+              for (int e = 0; e < 32; e += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(&full_pw[e]);
+                pk[e / 2] = pack_bf16x2(__uint_as_float(v[e]) * (w.x * rf),
+                                        __uint_as_float(v[e + 1]) * (w.y * rf));
+                pk[e / 2 + 1] = pack_bf16x2(__uint_as_float(v[e + 2]) * (w.z * rf),
+                                            __uint_as_float(v[e + 3]) * (w.w * rf));
+              }
+            } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            }
+            // P block b lies over S columns 16 b .. 16 b + 15, read already
+            tmem_st16(s_tm + 16 * b, pk);
           }
-          // P block b lies over S columns 16 b .. 16 b + 15, read already
-          tmem_st16(s_tm + 16 * b, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&br.p_full);
+          ok = __all_sync(0xffffffffu, mbar_wait(&br.o_full, ph, abort_flag, p.status));
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&br.p_full);
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(&br.o_full, (uint32_t)c & 1, abort_flag, p.status));
-      }
-      uint8_t* stage = smem + (c & 1) * L::kStage;  // x's tile: its readers are done
-      if (ok) {
-        tc_fence_after();
-        const bool live = r < n;
-        const float w2 = live ? (kRev ? linear_power(l2, n - 1 - r)
-                                      : p.scale * linear_power(l2, r + 1))
-                              : 0.f;
+        uint8_t* stage = smem + st * L::kStage;  // x's tile: its readers are done
+        if (ok) {
+          tc_fence_after();
+          const bool live = r < n;
+          const float w2 = live ? (kRev ? linear_power(l2, n - 1 - r)
+                                        : p.scale * linear_power(l2, r + 1))
+                                : 0.f;
 #pragma unroll 1
-        for (int b = 0; b < D / 32; ++b) {
-          uint32_t o1[32], o2[32];
-          tmem_ld32(tmem + lane_base + kColO1 + 32 * b, o1);
-          tmem_ld32(tmem + lane_base + kColO2 + 32 * b, o2);
-          tmem_ld_wait();
-          reg_fence32(o1);
-          reg_fence32(o2);
-          if (b == D / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&br.o_free);
-          }
-          uint8_t* line = stage + (b >> 1) * L::kAtom + r * 128;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t o4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 8 * g + 2 * e;
-              const float a0 = fmaf(w2, __uint_as_float(o2[i]), __uint_as_float(o1[i]));
-              const float a1 = fmaf(w2, __uint_as_float(o2[i + 1]), __uint_as_float(o1[i + 1]));
-              o4[e] = live ? pack_bf16x2(a0, a1) : 0u;
+          for (int b = 0; b < D / 32; ++b) {
+            uint32_t o1[32], o2[32];
+            tmem_ld32(tmem + lane_base + kColO1 + 32 * b, o1);
+            tmem_ld32(tmem + lane_base + kColO2 + 32 * b, o2);
+            tmem_ld_wait();
+            reg_fence32(o1);
+            reg_fence32(o2);
+            if (b == D / 32 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&br.o_free);
             }
-            const int ch = (b & 1) * 4 + g;
-            *reinterpret_cast<uint4*>(line + ((ch ^ (r & 7)) << 4)) =
-                make_uint4(o4[0], o4[1], o4[2], o4[3]);
+            uint8_t* line = stage + (b >> 1) * L::kAtom + r * 128;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t o4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int i = 8 * g + 2 * e;
+                const float a0 = fmaf(w2, __uint_as_float(o2[i]), __uint_as_float(o1[i]));
+                const float a1 = fmaf(w2, __uint_as_float(o2[i + 1]), __uint_as_float(o1[i + 1]));
+                o4[e] = live ? pack_bf16x2(a0, a1) : 0u;
+              }
+              const int ch = (b & 1) * 4 + g;
+              *reinterpret_cast<uint4*>(line + ((ch ^ (r & 7)) << 4)) =
+                  make_uint4(o4[0], o4[1], o4[2], o4[3]);
+            }
           }
+          fence_async_smem();
         }
-        fence_async_smem();
+        if (!out_bar_and(ok)) {
+          go = false;
+          break;
+        }
+        if (r == 0) {
+          for (int h = 0; h < D / 64; ++h)
+            tma_store_3d(&map_o, stage + h * L::kAtom, 64 * h, po.row(tile), po.bh);
+          tma_store_commit_wait_read();
+          mbar_arrive(&br.empty_x[st]);
+        }
       }
-      if (!out_bar_and(ok)) break;
-      if (r == 0) {
-        for (int h = 0; h < D / 64; ++h)
-          tma_store_3d(&map_o, stage + h * L::kAtom, 64 * h, tile_row(c), bh);
-        tma_store_commit_wait_read();
-        mbar_arrive(&br.empty_x[c & 1]);
-      }
+      // tiles past the sequence
+      const int t0 = po.row(po.first + po.live), t1 = min(po.row(po.last), p.T);
+      uint4* tail = reinterpret_cast<uint4*>(p.out + ((size_t)po.bh * p.T + t0) * D);
+      for (long long i = r; i < (long long)(t1 - t0) * (D / 8); i += 128)
+        tail[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    // tiles past the sequence
-    uint4* tail = reinterpret_cast<uint4*>(p.out + ((size_t)bh * p.T + t0 + (size_t)nt * kTok) * D);
-    const long long vecs = (long long)(t1 - t0 - nt * kTok) * (D / 8);
-    for (long long i = r; i < vecs; i += 128) tail[i] = make_uint4(0u, 0u, 0u, 0u);
   } else {
     // ------------------------------------------------ state, scaling of y --
     const int tid = threadIdx.x - 128;
     const int half = (warp - 4) >> 2;  // which half of the columns
     const int r = threadIdx.x & 127;   // state row (z dim) = TMEM lane
     constexpr int kCols = D / 2;
+    constexpr int kVecs = kTok * D / 8 / kStateThreads;  // 16-byte pieces of y a thread
     const bool mine = r < D;           // at d = 64 lanes 64.. repeat the rows
     const uint32_t ds_tm =
         tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColDS + half * kCols;
     float m[kCols];
-    const float* src = p.seg_states ? p.seg_states + (size_t)blockIdx.x * D * D
-                                    : (p.init ? p.init + (size_t)bh * D * D : nullptr);
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      const int col = half * kCols + i;
-      m[i] = src && mine ? (p.state_t ? src[(size_t)col * D + r] : src[(size_t)r * D + col]) : 0.f;
-    }
     // the state as the bf16 operand of O2: row r, this half's columns
     auto write_operand = [&]() {
       if (mine) {
@@ -461,78 +477,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&br.m_op);
     };
-    write_operand();
-    constexpr int kVecs = kTok * D / 8 / kStateThreads;  // 16-byte pieces of y a thread
-    const float g_full = linear_power(l2, kTok);
-    float w_full[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int j = (tid >> 3) + 32 * k;
-      w_full[k] = kRev ? p.scale * linear_power(l2, j + 1) : linear_power(l2, kTok - 1 - j);
-    }
+    int k = 0, ku = 0;
     bool ok = true;
-    for (int c = 0; c < nt && ok; ++c) {
-      const int n = tile_n(c);
-      uint8_t* ty = smem + (c & 1) * L::kStage + L::kTile;
-      ok = mbar_wait_warp(&br.full_xy[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status);
-      if (ok && ragged(c)) {
-        ok = mbar_wait_warp(&br.full_z[c & 1], (uint32_t)(c / 2) & 1, abort_flag, p.status);
+    for (int ip = 0; ip < n_po && ok; ++ip) {
+      const LinearPortion po = portion(ip);
+      const float l2 = linear_log2_decay(p.log_decay, po.bh % p.H);
+      const float* src = (kRev ? po.cut_right : po.cut_left)
+                             ? p.cuts + (size_t)(kRev ? blockIdx.x + 1 : blockIdx.x - 1) * D * D
+                             : (p.init ? p.init + (size_t)po.bh * D * D : nullptr);
+      if (!src || !mine) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) m[i] = 0.f;
+      } else if (p.state_t) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) m[i] = src[(size_t)(half * kCols + i) * D + r];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCols; i += 4) {
+          const float4 v =
+              *reinterpret_cast<const float4*>(src + (size_t)r * D + half * kCols + i);
+          m[i] = v.x;
+          m[i + 1] = v.y;
+          m[i + 2] = v.z;
+          m[i + 3] = v.w;
+        }
+      }
+      const float g_full = linear_power(l2, kTok);
+      float w_full[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = (tid >> 3) + 32 * q;
+        w_full[q] = kRev ? p.scale * linear_power(l2, j + 1) : linear_power(l2, kTok - 1 - j);
+      }
+      // the operand's last reader is done: this thread saw the update after it
+      // (ds_full), or, at the end of a portion without one, waits for o_full
+      if (po.live > 0) write_operand();
+      for (int c = 0; c < po.live; ++c, ++k) {
+        const int st = k & 1, tile = tile_of(po, c), n = po.tokens(tile);
+        uint8_t* ty = smem + st * L::kStage + L::kTile;
+        ok = mbar_wait_warp(&br.full_xy[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
+        if (ok && ragged(tile, n)) {
+          ok = mbar_wait_warp(&br.full_z[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
+          if (!ok) break;
+          zero_rows<D>(ty, n, tid);
+          zero_rows<D>(ty + L::kTile, n, tid);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&br.fixed);
+        }
         if (!ok) break;
-        zero_rows<D>(ty, n, tid);
-        zero_rows<D>(ty + L::kTile, n, tid);
+        if (!updates(po, c)) {
+          ok = mbar_wait_warp(&br.o_full, (uint32_t)k & 1, abort_flag, p.status);
+          if (!ok) break;
+          continue;
+        }
+        ok = mbar_wait_warp(&br.s_full, (uint32_t)k & 1, abort_flag, p.status);
+        if (!ok) break;
+        uint4 lo[kVecs];
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+          float w = w_full[q & 3];
+          if (n < kTok) {
+            const int j = (tid >> 3) + 32 * (q & 3);
+            w = j >= n ? 0.f : (kRev ? w : linear_power(l2, n - 1 - j));
+          }
+          uint4* at = reinterpret_cast<uint4*>(ty) + tid + kStateThreads * q;
+          uint4 hi;
+          split_vec(*at, w, hi, lo[q]);
+          *at = hi;
+        }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&br.fixed);
-      }
-      if (!ok || !updates(c)) break;
-      ok = mbar_wait_warp(&br.s_full, (uint32_t)c & 1, abort_flag, p.status);
-      if (!ok) break;
-      uint4 lo[kVecs];
+        if (lane == 0) mbar_arrive(&br.y_hi);
+        const uint32_t pu = (uint32_t)(ku++) & 1;
+        ok = mbar_wait_warp(&br.hi_done, pu, abort_flag, p.status);
+        if (!ok) break;
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        float w = w_full[k & 3];
-        if (n < kTok) {
-          const int j = (tid >> 3) + 32 * (k & 3);
-          w = j >= n ? 0.f : (kRev ? w : linear_power(l2, n - 1 - j));
+        for (int q = 0; q < kVecs; ++q)
+          reinterpret_cast<uint4*>(ty)[tid + kStateThreads * q] = lo[q];
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br.y_lo);
+        ok = mbar_wait_warp(&br.ds_full, pu, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const float g = n == kTok ? g_full : linear_power(l2, n);
+#pragma unroll
+        for (int b = 0; b < kCols / 32; ++b) {
+          uint32_t v[32];
+          tmem_ld32(ds_tm + 32 * b, v);
+          tmem_ld_wait();
+          reg_fence32(v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            m[32 * b + e] = fmaf(g, m[32 * b + e], __uint_as_float(v[e]));
         }
-        uint4* at = reinterpret_cast<uint4*>(ty) + tid + kStateThreads * k;
-        uint4 hi;
-        split_vec(*at, w, hi, lo[k]);
-        *at = hi;
+        // ds_full also says that O2 of this tile has read the operand
+        if (c + 1 < po.live) write_operand();
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&br.y_hi);
-      ok = mbar_wait_warp(&br.hi_done, (uint32_t)c & 1, abort_flag, p.status);
-      if (!ok) break;
+      if (ok && is_final(po) && mine) {
+        float* dst = p.final_state + ((size_t)po.bh * D + r) * D + half * kCols;
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k)
-        reinterpret_cast<uint4*>(ty)[tid + kStateThreads * k] = lo[k];
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&br.y_lo);
-      ok = mbar_wait_warp(&br.ds_full, (uint32_t)c & 1, abort_flag, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      const float g = n == kTok ? g_full : linear_power(l2, n);
-#pragma unroll
-      for (int b = 0; b < kCols / 32; ++b) {
-        uint32_t v[32];
-        tmem_ld32(ds_tm + 32 * b, v);
-        tmem_ld_wait();
-        reg_fence32(v);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          m[32 * b + e] = fmaf(g, m[32 * b + e], __uint_as_float(v[e]));
+        for (int i = 0; i < kCols; i += 4)
+          *reinterpret_cast<float4*>(dst + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
       }
-      // ds_full also says that O2 of this tile has read the operand
-      if (c + 1 < nt) write_operand();
-    }
-    if (ok && final && mine) {
-      float* dst = p.final_state + ((size_t)bh * D + r) * D + half * kCols;
-#pragma unroll
-      for (int i = 0; i < kCols; i += 4)
-        *reinterpret_cast<float4*>(dst + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
     }
   }
 
@@ -544,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------ segment states --
+// ------------------------------------------------------ states at cuts --
 
-// The state of each segment alone: one accumulator in TMEM over all of its
-// tiles, y weighted by the distance to the segment's end (start in reverse),
-// hi and lo, so nothing is ever rescaled.
+// Each run's own part of the head that its boundary cuts: one accumulator in
+// TMEM over the tiles, y weighted by the distance to the cut, hi and lo, so
+// nothing is ever rescaled.
 constexpr int kSThreads = 320;  // 8 scaling warps, TMA, MMA
 constexpr int kSWarpTMA = 8, kSWarpMMA = 9;
 
@@ -571,8 +619,9 @@ struct StateBars {
 struct StateParams {
   const float* log_decay;
   const int* lengths;
-  float* seg_states;
-  int H, T, nseg, seg_tokens, reverse;
+  float* cuts;
+  int BH, H, T, reverse;
+  LinearSplit split;
   float scale;
   int* status;
 };
@@ -588,10 +637,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   StateBars& br = *reinterpret_cast<StateBars*>(smem + L::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
-  const int len = linear_length(p.lengths, bh / p.H, p.T, p.status);
-  const int t0 = seg * p.seg_tokens, t1 = max(t0, min(t0 + p.seg_tokens, len));
-  const int nt = (t1 - t0 + kTok - 1) / kTok;
+  const LinearPortion po = linear_portion(
+      p.split, p.BH, p.H, p.T, p.lengths, p.status, blockIdx.x,
+      p.reverse ? 0 : linear_portions(p.split, p.BH, blockIdx.x) - 1);
+  if (!(p.reverse ? po.cut_left : po.cut_right)) return;  // the whole CTA
+  const int bh = po.bh, nt = po.live;
+  const int t0 = po.row(po.first), t1 = max(t0, min(po.row(po.last), po.len));
   const float l2 = linear_log2_decay(p.log_decay, bh % p.H);
 
   if (threadIdx.x == 0) {
@@ -703,7 +754,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     }
     const int half = warp >> 2, r = threadIdx.x & 127;
     constexpr int kCols = D / 2;
-    float* dst = p.seg_states + ((size_t)blockIdx.x * D + r) * D + half * kCols;
+    float* dst = p.cuts + ((size_t)blockIdx.x * D + r) * D + half * kCols;
     ok = ok && (nt == 0 || mbar_wait(&br.done, 0, abort_flag, p.status));
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -740,29 +791,29 @@ __global__ void __launch_bounds__(kSThreads, 1)
 template <int D, bool kRev>
 cudaError_t out_tc_d(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s) {
   using L = OutLayout<D>;
-  const OutParams p{a.log_decay, a.lengths, a.init, a.seg_states, a.final_state,
-                    static_cast<__nv_bfloat16*>(a.out), a.H, a.T, a.nseg, a.seg_tokens,
-                    a.state_t ? 1 : 0, a.scale, a.status};
+  const OutParams p{a.log_decay, a.lengths, a.init, a.cuts, a.final_state,
+                    static_cast<__nv_bfloat16*>(a.out), a.B * a.H, a.H, a.T, a.state_t ? 1 : 0,
+                    a.split, a.scale, a.status};
   auto kern = polar_linear_out_tc_kernel<D, kRev>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAsked);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)a.B * a.H * a.nseg, kThreads, L::kAsked, s>>>(maps[0], maps[1], maps[2],
-                                                                 maps[3], p);
+  kern<<<(unsigned)a.split.parts, kThreads, L::kAsked, s>>>(maps[0], maps[1], maps[2], maps[3],
+                                                            p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t state_tc_d(const LinearStateArgs& a, const CUtensorMap* maps, cudaStream_t s) {
   using L = StateLayout<D>;
-  const StateParams p{a.log_decay, a.lengths, a.seg_states, a.H, a.T, a.nseg, a.seg_tokens,
-                      a.reverse ? 1 : 0, a.scale, a.status};
+  const StateParams p{a.log_decay, a.lengths, a.cuts, a.B * a.H, a.H, a.T, a.reverse ? 1 : 0,
+                      a.split, a.scale, a.status};
   cudaError_t e = cudaFuncSetAttribute(polar_linear_state_tc_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kSmemBytes);
   if (e != cudaSuccess) return e;
   polar_linear_state_tc_kernel<D>
-      <<<(unsigned)a.B * a.H * a.nseg, kSThreads, L::kSmemBytes, s>>>(maps[0], maps[1], p);
+      <<<(unsigned)a.split.parts, kSThreads, L::kSmemBytes, s>>>(maps[0], maps[1], p);
   return cudaGetLastError();
 }
 

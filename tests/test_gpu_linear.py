@@ -197,12 +197,16 @@ def test_decay_extremes():
 def test_state_in_place_and_repeats():
     """state_out may be state; the same call gives the same bits."""
     import long_context_attention_causal_gb300 as pa
-    for dtype, T in (("bf16", 700), ("f32", 700), ("bf16", 90)):
+    for dtype, T in (("bf16", 700), ("f32", 700), ("bf16", 90), ("bf16", 9000)):
         x = make(2, 3, T, 128, dtype, 8, True)
+        # the second sequence ends early: the CTAs of its end have nothing to
+        # walk and write its state at once
+        lens = torch.tensor([T, 30], dtype=torch.int32, device=dev())
         a = pa.linear_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=x["state"],
-                          want_state=True)
+                          lengths=lens, want_state=True)
         S = x["state"].clone()
-        b = pa.linear_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=S, state_out=S)
+        b = pa.linear_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=S, state_out=S,
+                          lengths=lens)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], S)
         ga = pa.linear_bwd(x["q"], x["k"], x["v"], x["log_decay"], x["dmem"], state=x["state"],
                            dstate_out=x["dstate"], want_dstate=True)
@@ -311,9 +315,10 @@ def test_refusals():
         pa.linear_fwd(*a, lengths=torch.tensor([3], device=dev()))
     with pytest.raises(TypeError):
         pa.linear_fwd(x["q"].cpu(), *a[1:])
+    y = make(1, 2, 4000, 64, "f32", 1)  # few long heads are cut: a workspace is needed
     with pytest.raises(pa.PolarError):
-        pa.linear_fwd(*a, want_state=True, workspace=torch.empty(16, device=dev(),
-                                                                 dtype=torch.uint8))
+        pa.linear_fwd(y["q"], y["k"], y["v"], y["log_decay"],
+                      workspace=torch.empty(16, device=dev(), dtype=torch.uint8))
     with pytest.raises(pa.PolarError):
         pa.linear_fwd(*a, scale=float("nan"))
     h = [t.half() for t in a[:3]]
