@@ -10,21 +10,22 @@
 //   O2 = x M^T                 M as a bf16 operand in shared memory
 //   out_i = O1_i + g^(i+1) O2_i
 //   M' = g^n M + z^T (w y)
-// The state lives in fp32 registers (a row of TMEM's lanes a thread pair);
-// its products leave TMEM once a tile.  w y is not exact in bf16, so it
-// enters as two bf16 terms, hi + lo (2^-16 relative), both products in fp32:
-// the state is as good as fp32 inputs allow, and what it rounds to bf16 for
-// O2 is rounded once.  hi, then lo, are written over y in place, which only
-// the scores read unscaled: no second copy of a tile is needed, and two whole
-// stages of x, y, z fit beside the state operand (7 x 32 KB at d = 128).
+// The state lives in TMEM in fp32: once a tile it is read, rounded to bf16 as
+// O2's operand, and written back times g^n for the products to add to.  w y is
+// not exact in bf16, so it enters as two bf16 terms, hi + lo (2^-16 relative):
+// the state is as good as fp32 inputs allow, and its bf16 operand is rounded
+// once.  hi and lo take turns in one buffer; two buffers of x and
+// z, one of y, that one and the state operand fill shared memory (7 x 32 KB at
+// d = 128).  The outputs are staged in z's buffer, whose last reader makes them.
 //
 // Bound: HBM.  A tile moves 4 x 32 KB at d = 128 against 6 products of
 // 2 * 128^3 flop: at the measured rates 3.0 us of an SM's share of the copy
 // bandwidth to about 2.0 us of its tensor rate.
 //
-// Roles (448 threads, one CTA per SM): warps 0-3 P and the outputs (thread =
+// Roles (480 threads, one CTA per SM): warps 0-3 P and the outputs (thread =
 // row = TMEM lane), warps 4-11 the state and the scaling of y (two groups,
-// half of the columns each), warp 12 TMA, warp 13 MMA and TMEM.
+// half of the columns each), warp 12 TMA loads, warp 13 MMA and TMEM, warp 14
+// TMA stores.
 #include "polar_device.cuh"
 #include "polar_internal.h"
 #include "polar_linear.cuh"
@@ -34,21 +35,22 @@ namespace polar {
 namespace {
 
 constexpr int kTok = kLinearTile;  // tokens per tile
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr int kStateThreads = 256;
-constexpr int kWarpTMA = 12, kWarpMMA = 13;
+constexpr int kWarpTMA = 12, kWarpMMA = 13, kWarpStore = 14;
 constexpr int kStateWarps = 8;
-constexpr uint32_t kColS = 0, kColO1 = 128, kColO2 = 256, kColDS = 384;
+constexpr uint32_t kColS = 0, kColO1 = 128, kColO2 = 256, kColM = 384;
 
 struct OutBars {
-  uint64_t full_xy[2], full_z[2], empty_x[2], empty_yz[2];
-  uint64_t s_full, p_full, o_full, o_free, m_op;  // one phase a tile (m_op before it)
+  uint64_t full_x[2], full_z[2], empty_x[2], empty_z[2];
+  uint64_t full_y, empty_y;  // one phase a tile
+  uint64_t s_full, p_full, o_full, o_free, staged, m_op;  // one phase a tile
   uint64_t y_hi, y_lo, hi_done, ds_full;          // one phase a state update
   uint64_t fixed;  // one phase a tile with rows past the sequence: they are zeroed
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  float full_pw[2][32];  // g^31 .. g^0 (forward), g^0 .. g^31 (reverse); by portion parity
+  alignas(16) float full_pw[2][32];  // read as float4: g^31 .. g^0 (forward), g^0 .. g^31 (reverse); by portion parity
   float diag_pw[2][64];  // 31 zeros, then g^0 .. g^31
 };
 
@@ -56,8 +58,11 @@ template <int D>
 struct OutLayout {
   static constexpr int kTile = kTok * D * 2;
   static constexpr int kAtom = kTok * 128;  // 64 columns of a tile
-  static constexpr int kStage = 3 * kTile;  // x, y, z
-  static constexpr int kMOff = 2 * kStage;  // state operand, D rows
+  static constexpr int kXOff = 0;                  // two of x
+  static constexpr int kZOff = kXOff + 2 * kTile;  // two of z, then the staged outputs
+  static constexpr int kYOff = kZOff + 2 * kTile;  // one of y
+  static constexpr int kWOff = kYOff + kTile;      // scaled y: hi, then lo
+  static constexpr int kMOff = kWOff + kTile;      // state operand, D rows
   static constexpr int kMAtom = D * 128;
   static constexpr int kBarOff = kMOff + D * D * 2;
   static constexpr int kSmemBytes = kBarOff + (int)sizeof(OutBars) + 1024;
@@ -78,6 +83,11 @@ struct OutParams {
   int* status;
 };
 
+// Generic-proxy shared-memory writes made visible to TMA and the tensor core.
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x,
                                              int y, int z) {
   asm volatile(
@@ -90,38 +100,22 @@ __device__ __forceinline__ void tma_store_commit_wait_read() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
-// Generic-proxy shared-memory writes made visible to TMA and the tensor core.
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
-// Named barrier of the 128 output threads that also ANDs a predicate: after a
-// failed wait all of them leave together.
-__device__ __forceinline__ bool out_bar_and(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)ok)
-      : "memory");
-  return r != 0;
-}
-
-// The pair (f0, f1) as bf16 hi and the rest as bf16 lo.
-__device__ __forceinline__ void split_pair(float f0, float f1, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(f0, f1);
-  lo = pack_bf16x2(f0 - __uint_as_float(hi << 16), f1 - __uint_as_float(hi & 0xFFFF0000u));
-}
+// w y of eight bf16 values as bf16 hi and the bf16 of what hi leaves.
 __device__ __forceinline__ void split_vec(uint4 y, float w, uint4& hi, uint4& lo) {
   const uint32_t in[4] = {y.x, y.y, y.z, y.w};
+  const float2 w2 = make_float2(w, w), zero = make_float2(0.f, 0.f);
+  const float2 minus = make_float2(-1.f, -1.f);
   uint32_t h[4], l[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    split_pair(w * __uint_as_float(in[e] << 16), w * __uint_as_float(in[e] & 0xFFFF0000u), h[e],
-               l[e]);
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = ffma2(make_float2(__uint_as_float(in[e] << 16),
+                                       __uint_as_float(in[e] & 0xFFFF0000u)), w2, zero);
+    h[e] = pack_bf16x2(f.x, f.y);
+    const float2 r = ffma2(make_float2(__uint_as_float(h[e] << 16),
+                                       __uint_as_float(h[e] & 0xFFFF0000u)), minus, f);
+    l[e] = pack_bf16x2(r.x, r.y);
+  }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
@@ -152,15 +146,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&br.full_xy[i], 1);
+      mbar_init(&br.full_x[i], 1);
       mbar_init(&br.full_z[i], 1);
       mbar_init(&br.empty_x[i], 1);
-      mbar_init(&br.empty_yz[i], 1);
+      mbar_init(&br.empty_z[i], 1);
     }
+    mbar_init(&br.full_y, 1);
+    mbar_init(&br.empty_y, 1 + kStateWarps);  // the scores and the scaling have read it
     mbar_init(&br.s_full, 1);
     mbar_init(&br.p_full, 4);
     mbar_init(&br.o_full, 1);
     mbar_init(&br.o_free, 4);
+    mbar_init(&br.staged, 4);
     mbar_init(&br.m_op, kStateWarps);
     mbar_init(&br.y_hi, kStateWarps);
     mbar_init(&br.y_lo, kStateWarps);
@@ -202,39 +199,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map_z);
     }
     __syncwarp();
-    int k = 0;
+    int k = 0, nz = 0, nx = 0, ny = 0;  // tiles of each issued
     bool ok = true;
+    auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row, int bh) {
+      mbar_arrive_expect_tx_warp(bar, L::kTile);
+      for (int h = 0; h < D / 64; ++h)
+        tma_load_3d_warp(dst + h * L::kAtom, map, bar, 64 * h, row, bh);
+    };
     for (int ip = 0; ip < n_po && ok; ++ip) {
       const LinearPortion po = portion(ip);
       for (int c = 0; c < po.live; ++c, ++k) {
         const int st = k & 1, row = po.row(tile_of(po, c));
-        if (k >= 2) {
-          const uint32_t ph = (uint32_t)(k / 2 - 1) & 1;
-          ok = mbar_wait_warp(&br.empty_yz[st], ph, abort_flag, p.status) &&
-               mbar_wait_warp(&br.empty_x[st], ph, abort_flag, p.status);
-          if (!ok) break;
-        }
-        uint8_t* sx = smem + st * L::kStage;
-        mbar_arrive_expect_tx_warp(&br.full_xy[st], 2 * L::kTile);
-        for (int h = 0; h < D / 64; ++h) {
-          tma_load_3d_warp(sx + h * L::kAtom, &map_x, &br.full_xy[st], 64 * h, row, po.bh);
-          tma_load_3d_warp(sx + L::kTile + h * L::kAtom, &map_y, &br.full_xy[st], 64 * h, row,
-                           po.bh);
-        }
-        mbar_arrive_expect_tx_warp(&br.full_z[st], L::kTile);
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_3d_warp(sx + 2 * L::kTile + h * L::kAtom, &map_z, &br.full_z[st], 64 * h, row,
-                           po.bh);
+        const uint32_t ph = (uint32_t)(k / 2 - 1) & 1;
+        // in the order in which their buffers come free
+        if (k >= 2) ok = mbar_wait_warp(&br.empty_x[st], ph, abort_flag, p.status);
+        if (!ok) break;
+        load(smem + L::kXOff + st * L::kTile, &map_x, &br.full_x[st], row, po.bh);
+        ++nx;
+        if (k >= 1) ok = mbar_wait_warp(&br.empty_y, (uint32_t)(k - 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        load(smem + L::kYOff, &map_y, &br.full_y, row, po.bh);
+        ++ny;
+        if (k >= 2) ok = mbar_wait_warp(&br.empty_z[st], ph, abort_flag, p.status);
+        if (!ok) break;
+        load(smem + L::kZOff + st * L::kTile, &map_z, &br.full_z[st], row, po.bh);
+        ++nz;
       }
     }
     if (!ok) {
-      // aborted: let the copies already issued land before the CTA exits
+      // aborted: let the copies already issued land before the CTA exits (the
+      // last phase that each barrier was armed for)
       volatile int never = 0;
       const long long lim = kWaitLimitCycles / 4;
-      for (int c = k - 1; c >= 0 && c >= k - 2; --c) {
-        mbar_wait(&br.full_xy[c & 1], (uint32_t)(c / 2) & 1, &never, p.status, lim);
+      for (int c = nz - 1; c >= 0 && c >= nz - 2; --c)
         mbar_wait(&br.full_z[c & 1], (uint32_t)(c / 2) & 1, &never, p.status, lim);
-      }
+      for (int c = nx - 1; c >= 0 && c >= nx - 2; --c)
+        mbar_wait(&br.full_x[c & 1], (uint32_t)(c / 2) & 1, &never, p.status, lim);
+      if (ny > 0) mbar_wait(&br.full_y, (uint32_t)(ny - 1) & 1, &never, p.status, lim);
       __syncwarp();
     }
   } else if (warp == kWarpMMA) {
@@ -252,13 +253,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t m_desc = smem_desc_sw128(base + L::kMOff, 16, 1024);
     auto at = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
     auto kstep = [&](int kk, uint32_t atom) { return at((kk >> 2) * atom) + (uint64_t)(kk & 3) * 2; };
-    auto issue_ds = [&](int st, bool add) {
-      const uint64_t y0 = mn + at(st * L::kStage + L::kTile), z0 = y0 + at(L::kTile);
+    auto issue_ds = [&](int st) {
+      const uint64_t y0 = mn + at(L::kWOff), z0 = mn + at(L::kZOff + st * L::kTile);
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
-        umma_ss_warp(tmem + kColDS, z0 + at(kk * 2048), y0 + at(kk * 2048), kIdDS,
-                     (add || kk > 0) ? 1u : 0u);
+        umma_ss_warp(tmem + kColM, z0 + at(kk * 2048), y0 + at(kk * 2048), kIdDS, 1u);
     };
+    // Order of a tile's products: S, hi, O2, lo, O1.  O2 runs while lo is
+    // written; O1 and the next S run while the next y is scaled.
     int k = 0, ku = 0, kf = 0;
     bool ok = true, any = false;
     for (int ip = 0; ip < n_po && ok; ++ip) {
@@ -266,21 +268,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < po.live; ++c, ++k) {
         const int st = k & 1, tile = tile_of(po, c);
         const uint32_t ph = (uint32_t)k & 1, ph2 = (uint32_t)(k / 2) & 1;
-        // scores: over P of the tile before, whose product is issued already
-        ok = mbar_wait_warp(&br.full_xy[st], ph2, abort_flag, p.status);
+        const bool upd = updates(po, c);
+        const uint32_t pu = (uint32_t)ku & 1;
+        // S: over P of the tile before, whose product is issued already
+        ok = mbar_wait_warp(&br.full_x[st], ph2, abort_flag, p.status) &&
+             mbar_wait_warp(&br.full_y, ph, abort_flag, p.status);
         if (ok && ragged(tile, po.tokens(tile)))
           ok = mbar_wait_warp(&br.fixed, (uint32_t)(kf++) & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t x0 = km + at(st * L::kStage), y0 = x0 + at(L::kTile);
+        const uint64_t x0 = km + at(L::kXOff + st * L::kTile), y0 = km + at(L::kYOff);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_ss_warp(tmem + kColS, x0 + kstep(kk, L::kAtom), y0 + kstep(kk, L::kAtom), kIdS,
                        kk > 0);
         umma_commit_warp(&br.s_full);
+        umma_commit_warp(&br.empty_y);
         any = true;
+        ok = mbar_wait_warp(&br.full_z[st], ph2, abort_flag, p.status);
+        if (ok && upd) {
+          ok = mbar_wait_warp(&br.y_hi, pu, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_ds(st);
+          umma_commit_warp(&br.hi_done);
+        }
         // O2, once the state is written and the last outputs are read
-        ok = mbar_wait_warp(&br.m_op, ph, abort_flag, p.status);
+        ok = ok && mbar_wait_warp(&br.m_op, ph, abort_flag, p.status);
         if (ok && k > 0) ok = mbar_wait_warp(&br.o_free, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
@@ -288,30 +302,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk)
           umma_ss_warp(tmem + kColO2, x0 + kstep(kk, L::kAtom), m_desc + kstep(kk, L::kMAtom),
                        kIdO2, kk > 0);
-        // O1
-        ok = mbar_wait_warp(&br.full_z[st], ph2, abort_flag, p.status) &&
-             mbar_wait_warp(&br.p_full, ph, abort_flag, p.status);
+        umma_commit_warp(&br.empty_x[st]);
+        if (upd) {
+          ok = mbar_wait_warp(&br.y_lo, pu, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_ds(st);
+          umma_commit_warp(&br.ds_full);
+          ++ku;
+        }
+        ok = mbar_wait_warp(&br.p_full, ph, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t z0 = mn + at(st * L::kStage + 2 * L::kTile);
+        const uint64_t z0 = mn + at(L::kZOff + st * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < kTok / 16; ++kk)
           umma_ts_warp(tmem + kColO1, tmem + kColS + kk * 8, z0 + at(kk * 2048), kIdO1, kk > 0);
         umma_commit_warp(&br.o_full);
-        if (updates(po, c)) {
-          const uint32_t pu = (uint32_t)(ku++) & 1;
-          ok = mbar_wait_warp(&br.y_hi, pu, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          issue_ds(st, false);
-          umma_commit_warp(&br.hi_done);
-          ok = mbar_wait_warp(&br.y_lo, pu, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          issue_ds(st, true);
-          umma_commit_warp(&br.ds_full);
-        }
-        umma_commit_warp(&br.empty_yz[st]);
       }
     }
     if (!ok && any) {
@@ -322,23 +329,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&br.drain, 0, &never, p.status, kWaitLimitCycles / 4);
       __syncwarp();
     }
+  } else if (warp == kWarpStore) {
+    // ------------------------------------------------------- TMA stores --
+    if (lane == 0) {
+      int k = 0;
+      bool ok = true;
+      for (int ip = 0; ip < n_po && ok; ++ip) {
+        const LinearPortion po = portion(ip);
+        for (int c = 0; c < po.live; ++c, ++k) {
+          const int st = k & 1;
+          ok = mbar_wait(&br.staged, (uint32_t)k & 1, abort_flag, p.status);
+          if (!ok) break;
+          for (int h = 0; h < D / 64; ++h)
+            tma_store_3d(&map_o, smem + L::kZOff + st * L::kTile + h * L::kAtom, 64 * h,
+                         po.row(tile_of(po, c)), po.bh);
+          tma_store_commit_wait_read();
+          mbar_arrive(&br.empty_z[st]);
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------- P and the outputs --
     const int r = threadIdx.x;  // row of the tile
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + kColS;
     int k = 0;
-    bool go = true;
-    for (int ip = 0; ip < n_po && go; ++ip) {
+    bool go = true;  // after a failed wait a warp still joins the barriers
+    for (int ip = 0; ip < n_po; ++ip) {
       const LinearPortion po = portion(ip);
       const float l2 = linear_log2_decay(p.log_decay, po.bh % p.H);
       // powers of the head's decay; two sets, so that a warp still in the last
-      // portion keeps its own (every tile ends in a barrier of these warps)
+      // portion keeps its own (every portion starts with a barrier)
       float* full_pw = br.full_pw[ip & 1];
       float* diag_pw = br.diag_pw[ip & 1];
       if (r < 32) full_pw[r] = linear_power(l2, kRev ? r : 31 - r);
       if (r < 64) diag_pw[r] = r < 31 ? 0.f : linear_power(l2, r - 31);
-      go = out_bar_and(true);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (!go) continue;
       for (int c = 0; c < po.live; ++c, ++k) {
         const int st = k & 1, tile = tile_of(po, c), n = po.tokens(tile);
         const uint32_t ph = (uint32_t)k & 1;
@@ -393,13 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&br.p_full);
           ok = __all_sync(0xffffffffu, mbar_wait(&br.o_full, ph, abort_flag, p.status));
         }
-        uint8_t* stage = smem + st * L::kStage;  // x's tile: its readers are done
         if (ok) {
           tc_fence_after();
           const bool live = r < n;
           const float w2 = live ? (kRev ? linear_power(l2, n - 1 - r)
                                         : p.scale * linear_power(l2, r + 1))
                                 : 0.f;
+          uint8_t* line = smem + L::kZOff + st * L::kTile + r * 128;  // z's readers are done
 #pragma unroll 1
           for (int b = 0; b < D / 32; ++b) {
             uint32_t o1[32], o2[32];
@@ -413,7 +441,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&br.o_free);
             }
-            uint8_t* line = stage + (b >> 1) * L::kAtom + r * 128;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               uint32_t o4[4];
@@ -425,21 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o4[e] = live ? pack_bf16x2(a0, a1) : 0u;
               }
               const int ch = (b & 1) * 4 + g;
-              *reinterpret_cast<uint4*>(line + ((ch ^ (r & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(line + (b >> 1) * L::kAtom + ((ch ^ (r & 7)) << 4)) =
                   make_uint4(o4[0], o4[1], o4[2], o4[3]);
             }
           }
           fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&br.staged);
         }
-        if (!out_bar_and(ok)) {
+        if (!__all_sync(0xffffffffu, ok)) {
           go = false;
           break;
-        }
-        if (r == 0) {
-          for (int h = 0; h < D / 64; ++h)
-            tma_store_3d(&map_o, stage + h * L::kAtom, 64 * h, po.row(tile), po.bh);
-          tma_store_commit_wait_read();
-          mbar_arrive(&br.empty_x[st]);
         }
       }
       // tiles past the sequence
@@ -448,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long i = r; i < (long long)(t1 - t0) * (D / 8); i += 128)
         tail[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-  } else {
+  } else if (warp < 4 + kStateWarps) {
     // ------------------------------------------------ state, scaling of y --
     const int tid = threadIdx.x - 128;
     const int half = (warp - 4) >> 2;  // which half of the columns
@@ -456,130 +479,167 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kCols = D / 2;
     constexpr int kVecs = kTok * D / 8 / kStateThreads;  // 16-byte pieces of y a thread
     const bool mine = r < D;           // at d = 64 lanes 64.. repeat the rows
-    const uint32_t ds_tm =
-        tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColDS + half * kCols;
-    float m[kCols];
-    // the state as the bf16 operand of O2: row r, this half's columns
-    auto write_operand = [&]() {
-      if (mine) {
+    const uint32_t m_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColM + half * kCols;
+    // The state, 32 columns at a time: its bf16 operand for O2 and, if `scale`,
+    // the state times g back into TMEM, where the next products add to it.
+    auto hand_over = [&](bool scale, float g) {
+      int sw = r & 7;
+      asm volatile("" : "+r"(sw));  // not to be kept as eight addresses across the loop
 #pragma unroll
-        for (int i = 0; i < kCols; i += 8) {
-          const int col = half * kCols + i;
+      for (int b = 0; b < kCols / 32; ++b) {
+        uint32_t v[32];
+        tmem_ld32(m_tm + 32 * b, v);
+        tmem_ld_wait();
+        reg_fence32(v);
+        if (mine) {
+          const int col = half * kCols + 32 * b;
           uint8_t* line = smem + L::kMOff + (col >> 6) * L::kMAtom + r * 128;
-          const int ch = (col & 63) >> 3;
-          *reinterpret_cast<uint4*>(line + ((ch ^ (r & 7)) << 4)) =
-              make_uint4(pack_bf16x2(m[i], m[i + 1]), pack_bf16x2(m[i + 2], m[i + 3]),
-                         pack_bf16x2(m[i + 4], m[i + 5]), pack_bf16x2(m[i + 6], m[i + 7]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = pack_bf16x2(__uint_as_float(v[8 * q + 2 * e]),
+                                 __uint_as_float(v[8 * q + 2 * e + 1]));
+            const int ch = ((col & 63) >> 3) + q;
+            *reinterpret_cast<uint4*>(line + ((ch ^ sw) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        if (scale) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(g * __uint_as_float(v[e]));
+          tmem_st32(m_tm + 32 * b, v);
         }
       }
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&br.m_op);
+      if (scale) tmem_st_wait();
     };
     int k = 0, ku = 0;
     bool ok = true;
     for (int ip = 0; ip < n_po && ok; ++ip) {
       const LinearPortion po = portion(ip);
       const float l2 = linear_log2_decay(p.log_decay, po.bh % p.H);
-      const float* src = (kRev ? po.cut_right : po.cut_left)
-                             ? p.cuts + (size_t)(kRev ? blockIdx.x + 1 : blockIdx.x - 1) * D * D
-                             : (p.init ? p.init + (size_t)po.bh * D * D : nullptr);
-      if (!src || !mine) {
+      const bool fin = is_final(po);
+      if (po.live > 0 || fin) {
+        // the incoming state (every reader of the last portion's is done)
+        const float* src =
+            (kRev ? po.cut_right : po.cut_left)
+                ? p.cuts + (size_t)(kRev ? blockIdx.x + 1 : blockIdx.x - 1) * D * D
+                : (p.init ? p.init + (size_t)po.bh * D * D : nullptr);
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) m[i] = 0.f;
-      } else if (p.state_t) {
+        for (int b = 0; b < kCols / 32; ++b) {
+          const int col = half * kCols + 32 * b;
+          uint32_t v[32];
+          if (!src || !mine) {
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) m[i] = src[(size_t)(half * kCols + i) * D + r];
-      } else {
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
+          } else if (p.state_t) {
 #pragma unroll
-        for (int i = 0; i < kCols; i += 4) {
-          const float4 v =
-              *reinterpret_cast<const float4*>(src + (size_t)r * D + half * kCols + i);
-          m[i] = v.x;
-          m[i + 1] = v.y;
-          m[i + 2] = v.z;
-          m[i + 3] = v.w;
+            for (int e = 0; e < 32; ++e)
+              v[e] = __float_as_uint(src[(size_t)(col + e) * D + r]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const uint4 u = *reinterpret_cast<const uint4*>(src + (size_t)r * D + col + e);
+              v[e] = u.x;
+              v[e + 1] = u.y;
+              v[e + 2] = u.z;
+              v[e + 3] = u.w;
+            }
+          }
+          __syncwarp();
+          tmem_st32(m_tm + 32 * b, v);
         }
+        tmem_st_wait();
       }
-      const float g_full = linear_power(l2, kTok);
-      float w_full[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int j = (tid >> 3) + 32 * q;
-        w_full[q] = kRev ? p.scale * linear_power(l2, j + 1) : linear_power(l2, kTok - 1 - j);
-      }
-      // the operand's last reader is done: this thread saw the update after it
-      // (ds_full), or, at the end of a portion without one, waits for o_full
-      if (po.live > 0) write_operand();
+      bool wait_ds = false;  // products of the tile before are under way
       for (int c = 0; c < po.live; ++c, ++k) {
         const int st = k & 1, tile = tile_of(po, c), n = po.tokens(tile);
-        uint8_t* ty = smem + st * L::kStage + L::kTile;
-        ok = mbar_wait_warp(&br.full_xy[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
+        const bool upd = updates(po, c);
+        uint8_t* ty = smem + L::kYOff;
+        ok = mbar_wait_warp(&br.full_y, (uint32_t)k & 1, abort_flag, p.status);
         if (ok && ragged(tile, n)) {
           ok = mbar_wait_warp(&br.full_z[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
           if (!ok) break;
           zero_rows<D>(ty, n, tid);
-          zero_rows<D>(ty + L::kTile, n, tid);
+          zero_rows<D>(smem + L::kZOff + st * L::kTile, n, tid);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&br.fixed);
         }
         if (!ok) break;
-        if (!updates(po, c)) {
+        // y, in registers while the last products run
+        const uint4* from = reinterpret_cast<const uint4*>(ty) + tid;
+        uint4* to = reinterpret_cast<uint4*>(smem + L::kWOff) + tid;
+        uint4 lo[kVecs];  // y, then what hi leaves of it
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) lo[q] = from[kStateThreads * q];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&br.empty_y);
+        if (wait_ds) {
+          ok = mbar_wait_warp(&br.ds_full, (uint32_t)(ku - 1) & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (upd) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int j = (tid >> 3) + 32 * u;  // row of pieces u, u + 4
+            const float w = j >= n ? 0.f
+                                   : (kRev ? p.scale * linear_power(l2, j + 1)
+                                           : linear_power(l2, n - 1 - j));
+#pragma unroll
+            for (int q = u; q < kVecs; q += 4) {
+              uint4 hi;
+              split_vec(lo[q], w, hi, lo[q]);
+              to[kStateThreads * q] = hi;
+            }
+          }
+        }
+        hand_over(upd, linear_power(l2, n));
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (upd) mbar_arrive(&br.y_hi);
+          mbar_arrive(&br.m_op);
+        }
+        wait_ds = upd;
+        if (!upd) {  // the operand's reader, before the next portion's
           ok = mbar_wait_warp(&br.o_full, (uint32_t)k & 1, abort_flag, p.status);
           if (!ok) break;
           continue;
         }
-        ok = mbar_wait_warp(&br.s_full, (uint32_t)k & 1, abort_flag, p.status);
-        if (!ok) break;
-        uint4 lo[kVecs];
-#pragma unroll
-        for (int q = 0; q < kVecs; ++q) {
-          float w = w_full[q & 3];
-          if (n < kTok) {
-            const int j = (tid >> 3) + 32 * (q & 3);
-            w = j >= n ? 0.f : (kRev ? w : linear_power(l2, n - 1 - j));
-          }
-          uint4* at = reinterpret_cast<uint4*>(ty) + tid + kStateThreads * q;
-          uint4 hi;
-          split_vec(*at, w, hi, lo[q]);
-          *at = hi;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&br.y_hi);
-        const uint32_t pu = (uint32_t)(ku++) & 1;
-        ok = mbar_wait_warp(&br.hi_done, pu, abort_flag, p.status);
+        ok = mbar_wait_warp(&br.hi_done, (uint32_t)(ku++) & 1, abort_flag, p.status);
         if (!ok) break;
 #pragma unroll
-        for (int q = 0; q < kVecs; ++q)
-          reinterpret_cast<uint4*>(ty)[tid + kStateThreads * q] = lo[q];
+        for (int q = 0; q < kVecs; ++q) to[kStateThreads * q] = lo[q];
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&br.y_lo);
-        ok = mbar_wait_warp(&br.ds_full, pu, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        const float g = n == kTok ? g_full : linear_power(l2, n);
+      }
+      if (ok && fin) {
+        if (wait_ds) {
+          ok = mbar_wait_warp(&br.ds_full, (uint32_t)(ku - 1) & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        float* dst = p.final_state + ((size_t)po.bh * D + r) * D + half * kCols;
 #pragma unroll
         for (int b = 0; b < kCols / 32; ++b) {
           uint32_t v[32];
-          tmem_ld32(ds_tm + 32 * b, v);
+          tmem_ld32(m_tm + 32 * b, v);
           tmem_ld_wait();
           reg_fence32(v);
+          if (mine) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            m[32 * b + e] = fmaf(g, m[32 * b + e], __uint_as_float(v[e]));
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(dst + 32 * b + e) =
+                  make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          }
+          __syncwarp();
         }
-        // ds_full also says that O2 of this tile has read the operand
-        if (c + 1 < po.live) write_operand();
-      }
-      if (ok && is_final(po) && mine) {
-        float* dst = p.final_state + ((size_t)po.bh * D + r) * D + half * kCols;
-#pragma unroll
-        for (int i = 0; i < kCols; i += 4)
-          *reinterpret_cast<float4*>(dst + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+        tc_fence_before();
       }
     }
   }

@@ -217,6 +217,40 @@ def test_state_in_place_and_repeats():
             assert torch.equal(p, r)
 
 
+def test_tensors_on_odd_16_byte_boundaries():
+    """Pointers need 16-byte alignment only."""
+    import long_context_attention_causal_gb300 as pa
+    B, H, T, d = 1, 3, 333, 64
+    for dtype in ("bf16", "f32"):
+        x = make(B, H, T, d, dtype, 6, True)
+        want = pa.linear_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=x["state"],
+                             want_state=True)
+        gwant = pa.linear_bwd(x["q"], x["k"], x["v"], x["log_decay"], x["dmem"],
+                              state=x["state"], want_dstate=True)
+
+        def shifted(t):
+            buf = torch.empty(t.numel() + 64, dtype=t.dtype, device=t.device)
+            off = next(o for o in range(64) if (buf.data_ptr() + o * t.element_size()) % 32 == 16)
+            return buf[off:off + t.numel()].view(t.shape).copy_(t)
+
+        y = {n: shifted(t) for n, t in x.items() if n != "log_decay"}
+        mem, S = shifted(x["q"]), shifted(x["state"])
+        pa.linear_fwd(y["q"], y["k"], y["v"], x["log_decay"], state=y["state"], mem=mem,
+                      state_out=S)
+        assert torch.equal(mem, want[0]) and torch.equal(S, want[1])
+        g = [shifted(x["q"]) for _ in range(3)] + [shifted(x["state"])]
+        pa.linear_bwd(y["q"], y["k"], y["v"], x["log_decay"], y["dmem"], state=y["state"], dq=g[0],
+                      dk=g[1], dv=g[2], dstate=g[3])
+        for a, b in zip(g, gwant):
+            assert torch.equal(a, b)
+        tok = [shifted(x[n][:, :, 0].contiguous()) for n in ("q", "k", "v")]
+        S1, S2 = x["state"].clone(), shifted(x["state"])
+        a = pa.linear_step(S1, *(x[n][:, :, 0].contiguous() for n in ("q", "k", "v")),
+                           x["log_decay"])
+        b = pa.linear_step(S2, *tok, x["log_decay"], mem=shifted(a))
+        assert torch.equal(a, b) and torch.equal(S1, S2)
+
+
 def test_empty_prompt_passes_the_state():
     import long_context_attention_causal_gb300 as pa
     z = torch.empty((2, 3, 0, 64), device=dev())
