@@ -123,8 +123,10 @@ struct LinearStateArgs {
 cudaError_t launch_linear_states(const LinearStateArgs& a, cudaStream_t s);
 cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s);
 cudaError_t launch_linear_out(const LinearArgs& a, cudaStream_t s);
-// bf16 on the tensor cores.  maps: x, y, z, out / y, z (128-row boxes).
-cudaError_t launch_linear_out_tc(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s);
+// bf16 on the tensor cores: n applications (1, or 2 that differ in tensors and
+// states only).  maps: x, y, z, out of each / y, z (128-row boxes).
+cudaError_t launch_linear_out_tc(const LinearArgs* a, int n, const CUtensorMap* maps,
+                                 cudaStream_t s);
 cudaError_t launch_linear_states_tc(const LinearStateArgs& a, const CUtensorMap* maps,
                                     cudaStream_t s);
 // final = init (or zero) for prompts without tokens.

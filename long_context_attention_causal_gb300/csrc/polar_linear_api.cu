@@ -76,13 +76,23 @@ int run_states(const LinearStateArgs& a, int dtype, cudaStream_t s) {
   return cuda_status("linear scan launch", launch_linear_scan(a, s));
 }
 
-int run_out(const LinearArgs& a, int dtype, cudaStream_t s) {
-  if (dtype != POLAR_BF16) return cuda_status("linear output launch", launch_linear_out(a, s));
-  CUtensorMap maps[4];
-  const void* bases[4] = {a.x, a.y, a.z, a.out};
-  for (int i = 0; i < 4; ++i)
-    if (!make_map(&maps[i], bases[i], a.B * a.H, a.T, a.d)) return POLAR_ERR_CUDA;
-  return cuda_status("linear output launch", launch_linear_out_tc(a, maps, s));
+// n applications of the recurrence (1, or 2 that read the same tensors).
+int run_out(const LinearArgs* a, int n, int dtype, cudaStream_t s) {
+  if (dtype != POLAR_BF16) {
+    for (int i = 0; i < n; ++i) {
+      const int st = cuda_status("linear output launch", launch_linear_out(a[i], s));
+      if (st != POLAR_OK) return st;
+    }
+    return POLAR_OK;
+  }
+  CUtensorMap maps[8];
+  for (int i = 0; i < n; ++i) {
+    const void* bases[4] = {a[i].x, a[i].y, a[i].z, a[i].out};
+    for (int t = 0; t < 4; ++t)
+      if (!make_map(&maps[4 * i + t], bases[t], a[i].B * a[i].H, a[i].T, a[i].d))
+        return POLAR_ERR_CUDA;
+  }
+  return cuda_status("linear output launch", launch_linear_out_tc(a, n, maps, s));
 }
 
 }  // namespace
@@ -137,7 +147,7 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   }
   const LinearArgs a{q, k, v, mem, log_decay, lengths, B, H, T, d, scale, false, false,
                      g, copy ? copy : state_in, cuts, state_out, status};
-  return run_out(a, dtype, s);
+  return run_out(&a, 1, dtype, s);
 }
 
 int polar_linear_step(float* state, const void* q, const void* k, const void* v,
@@ -193,22 +203,29 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
                              g, state_in, cuts_s, status, nullptr};
     const LinearStateArgs ar{q, dmem, log_decay, lengths, B, H, T, d, scale, true,
                              g, dstate_out, cuts_r, status, copy};
-    st = run_states(as, dtype, s);
-    if (st == POLAR_OK) st = run_states(ar, dtype, s);
+    // dq's states last: its kernel then starts on tiles that are still in L2
+    st = run_states(ar, dtype, s);
+    if (st == POLAR_OK) st = run_states(as, dtype, s);
     if (st != POLAR_OK) return st;
   }
   const LinearArgs aq{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
                       g, state_in, cuts_s, nullptr, status};
-  const LinearArgs ak{v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
-                      g, dstate_out, cuts_r, nullptr, status};
-  // last: it may write dstate_in over dstate_out, which dk's kernel reads
-  const LinearArgs av{k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
-                      g, copy ? copy : dstate_out, cuts_r, dstate_in, status};
-  for (const LinearArgs* a : {&aq, &ak, &av}) {
-    st = run_out(*a, dtype, s);
+  // dk and dv read the same four tensors: one launch, unless dv's CTA would
+  // write dstate_in over the dstate_out that dk's has yet to read.
+  const float* r_init = copy ? copy : dstate_out;
+  const LinearArgs akv[2] = {
+      {v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
+       g, r_init, cuts_r, nullptr, status},
+      {k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
+       g, r_init, cuts_r, dstate_in, status}};
+  st = run_out(&aq, 1, dtype, s);
+  if (st != POLAR_OK) return st;
+  if (dstate_in && r_init == dstate_in) {
+    st = run_out(&akv[0], 1, dtype, s);
     if (st != POLAR_OK) return st;
+    return run_out(&akv[1], 1, dtype, s);
   }
-  return POLAR_OK;
+  return run_out(akv, 2, dtype, s);
 }
 
 }  // extern "C"

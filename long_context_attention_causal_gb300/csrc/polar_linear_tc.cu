@@ -71,13 +71,19 @@ struct OutLayout {
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
+struct OutMaps {
+  CUtensorMap m[2][4];  // x, y, z, out of each application
+};
+
 struct OutParams {
   const float* log_decay;
   const int* lengths;
-  const float *init, *cuts;  // see LinearArgs
-  float* final_state;
-  __nv_bfloat16* out;
-  int BH, H, T, state_t;
+  const float *init[2], *cuts[2];  // see LinearArgs
+  float* final_state[2];
+  __nv_bfloat16* out[2];
+  int state_t[2];
+  int ops;  // applications in this launch: 1 or 2
+  int BH, H, T;
   LinearSplit split;
   float scale;
   int* status;
@@ -132,17 +138,21 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int n, int tid) {
 // tiles with rows to zero (kf) for the phases of the barriers.
 template <int D, bool kRev>
 __global__ void __launch_bounds__(kThreads, 1)
-    polar_linear_out_tc_kernel(const __grid_constant__ CUtensorMap map_x,
-                               const __grid_constant__ CUtensorMap map_y,
-                               const __grid_constant__ CUtensorMap map_z,
-                               const __grid_constant__ CUtensorMap map_o, const OutParams p) {
+    polar_linear_out_tc_kernel(const __grid_constant__ OutMaps maps, const OutParams p) {
   using L = OutLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   OutBars& br = *reinterpret_cast<OutBars*>(smem + L::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_po = linear_portions(p.split, p.BH, blockIdx.x);
+  // two applications of one run are neighbours: they read the same tensors at
+  // about the same time, the second from L2
+  const int op = p.ops == 2 ? (int)(blockIdx.x & 1) : 0;
+  const int part = p.ops == 2 ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const CUtensorMap &map_x = maps.m[op][0], &map_y = maps.m[op][1], &map_z = maps.m[op][2],
+                    &map_o = maps.m[op][3];
+  float* const final_state = p.final_state[op];
+  const int n_po = linear_portions(p.split, p.BH, part);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -175,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = br.tmem_base;
   volatile int* abort_flag = &br.abort_flag;
   auto portion = [&](int i) {
-    return linear_portion(p.split, p.BH, p.H, p.T, p.lengths, p.status, blockIdx.x,
+    return linear_portion(p.split, p.BH, p.H, p.T, p.lengths, p.status, part,
                           kRev ? n_po - 1 - i : i);
   };
   // the c-th live tile of a portion
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto ragged = [&](int tile, int n) { return n < kTok && tile * kTok + n < p.T; };
   // the portion holds the head's last tile in walking order
   auto is_final = [&](const LinearPortion& po) {
-    return p.final_state != nullptr && !(kRev ? po.cut_left : po.cut_right);
+    return final_state != nullptr && !(kRev ? po.cut_left : po.cut_right);
   };
   // the state after tile c is read by tile c + 1, or is the final one
   auto updates = [&](const LinearPortion& po, int c) { return c + 1 < po.live || is_final(po); };
@@ -467,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // tiles past the sequence
       const int t0 = po.row(po.first + po.live), t1 = min(po.row(po.last), p.T);
-      uint4* tail = reinterpret_cast<uint4*>(p.out + ((size_t)po.bh * p.T + t0) * D);
+      uint4* tail = reinterpret_cast<uint4*>(p.out[op] + ((size_t)po.bh * p.T + t0) * D);
       for (long long i = r; i < (long long)(t1 - t0) * (D / 8); i += 128)
         tail[i] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -524,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the incoming state (every reader of the last portion's is done)
         const float* src =
             (kRev ? po.cut_right : po.cut_left)
-                ? p.cuts + (size_t)(kRev ? blockIdx.x + 1 : blockIdx.x - 1) * D * D
-                : (p.init ? p.init + (size_t)po.bh * D * D : nullptr);
+                ? p.cuts[op] + (size_t)(kRev ? part + 1 : part - 1) * D * D
+                : (p.init[op] ? p.init[op] + (size_t)po.bh * D * D : nullptr);
 #pragma unroll
         for (int b = 0; b < kCols / 32; ++b) {
           const int col = half * kCols + 32 * b;
@@ -533,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!src || !mine) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0u;
-          } else if (p.state_t) {
+          } else if (p.state_t[op]) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               v[e] = __float_as_uint(src[(size_t)(col + e) * D + r]);
@@ -624,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
         }
-        float* dst = p.final_state + ((size_t)po.bh * D + r) * D + half * kCols;
+        float* dst = final_state + ((size_t)po.bh * D + r) * D + half * kCols;
 #pragma unroll
         for (int b = 0; b < kCols / 32; ++b) {
           uint32_t v[32];
@@ -656,22 +666,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Each run's own part of the head that its boundary cuts: one accumulator in
 // TMEM over the tiles, y weighted by the distance to the cut, hi and lo, so
-// nothing is ever rescaled.
+// nothing is ever rescaled.  hi replaces y, lo goes through one buffer of its
+// own.  The tiles are walked so that those the output kernel starts with come
+// last: it then finds them in L2.  Bound: HBM (64 KB a tile at d = 128).
 constexpr int kSThreads = 320;  // 8 scaling warps, TMA, MMA
 constexpr int kSWarpTMA = 8, kSWarpMMA = 9;
 
 template <int D>
 struct StateLayout {
-  static constexpr int kNS = D == 128 ? 2 : 4;
+  static constexpr int kNS = D == 128 ? 3 : 6;
   static constexpr int kTile = kTok * D * 2;
   static constexpr int kAtom = kTok * 128;
-  static constexpr int kStage = 3 * kTile;  // y (then hi), z, lo
-  static constexpr int kBarOff = kNS * kStage;
-  static constexpr int kSmemBytes = kBarOff + 256 + 1024;
+  static constexpr int kStage = 2 * kTile;  // y (then hi), z
+  static constexpr int kLoOff = kNS * kStage;
+  static constexpr int kBarOff = kLoOff + kTile;
+  static constexpr int kSmemBytes = kBarOff + 512 + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
 struct StateBars {
-  uint64_t full[4], empty[4], scaled[4], done, drain;
+  uint64_t full[6], empty[6], hi[6];
+  uint64_t lo, lo_free;  // one phase a tile
+  uint64_t done, drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -709,8 +725,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
     for (int i = 0; i < NS; ++i) {
       mbar_init(&br.full[i], 1);
       mbar_init(&br.empty[i], 1);
-      mbar_init(&br.scaled[i], kStateWarps);
+      mbar_init(&br.hi[i], kStateWarps);
     }
+    mbar_init(&br.lo, kStateWarps);
+    mbar_init(&br.lo_free, 1);
     mbar_init(&br.done, 1);
     mbar_init(&br.drain, 1);
     br.abort_flag = 0;
@@ -722,6 +740,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   tc_fence_after();
   const uint32_t tmem = br.tmem_base;
   volatile int* abort_flag = &br.abort_flag;
+  auto tile_row = [&](int c) { return t0 + (p.reverse ? c : nt - 1 - c) * kTok; };
 
   if (warp == kSWarpTMA) {
     if (lane == 0) {
@@ -739,9 +758,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
       uint8_t* sy = smem + st * L::kStage;
       mbar_arrive_expect_tx_warp(&br.full[st], 2 * L::kTile);
       for (int h = 0; h < D / 64; ++h) {
-        tma_load_3d_warp(sy + h * L::kAtom, &map_y, &br.full[st], 64 * h, t0 + c * kTok, bh);
-        tma_load_3d_warp(sy + L::kTile + h * L::kAtom, &map_z, &br.full[st], 64 * h,
-                         t0 + c * kTok, bh);
+        tma_load_3d_warp(sy + h * L::kAtom, &map_y, &br.full[st], 64 * h, tile_row(c), bh);
+        tma_load_3d_warp(sy + L::kTile + h * L::kAtom, &map_z, &br.full[st], 64 * h, tile_row(c),
+                         bh);
       }
       issued = c + 1;
     }
@@ -759,19 +778,23 @@ __global__ void __launch_bounds__(kSThreads, 1)
     bool ok = true, any = false;
     for (int c = 0; c < nt; ++c) {
       const int st = c % NS;
-      ok = mbar_wait_warp(&br.scaled[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
+      ok = mbar_wait_warp(&br.hi[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
-      const uint64_t y0 = mn + at(st * L::kStage), z0 = y0 + at(L::kTile), l0 = z0 + at(L::kTile);
+      const uint64_t y0 = mn + at(st * L::kStage), z0 = y0 + at(L::kTile), l0 = mn + at(L::kLoOff);
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
         umma_ss_warp(tmem, z0 + at(kk * 2048), y0 + at(kk * 2048), kId,
                      (c > 0 || kk > 0) ? 1u : 0u);
+      any = true;
+      ok = mbar_wait_warp(&br.lo, (uint32_t)c & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
         umma_ss_warp(tmem, z0 + at(kk * 2048), l0 + at(kk * 2048), kId, 1u);
+      umma_commit_warp(&br.lo_free);
       umma_commit_warp(&br.empty[st]);
-      any = true;
     }
     if (ok && any) umma_commit_warp(&br.done);
     if (!ok && any) {
@@ -785,32 +808,41 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const int tid = threadIdx.x;
     bool ok = true;
     for (int c = 0; c < nt; ++c) {
-      const int st = c % NS, row = t0 + c * kTok, n = min(kTok, t1 - row);
+      const int st = c % NS, row = tile_row(c), n = min(kTok, t1 - row);
       ok = mbar_wait_warp(&br.full[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
       if (!ok) break;
       uint8_t* ty = smem + st * L::kStage;
       if (n < kTok) zero_rows<D>(ty + L::kTile, n, tid);
       constexpr int kVecs = kTok * D / 8 / kStateThreads;
-      float w[4];
+      uint4* at = reinterpret_cast<uint4*>(ty) + tid;
+      uint4 lo[kVecs];  // y, then what hi leaves of it
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = row + (tid >> 3) + 32 * k;
-        w[k] = p.scale * linear_power(l2, p.reverse ? t - t0 + 1 : max(t1 - 1 - t, 0));
-      }
+      for (int q = 0; q < kVecs; ++q) lo[q] = at[kStateThreads * q];
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k) {
-        const bool live = (tid >> 3) + 32 * (k & 3) < n;
-        uint4* at = reinterpret_cast<uint4*>(ty) + tid + kStateThreads * k;
-        uint4 hi, lo;
-        split_vec(*at, w[k & 3], hi, lo);
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        *at = live ? hi : zero;
-        *(reinterpret_cast<uint4*>(ty + 2 * L::kTile) + tid + kStateThreads * k) =
-            live ? lo : zero;
+      for (int u = 0; u < 4; ++u) {
+        const int j = (tid >> 3) + 32 * u, t = row + j;  // row of pieces u, u + 4
+        const float w = p.scale * linear_power(l2, p.reverse ? t - t0 + 1 : max(t1 - 1 - t, 0));
+#pragma unroll
+        for (int q = u; q < kVecs; q += 4) {
+          uint4 hi;
+          split_vec(lo[q], w, hi, lo[q]);
+          if (j >= n) hi = lo[q] = make_uint4(0u, 0u, 0u, 0u);
+          at[kStateThreads * q] = hi;
+        }
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&br.scaled[st]);
+      if (lane == 0) mbar_arrive(&br.hi[st]);
+      if (c > 0) {
+        ok = mbar_wait_warp(&br.lo_free, (uint32_t)(c - 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+      }
+      uint4* to = reinterpret_cast<uint4*>(smem + L::kLoOff) + tid;
+#pragma unroll
+      for (int q = 0; q < kVecs; ++q) to[kStateThreads * q] = lo[q];
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&br.lo);
     }
     const int half = warp >> 2, r = threadIdx.x & 127;
     constexpr int kCols = D / 2;
@@ -848,18 +880,36 @@ __global__ void __launch_bounds__(kSThreads, 1)
   }
 }
 
+// n applications (1 or 2) that differ in tensors and states only; maps: x, y,
+// z, out of each.
 template <int D, bool kRev>
-cudaError_t out_tc_d(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s) {
+cudaError_t out_tc_d(const LinearArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
   using L = OutLayout<D>;
-  const OutParams p{a.log_decay, a.lengths, a.init, a.cuts, a.final_state,
-                    static_cast<__nv_bfloat16*>(a.out), a.B * a.H, a.H, a.T, a.state_t ? 1 : 0,
-                    a.split, a.scale, a.status};
+  OutMaps m;
+  OutParams p;
+  p.log_decay = a->log_decay;
+  p.lengths = a->lengths;
+  for (int i = 0; i < 2; ++i) {
+    const int j = i < n ? i : 0;
+    for (int t = 0; t < 4; ++t) m.m[i][t] = maps[4 * j + t];
+    p.init[i] = a[j].init;
+    p.cuts[i] = a[j].cuts;
+    p.final_state[i] = a[j].final_state;
+    p.out[i] = static_cast<__nv_bfloat16*>(a[j].out);
+    p.state_t[i] = a[j].state_t ? 1 : 0;
+  }
+  p.ops = n;
+  p.BH = a->B * a->H;
+  p.H = a->H;
+  p.T = a->T;
+  p.split = a->split;
+  p.scale = a->scale;
+  p.status = a->status;
   auto kern = polar_linear_out_tc_kernel<D, kRev>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAsked);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)a.split.parts, kThreads, L::kAsked, s>>>(maps[0], maps[1], maps[2], maps[3],
-                                                            p);
+  kern<<<(unsigned)a->split.parts * n, kThreads, L::kAsked, s>>>(m, p);
   return cudaGetLastError();
 }
 
@@ -879,10 +929,11 @@ cudaError_t state_tc_d(const LinearStateArgs& a, const CUtensorMap* maps, cudaSt
 
 }  // namespace
 
-cudaError_t launch_linear_out_tc(const LinearArgs& a, const CUtensorMap* maps, cudaStream_t s) {
-  if (a.d == 64)
-    return a.reverse ? out_tc_d<64, true>(a, maps, s) : out_tc_d<64, false>(a, maps, s);
-  return a.reverse ? out_tc_d<128, true>(a, maps, s) : out_tc_d<128, false>(a, maps, s);
+cudaError_t launch_linear_out_tc(const LinearArgs* a, int n, const CUtensorMap* maps,
+                                 cudaStream_t s) {
+  if (a->d == 64)
+    return a->reverse ? out_tc_d<64, true>(a, n, maps, s) : out_tc_d<64, false>(a, n, maps, s);
+  return a->reverse ? out_tc_d<128, true>(a, n, maps, s) : out_tc_d<128, false>(a, n, maps, s);
 }
 
 cudaError_t launch_linear_states_tc(const LinearStateArgs& a, const CUtensorMap* maps,
