@@ -52,31 +52,32 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
   return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
 }
 
-// Rows [t0, t0 + kC) x D of a tensor into shared memory (row stride D + 4),
-// zeros from token `end` on: what lies past a sequence may be anything.
-template <int D, typename T>
-__device__ __forceinline__ void load_rows(float (*dst)[D + 4], const T* src, int t0, int end) {
-  constexpr int kV = D / 4;
-  for (int i = threadIdx.x; i < kC * kV; i += kThreads) {
-    const int r = i / kV, c = (i % kV) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t0 + r < end) x = load4<T>(src + (size_t)(t0 + r) * D + c);
-    *reinterpret_cast<float4*>(&dst[r][c]) = x;
+// The thread's pieces of rows [t0, t0 + kC) x W of a tensor, on their way to
+// shared memory: loaded while the chunk before is computed, so that a chunk
+// costs one memory latency at most.  Zeros from token `end` on: what lies past
+// a sequence may be anything.
+template <int W>
+struct Pieces {
+  static constexpr int kV = W / 4, kN = kC * kV / kThreads;
+  float4 v[kN];
+  template <typename T>
+  __device__ __forceinline__ void load(const T* src, int ld, int t0, int end) {
+#pragma unroll
+    for (int u = 0; u < kN; ++u) {
+      const int i = threadIdx.x + u * kThreads, r = i / kV, c = (i % kV) * 4;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t0 + r < end) v[u] = load4<T>(src + (size_t)(t0 + r) * ld + c);
+    }
   }
-}
-
-// Columns [z0, z0 + kZ) of the same rows.
-template <int D, typename T>
-__device__ __forceinline__ void load_cols(float (*dst)[kZ], const T* src, int t0, int end,
-                                          int z0) {
-  constexpr int kV = kZ / 4;
-  for (int i = threadIdx.x; i < kC * kV; i += kThreads) {
-    const int r = i / kV, c = (i % kV) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t0 + r < end) x = load4<T>(src + (size_t)(t0 + r) * D + z0 + c);
-    *reinterpret_cast<float4*>(&dst[r][c]) = x;
+  template <int S>
+  __device__ __forceinline__ void store(float (*dst)[S]) const {
+#pragma unroll
+    for (int u = 0; u < kN; ++u) {
+      const int i = threadIdx.x + u * kThreads, r = i / kV, c = (i % kV) * 4;
+      *reinterpret_cast<float4*>(&dst[r][c]) = v[u];
+    }
   }
-}
+};
 
 // The thread's share of a 32 x D state: rows r0 .. r0 + kR - 1, four columns.
 template <int D>
@@ -134,19 +135,24 @@ __global__ void __launch_bounds__(kThreads)
   float4 acc[S::kR];
 #pragma unroll
   for (int r = 0; r < S::kR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  Pieces<D> py;
+  Pieces<kZ> pz;
+  py.load(y, D, t0, t1);
+  pz.load(z + z0, D, t0, t1);
   for (int c0 = t0; c0 < t1; c0 += kC) {
     __syncthreads();
-    load_rows<D, T>(sm.y, y, c0, t1);
-    for (int i = threadIdx.x; i < kC * (kZ / 4); i += kThreads) {
-      const int r = i / (kZ / 4), c = (i % (kZ / 4)) * 4, t = c0 + r;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < t1) {
-        v = load4<T>(z + (size_t)t * D + z0 + c);
-        const float w = a.scale * linear_power(l2, a.reverse ? t - t0 + 1 : t1 - 1 - t);
-        v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
-      }
-      *reinterpret_cast<float4*>(&sm.zw[r][c]) = v;
+    py.store(sm.y);
+#pragma unroll
+    for (int u = 0; u < Pieces<kZ>::kN; ++u) {
+      const int t = c0 + (threadIdx.x + u * kThreads) / Pieces<kZ>::kV;
+      const float w =
+          t < t1 ? a.scale * linear_power(l2, a.reverse ? t - t0 + 1 : t1 - 1 - t) : 0.f;
+      float4& v = pz.v[u];
+      v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
     }
+    pz.store(sm.zw);
+    py.load(y, D, c0 + kC, t1);
+    pz.load(z + z0, D, c0 + kC, t1);
     __syncthreads();
     state_products<D>(acc, sm.y, sm.zw);
   }
@@ -261,15 +267,24 @@ __global__ void __launch_bounds__(kThreads)
   // state already carries it
   const float s_in = a.reverse ? 1.f : a.scale, s_z = a.reverse ? a.scale : 1.f;
   const int n_ch = (t1 - t0 + kC - 1) / kC;
+  const int end = min(len, t1);
+  auto chunk = [&](int ci) { return t0 + (a.reverse ? n_ch - 1 - ci : ci) * kC; };
+  Pieces<D> px, py;
+  Pieces<kZ> pz;
+  auto fetch = [&](int c0) {
+    px.load(x, D, c0, end);
+    py.load(y, D, c0, end);
+    pz.load(z + z0, D, c0, end);
+  };
+  fetch(chunk(0));
   for (int ci = 0; ci < n_ch; ++ci) {
-    const int c0 = t0 + (a.reverse ? n_ch - 1 - ci : ci) * kC;
-    const int n = min(max(len - c0, 0), min(kC, t1 - c0));  // tokens of the chunk
+    const int c0 = chunk(ci);
+    const int n = min(max(end - c0, 0), kC);  // tokens of the chunk
     __syncthreads();
-    if (n > 0) {
-      load_rows<D, T>(sm.x, x, c0, c0 + n);
-      load_rows<D, T>(sm.y, y, c0, c0 + n);
-      load_cols<D, T>(sm.z, z, c0, c0 + n, z0);
-    }
+    px.store(sm.x);
+    py.store(sm.y);
+    pz.store(sm.z);
+    if (ci + 1 < n_ch) fetch(chunk(ci + 1));
     __syncthreads();
     float o[4][2];
 #pragma unroll

@@ -8,6 +8,7 @@ device is not an sm_103 GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -50,6 +51,8 @@ def default_consts(floor_order: int = 1) -> Consts:
 def lib() -> ctypes.CDLL:
     """Load libpolarattn.so (build it first with __graft_entry__.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -479,6 +482,85 @@ def memory_step(state, q, k, v, alpha, beta, mem=None, eps=1e-6, stream=None):
     return mem
 
 
+# The calls below are made once a token and layer, where the host's time
+# counts: an argument is checked in one expression, and only one that fails
+# goes through the checks that name what is wrong.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _fail(t, name, dtype, shape, dev):
+    _dev(t, name, dtype)
+    _shape(t, name, shape)
+    raise ValueError(f"{name} must be on cuda:{dev}, like the first tensor, got {t.device}")
+
+
+def _in(t, name, dtype, shape, dev):
+    """Address of a tensor argument after its checks (0 for None)."""
+    if t is None:
+        return 0
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        _fail(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _need(t, name):
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t
+
+
+def _call(dev, where, f, *args):
+    """f(*args, stream) on `dev` and its current stream."""
+    if _raw_stream is not None:
+        raw = _raw_stream(dev)
+    else:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        st = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, raw)
+    if st != 0:
+        raise PolarError(st, where)
+
+
+def _on_stream(f):
+    """Adds the argument `stream`: the call, and what it allocates, belong to
+    that stream then."""
+    @functools.wraps(f)
+    def call(first, *args, stream=None, **kw):
+        if stream is None:
+            return f(first, *args, **kw)
+        if isinstance(first, torch.Tensor) and first.is_cuda and first.device != stream.device:
+            raise ValueError(f"the tensors are on {first.device}, the stream on {stream.device}")
+        with torch.cuda.stream(stream):
+            return f(first, *args, **kw)
+    return call
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(name, dev, *sizes):
+    """Workspace bytes of a call on device `dev` (None: the current one)."""
+    if dev is None or dev == torch.cuda.current_device():
+        return int(getattr(lib(), name)(*sizes))
+    with torch.cuda.device(dev):
+        return int(getattr(lib(), name)(*sizes))
+
+
+def _scratch(workspace, need, dev):
+    """(address, bytes, tensor to keep) of the caller's workspace or a new one."""
+    if workspace is None:
+        workspace = torch.empty(need if need > 16 else 16, device=torch.device("cuda", dev),
+                                dtype=torch.uint8)
+        return workspace.data_ptr(), need, workspace
+    _dev(workspace, "workspace")
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def linear_workspace_bytes(B, H, T, d, dtype=torch.bfloat16) -> int:
     code = 1 if dtype == torch.bfloat16 else 0
     return int(lib().polar_linear_workspace_bytes(B, H, T, d, code))
@@ -489,128 +571,88 @@ def linear_bwd_workspace_bytes(B, H, T, d, dtype=torch.bfloat16) -> int:
     return int(lib().polar_linear_bwd_workspace_bytes(B, H, T, d, code))
 
 
-def _same_device(q, *tensors):
-    for t in tensors:
-        if t is not None and t.device != q.device:
-            raise ValueError(f"all tensors must be on {q.device}, got one on {t.device}")
-
-
-def _linear_args(q, k, v, log_decay, state, lengths, scale):
-    """Checks shared by linear_fwd and linear_bwd; returns (B, H, T, d, scale)."""
-    _dev(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, H, T, d]")
-    B, H, T, d = q.shape
-    for name, t in (("k", k), ("v", v)):
-        _dev(t, name, q.dtype)
-        _shape(t, name, q.shape)
-    _dev(log_decay, "log_decay", torch.float32)
-    _shape(log_decay, "log_decay", (H,))
-    _dev(state, "state", torch.float32)
-    _shape(state, "state", (B, H, d, d))
-    _dev(lengths, "lengths", torch.int32)
-    _shape(lengths, "lengths", (B,))
-    _same_device(q, k, v, log_decay, state, lengths)
-    return B, H, T, d, (d ** -0.5 if scale is None else float(scale))
-
-
-def _workspace(workspace, need, q):
-    if workspace is None:
-        return torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
-    _dev(workspace, "workspace")
-    _same_device(q, workspace)
-    return workspace
-
-
+@_on_stream
 def linear_fwd(q, k, v, log_decay, state=None, lengths=None, scale=None, mem=None,
-               state_out=None, want_state=False, workspace=None, stream=None):
+               state_out=None, want_state=False, workspace=None):
     """Decayed linear attention over a prompt (a memory stream whose decay is
     one number per head): q, k, v [B, H, T, d] (bf16 or fp32); log_decay [H]
     fp32, <= 0; state [B, H, d, d] fp32 or None (zero); lengths [B] int32 or
     None (all T): tokens of a padded batch.  scale defaults to d ** -0.5.
     Returns (mem [B, H, T, d], state after the last token or None); rows of
     mem past a length are zero.  state_out may be state."""
-    B, H, T, d, scale = _linear_args(q, k, v, log_decay, state, lengths, scale)
+    _dev(_need(q, "q"), "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, d]")
+    B, H, T, d = shape = q.shape
+    dt, dev, code = q.dtype, q.get_device(), _dtype_code(q)
     if mem is None:
         mem = torch.empty_like(q)
+    square = (B, H, d, d)
     if state_out is None and want_state:
-        state_out = torch.empty((B, H, d, d), device=q.device, dtype=torch.float32)
-    _dev(mem, "mem", q.dtype)
-    _shape(mem, "mem", q.shape)
-    _dev(state_out, "state_out", torch.float32)
-    _shape(state_out, "state_out", (B, H, d, d))
-    _same_device(q, mem, state_out)
-    code = _dtype_code(q)
-    with torch.cuda.device(q.device):
-        need = int(lib().polar_linear_workspace_bytes(B, H, T, d, code))
-        workspace = _workspace(workspace, need, q)
-        st = lib().polar_linear_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(mem),
-            _ptr(state_out), B, H, T, d, code, scale, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "polar_linear_fwd")
+        state_out = torch.empty(square, device=q.device, dtype=torch.float32)
+    f32 = torch.float32
+    need = _bytes("polar_linear_workspace_bytes", dev, B, H, T, d, code)
+    ws, size, _ = _scratch(workspace, need, dev) if need or workspace is not None else (0, 0, None)
+    _call(dev, "polar_linear_fwd", lib().polar_linear_fwd, q.data_ptr(),
+          _in(_need(k, "k"), "k", dt, shape, dev), _in(_need(v, "v"), "v", dt, shape, dev),
+          _in(_need(log_decay, "log_decay"), "log_decay", f32, (H,), dev),
+          _in(lengths, "lengths", torch.int32, (B,), dev), _in(state, "state", f32, square, dev),
+          _in(mem, "mem", dt, shape, dev), _in(state_out, "state_out", f32, square, dev),
+          B, H, T, d, code, d ** -0.5 if scale is None else scale, ws, size)
     return mem, state_out
 
 
-def linear_step(state, q, k, v, log_decay, scale=None, mem=None, stream=None):
+@_on_stream
+def linear_step(state, q, k, v, log_decay, scale=None, mem=None):
     """One token of the decayed linear attention, the state updated in place:
     state [B, H, d, d] fp32; q, k, v [B, H, d] (bf16 or fp32); log_decay [H]
     fp32.  Returns mem [B, H, d]."""
-    _dev(state, "state", torch.float32)
-    _dev(q, "q")
+    _dev(_need(q, "q"), "q")
     if q.dim() != 3:
         raise ValueError("q must be [B, H, d]")
-    B, H, d = q.shape
-    for name, t in (("k", k), ("v", v)):
-        _dev(t, name, q.dtype)
-        _shape(t, name, q.shape)
-    _shape(state, "state", (B, H, d, d))
-    _dev(log_decay, "log_decay", torch.float32)
-    _shape(log_decay, "log_decay", (H,))
+    B, H, d = shape = q.shape
+    dt, dev = q.dtype, q.get_device()
     if mem is None:
         mem = torch.empty_like(q)
-    _dev(mem, "mem", q.dtype)
-    _shape(mem, "mem", q.shape)
-    _same_device(q, state, k, v, log_decay, mem)
-    with torch.cuda.device(q.device):
-        st = lib().polar_linear_step(
-            _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(mem), B, H, d,
-            _dtype_code(q), d ** -0.5 if scale is None else float(scale), _stream(stream))
-    _check(st, "polar_linear_step")
+    _call(dev, "polar_linear_step", lib().polar_linear_step,
+          _in(_need(state, "state"), "state", torch.float32, (B, H, d, d), dev), q.data_ptr(),
+          _in(_need(k, "k"), "k", dt, shape, dev), _in(_need(v, "v"), "v", dt, shape, dev),
+          _in(_need(log_decay, "log_decay"), "log_decay", torch.float32, (H,), dev),
+          _in(mem, "mem", dt, shape, dev), B, H, d, _dtype_code(q),
+          d ** -0.5 if scale is None else scale)
     return mem
 
 
+@_on_stream
 def linear_bwd(q, k, v, log_decay, dmem, state=None, dstate_out=None, lengths=None, scale=None,
-               dq=None, dk=None, dv=None, dstate=None, want_dstate=False, workspace=None,
-               stream=None):
+               dq=None, dk=None, dv=None, dstate=None, want_dstate=False, workspace=None):
     """Gradients of linear_fwd: dmem [B, H, T, d] in q's type and dstate_out
     [B, H, d, d] fp32 (None: zero) are the gradients of its two results.
     Returns (dq, dk, dv in q's type, dstate fp32 or None).  The decay is a
     constant and gets none."""
-    B, H, T, d, scale = _linear_args(q, k, v, log_decay, state, lengths, scale)
-    _dev(dmem, "dmem", q.dtype)
-    _shape(dmem, "dmem", q.shape)
+    _dev(_need(q, "q"), "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, T, d]")
+    B, H, T, d = shape = q.shape
+    dt, dev, code = q.dtype, q.get_device(), _dtype_code(q)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(q) if dk is None else dk
     dv = torch.empty_like(q) if dv is None else dv
-    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-        _dev(t, name, q.dtype)
-        _shape(t, name, q.shape)
+    square = (B, H, d, d)
     if dstate is None and want_dstate:
-        dstate = torch.empty((B, H, d, d), device=q.device, dtype=torch.float32)
-    for name, t in (("dstate_out", dstate_out), ("dstate", dstate)):
-        _dev(t, name, torch.float32)
-        _shape(t, name, (B, H, d, d))
-    _same_device(q, dmem, dq, dk, dv, dstate_out, dstate)
-    code = _dtype_code(q)
-    with torch.cuda.device(q.device):
-        need = int(lib().polar_linear_bwd_workspace_bytes(B, H, T, d, code))
-        workspace = _workspace(workspace, need, q)
-        st = lib().polar_linear_bwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(dmem),
-            _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate), B, H, T, d, code, scale,
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "polar_linear_bwd")
+        dstate = torch.empty(square, device=q.device, dtype=torch.float32)
+    f32 = torch.float32
+    need = _bytes("polar_linear_bwd_workspace_bytes", dev, B, H, T, d, code)
+    ws, size, _ = _scratch(workspace, need, dev) if need or workspace is not None else (0, 0, None)
+    _call(dev, "polar_linear_bwd", lib().polar_linear_bwd, q.data_ptr(),
+          _in(_need(k, "k"), "k", dt, shape, dev), _in(_need(v, "v"), "v", dt, shape, dev),
+          _in(_need(log_decay, "log_decay"), "log_decay", f32, (H,), dev),
+          _in(lengths, "lengths", torch.int32, (B,), dev), _in(state, "state", f32, square, dev),
+          _in(_need(dmem, "dmem"), "dmem", dt, shape, dev),
+          _in(dstate_out, "dstate_out", f32, square, dev), _in(dq, "dq", dt, shape, dev),
+          _in(dk, "dk", dt, shape, dev), _in(dv, "dv", dt, shape, dev),
+          _in(dstate, "dstate", f32, square, dev), B, H, T, d, code,
+          d ** -0.5 if scale is None else scale, ws, size)
     return dq, dk, dv, dstate
 
 
@@ -619,54 +661,52 @@ def decode_paged_weights_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits=
                                                                      num_splits))
 
 
+_DEFAULT_CONSTS = default_consts()
+
+
+@_on_stream
 def decode_paged_weights(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, weights,
                          max_seq_len=None, num_splits=0, workspace=None, out=None, n_eff=None,
-                         conf=None, consts=None, want_conf=False, stream=None):
+                         conf=None, consts=None, want_conf=False):
     """decode_paged that also adds every cache row's attention weight, summed
     over the query heads of its group, to weights [B, Hkv, stride] fp32
     (stride >= max_seq_len).  max_seq_len defaults to the smaller of the
     table's capacity and the stride.  Returns (out, n_eff, conf)."""
-    _dev(q, "q")
-    dt = q.dtype
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages), ("mem", mem)):
-        _dev(t, name, dt)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int32)
-    _dev(w_count, "w_count", torch.float32)
-    _dev(weights, "weights", torch.float32)
-    B, Hq, d = q.shape
-    num_pages, Hkv, page, d2 = k_pages.shape
-    if d2 != d or v_pages.shape != k_pages.shape or tuple(mem.shape) != (B, Hq, d):
-        raise ValueError("shape mismatch between q, mem and the pages")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages]")
-    _shape(seq_lens, "seq_lens", (B,))
-    _shape(w_count, "w_count", (Hq, d))
-    if weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv):
-        raise ValueError("weights must be [B, Hkv, stride]")
+    for name, t in (("q", q), ("k_pages", k_pages), ("block_table", block_table),
+                    ("weights", weights)):
+        _dev(_need(t, name), name)
+    if q.dim() != 3 or k_pages.dim() != 4 or block_table.dim() != 2 or weights.dim() != 3:
+        raise ValueError("q must be [B, Hq, d], the pages [num_pages, Hkv, page, d], block_table "
+                         "[B, max_pages], weights [B, Hkv, stride]")
+    B, Hq, d = shape = q.shape
+    num_pages, Hkv, page, _ = k_pages.shape
     max_pages, stride = block_table.shape[1], weights.shape[2]
+    dt, dev, f32, i32 = q.dtype, q.get_device(), torch.float32, torch.int32
     if max_seq_len is None:
         max_seq_len = min(max_pages * page, stride)
     if out is None:
         out = torch.empty_like(q)
     if n_eff is None:
-        n_eff = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+        n_eff = torch.empty((B, Hq), device=q.device, dtype=f32)
     if conf is None and want_conf:
-        conf = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
-    _dec_outputs(q, out, n_eff, conf, (B, Hq))
-    _same_device(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, weights, out, n_eff,
-                 conf)
-    c = consts or default_consts()
-    with torch.cuda.device(q.device):
-        need = decode_paged_weights_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits)
-        workspace = _workspace(workspace, need, q)
-        st = lib().polar_attn_decode_paged_weights(
-            _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(mem),
-            _ptr(w_count), _ptr(out), _ptr(n_eff), _ptr(conf), _ptr(weights), stride, B, Hq, Hkv,
-            d, page, num_pages, max_pages, int(max_seq_len), _dtype_code(q), ctypes.byref(c),
-            int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
-            _stream(stream))
-    _check(st, "polar_attn_decode_paged_weights")
+        conf = torch.empty((B, Hq), device=q.device, dtype=f32)
+    pages = (num_pages, Hkv, page, d)
+    need = _bytes("polar_attn_decode_paged_weights_workspace_bytes", dev, B, Hq, Hkv,
+                  int(max_seq_len), d, int(num_splits))
+    ws, size, _ = _scratch(workspace, need, dev)
+    c = _DEFAULT_CONSTS if consts is None else consts
+    _call(dev, "polar_attn_decode_paged_weights", lib().polar_attn_decode_paged_weights,
+          q.data_ptr(), _in(k_pages, "k_pages", dt, pages, dev),
+          _in(_need(v_pages, "v_pages"), "v_pages", dt, pages, dev),
+          _in(block_table, "block_table", i32, (B, max_pages), dev),
+          _in(_need(seq_lens, "seq_lens"), "seq_lens", i32, (B,), dev),
+          _in(_need(mem, "mem"), "mem", dt, shape, dev),
+          _in(_need(w_count, "w_count"), "w_count", f32, (Hq, d), dev),
+          _in(out, "out", dt, shape, dev), _in(n_eff, "n_eff", f32, (B, Hq), dev),
+          _in(conf, "conf", f32, (B, Hq), dev),
+          _in(weights, "weights", f32, (B, Hkv, stride), dev), stride, B, Hq, Hkv, d, page,
+          num_pages, max_pages, int(max_seq_len), _dtype_code(q), ctypes.byref(c),
+          int(num_splits), ws, size)
     return out, n_eff, conf
 
 
@@ -674,8 +714,9 @@ def cache_evict_workspace_bytes(B, Hkv, max_seq_len, keep) -> int:
     return int(lib().polar_cache_evict_workspace_bytes(B, Hkv, max_seq_len, keep))
 
 
+@_on_stream
 def cache_evict(k_pages, v_pages, block_table, seq_lens, weights, positions, keep, recent=0,
-                max_seq_len=None, new_lens=None, workspace=None, stream=None):
+                max_seq_len=None, new_lens=None, workspace=None):
     """Cuts every sequence of more than `keep` rows to `keep`, per KV head and
     in place: the rows of the newest `recent` tokens stay, then those of
     largest accumulated weight.
@@ -684,38 +725,30 @@ def cache_evict(k_pages, v_pages, block_table, seq_lens, weights, positions, kee
     and seq_lens [B] int32; weights [B, Hkv, stride] fp32 and positions [B,
     Hkv, stride] int32 move with the rows.  Returns the new lengths [B] int32
     (written into new_lens when given, which may be seq_lens)."""
-    _dev(k_pages, "k_pages")
-    _dev(v_pages, "v_pages", k_pages.dtype)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int32)
-    _dev(weights, "weights", torch.float32)
-    _dev(positions, "positions", torch.int32)
-    num_pages, Hkv, page, d = k_pages.shape
-    _shape(v_pages, "v_pages", k_pages.shape)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
+    for name, t in (("k_pages", k_pages), ("block_table", block_table), ("weights", weights)):
+        _dev(_need(t, name), name)
+    if k_pages.dim() != 4 or block_table.dim() != 2 or weights.dim() != 3:
+        raise ValueError("the pages must be [num_pages, Hkv, page, d], block_table [B, "
+                         "max_pages], weights [B, Hkv, stride]")
+    num_pages, Hkv, page, d = pages = k_pages.shape
     B, max_pages = block_table.shape
-    _shape(seq_lens, "seq_lens", (B,))
-    if weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv):
-        raise ValueError("weights must be [B, Hkv, stride]")
-    _shape(positions, "positions", weights.shape)
     stride = weights.shape[2]
+    dt, dev, i32 = k_pages.dtype, k_pages.get_device(), torch.int32
     if max_seq_len is None:
         max_seq_len = min(max_pages * page, stride)
     if new_lens is None:
-        new_lens = torch.empty_like(seq_lens)
-    _dev(new_lens, "new_lens", torch.int32)
-    _shape(new_lens, "new_lens", (B,))
-    _same_device(k_pages, v_pages, block_table, seq_lens, weights, positions, new_lens)
-    with torch.cuda.device(k_pages.device):
-        need = cache_evict_workspace_bytes(B, Hkv, max_seq_len, int(keep))
-        workspace = _workspace(workspace, need, k_pages)
-        st = lib().polar_cache_evict(
-            _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(weights),
-            _ptr(positions), _ptr(new_lens), B, Hkv, d, page, num_pages, max_pages,
-            int(max_seq_len), stride, _dtype_code(k_pages), int(keep), int(recent),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "polar_cache_evict")
+        new_lens = torch.empty((B,), device=k_pages.device, dtype=i32)
+    need = _bytes("polar_cache_evict_workspace_bytes", dev, B, Hkv, int(max_seq_len), int(keep))
+    ws, size, _ = _scratch(workspace, need, dev)
+    slots = (B, Hkv, stride)
+    _call(dev, "polar_cache_evict", lib().polar_cache_evict, k_pages.data_ptr(),
+          _in(_need(v_pages, "v_pages"), "v_pages", dt, pages, dev),
+          _in(block_table, "block_table", i32, (B, max_pages), dev),
+          _in(_need(seq_lens, "seq_lens"), "seq_lens", i32, (B,), dev),
+          _in(weights, "weights", torch.float32, slots, dev),
+          _in(_need(positions, "positions"), "positions", i32, slots, dev),
+          _in(new_lens, "new_lens", i32, (B,), dev), B, Hkv, d, page, num_pages, max_pages,
+          int(max_seq_len), stride, _dtype_code(k_pages), int(keep), int(recent), ws, size)
     return new_lens
 
 

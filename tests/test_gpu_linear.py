@@ -333,6 +333,25 @@ def test_two_streams_with_two_workspaces():
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+def test_given_stream_owns_what_is_allocated():
+    """Results and workspaces of a call on a given stream are not handed out
+    again by the current stream's allocations while it still runs."""
+    import long_context_attention_causal_gb300 as pa
+    x = make(1, 3, 3000, 128, "bf16", 31, True)
+    args = (x["q"], x["k"], x["v"], x["log_decay"])
+    want = pa.linear_fwd(*args, state=x["state"], want_state=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(6):
+        got.append(pa.linear_fwd(*args, state=x["state"], want_state=True, stream=side))
+        junk = [torch.full((1 << 20,), float("nan"), device=dev()) for _ in range(8)]
+        del junk
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+
+
 def test_refusals():
     import long_context_attention_causal_gb300 as pa
     x = make(1, 2, 16, 64, "f32", 1)
