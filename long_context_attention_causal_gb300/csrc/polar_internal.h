@@ -119,15 +119,17 @@ struct LinearStateArgs {
   int* status;
   float* init_copy;   // [B, H, d, d]: where the scan copies init, or null
 };
+// Each launch takes n applications that differ in tensors, states, direction
+// and scale only: states and scans 1 or 2, outputs in fp32 1 to 3.
 // fp32 on the FP32 pipes.
-cudaError_t launch_linear_states(const LinearStateArgs& a, cudaStream_t s);
-cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s);
-cudaError_t launch_linear_out(const LinearArgs& a, cudaStream_t s);
-// bf16 on the tensor cores: n applications (1, or 2 that differ in tensors and
-// states only).  maps: x, y, z, out of each / y, z (128-row boxes).
+cudaError_t launch_linear_states(const LinearStateArgs* a, int n, cudaStream_t s);
+cudaError_t launch_linear_scan(const LinearStateArgs* a, int n, cudaStream_t s);
+cudaError_t launch_linear_out(const LinearArgs* a, int n, cudaStream_t s);
+// bf16 on the tensor cores: outputs 1, or 2 of one direction.  maps: x, y, z,
+// out of each / y, z of each (128-row boxes).
 cudaError_t launch_linear_out_tc(const LinearArgs* a, int n, const CUtensorMap* maps,
                                  cudaStream_t s);
-cudaError_t launch_linear_states_tc(const LinearStateArgs& a, const CUtensorMap* maps,
+cudaError_t launch_linear_states_tc(const LinearStateArgs* a, int n, const CUtensorMap* maps,
                                     cudaStream_t s);
 // final = init (or zero) for prompts without tokens.
 cudaError_t launch_linear_copy_state(const float* init, float* final_state, size_t n,

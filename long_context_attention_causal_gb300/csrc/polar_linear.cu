@@ -48,8 +48,17 @@ __device__ __forceinline__ void store2(float* p, float a, float b) {
 __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
   *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+// Dot products and updates run on pairs of values (fma .f32x2): half the
+// instructions of scalar code, which is what bounds these kernels.
+__device__ __forceinline__ float2 dot4(float4 a, float4 b, float2 c) {
+  return ffma2(make_float2(a.x, a.y), make_float2(b.x, b.y),
+               ffma2(make_float2(a.z, a.w), make_float2(b.z, b.w), c));
+}
+__device__ __forceinline__ float4 axpy4(float w, float4 y, float4 c) {
+  const float2 w2 = make_float2(w, w);
+  const float2 lo = ffma2(w2, make_float2(y.x, y.y), make_float2(c.x, c.y));
+  const float2 hi = ffma2(w2, make_float2(y.z, y.w), make_float2(c.z, c.w));
+  return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
 
 // The thread's pieces of rows [t0, t0 + kC) x W of a tensor, on their way to
@@ -99,11 +108,7 @@ __device__ __forceinline__ void state_products(float4 (&acc)[StateTile<D>::kR],
     const float4 yv = *reinterpret_cast<const float4*>(&y[j][c0]);
 #pragma unroll
     for (int r = 0; r < S::kR; ++r) {
-      const float zv = zw[j][r0 + r];
-      acc[r].x = fmaf(zv, yv.x, acc[r].x);
-      acc[r].y = fmaf(zv, yv.y, acc[r].y);
-      acc[r].z = fmaf(zv, yv.z, acc[r].z);
-      acc[r].w = fmaf(zv, yv.w, acc[r].w);
+      acc[r] = axpy4(zw[j][r0 + r], yv, acc[r]);
     }
   }
 }
@@ -116,11 +121,20 @@ struct StateSmem {
   float zw[kC][kZ];
 };
 
+// Applications of one launch, by blockIdx.z.
+struct StateBatch {
+  LinearStateArgs a[2];
+};
+struct OutBatch {
+  LinearArgs a[3];
+};
+
 // Grid (parts, D / kZ): the part of the run that reaches its cut.  Weights are
 // taken from the cut, so the accumulators never need rescaling.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads)
-    polar_linear_state_kernel(const LinearStateArgs a) {
+    polar_linear_state_kernel(const StateBatch batch) {
+  const LinearStateArgs& a = batch.a[blockIdx.z];
   using S = StateTile<D>;
   __shared__ __align__(16) StateSmem<D> sm;
   const int BH = a.B * a.H, part = blockIdx.x, z0 = blockIdx.y * kZ;
@@ -165,7 +179,8 @@ __global__ void __launch_bounds__(kThreads)
 // Grid (BH, d * d / 512): four state elements a thread through the cuts of
 // the head in order; a run's own sum is replaced by the state at its cut.
 constexpr int kScanThreads = 128;
-__global__ void __launch_bounds__(kScanThreads) polar_linear_scan_kernel(const LinearStateArgs a) {
+__global__ void __launch_bounds__(kScanThreads) polar_linear_scan_kernel(const StateBatch batch) {
+  const LinearStateArgs& a = batch.a[blockIdx.z];
   const int bh = blockIdx.x, dd = a.d * a.d, per = a.split.per;
   const long long h0 = (long long)bh * a.split.tiles, h1 = h0 + a.split.tiles;
   // boundaries k * per strictly inside the head
@@ -229,8 +244,9 @@ struct OutSmem {
 // Grid (parts, D / kZ): the CTA walks its run's chunks with its 32 rows of the
 // state in shared memory.
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads)
-    polar_linear_out_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(kThreads, 2)
+    polar_linear_out_kernel(const OutBatch batch) {
+  const LinearArgs& a = batch.a[blockIdx.z];
   using S = StateTile<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   OutSmem<D>& sm = *reinterpret_cast<OutSmem<D>*>(smem_raw);
@@ -286,16 +302,17 @@ __global__ void __launch_bounds__(kThreads)
     pz.store(sm.z);
     if (ci + 1 < n_ch) fetch(chunk(ci + 1));
     __syncthreads();
+    const float2 zero = make_float2(0.f, 0.f);
     float o[4][2];
 #pragma unroll
     for (int ii = 0; ii < 4; ++ii) o[ii][0] = o[ii][1] = 0.f;
     if (n > 0) {
       // scores: rows 4 ty .., keys tx + 16 jj
-      float sc[4][4];
+      float2 sc[4][4];
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = 0.f;
+        for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = zero;
 #pragma unroll 2
       for (int k = 0; k < D; k += 4) {
         float4 xv[4], yv[4];
@@ -316,7 +333,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int jj = 0; jj < 4; ++jj) {
           const int i = 4 * ty + ii, j = tx + 16 * jj;
           const int dist = a.reverse ? j - i : i - j;
-          sm.p[i][j] = dist >= 0 ? sc[ii][jj] * sm.pw[dist] : 0.f;
+          sm.p[i][j] = dist >= 0 ? (sc[ii][jj].x + sc[ii][jj].y) * sm.pw[dist] : 0.f;
         }
       for (int i = tid; i < kC * kZ; i += kThreads) {
         const int r = i / kZ;
@@ -325,6 +342,9 @@ __global__ void __launch_bounds__(kThreads)
       }
       __syncthreads();
       // the state's part: rows 4 ty .., state rows 2 tx, 2 tx + 1
+      float2 m[4][2], q[4][2];
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) m[ii][0] = m[ii][1] = q[ii][0] = q[ii][1] = zero;
 #pragma unroll 2
       for (int k = 0; k < D; k += 4) {
         const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[2 * tx][k]);
@@ -332,21 +352,11 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
           const float4 xv = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
-          o[ii][0] = dot4(xv, m0, o[ii][0]);
-          o[ii][1] = dot4(xv, m1, o[ii][1]);
+          m[ii][0] = dot4(xv, m0, m[ii][0]);
+          m[ii][1] = dot4(xv, m1, m[ii][1]);
         }
       }
-#pragma unroll
-      for (int ii = 0; ii < 4; ++ii) {
-        const int i = 4 * ty + ii;
-        const float w = i < n ? s_in * sm.pw[a.reverse ? n - 1 - i : i + 1] : 0.f;
-        o[ii][0] *= w;
-        o[ii][1] *= w;
-      }
       // the chunk's own part
-      float q[4][2];
-#pragma unroll
-      for (int ii = 0; ii < 4; ++ii) q[ii][0] = q[ii][1] = 0.f;
 #pragma unroll 2
       for (int j = 0; j < kC; j += 4) {
         float2 zv[4];
@@ -356,14 +366,19 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
           const float4 pv = *reinterpret_cast<const float4*>(&sm.p[4 * ty + ii][j]);
-          q[ii][0] = dot4(pv, make_float4(zv[0].x, zv[1].x, zv[2].x, zv[3].x), q[ii][0]);
-          q[ii][1] = dot4(pv, make_float4(zv[0].y, zv[1].y, zv[2].y, zv[3].y), q[ii][1]);
+          // both columns at once
+          q[ii][0] = ffma2(make_float2(pv.x, pv.x), zv[0], q[ii][0]);
+          q[ii][1] = ffma2(make_float2(pv.y, pv.y), zv[1], q[ii][1]);
+          q[ii][0] = ffma2(make_float2(pv.z, pv.z), zv[2], q[ii][0]);
+          q[ii][1] = ffma2(make_float2(pv.w, pv.w), zv[3], q[ii][1]);
         }
       }
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
-        o[ii][0] = fmaf(a.scale, q[ii][0], o[ii][0]);
-        o[ii][1] = fmaf(a.scale, q[ii][1], o[ii][1]);
+        const int i = 4 * ty + ii;
+        const float w = i < n ? s_in * sm.pw[a.reverse ? n - 1 - i : i + 1] : 0.f;
+        o[ii][0] = fmaf(a.scale, q[ii][0].x + q[ii][1].x, w * (m[ii][0].x + m[ii][0].y));
+        o[ii][1] = fmaf(a.scale, q[ii][0].y + q[ii][1].y, w * (m[ii][1].x + m[ii][1].y));
       }
     }
 #pragma unroll
@@ -428,12 +443,10 @@ __global__ void __launch_bounds__(kStepWarps * 32)
   for (int r = 0; r < kN; ++r) {
     const int row = row0 + r * kRW;
     const float vr = linear_load(v + row);
-    s[r].x = fmaf(g, s[r].x, vr * k.x);
-    s[r].y = fmaf(g, s[r].y, vr * k.y);
-    s[r].z = fmaf(g, s[r].z, vr * k.z);
-    s[r].w = fmaf(g, s[r].w, vr * k.w);
+    s[r] = axpy4(g, s[r], make_float4(vr * k.x, vr * k.y, vr * k.z, vr * k.w));
     *reinterpret_cast<float4*>(S + (size_t)row * D + c0) = s[r];
-    float o = dot4(s[r], q, 0.f);
+    const float2 o2 = dot4(s[r], q, make_float2(0.f, 0.f));
+    float o = o2.x + o2.y;
 #pragma unroll
     for (int w = kL / 2; w > 0; w >>= 1) o += __shfl_xor_sync(0xffffffffu, o, w);
     if (lane % kL == 0) linear_store(mem + row, a.scale * o);
@@ -447,33 +460,41 @@ cudaError_t step_d(const LinearStepArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, typename T>
-cudaError_t states_d(const LinearStateArgs& a, cudaStream_t s) {
-  polar_linear_state_kernel<D, T>
-      <<<dim3((unsigned)a.split.parts, D / kZ), kThreads, 0, s>>>(a);
+template <int D>
+cudaError_t states_d(const StateBatch& batch, int n, cudaStream_t s) {
+  polar_linear_state_kernel<D, float>
+      <<<dim3((unsigned)batch.a[0].split.parts, D / kZ, n), kThreads, 0, s>>>(batch);
   return cudaGetLastError();
 }
 
-template <int D, typename T>
-cudaError_t out_d(const LinearArgs& a, cudaStream_t s) {
+template <int D>
+cudaError_t out_d(const OutBatch& batch, int n, cudaStream_t s) {
   const int smem = (int)sizeof(OutSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D, T>,
+  cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D, float>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  polar_linear_out_kernel<D, T>
-      <<<dim3((unsigned)a.split.parts, D / kZ), kThreads, smem, s>>>(a);
+  polar_linear_out_kernel<D, float>
+      <<<dim3((unsigned)batch.a[0].split.parts, D / kZ, n), kThreads, smem, s>>>(batch);
   return cudaGetLastError();
+}
+
+StateBatch state_batch(const LinearStateArgs* a, int n) {
+  StateBatch b;
+  for (int i = 0; i < 2; ++i) b.a[i] = a[i < n ? i : 0];
+  return b;
 }
 
 }  // namespace
 
-cudaError_t launch_linear_states(const LinearStateArgs& a, cudaStream_t s) {
-  return a.d == 64 ? states_d<64, float>(a, s) : states_d<128, float>(a, s);
+cudaError_t launch_linear_states(const LinearStateArgs* a, int n, cudaStream_t s) {
+  const StateBatch b = state_batch(a, n);
+  return a->d == 64 ? states_d<64>(b, n, s) : states_d<128>(b, n, s);
 }
 
-cudaError_t launch_linear_scan(const LinearStateArgs& a, cudaStream_t s) {
-  polar_linear_scan_kernel<<<dim3((unsigned)a.B * a.H, a.d * a.d / (4 * kScanThreads)),
-                             kScanThreads, 0, s>>>(a);
+cudaError_t launch_linear_scan(const LinearStateArgs* a, int n, cudaStream_t s) {
+  const StateBatch b = state_batch(a, n);
+  polar_linear_scan_kernel<<<dim3((unsigned)a->B * a->H, a->d * a->d / (4 * kScanThreads), n),
+                             kScanThreads, 0, s>>>(b);
   return cudaGetLastError();
 }
 
@@ -483,8 +504,10 @@ cudaError_t launch_linear_copy_state(const float* init, float* final_state, size
   return cudaGetLastError();
 }
 
-cudaError_t launch_linear_out(const LinearArgs& a, cudaStream_t s) {
-  return a.d == 64 ? out_d<64, float>(a, s) : out_d<128, float>(a, s);
+cudaError_t launch_linear_out(const LinearArgs* a, int n, cudaStream_t s) {
+  OutBatch b;
+  for (int i = 0; i < 3; ++i) b.a[i] = a[i < n ? i : 0];
+  return a->d == 64 ? out_d<64>(b, n, s) : out_d<128>(b, n, s);
 }
 
 cudaError_t launch_linear_step(const LinearStepArgs& a, int dtype, cudaStream_t s) {

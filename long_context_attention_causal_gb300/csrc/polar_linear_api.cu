@@ -60,39 +60,40 @@ size_t workspace_bytes_of(int B, int H, int T, int d, int dtype) {
   return B * H > 0 && T > 0 ? cut_bytes(split(B * H, T, d, dtype, sms), B * H, d) : 0;
 }
 
-// bf16 runs on the tensor cores, fp32 on the FP32 pipes.
-int run_states(const LinearStateArgs& a, int dtype, cudaStream_t s) {
+// bf16 runs on the tensor cores, fp32 on the FP32 pipes.  n applications that
+// differ in tensors, states, direction and scale.
+int run_states(const LinearStateArgs* a, int n, int dtype, cudaStream_t s) {
   int st;
   if (dtype == POLAR_BF16) {
-    CUtensorMap maps[2];
-    if (!make_map(&maps[0], a.y, a.B * a.H, a.T, a.d) ||
-        !make_map(&maps[1], a.z, a.B * a.H, a.T, a.d))
-      return POLAR_ERR_CUDA;
-    st = cuda_status("linear state launch", launch_linear_states_tc(a, maps, s));
+    CUtensorMap maps[4];
+    for (int i = 0; i < n; ++i)
+      if (!make_map(&maps[2 * i], a[i].y, a[i].B * a[i].H, a[i].T, a[i].d) ||
+          !make_map(&maps[2 * i + 1], a[i].z, a[i].B * a[i].H, a[i].T, a[i].d))
+        return POLAR_ERR_CUDA;
+    st = cuda_status("linear state launch", launch_linear_states_tc(a, n, maps, s));
   } else {
-    st = cuda_status("linear state launch", launch_linear_states(a, s));
+    st = cuda_status("linear state launch", launch_linear_states(a, n, s));
   }
   if (st != POLAR_OK) return st;
-  return cuda_status("linear scan launch", launch_linear_scan(a, s));
+  return cuda_status("linear scan launch", launch_linear_scan(a, n, s));
 }
 
-// n applications of the recurrence (1, or 2 that read the same tensors).
 int run_out(const LinearArgs* a, int n, int dtype, cudaStream_t s) {
-  if (dtype != POLAR_BF16) {
-    for (int i = 0; i < n; ++i) {
-      const int st = cuda_status("linear output launch", launch_linear_out(a[i], s));
-      if (st != POLAR_OK) return st;
+  if (dtype != POLAR_BF16) return cuda_status("linear output launch", launch_linear_out(a, n, s));
+  // one direction a launch
+  for (int i = 0; i < n;) {
+    const int m = i + 1 < n && a[i + 1].reverse == a[i].reverse ? 2 : 1;
+    CUtensorMap maps[8];
+    for (int j = 0; j < m; ++j) {
+      const void* bases[4] = {a[i + j].x, a[i + j].y, a[i + j].z, a[i + j].out};
+      for (int t = 0; t < 4; ++t)
+        if (!make_map(&maps[4 * j + t], bases[t], a->B * a->H, a->T, a->d)) return POLAR_ERR_CUDA;
     }
-    return POLAR_OK;
+    const int st = cuda_status("linear output launch", launch_linear_out_tc(a + i, m, maps, s));
+    if (st != POLAR_OK) return st;
+    i += m;
   }
-  CUtensorMap maps[8];
-  for (int i = 0; i < n; ++i) {
-    const void* bases[4] = {a[i].x, a[i].y, a[i].z, a[i].out};
-    for (int t = 0; t < 4; ++t)
-      if (!make_map(&maps[4 * i + t], bases[t], a[i].B * a[i].H, a[i].T, a[i].d))
-        return POLAR_ERR_CUDA;
-  }
-  return cuda_status("linear output launch", launch_linear_out_tc(a, n, maps, s));
+  return POLAR_OK;
 }
 
 }  // namespace
@@ -142,7 +143,7 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   if (g.cut) {
     const LinearStateArgs a{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
                             g, state_in, cuts, status, copy};
-    st = run_states(a, dtype, s);
+    st = run_states(&a, 1, dtype, s);
     if (st != POLAR_OK) return st;
   }
   const LinearArgs a{q, k, v, mem, log_decay, lengths, B, H, T, d, scale, false, false,
@@ -199,33 +200,26 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   float* copy =
       g.cut && dstate_out && dstate_out == dstate_in ? cuts_r + cut_floats(g, d) : nullptr;
   if (g.cut) {
-    const LinearStateArgs as{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
-                             g, state_in, cuts_s, status, nullptr};
-    const LinearStateArgs ar{q, dmem, log_decay, lengths, B, H, T, d, scale, true,
-                             g, dstate_out, cuts_r, status, copy};
     // dq's states last: its kernel then starts on tiles that are still in L2
-    st = run_states(ar, dtype, s);
-    if (st == POLAR_OK) st = run_states(as, dtype, s);
+    const LinearStateArgs a[2] = {{q, dmem, log_decay, lengths, B, H, T, d, scale, true,
+                                   g, dstate_out, cuts_r, status, copy},
+                                  {k, v, log_decay, lengths, B, H, T, d, 1.f, false,
+                                   g, state_in, cuts_s, status, nullptr}};
+    st = run_states(a, 2, dtype, s);
     if (st != POLAR_OK) return st;
   }
-  const LinearArgs aq{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
-                      g, state_in, cuts_s, nullptr, status};
-  // dk and dv read the same four tensors: one launch, unless dv's CTA would
-  // write dstate_in over the dstate_out that dk's has yet to read.
   const float* r_init = copy ? copy : dstate_out;
-  const LinearArgs akv[2] = {
-      {v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
-       g, r_init, cuts_r, nullptr, status},
-      {k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
-       g, r_init, cuts_r, dstate_in, status}};
-  st = run_out(&aq, 1, dtype, s);
-  if (st != POLAR_OK) return st;
-  if (dstate_in && r_init == dstate_in) {
-    st = run_out(&akv[0], 1, dtype, s);
-    if (st != POLAR_OK) return st;
-    return run_out(&akv[1], 1, dtype, s);
-  }
-  return run_out(akv, 2, dtype, s);
+  const LinearArgs a[3] = {{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
+                            g, state_in, cuts_s, nullptr, status},
+                           {v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
+                            g, r_init, cuts_r, nullptr, status},
+                           {k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
+                            g, r_init, cuts_r, dstate_in, status}};
+  // dv's CTA would write dstate_in over the dstate_out that dk's has yet to
+  // read: in place and uncopied, dv goes after the others
+  if (!dstate_in || r_init != dstate_in) return run_out(a, 3, dtype, s);
+  st = run_out(a, 2, dtype, s);
+  return st == POLAR_OK ? run_out(a + 2, 1, dtype, s) : st;
 }
 
 }  // extern "C"

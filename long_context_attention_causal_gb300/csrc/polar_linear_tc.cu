@@ -692,20 +692,24 @@ struct StateBars {
   int abort_flag;
 };
 
+struct StateMaps {
+  CUtensorMap m[2][2];  // y, z of each application (blockIdx.y)
+};
+
 struct StateParams {
   const float* log_decay;
   const int* lengths;
-  float* cuts;
-  int BH, H, T, reverse;
+  float* cuts[2];
+  int reverse[2];
+  float scale[2];
+  int BH, H, T;
   LinearSplit split;
-  float scale;
   int* status;
 };
 
 template <int D>
 __global__ void __launch_bounds__(kSThreads, 1)
-    polar_linear_state_tc_kernel(const __grid_constant__ CUtensorMap map_y,
-                                 const __grid_constant__ CUtensorMap map_z, const StateParams p) {
+    polar_linear_state_tc_kernel(const __grid_constant__ StateMaps maps, const StateParams p) {
   using L = StateLayout<D>;
   constexpr int NS = L::kNS;
   extern __shared__ uint8_t smem_raw[];
@@ -713,10 +717,13 @@ __global__ void __launch_bounds__(kSThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   StateBars& br = *reinterpret_cast<StateBars*>(smem + L::kBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int op = blockIdx.y;
+  const CUtensorMap &map_y = maps.m[op][0], &map_z = maps.m[op][1];
+  const bool reverse = p.reverse[op] != 0;
   const LinearPortion po = linear_portion(
       p.split, p.BH, p.H, p.T, p.lengths, p.status, blockIdx.x,
-      p.reverse ? 0 : linear_portions(p.split, p.BH, blockIdx.x) - 1);
-  if (!(p.reverse ? po.cut_left : po.cut_right)) return;  // the whole CTA
+      reverse ? 0 : linear_portions(p.split, p.BH, blockIdx.x) - 1);
+  if (!(reverse ? po.cut_left : po.cut_right)) return;  // the whole CTA
   const int bh = po.bh, nt = po.live;
   const int t0 = po.row(po.first), t1 = max(t0, min(po.row(po.last), po.len));
   const float l2 = linear_log2_decay(p.log_decay, bh % p.H);
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   tc_fence_after();
   const uint32_t tmem = br.tmem_base;
   volatile int* abort_flag = &br.abort_flag;
-  auto tile_row = [&](int c) { return t0 + (p.reverse ? c : nt - 1 - c) * kTok; };
+  auto tile_row = [&](int c) { return t0 + (reverse ? c : nt - 1 - c) * kTok; };
 
   if (warp == kSWarpTMA) {
     if (lane == 0) {
@@ -821,7 +828,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int j = (tid >> 3) + 32 * u, t = row + j;  // row of pieces u, u + 4
-        const float w = p.scale * linear_power(l2, p.reverse ? t - t0 + 1 : max(t1 - 1 - t, 0));
+        const float w =
+            p.scale[op] * linear_power(l2, reverse ? t - t0 + 1 : max(t1 - 1 - t, 0));
 #pragma unroll
         for (int q = u; q < kVecs; q += 4) {
           uint4 hi;
@@ -846,7 +854,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     }
     const int half = warp >> 2, r = threadIdx.x & 127;
     constexpr int kCols = D / 2;
-    float* dst = p.cuts + ((size_t)blockIdx.x * D + r) * D + half * kCols;
+    float* dst = p.cuts[op] + ((size_t)blockIdx.x * D + r) * D + half * kCols;
     ok = ok && (nt == 0 || mbar_wait(&br.done, 0, abort_flag, p.status));
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
@@ -914,16 +922,31 @@ cudaError_t out_tc_d(const LinearArgs* a, int n, const CUtensorMap* maps, cudaSt
 }
 
 template <int D>
-cudaError_t state_tc_d(const LinearStateArgs& a, const CUtensorMap* maps, cudaStream_t s) {
+cudaError_t state_tc_d(const LinearStateArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
   using L = StateLayout<D>;
-  const StateParams p{a.log_decay, a.lengths, a.cuts, a.B * a.H, a.H, a.T, a.reverse ? 1 : 0,
-                      a.split, a.scale, a.status};
+  StateMaps m;
+  StateParams p;
+  p.log_decay = a->log_decay;
+  p.lengths = a->lengths;
+  for (int i = 0; i < 2; ++i) {
+    const int j = i < n ? i : 0;
+    m.m[i][0] = maps[2 * j];
+    m.m[i][1] = maps[2 * j + 1];
+    p.cuts[i] = a[j].cuts;
+    p.reverse[i] = a[j].reverse ? 1 : 0;
+    p.scale[i] = a[j].scale;
+  }
+  p.BH = a->B * a->H;
+  p.H = a->H;
+  p.T = a->T;
+  p.split = a->split;
+  p.status = a->status;
   cudaError_t e = cudaFuncSetAttribute(polar_linear_state_tc_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kSmemBytes);
   if (e != cudaSuccess) return e;
   polar_linear_state_tc_kernel<D>
-      <<<(unsigned)a.split.parts, kSThreads, L::kSmemBytes, s>>>(maps[0], maps[1], p);
+      <<<dim3((unsigned)a->split.parts, n), kSThreads, L::kSmemBytes, s>>>(m, p);
   return cudaGetLastError();
 }
 
@@ -936,9 +959,9 @@ cudaError_t launch_linear_out_tc(const LinearArgs* a, int n, const CUtensorMap* 
   return a->reverse ? out_tc_d<128, true>(a, n, maps, s) : out_tc_d<128, false>(a, n, maps, s);
 }
 
-cudaError_t launch_linear_states_tc(const LinearStateArgs& a, const CUtensorMap* maps,
+cudaError_t launch_linear_states_tc(const LinearStateArgs* a, int n, const CUtensorMap* maps,
                                     cudaStream_t s) {
-  return a.d == 64 ? state_tc_d<64>(a, maps, s) : state_tc_d<128>(a, maps, s);
+  return a->d == 64 ? state_tc_d<64>(a, n, maps, s) : state_tc_d<128>(a, n, maps, s);
 }
 
 }  // namespace polar
