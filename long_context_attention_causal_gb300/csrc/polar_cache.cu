@@ -7,9 +7,13 @@
 // them into weights once the split records are there.
 //
 // Eviction: one CTA per (sequence, KV head) finds the keep-th largest
-// (protected, weight, lower row) key by four radix passes over 8 bits, lists
-// the evicted rows below `keep` and the kept rows past it, both ascending,
-// and moves weights and positions; a second kernel copies the K and V rows.
+// (protected, weight, lower row) key by radix passes over 11, 11 and 10 bits,
+// lists the evicted rows below `keep` and the kept rows past it, both
+// ascending, and moves weights and positions; a second kernel copies the K
+// and V rows.  The keys stay in shared memory between the passes (up to 48K
+// rows; longer heads read them again).  The first pass sorts by exponent and
+// two bits more, which spreads heavy-tailed weights over enough bins for
+// shared-memory atomics; the later ones touch one bin's rows only.
 #include <climits>
 #include <cstdint>
 
@@ -77,7 +81,9 @@ __global__ void __launch_bounds__(kWThreads) polar_decode_weights_kernel(const W
 
 constexpr int kEThreads = 1024;
 constexpr int kEWarps = kEThreads / 32;
-constexpr int kCopies = 8;  // copies of the histogram (fewer collisions)
+constexpr int kBins = 2048;
+constexpr int kCopies = 2;           // of the histogram (fewer collisions)
+constexpr int kKeysCached = 49152;   // keys that fit shared memory beside it
 
 // Weight -> unsigned order: NaN below everything, -0 equal to 0.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -87,7 +93,7 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 struct SelectSmem {
-  uint32_t hist[kCopies][256];
+  uint32_t hist[kCopies][kBins];
   uint32_t warp_a[kEWarps], warp_b[kEWarps];
   uint32_t prefix, need;
   int newest;
@@ -114,8 +120,10 @@ __device__ __forceinline__ void scan_warps(SelectSmem& sm) {
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const EvictArgs a,
+                                                                        int cached) {
   __shared__ SelectSmem sm;
+  extern __shared__ uint32_t s_keys[];
   const int bh = blockIdx.x, b = bh / a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int n = a.seq_lens[b];
@@ -135,155 +143,176 @@ __global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const Evi
   if (tid == 0) sm.newest = INT_MIN;
   __syncthreads();
   int newest = INT_MIN;
+#pragma unroll 8
   for (int j = tid; j < n; j += kEThreads) newest = max(newest, pos[j]);
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (lane == 0) atomicMax(&sm.newest, newest);
   __syncthreads();
   const long long guard = (long long)sm.newest - a.recent;  // positions above stay
-  auto key_of = [&](int j) -> uint32_t {
+  const bool fits = n <= cached;
+  auto make_key = [&](int j) -> uint32_t {
     return pos[j] > guard ? 0xFFFFFFFFu : order_key(w[j]);
   };
-  // key of the keep-th largest row, 8 bits a pass from the top
+  auto key_of = [&](int j) -> uint32_t { return fits ? s_keys[j] : make_key(j); };
+  if (fits) {
+#pragma unroll 8
+    for (int j = tid; j < n; j += kEThreads) s_keys[j] = make_key(j);
+  }
+  // key of the keep-th largest row, from the top bits down
   uint32_t prefix = 0, need = (uint32_t)a.keep;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < kCopies * 256; i += kEThreads) (&sm.hist[0][0])[i] = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    for (int i = tid; i < kCopies * kBins; i += kEThreads) (&sm.hist[0][0])[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int j = tid; j < n; j += kEThreads) {
       const uint32_t key = key_of(j);
-      if (shift == 24 || (key >> (shift + 8)) == prefix)
-        atomicAdd(&sm.hist[warp % kCopies][(key >> shift) & 255u], 1u);
+      if (pass == 0 || (key >> (shift + bits)) == prefix)
+        atomicAdd(&sm.hist[warp % kCopies][(key >> shift) & ((1u << bits) - 1u)], 1u);
     }
     __syncthreads();
-    if (warp == 0) {
-      // bin that holds the need-th largest, from the top: 8 bins a lane
-      uint32_t c[8], sum = 0;
+    // bin that holds the need-th largest: two bins a thread, from the top
+    const int top = kBins - 1 - 2 * tid;
+    uint32_t c0 = 0, c1 = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = 0;
+    for (int k = 0; k < kCopies; ++k) {
+      c0 += sm.hist[k][top];
+      c1 += sm.hist[k][top - 1];
+    }
+    uint32_t before = c0 + c1;
 #pragma unroll
-        for (int k = 0; k < kCopies; ++k) c[i] += sm.hist[k][255 - (lane * 8 + i)];
-        sum += c[i];
-      }
-      uint32_t before = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += t;
-      }
-      before -= sum;  // rows in larger bins
-      if (before < need && need <= before + sum) {
-        uint32_t acc = before;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (acc < need && need <= acc + c[i]) {
-            sm.prefix = (prefix << 8) | (uint32_t)(255 - (lane * 8 + i));
-            sm.need = need - acc;
-          }
-          acc += c[i];
-        }
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += t;
+    }
+    if (lane == 31) {
+      sm.warp_a[warp] = before;
+      sm.warp_b[warp] = 0;
+    }
+    scan_warps(sm);
+    before += sm.warp_a[warp] - (c0 + c1);  // rows in larger bins
+    if (before < need && need <= before + c0 + c1) {
+      const bool first = need <= before + c0;
+      sm.prefix = (prefix << bits) | (uint32_t)(first ? top : top - 1);
+      sm.need = need - before - (first ? 0u : c0);
     }
     __syncthreads();
     prefix = sm.prefix;
     need = sm.need;
+    __syncthreads();
   }
-  // rows above the threshold stay, and the first `need` equal to it.  Each
-  // warp owns a run of rows: ranks come from ballots and a scan over warps.
+  // Rows above the threshold stay, and the first `need` equal to it.  Each
+  // warp owns a run of rows.  One walk counts rows above and equal on both
+  // sides of the cut: the equal rows that stay are the first ones, so their
+  // numbers follow from a scan, and with them the ranks of the rows that move.
   const int span = (n + kEThreads - 1) / kEThreads * 32;
-  const int w0 = warp * span, w1 = min(w0 + span, n);
-  uint32_t eq = 0;
+  const int w0 = min(warp * span, n), w1 = min(w0 + span, n);
+  uint32_t above_lo = 0, above_hi = 0, eq_lo = 0, eq_hi = 0;
   for (int j0 = w0; j0 < w1; j0 += 32) {
     const int j = j0 + lane;
-    eq += __popc(__ballot_sync(0xffffffffu, j < w1 && key_of(j) == prefix));
+    const uint32_t key = j < w1 ? key_of(j) : 0u;
+    const uint32_t lo = __ballot_sync(0xffffffffu, j < a.keep);
+    const uint32_t up = __ballot_sync(0xffffffffu, j < w1 && key > prefix);
+    const uint32_t eq = __ballot_sync(0xffffffffu, j < w1 && key == prefix);
+    above_lo += __popc(up & lo);
+    above_hi += __popc(up & ~lo);
+    eq_lo += __popc(eq & lo);
+    eq_hi += __popc(eq & ~lo);
   }
   if (lane == 0) {
-    sm.warp_a[warp] = eq;
+    sm.warp_a[warp] = eq_lo + eq_hi;
     sm.warp_b[warp] = 0;
   }
   scan_warps(sm);
-  const uint32_t eq0 = sm.warp_a[warp];
+  uint32_t rank = sm.warp_a[warp];  // equal rows before this warp's
   __syncthreads();
+  const uint32_t stay = min(need > rank ? need - rank : 0u, eq_lo + eq_hi);
+  const uint32_t stay_lo = min(stay, eq_lo);
+  const uint32_t rows_lo = (uint32_t)(min(w1, a.keep) - min(w0, a.keep));
+  const uint32_t holes = rows_lo - above_lo - stay_lo;
+  if (lane == 0) {
+    sm.warp_a[warp] = holes;
+    sm.warp_b[warp] = above_hi + stay - stay_lo;
+  }
+  scan_warps(sm);
+  uint32_t hole_at = sm.warp_a[warp], mover_at = sm.warp_b[warp];
+  if (warp == kEWarps - 1 && lane == 0) {
+    a.counts[bh] = (int)(hole_at + holes);
+    a.counts[gridDim.x + bh] = n;
+    sm.need = hole_at + holes;
+  }
   const uint32_t below = (1u << lane) - 1u;
-  uint32_t holes = 0, movers = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    uint32_t rank = eq0;
-    uint32_t hole_at = 0, mover_at = 0;
-    if (pass == 1) {
-      hole_at = sm.warp_a[warp];
-      mover_at = sm.warp_b[warp];
-    }
-    int2* mv = a.moves + (size_t)bh * a.max_moves;
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-      const int j = j0 + lane;
-      const uint32_t key = j < w1 ? key_of(j) : 0u;
-      const bool is_eq = j < w1 && key == prefix;
-      const uint32_t m_eq = __ballot_sync(0xffffffffu, is_eq);
-      const bool kept =
-          j < w1 && (key > prefix || (is_eq && rank + __popc(m_eq & below) < need));
-      rank += __popc(m_eq);
-      const bool hole = j < w1 && !kept && j < a.keep, mover = kept && j >= a.keep;
-      const uint32_t m_h = __ballot_sync(0xffffffffu, hole);
-      const uint32_t m_m = __ballot_sync(0xffffffffu, mover);
-      if (pass == 0) {
-        holes += __popc(m_h);
-        movers += __popc(m_m);
-      } else {
-        if (hole) mv[hole_at + __popc(m_h & below)].y = j;
-        if (mover) mv[mover_at + __popc(m_m & below)].x = j;
-        hole_at += __popc(m_h);
-        mover_at += __popc(m_m);
-      }
-    }
-    if (pass == 0) {
-      if (lane == 0) {
-        sm.warp_a[warp] = holes;
-        sm.warp_b[warp] = movers;
-      }
-      scan_warps(sm);
-      if (warp == kEWarps - 1 && lane == 0) {
-        a.counts[bh] = (int)(sm.warp_a[warp] + holes);
-        a.counts[gridDim.x + bh] = n;
-        sm.need = sm.warp_a[warp] + holes;
-      }
-    }
+  int2* mv = a.moves + (size_t)bh * a.max_moves;
+  for (int j0 = w0; j0 < w1; j0 += 32) {
+    const int j = j0 + lane;
+    const uint32_t key = j < w1 ? key_of(j) : 0u;
+    const bool is_eq = j < w1 && key == prefix;
+    const uint32_t m_eq = __ballot_sync(0xffffffffu, is_eq);
+    const bool kept = j < w1 && (key > prefix || (is_eq && rank + __popc(m_eq & below) < need));
+    rank += __popc(m_eq);
+    const bool hole = j < w1 && !kept && j < a.keep, mover = kept && j >= a.keep;
+    const uint32_t m_h = __ballot_sync(0xffffffffu, hole);
+    const uint32_t m_m = __ballot_sync(0xffffffffu, mover);
+    if (hole) mv[hole_at + __popc(m_h & below)].y = j;
+    if (mover) mv[mover_at + __popc(m_m & below)].x = j;
+    hole_at += __popc(m_h);
+    mover_at += __popc(m_m);
   }
   __syncthreads();
   const int total = (int)sm.need;
-  const int2* mv = a.moves + (size_t)bh * a.max_moves;
+#pragma unroll 4
   for (int i = tid; i < total; i += kEThreads) {
     const int2 m = mv[i];
-    w[m.y] = w[m.x];
-    pos[m.y] = pos[m.x];
+    const float wv = w[m.x];
+    const int pv = pos[m.x];
+    w[m.y] = wv;
+    pos[m.y] = pv;
   }
   __syncthreads();
   for (int j = a.keep + tid; j < n; j += kEThreads) w[j] = 0.f;
 }
 
-// Grid (parts, B * Hkv): the listed rows of K and V, 16 bytes a thread.
-__global__ void __launch_bounds__(256) polar_evict_move_kernel(const EvictArgs a) {
+// Grid (parts, B * Hkv): the listed rows of K and V, 16 bytes a thread, four
+// pieces in flight.  Sources lie past the cut and targets before it, so loads
+// may run ahead of stores.  Bound: HBM.
+constexpr int kMThreads = 256, kMUnroll = 4;
+__global__ void __launch_bounds__(kMThreads) polar_evict_move_kernel(const EvictArgs a) {
   const int bh = blockIdx.y, b = bh / a.Hkv, h = bh % a.Hkv;
   const int total = a.counts[bh], n = a.counts[gridDim.y + bh];
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = min(n, a.keep);
-  const int vecs = a.row_bytes >> 4;  // 16-byte pieces of a row
-  const int per = 2 * vecs;           // of a K and a V row
+  const int vecs = a.row_bytes >> 4;            // 16-byte pieces of a row (a power of two)
+  const int shift = 31 - __clz(vecs) + 1;       // of a K and a V row
   const int* table = a.block_table + (size_t)b * a.max_pages;
   const int2* mv = a.moves + (size_t)bh * a.max_moves;
   const int page = 1 << a.page_shift;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)total * per;
-       i += (long long)gridDim.x * 256) {
-    const int2 m = mv[i / per];
-    const int piece = (int)(i % per);
-    const int p_from = table[m.x >> a.page_shift], p_to = table[m.y >> a.page_shift];
-    if (p_from < 0 || p_from >= a.num_pages || p_to < 0 || p_to >= a.num_pages) {
-      atomicExch(a.status, 3);
-      continue;
+  const long long pieces = (long long)total << shift, step = (long long)gridDim.x * kMThreads;
+  for (long long i0 = (long long)blockIdx.x * kMThreads + threadIdx.x; i0 < pieces;
+       i0 += kMUnroll * step) {
+    uint4 v[kMUnroll];
+    uint4* to[kMUnroll];
+#pragma unroll
+    for (int u = 0; u < kMUnroll; ++u) {
+      const long long i = i0 + u * step;
+      to[u] = nullptr;
+      if (i >= pieces) continue;
+      const int2 m = mv[i >> shift];
+      const int piece = (int)(i & ((1 << shift) - 1));
+      const int p_from = table[m.x >> a.page_shift], p_to = table[m.y >> a.page_shift];
+      if (p_from < 0 || p_from >= a.num_pages || p_to < 0 || p_to >= a.num_pages) {
+        atomicExch(a.status, 3);
+        continue;
+      }
+      const size_t from = ((size_t)p_from * a.Hkv + h) * page + (m.x & (page - 1));
+      const size_t dst = ((size_t)p_to * a.Hkv + h) * page + (m.y & (page - 1));
+      uint8_t* pool = static_cast<uint8_t*>(piece < vecs ? a.k_pages : a.v_pages);
+      const size_t off = (size_t)(piece & (vecs - 1)) * 16;
+      v[u] = *reinterpret_cast<const uint4*>(pool + from * a.row_bytes + off);
+      to[u] = reinterpret_cast<uint4*>(pool + dst * a.row_bytes + off);
     }
-    const size_t from = ((size_t)p_from * a.Hkv + h) * page + (m.x & (page - 1));
-    const size_t to = ((size_t)p_to * a.Hkv + h) * page + (m.y & (page - 1));
-    uint8_t* pool = static_cast<uint8_t*>(piece < vecs ? a.k_pages : a.v_pages);
-    const size_t off = (size_t)(piece < vecs ? piece : piece - vecs) * 16;
-    *reinterpret_cast<uint4*>(pool + to * a.row_bytes + off) =
-        *reinterpret_cast<const uint4*>(pool + from * a.row_bytes + off);
+#pragma unroll
+    for (int u = 0; u < kMUnroll; ++u)
+      if (to[u]) *to[u] = v[u];
   }
 }
 
@@ -302,13 +331,19 @@ cudaError_t launch_decode_weights(const WeightsArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const int heads = a.B * a.Hkv;
-  polar_evict_select_kernel<<<heads, kEThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const int cached = a.max_seq_len < kKeysCached ? a.max_seq_len : kKeysCached;
+  const int smem = cached * (int)sizeof(uint32_t);
+  cudaError_t e = cudaFuncSetAttribute(polar_evict_select_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  polar_evict_select_kernel<<<heads, kEThreads, smem, s>>>(a, cached);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const long long pieces = (long long)a.max_moves * 2 * (a.row_bytes >> 4);
-  long long parts = (pieces + 1023) / 1024;
+  const long long each = 2 * kMThreads * kMUnroll;  // pieces a CTA should have
+  long long parts = (pieces + each - 1) / each;
   parts = parts < 1 ? 1 : (parts > 64 ? 64 : parts);
-  polar_evict_move_kernel<<<dim3((unsigned)parts, heads), 256, 0, s>>>(a);
+  polar_evict_move_kernel<<<dim3((unsigned)parts, heads), kMThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
