@@ -28,17 +28,34 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWThreads = 256;
 constexpr int kWRows = 1024;  // cache rows per CTA
 
-// One CTA per kWRows rows of a (sequence, KV head).
+// One CTA per kWRows rows of a (sequence, KV head).  Every load of a thread's
+// rows is issued before the logsumexp is formed from the split records, so the
+// CTA costs about one memory latency.  Bound: HBM (4 G bytes of logits and 8
+// of weights a row).
 template <int G>
 __global__ void __launch_bounds__(kWThreads) polar_decode_weights_kernel(const WeightsArgs a) {
   __shared__ float s_lse[G];
+  constexpr int kR = kWRows / kWThreads;
   const int parts = (a.max_seq_len + kWRows - 1) / kWRows;
   const int bh = blockIdx.x / parts, b = bh / a.Hkv, hkv = bh % a.Hkv;
   const int n = min(max(a.seq_lens[b], 0), a.max_seq_len);
-  const int j0 = (int)(blockIdx.x % parts) * kWRows;
-  if (j0 >= n) return;
+  const int j0 = (int)(blockIdx.x % parts) * kWRows + threadIdx.x;
+  // the logits and records come from the launches before (programmatic launch)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (j0 - (int)threadIdx.x >= n) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t head0 = (size_t)b * a.Hq + (size_t)hkv * G;
+  const float* x = a.logits + head0 * a.max_seq_len;
+  float* w = a.weights + (size_t)bh * a.stride;
+  float xv[kR][G], wv[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    const int j = j0 + r * kWThreads;
+    wv[r] = j < n ? w[j] : 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      xv[r][g] = j < n ? __ldcs(x + (size_t)g * a.max_seq_len + j) : -INFINITY;
+  }
   if (warp < G) {
     // logsumexp of the head over its splits, log2 units
     const float* rec = a.partials + (head0 + warp) * a.splits * (a.d + 4);
@@ -63,17 +80,13 @@ __global__ void __launch_bounds__(kWThreads) polar_decode_weights_kernel(const W
     if (lane == 0) s_lse[warp] = m == -INFINITY ? INFINITY : m * kLog2e + log2f(l);
   }
   __syncthreads();
-  float lse[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) lse[g] = s_lse[g];
-  const float* x = a.logits + head0 * a.max_seq_len;
-  float* w = a.weights + (size_t)bh * a.stride;
-  const int j1 = min(j0 + kWRows, n);
-  for (int j = j0 + threadIdx.x; j < j1; j += kWThreads) {
+  for (int r = 0; r < kR; ++r) {
+    const int j = j0 + r * kWThreads;
     float p = 0.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) p += exp2f(x[(size_t)g * a.max_seq_len + j] - lse[g]);
-    w[j] += p;
+    for (int g = 0; g < G; ++g) p += exp2f(xv[r][g] - s_lse[g]);
+    if (j < n) w[j] = wv[r] + p;
   }
 }
 
@@ -319,14 +332,21 @@ __global__ void __launch_bounds__(kMThreads) polar_evict_move_kernel(const Evict
 }  // namespace
 
 cudaError_t launch_decode_weights(const WeightsArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)((a.max_seq_len + kWRows - 1) / kWRows) * a.B * a.Hkv;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.max_seq_len + kWRows - 1) / kWRows) * a.B * a.Hkv);
+  cfg.blockDim = dim3(kWThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   switch (a.Hq / a.Hkv) {
-    case 1: polar_decode_weights_kernel<1><<<grid, kWThreads, 0, s>>>(a); break;
-    case 2: polar_decode_weights_kernel<2><<<grid, kWThreads, 0, s>>>(a); break;
-    case 4: polar_decode_weights_kernel<4><<<grid, kWThreads, 0, s>>>(a); break;
-    default: polar_decode_weights_kernel<8><<<grid, kWThreads, 0, s>>>(a); break;
+    case 1: return cudaLaunchKernelEx(&cfg, polar_decode_weights_kernel<1>, a);
+    case 2: return cudaLaunchKernelEx(&cfg, polar_decode_weights_kernel<2>, a);
+    case 4: return cudaLaunchKernelEx(&cfg, polar_decode_weights_kernel<4>, a);
+    default: return cudaLaunchKernelEx(&cfg, polar_decode_weights_kernel<8>, a);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {

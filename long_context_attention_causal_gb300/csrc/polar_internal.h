@@ -101,6 +101,7 @@ struct LinearArgs {
   const float* cuts;      // states at the cuts (LinearStateArgs), null without cuts
   float* final_state;     // [B, H, d, d] state at the other end, or null (not with state_t)
   int* status;
+  bool chained = false;   // follows a kernel of the same call (programmatic launch)
 };
 
 // States at the cuts.  Forward: slot i is the state at the end of run i,

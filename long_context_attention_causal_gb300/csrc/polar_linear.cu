@@ -135,6 +135,7 @@ template <int D, typename T>
 __global__ void __launch_bounds__(kThreads)
     polar_linear_state_kernel(const StateBatch batch) {
   const LinearStateArgs& a = batch.a[blockIdx.z];
+  linear_let_next_start();
   using S = StateTile<D>;
   __shared__ __align__(16) StateSmem<D> sm;
   const int BH = a.B * a.H, part = blockIdx.x, z0 = blockIdx.y * kZ;
@@ -181,6 +182,8 @@ __global__ void __launch_bounds__(kThreads)
 constexpr int kScanThreads = 128;
 __global__ void __launch_bounds__(kScanThreads) polar_linear_scan_kernel(const StateBatch batch) {
   const LinearStateArgs& a = batch.a[blockIdx.z];
+  linear_let_next_start();
+  linear_wait_previous();
   const int bh = blockIdx.x, dd = a.d * a.d, per = a.split.per;
   const long long h0 = (long long)bh * a.split.tiles, h1 = h0 + a.split.tiles;
   // boundaries k * per strictly inside the head
@@ -247,6 +250,8 @@ template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 2)
     polar_linear_out_kernel(const OutBatch batch) {
   const LinearArgs& a = batch.a[blockIdx.z];
+  linear_let_next_start();
+  linear_wait_previous();
   using S = StateTile<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   OutSmem<D>& sm = *reinterpret_cast<OutSmem<D>*>(smem_raw);
@@ -473,9 +478,9 @@ cudaError_t out_d(const OutBatch& batch, int n, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D, float>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  polar_linear_out_kernel<D, float>
-      <<<dim3((unsigned)batch.a[0].split.parts, D / kZ, n), kThreads, smem, s>>>(batch);
-  return cudaGetLastError();
+  return linear_launch(polar_linear_out_kernel<D, float>,
+                       dim3((unsigned)batch.a[0].split.parts, D / kZ, n), kThreads, smem, s,
+                       batch.a[0].chained, batch);
 }
 
 StateBatch state_batch(const LinearStateArgs* a, int n) {
@@ -493,9 +498,9 @@ cudaError_t launch_linear_states(const LinearStateArgs* a, int n, cudaStream_t s
 
 cudaError_t launch_linear_scan(const LinearStateArgs* a, int n, cudaStream_t s) {
   const StateBatch b = state_batch(a, n);
-  polar_linear_scan_kernel<<<dim3((unsigned)a->B * a->H, a->d * a->d / (4 * kScanThreads), n),
-                             kScanThreads, 0, s>>>(b);
-  return cudaGetLastError();
+  return linear_launch(polar_linear_scan_kernel,
+                       dim3((unsigned)a->B * a->H, a->d * a->d / (4 * kScanThreads), n),
+                       kScanThreads, 0, s, true, b);
 }
 
 cudaError_t launch_linear_copy_state(const float* init, float* final_state, size_t n,

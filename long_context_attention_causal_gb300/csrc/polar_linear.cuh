@@ -28,6 +28,34 @@ __device__ __forceinline__ float linear_log2_decay(const float* log_decay, int h
 // relative: a power that still weighs (above 2^-24) is right to 1e-6.
 __device__ __forceinline__ float linear_power(float l2, int n) { return exp2f(l2 * (float)n); }
 
+// Programmatic launch: the kernels of one call follow each other without a
+// drain between them.  A kernel lets its successor start (once all of its own
+// CTAs have) and waits for its predecessor before it touches what that wrote
+// or still reads; tensors of the call that no kernel of it writes need no wait.
+__device__ __forceinline__ void linear_let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void linear_wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Launch of `kern`, chained to the kernel before it in the stream or not.
+template <typename K, typename... A>
+inline cudaError_t linear_launch(K kern, dim3 grid, int threads, int smem, cudaStream_t s,
+                                 bool chained, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // The tiles of one head that one run holds.
 struct LinearPortion {
   int bh;

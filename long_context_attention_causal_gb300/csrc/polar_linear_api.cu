@@ -78,11 +78,12 @@ int run_states(const LinearStateArgs* a, int n, int dtype, cudaStream_t s) {
   return cuda_status("linear scan launch", launch_linear_scan(a, n, s));
 }
 
-int run_out(const LinearArgs* a, int n, int dtype, cudaStream_t s) {
+int run_out(LinearArgs* a, int n, int dtype, cudaStream_t s) {
   if (dtype != POLAR_BF16) return cuda_status("linear output launch", launch_linear_out(a, n, s));
   // one direction a launch
   for (int i = 0; i < n;) {
     const int m = i + 1 < n && a[i + 1].reverse == a[i].reverse ? 2 : 1;
+    if (i > 0) a[i].chained = true;
     CUtensorMap maps[8];
     for (int j = 0; j < m; ++j) {
       const void* bases[4] = {a[i + j].x, a[i + j].y, a[i + j].z, a[i + j].out};
@@ -146,8 +147,8 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
     st = run_states(&a, 1, dtype, s);
     if (st != POLAR_OK) return st;
   }
-  const LinearArgs a{q, k, v, mem, log_decay, lengths, B, H, T, d, scale, false, false,
-                     g, copy ? copy : state_in, cuts, state_out, status};
+  LinearArgs a{q, k, v, mem, log_decay, lengths, B, H, T, d, scale, false, false,
+               g, copy ? copy : state_in, cuts, state_out, status, g.cut};
   return run_out(&a, 1, dtype, s);
 }
 
@@ -209,12 +210,12 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
     if (st != POLAR_OK) return st;
   }
   const float* r_init = copy ? copy : dstate_out;
-  const LinearArgs a[3] = {{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
-                            g, state_in, cuts_s, nullptr, status},
-                           {v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
-                            g, r_init, cuts_r, nullptr, status},
-                           {k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
-                            g, r_init, cuts_r, dstate_in, status}};
+  LinearArgs a[3] = {{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
+                      g, state_in, cuts_s, nullptr, status, g.cut},
+                     {v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
+                      g, r_init, cuts_r, nullptr, status},
+                     {k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
+                      g, r_init, cuts_r, dstate_in, status}};
   // dv's CTA would write dstate_in over the dstate_out that dk's has yet to
   // read: in place and uncopied, dv goes after the others
   if (!dstate_in || r_init != dstate_in) return run_out(a, 3, dtype, s);

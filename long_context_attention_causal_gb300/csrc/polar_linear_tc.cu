@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     br.abort_flag = 0;
     fence_barrier_init();
   }
+  linear_let_next_start();
   if (warp == kWarpMMA) tmem_alloc(&br.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
@@ -526,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int k = 0, ku = 0;
     bool ok = true;
+    linear_wait_previous();  // only these warps read states or write the final one
     for (int ip = 0; ip < n_po && ok; ++ip) {
       const LinearPortion po = portion(ip);
       const float l2 = linear_log2_decay(p.log_decay, po.bh % p.H);
@@ -723,6 +725,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const LinearPortion po = linear_portion(
       p.split, p.BH, p.H, p.T, p.lengths, p.status, blockIdx.x,
       reverse ? 0 : linear_portions(p.split, p.BH, blockIdx.x) - 1);
+  linear_let_next_start();
   if (!(reverse ? po.cut_left : po.cut_right)) return;  // the whole CTA
   const int bh = po.bh, nt = po.live;
   const int t0 = po.row(po.first), t1 = max(t0, min(po.row(po.last), po.len));
@@ -917,8 +920,8 @@ cudaError_t out_tc_d(const LinearArgs* a, int n, const CUtensorMap* maps, cudaSt
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAsked);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)a->split.parts * n, kThreads, L::kAsked, s>>>(m, p);
-  return cudaGetLastError();
+  return linear_launch(kern, dim3((unsigned)a->split.parts * n), kThreads, L::kAsked, s,
+                       a->chained, m, p);
 }
 
 template <int D>
