@@ -407,6 +407,8 @@ size_t polar_linear_bwd_workspace_bytes(int B, int H, int T, int d, int dtype);
  * added to by one thread, so results do not depend on timing.  workspace: at
  * least polar_attn_decode_paged_weights_workspace_bytes(...) bytes (the
  * split records and one fp32 logit per query head and cache row).
+ * num_splits = 0: polar_attn_decode_paged_weights_num_splits, which cuts few
+ * heads into more splits than polar_attn_decode_paged does.
  */
 int polar_attn_decode_paged_weights(const void* q, const void* k_pages, const void* v_pages,
                                     const int* block_table, const int* seq_lens,
@@ -419,6 +421,7 @@ int polar_attn_decode_paged_weights(const void* q, const void* k_pages, const vo
                                     void* stream);
 size_t polar_attn_decode_paged_weights_workspace_bytes(int B, int Hq, int Hkv, int max_seq_len,
                                                        int d, int num_splits);
+int polar_attn_decode_paged_weights_num_splits(int B, int Hkv, int max_seq_len, int d);
 
 /*
  * Eviction from a paged cache by accumulated attention weight, in place.

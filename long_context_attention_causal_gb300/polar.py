@@ -121,6 +121,8 @@ def lib() -> ctypes.CDLL:
                 ci, cp, ci, vp, cs, vp]
             L.polar_attn_decode_paged_weights_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci]
             L.polar_attn_decode_paged_weights_workspace_bytes.restype = cs
+            L.polar_attn_decode_paged_weights_num_splits.argtypes = [ci, ci, ci, ci]
+            L.polar_attn_decode_paged_weights_num_splits.restype = ci
             L.polar_cache_evict.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci,
                                             ci, ci, ci, ci, ci, vp, cs, vp]
             L.polar_cache_evict_workspace_bytes.argtypes = [ci, ci, ci, ci]
@@ -659,6 +661,10 @@ def linear_bwd(q, k, v, log_decay, dmem, state=None, dstate_out=None, lengths=No
 def decode_paged_weights_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits=0) -> int:
     return int(lib().polar_attn_decode_paged_weights_workspace_bytes(B, Hq, Hkv, max_seq_len, d,
                                                                      num_splits))
+
+
+def decode_paged_weights_num_splits(B, Hkv, max_seq_len, d) -> int:
+    return int(lib().polar_attn_decode_paged_weights_num_splits(B, Hkv, max_seq_len, d))
 
 
 _DEFAULT_CONSTS = default_consts()

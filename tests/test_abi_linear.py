@@ -93,6 +93,14 @@ def test_decode_paged_weights_validation(L):
     assert size(2, 8, 2, 1000, 64, 4) == \
         L.polar_attn_decode_paged_workspace_bytes(2, 8, 2, 1000, 64, 4) + 2 * 8 * 1000 * 4
     assert size(2, 6, 2, 1000, 64, 4) == 0
+    count = L.polar_attn_decode_paged_weights_num_splits
+    own = L.polar_attn_decode_paged_num_splits
+    assert size(2, 8, 2, 1000, 64, 0) == size(2, 8, 2, 1000, 64, count(2, 2, 1000, 64))
+    for B, Hkv, T in ((1, 1, 1), (4, 4, 1500), (1, 1, 32768), (32, 4, 32768), (1, 2, 100)):
+        s = count(B, Hkv, T, 64)
+        assert s >= own(B, Hkv, T, 64)
+        assert s == own(B, Hkv, T, 64) or (s <= 64 and s * 128 <= T and s * B * Hkv <= 2 * 160)
+    assert count(1, 0, 5, 64) == 0
 
 
 def test_cache_evict_validation(L):

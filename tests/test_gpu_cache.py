@@ -55,7 +55,8 @@ def test_weights(B, Hq, Hkv, T, d, page, dtype, splits):
     w = torch.full((B, Hkv, stride), 0.25, device=dev())
     args = [g[k] for k in ("q", "k_pages", "v_pages", "block_table", "seq_lens", "mem", "w_count")]
     got = pa.decode_paged_weights(*args, w, max_seq_len=T, num_splits=splits, want_conf=True)
-    plain = pa.decode_paged(*args, max_seq_len=T, num_splits=splits, want_conf=True)
+    same = splits or pa.decode_paged_weights_num_splits(B, Hkv, T, d)
+    plain = pa.decode_paged(*args, max_seq_len=T, num_splits=same, want_conf=True)
     for a, b in zip(got, plain):
         assert torch.equal(a, b)   # the decode itself is untouched
     for b in range(B):
