@@ -36,7 +36,8 @@ LinearSplit split(int BH, int T, int d, int dtype, int sms) {
 bool sizes_ok(int B, int H, int T, int d, int dtype) {
   return B >= 0 && H >= 0 && T >= 0 && (d == 64 || d == 128) &&
          (dtype == POLAR_F32 || dtype == POLAR_BF16) && (long long)B * H <= (1 << 20) &&
-         T <= (1 << 28);
+         T <= (1 << 28) &&
+         (long long)B * H * ((T + kLinearTile - 1) / kLinearTile) <= INT_MAX;
 }
 
 int check_sizes(int B, int H, int T, int d, int dtype, float scale) {
@@ -123,6 +124,7 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   if (st != POLAR_OK) return st;
   if (B == 0 || H == 0 || (T == 0 && !state_out)) return POLAR_OK;
   if (!log_decay || (T > 0 && (!q || !k || !v || !mem))) return POLAR_ERR_INVALID;
+  if (T > 0 && (mem == q || mem == k || mem == v)) return POLAR_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(mem) ||
       !aligned16(state_in) || !aligned16(state_out) || !aligned4(log_decay) || !aligned4(lengths))
     return POLAR_ERR_MISALIGNED;
@@ -179,6 +181,12 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   if (B == 0 || H == 0 || (T == 0 && !dstate_in)) return POLAR_OK;
   if (!log_decay || (T > 0 && (!q || !k || !v || !dmem || !dq || !dk || !dv)))
     return POLAR_ERR_INVALID;
+  if (T > 0) {
+    if (dq == dk || dq == dv || dk == dv) return POLAR_ERR_INVALID;
+    const void* const ins[] = {q, k, v, dmem};
+    for (const void* in : ins)
+      if (in == dq || in == dk || in == dv) return POLAR_ERR_INVALID;
+  }
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dmem) || !aligned16(dq) ||
       !aligned16(dk) || !aligned16(dv) || !aligned16(state_in) || !aligned16(dstate_out) ||
       !aligned16(dstate_in) || !aligned4(log_decay) || !aligned4(lengths))

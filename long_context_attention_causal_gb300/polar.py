@@ -600,7 +600,7 @@ def linear_fwd(q, k, v, log_decay, state=None, lengths=None, scale=None, mem=Non
           _in(_need(log_decay, "log_decay"), "log_decay", f32, (H,), dev),
           _in(lengths, "lengths", torch.int32, (B,), dev), _in(state, "state", f32, square, dev),
           _in(mem, "mem", dt, shape, dev), _in(state_out, "state_out", f32, square, dev),
-          B, H, T, d, code, d ** -0.5 if scale is None else scale, ws, size)
+          B, H, T, d, code, d ** -0.5 if scale is None else float(scale), ws, size)
     return mem, state_out
 
 
@@ -621,7 +621,7 @@ def linear_step(state, q, k, v, log_decay, scale=None, mem=None):
           _in(_need(k, "k"), "k", dt, shape, dev), _in(_need(v, "v"), "v", dt, shape, dev),
           _in(_need(log_decay, "log_decay"), "log_decay", torch.float32, (H,), dev),
           _in(mem, "mem", dt, shape, dev), B, H, d, _dtype_code(q),
-          d ** -0.5 if scale is None else scale)
+          d ** -0.5 if scale is None else float(scale))
     return mem
 
 
@@ -654,7 +654,7 @@ def linear_bwd(q, k, v, log_decay, dmem, state=None, dstate_out=None, lengths=No
           _in(dstate_out, "dstate_out", f32, square, dev), _in(dq, "dq", dt, shape, dev),
           _in(dk, "dk", dt, shape, dev), _in(dv, "dv", dt, shape, dev),
           _in(dstate, "dstate", f32, square, dev), B, H, T, d, code,
-          d ** -0.5 if scale is None else scale, ws, size)
+          d ** -0.5 if scale is None else float(scale), ws, size)
     return dq, dk, dv, dstate
 
 

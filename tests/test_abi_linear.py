@@ -10,6 +10,7 @@ import pytest
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 OK = ctypes.c_void_p(1 << 20)            # never dereferenced: validation fails first
+OUT = [ctypes.c_void_p((2 + i) << 20) for i in range(3)]  # distinct outputs
 ODD = ctypes.c_void_p((1 << 20) + 8)
 ODD2 = ctypes.c_void_p((1 << 20) + 2)
 NULL = ctypes.c_void_p(0)
@@ -33,7 +34,7 @@ def test_every_declared_symbol_is_exported(L):
     assert not [n for n in names if not hasattr(L, n)]
 
 
-def fwd(L, q=OK, ld=OK, lens=NULL, s_in=NULL, mem=OK, s_out=NULL, B=1, H=2, T=64, d=64, dtype=1,
+def fwd(L, q=OK, ld=OK, lens=NULL, s_in=NULL, mem=OUT[0], s_out=NULL, B=1, H=2, T=64, d=64, dtype=1,
         scale=1.0, ws=OK, wsb=BIG):
     return L.polar_linear_fwd(q, OK, OK, ld, lens, s_in, mem, s_out, B, H, T, d, dtype, scale, ws,
                               wsb, NULL)
@@ -47,13 +48,16 @@ def test_linear_fwd_validation(L):
     assert fwd(L, q=NULL) == 1 and fwd(L, ld=NULL) == 1 and fwd(L, mem=NULL) == 1
     assert fwd(L, q=ODD) == 3 and fwd(L, s_in=ODD) == 3 and fwd(L, s_out=ODD) == 3
     assert fwd(L, ld=ODD2) == 3 and fwd(L, lens=ODD2) == 3
+    assert fwd(L, mem=OK) == 1                      # over an input
+    assert fwd(L, B=1 << 10, H=1 << 10, T=1 << 28) == 2
     assert fwd(L, B=0, q=NULL) == 0 and fwd(L, T=0, q=NULL) == 0
 
 
 def test_linear_bwd_validation(L):
-    def bwd(dq=OK, dmem=OK, ds_out=NULL, ds=NULL, T=64, d=64, B=1):
-        return L.polar_linear_bwd(OK, OK, OK, OK, NULL, NULL, dmem, ds_out, dq, OK, OK, ds, B, 2,
-                                  T, d, 1, 1.0, OK, BIG, NULL)
+    def bwd(dq=OUT[0], dk=OUT[1], dmem=OK, ds_out=NULL, ds=NULL, T=64, d=64, B=1):
+        return L.polar_linear_bwd(OK, OK, OK, OK, NULL, NULL, dmem, ds_out, dq, dk, OUT[2], ds, B,
+                                  2, T, d, 1, 1.0, OK, BIG, NULL)
+    assert bwd(dq=OK) == 1 and bwd(dk=OUT[0]) == 1 and bwd(dk=OUT[2]) == 1
     assert bwd(d=80) == 2 and bwd(T=-2) == 1
     assert bwd(dq=NULL) == 1 and bwd(dmem=NULL) == 1
     assert bwd(dq=ODD) == 3 and bwd(ds_out=ODD) == 3 and bwd(ds=ODD) == 3
