@@ -6,21 +6,29 @@
 // w_j the powers of the decay:
 //   S  = x y^T                 scores            A, B in shared memory
 //   P  = S * decay, bf16                         over S in TMEM
-//   O1 = P z                                     A in TMEM
-//   O2 = x M^T                 M as a bf16 operand in shared memory
-//   out_i = O1_i + g^(i+1) O2_i
+//   O  = x M^T                 M as a bf16 operand in shared memory
+//   O_i *= g^(i+1), then O += P z                A in TMEM
 //   M' = g^n M + z^T (w y)
-// The state lives in TMEM in fp32: once a tile it is read, rounded to bf16 as
-// O2's operand, and written back times g^n for the products to add to.  w y is
-// not exact in bf16, so it enters as two bf16 terms, hi + lo (2^-16 relative):
-// the state is as good as fp32 inputs allow, and its bf16 operand is rounded
-// once.  hi and lo take turns in one buffer; two buffers of x and
-// z, one of y, that one and the state operand fill shared memory (7 x 32 KB at
-// d = 128).  The outputs are staged in z's buffer, whose last reader makes them.
+// P and the operand copy of M are rounded to bf16 once, a relative 2^-9 of what
+// the bf16 outputs are rounded by again.  The state itself stays in fp32 in
+// TMEM: once a tile it is read, multiplied by g^n and added to the tile's
+// products in one fp32 fma.  Those have an accumulator of their own, because
+// the tensor core cuts off, rather than rounds, what it adds to: 16 products a
+// tile straight into the state lost 1.6e-5 of it over 16K tokens of a slow
+// decay, against 2.9e-6 this way, which takes 4 % more time.  w y is not exact
+// in bf16, so it enters as two bf16 terms, hi + lo (2^-18 relative); a third would
+// cost a sixth product.  hi and lo take turns in one buffer; two buffers of x
+// and z, one of y, that one and the state operand fill shared memory (7 x 32 KB
+// at d = 128), and S, O, the tile's products and the state fill TMEM.  The
+// outputs are staged in z's buffer, whose last reader makes them.
 //
-// Bound: HBM.  A tile moves 4 x 32 KB at d = 128 against 6 products of
-// 2 * 128^3 flop: at the measured rates 3.0 us of an SM's share of the copy
-// bandwidth to about 2.0 us of its tensor rate.
+// Bound: HBM, closely followed by shared memory.  A tile moves 4 x 32 KB at
+// d = 128, 5600 cycles at an SM's share of the measured copy bandwidth; its
+// operands, hi and lo, the state operand and the staged outputs are about
+// 576 KB of shared memory traffic, 4500 cycles at 128 bytes each; the products
+// need 2600.  Measured: 5800 cycles a tile.  B2 H16 T16384 d128 (27 tiles a
+// CTA) takes 98 us, 5.5 TB/s, 81 % of the copy bandwidth: the rest is the
+// first loads, the last stores and the change of heads inside a run.
 //
 // Roles (480 threads, one CTA per SM): warps 0-3 P and the outputs (thread =
 // row = TMEM lane), warps 4-11 the state and the scaling of y (two groups,
@@ -39,18 +47,19 @@ constexpr int kThreads = 480;
 constexpr int kStateThreads = 256;
 constexpr int kWarpTMA = 12, kWarpMMA = 13, kWarpStore = 14;
 constexpr int kStateWarps = 8;
-constexpr uint32_t kColS = 0, kColO1 = 128, kColO2 = 256, kColM = 384;
+constexpr uint32_t kColS = 0, kColO = 128, kColDS = 256, kColM = 384;  // TMEM columns
 
 struct OutBars {
   uint64_t full_x[2], full_z[2], empty_x[2], empty_z[2];
   uint64_t full_y, empty_y;  // one phase a tile
   uint64_t s_full, p_full, o_full, o_free, staged, m_op;  // one phase a tile
-  uint64_t y_hi, y_lo, hi_done, ds_full;          // one phase a state update
+  uint64_t y_hi, y_lo, hi_done, ds_full;                  // one phase a state update
   uint64_t fixed;  // one phase a tile with rows past the sequence: they are zeroed
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  alignas(16) float full_pw[2][32];  // read as float4: g^31 .. g^0 (forward), g^0 .. g^31 (reverse); by portion parity
+  // by portion parity: g^31 .. g^0 (forward) or g^0 .. g^31 (reverse), read as float4
+  alignas(16) float full_pw[2][32];
   float diag_pw[2][64];  // 31 zeros, then g^0 .. g^31
 };
 
@@ -253,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------- MMA issuer --
     // whole warp: uniform waits and descriptors, one elected lane issues
     constexpr uint32_t kIdS = idesc_bf16_f32(kTok, kTok, 0, 0);
-    constexpr uint32_t kIdO1 = idesc_bf16_f32(kTok, D, 0, 1);
-    constexpr uint32_t kIdO2 = idesc_bf16_f32(kTok, D, 0, 0);
+    constexpr uint32_t kIdPV = idesc_bf16_f32(kTok, D, 0, 1);
+    constexpr uint32_t kIdXM = idesc_bf16_f32(kTok, D, 0, 0);
     constexpr uint32_t kIdDS = idesc_bf16_f32(128, D, 1, 1);
     const uint32_t lbo = D == 128 ? L::kAtom : 0;
     const uint32_t base = smem_u32(smem);
@@ -263,15 +272,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t mn = smem_desc_sw128(base, lbo, 1024);
     const uint64_t m_desc = smem_desc_sw128(base + L::kMOff, 16, 1024);
     auto at = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
-    auto kstep = [&](int kk, uint32_t atom) { return at((kk >> 2) * atom) + (uint64_t)(kk & 3) * 2; };
-    auto issue_ds = [&](int st) {
+    auto kstep = [&](int kk, uint32_t atom) {
+      return at((kk >> 2) * atom) + (uint64_t)(kk & 3) * 2;
+    };
+    auto issue_ds = [&](int st, bool add) {
       const uint64_t y0 = mn + at(L::kWOff), z0 = mn + at(L::kZOff + st * L::kTile);
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
-        umma_ss_warp(tmem + kColM, z0 + at(kk * 2048), y0 + at(kk * 2048), kIdDS, 1u);
+        umma_ss_warp(tmem + kColDS, z0 + at(kk * 2048), y0 + at(kk * 2048), kIdDS,
+                     add || kk > 0);
     };
-    // Order of a tile's products: S, hi, O2, lo, O1.  O2 runs while lo is
-    // written; O1 and the next S run while the next y is scaled.
+    // Order of a tile's products: S, hi, x M^T, lo, P z.  x M^T runs while lo
+    // is written; P z and the next S run while the next y is scaled.  (Waiting
+    // for the next tile's inputs before P z, so that S follows without a pause,
+    // measured 109 us against 100: the scaling then waits for its turn.)
     int k = 0, ku = 0, kf = 0;
     bool ok = true, any = false;
     for (int ip = 0; ip < n_po && ok; ++ip) {
@@ -301,34 +315,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_warp(&br.y_hi, pu, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
-          issue_ds(st);
+          issue_ds(st, false);
           umma_commit_warp(&br.hi_done);
         }
-        // O2, once the state is written and the last outputs are read
+        // x M^T, once the state is written and the last outputs are read
         ok = ok && mbar_wait_warp(&br.m_op, ph, abort_flag, p.status);
         if (ok && k > 0) ok = mbar_wait_warp(&br.o_free, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_warp(tmem + kColO2, x0 + kstep(kk, L::kAtom), m_desc + kstep(kk, L::kMAtom),
-                       kIdO2, kk > 0);
+          umma_ss_warp(tmem + kColO, x0 + kstep(kk, L::kAtom), m_desc + kstep(kk, L::kMAtom),
+                       kIdXM, kk > 0);
         umma_commit_warp(&br.empty_x[st]);
         if (upd) {
           ok = mbar_wait_warp(&br.y_lo, pu, abort_flag, p.status);
           if (!ok) break;
           tc_fence_after();
-          issue_ds(st);
+          issue_ds(st, true);
           umma_commit_warp(&br.ds_full);
           ++ku;
         }
+        // P z, added to x M^T once that has its powers of the decay
         ok = mbar_wait_warp(&br.p_full, ph, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t z0 = mn + at(L::kZOff + st * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < kTok / 16; ++kk)
-          umma_ts_warp(tmem + kColO1, tmem + kColS + kk * 8, z0 + at(kk * 2048), kIdO1, kk > 0);
+          umma_ts_warp(tmem + kColO, tmem + kColS + kk * 8, z0 + at(kk * 2048), kIdPV, 1u);
         umma_commit_warp(&br.o_full);
       }
     }
@@ -427,6 +442,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(s_tm + 16 * b, pk);
           }
           tmem_st_wait();
+          // x is free once x M^T is there: its rows times their powers
+          ok = __all_sync(0xffffffffu, mbar_wait(&br.empty_x[st], (uint32_t)(k / 2) & 1,
+                                                 abort_flag, p.status));
+        }
+        const bool live = r < n;
+        if (ok) {
+          tc_fence_after();
+          const float w2 = live ? (kRev ? linear_power(l2, n - 1 - r)
+                                        : p.scale * linear_power(l2, r + 1))
+                                : 0.f;
+#pragma unroll 1
+          for (int b = 0; b < D / 32; ++b) {
+            uint32_t v[32];
+            tmem_ld32(tmem + lane_base + kColO + 32 * b, v);
+            tmem_ld_wait();
+            reg_fence32(v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(w2 * __uint_as_float(v[e]));
+            tmem_st32(tmem + lane_base + kColO + 32 * b, v);
+          }
+          tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&br.p_full);
@@ -434,19 +470,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) {
           tc_fence_after();
-          const bool live = r < n;
-          const float w2 = live ? (kRev ? linear_power(l2, n - 1 - r)
-                                        : p.scale * linear_power(l2, r + 1))
-                                : 0.f;
           uint8_t* line = smem + L::kZOff + st * L::kTile + r * 128;  // z's readers are done
 #pragma unroll 1
           for (int b = 0; b < D / 32; ++b) {
-            uint32_t o1[32], o2[32];
-            tmem_ld32(tmem + lane_base + kColO1 + 32 * b, o1);
-            tmem_ld32(tmem + lane_base + kColO2 + 32 * b, o2);
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_base + kColO + 32 * b, o);
             tmem_ld_wait();
-            reg_fence32(o1);
-            reg_fence32(o2);
+            reg_fence32(o);
             if (b == D / 32 - 1) {
               tc_fence_before();
               __syncwarp();
@@ -458,9 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int i = 8 * g + 2 * e;
-                const float a0 = fmaf(w2, __uint_as_float(o2[i]), __uint_as_float(o1[i]));
-                const float a1 = fmaf(w2, __uint_as_float(o2[i + 1]), __uint_as_float(o1[i + 1]));
-                o4[e] = live ? pack_bf16x2(a0, a1) : 0u;
+                o4[e] = live ? pack_bf16x2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])) : 0u;
               }
               const int ch = (b & 1) * 4 + g;
               *reinterpret_cast<uint4*>(line + (b >> 1) * L::kAtom + ((ch ^ (r & 7)) << 4)) =
@@ -491,17 +519,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kVecs = kTok * D / 8 / kStateThreads;  // 16-byte pieces of y a thread
     const bool mine = r < D;           // at d = 64 lanes 64.. repeat the rows
     const uint32_t m_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColM + half * kCols;
-    // The state, 32 columns at a time: its bf16 operand for O2 and, if `scale`,
-    // the state times g back into TMEM, where the next products add to it.
-    auto hand_over = [&](bool scale, float g) {
+    const uint32_t ds_tm = m_tm - kColM + kColDS;
+    // 32 columns of the state: after a tile, g times the one before it plus the
+    // tile's products.
+    auto state_block = [&](int b, bool add, float g, uint32_t (&v)[32]) {
+      tmem_ld32(m_tm + 32 * b, v);
+      if (add) {
+        uint32_t ds[32];
+        tmem_ld32(ds_tm + 32 * b, ds);
+        tmem_ld_wait();
+        reg_fence32(v);
+        reg_fence32(ds);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          v[e] = __float_as_uint(fmaf(g, __uint_as_float(v[e]), __uint_as_float(ds[e])));
+      } else {
+        tmem_ld_wait();
+        reg_fence32(v);
+      }
+    };
+    // The state to its bf16 operand for x M^T and, if new, back into TMEM.
+    auto hand_over = [&](bool add, float g) {
       int sw = r & 7;
       asm volatile("" : "+r"(sw));  // not to be kept as eight addresses across the loop
 #pragma unroll
       for (int b = 0; b < kCols / 32; ++b) {
         uint32_t v[32];
-        tmem_ld32(m_tm + 32 * b, v);
-        tmem_ld_wait();
-        reg_fence32(v);
+        state_block(b, add, g, v);
         if (mine) {
           const int col = half * kCols + 32 * b;
           uint8_t* line = smem + L::kMOff + (col >> 6) * L::kMAtom + r * 128;
@@ -517,13 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        if (scale) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(g * __uint_as_float(v[e]));
-          tmem_st32(m_tm + 32 * b, v);
-        }
+        if (add) tmem_st32(m_tm + 32 * b, v);
       }
-      if (scale) tmem_st_wait();
+      if (add) tmem_st_wait();
     };
     int k = 0, ku = 0;
     bool ok = true;
@@ -565,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
       }
       bool wait_ds = false;  // products of the tile before are under way
+      float g = 0.f;         // what the state decays by over that tile
       for (int c = 0; c < po.live; ++c, ++k) {
         const int st = k & 1, tile = tile_of(po, c), n = po.tokens(tile);
         const bool upd = updates(po, c);
@@ -608,7 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        hand_over(upd, linear_power(l2, n));
+        hand_over(wait_ds, g);
+        g = linear_power(l2, n);
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -640,9 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < kCols / 32; ++b) {
           uint32_t v[32];
-          tmem_ld32(m_tm + 32 * b, v);
-          tmem_ld_wait();
-          reg_fence32(v);
+          state_block(b, wait_ds, g, v);
           if (mine) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
@@ -666,11 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------ states at cuts --
 
-// Each run's own part of the head that its boundary cuts: one accumulator in
-// TMEM over the tiles, y weighted by the distance to the cut, hi and lo, so
-// nothing is ever rescaled.  hi replaces y, lo goes through one buffer of its
-// own.  The tiles are walked so that those the output kernel starts with come
-// last: it then finds them in L2.  Bound: HBM (64 KB a tile at d = 128).
+// Each run's own part of the head that its boundary cuts, y weighted by the
+// distance to the cut, so nothing is ever rescaled: a tile's products (hi and
+// lo, as above) go to one of two accumulators in TMEM and are added up in fp32
+// registers while the next tile's run.  hi replaces y, lo goes through one
+// buffer of its own.  The tiles are walked so that those the output kernel
+// starts with come last: it then finds them in L2.  Bound: HBM (64 KB a tile at
+// d = 128).  B2 H16 T16384 d128: 45 us, 5.3 TB/s, 79 % of the copy bandwidth.
 constexpr int kSThreads = 320;  // 8 scaling warps, TMA, MMA
 constexpr int kSWarpTMA = 8, kSWarpMMA = 9;
 
@@ -688,8 +730,8 @@ struct StateLayout {
 
 struct StateBars {
   uint64_t full[6], empty[6], hi[6];
-  uint64_t lo, lo_free;  // one phase a tile
-  uint64_t done, drain;
+  uint64_t lo, lo_done;  // one phase a tile
+  uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -738,13 +780,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
       mbar_init(&br.hi[i], kStateWarps);
     }
     mbar_init(&br.lo, kStateWarps);
-    mbar_init(&br.lo_free, 1);
-    mbar_init(&br.done, 1);
+    mbar_init(&br.lo_done, 1);
     mbar_init(&br.drain, 1);
     br.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kSWarpMMA) tmem_alloc(&br.tmem_base, 128);
+  if (warp == kSWarpMMA) tmem_alloc(&br.tmem_base, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -792,21 +833,20 @@ __global__ void __launch_bounds__(kSThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint64_t y0 = mn + at(st * L::kStage), z0 = y0 + at(L::kTile), l0 = mn + at(L::kLoOff);
+      const uint32_t acc = tmem + (c & 1) * 128;
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
-        umma_ss_warp(tmem, z0 + at(kk * 2048), y0 + at(kk * 2048), kId,
-                     (c > 0 || kk > 0) ? 1u : 0u);
+        umma_ss_warp(acc, z0 + at(kk * 2048), y0 + at(kk * 2048), kId, kk > 0);
       any = true;
       ok = mbar_wait_warp(&br.lo, (uint32_t)c & 1, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
-        umma_ss_warp(tmem, z0 + at(kk * 2048), l0 + at(kk * 2048), kId, 1u);
-      umma_commit_warp(&br.lo_free);
+        umma_ss_warp(acc, z0 + at(kk * 2048), l0 + at(kk * 2048), kId, 1u);
+      umma_commit_warp(&br.lo_done);
       umma_commit_warp(&br.empty[st]);
     }
-    if (ok && any) umma_commit_warp(&br.done);
     if (!ok && any) {
       volatile int never = 0;
       umma_commit_warp(&br.drain);
@@ -816,6 +856,28 @@ __global__ void __launch_bounds__(kSThreads, 1)
     }
   } else {
     const int tid = threadIdx.x;
+    const int half = warp >> 2, r = threadIdx.x & 127;
+    constexpr int kCols = D / 2;
+    float sum[kCols];  // row r of the state, half of its columns
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) sum[e] = 0.f;
+    // the products of tile c, once they are done
+    auto collect = [&](int c) {
+      if (!mbar_wait_warp(&br.lo_done, (uint32_t)c & 1, abort_flag, p.status)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < kCols / 32; ++b) {
+        uint32_t v[32];
+        tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (c & 1) * 128 + half * kCols +
+                      32 * b, v);
+        tmem_ld_wait();
+        reg_fence32(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum[32 * b + e] += __uint_as_float(v[e]);
+      }
+      tc_fence_before();
+      return true;
+    };
     bool ok = true;
     for (int c = 0; c < nt; ++c) {
       const int st = c % NS, row = tile_row(c), n = min(kTok, t1 - row);
@@ -844,10 +906,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&br.hi[st]);
-      if (c > 0) {
-        ok = mbar_wait_warp(&br.lo_free, (uint32_t)(c - 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-      }
+      if (c > 0) ok = collect(c - 1);  // lo is free then, too
+      if (!ok) break;
       uint4* to = reinterpret_cast<uint4*>(smem + L::kLoOff) + tid;
 #pragma unroll
       for (int q = 0; q < kVecs; ++q) to[kStateThreads * q] = lo[q];
@@ -855,31 +915,13 @@ __global__ void __launch_bounds__(kSThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&br.lo);
     }
-    const int half = warp >> 2, r = threadIdx.x & 127;
-    constexpr int kCols = D / 2;
-    float* dst = p.cuts[op] + ((size_t)blockIdx.x * D + r) * D + half * kCols;
-    ok = ok && (nt == 0 || mbar_wait(&br.done, 0, abort_flag, p.status));
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
+    if (ok && nt > 0) ok = collect(nt - 1);
+    if (ok && r < D) {
+      float* dst = p.cuts[op] + ((size_t)blockIdx.x * D + r) * D + half * kCols;
 #pragma unroll
-      for (int b = 0; b < kCols / 32; ++b) {
-        uint32_t v[32];
-        if (nt > 0) {
-          tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * kCols + 32 * b, v);
-          tmem_ld_wait();
-          reg_fence32(v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0u;
-        }
-        if (r < D) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(dst + 32 * b + e) =
-                make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        }
-      }
+      for (int e = 0; e < kCols; e += 4)
+        *reinterpret_cast<float4*>(dst + e) =
+            make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
     }
   }
 
@@ -887,7 +929,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   __syncthreads();
   if (warp == kSWarpMMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 

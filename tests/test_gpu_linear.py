@@ -194,6 +194,26 @@ def test_decay_extremes():
         assert torch.isfinite(step.float()).all()
 
 
+@pytest.mark.parametrize("H,T,d", [(2, 16384, 128), (304, 8192, 64)])
+def test_state_without_decay_stays_fp32(H, T, d):
+    """Positive inputs and no decay: the state grows to T products of one sign,
+    where accumulation errors show.  w = 1 exactly and bf16 inputs are exact as
+    hi, so per element, relative: the tensor core adds 16 products a tile into
+    the tile's own sum (cut off, 2^-22 each of a sum that holds T / tiles), and
+    each tile rounds the fp32 state once, 2^-24; joining runs once more each.
+    2^-18 covers inputs that need lo."""
+    import long_context_attention_causal_gb300 as pa
+
+    g = torch.Generator(device=dev()).manual_seed(40 + d)
+    q, k, v = (torch.randn(1, H, T, d, generator=g, device=dev()).abs().bfloat16()
+               for _ in range(3))
+    state = pa.linear_fwd(q, k, v, torch.zeros(H, device=dev()), want_state=True)[1]
+    tol = 2.0 ** -18 + 16 * 2.0 ** -22 + 2 * (T / 128) * 2.0 ** -24
+    for h in (0, H // 2, H - 1):
+        ref = v[0, h].double().T @ k[0, h].double()
+        assert float(((state[0, h].double() - ref).abs() / ref).max()) <= tol
+
+
 def test_state_in_place_and_repeats():
     """state_out may be state; the same call gives the same bits."""
     import long_context_attention_causal_gb300 as pa
