@@ -42,12 +42,6 @@ __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
                      __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
 }
-__device__ __forceinline__ void store2(float* p, float a, float b) {
-  *reinterpret_cast<float2*>(p) = make_float2(a, b);
-}
-__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
-  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
-}
 // Dot products and updates run on pairs of values (fma .f32x2): half the
 // instructions of scalar code, which is what bounds these kernels.
 __device__ __forceinline__ float2 dot4(float4 a, float4 b, float2 c) {
@@ -69,13 +63,12 @@ template <int W>
 struct Pieces {
   static constexpr int kV = W / 4, kN = kC * kV / kThreads;
   float4 v[kN];
-  template <typename T>
-  __device__ __forceinline__ void load(const T* src, int ld, int t0, int end) {
+  __device__ __forceinline__ void load(const float* src, int ld, int t0, int end) {
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
       const int i = threadIdx.x + u * kThreads, r = i / kV, c = (i % kV) * 4;
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t0 + r < end) v[u] = load4<T>(src + (size_t)(t0 + r) * ld + c);
+      if (t0 + r < end) v[u] = load4<float>(src + (size_t)(t0 + r) * ld + c);
     }
   }
   template <int S>
@@ -131,7 +124,7 @@ struct OutBatch {
 
 // Grid (parts, D / kZ): the part of the run that reaches its cut.  Weights are
 // taken from the cut, so the accumulators never need rescaling.
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
     polar_linear_state_kernel(const StateBatch batch) {
   const LinearStateArgs& a = batch.a[blockIdx.z];
@@ -145,8 +138,8 @@ __global__ void __launch_bounds__(kThreads)
   if (!(a.reverse ? po.cut_left : po.cut_right)) return;
   const int t0 = po.row(po.first), t1 = max(t0, min(po.row(po.last), po.len));
   const float l2 = linear_log2_decay(a.log_decay, po.bh % a.H);
-  const T* y = static_cast<const T*>(a.y) + (size_t)po.bh * a.T * D;
-  const T* z = static_cast<const T*>(a.z) + (size_t)po.bh * a.T * D;
+  const float* y = static_cast<const float*>(a.y) + (size_t)po.bh * a.T * D;
+  const float* z = static_cast<const float*>(a.z) + (size_t)po.bh * a.T * D;
   float4 acc[S::kR];
 #pragma unroll
   for (int r = 0; r < S::kR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -246,7 +239,7 @@ struct OutSmem {
 
 // Grid (parts, D / kZ): the CTA walks its run's chunks with its 32 rows of the
 // state in shared memory.
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
     polar_linear_out_kernel(const OutBatch batch) {
   const LinearArgs& a = batch.a[blockIdx.z];
@@ -260,159 +253,159 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tx = tid & 15, ty = tid >> 4;
   const int n_po = linear_portions(a.split, BH, part);
   for (int ip = 0; ip < n_po; ++ip) {
-  const LinearPortion po = linear_portion(a.split, BH, a.H, a.T, a.lengths, a.status, part,
-                                          a.reverse ? n_po - 1 - ip : ip);
-  const int bh = po.bh, len = po.len;
-  const int t0 = po.row(po.first), t1 = min(po.row(po.last), a.T);
-  const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
-  const T* x = static_cast<const T*>(a.x) + (size_t)bh * a.T * D;
-  const T* y = static_cast<const T*>(a.y) + (size_t)bh * a.T * D;
-  const T* z = static_cast<const T*>(a.z) + (size_t)bh * a.T * D;
-  T* out = static_cast<T*>(a.out) + (size_t)bh * a.T * D;
-  float* fin = a.final_state && !(a.reverse ? po.cut_left : po.cut_right)
-                   ? a.final_state + (size_t)bh * D * D
-                   : nullptr;
+    const LinearPortion po = linear_portion(a.split, BH, a.H, a.T, a.lengths, a.status, part,
+                                            a.reverse ? n_po - 1 - ip : ip);
+    const int bh = po.bh, len = po.len;
+    const int t0 = po.row(po.first), t1 = min(po.row(po.last), a.T);
+    const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
+    const float* x = static_cast<const float*>(a.x) + (size_t)bh * a.T * D;
+    const float* y = static_cast<const float*>(a.y) + (size_t)bh * a.T * D;
+    const float* z = static_cast<const float*>(a.z) + (size_t)bh * a.T * D;
+    float* out = static_cast<float*>(a.out) + (size_t)bh * a.T * D;
+    float* fin = a.final_state && !(a.reverse ? po.cut_left : po.cut_right)
+                     ? a.final_state + (size_t)bh * D * D
+                     : nullptr;
 
-  const float* st = (a.reverse ? po.cut_right : po.cut_left)
-                        ? a.cuts + (size_t)(a.reverse ? part + 1 : part - 1) * D * D
-                        : (a.init ? a.init + (size_t)bh * D * D : nullptr);
-  __syncthreads();  // the last portion's reads are done
-  for (int i = tid; i < kZ * D; i += kThreads) {
-    const int r = a.state_t ? i % kZ : i / D, c = a.state_t ? i / kZ : i % D;
-    float v = 0.f;
-    if (st) v = a.state_t ? st[(size_t)c * D + z0 + r] : st[(size_t)(z0 + r) * D + c];
-    sm.m[r][c] = v;
-  }
-  for (int i = tid; i <= kC; i += kThreads) sm.pw[i] = linear_power(l2, i);
-  // forward: the output scale applies to the state's part too; reverse: the
-  // state already carries it
-  const float s_in = a.reverse ? 1.f : a.scale, s_z = a.reverse ? a.scale : 1.f;
-  const int n_ch = (t1 - t0 + kC - 1) / kC;
-  const int end = min(len, t1);
-  auto chunk = [&](int ci) { return t0 + (a.reverse ? n_ch - 1 - ci : ci) * kC; };
-  Pieces<D> px, py;
-  Pieces<kZ> pz;
-  auto fetch = [&](int c0) {
-    px.load(x, D, c0, end);
-    py.load(y, D, c0, end);
-    pz.load(z + z0, D, c0, end);
-  };
-  fetch(chunk(0));
-  for (int ci = 0; ci < n_ch; ++ci) {
-    const int c0 = chunk(ci);
-    const int n = min(max(end - c0, 0), kC);  // tokens of the chunk
-    __syncthreads();
-    px.store(sm.x);
-    py.store(sm.y);
-    pz.store(sm.z);
-    if (ci + 1 < n_ch) fetch(chunk(ci + 1));
-    __syncthreads();
-    const float2 zero = make_float2(0.f, 0.f);
-    float o[4][2];
-#pragma unroll
-    for (int ii = 0; ii < 4; ++ii) o[ii][0] = o[ii][1] = 0.f;
-    if (n > 0) {
-      // scores: rows 4 ty .., keys tx + 16 jj
-      float2 sc[4][4];
-#pragma unroll
-      for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = zero;
-#pragma unroll 2
-      for (int k = 0; k < D; k += 4) {
-        float4 xv[4], yv[4];
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
-          xv[ii] = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj)
-          yv[jj] = *reinterpret_cast<const float4*>(&sm.y[tx + 16 * jj][k]);
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = dot4(xv[ii], yv[jj], sc[ii][jj]);
-      }
-#pragma unroll
-      for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          const int i = 4 * ty + ii, j = tx + 16 * jj;
-          const int dist = a.reverse ? j - i : i - j;
-          sm.p[i][j] = dist >= 0 ? (sc[ii][jj].x + sc[ii][jj].y) * sm.pw[dist] : 0.f;
-        }
-      for (int i = tid; i < kC * kZ; i += kThreads) {
-        const int r = i / kZ;
-        const float w = r < n ? s_z * sm.pw[a.reverse ? r + 1 : n - 1 - r] : 0.f;
-        sm.zw[r][i % kZ] = sm.z[r][i % kZ] * w;
-      }
+    const float* st = (a.reverse ? po.cut_right : po.cut_left)
+                          ? a.cuts + (size_t)(a.reverse ? part + 1 : part - 1) * D * D
+                          : (a.init ? a.init + (size_t)bh * D * D : nullptr);
+    __syncthreads();  // the last portion's reads are done
+    for (int i = tid; i < kZ * D; i += kThreads) {
+      const int r = a.state_t ? i % kZ : i / D, c = a.state_t ? i / kZ : i % D;
+      float v = 0.f;
+      if (st) v = a.state_t ? st[(size_t)c * D + z0 + r] : st[(size_t)(z0 + r) * D + c];
+      sm.m[r][c] = v;
+    }
+    for (int i = tid; i <= kC; i += kThreads) sm.pw[i] = linear_power(l2, i);
+    // forward: the output scale applies to the state's part too; reverse: the
+    // state already carries it
+    const float s_in = a.reverse ? 1.f : a.scale, s_z = a.reverse ? a.scale : 1.f;
+    const int n_ch = (t1 - t0 + kC - 1) / kC;
+    const int end = min(len, t1);
+    auto chunk = [&](int ci) { return t0 + (a.reverse ? n_ch - 1 - ci : ci) * kC; };
+    Pieces<D> px, py;
+    Pieces<kZ> pz;
+    auto fetch = [&](int c0) {
+      px.load(x, D, c0, end);
+      py.load(y, D, c0, end);
+      pz.load(z + z0, D, c0, end);
+    };
+    fetch(chunk(0));
+    for (int ci = 0; ci < n_ch; ++ci) {
+      const int c0 = chunk(ci);
+      const int n = min(max(end - c0, 0), kC);  // tokens of the chunk
       __syncthreads();
-      // the state's part: rows 4 ty .., state rows 2 tx, 2 tx + 1
-      float2 m[4][2], q[4][2];
+      px.store(sm.x);
+      py.store(sm.y);
+      pz.store(sm.z);
+      if (ci + 1 < n_ch) fetch(chunk(ci + 1));
+      __syncthreads();
+      const float2 zero = make_float2(0.f, 0.f);
+      float o[4][2];
 #pragma unroll
-      for (int ii = 0; ii < 4; ++ii) m[ii][0] = m[ii][1] = q[ii][0] = q[ii][1] = zero;
+      for (int ii = 0; ii < 4; ++ii) o[ii][0] = o[ii][1] = 0.f;
+      if (n > 0) {
+        // scores: rows 4 ty .., keys tx + 16 jj
+        float2 sc[4][4];
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = zero;
 #pragma unroll 2
-      for (int k = 0; k < D; k += 4) {
-        const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[2 * tx][k]);
-        const float4 m1 = *reinterpret_cast<const float4*>(&sm.m[2 * tx + 1][k]);
+        for (int k = 0; k < D; k += 4) {
+          float4 xv[4], yv[4];
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-          const float4 xv = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
-          m[ii][0] = dot4(xv, m0, m[ii][0]);
-          m[ii][1] = dot4(xv, m1, m[ii][1]);
+          for (int ii = 0; ii < 4; ++ii)
+            xv[ii] = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
+            yv[jj] = *reinterpret_cast<const float4*>(&sm.y[tx + 16 * jj][k]);
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = dot4(xv[ii], yv[jj], sc[ii][jj]);
         }
-      }
-      // the chunk's own part
-#pragma unroll 2
-      for (int j = 0; j < kC; j += 4) {
-        float2 zv[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          zv[e] = *reinterpret_cast<const float2*>(&sm.z[j + e][2 * tx]);
+        for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) {
+            const int i = 4 * ty + ii, j = tx + 16 * jj;
+            const int dist = a.reverse ? j - i : i - j;
+            sm.p[i][j] = dist >= 0 ? (sc[ii][jj].x + sc[ii][jj].y) * sm.pw[dist] : 0.f;
+          }
+        for (int i = tid; i < kC * kZ; i += kThreads) {
+          const int r = i / kZ;
+          const float w = r < n ? s_z * sm.pw[a.reverse ? r + 1 : n - 1 - r] : 0.f;
+          sm.zw[r][i % kZ] = sm.z[r][i % kZ] * w;
+        }
+        __syncthreads();
+        // the state's part: rows 4 ty .., state rows 2 tx, 2 tx + 1
+        float2 m[4][2], q[4][2];
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) m[ii][0] = m[ii][1] = q[ii][0] = q[ii][1] = zero;
+#pragma unroll 2
+        for (int k = 0; k < D; k += 4) {
+          const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[2 * tx][k]);
+          const float4 m1 = *reinterpret_cast<const float4*>(&sm.m[2 * tx + 1][k]);
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) {
+            const float4 xv = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
+            m[ii][0] = dot4(xv, m0, m[ii][0]);
+            m[ii][1] = dot4(xv, m1, m[ii][1]);
+          }
+        }
+        // the chunk's own part
+#pragma unroll 2
+        for (int j = 0; j < kC; j += 4) {
+          float2 zv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            zv[e] = *reinterpret_cast<const float2*>(&sm.z[j + e][2 * tx]);
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) {
+            const float4 pv = *reinterpret_cast<const float4*>(&sm.p[4 * ty + ii][j]);
+            // both columns at once
+            q[ii][0] = ffma2(make_float2(pv.x, pv.x), zv[0], q[ii][0]);
+            q[ii][1] = ffma2(make_float2(pv.y, pv.y), zv[1], q[ii][1]);
+            q[ii][0] = ffma2(make_float2(pv.z, pv.z), zv[2], q[ii][0]);
+            q[ii][1] = ffma2(make_float2(pv.w, pv.w), zv[3], q[ii][1]);
+          }
+        }
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
-          const float4 pv = *reinterpret_cast<const float4*>(&sm.p[4 * ty + ii][j]);
-          // both columns at once
-          q[ii][0] = ffma2(make_float2(pv.x, pv.x), zv[0], q[ii][0]);
-          q[ii][1] = ffma2(make_float2(pv.y, pv.y), zv[1], q[ii][1]);
-          q[ii][0] = ffma2(make_float2(pv.z, pv.z), zv[2], q[ii][0]);
-          q[ii][1] = ffma2(make_float2(pv.w, pv.w), zv[3], q[ii][1]);
+          const int i = 4 * ty + ii;
+          const float w = i < n ? s_in * sm.pw[a.reverse ? n - 1 - i : i + 1] : 0.f;
+          o[ii][0] = fmaf(a.scale, q[ii][0].x + q[ii][1].x, w * (m[ii][0].x + m[ii][0].y));
+          o[ii][1] = fmaf(a.scale, q[ii][0].y + q[ii][1].y, w * (m[ii][1].x + m[ii][1].y));
         }
       }
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
         const int i = 4 * ty + ii;
-        const float w = i < n ? s_in * sm.pw[a.reverse ? n - 1 - i : i + 1] : 0.f;
-        o[ii][0] = fmaf(a.scale, q[ii][0].x + q[ii][1].x, w * (m[ii][0].x + m[ii][0].y));
-        o[ii][1] = fmaf(a.scale, q[ii][0].y + q[ii][1].y, w * (m[ii][1].x + m[ii][1].y));
+        if (c0 + i < t1)
+          *reinterpret_cast<float2*>(out + (size_t)(c0 + i) * D + z0 + 2 * tx) =
+              make_float2(i < n ? o[ii][0] : 0.f, i < n ? o[ii][1] : 0.f);
+      }
+      if (n > 0 && (ci + 1 < n_ch || fin)) {
+        __syncthreads();  // every read of the state is done
+        float4 acc[S::kR];
+        const float g = sm.pw[n];
+#pragma unroll
+        for (int r = 0; r < S::kR; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(&sm.m[S::row0() + r][S::col0()]);
+          acc[r] = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
+        }
+        state_products<D>(acc, sm.y, sm.zw);
+#pragma unroll
+        for (int r = 0; r < S::kR; ++r)
+          *reinterpret_cast<float4*>(&sm.m[S::row0() + r][S::col0()]) = acc[r];
       }
     }
-#pragma unroll
-    for (int ii = 0; ii < 4; ++ii) {
-      const int i = 4 * ty + ii;
-      if (c0 + i < t1)
-        store2(out + (size_t)(c0 + i) * D + z0 + 2 * tx, i < n ? o[ii][0] : 0.f,
-               i < n ? o[ii][1] : 0.f);
+    if (fin) {
+      __syncthreads();
+      for (int i = tid; i < kZ * D; i += kThreads)
+        fin[(size_t)(z0 + i / D) * D + i % D] = sm.m[i / D][i % D];
     }
-    if (n > 0 && (ci + 1 < n_ch || fin)) {
-      __syncthreads();  // every read of the state is done
-      float4 acc[S::kR];
-      const float g = sm.pw[n];
-#pragma unroll
-      for (int r = 0; r < S::kR; ++r) {
-        const float4 v = *reinterpret_cast<const float4*>(&sm.m[S::row0() + r][S::col0()]);
-        acc[r] = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
-      }
-      state_products<D>(acc, sm.y, sm.zw);
-#pragma unroll
-      for (int r = 0; r < S::kR; ++r)
-        *reinterpret_cast<float4*>(&sm.m[S::row0() + r][S::col0()]) = acc[r];
-    }
-  }
-  if (fin) {
-    __syncthreads();
-    for (int i = tid; i < kZ * D; i += kThreads)
-      fin[(size_t)(z0 + i / D) * D + i % D] = sm.m[i / D][i % D];
-  }
   }
 }
 
@@ -467,7 +460,7 @@ cudaError_t step_d(const LinearStepArgs& a, cudaStream_t s) {
 
 template <int D>
 cudaError_t states_d(const StateBatch& batch, int n, cudaStream_t s) {
-  polar_linear_state_kernel<D, float>
+  polar_linear_state_kernel<D>
       <<<dim3((unsigned)batch.a[0].split.parts, D / kZ, n), kThreads, 0, s>>>(batch);
   return cudaGetLastError();
 }
@@ -475,10 +468,10 @@ cudaError_t states_d(const StateBatch& batch, int n, cudaStream_t s) {
 template <int D>
 cudaError_t out_d(const OutBatch& batch, int n, cudaStream_t s) {
   const int smem = (int)sizeof(OutSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D, float>,
+  cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return linear_launch(polar_linear_out_kernel<D, float>,
+  return linear_launch(polar_linear_out_kernel<D>,
                        dim3((unsigned)batch.a[0].split.parts, D / kZ, n), kThreads, smem, s,
                        batch.a[0].chained, batch);
 }
