@@ -348,9 +348,9 @@ int polar_memory_step(float* state, const void* q, const void* k, const void* v,
  *   state_in     : [B, H, d, d] fp32 or NULL (zero)
  *   state_out    : [B, H, d, d] fp32 or NULL: S after each sequence's last
  *                  token (after lengths[b] = 0 tokens: state_in).  May be
- *                  state_in itself; other overlaps are not allowed.
- * mem must not overlap the inputs.  Rows at or past lengths[b] are written as
- * zeros.  A token that holds an infinity or NaN may make other rows of its
+ *                  state_in itself.
+ * Other overlaps of an output with a tensor of the call are refused
+ * (POLAR_ERR_INVALID).  Rows at or past lengths[b] are written as zeros.  A token that holds an infinity or NaN may make other rows of its
  * 128-token tile non-finite, earlier ones included.  A length outside
  * [0, T] is clamped and records status 3 in polar_attn_device_status.
  * polar_linear_fwd takes a prompt by chunks of tokens; polar_linear_step is
@@ -377,10 +377,9 @@ int polar_linear_step(float* state, const void* q, const void* k, const void* v,
  *   dmem       : [B, H, T, d] of dtype (rows past lengths[b] are not read
  *                into any result)
  *   dstate_out : [B, H, d, d] fp32 or NULL (zero): gradient of state_out
- *   dq, dk, dv : [B, H, T, d] of dtype (written; rows past lengths[b] zero;
- *                not over the inputs)
+ *   dq, dk, dv : [B, H, T, d] of dtype (written; rows past lengths[b] zero)
  *   dstate_in  : [B, H, d, d] fp32 or NULL (may be dstate_out itself)
- * The other arguments are the forward's.  The decay is a constant of the
+ * The other arguments are the forward's, overlaps too.  The decay is a constant of the
  * layer, as the temperature's and the gate's constants are: it carries no
  * gradient.  workspace: polar_linear_bwd_workspace_bytes(...) bytes.
  */

@@ -5,6 +5,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "polar_device.cuh"
 #include "polar_internal.h"
@@ -44,6 +45,37 @@ int check_sizes(int B, int H, int T, int d, int dtype, float scale) {
   if (B < 0 || H < 0 || T < 0 || !std::isfinite(scale)) return POLAR_ERR_INVALID;
   return sizes_ok(B, H, T, d, dtype) ? POLAR_OK : POLAR_ERR_UNSUPPORTED;
 }
+
+// Bytes of a tensor; an output that meets another tensor is refused.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+bool any_meet(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span& o : outs) {
+    for (const Span& i : ins)
+      if (meet(o, i)) return true;
+    for (const Span& other : outs)
+      if (&other != &o && meet(o, other)) return true;
+  }
+  return false;
+}
+// The spans of a [B, H, T, d] tensor and of the states; `same` is left out of
+// the latter where an output may be that input itself.
+struct Sizes {
+  size_t rows, states;
+  Sizes(int B, int H, int T, int d, int dtype)
+      : rows((size_t)B * H * T * d * (dtype == POLAR_BF16 ? 2 : 4)),
+        states((size_t)B * H * d * d * 4) {}
+  Span row(const void* p) const { return {p, rows}; }
+  Span state(const void* p, const void* same = nullptr) const {
+    return {p == same ? nullptr : p, states};
+  }
+};
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -124,10 +156,13 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   if (st != POLAR_OK) return st;
   if (B == 0 || H == 0 || (T == 0 && !state_out)) return POLAR_OK;
   if (!log_decay || (T > 0 && (!q || !k || !v || !mem))) return POLAR_ERR_INVALID;
-  if (T > 0 && (mem == q || mem == k || mem == v)) return POLAR_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(mem) ||
       !aligned16(state_in) || !aligned16(state_out) || !aligned4(log_decay) || !aligned4(lengths))
     return POLAR_ERR_MISALIGNED;
+  const Sizes z(B, H, T, d, dtype);
+  if (any_meet({z.row(mem), z.state(state_out)},
+               {z.row(q), z.row(k), z.row(v), z.state(state_in, state_out)}))
+    return POLAR_ERR_INVALID;
   int sms = 0;
   st = check_device(&sms);
   if (st != POLAR_OK) return st;
@@ -164,6 +199,9 @@ int polar_linear_step(float* state, const void* q, const void* k, const void* v,
   if (!aligned16(state) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(mem) ||
       !aligned4(log_decay))
     return POLAR_ERR_MISALIGNED;
+  const Sizes z(B, H, 1, d, dtype);
+  if (any_meet({z.row(mem), z.state(state)}, {z.row(q), z.row(k), z.row(v)}))
+    return POLAR_ERR_INVALID;
   st = check_device(nullptr);
   if (st != POLAR_OK) return st;
   const LinearStepArgs a{state, q, k, v, log_decay, mem, B, H, d, scale};
@@ -181,16 +219,15 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   if (B == 0 || H == 0 || (T == 0 && !dstate_in)) return POLAR_OK;
   if (!log_decay || (T > 0 && (!q || !k || !v || !dmem || !dq || !dk || !dv)))
     return POLAR_ERR_INVALID;
-  if (T > 0) {
-    if (dq == dk || dq == dv || dk == dv) return POLAR_ERR_INVALID;
-    const void* const ins[] = {q, k, v, dmem};
-    for (const void* in : ins)
-      if (in == dq || in == dk || in == dv) return POLAR_ERR_INVALID;
-  }
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dmem) || !aligned16(dq) ||
       !aligned16(dk) || !aligned16(dv) || !aligned16(state_in) || !aligned16(dstate_out) ||
       !aligned16(dstate_in) || !aligned4(log_decay) || !aligned4(lengths))
     return POLAR_ERR_MISALIGNED;
+  const Sizes z(B, H, T, d, dtype);
+  if (any_meet({z.row(dq), z.row(dk), z.row(dv), z.state(dstate_in)},
+               {z.row(q), z.row(k), z.row(v), z.row(dmem), z.state(state_in),
+                z.state(dstate_out, dstate_in)}))
+    return POLAR_ERR_INVALID;
   int sms = 0;
   st = check_device(&sms);
   if (st != POLAR_OK) return st;

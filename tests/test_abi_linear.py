@@ -71,6 +71,45 @@ def test_linear_step_validation(L):
     assert step(dtype=5) == 2 and step(scale=float("nan")) == 1 and step(B=0, q=NULL) == 0
 
 
+def test_linear_overlaps_are_refused(L):
+    """Outputs that meet another tensor of the call, at their first or last
+    bytes; a state may be updated in place.  Two heads of 4000 tokens are cut
+    and need a workspace, which is not given: nothing can launch anywhere."""
+    at = [1 << 24 | i << 22 for i in range(4)] + [1 << 26 | i << 22 for i in range(8)]
+    n, ns = 2 * 4000 * 64 * 2, 2 * 64 * 64 * 4
+    P = ctypes.c_void_p
+
+    def fwd(q=at[0], k=at[1], v=at[2], s_in=at[3], mem=at[4], s_out=at[5]):
+        return L.polar_linear_fwd(P(q), P(k), P(v), OK, NULL, P(s_in), P(mem), P(s_out), 1, 2,
+                                  4000, 64, 1, 1.0, NULL, 0, NULL)
+    free = fwd()
+    assert free != 1                     # past validation: no device, or no workspace
+    assert fwd(s_out=at[3]) == free and fwd(mem=at[0] + n) == free and fwd(mem=at[0] - n) == free
+    for other in at[:3]:
+        assert fwd(mem=other + n - 16) == 1 and fwd(mem=other - n + 16) == 1
+        assert fwd(s_out=other + n - 16) == 1 and fwd(s_out=other - ns + 16) == 1
+    assert fwd(mem=at[3] + ns - 16) == 1 and fwd(mem=at[5]) == 1
+    assert fwd(s_out=at[3] + 16) == 1
+
+    def step(state=at[0], q=at[1], k=at[2], v=at[3], mem=at[4]):
+        return L.polar_linear_step(P(state), P(q), P(k), P(v), OK, P(mem), 1, 2, 64, 1, 1.0, NULL)
+    one = 2 * 64 * 2
+    for other in at[1:4]:
+        assert step(mem=other) == 1 and step(mem=other + one - 16) == 1
+    assert step(mem=at[0] + ns - 16) == 1 and step(q=at[0]) == 1
+
+    def bwd(dq=at[4], dk=at[5], dv=at[6], s_in=at[7], ds_out=at[8], ds=at[9]):
+        return L.polar_linear_bwd(P(at[0]), P(at[1]), P(at[2]), OK, NULL, P(s_in), P(at[3]),
+                                  P(ds_out), P(dq), P(dk), P(dv), P(ds), 1, 2, 4000, 64, 1,
+                                  1.0, NULL, 0, NULL)
+    free = bwd()
+    assert free != 1 and bwd(ds=at[8]) == free
+    for other in at[:4] + at[7:10]:
+        assert bwd(dq=other + 16) == 1 and bwd(dv=other - 16) == 1
+    assert bwd(dk=at[4] + n - 16) == 1 and bwd(ds=at[7]) == 1 and bwd(ds=at[8] + 16) == 1
+    assert bwd(ds=at[6]) == 1
+
+
 def test_linear_workspace(L):
     ws = L.polar_linear_workspace_bytes
     assert ws(1, 1, 0, 64, 1) == 0 and ws(1, 1, 10, 96, 1) == 0 and ws(-1, 1, 10, 64, 1) == 0
