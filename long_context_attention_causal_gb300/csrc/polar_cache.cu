@@ -11,7 +11,7 @@
 // lists the evicted rows below `keep` and the kept rows past it, both
 // ascending, and moves weights and positions; a second kernel copies the K
 // and V rows.  The keys stay in shared memory between the passes (up to 48K
-// rows; longer heads read them again).  The first pass sorts by exponent and
+// rows; longer heads form them again).  The first pass sorts by exponent and
 // two bits more, which spreads heavy-tailed weights over enough bins for
 // shared-memory atomics; the later ones touch one bin's rows only.
 #include <climits>
@@ -31,7 +31,8 @@ constexpr int kWRows = 1024;  // cache rows per CTA
 // One CTA per kWRows rows of a (sequence, KV head).  Every load of a thread's
 // rows is issued before the logsumexp is formed from the split records, so the
 // CTA costs about one memory latency.  Bound: HBM (4 G bytes of logits and 8
-// of weights a row).
+// of weights a row): 20 us for 32 x 4 KV heads of 32K rows, G = 4, 100 MB,
+// 5.0 TB/s.
 template <int G>
 __global__ void __launch_bounds__(kWThreads) polar_decode_weights_kernel(const WeightsArgs a) {
   __shared__ float s_lse[G];
@@ -133,43 +134,56 @@ __device__ __forceinline__ void scan_warps(SelectSmem& sm) {
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const EvictArgs a,
-                                                                        int cached) {
-  __shared__ SelectSmem sm;
-  extern __shared__ uint32_t s_keys[];
-  const int bh = blockIdx.x, b = bh / a.Hkv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int n = a.seq_lens[b];
-  if (n < 0 || n > a.max_seq_len) {
-    if (tid == 0) atomicExch(a.status, 3);
-    n = min(max(n, 0), a.max_seq_len);
-  }
-  if (n <= a.keep) {
-    if (tid == 0) {
-      a.counts[bh] = 0;
-      a.counts[gridDim.x + bh] = n;
-    }
-    return;
-  }
+// The rows that stay and the moves of one head of n > keep rows.  kFits: the
+// keys are in shared memory.  One CTA a head leaves the walks bound by issue and
+// by latency, so every walk takes kRows rows a thread at a time, all loaded
+// before the first is used, and steps whose rows lie on one side of the cut
+// count and list only what that side has: 52 -> 32 us at 128 heads of 32K rows
+// (reading weights and positions once would take 5).
+template <bool kFits>
+__device__ __forceinline__ void select_rows(const EvictArgs& a, SelectSmem& sm, uint32_t* s_keys,
+                                            int n) {
+  constexpr int kRows = 8;
+  const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   float* w = a.weights + (size_t)bh * a.stride;
   int* pos = a.positions + (size_t)bh * a.stride;
-  if (tid == 0) sm.newest = INT_MIN;
-  __syncthreads();
   int newest = INT_MIN;
-#pragma unroll 8
+#pragma unroll kRows
   for (int j = tid; j < n; j += kEThreads) newest = max(newest, pos[j]);
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (lane == 0) atomicMax(&sm.newest, newest);
   __syncthreads();
   const long long guard = (long long)sm.newest - a.recent;  // positions above stay
-  const bool fits = n <= cached;
-  auto make_key = [&](int j) -> uint32_t {
-    return pos[j] > guard ? 0xFFFFFFFFu : order_key(w[j]);
+  // keys of rows j0, j0 + step, .. below `end`; 0 past it
+  auto make_keys = [&](int j0, int step, int end, uint32_t (&key)[kRows]) {
+    int p[kRows];
+    float x[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int j = j0 + u * step;
+      p[u] = j < end ? pos[j] : INT_MIN;
+      x[u] = j < end ? w[j] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) key[u] = p[u] > guard ? 0xFFFFFFFFu : order_key(x[u]);
   };
-  auto key_of = [&](int j) -> uint32_t { return fits ? s_keys[j] : make_key(j); };
-  if (fits) {
-#pragma unroll 8
-    for (int j = tid; j < n; j += kEThreads) s_keys[j] = make_key(j);
+  auto get_keys = [&](int j0, int step, int end, uint32_t (&key)[kRows]) {
+    if constexpr (kFits) {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) key[u] = j0 + u * step < end ? s_keys[j0 + u * step] : 0u;
+    } else {
+      make_keys(j0, step, end, key);
+    }
+  };
+  constexpr int kStep = kRows * kEThreads;
+  if constexpr (kFits) {
+    for (int j0 = tid; j0 < n; j0 += kStep) {
+      uint32_t key[kRows];
+      make_keys(j0, kEThreads, n, key);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
+        if (j0 + u * kEThreads < n) s_keys[j0 + u * kEThreads] = key[u];
+    }
   }
   // key of the keep-th largest row, from the top bits down
   uint32_t prefix = 0, need = (uint32_t)a.keep;
@@ -178,11 +192,13 @@ __global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const Evi
     const int bits = pass < 2 ? 11 : 10, shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     for (int i = tid; i < kCopies * kBins; i += kEThreads) (&sm.hist[0][0])[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int j = tid; j < n; j += kEThreads) {
-      const uint32_t key = key_of(j);
-      if (pass == 0 || (key >> (shift + bits)) == prefix)
-        atomicAdd(&sm.hist[warp % kCopies][(key >> shift) & ((1u << bits) - 1u)], 1u);
+    for (int j0 = tid; j0 < n; j0 += kStep) {
+      uint32_t key[kRows];
+      get_keys(j0, kEThreads, n, key);
+#pragma unroll
+      for (int u = 0; u < kRows; ++u)
+        if (j0 + u * kEThreads < n && (pass == 0 || (key[u] >> (shift + bits)) == prefix))
+          atomicAdd(&sm.hist[warp % kCopies][(key[u] >> shift) & ((1u << bits) - 1u)], 1u);
     }
     __syncthreads();
     // bin that holds the need-th largest: two bins a thread, from the top
@@ -221,18 +237,48 @@ __global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const Evi
   // numbers follow from a scan, and with them the ranks of the rows that move.
   const int span = (n + kEThreads - 1) / kEThreads * 32;
   const int w0 = min(warp * span, n), w1 = min(w0 + span, n);
+  // all of a step's rows are the warp's, on one side of the cut
+  auto one_side = [&](int j0) {
+    return j0 + 32 * kRows <= w1 && (j0 + 32 * kRows <= a.keep || j0 >= a.keep);
+  };
   uint32_t above_lo = 0, above_hi = 0, eq_lo = 0, eq_hi = 0;
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < w1 ? key_of(j) : 0u;
-    const uint32_t lo = __ballot_sync(0xffffffffu, j < a.keep);
-    const uint32_t up = __ballot_sync(0xffffffffu, j < w1 && key > prefix);
-    const uint32_t eq = __ballot_sync(0xffffffffu, j < w1 && key == prefix);
-    above_lo += __popc(up & lo);
-    above_hi += __popc(up & ~lo);
-    eq_lo += __popc(eq & lo);
-    eq_hi += __popc(eq & ~lo);
+  for (int j0 = w0; j0 < w1; j0 += 32 * kRows) {
+    uint32_t key[kRows];
+    get_keys(j0 + lane, 32, w1, key);
+    if (one_side(j0)) {
+      uint32_t up = 0, eq = 0;
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        up += key[u] > prefix;
+        eq += key[u] == prefix;
+      }
+      if (j0 < a.keep) {
+        above_lo += up;
+        eq_lo += eq;
+      } else {
+        above_hi += up;
+        eq_hi += eq;
+      }
+      continue;
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int j = j0 + 32 * u + lane;
+      if (j >= w1) continue;
+      const bool up = key[u] > prefix, eq = key[u] == prefix;
+      if (j < a.keep) {
+        above_lo += up;
+        eq_lo += eq;
+      } else {
+        above_hi += up;
+        eq_hi += eq;
+      }
+    }
   }
+  above_lo = __reduce_add_sync(0xffffffffu, above_lo);
+  above_hi = __reduce_add_sync(0xffffffffu, above_hi);
+  eq_lo = __reduce_add_sync(0xffffffffu, eq_lo);
+  eq_hi = __reduce_add_sync(0xffffffffu, eq_hi);
   if (lane == 0) {
     sm.warp_a[warp] = eq_lo + eq_hi;
     sm.warp_b[warp] = 0;
@@ -257,41 +303,108 @@ __global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const Evi
   }
   const uint32_t below = (1u << lane) - 1u;
   int2* mv = a.moves + (size_t)bh * a.max_moves;
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < w1 ? key_of(j) : 0u;
-    const bool is_eq = j < w1 && key == prefix;
-    const uint32_t m_eq = __ballot_sync(0xffffffffu, is_eq);
-    const bool kept = j < w1 && (key > prefix || (is_eq && rank + __popc(m_eq & below) < need));
-    rank += __popc(m_eq);
-    const bool hole = j < w1 && !kept && j < a.keep, mover = kept && j >= a.keep;
-    const uint32_t m_h = __ballot_sync(0xffffffffu, hole);
-    const uint32_t m_m = __ballot_sync(0xffffffffu, mover);
-    if (hole) mv[hole_at + __popc(m_h & below)].y = j;
-    if (mover) mv[mover_at + __popc(m_m & below)].x = j;
-    hole_at += __popc(m_h);
-    mover_at += __popc(m_m);
+  // only the warp that holds the last equal row that stays ranks equal rows
+  const bool ranked = stay > 0 && stay < eq_lo + eq_hi;
+  for (int j0 = w0; j0 < w1; j0 += 32 * kRows) {
+    uint32_t key[kRows];
+    get_keys(j0 + lane, 32, w1, key);
+    if (!ranked && one_side(j0)) {
+      const bool lo = j0 < a.keep;
+      uint32_t at = lo ? hole_at : mover_at;
+      int* list = lo ? &mv->y : &mv->x;
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const bool kept = key[u] > prefix || (stay > 0 && key[u] == prefix);
+        const uint32_t m = __ballot_sync(0xffffffffu, kept != lo);
+        if (kept != lo) list[2 * (size_t)(at + __popc(m & below))] = j0 + 32 * u + lane;
+        at += __popc(m);
+      }
+      if (lo)
+        hole_at = at;
+      else
+        mover_at = at;
+      continue;
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int j = j0 + 32 * u + lane;
+      const bool is_eq = j < w1 && key[u] == prefix;
+      const uint32_t m_eq = __ballot_sync(0xffffffffu, is_eq);
+      const bool kept =
+          j < w1 && (key[u] > prefix || (is_eq && rank + __popc(m_eq & below) < need));
+      rank += __popc(m_eq);
+      const bool hole = j < w1 && !kept && j < a.keep, mover = kept && j >= a.keep;
+      const uint32_t m_h = __ballot_sync(0xffffffffu, hole);
+      const uint32_t m_m = __ballot_sync(0xffffffffu, mover);
+      if (hole) mv[hole_at + __popc(m_h & below)].y = j;
+      if (mover) mv[mover_at + __popc(m_m & below)].x = j;
+      hole_at += __popc(m_h);
+      mover_at += __popc(m_m);
+    }
   }
   __syncthreads();
   const int total = (int)sm.need;
-#pragma unroll 4
-  for (int i = tid; i < total; i += kEThreads) {
-    const int2 m = mv[i];
-    const float wv = w[m.x];
-    const int pv = pos[m.x];
-    w[m.y] = wv;
-    pos[m.y] = pv;
+  // sources lie past the cut and targets before it: all loads may go first
+  for (int i0 = tid; i0 < total; i0 += kStep) {
+    int2 m[kRows];
+    float wv[kRows];
+    int pv[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      m[u] = i0 + u * kEThreads < total ? mv[i0 + u * kEThreads] : make_int2(0, -1);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      wv[u] = w[m[u].x];
+      pv[u] = pos[m[u].x];
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (m[u].y >= 0) {
+        w[m[u].y] = wv[u];
+        pos[m[u].y] = pv[u];
+      }
   }
   __syncthreads();
   for (int j = a.keep + tid; j < n; j += kEThreads) w[j] = 0.f;
 }
 
+__global__ void __launch_bounds__(kEThreads) polar_evict_select_kernel(const EvictArgs a,
+                                                                        int cached) {
+  __shared__ SelectSmem sm;
+  extern __shared__ uint32_t s_keys[];
+  // the move kernel may be launched; it waits for this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int bh = blockIdx.x;
+  int n = a.seq_lens[bh / a.Hkv];
+  if (n < 0 || n > a.max_seq_len) {
+    if (threadIdx.x == 0) atomicExch(a.status, 3);
+    n = min(max(n, 0), a.max_seq_len);
+  }
+  if (n <= a.keep) {
+    if (threadIdx.x == 0) {
+      a.counts[bh] = 0;
+      a.counts[gridDim.x + bh] = n;
+    }
+    return;
+  }
+  if (threadIdx.x == 0) sm.newest = INT_MIN;
+  __syncthreads();
+  if (n <= cached)
+    select_rows<true>(a, sm, s_keys, n);
+  else
+    select_rows<false>(a, sm, s_keys, n);
+}
+
 // Grid (parts, B * Hkv): the listed rows of K and V, 16 bytes a thread, four
 // pieces in flight.  Sources lie past the cut and targets before it, so loads
-// may run ahead of stores.  Bound: HBM.
+// may run ahead of stores.  Bound: HBM.  128 heads of 32K rows, d = 128 bf16,
+// half of them evicted: 146 us for 777 MB of traffic, 5.3 TB/s, 78 % of the
+// copy bandwidth (single rows of 256 bytes).  Eight pieces in flight: 229 us;
+// 16 CTAs a head instead of 64: 170 us; streaming loads and stores: 150 us.
 constexpr int kMThreads = 256, kMUnroll = 4;
 __global__ void __launch_bounds__(kMThreads) polar_evict_move_kernel(const EvictArgs a) {
   const int bh = blockIdx.y, b = bh / a.Hkv, h = bh % a.Hkv;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int total = a.counts[bh], n = a.counts[gridDim.y + bh];
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = min(n, a.keep);
   const int vecs = a.row_bytes >> 4;            // 16-byte pieces of a row (a power of two)
@@ -363,8 +476,16 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const long long each = 2 * kMThreads * kMUnroll;  // pieces a CTA should have
   long long parts = (pieces + each - 1) / each;
   parts = parts < 1 ? 1 : (parts > 64 ? 64 : parts);
-  polar_evict_move_kernel<<<dim3((unsigned)parts, heads), kMThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)parts, heads);
+  cfg.blockDim = dim3(kMThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, polar_evict_move_kernel, a);
 }
 
 }  // namespace polar

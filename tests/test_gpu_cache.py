@@ -205,6 +205,21 @@ def test_evict_ties_and_odd_weights():
                 assert same_bits(got, ref), (pattern, recent, name)
 
 
+@pytest.mark.parametrize("T,keep", [(40000, 17001), (40000, 39999), (70001, 30000)])
+def test_evict_long_ties(T, keep):
+    """Many equal rows on both sides of the cut and across the warps' runs, with
+    the keys in shared memory and without."""
+    x = evict_case(1, 2, T, 64, 256, "bf16", 78)
+    g = torch.Generator().manual_seed(2)
+    x["w"][0, 0] = torch.randint(0, 3, x["w"].shape[2:], generator=g).float()
+    x["w"][0, 1] = (torch.arange(x["w"].shape[2]) // 5000).float()
+    for recent in (0, 700):
+        want = evict_expect(x, keep, recent, 256)
+        for got, ref, name in zip(run_evict(x, keep, recent, T), want,
+                                  ("k", "v", "w", "pos", "lens")):
+            assert same_bits(got, ref), (recent, name)
+
+
 def test_evict_permuted_and_equal_positions():
     """Protection goes by position, wherever the rows lie; more protected
     rows than `keep` (equal positions) still leave exactly `keep`."""
