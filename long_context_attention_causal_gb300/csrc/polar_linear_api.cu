@@ -16,19 +16,31 @@ namespace {
 
 // Runs of tiles.  Whole heads to a CTA need one launch and read every row
 // once, but leave SMs idle when heads are few.  Equal runs over all slots
-// cut heads: y and z of what lies before a cut are read a second time (about
-// 0.45 of a tile's time), and the state and scan launches cost about four
-// tiles' time.  The cheaper of the two is taken.
+// cut heads: y and z of what lies before a cut are read a second time, and a
+// state and a scan launch come first.  The cheaper of the two is taken.  In
+// tiles of an SM's time, equal runs of `even` tiles cost about 1.6 even + 5 for
+// bf16 (d = 128, whole / cut: 64 heads of 2048 tokens 55 / 65 us, 100 of 2048
+// 57 / 85, 200 of 4096 191 / 220, 160 of 8192 358 / 333, 32 of 16384 354 / 159).
+// fp32 tiles take longer than the launches do, and a second CTA on an SM adds
+// little: by runs of one CTA a SM, about 1.45 even (d = 64, whole / cut: 2
+// heads of 256 tokens 37 / 30 us, 8 of 512 66 / 42, 76 of 1024 127 / 142, 24 of
+// 2048 242 / 110).
 LinearSplit split(int BH, int T, int d, int dtype, int sms) {
   LinearSplit r;
   r.tiles = (T + kLinearTile - 1) / kLinearTile;
   const long long n = (long long)BH * r.tiles;
-  // CTAs at once: one a SM on the tensor cores; fp32 two, d / 32 to a run
-  const long long slots = dtype == POLAR_BF16 ? sms : std::max(1, 2 * sms / (d / 32));
-  const long long whole = r.tiles * ((BH + slots - 1) / slots);
-  const long long even = (n + slots - 1) / slots;
-  r.per = (int)((double)whole <= 1.45 * (double)even + 4.0 ? whole : even);
-  if (r.per < 1) r.per = 1;
+  auto whole = [&](long long slots) { return r.tiles * ((BH + slots - 1) / slots); };
+  auto even = [&](long long slots) { return (n + slots - 1) / slots; };
+  long long slots = sms;  // CTAs at once: one a SM on the tensor cores
+  bool uncut;
+  if (dtype == POLAR_BF16) {
+    uncut = whole(slots) <= 1.6 * even(slots) + 5.0;
+  } else {  // d / 32 CTAs to a run, two on a SM
+    const long long one = std::max(1, sms / (d / 32));
+    uncut = whole(one) <= 1.45 * even(one);
+    slots = std::max(1, 2 * sms / (d / 32));
+  }
+  r.per = (int)std::max(1LL, uncut ? whole(slots) : even(slots));
   r.parts = (int)((n + r.per - 1) / r.per);
   r.cut = r.per % std::max(r.tiles, 1) != 0;
   return r;
