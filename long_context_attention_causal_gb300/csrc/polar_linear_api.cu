@@ -22,9 +22,10 @@ namespace {
 // bf16 (d = 128, whole / cut: 64 heads of 2048 tokens 55 / 65 us, 100 of 2048
 // 57 / 85, 200 of 4096 191 / 220, 160 of 8192 358 / 333, 32 of 16384 354 / 159).
 // fp32 tiles take longer than the launches do, and a second CTA on an SM adds
-// little: by runs of one CTA a SM, about 1.45 even (d = 64, whole / cut: 2
-// heads of 256 tokens 37 / 30 us, 8 of 512 66 / 42, 76 of 1024 127 / 142, 24 of
-// 2048 242 / 110).
+// little: counted in runs of one CTA a SM, about 1.05 even + 0.9 (d = 64, whole
+// / cut: 2 heads of 256 tokens 37 / 30 us, 8 of 512 66 / 42, 76 of 1024 127 /
+// 142, 24 of 2048 242 / 110, 200 of 2048 833 / 665; d = 128: 20 of 512 115 /
+// 134, 40 of 2048 858 / 579, 32 of 16384 3413 / 3342).
 LinearSplit split(int BH, int T, int d, int dtype, int sms) {
   LinearSplit r;
   r.tiles = (T + kLinearTile - 1) / kLinearTile;
@@ -37,7 +38,7 @@ LinearSplit split(int BH, int T, int d, int dtype, int sms) {
     uncut = whole(slots) <= 1.6 * even(slots) + 5.0;
   } else {  // d / 32 CTAs to a run, two on a SM
     const long long one = std::max(1, sms / (d / 32));
-    uncut = whole(one) <= 1.45 * even(one);
+    uncut = whole(one) <= 1.05 * even(one) + 0.9;
     slots = std::max(1, 2 * sms / (d / 32));
   }
   r.per = (int)std::max(1LL, uncut ? whole(slots) : even(slots));
