@@ -520,7 +520,6 @@ int polar_attn_decode_paged_weights(const void* q, const void* k_pages, const vo
                       max_seq_len, dtype, c, num_splits, workspace, workspace_bytes, stream);
 }
 
-
 int polar_memory_step(float* state, const void* q, const void* k, const void* v,
                       const float* alpha, const float* beta, void* mem, int B, int H, int T,
                       int d, int dtype, float eps, void* stream) {

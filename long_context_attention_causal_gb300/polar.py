@@ -532,13 +532,14 @@ def _on_stream(f):
     """Adds the argument `stream`: the call, and what it allocates, belong to
     that stream then."""
     @functools.wraps(f)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         if stream is None:
-            return f(first, *args, **kw)
+            return f(*args, **kw)
+        first = args[0] if args else next(iter(kw.values()), None)
         if isinstance(first, torch.Tensor) and first.is_cuda and first.device != stream.device:
             raise ValueError(f"the tensors are on {first.device}, the stream on {stream.device}")
         with torch.cuda.stream(stream):
-            return f(first, *args, **kw)
+            return f(*args, **kw)
     return call
 
 

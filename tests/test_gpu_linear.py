@@ -372,6 +372,22 @@ def test_given_stream_owns_what_is_allocated():
         assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
 
 
+def test_arguments_by_name():
+    """Every argument may be given by name, the first included, with or
+    without a stream."""
+    import long_context_attention_causal_gb300 as pa
+    x = make(1, 2, 200, 64, "bf16", 3, state=True)
+    args = {n: x[n] for n in ("q", "k", "v", "log_decay", "state")}
+    want = pa.linear_fwd(*args.values(), want_state=True)
+    for stream in (None, torch.cuda.Stream()):
+        got = pa.linear_fwd(want_state=True, stream=stream, **args)
+        one = pa.linear_step(state=x["state"].clone(), log_decay=x["log_decay"], stream=stream,
+                             **{n: x[n][:, :, 0].contiguous() for n in ("q", "k", "v")})
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.isfinite(one.float()).all()
+
+
 def test_refusals():
     import long_context_attention_causal_gb300 as pa
     x = make(1, 2, 16, 64, "f32", 1)
