@@ -16,9 +16,9 @@
 //
 // fp32 tensors: dot products of 24-bit values have no exact form on the tensor
 // cores, so chunks of 64 tokens run on packed fp32 fma.  Bound: those and the
-// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 3.34
-// ms, 26 TFLOP/s, a third of the FP32 pipes' nominal rate; two CTAs a SM give
-// 1.2 times one).  Each CTA holds 32 rows of the state: a head then spreads
+// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 2.96
+// ms, 35 TFLOP/s, under half of the FP32 pipes' nominal rate; a chunk's phases
+// are short and a CTA alone on a SM waits for their latencies).  Each CTA holds 32 rows of the state: a head then spreads
 // over d / 32 CTAs, whose scores are computed as often.
 //
 // The 128-token tiles of all heads are dealt out to the CTAs in equal runs, so
@@ -107,9 +107,7 @@ __device__ __forceinline__ void state_products(float4 (&acc)[StateTile<D>::kR],
   for (int j = 0; j < kC; ++j) {
     const float4 yv = *reinterpret_cast<const float4*>(&y[j][c0]);
 #pragma unroll
-    for (int r = 0; r < S::kR; ++r) {
-      acc[r] = axpy4(zw[j][r0 + r], yv, acc[r]);
-    }
+    for (int r = 0; r < S::kR; ++r) acc[r] = axpy4(zw[j][r0 + r], yv, acc[r]);
   }
 }
 
@@ -235,11 +233,15 @@ __global__ void __launch_bounds__(256) polar_linear_copy_kernel(const float* ini
 
 // -------------------------------------------------------------- outputs --
 
+// A thread's dot products take rows 2 tx and 2 tx + 1: at tx and tx + 16 they
+// lie in different banks.
+__device__ __forceinline__ int state_slot(int r) { return (r >> 1) + (r & 1) * (kZ / 2); }
+
 template <int D>
 struct OutSmem {
   float x[kC][D + 4];
   float y[kC][D + 4];
-  float m[kZ][D + 4];  // rows z0 .. of the state
+  float m[kZ][D + 4];  // rows z0 .. of the state, row r at state_slot(r)
   float z[kC][kZ];
   float zw[kC][kZ];
   float p[kC][kC + 4];  // decayed scores
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int r = a.state_t ? i % kZ : i / D, c = a.state_t ? i / kZ : i % D;
       float v = 0.f;
       if (st) v = a.state_t ? st[(size_t)c * D + z0 + r] : st[(size_t)(z0 + r) * D + c];
-      sm.m[r][c] = v;
+      sm.m[state_slot(r)][c] = v;
     }
     for (int i = tid; i <= kC; i += kThreads) sm.pw[i] = linear_power(l2, i);
     // forward: the output scale applies to the state's part too; reverse: the
@@ -307,6 +309,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       px.store(sm.x);
       py.store(sm.y);
       pz.store(sm.z);
+#pragma unroll
+      for (int u = 0; u < Pieces<kZ>::kN; ++u) {
+        const int r = (tid + u * kThreads) / Pieces<kZ>::kV;
+        const float w = r < n ? s_z * sm.pw[a.reverse ? r + 1 : n - 1 - r] : 0.f;
+        float4& v = pz.v[u];
+        v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
+      }
+      pz.store(sm.zw);
       if (ci + 1 < n_ch) fetch(chunk(ci + 1));
       __syncthreads();
       const float2 zero = make_float2(0.f, 0.f);
@@ -342,11 +352,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int dist = a.reverse ? j - i : i - j;
             sm.p[i][j] = dist >= 0 ? (sc[ii][jj].x + sc[ii][jj].y) * sm.pw[dist] : 0.f;
           }
-        for (int i = tid; i < kC * kZ; i += kThreads) {
-          const int r = i / kZ;
-          const float w = r < n ? s_z * sm.pw[a.reverse ? r + 1 : n - 1 - r] : 0.f;
-          sm.zw[r][i % kZ] = sm.z[r][i % kZ] * w;
-        }
         __syncthreads();
         // the state's part: rows 4 ty .., state rows 2 tx, 2 tx + 1
         float2 m[4][2], q[4][2];
@@ -354,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int ii = 0; ii < 4; ++ii) m[ii][0] = m[ii][1] = q[ii][0] = q[ii][1] = zero;
 #pragma unroll 2
         for (int k = 0; k < D; k += 4) {
-          const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[2 * tx][k]);
-          const float4 m1 = *reinterpret_cast<const float4*>(&sm.m[2 * tx + 1][k]);
+          const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[tx][k]);
+          const float4 m1 = *reinterpret_cast<const float4*>(&sm.m[tx + kZ / 2][k]);
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {
             const float4 xv = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
@@ -401,19 +406,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float g = sm.pw[n];
 #pragma unroll
         for (int r = 0; r < S::kR; ++r) {
-          const float4 v = *reinterpret_cast<const float4*>(&sm.m[S::row0() + r][S::col0()]);
+          const float4 v =
+              *reinterpret_cast<const float4*>(&sm.m[state_slot(S::row0() + r)][S::col0()]);
           acc[r] = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
         }
         state_products<D>(acc, sm.y, sm.zw);
 #pragma unroll
         for (int r = 0; r < S::kR; ++r)
-          *reinterpret_cast<float4*>(&sm.m[S::row0() + r][S::col0()]) = acc[r];
+          *reinterpret_cast<float4*>(&sm.m[state_slot(S::row0() + r)][S::col0()]) = acc[r];
       }
     }
     if (fin) {
       __syncthreads();
       for (int i = tid; i < kZ * D; i += kThreads)
-        fin[(size_t)(z0 + i / D) * D + i % D] = sm.m[i / D][i % D];
+        fin[(size_t)(z0 + i / D) * D + i % D] = sm.m[state_slot(i / D)][i % D];
     }
   }
 }

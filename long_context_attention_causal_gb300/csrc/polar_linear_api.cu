@@ -23,9 +23,9 @@ namespace {
 // 57 / 85, 200 of 4096 191 / 220, 160 of 8192 358 / 333, 32 of 16384 354 / 159).
 // fp32 tiles take longer than the launches do, and a second CTA on an SM adds
 // little: counted in runs of one CTA a SM, about 1.05 even + 0.9 (d = 64, whole
-// / cut: 2 heads of 256 tokens 37 / 30 us, 8 of 512 66 / 42, 76 of 1024 127 /
-// 142, 24 of 2048 242 / 110, 200 of 2048 833 / 665; d = 128: 20 of 512 115 /
-// 134, 40 of 2048 858 / 579, 32 of 16384 3413 / 3342).
+// / cut: 2 heads of 256 tokens 33 / 28 us, 8 of 512 59 / 38, 76 of 1024 115 /
+// 132, 24 of 2048 219 / 101, 200 of 2048 756 / 613; d = 128: 20 of 512 100 /
+// 120, 40 of 2048 748 / 515, 32 of 16384 2970 / 2960).
 LinearSplit split(int BH, int T, int d, int dtype, int sms) {
   LinearSplit r;
   r.tiles = (T + kLinearTile - 1) / kLinearTile;
