@@ -16,15 +16,17 @@
 //
 // fp32 tensors: dot products of 24-bit values have no exact form on the tensor
 // cores, so chunks of 64 tokens run on packed fp32 fma.  Bound: those and the
-// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 2.96
-// ms, 35 TFLOP/s, under half of the FP32 pipes' nominal rate; a chunk's phases
-// are short and a CTA alone on a SM waits for their latencies).  Each CTA holds 32 rows of the state: a head then spreads
+// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 2.30
+// ms, 32 TFLOP/s without the masked products, 43 % of the FP32 pipes' nominal
+// rate).  Each CTA holds 32 rows of the state: a head then spreads
 // over d / 32 CTAs, whose scores are computed as often.
 //
 // The 128-token tiles of all heads are dealt out to the CTAs in equal runs, so
 // that few heads still fill the GPU.  A head that a run boundary cuts needs
 // its state there first: one kernel sums each run's own part of the cut head,
 // a scan joins the parts, and the output kernel walks all runs in parallel.
+#include <type_traits>
+
 #include "polar_device.cuh"
 #include "polar_internal.h"
 #include "polar_linear.cuh"
@@ -249,9 +251,14 @@ struct OutSmem {
 };
 
 // Grid (parts, D / kZ): the CTA walks its run's chunks with its 32 rows of the
-// state in shared memory.
+// state in shared memory.  Scores, the state's part and the chunk's own part
+// of a row stay in one warp, so a chunk has two barriers; scores and products
+// that the mask makes zero are not computed.  d = 64 runs two CTAs a SM (one:
+// 392 us against 364 at 64 heads of 4096 tokens); d = 128 needs 246 registers
+// to keep its products apart and runs one (two, spilling: 818 against 589 at
+// 32 heads of 4096).
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
     polar_linear_out_kernel(const OutBatch batch) {
   const LinearArgs& a = batch.a[blockIdx.z];
   linear_let_next_start();
@@ -261,7 +268,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   OutSmem<D>& sm = *reinterpret_cast<OutSmem<D>*>(smem_raw);
   const int BH = a.B * a.H, part = blockIdx.x;
   const int z0 = blockIdx.y * kZ, tid = threadIdx.x;
-  const int tx = tid & 15, ty = tid >> 4;
+  // Rows 8 group .. of a chunk to a warp, which computes scores and products
+  // only where they can be non-zero: the warps of one scheduler (w and w + 4)
+  // get groups whose shares add up to the same.
+  const int warp = tid >> 5, group = warp < 4 ? warp : 11 - warp;
+  const int tx = tid & 15, ty = 2 * group + ((tid >> 4) & 1);
   const int n_po = linear_portions(a.split, BH, part);
   for (int ip = 0; ip < n_po; ++ip) {
     const LinearPortion po = linear_portion(a.split, BH, a.H, a.T, a.lengths, a.status, part,
@@ -302,10 +313,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       pz.load(z + z0, D, c0, end);
     };
     fetch(chunk(0));
+    __syncthreads();  // the powers are there
     for (int ci = 0; ci < n_ch; ++ci) {
       const int c0 = chunk(ci);
       const int n = min(max(end - c0, 0), kC);  // tokens of the chunk
-      __syncthreads();
+      // every read of the last chunk is done: its state's update waited for them
       px.store(sm.x);
       py.store(sm.y);
       pz.store(sm.z);
@@ -317,47 +329,58 @@ __global__ void __launch_bounds__(kThreads, 2)
         v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
       }
       pz.store(sm.zw);
-      if (ci + 1 < n_ch) fetch(chunk(ci + 1));
       __syncthreads();
       const float2 zero = make_float2(0.f, 0.f);
       float o[4][2];
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) o[ii][0] = o[ii][1] = 0.f;
       if (n > 0) {
-        // scores: rows 4 ty .., keys tx + 16 jj
-        float2 sc[4][4];
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = zero;
-#pragma unroll 2
-        for (int k = 0; k < D; k += 4) {
-          float4 xv[4], yv[4];
-#pragma unroll
-          for (int ii = 0; ii < 4; ++ii)
-            xv[ii] = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
-#pragma unroll
-          for (int jj = 0; jj < 4; ++jj)
-            yv[jj] = *reinterpret_cast<const float4*>(&sm.y[tx + 16 * jj][k]);
+        // scores: rows 4 ty .., keys tx + 16 jj of the blocks that the
+        // warp's rows can see
+        auto scores = [&](auto blocks, int jj0) {
+          constexpr int kB = decltype(blocks)::value;
+          float2 sc[4][kB];
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) sc[ii][jj] = dot4(xv[ii], yv[jj], sc[ii][jj]);
-        }
+            for (int jj = 0; jj < kB; ++jj) sc[ii][jj] = zero;
+#pragma unroll(D / 32)
+          for (int k = 0; k < D; k += 4) {
+            float4 xv[4], yv[kB];
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
+            for (int ii = 0; ii < 4; ++ii)
+              xv[ii] = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj) {
-            const int i = 4 * ty + ii, j = tx + 16 * jj;
-            const int dist = a.reverse ? j - i : i - j;
-            sm.p[i][j] = dist >= 0 ? (sc[ii][jj].x + sc[ii][jj].y) * sm.pw[dist] : 0.f;
+            for (int jj = 0; jj < kB; ++jj)
+              yv[jj] = *reinterpret_cast<const float4*>(&sm.y[tx + 16 * (jj0 + jj)][k]);
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+              for (int jj = 0; jj < kB; ++jj) sc[ii][jj] = dot4(xv[ii], yv[jj], sc[ii][jj]);
           }
-        __syncthreads();
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+            for (int jj = 0; jj < kB; ++jj) {
+              const int i = 4 * ty + ii, j = tx + 16 * (jj0 + jj);
+              const int dist = a.reverse ? j - i : i - j;
+              sm.p[i][j] = dist >= 0 ? (sc[ii][jj].x + sc[ii][jj].y) * sm.pw[dist] : 0.f;
+            }
+        };
+        const int half = group / 2;  // 16 rows
+        const int jj0 = a.reverse ? half : 0;
+        switch (a.reverse ? 4 - half : half + 1) {
+          case 1: scores(std::integral_constant<int, 1>{}, jj0); break;
+          case 2: scores(std::integral_constant<int, 2>{}, jj0); break;
+          case 3: scores(std::integral_constant<int, 3>{}, jj0); break;
+          default: scores(std::integral_constant<int, 4>{}, jj0); break;
+        }
+        __syncwarp();  // a warp reads its own rows of p only
         // the state's part: rows 4 ty .., state rows 2 tx, 2 tx + 1
         float2 m[4][2], q[4][2];
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) m[ii][0] = m[ii][1] = q[ii][0] = q[ii][1] = zero;
-#pragma unroll 2
+#pragma unroll(D / 32)
         for (int k = 0; k < D; k += 4) {
           const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[tx][k]);
           const float4 m1 = *reinterpret_cast<const float4*>(&sm.m[tx + kZ / 2][k]);
@@ -369,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         // the chunk's own part
+        const int j_lo = a.reverse ? 8 * group : 0, j_hi = a.reverse ? kC : 8 * group + 8;
 #pragma unroll 2
-        for (int j = 0; j < kC; j += 4) {
+        for (int j = j_lo; j < j_hi; j += 4) {
           float2 zv[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -400,10 +424,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           *reinterpret_cast<float2*>(out + (size_t)(c0 + i) * D + z0 + 2 * tx) =
               make_float2(i < n ? o[ii][0] : 0.f, i < n ? o[ii][1] : 0.f);
       }
+      // on their way while the state is updated: earlier they would hold
+      // registers that the products need
+      if (ci + 1 < n_ch) fetch(chunk(ci + 1));
       if (n > 0 && (ci + 1 < n_ch || fin)) {
-        __syncthreads();  // every read of the state is done
-        float4 acc[S::kR];
         const float g = sm.pw[n];
+        float4 acc[S::kR];
 #pragma unroll
         for (int r = 0; r < S::kR; ++r) {
           const float4 v =
@@ -411,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           acc[r] = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
         }
         state_products<D>(acc, sm.y, sm.zw);
+        __syncthreads();  // every read of the state and the chunk is done
 #pragma unroll
         for (int r = 0; r < S::kR; ++r)
           *reinterpret_cast<float4*>(&sm.m[state_slot(S::row0() + r)][S::col0()]) = acc[r];

@@ -23,9 +23,9 @@ namespace {
 // 57 / 85, 200 of 4096 191 / 220, 160 of 8192 358 / 333, 32 of 16384 354 / 159).
 // fp32 tiles take longer than the launches do, and a second CTA on an SM adds
 // little: counted in runs of one CTA a SM, about 1.05 even + 0.9 (d = 64, whole
-// / cut: 2 heads of 256 tokens 33 / 28 us, 8 of 512 59 / 38, 76 of 1024 115 /
-// 132, 24 of 2048 219 / 101, 200 of 2048 756 / 613; d = 128: 20 of 512 100 /
-// 120, 40 of 2048 748 / 515, 32 of 16384 2970 / 2960).
+// / cut: 2 heads of 256 tokens 29 / 26 us, 8 of 512 49 / 34, 76 of 1024 94 /
+// 114, 24 of 2048 180 / 89, 200 of 2048 614 / 515; d = 128: 20 of 512 74 / 79,
+// 40 of 2048 530 / 368, 32 of 16384 2094 / 2297, backward 6247 / 6140).
 LinearSplit split(int BH, int T, int d, int dtype, int sms) {
   LinearSplit r;
   r.tiles = (T + kLinearTile - 1) / kLinearTile;
@@ -36,10 +36,10 @@ LinearSplit split(int BH, int T, int d, int dtype, int sms) {
   bool uncut;
   if (dtype == POLAR_BF16) {
     uncut = whole(slots) <= 1.6 * even(slots) + 5.0;
-  } else {  // d / 32 CTAs to a run, two on a SM
+  } else {  // d / 32 CTAs to a run, two on a SM at d = 64, one at d = 128
     const long long one = std::max(1, sms / (d / 32));
     uncut = whole(one) <= 1.05 * even(one) + 0.9;
-    slots = std::max(1, 2 * sms / (d / 32));
+    slots = d == 64 ? sms : one;
   }
   r.per = (int)std::max(1LL, uncut ? whole(slots) : even(slots));
   r.parts = (int)((n + r.per - 1) / r.per);
