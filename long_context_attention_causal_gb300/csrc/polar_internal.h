@@ -81,6 +81,7 @@ struct LinearSplit {
   int tiles;  // of one head
   int per, parts;
   bool cut;   // some boundary lies inside a head
+  int sms;
 };
 
 // One application of the recurrence over all (b, h):

@@ -16,10 +16,10 @@
 //
 // fp32 tensors: dot products of 24-bit values have no exact form on the tensor
 // cores, so chunks of 64 tokens run on packed fp32 fma.  Bound: those and the
-// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 2.30
-// ms, 32 TFLOP/s without the masked products, 43 % of the FP32 pipes' nominal
-// rate).  Each CTA holds 32 rows of the state: a head then spreads
-// over d / 32 CTAs, whose scores are computed as often.
+// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 1.63
+// ms, 38 TFLOP/s without the masked products, half of the FP32 pipes' nominal
+// rate).  Each CTA holds 64 or 32 rows of the state: a head then spreads
+// over as many CTAs, whose scores are computed as often.
 //
 // The 128-token tiles of all heads are dealt out to the CTAs in equal runs, so
 // that few heads still fill the GPU.  A head that a run boundary cuts needs
@@ -36,7 +36,7 @@ namespace polar {
 namespace {
 
 constexpr int kC = 64;        // tokens per chunk
-constexpr int kZ = 32;        // z columns (rows of the state) per CTA
+constexpr int kZ = 32;        // z columns (rows of the state) per CTA, cut states
 constexpr int kThreads = 256;
 
 template <typename T>
@@ -90,20 +90,20 @@ struct Pieces {
   }
 };
 
-// The thread's share of a 32 x D state: rows r0 .. r0 + kR - 1, four columns.
-template <int D>
+// The thread's share of a Z x D state: rows r0 .. r0 + kR - 1, four columns.
+template <int D, int Z>
 struct StateTile {
   static constexpr int kLanes = D / 4;
-  static constexpr int kR = kZ * kLanes / kThreads;
+  static constexpr int kR = Z * kLanes / kThreads;
   static __device__ __forceinline__ int row0() { return (int)(threadIdx.x / kLanes) * kR; }
   static __device__ __forceinline__ int col0() { return (int)(threadIdx.x % kLanes) * 4; }
 };
 
 // acc += sum_j w_j z_j y_j^T over the rows of a chunk (zw holds w_j z_j).
-template <int D>
-__device__ __forceinline__ void state_products(float4 (&acc)[StateTile<D>::kR],
-                                               const float (*y)[D + 4], const float (*zw)[kZ]) {
-  using S = StateTile<D>;
+template <int D, int Z>
+__device__ __forceinline__ void state_products(float4 (&acc)[StateTile<D, Z>::kR],
+                                               const float (*y)[D + 4], const float (*zw)[Z]) {
+  using S = StateTile<D, Z>;
   const int r0 = S::row0(), c0 = S::col0();
 #pragma unroll 4
   for (int j = 0; j < kC; ++j) {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads)
     polar_linear_state_kernel(const StateBatch batch) {
   const LinearStateArgs& a = batch.a[blockIdx.z];
   linear_let_next_start();
-  using S = StateTile<D>;
+  using S = StateTile<D, kZ>;
   __shared__ __align__(16) StateSmem<D> sm;
   const int BH = a.B * a.H, part = blockIdx.x, z0 = blockIdx.y * kZ;
   const int i = a.reverse ? 0 : linear_portions(a.split, BH, part) - 1;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads)
     py.load(y, D, c0 + kC, t1);
     pz.load(z + z0, D, c0 + kC, t1);
     __syncthreads();
-    state_products<D>(acc, sm.y, sm.zw);
+    state_products<D, kZ>(acc, sm.y, sm.zw);
   }
   float* dst = a.cuts + ((size_t)part * D + z0) * D;
 #pragma unroll
@@ -235,39 +235,43 @@ __global__ void __launch_bounds__(256) polar_linear_copy_kernel(const float* ini
 
 // -------------------------------------------------------------- outputs --
 
-// A thread's dot products take rows 2 tx and 2 tx + 1: at tx and tx + 16 they
-// lie in different banks.
-__device__ __forceinline__ int state_slot(int r) { return (r >> 1) + (r & 1) * (kZ / 2); }
+// A thread's dot products take the kE state rows from kE tx on: at tx, tx + 16
+// .. they lie in different banks.
+template <int Z>
+__device__ __forceinline__ int state_slot(int r) {
+  constexpr int kE = Z / 16;
+  return r / kE + r % kE * 16;
+}
 
-template <int D>
+template <int D, int Z>
 struct OutSmem {
   float x[kC][D + 4];
   float y[kC][D + 4];
-  float m[kZ][D + 4];  // rows z0 .. of the state, row r at state_slot(r)
-  float z[kC][kZ];
-  float zw[kC][kZ];
+  float m[Z][D + 4];  // rows z0 .. of the state, row r at state_slot(r)
+  float z[kC][Z];
+  float zw[kC][Z];
   float p[kC][kC + 4];  // decayed scores
   float pw[kC + 1];     // powers of g
 };
 
-// Grid (parts, D / kZ): the CTA walks its run's chunks with its 32 rows of the
+// Grid (parts, D / Z): the CTA walks its run's chunks with its rows of the
 // state in shared memory.  Scores, the state's part and the chunk's own part
 // of a row stay in one warp, so a chunk has two barriers; scores and products
-// that the mask makes zero are not computed.  d = 64 runs two CTAs a SM (one:
-// 392 us against 364 at 64 heads of 4096 tokens); d = 128 needs 246 registers
-// to keep its products apart and runs one (two, spilling: 818 against 589 at
-// 32 heads of 4096).
-template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
+// that the mask makes zero are not computed.  One CTA a SM: with the 247
+// registers that this leaves, the products of a step stay apart (two CTAs,
+// spilling: 818 us against 589 at 32 heads of 4096 tokens, d = 128, 32 rows).
+template <int D, int Z>
+__global__ void __launch_bounds__(kThreads, 1)
     polar_linear_out_kernel(const OutBatch batch) {
   const LinearArgs& a = batch.a[blockIdx.z];
   linear_let_next_start();
   linear_wait_previous();
-  using S = StateTile<D>;
+  constexpr int kE = Z / 16;
+  using S = StateTile<D, Z>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  OutSmem<D>& sm = *reinterpret_cast<OutSmem<D>*>(smem_raw);
+  OutSmem<D, Z>& sm = *reinterpret_cast<OutSmem<D, Z>*>(smem_raw);
   const int BH = a.B * a.H, part = blockIdx.x;
-  const int z0 = blockIdx.y * kZ, tid = threadIdx.x;
+  const int z0 = blockIdx.y * Z, tid = threadIdx.x;
   // Rows 8 group .. of a chunk to a warp, which computes scores and products
   // only where they can be non-zero: the warps of one scheduler (w and w + 4)
   // get groups whose shares add up to the same.
@@ -292,11 +296,11 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
                           ? a.cuts + (size_t)(a.reverse ? part + 1 : part - 1) * D * D
                           : (a.init ? a.init + (size_t)bh * D * D : nullptr);
     __syncthreads();  // the last portion's reads are done
-    for (int i = tid; i < kZ * D; i += kThreads) {
-      const int r = a.state_t ? i % kZ : i / D, c = a.state_t ? i / kZ : i % D;
+    for (int i = tid; i < Z * D; i += kThreads) {
+      const int r = a.state_t ? i % Z : i / D, c = a.state_t ? i / Z : i % D;
       float v = 0.f;
       if (st) v = a.state_t ? st[(size_t)c * D + z0 + r] : st[(size_t)(z0 + r) * D + c];
-      sm.m[state_slot(r)][c] = v;
+      sm.m[state_slot<Z>(r)][c] = v;
     }
     for (int i = tid; i <= kC; i += kThreads) sm.pw[i] = linear_power(l2, i);
     // forward: the output scale applies to the state's part too; reverse: the
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
     const int end = min(len, t1);
     auto chunk = [&](int ci) { return t0 + (a.reverse ? n_ch - 1 - ci : ci) * kC; };
     Pieces<D> px, py;
-    Pieces<kZ> pz;
+    Pieces<Z> pz;
     auto fetch = [&](int c0) {
       px.load(x, D, c0, end);
       py.load(y, D, c0, end);
@@ -322,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
       py.store(sm.y);
       pz.store(sm.z);
 #pragma unroll
-      for (int u = 0; u < Pieces<kZ>::kN; ++u) {
-        const int r = (tid + u * kThreads) / Pieces<kZ>::kV;
+      for (int u = 0; u < Pieces<Z>::kN; ++u) {
+        const int r = (tid + u * kThreads) / Pieces<Z>::kV;
         const float w = r < n ? s_z * sm.pw[a.reverse ? r + 1 : n - 1 - r] : 0.f;
         float4& v = pz.v[u];
         v = make_float4(v.x * w, v.y * w, v.z * w, v.w * w);
@@ -331,9 +335,11 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
       pz.store(sm.zw);
       __syncthreads();
       const float2 zero = make_float2(0.f, 0.f);
-      float o[4][2];
+      float o[4][kE];
 #pragma unroll
-      for (int ii = 0; ii < 4; ++ii) o[ii][0] = o[ii][1] = 0.f;
+      for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[ii][e] = 0.f;
       if (n > 0) {
         // scores: rows 4 ty .., keys tx + 16 jj of the blocks that the
         // warp's rows can see
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
           for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
             for (int jj = 0; jj < kB; ++jj) sc[ii][jj] = zero;
-#pragma unroll(D / 32)
+#pragma unroll 4
           for (int k = 0; k < D; k += 4) {
             float4 xv[4], yv[kB];
 #pragma unroll
@@ -376,53 +382,67 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
           default: scores(std::integral_constant<int, 4>{}, jj0); break;
         }
         __syncwarp();  // a warp reads its own rows of p only
-        // the state's part: rows 4 ty .., state rows 2 tx, 2 tx + 1
-        float2 m[4][2], q[4][2];
+        // the state's part: rows 4 ty .., state rows kE tx ..
+        float2 m[4][kE], q[4][kE];
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii) m[ii][0] = m[ii][1] = q[ii][0] = q[ii][1] = zero;
-#pragma unroll(D / 32)
+        for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) m[ii][e] = q[ii][e] = zero;
+#pragma unroll 4
         for (int k = 0; k < D; k += 4) {
-          const float4 m0 = *reinterpret_cast<const float4*>(&sm.m[tx][k]);
-          const float4 m1 = *reinterpret_cast<const float4*>(&sm.m[tx + kZ / 2][k]);
+          float4 mv[kE];
+#pragma unroll
+          for (int e = 0; e < kE; ++e) mv[e] = *reinterpret_cast<const float4*>(&sm.m[tx + 16 * e][k]);
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {
             const float4 xv = *reinterpret_cast<const float4*>(&sm.x[4 * ty + ii][k]);
-            m[ii][0] = dot4(xv, m0, m[ii][0]);
-            m[ii][1] = dot4(xv, m1, m[ii][1]);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) m[ii][e] = dot4(xv, mv[e], m[ii][e]);
           }
         }
-        // the chunk's own part
+        // the chunk's own part, two columns at once: q[e] of columns 2 (e / 2)
+        // and the next, odd and even j apart
         const int j_lo = a.reverse ? 8 * group : 0, j_hi = a.reverse ? kC : 8 * group + 8;
 #pragma unroll 2
         for (int j = j_lo; j < j_hi; j += 4) {
-          float2 zv[4];
+          float2 zv[4][kE / 2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            zv[e] = *reinterpret_cast<const float2*>(&sm.z[j + e][2 * tx]);
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int c = 0; c < kE / 2; ++c)
+              zv[u][c] = *reinterpret_cast<const float2*>(&sm.z[j + u][kE * tx + 2 * c]);
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {
             const float4 pv = *reinterpret_cast<const float4*>(&sm.p[4 * ty + ii][j]);
-            // both columns at once
-            q[ii][0] = ffma2(make_float2(pv.x, pv.x), zv[0], q[ii][0]);
-            q[ii][1] = ffma2(make_float2(pv.y, pv.y), zv[1], q[ii][1]);
-            q[ii][0] = ffma2(make_float2(pv.z, pv.z), zv[2], q[ii][0]);
-            q[ii][1] = ffma2(make_float2(pv.w, pv.w), zv[3], q[ii][1]);
+#pragma unroll
+            for (int c = 0; c < kE / 2; ++c) {
+              q[ii][2 * c] = ffma2(make_float2(pv.x, pv.x), zv[0][c], q[ii][2 * c]);
+              q[ii][2 * c + 1] = ffma2(make_float2(pv.y, pv.y), zv[1][c], q[ii][2 * c + 1]);
+              q[ii][2 * c] = ffma2(make_float2(pv.z, pv.z), zv[2][c], q[ii][2 * c]);
+              q[ii][2 * c + 1] = ffma2(make_float2(pv.w, pv.w), zv[3][c], q[ii][2 * c + 1]);
+            }
           }
         }
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
           const int i = 4 * ty + ii;
           const float w = i < n ? s_in * sm.pw[a.reverse ? n - 1 - i : i + 1] : 0.f;
-          o[ii][0] = fmaf(a.scale, q[ii][0].x + q[ii][1].x, w * (m[ii][0].x + m[ii][0].y));
-          o[ii][1] = fmaf(a.scale, q[ii][0].y + q[ii][1].y, w * (m[ii][1].x + m[ii][1].y));
+#pragma unroll
+          for (int c = 0; c < kE; c += 2) {
+            o[ii][c] = fmaf(a.scale, q[ii][c].x + q[ii][c + 1].x, w * (m[ii][c].x + m[ii][c].y));
+            o[ii][c + 1] =
+                fmaf(a.scale, q[ii][c].y + q[ii][c + 1].y, w * (m[ii][c + 1].x + m[ii][c + 1].y));
+          }
         }
       }
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
         const int i = 4 * ty + ii;
         if (c0 + i < t1)
-          *reinterpret_cast<float2*>(out + (size_t)(c0 + i) * D + z0 + 2 * tx) =
-              make_float2(i < n ? o[ii][0] : 0.f, i < n ? o[ii][1] : 0.f);
+#pragma unroll
+          for (int c = 0; c < kE; c += 2)
+            *reinterpret_cast<float2*>(out + (size_t)(c0 + i) * D + z0 + kE * tx + c) =
+                make_float2(i < n ? o[ii][c] : 0.f, i < n ? o[ii][c + 1] : 0.f);
       }
       // on their way while the state is updated: earlier they would hold
       // registers that the products need
@@ -433,20 +453,20 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 2 : 1)
 #pragma unroll
         for (int r = 0; r < S::kR; ++r) {
           const float4 v =
-              *reinterpret_cast<const float4*>(&sm.m[state_slot(S::row0() + r)][S::col0()]);
+              *reinterpret_cast<const float4*>(&sm.m[state_slot<Z>(S::row0() + r)][S::col0()]);
           acc[r] = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
         }
-        state_products<D>(acc, sm.y, sm.zw);
+        state_products<D, Z>(acc, sm.y, sm.zw);
         __syncthreads();  // every read of the state and the chunk is done
 #pragma unroll
         for (int r = 0; r < S::kR; ++r)
-          *reinterpret_cast<float4*>(&sm.m[state_slot(S::row0() + r)][S::col0()]) = acc[r];
+          *reinterpret_cast<float4*>(&sm.m[state_slot<Z>(S::row0() + r)][S::col0()]) = acc[r];
       }
     }
     if (fin) {
       __syncthreads();
-      for (int i = tid; i < kZ * D; i += kThreads)
-        fin[(size_t)(z0 + i / D) * D + i % D] = sm.m[state_slot(i / D)][i % D];
+      for (int i = tid; i < Z * D; i += kThreads)
+        fin[(size_t)(z0 + i / D) * D + i % D] = sm.m[state_slot<Z>(i / D)][i % D];
     }
   }
 }
@@ -508,15 +528,27 @@ cudaError_t states_d(const StateBatch& batch, int n, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t out_d(const OutBatch& batch, int n, cudaStream_t s) {
-  const int smem = (int)sizeof(OutSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D>,
+template <int D, int Z>
+cudaError_t out_dz(const OutBatch& batch, int n, cudaStream_t s) {
+  const int smem = (int)sizeof(OutSmem<D, Z>);
+  cudaError_t e = cudaFuncSetAttribute(polar_linear_out_kernel<D, Z>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return linear_launch(polar_linear_out_kernel<D>,
-                       dim3((unsigned)batch.a[0].split.parts, D / kZ, n), kThreads, smem, s,
+  return linear_launch(polar_linear_out_kernel<D, Z>,
+                       dim3((unsigned)batch.a[0].split.parts, D / Z, n), kThreads, smem, s,
                        batch.a[0].chained, batch);
+}
+
+// 64 state rows a CTA, so that fewer CTAs compute the same scores (290 us
+// against 392 with 32 at 64 heads of 4096 tokens, d = 64; 439 against 589 at 32
+// heads, d = 128), unless 32 rows a CTA find an SM each: a chunk then takes less
+// time (2 heads of 100 tokens, d = 64, 16 us against 20; 8 of 300, d = 128, 34
+// against 42).
+template <int D>
+cudaError_t out_d(const OutBatch& batch, int n, cudaStream_t s) {
+  const LinearSplit& g = batch.a[0].split;
+  return (long long)g.parts * (D / 32) * n <= g.sms ? out_dz<D, 32>(batch, n, s)
+                                                    : out_dz<D, 64>(batch, n, s);
 }
 
 StateBatch state_batch(const LinearStateArgs* a, int n) {

@@ -21,28 +21,25 @@ namespace {
 // tiles of an SM's time, equal runs of `even` tiles cost about 1.6 even + 5 for
 // bf16 (d = 128, whole / cut: 64 heads of 2048 tokens 55 / 65 us, 100 of 2048
 // 57 / 85, 200 of 4096 191 / 220, 160 of 8192 358 / 333, 32 of 16384 354 / 159).
-// fp32 tiles take longer than the launches do, and a second CTA on an SM adds
-// little: counted in runs of one CTA a SM, about 1.05 even + 0.9 (d = 64, whole
-// / cut: 2 heads of 256 tokens 29 / 26 us, 8 of 512 49 / 34, 76 of 1024 94 /
-// 114, 24 of 2048 180 / 89, 200 of 2048 614 / 515; d = 128: 20 of 512 74 / 79,
-// 40 of 2048 530 / 368, 32 of 16384 2094 / 2297, backward 6247 / 6140).
-LinearSplit split(int BH, int T, int d, int dtype, int sms) {
+// fp32 tiles take longer than the launches do: about 1.05 even + 0.9 (d = 64,
+// whole / cut: 2 heads of 256 tokens 29 / 26 us, 8 of 512 47 / 26, 76 of 1024 90
+// / 95, 24 of 2048 172 / 75, 64 of 4096 338 / 290, 200 of 2048 444 / 400; d =
+// 128: 20 of 512 74 / 79, 40 of 2048 363 / 290).  The backward's three outputs
+// share a launch there, so whole heads fill the SMs sooner (200 heads of 2048,
+// d = 64, 874 / 1031; 20 of 512, d = 128, 94 / 124).
+LinearSplit split(int BH, int T, int d, int dtype, int sms, bool backward) {
   LinearSplit r;
+  r.sms = sms;
   r.tiles = (T + kLinearTile - 1) / kLinearTile;
-  const long long n = (long long)BH * r.tiles;
-  auto whole = [&](long long slots) { return r.tiles * ((BH + slots - 1) / slots); };
-  auto even = [&](long long slots) { return (n + slots - 1) / slots; };
-  long long slots = sms;  // CTAs at once: one a SM on the tensor cores
-  bool uncut;
-  if (dtype == POLAR_BF16) {
-    uncut = whole(slots) <= 1.6 * even(slots) + 5.0;
-  } else {  // d / 32 CTAs to a run, two on a SM at d = 64, one at d = 128
-    const long long one = std::max(1, sms / (d / 32));
-    uncut = whole(one) <= 1.05 * even(one) + 0.9;
-    slots = d == 64 ? sms : one;
-  }
-  r.per = (int)std::max(1LL, uncut ? whole(slots) : even(slots));
-  r.parts = (int)((n + r.per - 1) / r.per);
+  // CTAs at once: one a SM, in fp32 d / 64 to a run
+  const long long slots = dtype == POLAR_BF16 ? sms : std::max(1, sms / (d / 64));
+  auto whole = [&](long long heads) { return r.tiles * ((heads + slots - 1) / slots); };
+  auto even = [&](long long heads) { return (heads * r.tiles + slots - 1) / slots; };
+  const long long heads = dtype == POLAR_F32 && backward ? 3LL * BH : BH;
+  const bool uncut = dtype == POLAR_BF16 ? whole(heads) <= 1.6 * even(heads) + 5.0
+                                         : whole(heads) <= 1.05 * even(heads) + 0.9;
+  r.per = (int)std::max(1LL, uncut ? whole(BH) : even(BH));
+  r.parts = (int)(((long long)BH * r.tiles + r.per - 1) / r.per);
   r.cut = r.per % std::max(r.tiles, 1) != 0;
   return r;
 }
@@ -100,10 +97,10 @@ size_t cut_bytes(const LinearSplit& g, int BH, int d) {
   return g.cut ? (cut_floats(g, d) + (size_t)BH * d * d) * sizeof(float) : 0;
 }
 
-size_t workspace_bytes_of(int B, int H, int T, int d, int dtype) {
+size_t workspace_bytes_of(int B, int H, int T, int d, int dtype, bool backward) {
   int sms = 0;
   if (check_device(&sms) != POLAR_OK) sms = 148;
-  return B * H > 0 && T > 0 ? cut_bytes(split(B * H, T, d, dtype, sms), B * H, d) : 0;
+  return B * H > 0 && T > 0 ? cut_bytes(split(B * H, T, d, dtype, sms, backward), B * H, d) : 0;
 }
 
 // bf16 runs on the tensor cores, fp32 on the FP32 pipes.  n applications that
@@ -153,12 +150,12 @@ extern "C" {
 
 size_t polar_linear_workspace_bytes(int B, int H, int T, int d, int dtype) {
   if (!sizes_ok(B, H, T, d, dtype)) return 0;
-  return workspace_bytes_of(B, H, T, d, dtype);
+  return workspace_bytes_of(B, H, T, d, dtype, false);
 }
 
 size_t polar_linear_bwd_workspace_bytes(int B, int H, int T, int d, int dtype) {
   if (!sizes_ok(B, H, T, d, dtype)) return 0;
-  return 2 * workspace_bytes_of(B, H, T, d, dtype);
+  return 2 * workspace_bytes_of(B, H, T, d, dtype, true);
 }
 
 int polar_linear_fwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -183,7 +180,7 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   if (T == 0)
     return cuda_status("linear state copy", launch_linear_copy_state(
                                                 state_in, state_out, (size_t)B * H * d * d, s));
-  const LinearSplit g = split(B * H, T, d, dtype, sms);
+  const LinearSplit g = split(B * H, T, d, dtype, sms, false);
   const size_t need = cut_bytes(g, B * H, d);
   if (need && (!workspace || workspace_bytes < need)) return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
@@ -248,7 +245,7 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   if (T == 0)
     return cuda_status("linear state copy",
                        launch_linear_copy_state(dstate_out, dstate_in, (size_t)B * H * d * d, s));
-  const LinearSplit g = split(B * H, T, d, dtype, sms);
+  const LinearSplit g = split(B * H, T, d, dtype, sms, true);
   const size_t one = cut_bytes(g, B * H, d), need = 2 * one;
   if (need && (!workspace || workspace_bytes < need)) return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
