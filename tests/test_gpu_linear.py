@@ -128,6 +128,20 @@ def test_backward(case, dtype):
     assert pa.device_status() == 0
 
 
+MANY = [  # enough heads to fill the SMs: whole heads, runs that hold parts of several
+    (2, 40, 100, 64, None, True), (2, 20, 300, 128, (300, 171), True),
+    (1, 45, 1000, 128, None, True), (3, 30, 777, 64, (777, 1, 500), True),
+    (1, 160, 3000, 64, None, True),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "x".join(map(str, c[:4])))
+def test_many_heads(case, dtype):
+    test_forward(case, dtype)
+    test_backward(case, dtype)
+
+
 def test_gradients_are_differences_of_the_loss():
     """The loss sum(dmem * mem) + sum(dstate * state) is linear in each of q,
     k, v and the state, so its difference along a direction is exact."""
