@@ -659,8 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&br.m_op);
         }
         wait_ds = upd;
-        if (!upd) {  // the operand's reader, before the next portion's
-          ok = mbar_wait_warp(&br.o_full, (uint32_t)k & 1, abort_flag, p.status);
+        if (!upd) {
+          // the operand's reader, before the next portion's: x M^T of this tile.
+          // Its barrier's phase before (tile k - 2) is over for sure, which a
+          // wait by parity needs; that of o_full need not be.
+          ok = mbar_wait_warp(&br.empty_x[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
           if (!ok) break;
           continue;
         }

@@ -142,6 +142,36 @@ def test_many_heads(case, dtype):
     test_backward(case, dtype)
 
 
+@pytest.mark.parametrize("d,T,H", [(64, 130, 640), (64, 256, 2000), (128, 200, 900), (128, 40, 3000)])
+def test_many_short_heads_repeat(d, T, H):
+    """Runs of many whole heads change from one head's state to the next all
+    the time.  Ten calls into buffers that hold NaN give the same bits, and
+    single heads what they give alone (other tile cuts do not arise: one head
+    is one or two tiles)."""
+    import long_context_attention_causal_gb300 as pa
+    x = make(1, H, T, d, "bf16", 5 * d + T, state=True)
+    args = [x[n] for n in ("q", "k", "v", "log_decay", "dmem")]
+    first = None
+    for _ in range(10):
+        out = [torch.full_like(x["q"], float("nan")) for _ in range(4)]
+        S = pa.linear_fwd(*args[:4], state=x["state"], mem=out[0], want_state=True)[1]
+        pa.linear_bwd(*args, state=x["state"], dstate_out=x["dstate"], dq=out[1], dk=out[2],
+                      dv=out[3])
+        first = first or (*out, S)
+        for a, b in zip(first, (*out, S)):
+            assert torch.equal(a, b)
+    for h in (0, 1, H // 2, H - 1):
+        cut = lambda t: t[:, h:h + 1].contiguous()  # noqa: E731
+        one = [cut(x[n]) for n in ("q", "k", "v")]
+        mem, S = pa.linear_fwd(*one, x["log_decay"][h:h + 1], state=cut(x["state"]),
+                               want_state=True)
+        got = pa.linear_bwd(*one, x["log_decay"][h:h + 1], cut(x["dmem"]), state=cut(x["state"]),
+                            dstate_out=cut(x["dstate"]))
+        for a, b in zip((mem, *got[:3], S), first):
+            assert torch.equal(a, cut(b)), h
+    assert pa.device_status() == 0
+
+
 def test_gradients_are_differences_of_the_loss():
     """The loss sum(dmem * mem) + sum(dstate * state) is linear in each of q,
     k, v and the state, so its difference along a direction is exact."""
