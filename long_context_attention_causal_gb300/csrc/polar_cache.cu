@@ -466,8 +466,11 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   const int heads = a.B * a.Hkv;
   const int cached = a.max_seq_len < kKeysCached ? a.max_seq_len : kKeysCached;
   const int smem = cached * (int)sizeof(uint32_t);
+  // the attribute belongs to the function, not to the call: one value for all,
+  // or a call of another thread could lower it before this one's launch
   cudaError_t e = cudaFuncSetAttribute(polar_evict_select_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kKeysCached * (int)sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   polar_evict_select_kernel<<<heads, kEThreads, smem, s>>>(a, cached);
   e = cudaGetLastError();
