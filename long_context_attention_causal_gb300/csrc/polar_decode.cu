@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   const int split = blockIdx.y;
   const int page = 1 << page_shift;
   int n = lens[b];
-  const int n_max = min(splits * chunk, max_pages << page_shift);
+  // with logits: the rows that get weights are the rows of the softmax
+  const int n_max = kLogits ? logit_stride : min(splits * chunk, max_pages << page_shift);
   if (n < 1 || n > n_max) {
     if (threadIdx.x == 0 && split == 0) atomicExch(status, 3);
     n = n < 1 ? 0 : n_max;
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
           const float sc = my_valid ? v[0] : -INFINITY;
           if constexpr (kLogits) {
             const int key = key0 + (u0 + my_u) * NG + g;
-            if (key < k1 && key < logit_stride)
+            if (key < k1)
               logits[((size_t)b * Hq + hkv * G + my_g) * logit_stride + key] = sc;
           }
           float bm = sc;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
               for (int o = LPK / 2; o > 0; o >>= 1) d0 += __shfl_xor_sync(0xffffffffu, d0, o);
               sc[gi][u] = valid ? d0 : -INFINITY;
               if constexpr (kLogits) {
-                if (sub == 0 && key0 + kk < k1 && key0 + kk < logit_stride)
+                if (sub == 0 && key0 + kk < k1)
                   logits[((size_t)b * Hq + hkv * G + gi) * logit_stride + key0 + kk] = sc[gi][u];
               }
             }

@@ -184,7 +184,9 @@ __global__ void __launch_bounds__(kPThreads, 2)
   const int split = blockIdx.y;
   const int page = 1 << p.page_shift;
   int n = p.lens[b];
-  const int n_max = min(p.splits * p.chunk, p.max_pages << p.page_shift);
+  // with logits: the rows that get weights are the rows of the softmax
+  const int n_max =
+      kLogits ? p.logit_stride : min(p.splits * p.chunk, p.max_pages << p.page_shift);
   if (n < 1 || n > n_max) {
     if (threadIdx.x == 0 && split == 0) atomicExch(p.status, 3);
     n = n < 1 ? 0 : n_max;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kPThreads, 2)
       }
       if constexpr (kLogits) {
         // consecutive threads hold consecutive keys: coalesced per head
-        if (w && mine && key < k1 && key < p.logit_stride) {
+        if (w && mine && key < k1) {
           float* lg = p.logits + ((size_t)b * p.Hq + (size_t)hkv * G) * p.logit_stride + key;
 #pragma unroll
           for (int g = 0; g < G; ++g) lg[(size_t)g * p.logit_stride] = x[g];
