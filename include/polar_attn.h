@@ -349,10 +349,12 @@ int polar_memory_step(float* state, const void* q, const void* k, const void* v,
  *   state_out    : [B, H, d, d] fp32 or NULL: S after each sequence's last
  *                  token (after lengths[b] = 0 tokens: state_in).  May be
  *                  state_in itself.
- * Other overlaps of an output with a tensor of the call are refused
- * (POLAR_ERR_INVALID).  Rows at or past lengths[b] are written as zeros.  A token that holds an infinity or NaN may make other rows of its
- * 128-token tile non-finite, earlier ones included.  A length outside
- * [0, T] is clamped and records status 3 in polar_attn_device_status.
+ * Other overlaps of an output, or of the workspace that the call needs, with
+ * a tensor of the call are refused (POLAR_ERR_INVALID).  Rows at or past
+ * lengths[b] are written as zeros.  A token that holds an infinity or NaN may
+ * make other rows of its 128-token tile non-finite, earlier ones included.  A
+ * length outside [0, T] is clamped and records status 3 in
+ * polar_attn_device_status.
  * polar_linear_fwd takes a prompt by chunks of tokens; polar_linear_step is
  * the same recurrence for one token, q, k, v, mem [B, H, d], with the state
  * updated in place.  bf16 prompts run on the tensor cores: the state is

@@ -56,14 +56,15 @@ int check_sizes(int B, int H, int T, int d, int dtype, float scale) {
   return sizes_ok(B, H, T, d, dtype) ? POLAR_OK : POLAR_ERR_UNSUPPORTED;
 }
 
-// Bytes of a tensor; an output that meets another tensor is refused.
+// Bytes of a tensor; an output that meets another tensor is refused, and the
+// workspace, which is written too, where it meets any.
 struct Span {
   const void* p;
   size_t bytes;
 };
 bool meet(const Span& a, const Span& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x && y && x < y + b.bytes && y < x + a.bytes;
+  return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
 }
 bool any_meet(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
   for (const Span& o : outs) {
@@ -74,14 +75,19 @@ bool any_meet(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
   }
   return false;
 }
-// The spans of a [B, H, T, d] tensor and of the states; `same` is left out of
-// the latter where an output may be that input itself.
+// The spans of a [B, H, T, d] tensor, of the states, the decay and the
+// lengths; `same` is left out of the states where an output may be that input
+// itself.
 struct Sizes {
-  size_t rows, states;
+  size_t rows, states, heads, batch;
   Sizes(int B, int H, int T, int d, int dtype)
       : rows((size_t)B * H * T * d * (dtype == POLAR_BF16 ? 2 : 4)),
-        states((size_t)B * H * d * d * 4) {}
+        states((size_t)B * H * d * d * 4),
+        heads((size_t)H * 4),
+        batch((size_t)B * 4) {}
   Span row(const void* p) const { return {p, rows}; }
+  Span decay(const void* p) const { return {p, heads}; }
+  Span lengths(const void* p) const { return {p, batch}; }
   Span state(const void* p, const void* same = nullptr) const {
     return {p == same ? nullptr : p, states};
   }
@@ -97,9 +103,17 @@ size_t cut_bytes(const LinearSplit& g, int BH, int d) {
   return g.cut ? (cut_floats(g, d) + (size_t)BH * d * d) * sizeof(float) : 0;
 }
 
+// check_device with an assumed SM count where there is no device: sizes and
+// refusals do not need one.
+int device_or_assumed(int* sms) {
+  const int st = check_device(sms);
+  if (st != POLAR_OK) *sms = 148;
+  return st;
+}
+
 size_t workspace_bytes_of(int B, int H, int T, int d, int dtype, bool backward) {
   int sms = 0;
-  if (check_device(&sms) != POLAR_OK) sms = 148;
+  device_or_assumed(&sms);
   return B * H > 0 && T > 0 ? cut_bytes(split(B * H, T, d, dtype, sms, backward), B * H, d) : 0;
 }
 
@@ -169,19 +183,21 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(mem) ||
       !aligned16(state_in) || !aligned16(state_out) || !aligned4(log_decay) || !aligned4(lengths))
     return POLAR_ERR_MISALIGNED;
-  const Sizes z(B, H, T, d, dtype);
-  if (any_meet({z.row(mem), z.state(state_out)},
-               {z.row(q), z.row(k), z.row(v), z.state(state_in, state_out)}))
-    return POLAR_ERR_INVALID;
   int sms = 0;
-  st = check_device(&sms);
-  if (st != POLAR_OK) return st;
+  const int device = device_or_assumed(&sms);
+  const LinearSplit g = split(B * H, T, d, dtype, sms, false);
+  const size_t need = cut_bytes(g, B * H, d);
+  const Sizes z(B, H, T, d, dtype);
+  const Span scratch{workspace, std::min(need, workspace_bytes)};  // what may be written of it
+  if (any_meet({z.row(mem), z.state(state_out), scratch},
+               {z.row(q), z.row(k), z.row(v), z.state(state_in, state_out), z.decay(log_decay),
+                z.lengths(lengths)}))
+    return POLAR_ERR_INVALID;
+  if (device != POLAR_OK) return device;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0)
     return cuda_status("linear state copy", launch_linear_copy_state(
                                                 state_in, state_out, (size_t)B * H * d * d, s));
-  const LinearSplit g = split(B * H, T, d, dtype, sms, false);
-  const size_t need = cut_bytes(g, B * H, d);
   if (need && (!workspace || workspace_bytes < need)) return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
   int* status = status_word();
@@ -210,7 +226,8 @@ int polar_linear_step(float* state, const void* q, const void* k, const void* v,
       !aligned4(log_decay))
     return POLAR_ERR_MISALIGNED;
   const Sizes z(B, H, 1, d, dtype);
-  if (any_meet({z.row(mem), z.state(state)}, {z.row(q), z.row(k), z.row(v)}))
+  if (any_meet({z.row(mem), z.state(state)},
+               {z.row(q), z.row(k), z.row(v), z.decay(log_decay)}))
     return POLAR_ERR_INVALID;
   st = check_device(nullptr);
   if (st != POLAR_OK) return st;
@@ -233,20 +250,21 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
       !aligned16(dk) || !aligned16(dv) || !aligned16(state_in) || !aligned16(dstate_out) ||
       !aligned16(dstate_in) || !aligned4(log_decay) || !aligned4(lengths))
     return POLAR_ERR_MISALIGNED;
-  const Sizes z(B, H, T, d, dtype);
-  if (any_meet({z.row(dq), z.row(dk), z.row(dv), z.state(dstate_in)},
-               {z.row(q), z.row(k), z.row(v), z.row(dmem), z.state(state_in),
-                z.state(dstate_out, dstate_in)}))
-    return POLAR_ERR_INVALID;
   int sms = 0;
-  st = check_device(&sms);
-  if (st != POLAR_OK) return st;
+  const int device = device_or_assumed(&sms);
+  const LinearSplit g = split(B * H, T, d, dtype, sms, true);
+  const size_t one = cut_bytes(g, B * H, d), need = 2 * one;
+  const Sizes z(B, H, T, d, dtype);
+  const Span scratch{workspace, std::min(need, workspace_bytes)};  // what may be written of it
+  if (any_meet({z.row(dq), z.row(dk), z.row(dv), z.state(dstate_in), scratch},
+               {z.row(q), z.row(k), z.row(v), z.row(dmem), z.state(state_in),
+                z.state(dstate_out, dstate_in), z.decay(log_decay), z.lengths(lengths)}))
+    return POLAR_ERR_INVALID;
+  if (device != POLAR_OK) return device;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0)
     return cuda_status("linear state copy",
                        launch_linear_copy_state(dstate_out, dstate_in, (size_t)B * H * d * d, s));
-  const LinearSplit g = split(B * H, T, d, dtype, sms, true);
-  const size_t one = cut_bytes(g, B * H, d), need = 2 * one;
   if (need && (!workspace || workspace_bytes < need)) return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
   int* status = status_word();
