@@ -52,7 +52,10 @@ constexpr uint32_t kColS = 0, kColO = 128, kColDS = 256, kColM = 384;  // TMEM c
 struct OutBars {
   uint64_t full_x[2], full_z[2], empty_x[2], empty_z[2];
   uint64_t full_y, empty_y;  // one phase a tile
-  uint64_t s_full, p_full, o_full, o_free, staged, m_op;  // one phase a tile
+  // outputs staged in a z buffer: one a buffer, so that the next phase needs
+  // the store warp to have given that buffer back
+  uint64_t staged[2];
+  uint64_t s_full, p_full, o_full, o_free, m_op;  // one phase a tile
   uint64_t y_hi, y_lo, hi_done, ds_full;                  // one phase a state update
   uint64_t fixed;  // one phase a tile with rows past the sequence: they are zeroed
   uint64_t drain;
@@ -169,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&br.full_z[i], 1);
       mbar_init(&br.empty_x[i], 1);
       mbar_init(&br.empty_z[i], 1);
+      mbar_init(&br.staged[i], 4);
     }
     mbar_init(&br.full_y, 1);
     mbar_init(&br.empty_y, 1 + kStateWarps);  // the scores and the scaling have read it
@@ -176,7 +180,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&br.p_full, 4);
     mbar_init(&br.o_full, 1);
     mbar_init(&br.o_free, 4);
-    mbar_init(&br.staged, 4);
     mbar_init(&br.m_op, kStateWarps);
     mbar_init(&br.y_hi, kStateWarps);
     mbar_init(&br.y_lo, kStateWarps);
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const LinearPortion po = portion(ip);
         for (int c = 0; c < po.live; ++c, ++k) {
           const int st = k & 1;
-          ok = mbar_wait(&br.staged, (uint32_t)k & 1, abort_flag, p.status);
+          ok = mbar_wait(&br.staged[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
           if (!ok) break;
           for (int h = 0; h < D / 64; ++h)
             tma_store_3d(&map_o, smem + L::kZOff + st * L::kTile + h * L::kAtom, 64 * h,
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&br.staged);
+          if (lane == 0) mbar_arrive(&br.staged[st]);
         }
         if (!__all_sync(0xffffffffu, ok)) {
           go = false;
