@@ -16,7 +16,7 @@
 //
 // fp32 tensors: dot products of 24-bit values have no exact form on the tensor
 // cores, so chunks of 64 tokens run on packed fp32 fma.  Bound: those and the
-// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 1.63
+// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 1.65
 // ms, 38 TFLOP/s without the masked products, half of the FP32 pipes' nominal
 // rate).  Each CTA holds 64 or 32 rows of the state: a head then spreads
 // over as many CTAs, whose scores are computed as often.
@@ -99,12 +99,17 @@ struct StateTile {
   static __device__ __forceinline__ int col0() { return (int)(threadIdx.x % kLanes) * 4; }
 };
 
-// acc += sum_j w_j z_j y_j^T over the rows of a chunk (zw holds w_j z_j).
+// acc = sum_j w_j z_j y_j^T over the rows of a chunk (zw holds w_j z_j).  The
+// chunk is summed on its own and joined to what came before by the caller: the
+// state is rounded once a chunk, not once a token (8192 tokens without decay:
+// 1.8e-7 of the state's 2-norm instead of 1.4e-6, for 0 to 2.4 % of the time).
 template <int D, int Z>
 __device__ __forceinline__ void state_products(float4 (&acc)[StateTile<D, Z>::kR],
                                                const float (*y)[D + 4], const float (*zw)[Z]) {
   using S = StateTile<D, Z>;
   const int r0 = S::row0(), c0 = S::col0();
+#pragma unroll
+  for (int r = 0; r < S::kR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int j = 0; j < kC; ++j) {
     const float4 yv = *reinterpret_cast<const float4*>(&y[j][c0]);
@@ -147,9 +152,9 @@ __global__ void __launch_bounds__(kThreads)
   const float l2 = linear_log2_decay(a.log_decay, po.bh % a.H);
   const float* y = static_cast<const float*>(a.y) + (size_t)po.bh * a.T * D;
   const float* z = static_cast<const float*>(a.z) + (size_t)po.bh * a.T * D;
-  float4 acc[S::kR];
+  float4 sum[S::kR];
 #pragma unroll
-  for (int r = 0; r < S::kR; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r = 0; r < S::kR; ++r) sum[r] = make_float4(0.f, 0.f, 0.f, 0.f);
   Pieces<D> py;
   Pieces<kZ> pz;
   py.load(y, D, t0, t1);
@@ -169,12 +174,15 @@ __global__ void __launch_bounds__(kThreads)
     py.load(y, D, c0 + kC, t1);
     pz.load(z + z0, D, c0 + kC, t1);
     __syncthreads();
+    float4 acc[S::kR];
     state_products<D, kZ>(acc, sm.y, sm.zw);
+#pragma unroll
+    for (int r = 0; r < S::kR; ++r) sum[r] = axpy4(1.f, acc[r], sum[r]);
   }
   float* dst = a.cuts + ((size_t)part * D + z0) * D;
 #pragma unroll
   for (int r = 0; r < S::kR; ++r)
-    *reinterpret_cast<float4*>(dst + (size_t)(S::row0() + r) * D + S::col0()) = acc[r];
+    *reinterpret_cast<float4*>(dst + (size_t)(S::row0() + r) * D + S::col0()) = sum[r];
 }
 
 // Grid (BH, d * d / 512): four state elements a thread through the cuts of
@@ -450,13 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0 && (ci + 1 < n_ch || fin)) {
         const float g = sm.pw[n];
         float4 acc[S::kR];
-#pragma unroll
-        for (int r = 0; r < S::kR; ++r) {
-          const float4 v =
-              *reinterpret_cast<const float4*>(&sm.m[state_slot<Z>(S::row0() + r)][S::col0()]);
-          acc[r] = make_float4(g * v.x, g * v.y, g * v.z, g * v.w);
-        }
         state_products<D, Z>(acc, sm.y, sm.zw);
+#pragma unroll
+        for (int r = 0; r < S::kR; ++r)
+          acc[r] = axpy4(
+              g, *reinterpret_cast<const float4*>(&sm.m[state_slot<Z>(S::row0() + r)][S::col0()]),
+              acc[r]);
         __syncthreads();  // every read of the state and the chunk is done
 #pragma unroll
         for (int r = 0; r < S::kR; ++r)
@@ -539,8 +546,8 @@ cudaError_t out_dz(const OutBatch& batch, int n, cudaStream_t s) {
                        batch.a[0].chained, batch);
 }
 
-// 64 state rows a CTA, so that fewer CTAs compute the same scores (290 us
-// against 392 with 32 at 64 heads of 4096 tokens, d = 64; 439 against 589 at 32
+// 64 state rows a CTA, so that fewer CTAs compute the same scores (294 us
+// against 392 with 32 at 64 heads of 4096 tokens, d = 64; 445 against 589 at 32
 // heads, d = 128), unless 32 rows a CTA find an SM each: a chunk then takes less
 // time (2 heads of 100 tokens, d = 64, 16 us against 20; 8 of 300, d = 128, 34
 // against 42).
