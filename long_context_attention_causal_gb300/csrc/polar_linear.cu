@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kScanThreads) polar_linear_scan_kernel(const S
         *reinterpret_cast<const float4*>(a.init + (size_t)bh * dd + e);
   if (cuts < 1) return;
   const int len = linear_length(a.lengths, bh / a.H, a.T, nullptr);
-  const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
+  const float ln = linear_log_decay(a.log_decay, bh % a.H);
   float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.init) m = *reinterpret_cast<const float4*>(a.init + (size_t)bh * dd + e);
   // forward: boundary k closes run k - 1; reverse: it opens run k
@@ -226,9 +226,7 @@ __global__ void __launch_bounds__(kScanThreads) polar_linear_scan_kernel(const S
         const long long lo = a.reverse ? k * per : max(h0, (k - 1) * per);
         const long long hi = a.reverse ? min(h1, (k + 1) * per) : k * per;
         const int ta = (int)(lo - h0) * kLinearTile, tb = (int)(hi - h0) * kLinearTile;
-        const float g = linear_power(l2, max(min(len, tb) - ta, 0));
-        m = make_float4(fmaf(g, m.x, own[u].x), fmaf(g, m.y, own[u].y), fmaf(g, m.z, own[u].z),
-                        fmaf(g, m.w, own[u].w));
+        m = linear_decay(ln, max(min(len, tb) - ta, 0)).join(m, own[u]);
         *slot(i0 + u) = m;
       }
     }
@@ -291,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             a.reverse ? n_po - 1 - ip : ip);
     const int bh = po.bh, len = po.len;
     const int t0 = po.row(po.first), t1 = min(po.row(po.last), a.T);
+    const float ln = linear_log_decay(a.log_decay, bh % a.H);
     const float l2 = linear_log2_decay(a.log_decay, bh % a.H);
     const float* x = static_cast<const float*>(a.x) + (size_t)bh * a.T * D;
     const float* y = static_cast<const float*>(a.y) + (size_t)bh * a.T * D;
@@ -456,13 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // registers that the products need
       if (ci + 1 < n_ch) fetch(chunk(ci + 1));
       if (n > 0 && (ci + 1 < n_ch || fin)) {
-        const float g = sm.pw[n];
+        const LinearDecay g = linear_decay(ln, n);
         float4 acc[S::kR];
         state_products<D, Z>(acc, sm.y, sm.zw);
 #pragma unroll
         for (int r = 0; r < S::kR; ++r)
-          acc[r] = axpy4(
-              g, *reinterpret_cast<const float4*>(&sm.m[state_slot<Z>(S::row0() + r)][S::col0()]),
+          acc[r] = g.join(
+              *reinterpret_cast<const float4*>(&sm.m[state_slot<Z>(S::row0() + r)][S::col0()]),
               acc[r]);
         __syncthreads();  // every read of the state and the chunk is done
 #pragma unroll
@@ -504,14 +503,14 @@ __global__ void __launch_bounds__(kStepWarps * 32)
     s[r] = *reinterpret_cast<const float4*>(S + (size_t)(row0 + r * kRW) * D + c0);
   const float4 k = load4<T>(static_cast<const T*>(a.k) + bh * D + c0);
   const float4 q = load4<T>(static_cast<const T*>(a.q) + bh * D + c0);
-  const float g = linear_power(linear_log2_decay(a.log_decay, (int)(bh % a.H)), 1);
+  const LinearDecay g = linear_decay(linear_log_decay(a.log_decay, (int)(bh % a.H)), 1);
   const T* v = static_cast<const T*>(a.v) + bh * D;
   T* mem = static_cast<T*>(a.mem) + bh * D;
 #pragma unroll
   for (int r = 0; r < kN; ++r) {
     const int row = row0 + r * kRW;
     const float vr = linear_load(v + row);
-    s[r] = axpy4(g, s[r], make_float4(vr * k.x, vr * k.y, vr * k.z, vr * k.w));
+    s[r] = g.join(s[r], make_float4(vr * k.x, vr * k.y, vr * k.z, vr * k.w));
     *reinterpret_cast<float4*>(S + (size_t)row * D + c0) = s[r];
     const float2 o2 = dot4(s[r], q, make_float2(0.f, 0.f));
     float o = o2.x + o2.y;

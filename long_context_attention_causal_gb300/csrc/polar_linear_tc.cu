@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ds_tm = m_tm - kColM + kColDS;
     // 32 columns of the state: after a tile, g times the one before it plus the
     // tile's products.
-    auto state_block = [&](int b, bool add, float g, uint32_t (&v)[32]) {
+    auto state_block = [&](int b, bool add, LinearDecay g, uint32_t (&v)[32]) {
       tmem_ld32(m_tm + 32 * b, v);
       if (add) {
         uint32_t ds[32];
@@ -534,15 +534,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_fence32(v);
         reg_fence32(ds);
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          v[e] = __float_as_uint(fmaf(g, __uint_as_float(v[e]), __uint_as_float(ds[e])));
+        for (int e = 0; e < 32; e += 2) {
+          const float2 m =
+              g.join(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                     make_float2(__uint_as_float(ds[e]), __uint_as_float(ds[e + 1])));
+          v[e] = __float_as_uint(m.x);
+          v[e + 1] = __float_as_uint(m.y);
+        }
       } else {
         tmem_ld_wait();
         reg_fence32(v);
       }
     };
     // The state to its bf16 operand for x M^T and, if new, back into TMEM.
-    auto hand_over = [&](bool add, float g) {
+    auto hand_over = [&](bool add, LinearDecay g) {
       int sw = r & 7;
       asm volatile("" : "+r"(sw));  // not to be kept as eight addresses across the loop
 #pragma unroll
@@ -573,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_wait_previous();  // only these warps read states or write the final one
     for (int ip = 0; ip < n_po && ok; ++ip) {
       const LinearPortion po = portion(ip);
+      const float ln = linear_log_decay(p.log_decay, po.bh % p.H);
       const float l2 = linear_log2_decay(p.log_decay, po.bh % p.H);
       const bool fin = is_final(po);
       if (po.live > 0 || fin) {
@@ -608,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
       }
       bool wait_ds = false;  // products of the tile before are under way
-      float g = 0.f;         // what the state decays by over that tile
+      int last_n = 0;        // its tokens
       for (int c = 0; c < po.live; ++c, ++k) {
         const int st = k & 1, tile = tile_of(po, c), n = po.tokens(tile);
         const bool upd = updates(po, c);
@@ -632,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < kVecs; ++q) lo[q] = from[kStateThreads * q];
         __syncwarp();
         if (lane == 0) mbar_arrive(&br.empty_y);
+        const LinearDecay g = linear_decay(ln, last_n);
         if (wait_ds) {
           ok = mbar_wait_warp(&br.ds_full, (uint32_t)(ku - 1) & 1, abort_flag, p.status);
           if (!ok) break;
@@ -653,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         hand_over(wait_ds, g);
-        g = linear_power(l2, n);
+        last_n = n;
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -684,6 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
         }
+        const LinearDecay g = linear_decay(ln, last_n);
         float* dst = final_state + ((size_t)po.bh * D + r) * D + half * kCols;
 #pragma unroll
         for (int b = 0; b < kCols / 32; ++b) {
