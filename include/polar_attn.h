@@ -357,9 +357,13 @@ int polar_memory_step(float* state, const void* q, const void* k, const void* v,
  * polar_attn_device_status.
  * polar_linear_fwd takes a prompt by chunks of tokens; polar_linear_step is
  * the same recurrence for one token, q, k, v, mem [B, H, d], with the state
- * updated in place.  bf16 prompts run on the tensor cores: the state is
- * carried in fp32 and rounded to bf16 only as an operand of the product that
- * reads it; fp32 runs on the FP32 pipes.
+ * updated in place.  States are expected to be finite.  bf16 prompts run on
+ * the tensor cores with fp32 accumulation.  Rounded to bf16 there: the decayed
+ * scores, and the state as an operand of the product that reads it (not the
+ * state that is carried on, which is fp32).  Tokens enter the state as sums of
+ * three bf16 terms where state_out is given, so that it has the precision of
+ * fp32 sums, of two where it is not; mem may differ in its last bit between
+ * the two.  fp32 runs on the FP32 pipes.
  * workspace: polar_linear_workspace_bytes(B, H, T, d, dtype) bytes, device,
  * 16-byte aligned; its contents on entry do not affect the results.
  */
@@ -381,7 +385,9 @@ int polar_linear_step(float* state, const void* q, const void* k, const void* v,
  *   dstate_out : [B, H, d, d] fp32 or NULL (zero): gradient of state_out
  *   dq, dk, dv : [B, H, T, d] of dtype (written; rows past lengths[b] zero)
  *   dstate_in  : [B, H, d, d] fp32 or NULL (may be dstate_out itself)
- * The other arguments are the forward's, overlaps too.  The decay is a constant of the
+ * The other arguments are the forward's, overlaps and precision (dstate_in in
+ * the place of state_out) too.  dq, dk and dv have the inputs' type, unlike
+ * polar_attn_bwd's, which are fp32.  The decay is a constant of the
  * layer, as the temperature's and the gate's constants are: it carries no
  * gradient.  workspace: polar_linear_bwd_workspace_bytes(...) bytes.
  */

@@ -102,6 +102,7 @@ struct LinearArgs {
   const float* cuts;      // states at the cuts (LinearStateArgs), null without cuts
   float* final_state;     // [B, H, d, d] state at the other end, or null (not with state_t)
   int* status;
+  bool exact;             // the caller asks for the state at the other end
   bool chained = false;   // follows a kernel of the same call (programmatic launch)
 };
 
@@ -120,6 +121,7 @@ struct LinearStateArgs {
   float* cuts;        // [parts][d][d]
   int* status;
   float* init_copy;   // [B, H, d, d]: where the scan copies init, or null
+  bool exact;         // the caller asks for the final state
 };
 // Each launch takes n applications that differ in tensors, states, direction
 // and scale only: states and scans 1 or 2, outputs in fp32 1 to 3.

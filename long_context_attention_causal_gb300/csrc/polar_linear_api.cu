@@ -137,9 +137,10 @@ int run_states(const LinearStateArgs* a, int n, int dtype, cudaStream_t s) {
 
 int run_out(LinearArgs* a, int n, int dtype, cudaStream_t s) {
   if (dtype != POLAR_BF16) return cuda_status("linear output launch", launch_linear_out(a, n, s));
-  // one direction a launch
+  // one direction and one number of terms a launch
   for (int i = 0; i < n;) {
-    const int m = i + 1 < n && a[i + 1].reverse == a[i].reverse ? 2 : 1;
+    const int m =
+        i + 1 < n && a[i + 1].reverse == a[i].reverse && a[i + 1].exact == a[i].exact ? 2 : 1;
     if (i > 0) a[i].chained = true;
     CUtensorMap maps[8];
     for (int j = 0; j < m; ++j) {
@@ -206,12 +207,13 @@ int polar_linear_fwd(const void* q, const void* k, const void* v, const float* l
   float* copy = g.cut && state_in && state_in == state_out ? cuts + cut_floats(g, d) : nullptr;
   if (g.cut) {
     const LinearStateArgs a{k, v, log_decay, lengths, B, H, T, d, 1.f, false,
-                            g, state_in, cuts, status, copy};
+                            g, state_in, cuts, status, copy, state_out != nullptr};
     st = run_states(&a, 1, dtype, s);
     if (st != POLAR_OK) return st;
   }
   LinearArgs a{q, k, v, mem, log_decay, lengths, B, H, T, d, scale, false, false,
-               g, copy ? copy : state_in, cuts, state_out, status, g.cut};
+               g, copy ? copy : state_in, cuts, state_out, status, state_out != nullptr,
+               g.cut};
   return run_out(&a, 1, dtype, s);
 }
 
@@ -276,19 +278,23 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   if (g.cut) {
     // dq's states last: its kernel then starts on tiles that are still in L2
     const LinearStateArgs a[2] = {{q, dmem, log_decay, lengths, B, H, T, d, scale, true,
-                                   g, dstate_out, cuts_r, status, copy},
+                                   g, dstate_out, cuts_r, status, copy, dstate_in != nullptr},
                                   {k, v, log_decay, lengths, B, H, T, d, 1.f, false,
-                                   g, state_in, cuts_s, status, nullptr}};
+                                   g, state_in, cuts_s, status, nullptr, false}};
     st = run_states(a, 2, dtype, s);
     if (st != POLAR_OK) return st;
   }
+  // dk and dv share a launch where they share their terms.  dk needs no more
+  // than two, and the two launches that follow from that take less time (B2 H16
+  // T16384 d128: 427 us, 444 in one), unless one leaves half of the SMs idle (B8
+  // H8 T1111 d64: 84, 59 in one).
   const float* r_init = copy ? copy : dstate_out;
   LinearArgs a[3] = {{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
-                      g, state_in, cuts_s, nullptr, status, g.cut},
+                      g, state_in, cuts_s, nullptr, status, false, g.cut},
                      {v, dmem, q, dk, log_decay, lengths, B, H, T, d, scale, true, true,
-                      g, r_init, cuts_r, nullptr, status},
+                      g, r_init, cuts_r, nullptr, status, dstate_in && 2LL * g.parts <= sms},
                      {k, q, dmem, dv, log_decay, lengths, B, H, T, d, scale, true, false,
-                      g, r_init, cuts_r, dstate_in, status}};
+                      g, r_init, cuts_r, dstate_in, status, dstate_in != nullptr}};
   // dv's CTA would write dstate_in over the dstate_out that dk's has yet to
   // read: in place and uncopied, dv goes after the others
   if (!dstate_in || r_init != dstate_in) return run_out(a, 3, dtype, s);

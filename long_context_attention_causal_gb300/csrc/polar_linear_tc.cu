@@ -9,31 +9,39 @@
 //   O  = x M^T                 M as a bf16 operand in shared memory
 //   O_i *= g^(i+1), then O += P z                A in TMEM
 //   M' = g^n M + z^T (w y)
-// P and the operand copy of M are rounded to bf16 once, a relative 2^-9 of what
-// the bf16 outputs are rounded by again.  The state itself stays in fp32 in
-// TMEM: once a tile it is read, multiplied by g^n and added to the tile's
-// products in one fp32 fma.  Those have an accumulator of their own, because
-// the tensor core cuts off, rather than rounds, what it adds to: 16 products a
-// tile straight into the state lost 1.6e-5 of it over 16K tokens of a slow
-// decay, against 2.9e-6 this way, which takes 4 % more time.  w y is not exact
-// in bf16, so it enters as two bf16 terms, hi + lo (2^-18 relative); a third would
-// cost a sixth product.  hi and lo take turns in one buffer; two buffers of x
-// and z, one of y, that one and the state operand fill shared memory (7 x 32 KB
-// at d = 128), and S, O, the tile's products and the state fill TMEM.  The
-// outputs are staged in z's buffer, whose last reader makes them.
+// P and the operand copy of M are rounded to bf16 once, at most 2^-8 of a value
+// that the bf16 outputs round by as much again.  The state itself stays in fp32
+// in TMEM: once a tile it is read, multiplied by g^n (LinearDecay) and added to
+// the tile's products.  Those have an accumulator of their own, because the
+// tensor core cuts off, rather than rounds, what it adds to: 16 products a tile
+// straight into the state lost 1.6e-5 of it over 16K tokens of a slow decay.
+// w y is not exact in bf16 and enters as a sum of bf16 terms.  Two leave at most
+// 2^-17 of it (2.5e-6 of the state in the 2-norm), which no operand of x M^T
+// shows; three leave 2^-25 and are taken where the caller asks for the state,
+// in fp32 (kThree: 2e-7 of the state, what fp32 sums have).  The smaller terms
+// are added first, so that little is cut off.  B2 H16 T16384 d128 takes 149 us
+// with two terms and 175 with three.
+//
+// Shared memory at d = 128 is full (7 x 32 KB): two buffers of x and z, one of
+// y, the state operand and one for a term of w y; see OutLayout for the other
+// terms.  S, O, the tile's products and the state fill TMEM.  The outputs are
+// staged in z's buffer, whose last reader makes them.
 //
 // Bound: HBM, closely followed by shared memory.  A tile moves 4 x 32 KB at
 // d = 128, 5600 cycles at an SM's share of the measured copy bandwidth; its
-// operands, hi and lo, the state operand and the staged outputs are about
-// 576 KB of shared memory traffic, 4500 cycles at 128 bytes each; the products
-// need 2600.  Measured: 5800 cycles a tile.  B2 H16 T16384 d128 (27 tiles a
-// CTA) takes 98 us, 5.5 TB/s, 81 % of the copy bandwidth: the rest is the
-// first loads, the last stores and the change of heads inside a run.
+// operands, two terms, the state operand and the staged outputs are about
+// 576 KB of shared memory traffic, 4500 cycles at 128 bytes each (672 KB with
+// three terms); the products need 2600 (3100).  Measured: 5800 cycles a tile.
+// B2 H16 T16384 d128 (27 tiles a CTA) takes 98 us, 5.5 TB/s, 81 % of the copy
+// bandwidth: the rest is the first loads, the last stores and the change of
+// heads inside a run.
 //
-// Roles (480 threads, one CTA per SM): warps 0-3 P and the outputs (thread =
-// row = TMEM lane), warps 4-11 the state and the scaling of y (two groups,
-// half of the columns each), warp 12 TMA loads, warp 13 MMA and TMEM, warp 14
-// TMA stores.
+// Roles (one CTA per SM): warps 0-3 P and the outputs (thread = row = TMEM
+// lane), the next 8 or 16 the state and the scaling of y (each group of four
+// has all of its rows, and a share of the columns), then one warp each for TMA
+// loads, MMA and TMEM, TMA stores.  With three terms the state's warps are the
+// longest chain; 16 of them, of 80 registers a thread, take 107 us where 8 take
+// 116, but none with two terms.
 #include "polar_device.cuh"
 #include "polar_internal.h"
 #include "polar_linear.cuh"
@@ -43,10 +51,14 @@ namespace polar {
 namespace {
 
 constexpr int kTok = kLinearTile;  // tokens per tile
-constexpr int kThreads = 480;
-constexpr int kStateThreads = 256;
-constexpr int kWarpTMA = 12, kWarpMMA = 13, kWarpStore = 14;
-constexpr int kStateWarps = 8;
+// Warps of the output kernel: four for P and the outputs, then these.
+template <bool kThree>
+struct OutRoles {
+  static constexpr int kStateWarps = kThree ? 16 : 8;
+  static constexpr int kStateThreads = 32 * kStateWarps;
+  static constexpr int kTMA = 4 + kStateWarps, kMMA = kTMA + 1, kStore = kTMA + 2;
+  static constexpr int kThreads = 32 * (kStore + 1);
+};
 constexpr uint32_t kColS = 0, kColO = 128, kColDS = 256, kColM = 384;  // TMEM columns
 
 struct OutBars {
@@ -56,7 +68,7 @@ struct OutBars {
   // the store warp to have given that buffer back
   uint64_t staged[2];
   uint64_t s_full, p_full, o_full, o_free, m_op;  // one phase a tile
-  uint64_t y_hi, y_lo, hi_done, ds_full;                  // one phase a state update
+  uint64_t first, first_done, second, last, ds_full;  // one phase a state update
   uint64_t fixed;  // one phase a tile with rows past the sequence: they are zeroed
   uint64_t drain;
   uint32_t tmem_base;
@@ -73,10 +85,15 @@ struct OutLayout {
   static constexpr int kXOff = 0;                  // two of x
   static constexpr int kZOff = kXOff + 2 * kTile;  // two of z, then the staged outputs
   static constexpr int kYOff = kZOff + 2 * kTile;  // one of y
-  static constexpr int kWOff = kYOff + kTile;      // scaled y: hi, then lo
-  static constexpr int kMOff = kWOff + kTile;      // state operand, D rows
+  static constexpr int kMOff = kYOff + kTile;      // state operand, D rows
   static constexpr int kMAtom = D * 128;
-  static constexpr int kBarOff = kMOff + D * D * 2;
+  // Terms of scaled y, in the order of their products.  d = 64 has room for each;
+  // at d = 128 the last takes the place of the state operand once x M^T has read
+  // that, and the first of three makes room for the second.
+  static constexpr bool kApart = D == 64;
+  static constexpr int kWOff = kMOff + (kApart ? D * D * 2 : kTile);
+  static constexpr int kLastOff = kApart ? kWOff + 2 * kTile : kMOff;
+  static constexpr int kBarOff = kWOff + (kApart ? 3 : 1) * kTile;
   static constexpr int kSmemBytes = kBarOff + (int)sizeof(OutBars) + 1024;
   // more than half of the SM's, so one CTA holds the 512 TMEM columns
   static constexpr int kAsked = kSmemBytes > 120000 ? kSmemBytes : 120000;
@@ -119,39 +136,73 @@ __device__ __forceinline__ void tma_store_commit_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// w y of eight bf16 values as bf16 hi and the bf16 of what hi leaves.
-__device__ __forceinline__ void split_vec(uint4 y, float w, uint4& hi, uint4& lo) {
+__device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+// 16 consecutive TMEM columns of this thread's lane -> 16 registers, and by the
+// size of the array.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  tmem_st16(taddr, r);
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
+  tmem_st32(taddr, r);
+}
+__device__ __forceinline__ void fence_regs(uint32_t (&r)[16]) { reg_fence16(r); }
+__device__ __forceinline__ void fence_regs(uint32_t (&r)[32]) { reg_fence32(r); }
+
+// w y of eight bf16 values as a sum of bf16 values: hi, the rounding of what hi
+// leaves, and, if three, that of what the two leave.
+template <bool kThree>
+__device__ __forceinline__ void split_vec(uint4 y, float w, uint4& hi, uint4& lo, uint4& rest) {
   const uint32_t in[4] = {y.x, y.y, y.z, y.w};
-  const float2 w2 = make_float2(w, w), zero = make_float2(0.f, 0.f);
-  const float2 minus = make_float2(-1.f, -1.f);
-  uint32_t h[4], l[4];
+  const float2 w2 = make_float2(w, w), minus = make_float2(-1.f, -1.f);
+  uint32_t h[4], l[4], s[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 f = ffma2(make_float2(__uint_as_float(in[e] << 16),
-                                       __uint_as_float(in[e] & 0xFFFF0000u)), w2, zero);
+    const float2 f = ffma2(unpack_bf16x2(in[e]), w2, make_float2(0.f, 0.f));
     h[e] = pack_bf16x2(f.x, f.y);
-    const float2 r = ffma2(make_float2(__uint_as_float(h[e] << 16),
-                                       __uint_as_float(h[e] & 0xFFFF0000u)), minus, f);
+    const float2 r = ffma2(unpack_bf16x2(h[e]), minus, f);
     l[e] = pack_bf16x2(r.x, r.y);
+    if constexpr (kThree) {
+      const float2 t = ffma2(unpack_bf16x2(l[e]), minus, r);
+      s[e] = pack_bf16x2(t.x, t.y);
+    }
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
+  rest = make_uint4(s[0], s[1], s[2], s[3]);
 }
 
-// Zero rows [n, 128) of a tile in shared memory (state threads).
-template <int D>
+// Zero rows [n, 128) of a tile in shared memory (kN threads).
+template <int D, int kN>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int n, int tid) {
-  for (int i = tid; i < kTok * D / 8; i += kStateThreads)
+  for (int i = tid; i < kTok * D / 8; i += kN)
     if (((i >> 3) & (kTok - 1)) >= n) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
 }
 
-// One run of tiles a CTA.  kRev: from the last tile back.  Every role walks
-// the same portions and tiles; it counts tiles (k), state updates (ku) and
-// tiles with rows to zero (kf) for the phases of the barriers.
-template <int D, bool kRev>
-__global__ void __launch_bounds__(kThreads, 1)
+// One run of tiles a CTA.  kRev: from the last tile back.  kThree: terms of
+// scaled y, the same number in every portion (a choice by portion in one kernel
+// cost 12 us for its code).  Every role walks the same portions and tiles; it
+// counts tiles (k), state updates (ku) and tiles with rows to zero (kf) for the
+// phases of the barriers.
+template <int D, bool kRev, bool kThree>
+__global__ void __launch_bounds__(OutRoles<kThree>::kThreads, 1)
     polar_linear_out_tc_kernel(const __grid_constant__ OutMaps maps, const OutParams p) {
   using L = OutLayout<D>;
+  using R = OutRoles<kThree>;
+  constexpr int kStateWarps = R::kStateWarps, kStateThreads = R::kStateThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -181,17 +232,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&br.o_full, 1);
     mbar_init(&br.o_free, 4);
     mbar_init(&br.m_op, kStateWarps);
-    mbar_init(&br.y_hi, kStateWarps);
-    mbar_init(&br.y_lo, kStateWarps);
-    mbar_init(&br.hi_done, 1);
+    mbar_init(&br.first, kStateWarps);
+    mbar_init(&br.second, kStateWarps);
     mbar_init(&br.ds_full, 1);
+    mbar_init(&br.first_done, 1);
+    mbar_init(&br.last, kStateWarps);
     mbar_init(&br.fixed, kStateWarps);
     mbar_init(&br.drain, 1);
     br.abort_flag = 0;
     fence_barrier_init();
   }
   linear_let_next_start();
-  if (warp == kWarpMMA) tmem_alloc(&br.tmem_base, 512);
+  if (warp == R::kMMA) tmem_alloc(&br.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -214,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the state after tile c is read by tile c + 1, or is the final one
   auto updates = [&](const LinearPortion& po, int c) { return c + 1 < po.live || is_final(po); };
 
-  if (warp == kWarpTMA) {
+  if (warp == R::kTMA) {
     // ------------------------------------------------------ TMA producer --
     if (lane == 0) {
       tma_prefetch_desc(&map_x);
@@ -261,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ny > 0) mbar_wait(&br.full_y, (uint32_t)(ny - 1) & 1, &never, p.status, lim);
       __syncwarp();
     }
-  } else if (warp == kWarpMMA) {
+  } else if (warp == R::kMMA) {
     // ------------------------------------------------------- MMA issuer --
     // whole warp: uniform waits and descriptors, one elected lane issues
     constexpr uint32_t kIdS = idesc_bf16_f32(kTok, kTok, 0, 0);
@@ -278,17 +330,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto kstep = [&](int kk, uint32_t atom) {
       return at((kk >> 2) * atom) + (uint64_t)(kk & 3) * 2;
     };
-    auto issue_ds = [&](int st, bool add) {
-      const uint64_t y0 = mn + at(L::kWOff), z0 = mn + at(L::kZOff + st * L::kTile);
+    // a term of scaled y, at `off`
+    auto issue_ds = [&](int st, uint32_t off, bool add) {
+      tc_fence_after();
+      const uint64_t y0 = mn + at(off), z0 = mn + at(L::kZOff + st * L::kTile);
 #pragma unroll
       for (int kk = 0; kk < kTok / 16; ++kk)
         umma_ss_warp(tmem + kColDS, z0 + at(kk * 2048), y0 + at(kk * 2048), kIdDS,
                      add || kk > 0);
     };
-    // Order of a tile's products: S, hi, x M^T, lo, P z.  x M^T runs while lo
-    // is written; P z and the next S run while the next y is scaled.  (Waiting
-    // for the next tile's inputs before P z, so that S follows without a pause,
-    // measured 109 us against 100: the scaling then waits for its turn.)
+    // Order of a tile's products: S, x M^T, the terms of y, P z.  P z and the
+    // next S run while the next y is scaled.  (Waiting for the next tile's
+    // inputs before P z, so that S follows without a pause, measured 109 us
+    // against 100: the scaling then waits for its turn.)
     int k = 0, ku = 0, kf = 0;
     bool ok = true, any = false;
     for (int ip = 0; ip < n_po && ok; ++ip) {
@@ -296,8 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < po.live; ++c, ++k) {
         const int st = k & 1, tile = tile_of(po, c);
         const uint32_t ph = (uint32_t)k & 1, ph2 = (uint32_t)(k / 2) & 1;
-        const bool upd = updates(po, c);
-        const uint32_t pu = (uint32_t)ku & 1;
         // S: over P of the tile before, whose product is issued already
         ok = mbar_wait_warp(&br.full_x[st], ph2, abort_flag, p.status) &&
              mbar_wait_warp(&br.full_y, ph, abort_flag, p.status);
@@ -313,16 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_warp(&br.s_full);
         umma_commit_warp(&br.empty_y);
         any = true;
-        ok = mbar_wait_warp(&br.full_z[st], ph2, abort_flag, p.status);
-        if (ok && upd) {
-          ok = mbar_wait_warp(&br.y_hi, pu, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          issue_ds(st, false);
-          umma_commit_warp(&br.hi_done);
-        }
         // x M^T, once the state is written and the last outputs are read
-        ok = ok && mbar_wait_warp(&br.m_op, ph, abort_flag, p.status);
+        ok = mbar_wait_warp(&br.m_op, ph, abort_flag, p.status);
         if (ok && k > 0) ok = mbar_wait_warp(&br.o_free, ph ^ 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
@@ -331,16 +375,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_ss_warp(tmem + kColO, x0 + kstep(kk, L::kAtom), m_desc + kstep(kk, L::kMAtom),
                        kIdXM, kk > 0);
         umma_commit_warp(&br.empty_x[st]);
-        if (upd) {
-          ok = mbar_wait_warp(&br.y_lo, pu, abort_flag, p.status);
+        ok = mbar_wait_warp(&br.full_z[st], ph2, abort_flag, p.status);
+        if (ok && updates(po, c)) {
+          ok = mbar_wait_warp(&br.first, (uint32_t)ku & 1, abort_flag, p.status);
           if (!ok) break;
-          tc_fence_after();
-          issue_ds(st, true);
+          issue_ds(st, L::kWOff, false);
+          if constexpr (L::kApart) {
+            if constexpr (kThree) issue_ds(st, L::kWOff + L::kTile, true);
+          } else {
+            if constexpr (kThree) {
+              umma_commit_warp(&br.first_done);
+              ok = mbar_wait_warp(&br.second, (uint32_t)ku & 1, abort_flag, p.status);
+              if (!ok) break;
+              issue_ds(st, L::kWOff, true);
+            }
+            ok = mbar_wait_warp(&br.last, (uint32_t)ku & 1, abort_flag, p.status);
+            if (!ok) break;
+          }
+          issue_ds(st, L::kLastOff, true);
           umma_commit_warp(&br.ds_full);
           ++ku;
         }
         // P z, added to x M^T once that has its powers of the decay
-        ok = mbar_wait_warp(&br.p_full, ph, abort_flag, p.status);
+        ok = ok && mbar_wait_warp(&br.p_full, ph, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t z0 = mn + at(L::kZOff + st * L::kTile);
@@ -358,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&br.drain, 0, &never, p.status, kWaitLimitCycles / 4);
       __syncwarp();
     }
-  } else if (warp == kWarpStore) {
+  } else if (warp == R::kStore) {
     // ------------------------------------------------------- TMA stores --
     if (lane == 0) {
       int k = 0;
@@ -516,25 +573,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 4 + kStateWarps) {
     // ------------------------------------------------ state, scaling of y --
     const int tid = threadIdx.x - 128;
-    const int half = (warp - 4) >> 2;  // which half of the columns
     const int r = threadIdx.x & 127;   // state row (z dim) = TMEM lane
-    constexpr int kCols = D / 2;
+    constexpr int kCols = 128 * D / kStateThreads;
+    constexpr int kB = kThree ? 16 : 32;         // columns at a time
+    const int col0 = ((warp - 4) >> 2) * kCols;  // the warp's columns
     constexpr int kVecs = kTok * D / 8 / kStateThreads;  // 16-byte pieces of y a thread
+    constexpr int kRows = kStateThreads / 8;
     const bool mine = r < D;           // at d = 64 lanes 64.. repeat the rows
-    const uint32_t m_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColM + half * kCols;
+    const uint32_t m_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColM + col0;
     const uint32_t ds_tm = m_tm - kColM + kColDS;
-    // 32 columns of the state: after a tile, g times the one before it plus the
+    // kB columns of the state: after a tile, g times the one before it plus the
     // tile's products.
-    auto state_block = [&](int b, bool add, LinearDecay g, uint32_t (&v)[32]) {
-      tmem_ld32(m_tm + 32 * b, v);
+    auto state_block = [&](int b, bool add, LinearDecay g, uint32_t (&v)[kB]) {
+      tmem_ld(m_tm + kB * b, v);
       if (add) {
-        uint32_t ds[32];
-        tmem_ld32(ds_tm + 32 * b, ds);
+        uint32_t ds[kB];
+        tmem_ld(ds_tm + kB * b, ds);
         tmem_ld_wait();
-        reg_fence32(v);
-        reg_fence32(ds);
+        fence_regs(v);
+        fence_regs(ds);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < kB; e += 2) {
           const float2 m =
               g.join(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
                      make_float2(__uint_as_float(ds[e]), __uint_as_float(ds[e + 1])));
@@ -543,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         tmem_ld_wait();
-        reg_fence32(v);
+        fence_regs(v);
       }
     };
     // The state to its bf16 operand for x M^T and, if new, back into TMEM.
@@ -551,14 +610,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int sw = r & 7;
       asm volatile("" : "+r"(sw));  // not to be kept as eight addresses across the loop
 #pragma unroll
-      for (int b = 0; b < kCols / 32; ++b) {
-        uint32_t v[32];
+      for (int b = 0; b < kCols / kB; ++b) {
+        uint32_t v[kB];
         state_block(b, add, g, v);
         if (mine) {
-          const int col = half * kCols + 32 * b;
+          const int col = col0 + kB * b;
           uint8_t* line = smem + L::kMOff + (col >> 6) * L::kMAtom + r * 128;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < kB / 8; ++q) {
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -569,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        if (add) tmem_st32(m_tm + 32 * b, v);
+        if (add) tmem_st(m_tm + kB * b, v);
       }
       if (add) tmem_st_wait();
     };
@@ -588,19 +647,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ? p.cuts[op] + (size_t)(kRev ? part + 1 : part - 1) * D * D
                 : (p.init[op] ? p.init[op] + (size_t)po.bh * D * D : nullptr);
 #pragma unroll
-        for (int b = 0; b < kCols / 32; ++b) {
-          const int col = half * kCols + 32 * b;
-          uint32_t v[32];
+        for (int b = 0; b < kCols / kB; ++b) {
+          const int col = col0 + kB * b;
+          uint32_t v[kB];
           if (!src || !mine) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0u;
+            for (int e = 0; e < kB; ++e) v[e] = 0u;
           } else if (p.state_t[op]) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < kB; ++e)
               v[e] = __float_as_uint(src[(size_t)(col + e) * D + r]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < kB; e += 4) {
               const uint4 u = *reinterpret_cast<const uint4*>(src + (size_t)r * D + col + e);
               v[e] = u.x;
               v[e + 1] = u.y;
@@ -609,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          tmem_st32(m_tm + 32 * b, v);
+          tmem_st(m_tm + kB * b, v);
         }
         tmem_st_wait();
       }
@@ -623,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && ragged(tile, n)) {
           ok = mbar_wait_warp(&br.full_z[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
           if (!ok) break;
-          zero_rows<D>(ty, n, tid);
-          zero_rows<D>(smem + L::kZOff + st * L::kTile, n, tid);
+          zero_rows<D, kStateThreads>(ty, n, tid);
+          zero_rows<D, kStateThreads>(smem + L::kZOff + st * L::kTile, n, tid);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&br.fixed);
@@ -633,9 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // y, in registers while the last products run
         const uint4* from = reinterpret_cast<const uint4*>(ty) + tid;
         uint4* to = reinterpret_cast<uint4*>(smem + L::kWOff) + tid;
-        uint4 lo[kVecs];  // y, then what hi leaves of it
+        uint4 hi[kVecs];  // y, then its hi
 #pragma unroll
-        for (int q = 0; q < kVecs; ++q) lo[q] = from[kStateThreads * q];
+        for (int q = 0; q < kVecs; ++q) hi[q] = from[kStateThreads * q];
         __syncwarp();
         if (lane == 0) mbar_arrive(&br.empty_y);
         const LinearDecay g = linear_decay(ln, last_n);
@@ -644,30 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
         }
-        if (upd) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int j = (tid >> 3) + 32 * u;  // row of pieces u, u + 4
-            const float w = j >= n ? 0.f
-                                   : (kRev ? p.scale * linear_power(l2, j + 1)
-                                           : linear_power(l2, n - 1 - j));
-#pragma unroll
-            for (int q = u; q < kVecs; q += 4) {
-              uint4 hi;
-              split_vec(lo[q], w, hi, lo[q]);
-              to[kStateThreads * q] = hi;
-            }
-          }
-        }
         hand_over(wait_ds, g);
         last_n = n;
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (upd) mbar_arrive(&br.y_hi);
-          mbar_arrive(&br.m_op);
-        }
+        if (lane == 0) mbar_arrive(&br.m_op);
         wait_ds = upd;
         if (!upd) {
           // the operand's reader, before the next portion's: x M^T of this tile.
@@ -677,13 +718,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           continue;
         }
-        ok = mbar_wait_warp(&br.hi_done, (uint32_t)(ku++) & 1, abort_flag, p.status);
-        if (!ok) break;
+        ++ku;
+        // the smallest term first: the larger ones, added last, are cut off least
+        uint4 lo[kVecs];
+        auto write = [&](int off, const uint4 (&v)[kVecs]) {
+          uint4* dst = reinterpret_cast<uint4*>(smem + off) + tid;
 #pragma unroll
-        for (int q = 0; q < kVecs; ++q) to[kStateThreads * q] = lo[q];
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&br.y_lo);
+          for (int q = 0; q < kVecs; ++q) dst[kStateThreads * q] = v[q];
+        };
+        auto written = [&](uint64_t* bar) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+#pragma unroll
+        for (int u = 0; u < kTok / kRows; ++u) {
+          const int j = (tid >> 3) + kRows * u;  // row of pieces u, u + kTok / kRows
+          const float w = j >= n ? 0.f
+                                 : (kRev ? p.scale * linear_power(l2, j + 1)
+                                         : linear_power(l2, n - 1 - j));
+#pragma unroll
+          for (int q = u; q < kVecs; q += kTok / kRows) {
+            uint4 rest;
+            split_vec<kThree>(hi[q], w, hi[q], lo[q], rest);
+            to[kStateThreads * q] = kThree ? rest : lo[q];
+          }
+        }
+        if constexpr (L::kApart) {
+          if constexpr (kThree) write(L::kWOff + L::kTile, lo);
+          write(L::kLastOff, hi);
+          written(&br.first);
+        } else {
+          written(&br.first);
+          if constexpr (kThree) {
+            ok = mbar_wait_warp(&br.first_done, (uint32_t)(ku - 1) & 1, abort_flag, p.status);
+            if (!ok) break;
+            write(L::kWOff, lo);
+            written(&br.second);
+          }
+          // x M^T has read the state operand
+          ok = mbar_wait_warp(&br.empty_x[st], (uint32_t)(k / 2) & 1, abort_flag, p.status);
+          if (!ok) break;
+          write(L::kLastOff, hi);
+          written(&br.last);
+        }
       }
       if (ok && fin) {
         if (wait_ds) {
@@ -692,15 +770,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
         }
         const LinearDecay g = linear_decay(ln, last_n);
-        float* dst = final_state + ((size_t)po.bh * D + r) * D + half * kCols;
+        float* dst = final_state + ((size_t)po.bh * D + r) * D + col0;
 #pragma unroll
-        for (int b = 0; b < kCols / 32; ++b) {
-          uint32_t v[32];
+        for (int b = 0; b < kCols / kB; ++b) {
+          uint32_t v[kB];
           state_block(b, wait_ds, g, v);
           if (mine) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(dst + 32 * b + e) =
+            for (int e = 0; e < kB; e += 4)
+              *reinterpret_cast<uint4*>(dst + kB * b + e) =
                   make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
           __syncwarp();
@@ -712,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMMA) {
+  if (warp == R::kMMA) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -721,30 +799,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------ states at cuts --
 
 // Each run's own part of the head that its boundary cuts, y weighted by the
-// distance to the cut, so nothing is ever rescaled: a tile's products (hi and
-// lo, as above) go to one of two accumulators in TMEM and are added up in fp32
-// registers while the next tile's run.  hi replaces y, lo goes through one
-// buffer of its own.  The tiles are walked so that those the output kernel
+// distance to the cut, so nothing is ever rescaled: a tile's products (two or
+// three terms, as above) go to one of two accumulators in TMEM and are added up
+// in fp32 registers while the next tile's run.  The first term replaces y, the
+// second goes through one buffer of its own, the third replaces the first.  The tiles are walked so that those the output kernel
 // starts with come last: it then finds them in L2.  Bound: HBM (64 KB a tile at
 // d = 128).  B2 H16 T16384 d128: 45 us, 5.3 TB/s, 79 % of the copy bandwidth.
-constexpr int kSThreads = 320;  // 8 scaling warps, TMA, MMA
-constexpr int kSWarpTMA = 8, kSWarpMMA = 9;
+// With three terms shared memory (384 KB a tile) and the scaling warps: 62 us
+// with 8 of them, 56 with 16.
+template <bool kThree>
+struct StateRoles {
+  static constexpr int kScale = kThree ? 16 : 8;  // warps that scale y and sum products
+  static constexpr int kTMA = kScale, kMMA = kScale + 1;
+  static constexpr int kThreads = 32 * (kScale + 2);
+};
 
 template <int D>
 struct StateLayout {
   static constexpr int kNS = D == 128 ? 3 : 6;
   static constexpr int kTile = kTok * D * 2;
   static constexpr int kAtom = kTok * 128;
-  static constexpr int kStage = 2 * kTile;  // y (then hi), z
-  static constexpr int kLoOff = kNS * kStage;
-  static constexpr int kBarOff = kLoOff + kTile;
+  static constexpr int kStage = 2 * kTile;  // y (then terms of it), z
+  static constexpr int kWOff = kNS * kStage;
+  static constexpr int kBarOff = kWOff + kTile;
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
 struct StateBars {
-  uint64_t full[6], empty[6], hi[6];
-  uint64_t lo, lo_done;  // one phase a tile
+  uint64_t full[6], empty[6], first[6];
+  uint64_t second, sums;       // one phase a tile
+  uint64_t first_done, third;  // one phase a tile, with three terms
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -765,10 +850,11 @@ struct StateParams {
   int* status;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kSThreads, 1)
+template <int D, bool kThree>
+__global__ void __launch_bounds__(StateRoles<kThree>::kThreads, 1)
     polar_linear_state_tc_kernel(const __grid_constant__ StateMaps maps, const StateParams p) {
   using L = StateLayout<D>;
+  using R = StateRoles<kThree>;
   constexpr int NS = L::kNS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -791,15 +877,17 @@ __global__ void __launch_bounds__(kSThreads, 1)
     for (int i = 0; i < NS; ++i) {
       mbar_init(&br.full[i], 1);
       mbar_init(&br.empty[i], 1);
-      mbar_init(&br.hi[i], kStateWarps);
+      mbar_init(&br.first[i], R::kScale);
     }
-    mbar_init(&br.lo, kStateWarps);
-    mbar_init(&br.lo_done, 1);
+    mbar_init(&br.second, R::kScale);
+    mbar_init(&br.sums, 1);
+    mbar_init(&br.first_done, 1);
+    mbar_init(&br.third, R::kScale);
     mbar_init(&br.drain, 1);
     br.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kSWarpMMA) tmem_alloc(&br.tmem_base, 256);
+  if (warp == R::kMMA) tmem_alloc(&br.tmem_base, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -807,7 +895,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   volatile int* abort_flag = &br.abort_flag;
   auto tile_row = [&](int c) { return t0 + (reverse ? c : nt - 1 - c) * kTok; };
 
-  if (warp == kSWarpTMA) {
+  if (warp == R::kTMA) {
     if (lane == 0) {
       tma_prefetch_desc(&map_y);
       tma_prefetch_desc(&map_z);
@@ -836,29 +924,35 @@ __global__ void __launch_bounds__(kSThreads, 1)
                   kWaitLimitCycles / 4);
       __syncwarp();
     }
-  } else if (warp == kSWarpMMA) {
+  } else if (warp == R::kMMA) {
     constexpr uint32_t kId = idesc_bf16_f32(128, D, 1, 1);
     const uint64_t mn = smem_desc_sw128(smem_u32(smem), D == 128 ? L::kAtom : 0, 1024);
     auto at = [](uint32_t bytes) { return (uint64_t)(bytes >> 4); };
     bool ok = true, any = false;
     for (int c = 0; c < nt; ++c) {
       const int st = c % NS;
-      ok = mbar_wait_warp(&br.hi[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t y0 = mn + at(st * L::kStage), z0 = y0 + at(L::kTile), l0 = mn + at(L::kLoOff);
+      const uint64_t y0 = mn + at(st * L::kStage), z0 = y0 + at(L::kTile), w0 = mn + at(L::kWOff);
       const uint32_t acc = tmem + (c & 1) * 128;
+      auto products = [&](uint64_t term, bool add) {
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < kTok / 16; ++kk)
-        umma_ss_warp(acc, z0 + at(kk * 2048), y0 + at(kk * 2048), kId, kk > 0);
-      any = true;
-      ok = mbar_wait_warp(&br.lo, (uint32_t)c & 1, abort_flag, p.status);
+        for (int kk = 0; kk < kTok / 16; ++kk)
+          umma_ss_warp(acc, z0 + at(kk * 2048), term + at(kk * 2048), kId, add || kk > 0);
+      };
+      ok = mbar_wait_warp(&br.first[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
       if (!ok) break;
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < kTok / 16; ++kk)
-        umma_ss_warp(acc, z0 + at(kk * 2048), l0 + at(kk * 2048), kId, 1u);
-      umma_commit_warp(&br.lo_done);
+      products(y0, false);
+      any = true;
+      if constexpr (kThree) umma_commit_warp(&br.first_done);
+      ok = mbar_wait_warp(&br.second, (uint32_t)c & 1, abort_flag, p.status);
+      if (!ok) break;
+      products(w0, true);
+      if constexpr (kThree) {
+        ok = mbar_wait_warp(&br.third, (uint32_t)c & 1, abort_flag, p.status);
+        if (!ok) break;
+        products(y0, true);
+      }
+      umma_commit_warp(&br.sums);
       umma_commit_warp(&br.empty[st]);
     }
     if (!ok && any) {
@@ -870,24 +964,25 @@ __global__ void __launch_bounds__(kSThreads, 1)
     }
   } else {
     const int tid = threadIdx.x;
-    const int half = warp >> 2, r = threadIdx.x & 127;
-    constexpr int kCols = D / 2;
-    float sum[kCols];  // row r of the state, half of its columns
+    const int r = threadIdx.x & 127;
+    constexpr int kScaleThreads = 32 * R::kScale;
+    constexpr int kCols = 128 * D / kScaleThreads;
+    const int col = (warp >> 2) * kCols;
+    float sum[kCols];  // row r of the state, columns col ..
 #pragma unroll
     for (int e = 0; e < kCols; ++e) sum[e] = 0.f;
     // the products of tile c, once they are done
     auto collect = [&](int c) {
-      if (!mbar_wait_warp(&br.lo_done, (uint32_t)c & 1, abort_flag, p.status)) return false;
+      if (!mbar_wait_warp(&br.sums, (uint32_t)c & 1, abort_flag, p.status)) return false;
       tc_fence_after();
 #pragma unroll
-      for (int b = 0; b < kCols / 32; ++b) {
-        uint32_t v[32];
-        tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (c & 1) * 128 + half * kCols +
-                      32 * b, v);
+      for (int b = 0; b < kCols / 16; ++b) {
+        uint32_t v[16];
+        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (c & 1) * 128 + col + 16 * b, v);
         tmem_ld_wait();
-        reg_fence32(v);
+        reg_fence16(v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sum[32 * b + e] += __uint_as_float(v[e]);
+        for (int e = 0; e < 16; ++e) sum[16 * b + e] += __uint_as_float(v[e]);
       }
       tc_fence_before();
       return true;
@@ -898,40 +993,51 @@ __global__ void __launch_bounds__(kSThreads, 1)
       ok = mbar_wait_warp(&br.full[st], (uint32_t)(c / NS) & 1, abort_flag, p.status);
       if (!ok) break;
       uint8_t* ty = smem + st * L::kStage;
-      if (n < kTok) zero_rows<D>(ty + L::kTile, n, tid);
-      constexpr int kVecs = kTok * D / 8 / kStateThreads;
+      if (n < kTok) zero_rows<D, kScaleThreads>(ty + L::kTile, n, tid);
+      constexpr int kVecs = kTok * D / 8 / kScaleThreads;
+      constexpr int kRows = kScaleThreads / 8;  // rows of 64 columns that the warps take at once
       uint4* at = reinterpret_cast<uint4*>(ty) + tid;
-      uint4 lo[kVecs];  // y, then what hi leaves of it
+      uint4 hi[kVecs], lo[kVecs];  // y, then its terms
 #pragma unroll
-      for (int q = 0; q < kVecs; ++q) lo[q] = at[kStateThreads * q];
+      for (int q = 0; q < kVecs; ++q) hi[q] = at[kScaleThreads * q];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = (tid >> 3) + 32 * u, t = row + j;  // row of pieces u, u + 4
+      for (int u = 0; u < kTok / kRows; ++u) {
+        const int j = (tid >> 3) + kRows * u, t = row + j;  // row of pieces u, u + kTok / kRows
         const float w =
             p.scale[op] * linear_power(l2, reverse ? t - t0 + 1 : max(t1 - 1 - t, 0));
 #pragma unroll
-        for (int q = u; q < kVecs; q += 4) {
-          uint4 hi;
-          split_vec(lo[q], w, hi, lo[q]);
-          if (j >= n) hi = lo[q] = make_uint4(0u, 0u, 0u, 0u);
-          at[kStateThreads * q] = hi;
+        for (int q = u; q < kVecs; q += kTok / kRows) {
+          uint4 rest;
+          split_vec<kThree>(hi[q], w, hi[q], lo[q], rest);
+          if (j >= n) hi[q] = lo[q] = rest = make_uint4(0u, 0u, 0u, 0u);
+          at[kScaleThreads * q] = kThree ? rest : lo[q];
         }
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&br.hi[st]);
-      if (c > 0) ok = collect(c - 1);  // lo is free then, too
-      if (!ok) break;
-      uint4* to = reinterpret_cast<uint4*>(smem + L::kLoOff) + tid;
+      auto write = [&](uint4* to, const uint4 (&v)[kVecs], uint64_t* bar) {
 #pragma unroll
-      for (int q = 0; q < kVecs; ++q) to[kStateThreads * q] = lo[q];
+        for (int q = 0; q < kVecs; ++q) to[kScaleThreads * q] = v[q];
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      };
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&br.lo);
+      if (lane == 0) mbar_arrive(&br.first[st]);
+      if (c > 0) ok = collect(c - 1);  // the buffer of the second term is free then, too
+      if (!ok) break;
+      uint4* to = reinterpret_cast<uint4*>(smem + L::kWOff) + tid;
+      if constexpr (kThree) {
+        write(to, lo, &br.second);
+        ok = mbar_wait_warp(&br.first_done, (uint32_t)c & 1, abort_flag, p.status);
+        if (!ok) break;
+        write(at, hi, &br.third);
+      } else {
+        write(to, hi, &br.second);
+      }
     }
     if (ok && nt > 0) ok = collect(nt - 1);
     if (ok && r < D) {
-      float* dst = p.cuts[op] + ((size_t)blockIdx.x * D + r) * D + half * kCols;
+      float* dst = p.cuts[op] + ((size_t)blockIdx.x * D + r) * D + col;
 #pragma unroll
       for (int e = 0; e < kCols; e += 4)
         *reinterpret_cast<float4*>(dst + e) =
@@ -941,7 +1047,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kSWarpMMA) {
+  if (warp == R::kMMA) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
@@ -949,8 +1055,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
 // n applications (1 or 2) that differ in tensors and states only; maps: x, y,
 // z, out of each.
-template <int D, bool kRev>
-cudaError_t out_tc_d(const LinearArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
+template <int D, bool kRev, bool kThree>
+cudaError_t out_tc_t(const LinearArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
   using L = OutLayout<D>;
   OutMaps m;
   OutParams p;
@@ -972,16 +1078,21 @@ cudaError_t out_tc_d(const LinearArgs* a, int n, const CUtensorMap* maps, cudaSt
   p.split = a->split;
   p.scale = a->scale;
   p.status = a->status;
-  auto kern = polar_linear_out_tc_kernel<D, kRev>;
+  auto kern = polar_linear_out_tc_kernel<D, kRev, kThree>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAsked);
   if (e != cudaSuccess) return e;
-  return linear_launch(kern, dim3((unsigned)a->split.parts * n), kThreads, L::kAsked, s,
+  return linear_launch(kern, dim3((unsigned)a->split.parts * n), OutRoles<kThree>::kThreads, L::kAsked, s,
                        a->chained, m, p);
 }
 
-template <int D>
-cudaError_t state_tc_d(const LinearStateArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
+template <int D, bool kRev>
+cudaError_t out_tc_d(const LinearArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
+  return a->exact ? out_tc_t<D, kRev, true>(a, n, maps, s) : out_tc_t<D, kRev, false>(a, n, maps, s);
+}
+
+template <int D, bool kThree>
+cudaError_t state_tc_t(const LinearStateArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
   using L = StateLayout<D>;
   StateMaps m;
   StateParams p;
@@ -1000,13 +1111,22 @@ cudaError_t state_tc_d(const LinearStateArgs* a, int n, const CUtensorMap* maps,
   p.T = a->T;
   p.split = a->split;
   p.status = a->status;
-  cudaError_t e = cudaFuncSetAttribute(polar_linear_state_tc_kernel<D>,
+  cudaError_t e = cudaFuncSetAttribute(polar_linear_state_tc_kernel<D, kThree>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kSmemBytes);
   if (e != cudaSuccess) return e;
-  polar_linear_state_tc_kernel<D>
-      <<<dim3((unsigned)a->split.parts, n), kSThreads, L::kSmemBytes, s>>>(m, p);
+  polar_linear_state_tc_kernel<D, kThree>
+      <<<dim3((unsigned)a->split.parts, n), StateRoles<kThree>::kThreads, L::kSmemBytes, s>>>(m, p);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t state_tc_d(const LinearStateArgs* a, int n, const CUtensorMap* maps, cudaStream_t s) {
+  if (n == 2 && a[0].exact != a[1].exact) {
+    const cudaError_t e = state_tc_d<D>(a, 1, maps, s);
+    return e != cudaSuccess ? e : state_tc_d<D>(a + 1, 1, maps + 2, s);
+  }
+  return a->exact ? state_tc_t<D, true>(a, n, maps, s) : state_tc_t<D, false>(a, n, maps, s);
 }
 
 }  // namespace

@@ -72,3 +72,32 @@ def test_single_tokens(dtype):
         ref = exact(v[:, 0, h], k[:, 0, h], ld[h], first=False)
         worst = max(worst, float((S[0, h].double() - ref).norm() / ref.norm()))
     assert worst <= tol, (worst, tol)
+
+
+@pytest.mark.parametrize("signs", ["positive", "both"])
+@pytest.mark.parametrize("H,T,d", [(152, 16384, 64), (76, 8192, 128), (3, 65536, 128),
+                                   (300, 700, 64)])
+def test_prompt_of_bf16(H, T, d, signs):
+    """bf16 inputs are exact, but weighted by a power of the decay they are
+    not: they enter as three bf16 terms, 2^-25 of them and less is left out
+    (two terms would leave up to 2^-17, 2^-18.7 rms: 40 u).  The tensor core
+    cuts off what it adds, less than 2 u of the sum so far, in the eight steps
+    of a tile's largest term: 9 u.  A state is joined once a tile, C = T / 128
+    times: twice sqrt(C / 3) / sqrt 3.  Powers of the decay, by the bounds
+    above: exp2f 2, exponents 2, the state's decay 3."""
+    import long_context_attention_causal_gb300 as pa
+    gen = torch.Generator(device=dev()).manual_seed(160 + d + T)
+    q, k, v, g = (torch.randn((1, H, T, d), generator=gen, device=dev()).bfloat16()
+                  for _ in range(4))
+    if signs == "positive":
+        q, k, v, g = (t.abs() for t in (q, k, v, g))
+    ld = decays(H)
+    state = pa.linear_fwd(q, k, v, ld, want_state=True)[1]
+    dstate = pa.linear_bwd(q, k, v, ld, g, scale=1.0, want_dstate=True)[3]
+    tol = (2 * math.sqrt(T / 128 / 3) / math.sqrt(3) + 9 + 7) * U
+    worst = [0.0, 0.0]
+    for h in sorted({*range(0, H, max(1, H // 24)), H - 1}):
+        for i, (got, z, y) in enumerate(((state, v, k), (dstate, g, q))):
+            ref = exact(z[0, h], y[0, h], ld[h], first=i == 1)
+            worst[i] = max(worst[i], float((got[0, h].double() - ref).norm() / ref.norm()))
+    assert max(worst) <= tol, (worst, tol)

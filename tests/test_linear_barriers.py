@@ -22,7 +22,7 @@ import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SOURCE = os.path.join(ROOT, "long_context_attention_causal_gb300", "csrc", "polar_linear_tc.cu")
-STATE_WARPS, OUT_WARPS = 8, 4
+OUT_WARPS = 4
 
 
 def staged_barriers():
@@ -94,8 +94,13 @@ def check(roles, counts):
             assert m.step(held), f"{held} stands still at {roles[held][m.at[held]]}"
 
 
-def out_roles(portions, staged):
-    """portions: [(tiles, final state wanted, rows to zero in these tiles)]."""
+def state_warps(terms):
+    return 16 if terms == 3 else 8
+
+
+def out_roles(portions, staged, terms, apart):
+    """portions: [(tiles, final state wanted, rows to zero in these tiles)];
+    terms: of scaled y; apart: each has a buffer of its own."""
     tma, mma, store, out, state = [], [], [], [], []
 
     def two(bar, k):
@@ -127,16 +132,18 @@ def out_roles(portions, staged):
             if c in ragged:
                 add(mma, "wait", one("fixed", kf))
             add(mma, "arrive", one("s_full", k), one("empty_y", k))
-            add(mma, "wait", two("full_z", k))
-            if upd:
-                add(mma, "wait", one("y_hi", ku))
-                add(mma, "arrive", one("hi_done", ku))
             add(mma, "wait", one("m_op", k))
             if k > 0:
                 add(mma, "wait", one("o_free", k - 1))
             add(mma, "arrive", two("empty_x", k))
+            add(mma, "wait", two("full_z", k))
             if upd:
-                add(mma, "wait", one("y_lo", ku))
+                add(mma, "wait", one("first", ku))
+                if not apart:
+                    if terms == 3:
+                        add(mma, "arrive", one("first_done", ku))
+                        add(mma, "wait", one("second", ku))
+                    add(mma, "wait", one("last", ku))
                 add(mma, "arrive", one("ds_full", ku))
             add(mma, "wait", one("p_full", k))
             add(mma, "arrive", one("o_full", k))
@@ -158,13 +165,16 @@ def out_roles(portions, staged):
             add(state, "arrive", one("empty_y", k))
             if wait_ds:
                 add(state, "wait", one("ds_full", ku - 1))
-            if upd:
-                add(state, "arrive", one("y_hi", ku))
             add(state, "arrive", one("m_op", k))
             if upd:
-                add(state, "wait", one("hi_done", ku))
+                add(state, "arrive", one("first", ku))
+                if not apart:
+                    if terms == 3:
+                        add(state, "wait", one("first_done", ku))
+                        add(state, "arrive", one("second", ku))
+                    add(state, "wait", two("empty_x", k))
+                    add(state, "arrive", one("last", ku))
                 ku += 1
-                add(state, "arrive", one("y_lo", ku - 1))
             else:
                 add(state, "wait", two("empty_x", k))
             wait_ds = upd
@@ -173,16 +183,16 @@ def out_roles(portions, staged):
             add(state, "wait", one("ds_full", ku - 1))
     roles = {"tma": tma, "mma": mma, "store": store}
     roles.update({f"out{i}": out for i in range(OUT_WARPS)})
-    roles.update({f"state{i}": state for i in range(STATE_WARPS)})
-    counts = dict.fromkeys("full_x full_z empty_x empty_z full_y s_full o_full hi_done ds_full"
+    roles.update({f"state{i}": state for i in range(state_warps(terms))})
+    counts = dict.fromkeys("full_x full_z empty_x empty_z full_y s_full o_full ds_full first_done"
                            .split(), 1)
     counts.update(dict.fromkeys("p_full o_free staged".split(), OUT_WARPS))
-    counts.update(dict.fromkeys("m_op y_hi y_lo fixed".split(), STATE_WARPS))
-    counts["empty_y"] = 1 + STATE_WARPS
+    counts.update(dict.fromkeys("m_op first second last fixed".split(), state_warps(terms)))
+    counts["empty_y"] = 1 + state_warps(terms)
     return roles, counts
 
 
-def state_roles(tiles, stages):
+def state_roles(tiles, stages, terms):
     tma, mma, work = [], [], []
 
     def ring(bar, c):
@@ -192,16 +202,25 @@ def state_roles(tiles, stages):
         if c >= stages:
             tma.append(("wait", *ring("empty", c - stages)))
         tma.append(("arrive", *ring("full", c)))
-        mma += [("wait", *ring("hi", c)), ("wait", ("lo",), c), ("arrive", ("lo_done",), c),
-                ("arrive", *ring("empty", c))]
-        work += [("wait", *ring("full", c)), ("arrive", *ring("hi", c))]
+        mma.append(("wait", *ring("first", c)))
+        if terms == 3:
+            mma.append(("arrive", ("first_done",), c))
+        mma.append(("wait", ("second",), c))
+        if terms == 3:
+            mma.append(("wait", ("third",), c))
+        mma += [("arrive", ("sums",), c), ("arrive", *ring("empty", c))]
+        work += [("wait", *ring("full", c)), ("arrive", *ring("first", c))]
         if c:
-            work.append(("wait", ("lo_done",), c - 1))
-        work.append(("arrive", ("lo",), c))
+            work.append(("wait", ("sums",), c - 1))
+        work.append(("arrive", ("second",), c))
+        if terms == 3:
+            work += [("wait", ("first_done",), c), ("arrive", ("third",), c)]
     if tiles:
-        work.append(("wait", ("lo_done",), tiles - 1))
-    roles = {"tma": tma, "mma": mma, **{f"work{i}": work for i in range(STATE_WARPS)}}
-    return roles, {"full": 1, "empty": 1, "hi": STATE_WARPS, "lo": STATE_WARPS, "lo_done": 1}
+        work.append(("wait", ("sums",), tiles - 1))
+    roles = {"tma": tma, "mma": mma, **{f"work{i}": work for i in range(state_warps(terms))}}
+    counts = dict.fromkeys("full empty sums first_done".split(), 1)
+    counts.update(dict.fromkeys("first second third".split(), state_warps(terms)))
+    return roles, counts
 
 
 def walks():
@@ -216,17 +235,20 @@ def walks():
                 (n - 1,) if n and rng.random() < 0.5 else ()) for _ in range(rng.randint(1, 6))]
 
 
-def test_output_kernel():
+@pytest.mark.parametrize("terms", [2, 3])
+@pytest.mark.parametrize("apart", [False, True])
+def test_output_kernel(terms, apart):
     for portions in walks():
-        check(*out_roles(portions, staged_barriers()))
+        check(*out_roles(portions, staged_barriers(), terms, apart))
 
 
 def test_one_staged_barrier_would_not_do():
     with pytest.raises(Hazard, match="store waits"):
-        check(*out_roles([(9, False, ())], 1))
+        check(*out_roles([(9, False, ())], 1, 2, False))
 
 
 @pytest.mark.parametrize("stages", [3, 6])
-def test_state_kernel(stages):
+@pytest.mark.parametrize("terms", [2, 3])
+def test_state_kernel(stages, terms):
     for tiles in (0, 1, 2, 3, 7, 20):
-        check(*state_roles(tiles, stages))
+        check(*state_roles(tiles, stages, terms))
