@@ -210,9 +210,10 @@ int polar_attn_combine(const float* partials, int num_splits, const void* q,
  * page_size (it sizes the splits).  Key j of sequence b is row j % page_size
  * of page block_table[b][j / page_size]; n = seq_lens[b] per sequence.
  * A page index outside [0, num_pages) is not read (its keys are skipped) and
- * a length outside [1, max_seq_len] is clamped on the device; either records
- * status 3 in polar_attn_device_status and leaves that row's result
- * meaningless (a row with no visible key returns out = mem, n_eff = conf = 0).
+ * a length below 1 or past max_seq_len, counted up to the whole pages of the
+ * splits, is clamped on the device; either records status 3 in
+ * polar_attn_device_status and leaves that row's result meaningless (a row
+ * with no visible key returns out = mem, n_eff = conf = 0).
  * workspace: at least polar_attn_decode_paged_workspace_bytes(...) bytes;
  * num_splits = 0 chooses automatically.  Launches the paged split kernel
  * and the combine kernel on `stream`.  B = 0 is a no-op.  bf16 pools of
@@ -410,10 +411,12 @@ size_t polar_linear_bwd_workspace_bytes(int B, int H, int T, int d, int dtype);
  *             softmax weights of the decode; rows on page indices outside
  *             the pool get none).  The caller zeroes a row's entry when it
  *             appends the row.
- * Other arguments and results as polar_attn_decode_paged; every entry is
- * added to by one thread, so results do not depend on timing.  workspace: at
- * least polar_attn_decode_paged_weights_workspace_bytes(...) bytes (the
- * split records and one fp32 logit per query head and cache row).
+ * Other arguments and results as polar_attn_decode_paged, but a length past
+ * max_seq_len is cut to max_seq_len itself, so that the rows of the softmax
+ * are those that get weights.  Every entry is added to by one thread, so
+ * results do not depend on timing.  workspace: at least
+ * polar_attn_decode_paged_weights_workspace_bytes(...) bytes (the split
+ * records and one fp32 logit per query head and cache row).
  * num_splits = 0: polar_attn_decode_paged_weights_num_splits, which cuts few
  * heads into more splits than polar_attn_decode_paged does.
  */

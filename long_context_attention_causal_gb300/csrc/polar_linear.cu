@@ -14,12 +14,13 @@
 //   out_i = c sum_{j >= i} g^(j-i) (x_i . y_j) z_j + g^(n-1-i) M x_i
 //   M'    = g^n M + c sum_j g^(j+1) z_j y_j^T
 //
-// fp32 tensors: dot products of 24-bit values have no exact form on the tensor
-// cores, so chunks of 64 tokens run on packed fp32 fma.  Bound: those and the
-// shared memory reads that feed them (32 heads of 16384 tokens, d = 128: 1.65
-// ms, 38 TFLOP/s without the masked products, half of the FP32 pipes' nominal
-// rate).  Each CTA holds 64 or 32 rows of the state: a head then spreads
-// over as many CTAs, whose scores are computed as often.
+// fp32 tensors: the tensor cores take 24-bit values only as sums of shorter
+// terms, six products for one; chunks of 64 tokens run on packed fp32 fma
+// instead.  Bound: those and the shared memory reads that feed them (32 heads
+// of 16384 tokens, d = 128: 1.66 ms, 38 TFLOP/s without the masked products,
+// half of the FP32 pipes' nominal rate).  Each CTA holds 64 or 32 rows of the
+// state: a head then spreads over as many CTAs, whose scores are computed as
+// often.
 //
 // The 128-token tiles of all heads are dealt out to the CTAs in equal runs, so
 // that few heads still fill the GPU.  A head that a run boundary cuts needs
@@ -483,7 +484,7 @@ constexpr int kStepRows = 8;   // state rows per warp
 constexpr int kStepWarps = 4;
 
 // One token: the state is read and written once, which is all of the time
-// (256 sequences of 16 heads, d = 128: 82 us, 6.6 TB/s, 98 % of the copy
+// (256 sequences of 16 heads, d = 128: 82 us, 6.6 TB/s, 97 % of the copy
 // bandwidth).  Rows are independent, so a head's rows are spread over d / 32
 // CTAs: the smallest calls then use several SMs a head (16 heads, d = 64: 3 us).
 template <int D, typename T>

@@ -19,8 +19,9 @@ namespace {
 // cut heads: y and z of what lies before a cut are read a second time, and a
 // state and a scan launch come first.  The cheaper of the two is taken.  In
 // tiles of an SM's time, equal runs of `even` tiles cost about 1.6 even + 5 for
-// bf16 (d = 128, whole / cut: 64 heads of 2048 tokens 55 / 65 us, 100 of 2048
-// 57 / 85, 200 of 4096 191 / 220, 160 of 8192 358 / 333, 32 of 16384 354 / 159).
+// bf16 (d = 128, states of two terms, whole / cut: 64 heads of 2048 tokens 55 /
+// 65 us, 100 of 2048 57 / 85, 200 of 4096 191 / 220, 160 of 8192 358 / 333, 32 of
+// 16384 354 / 159).
 // fp32 tiles take longer than the launches do: about 1.05 even + 0.9 (d = 64,
 // whole / cut: 2 heads of 256 tokens 29 / 26 us, 8 of 512 47 / 26, 76 of 1024 90
 // / 95, 24 of 2048 172 / 75, 64 of 4096 338 / 290, 200 of 2048 444 / 400; d =
@@ -286,8 +287,8 @@ int polar_linear_bwd(const void* q, const void* k, const void* v, const float* l
   }
   // dk and dv share a launch where they share their terms.  dk needs no more
   // than two, and the two launches that follow from that take less time (B2 H16
-  // T16384 d128: 427 us, 444 in one), unless one leaves half of the SMs idle (B8
-  // H8 T1111 d64: 84, 59 in one).
+  // T16384 d128: 424 us, 444 in one), unless one leaves half of the SMs idle (B8
+  // H8 T1111 d64: 84, 55 in one).
   const float* r_init = copy ? copy : dstate_out;
   LinearArgs a[3] = {{dmem, v, k, dq, log_decay, lengths, B, H, T, d, scale, false, true,
                       g, state_in, cuts_s, nullptr, status, false, g.cut},

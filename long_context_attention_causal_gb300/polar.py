@@ -678,7 +678,9 @@ def decode_paged_weights(q, k_pages, v_pages, block_table, seq_lens, mem, w_coun
     """decode_paged that also adds every cache row's attention weight, summed
     over the query heads of its group, to weights [B, Hkv, stride] fp32
     (stride >= max_seq_len).  max_seq_len defaults to the smaller of the
-    table's capacity and the stride.  Returns (out, n_eff, conf)."""
+    table's capacity and the stride; the workspace holds one fp32 value per
+    query head and row up to it, so with a generous table give the longest
+    length.  Returns (out, n_eff, conf)."""
     for name, t in (("q", q), ("k_pages", k_pages), ("block_table", block_table),
                     ("weights", weights)):
         _dev(_need(t, name), name)
