@@ -118,7 +118,8 @@ struct OutParams {
   int* status;
 };
 
-// Generic-proxy shared-memory writes made visible to TMA and the tensor core.
+// Generic-proxy accesses of shared memory come before what TMA and the tensor
+// core do after it: writes are visible to them, reads are over.
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -695,6 +696,10 @@ __global__ void __launch_bounds__(OutRoles<kThree>::kThreads, 1)
         uint4 hi[kVecs];  // y, then its hi
 #pragma unroll
         for (int q = 0; q < kVecs; ++q) hi[q] = from[kStateThreads * q];
+        // Nothing uses y yet, so the loads may still be on their way, behind
+        // slower accesses of the SM, when the arrival is seen and TMA writes the
+        // next y over this one: they have to be over first.
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&br.empty_y);
         const LinearDecay g = linear_decay(ln, last_n);
