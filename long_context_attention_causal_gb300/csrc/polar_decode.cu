@@ -609,6 +609,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             }
           }
         }
+        // the stored logits go through the same queue as the reads of V, which
+        // have to be over before the stage is copied over
+        if constexpr (kLogits) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[slot]);
       }
@@ -696,6 +699,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             }
           }
         }
+        // the stored logits go through the same queue as the reads of V, which
+        // have to be over before the stage is copied over
+        if constexpr (kLogits) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[slot]);
       }
