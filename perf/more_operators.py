@@ -16,9 +16,10 @@ long_context_attention_causal_gb300.
 The 4-bit cache: pages [num_pages, Hkv, page, 9 d / 16] of bytes.  The block
 of a (page, head) holds page * d / 2 bytes of codes, row after row, then page *
 d / 32 bf16 scales, row after row.  32 consecutive channels share a scale s =
-bf16(max |x| / 7); a code is n + 8 with n = round(x / s), -7 <= n <= 7.  Eight
-codes make a 32-bit word (channel 8 w + j in bits 4 j ..), and word w = 4 i + c
-(i < d / 32, c < 4) of a row stands in place c * d / 32 + i.
+bf16(max |x| / 7); a code is n = round(x / s), -7 <= n <= 7, as a sign and
+three bits.  Channels 4 p + j, j < 4, make 16 bits: signs in bits 15, 11, 7, 3,
+|n| from bits 4, 0, 12, 8 on.  Two of them make a 32-bit word, and word w = 4 i
++ c (i < d / 32, c < 4) of a row stands in place c * d / 32 + i.
 """
 import math
 
@@ -29,6 +30,7 @@ own = False
 DEV = "cuda"
 LOG_T0 = math.log(2048.0)  # neutral length of the temperature, and kappa
 GROUP = 32  # channels that share a scale
+SIGN_AT, SIZE_AT = (15, 11, 7, 3), (4, 0, 12, 8)  # bits of a code in its 16
 
 
 # ------------------------------------------------------------------ cases --
@@ -248,13 +250,18 @@ def _quantise(x):
     return n.flatten(-2).to(torch.int32), s
 
 
+def _bits(at):
+    return torch.tensor(at, dtype=torch.int32, device=DEV)
+
+
 def _pack(n, s):
     """Page blocks of codes and scales [..., page, :]."""
-    c = (n + 8).to(torch.uint8).unflatten(-1, (-1, 2))
-    c = c[..., 0] | (c[..., 1] << 4)  # [..., page, d / 2], channels in order
+    n = n.unflatten(-1, (-1, 4))
+    c = (((n < 0).int() << _bits(SIGN_AT)) + (n.abs() << _bits(SIZE_AT))).sum(-1)  # [..., d / 4]
+    c = torch.stack([c & 255, c >> 8], -1).to(torch.uint8).flatten(-2)
     c = c.unflatten(-1, (-1, 4, 4)).transpose(-2, -3).flatten(-4)
     s = s.contiguous().view(torch.uint8).flatten(-2)
-    return torch.cat([c, s], -1).unflatten(-1, (n.shape[-2], -1))
+    return torch.cat([c, s], -1).unflatten(-1, (n.shape[-3], -1))
 
 
 def _unpack(pages, d):
@@ -262,11 +269,12 @@ def _unpack(pages, d):
     page = pages.shape[-2]
     flat = pages.flatten(-2)
     c = flat[..., :page * d // 2].unflatten(-1, (page, 4, d // GROUP, 4))
-    c = c.transpose(-2, -3).flatten(-3)
-    n = torch.stack([c & 15, c >> 4], -1).flatten(-2).float() - 8.0
+    c = c.transpose(-2, -3).reshape(*flat.shape[:-1], page, -1, 2).int()
+    c = (c[..., 0] + (c[..., 1] << 8))[..., None]
+    n = ((c >> _bits(SIZE_AT)) & 7) * (1 - 2 * ((c >> _bits(SIGN_AT)) & 1))
     s = flat[..., page * d // 2:].contiguous().view(torch.bfloat16).float()
     s = s.unflatten(-1, (page, d // GROUP, 1))
-    return (n.unflatten(-1, (-1, GROUP)) * s).flatten(-2)
+    return (n.flatten(-2).float().unflatten(-1, (-1, GROUP)) * s).flatten(-2)
 
 
 def _run_pages(st):
@@ -590,13 +598,15 @@ def _exact_values(pages, d):
     P, H, page, _ = pages.shape
     raw = pages.reshape(P, H, -1)
     row, ch = torch.arange(page, device=DEV)[:, None], torch.arange(d, device=DEV)[None, :]
-    word, part = (ch // 8) % 4 * (d // 32) + ch // 32, ch % 8
-    byte = raw[:, :, row * (d // 2) + 4 * word + part // 2].int()
-    n = (byte >> (4 * (part % 2)).int()) & 15
+    word = (ch // 8) % 4 * (d // 32) + ch // 32
+    at = row * (d // 2) + 4 * word + 2 * (ch // 4 % 2)
+    code = raw[:, :, at].int() + 256 * raw[:, :, at + 1].int()
+    sign = torch.where((code << (4 * (ch % 4)).int()) & 0x8000 != 0, -1, 1)
+    n = sign * torch.where(ch % 4 < 2, code << (4 * (ch % 4)).int() >> 4, code >> (20 - 4 * (ch % 4)).int()).bitwise_and(7)
     lo = page * (d // 2) + 2 * (row * (d // 32) + ch // 32)
     bits = raw[:, :, lo].int() + 256 * raw[:, :, lo + 1].int()
     s = (bits << 16).view(torch.float32).double()
-    return (s * (n - 8).double()).transpose(0, 1).reshape(H, P * page, d)
+    return (s * n.double()).transpose(0, 1).reshape(H, P * page, d)
 
 
 def _exact_decode(st, case):
