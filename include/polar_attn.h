@@ -465,6 +465,125 @@ int polar_cache_evict(void* k_pages, void* v_pages, const int* block_table,
                       void* workspace, size_t workspace_bytes, void* stream);
 size_t polar_cache_evict_workspace_bytes(int B, int Hkv, int max_seq_len, int keep);
 
+/*
+ * Pages of a paged cache, handed out and taken back on the device.  (No
+ * counterpart on the pages.)  The free pages are a stack: free_pages
+ * [free_capacity] int32, *free_count of them in use, the top the last.  All
+ * arrays are int32 on the device; B, the tables and the stack may be captured
+ * in a CUDA graph whose replays go on from one another.
+ * polar_pages_extend gives every sequence pages for its new tokens:
+ *   block_table : [B, max_pages], entries of the new pages written
+ *   seq_lens    : [B] rows held, in [0, max_pages * page_size]
+ *   new_tokens  : [B] rows to add, >= 0
+ *   lens_out    : [B] (written) the new lengths; may be seq_lens
+ *   count_out   : [1] (written) pages left; may be free_count
+ *   cu_seqlens  : [B + 1] (written) packed offsets, prefix sums of new_tokens
+ *   positions   : [max_tokens] (written) position of each packed new token
+ *   slots       : [max_tokens] (written) its cache row, page * page_size + row
+ * Sequences take pages off the top in order.  A sequence that needs pages gets
+ * them, and all its tokens, only if its need and those of all sequences before
+ * it fit the stack; otherwise its length stays and its tokens have slot -1 and
+ * position 0, as entries past the last token have.  So has, with status 3 in
+ * polar_attn_device_status, a sequence with a length or count out of bounds or
+ * with tokens past its table's row or past max_tokens (cu_seqlens is cut to
+ * max_tokens; such a sequence needs no pages), and a token whose page's number
+ * is outside [0, num_pages).
+ * polar_pages_release takes back the pages past the first keep_lens[b] rows of
+ * each sequence (0: all of an ended one; polar_cache_evict's new_lens: those
+ * that the eviction emptied), pushed in the order of sequences and pages:
+ *   keep_lens   : [B], in [0, seq_lens[b]]; lens_out = keep_lens
+ * The table keeps its entries.  An entry outside [0, num_pages) is pushed as
+ * -1, pages past free_capacity are dropped, a sequence with a length or
+ * keep_lens out of bounds is left as it is; each records status 3.
+ * page_size: a power of two in [8, 1024]; num_pages * page_size and max_pages *
+ * page_size below 2^31.  workspace: polar_pages_workspace_bytes(B) bytes,
+ * 16-byte aligned.  Written arrays must not overlap others of the call.
+ */
+int polar_pages_extend(int* block_table, const int* seq_lens, const int* new_tokens,
+                       const int* free_pages, const int* free_count, int* lens_out,
+                       int* count_out, int* cu_seqlens, int* positions, int* slots, int B,
+                       int max_pages, int page_size, int num_pages, int free_capacity,
+                       int max_tokens, void* workspace, size_t workspace_bytes, void* stream);
+int polar_pages_release(const int* block_table, const int* seq_lens, const int* keep_lens,
+                        int* free_pages, const int* free_count, int* lens_out, int* count_out,
+                        int B, int max_pages, int page_size, int num_pages, int free_capacity,
+                        void* workspace, size_t workspace_bytes, void* stream);
+size_t polar_pages_workspace_bytes(int B);
+
+/*
+ * Rotary positions of packed q and k.  (No counterpart on the pages.)  Pair i
+ * < rot / 2 of every head's first `rot` channels is turned by the angle
+ * positions[t] * inv_freq[i] and scaled:
+ *   y_a = scale (x_a cos - x_b sin),  y_b = scale (x_b cos + x_a sin)
+ * interleaved 0: (a, b) = (i, i + rot / 2); 1: (2 i, 2 i + 1).  inverse 1 turns
+ * the other way (same scale): the gradient of q and k from those of q_out and
+ * k_out.  Channels from rot on are copied.
+ *   q, q_out  : [N, Hq, d] of dtype, tokens q_stride, q_out_stride elements
+ *               apart (>= Hq * d), heads contiguous; q_out may be q
+ *   k, k_out  : [N, Hkv, d], as q.  Hq or Hkv may be 0 (then the pointers may
+ *               be NULL).
+ *   positions : [N] int32, any value
+ *   inv_freq  : [rot / 2] fp64, device: radians a token (8-byte aligned)
+ *   rot       : even, 2 .. d
+ * Angles are exact to 2^-32 of a turn at any position (for the given
+ * frequencies up to 2^-53 of their own size).  A rot that is a multiple of 16
+ * (bf16) or 8 (fp32) and strides that are multiples of 16 bytes take 16-byte
+ * accesses.  Other overlaps of an output with a tensor of the call are refused.
+ */
+int polar_rope(const void* q, const void* k, const int* positions, const double* inv_freq,
+               void* q_out, void* k_out, long long q_stride, long long k_stride,
+               long long q_out_stride, long long k_out_stride, int N, int Hq, int Hkv, int d,
+               int rot, int dtype, int interleaved, int inverse, float scale, void* stream);
+
+/*
+ * A paged cache in 4 bits.  (No counterpart on the pages.)  32 consecutive
+ * channels of a row share a bf16 scale s = max |x| / 7, and hold x / s rounded
+ * to nearest (ties to even), -7 .. 7, as a sign and three bits: 4.5 bits a
+ * value, an error of at most s / 2 (and of the scale's rounding, which the codes
+ * allow for).  A group with an infinity or NaN reads as NaN.
+ *   k_pages, v_pages : [num_pages, Hkv, page_size, 9 d / 16] bytes, 16-byte
+ *       aligned.  The block of a (page, head): page_size * d / 2 bytes of codes,
+ *       row after row, then page_size * d / 32 scales, row after row.  In a row's
+ *       codes, channels 4 p + j (j < 4) make 16 bits, signs in bits 15, 11, 7, 3,
+ *       sizes from bits 4, 0, 12, 8 on; channels 8 w .. 8 w + 7 make the 32-bit
+ *       word w, and word 4 i + c (c < 4) stands in place c * d / 32 + i.
+ *   slots : [N] int32, device: row page * page_size + offset of each token, as
+ *       polar_pages_extend gives; a negative slot has no row, one past the pool
+ *       has none either and records status 3 in polar_attn_device_status
+ * polar_cache_append_q4 writes rows: k, v [N, Hkv, d] of dtype, tokens k_stride,
+ * v_stride elements apart (>= Hkv * d, multiples of 16 bytes).  A slot may be
+ * named once in a call (a row named twice holds a mixture).
+ * polar_cache_read_q4 gives rows back: k, v [N, Hkv, d] of dtype (contiguous;
+ * zeros for tokens without a row; s n is exact in fp32).
+ * page_size as in polar_attn_decode_paged; num_pages * page_size below 2^31.
+ * Outputs must not overlap inputs.
+ */
+int polar_cache_append_q4(const void* k, const void* v, const int* slots, void* k_pages,
+                          void* v_pages, long long k_stride, long long v_stride, int N, int Hkv,
+                          int d, int page_size, int num_pages, int dtype, void* stream);
+int polar_cache_read_q4(const void* k_pages, const void* v_pages, const int* slots, void* k,
+                        void* v, int N, int Hkv, int d, int page_size, int num_pages, int dtype,
+                        void* stream);
+
+/*
+ * polar_attn_decode_paged over a 4-bit cache: k_pages and v_pages as above,
+ * dtype the type of q, mem and out, other arguments and results as there, but
+ * a length past max_seq_len is cut to max_seq_len itself.  bf16 q: the weights
+ * times V's scales are rounded to bf16, sums are fp32.  fp32 q: q and those
+ * weights are taken to 24 bits.  Rows whose scales are in [2^-50, 2^50] and q
+ * below 2^60 keep that precision.
+ */
+int polar_attn_decode_paged_q4(const void* q, const void* k_pages, const void* v_pages,
+                               const int* block_table, const int* seq_lens, const void* mem,
+                               const float* w_count, void* out, float* n_eff, float* conf, int B,
+                               int Hq, int Hkv, int d, int page_size, int num_pages,
+                               int max_pages, int max_seq_len, int dtype, const polar_consts_t* c,
+                               int num_splits, void* workspace, size_t workspace_bytes,
+                               void* stream);
+int polar_attn_decode_paged_q4_num_splits(int B, int Hkv, int max_seq_len, int d);
+size_t polar_attn_decode_paged_q4_workspace_bytes(int B, int Hq, int Hkv, int max_seq_len, int d,
+                                                  int num_splits);
+
 /* Size of the library-owned device array used by
  * polar_attn_decode_static_scratch (8 MiB per GPU that loads the library). */
 #define POLAR_ATTN_STATIC_SCRATCH_BYTES (8u * 1024u * 1024u)

@@ -1,0 +1,244 @@
+// Rows of k and v into a paged 4-bit cache, and back.  (No counterpart on the
+// pages; layout and rounding: polar_cache_q4.cuh.)
+//
+// Bound by DRAM: the rows are read once and 9 bits are written for each 32.
+// Eight channels, one word of codes, are a thread's; the four threads of a
+// scale's group share its maximum by two shuffles (of the bits of |x|, whose
+// order as integers is that of the numbers, with infinity and NaN above).
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "polar_cache_q4.cuh"
+#include "polar_device.cuh"
+#include "polar_internal.h"
+#include "polar_span.h"
+
+namespace polar {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Q4Args {
+  const void* rows[2];  // k, v
+  void* out[2];         // cache_read: k, v
+  uint8_t* pages[2];
+  const int* slots;
+  long long stride[2];  // elements between tokens
+  int N, Hkv, shift, num_pages;
+  int* status;
+};
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+  x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Slot of token t: the page and its row, or false (negative: no slot; past
+// the pool: recorded).
+__device__ __forceinline__ bool place(const Q4Args& a, long long t, long long& page, int& row) {
+  const int slot = __ldg(a.slots + t);
+  page = slot >> a.shift;
+  row = slot & ((1 << a.shift) - 1);
+  if (slot < 0) return false;
+  if (page >= a.num_pages) {
+    atomicExch(a.status, 3);
+    return false;
+  }
+  return true;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) q4_append_kernel(const Q4Args a) {
+  constexpr int W = D / 8;  // words (threads) of a row
+  const bool is_v = blockIdx.y != 0;
+  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long th = id / W;  // (token, head)
+  const int w = (int)(id % W);
+  const bool in = th < (long long)a.N * a.Hkv;  // the same for a group's threads
+  long long page = 0;
+  int row = 0;
+  const long long token = in ? th / a.Hkv : 0;
+  const int head = in ? (int)(th - token * a.Hkv) : 0;
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (in)
+    load8(static_cast<const T*>(is_v ? a.rows[1] : a.rows[0]) +
+              token * (is_v ? a.stride[1] : a.stride[0]) + head * D + 8 * w, x);
+  const bool ok = in && place(a, token, page, row);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const bool finite = top < 0x7F800000u;
+  const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
+  const float s = __bfloat162float(sb);
+  uint32_t code = 0;
+  if (finite && s > 1e-30f) {
+    const float inv = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) code |= q4_code(q4_round(x[i], s, inv), i & 3) << (16 * (i >> 2));
+  } else if (finite && s > 0.f) {
+    // near the subnormal range 1 / s and the remainder lose bits
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double n = fmin(fmax(rint((double)x[i] / (double)s), -7.0), 7.0);
+      code |= q4_code((int)n, i & 3) << (16 * (i >> 2));
+    }
+  }
+  if (!ok) return;
+  uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head, a.Hkv, a.shift, D);
+  reinterpret_cast<uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)] = code;
+  if ((w & 3) == 0) {
+    uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
+    const uint16_t bits = finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FFF;
+    reinterpret_cast<uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] = bits;
+  }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Args a) {
+  constexpr int W = D / 8;
+  const bool is_v = blockIdx.y != 0;
+  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long th = id / W;
+  const int w = (int)(id % W);
+  if (th >= (long long)a.N * a.Hkv) return;
+  const long long token = th / a.Hkv;
+  const int head = (int)(th - token * a.Hkv);
+  long long page;
+  int row;
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (place(a, token, page, row)) {
+    const uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head, a.Hkv, a.shift, D);
+    const uint32_t code =
+        reinterpret_cast<const uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)];
+    const uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
+    const float s = __uint_as_float(
+        (uint32_t)reinterpret_cast<const uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] << 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s * (float)q4_value(code >> (16 * (i >> 2)), i & 3);
+  }
+  store8(static_cast<T*>(is_v ? a.out[1] : a.out[0]) + (token * a.Hkv + head) * D + 8 * w, x);
+}
+
+template <bool kRead>
+cudaError_t launch(const Q4Args& a, int d, int dtype, cudaStream_t s) {
+  const long long threads = (long long)a.N * a.Hkv * (d / 8);
+  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), 2);
+#define POLAR_Q4(D, T)                                       \
+  if (kRead) q4_read_kernel<D, T><<<grid, kThreads, 0, s>>>(a); \
+  else q4_append_kernel<D, T><<<grid, kThreads, 0, s>>>(a)
+  if (dtype == POLAR_BF16) {
+    if (d == 64) { POLAR_Q4(64, __nv_bfloat16); }
+    else { POLAR_Q4(128, __nv_bfloat16); }
+  } else {
+    if (d == 64) { POLAR_Q4(64, float); }
+    else { POLAR_Q4(128, float); }
+  }
+#undef POLAR_Q4
+  return cudaGetLastError();
+}
+
+int check(const Q4Args& a, int d, int page_size, int dtype, int* shift) {
+  if (a.N < 0 || a.Hkv < 1 || a.num_pages < 1) return POLAR_ERR_INVALID;
+  if ((d != 64 && d != 128) || (dtype != POLAR_F32 && dtype != POLAR_BF16))
+    return POLAR_ERR_UNSUPPORTED;
+  if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+    return POLAR_ERR_UNSUPPORTED;
+  if ((long long)a.num_pages * page_size > INT_MAX || a.Hkv > 4096 ||
+      (long long)a.N * a.Hkv > (long long)INT_MAX * 8)
+    return POLAR_ERR_UNSUPPORTED;
+  *shift = 0;
+  while ((1 << *shift) < page_size) ++*shift;
+  if (a.N == 0) return POLAR_OK;
+  if (!a.pages[0] || !a.pages[1] || !a.slots) return POLAR_ERR_INVALID;
+  if (!aligned16(a.pages[0]) || !aligned16(a.pages[1]) ||
+      (reinterpret_cast<uintptr_t>(a.slots) & 3u))
+    return POLAR_ERR_MISALIGNED;
+  return POLAR_OK;
+}
+
+}  // namespace
+
+}  // namespace polar
+
+using namespace polar;
+
+extern "C" {
+
+int polar_cache_append_q4(const void* k, const void* v, const int* slots, void* k_pages,
+                          void* v_pages, long long k_stride, long long v_stride, int N, int Hkv,
+                          int d, int page_size, int num_pages, int dtype, void* stream) {
+  Q4Args a{{k, v}, {nullptr, nullptr}, {static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages)},
+           slots, {k_stride, v_stride}, N, Hkv, 0, num_pages, nullptr};
+  int st = check(a, d, page_size, dtype, &a.shift);
+  if (st != POLAR_OK || N == 0) return st;
+  if (!k || !v) return POLAR_ERR_INVALID;
+  const long long width = (long long)Hkv * d;
+  const size_t es = dtype == POLAR_BF16 ? 2 : 4;
+  const int vec = (int)(16 / es);
+  if (N > 1 && (k_stride < width || v_stride < width)) return POLAR_ERR_INVALID;
+  if (!aligned16(k) || !aligned16(v) || (N > 1 && (k_stride % vec || v_stride % vec)))
+    return POLAR_ERR_MISALIGNED;
+  const size_t pool = (size_t)num_pages * Hkv * page_size * q4_row_bytes(d);
+  const Strided ins[] = {{k, (size_t)N, (size_t)width * es, (size_t)k_stride * es},
+                         {v, (size_t)N, (size_t)width * es, (size_t)v_stride * es},
+                         span(slots, (size_t)N * 4)};
+  for (const Strided& i : ins)
+    if (meet(i, span(k_pages, pool)) || meet(i, span(v_pages, pool))) return POLAR_ERR_INVALID;
+  if (meet(span(k_pages, pool), span(v_pages, pool))) return POLAR_ERR_INVALID;
+  st = check_device(nullptr);
+  if (st != POLAR_OK) return st;
+  a.status = status_word();
+  if (!a.status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
+  return cuda_status("4-bit append launch",
+                     launch<false>(a, d, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int polar_cache_read_q4(const void* k_pages, const void* v_pages, const int* slots, void* k,
+                        void* v, int N, int Hkv, int d, int page_size, int num_pages, int dtype,
+                        void* stream) {
+  Q4Args a{{nullptr, nullptr}, {k, v},
+           {static_cast<uint8_t*>(const_cast<void*>(k_pages)),
+            static_cast<uint8_t*>(const_cast<void*>(v_pages))},
+           slots, {0, 0}, N, Hkv, 0, num_pages, nullptr};
+  int st = check(a, d, page_size, dtype, &a.shift);
+  if (st != POLAR_OK || N == 0) return st;
+  if (!k || !v) return POLAR_ERR_INVALID;
+  if (!aligned16(k) || !aligned16(v)) return POLAR_ERR_MISALIGNED;
+  const size_t pool = (size_t)num_pages * Hkv * page_size * q4_row_bytes(d);
+  const size_t rows = (size_t)N * Hkv * d * (dtype == POLAR_BF16 ? 2 : 4);
+  const Strided ins[] = {span(k_pages, pool), span(v_pages, pool), span(slots, (size_t)N * 4)};
+  for (const Strided& i : ins)
+    if (meet(i, span(k, rows)) || meet(i, span(v, rows))) return POLAR_ERR_INVALID;
+  if (meet(span(k, rows), span(v, rows))) return POLAR_ERR_INVALID;
+  st = check_device(nullptr);
+  if (st != POLAR_OK) return st;
+  a.status = status_word();
+  if (!a.status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
+  return cuda_status("4-bit read launch",
+                     launch<true>(a, d, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -127,6 +127,18 @@ def lib() -> ctypes.CDLL:
                                             ci, ci, ci, ci, ci, vp, cs, vp]
             L.polar_cache_evict_workspace_bytes.argtypes = [ci, ci, ci, ci]
             L.polar_cache_evict_workspace_bytes.restype = cs
+            cl = ctypes.c_longlong
+            L.polar_pages_extend.argtypes = [vp] * 10 + [ci] * 6 + [vp, cs, vp]
+            L.polar_pages_release.argtypes = [vp] * 7 + [ci] * 5 + [vp, cs, vp]
+            L.polar_pages_workspace_bytes.argtypes = [ci]
+            L.polar_pages_workspace_bytes.restype = cs
+            L.polar_rope.argtypes = [vp] * 6 + [cl] * 4 + [ci] * 8 + [cf, vp]
+            L.polar_cache_append_q4.argtypes = [vp] * 5 + [cl] * 2 + [ci] * 6 + [vp]
+            L.polar_cache_read_q4.argtypes = [vp] * 5 + [ci] * 6 + [vp]
+            L.polar_attn_decode_paged_q4.argtypes = [vp] * 10 + [ci] * 9 + [cp, ci, vp, cs, vp]
+            L.polar_attn_decode_paged_q4_num_splits.argtypes = [ci] * 4
+            L.polar_attn_decode_paged_q4_workspace_bytes.argtypes = [ci] * 6
+            L.polar_attn_decode_paged_q4_workspace_bytes.restype = cs
             L.polar_attn_last_error.argtypes = []
             L.polar_attn_last_error.restype = ctypes.c_char_p
             for f in ("polar_attn_fwd", "polar_attn_decode", "polar_attn_combine",
@@ -134,7 +146,9 @@ def lib() -> ctypes.CDLL:
                       "polar_attn_selftest_wait_timeout", "polar_attn_version",
                       "polar_attn_default_consts", "polar_linear_fwd", "polar_linear_step",
                       "polar_linear_bwd", "polar_attn_decode_paged_weights",
-                      "polar_cache_evict"):
+                      "polar_cache_evict", "polar_pages_extend", "polar_pages_release",
+                      "polar_rope", "polar_cache_append_q4", "polar_cache_read_q4",
+                      "polar_attn_decode_paged_q4", "polar_attn_decode_paged_q4_num_splits"):
                 getattr(L, f).restype = ci
             _lib = L
     return _lib
@@ -759,6 +773,276 @@ def cache_evict(k_pages, v_pages, block_table, seq_lens, weights, positions, kee
           _in(new_lens, "new_lens", i32, (B,), dev), B, Hkv, d, page, num_pages, max_pages,
           int(max_seq_len), stride, _dtype_code(k_pages), int(keep), int(recent), ws, size)
     return new_lens
+
+
+def _row_in(t, name, dtype, shape, dev):
+    """(address, elements between tokens) of a [N, heads, d] argument whose
+    heads are contiguous; tokens may be further apart (part of a projection)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.get_device() == dev:
+        s0, s1, s2 = t.stride()
+        if t.numel() == 0:
+            return t.data_ptr(), shape[1] * shape[2]
+        if (s2 == 1 or shape[2] == 1) and (s1 == shape[2] or shape[1] == 1):
+            return t.data_ptr(), s0 if shape[0] > 1 else shape[1] * shape[2]
+        raise ValueError(f"the heads of {name} must be contiguous")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _shape(t, name, shape)
+    raise ValueError(f"{name} must be on cuda:{dev}, like the first tensor, got {t.device}")
+
+
+def pages_workspace_bytes(B) -> int:
+    return int(lib().polar_pages_workspace_bytes(B))
+
+
+def _pages(block_table, lens, other, other_name, free_pages, free_count, lens_out, count_out,
+           num_pages, workspace):
+    """Checked arguments that the two page calls share."""
+    for name, t in (("block_table", block_table), ("free_pages", free_pages)):
+        _dev(_need(t, name), name)
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages], free_pages [capacity]")
+    B, max_pages = block_table.shape
+    cap, dev, i32 = free_pages.shape[0], block_table.get_device(), torch.int32
+    lens_out = lens if lens_out is None else lens_out
+    count_out = free_count if count_out is None else count_out
+    ws, size, keep = _scratch(workspace, 8 * B + 8, dev)
+    ptrs = (_in(block_table, "block_table", i32, (B, max_pages), dev),
+            _in(_need(lens, "seq_lens"), "seq_lens", i32, (B,), dev),
+            _in(_need(other, other_name), other_name, i32, (B,), dev),
+            _in(free_pages, "free_pages", i32, (cap,), dev),
+            _in(_need(free_count, "free_count"), "free_count", i32, (1,), dev),
+            _in(lens_out, "lens_out", i32, (B,), dev),
+            _in(count_out, "count_out", i32, (1,), dev))
+    return dev, ptrs, B, max_pages, cap if num_pages is None else int(num_pages), cap, ws, size, keep
+
+
+@_on_stream
+def pages_extend(block_table, seq_lens, new_tokens, free_pages, free_count, page_size, max_tokens,
+                 num_pages=None, lens_out=None, count_out=None, cu_seqlens=None, positions=None,
+                 slots=None, workspace=None):
+    """Pages for new tokens, on the device: block_table [B, max_pages],
+    seq_lens and new_tokens [B], the stack free_pages [capacity] with free_count
+    [1] pages on it (all int32).  The table gets the new pages; lengths and count
+    are updated in place unless lens_out, count_out are given.  num_pages: the
+    pool's size (default: the stack's capacity).  max_tokens bounds the sum of
+    new_tokens.  Returns (cu_seqlens [B + 1], positions [max_tokens], slots
+    [max_tokens]); a token without a row has slot -1."""
+    dev, ptrs, B, max_pages, pool, cap, ws, size, _ = _pages(
+        block_table, seq_lens, new_tokens, "new_tokens", free_pages, free_count, lens_out,
+        count_out, num_pages, workspace)
+    i32, n = torch.int32, int(max_tokens)
+    if n < 0:
+        raise ValueError("max_tokens must not be negative")
+    if cu_seqlens is None:
+        cu_seqlens = (torch.zeros if B == 0 else torch.empty)((B + 1,), device=block_table.device,
+                                                              dtype=i32)
+    if positions is None:
+        positions = torch.empty((n,), device=block_table.device, dtype=i32)
+    if slots is None:
+        slots = torch.empty((n,), device=block_table.device, dtype=i32)
+    _call(dev, "polar_pages_extend", lib().polar_pages_extend, *ptrs,
+          _in(cu_seqlens, "cu_seqlens", i32, (B + 1,), dev),
+          _in(positions, "positions", i32, (n,), dev), _in(slots, "slots", i32, (n,), dev), B,
+          max_pages, int(page_size), pool, cap, n, ws, size)
+    return cu_seqlens, positions, slots
+
+
+@_on_stream
+def pages_release(block_table, seq_lens, keep_lens, free_pages, free_count, page_size,
+                  num_pages=None, lens_out=None, count_out=None, workspace=None):
+    """Puts the pages past the first keep_lens [B] rows of every sequence back
+    on the stack (0: those of an ended sequence); lengths and count are updated in
+    place unless lens_out, count_out are given.  Returns (lens_out, count_out)."""
+    dev, ptrs, B, max_pages, pool, cap, ws, size, _ = _pages(
+        block_table, seq_lens, keep_lens, "keep_lens", free_pages, free_count, lens_out, count_out,
+        num_pages, workspace)
+    _call(dev, "polar_pages_release", lib().polar_pages_release, *ptrs, B, max_pages,
+          int(page_size), pool, cap, ws, size)
+    return (seq_lens if lens_out is None else lens_out,
+            free_count if count_out is None else count_out)
+
+
+def rope_inv_freq(rot, base=10000.0, factor=1.0, scaling="none", context=None, fast=32.0,
+                  slow=1.0, device="cuda"):
+    """(frequencies [rot / 2] fp64 in radians a token, scale) for rope().
+
+    scaling "none"; "linear": positions in steps of 1 / factor; "base": a base
+    whose slowest pair turns `factor` times slower and whose fastest as before;
+    "bands": pairs that turn more than `fast` times over `context` tokens (the
+    trained length) as before, less than `slow` times `factor` times slower, a
+    linear mixture by turns' logarithm between, and the scale 0.1 ln factor + 1."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1, factor at least 1")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "base":
+        if rot == 2:
+            raise ValueError("scaling 'base' needs more than one pair")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-2.0 * i / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        if context is None or not context > 0 or not fast > slow > 0:
+            raise ValueError("scaling 'bands' needs context > 0 and fast > slow > 0")
+        turns = f * context / (2.0 * math.pi)
+        keep = (torch.log(turns / slow) / math.log(fast / slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device), scale
+
+
+@_on_stream
+def rope(q, k, positions, inv_freq, scale=1.0, interleaved=False, inverse=False, q_out=None,
+         k_out=None):
+    """Rotary positions: q [N, Hq, d] and k [N, Hkv, d] (or None), bf16 or fp32,
+    tokens may be apart (parts of a projection's output); positions [N] int32;
+    inv_freq [rot / 2] fp64, rot <= d the channels that turn.  interleaved: pairs
+    (2 i, 2 i + 1), otherwise (i, i + rot / 2).  inverse: the gradient (dq, dk from
+    the gradients of the results).  q_out, k_out may be q, k.  Returns (q, k)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q must be [N, Hq, d], k [N, Hkv, d]")
+    N, Hq, d = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    dt, dev = q.dtype, q.get_device()
+    code = _dtype_code(q)
+    if q_out is None:
+        q_out = torch.empty((N, Hq, d), device=q.device, dtype=dt)
+    if k is not None and k_out is None:
+        k_out = torch.empty((N, Hkv, d), device=q.device, dtype=dt)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    _dev(_need(inv_freq, "inv_freq"), "inv_freq")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    half = inv_freq.shape[0]
+    qp, qs = _row_in(q, "q", dt, (N, Hq, d), dev)
+    qop, qos = _row_in(q_out, "q_out", dt, (N, Hq, d), dev)
+    kp = kop = ks = kos = 0
+    if k is not None:
+        kp, ks = _row_in(k, "k", dt, (N, Hkv, d), dev)
+        kop, kos = _row_in(k_out, "k_out", dt, (N, Hkv, d), dev)
+    _call(dev, "polar_rope", lib().polar_rope, qp, kp,
+          _in(_need(positions, "positions"), "positions", torch.int32, (N,), dev),
+          _in(inv_freq, "inv_freq", torch.float64, (half,), dev), qop, kop, qs, ks, qos, kos, N, Hq,
+          Hkv, d, 2 * half, code, 1 if interleaved else 0, 1 if inverse else 0, float(scale))
+    return q_out, k_out
+
+
+def _pages_q4(k_pages, v_pages, dev=None):
+    """(addresses, num_pages, Hkv, page, d) of a 4-bit cache's pages."""
+    _dev(_need(k_pages, "k_pages"), "k_pages", torch.uint8)
+    if k_pages.dim() != 4:
+        raise ValueError("the pages must be [num_pages, Hkv, page, 9 d / 16]")
+    num_pages, Hkv, page, row = shape = k_pages.shape
+    dev = k_pages.get_device() if dev is None else dev
+    if row % 9:
+        raise ValueError(f"the pages must be [num_pages, Hkv, page, 9 d / 16], got {tuple(shape)}")
+    return (_in(k_pages, "k_pages", torch.uint8, shape, dev),
+            _in(_need(v_pages, "v_pages"), "v_pages", torch.uint8, shape, dev), num_pages, Hkv, page,
+            row // 9 * 16)
+
+
+def cache_q4(num_pages, Hkv, page, d, device="cuda"):
+    """Zeroed (k_pages, v_pages) of a 4-bit cache."""
+    if d % 32:
+        raise ValueError("d must be a multiple of 32")
+    return tuple(torch.zeros((num_pages, Hkv, page, 9 * d // 16), dtype=torch.uint8, device=device)
+                 for _ in range(2))
+
+
+@_on_stream
+def cache_append_q4(k, v, slots, k_pages, v_pages):
+    """Rounds rows to 4 bits into their slots of a paged cache: k, v [N, Hkv, d]
+    (bf16 or fp32, tokens may be apart), slots [N] int32 (negative: skipped),
+    k_pages, v_pages [num_pages, Hkv, page, 9 d / 16] uint8 (cache_q4)."""
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise TypeError("k must be a CUDA tensor")
+    if k.dim() != 3:
+        raise ValueError("k must be [N, Hkv, d]")
+    N, dev, dt = k.shape[0], k.get_device(), k.dtype
+    kpg, vpg, num_pages, Hkv, page, d = _pages_q4(k_pages, v_pages, dev)
+    kp, ks = _row_in(k, "k", dt, (N, Hkv, d), dev)
+    vp, vs = _row_in(v, "v", dt, (N, Hkv, d), dev)
+    _call(dev, "polar_cache_append_q4", lib().polar_cache_append_q4, kp, vp,
+          _in(_need(slots, "slots"), "slots", torch.int32, (N,), dev), kpg, vpg, ks, vs, N, Hkv, d,
+          page, num_pages, _dtype_code(k))
+
+
+@_on_stream
+def cache_read_q4(k_pages, v_pages, slots, k=None, v=None, dtype=torch.bfloat16):
+    """Rows of a 4-bit cache as their values: (k, v) [N, Hkv, d] of dtype, zeros
+    for negative slots."""
+    kpg, vpg, num_pages, Hkv, page, d = _pages_q4(k_pages, v_pages)
+    dev = k_pages.get_device()
+    _dev(_need(slots, "slots"), "slots")
+    shape = (slots.shape[0] if slots.dim() else 0, Hkv, d)
+    if k is None:
+        k = torch.empty(shape, device=k_pages.device, dtype=dtype)
+    if v is None:
+        v = torch.empty(shape, device=k_pages.device, dtype=k.dtype)
+    _call(dev, "polar_cache_read_q4", lib().polar_cache_read_q4, kpg, vpg,
+          _in(slots, "slots", torch.int32, (shape[0],), dev), _in(k, "k", k.dtype, shape, dev),
+          _in(v, "v", k.dtype, shape, dev), shape[0], Hkv, d, page, num_pages, _dtype_code(k))
+    return k, v
+
+
+def decode_paged_q4_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits=0) -> int:
+    return int(lib().polar_attn_decode_paged_q4_workspace_bytes(B, Hq, Hkv, max_seq_len, d,
+                                                                num_splits))
+
+
+def decode_paged_q4_num_splits(B, Hkv, max_seq_len, d) -> int:
+    return int(lib().polar_attn_decode_paged_q4_num_splits(B, Hkv, max_seq_len, d))
+
+
+@_on_stream
+def decode_paged_q4(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, max_seq_len=None,
+                    num_splits=0, workspace=None, out=None, n_eff=None, conf=None, consts=None,
+                    want_conf=False):
+    """decode_paged against a 4-bit cache (k_pages, v_pages uint8 as
+    cache_append_q4 fills them); other arguments and results as there."""
+    for name, t in (("q", q), ("block_table", block_table)):
+        _dev(_need(t, name), name)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q must be [B, Hq, d], block_table [B, max_pages]")
+    B, Hq, d = shape = q.shape
+    dt, dev, f32, i32 = q.dtype, q.get_device(), torch.float32, torch.int32
+    kpg, vpg, num_pages, Hkv, page, cache_d = _pages_q4(k_pages, v_pages, dev)
+    if cache_d != d:
+        raise ValueError(f"the cache holds rows of {cache_d} channels, q of {d}")
+    max_pages = block_table.shape[1]
+    if max_seq_len is None:
+        max_seq_len = max_pages * page
+    if out is None:
+        out = torch.empty_like(q)
+    if n_eff is None:
+        n_eff = torch.empty((B, Hq), device=q.device, dtype=f32)
+    if conf is None and want_conf:
+        conf = torch.empty((B, Hq), device=q.device, dtype=f32)
+    need = _bytes("polar_attn_decode_paged_q4_workspace_bytes", dev, B, Hq, Hkv, int(max_seq_len),
+                  d, int(num_splits))
+    ws, size, _ = _scratch(workspace, need, dev)
+    c = _DEFAULT_CONSTS if consts is None else consts
+    _call(dev, "polar_attn_decode_paged_q4", lib().polar_attn_decode_paged_q4, q.data_ptr(), kpg,
+          vpg, _in(block_table, "block_table", i32, (B, max_pages), dev),
+          _in(_need(seq_lens, "seq_lens"), "seq_lens", i32, (B,), dev),
+          _in(_need(mem, "mem"), "mem", dt, shape, dev),
+          _in(_need(w_count, "w_count"), "w_count", f32, (Hq, d), dev),
+          _in(out, "out", dt, shape, dev), _in(n_eff, "n_eff", f32, (B, Hq), dev),
+          _in(conf, "conf", f32, (B, Hq), dev), B, Hq, Hkv, d, page, num_pages, max_pages,
+          int(max_seq_len), _dtype_code(q), ctypes.byref(c), int(num_splits), ws, size)
+    return out, n_eff, conf
 
 
 def bwd_workspace_bytes(B, H, T, d) -> int:
