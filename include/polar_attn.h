@@ -536,6 +536,33 @@ int polar_rope(const void* q, const void* k, const int* positions, const double*
                int rot, int dtype, int interleaved, int inverse, float scale, void* stream);
 
 /*
+ * polar_attn_fwd over packed sequences with grouped-query heads: prompts of
+ * different lengths one after another, without padding (ATMA §2.2's grouped
+ * heads in the prefill).
+ *   q          : [N, Hq, d] of dtype, tokens q_stride elements apart (>= Hq * d,
+ *                a multiple of 16 bytes), heads contiguous; k, v : [N, Hkv, d]
+ *                with k_stride, v_stride (parts of one projection's output)
+ *   mem, out   : [N, Hq, d] of dtype, contiguous
+ *   cu_seqlens : [B + 1] int32, device, ascending: sequence b is the tokens
+ *                cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (none: an empty one)
+ *   w_count    : [Hq, d] fp32;  n_eff, conf : [N, Hq] fp32 (conf may be NULL)
+ * Token i of a sequence sees its tokens 0 .. i (n = i + 1); query head h reads
+ * KV head h / (Hq / Hkv), Hq / Hkv 1, 2, 4 or 8.  Rows before cu_seqlens[0] and
+ * from cu_seqlens[B] on are neither read into a result nor written.  A token
+ * that holds an infinity or NaN may make other rows of its sequence's 128-token
+ * tile non-finite, earlier ones included; other sequences it does not reach.
+ * Offsets outside [0, N] or descending are cut and record status 3 in
+ * polar_attn_device_status.  Memory beyond inputs and outputs: none.  Precision
+ * as polar_attn_fwd.  An output that overlaps another tensor of the call is
+ * refused.
+ */
+int polar_attn_fwd_packed(const void* q, const void* k, const void* v, const void* mem,
+                          const float* w_count, const int* cu_seqlens, void* out, float* n_eff,
+                          float* conf, long long q_stride, long long k_stride, long long v_stride,
+                          int N, int B, int Hq, int Hkv, int d, int dtype, const polar_consts_t* c,
+                          void* stream);
+
+/*
  * A paged cache in 4 bits.  (No counterpart on the pages.)  32 consecutive
  * channels of a row share a bf16 scale s = max |x| / 7, and hold x / s rounded
  * to nearest (ties to even), -7 .. 7, as a sign and three bits: 4.5 bits a

@@ -22,7 +22,8 @@ SOURCES = ["polar_api.cu", "polar_prefill_tc.cu", "polar_prefill_f32.cu",
            "polar_backward.cu", "polar_backward_tc.cu", "polar_host.cu",
            "polar_decode_paged_tc.cu", "polar_linear.cu", "polar_linear_tc.cu",
            "polar_linear_api.cu", "polar_cache.cu", "polar_pages.cu",
-           "polar_rope.cu", "polar_cache_q4.cu", "polar_decode_q4.cu"]
+           "polar_rope.cu", "polar_cache_q4.cu", "polar_decode_q4.cu",
+           "polar_packed_tc.cu", "polar_packed_f32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -118,6 +118,25 @@ bool make_map(CUtensorMap* map, const void* base, int BH, int T, int d, int rows
   return r == CUDA_SUCCESS;
 }
 
+bool make_map_tokens(CUtensorMap* map, const void* base, int N, int heads, int d, long long stride,
+                     int box_heads, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) {
+    note("cudaGetDriverEntryPointByVersion(cuTensorMapEncodeTiled)", -1, "");
+    return false;
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)N};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) note("cuTensorMapEncodeTiled", (int)r, "");
+  return r == CUDA_SUCCESS;
+}
+
 namespace {
 
 // 2-D map over a [rows, d] bf16 tensor with a {64, box_rows} box and

@@ -210,6 +210,24 @@ constexpr int kPagedTcStageKeys = 64;
 cudaError_t launch_decode_paged_tc(const PagedArgs& a, const CUtensorMap& mk,
                                    const CUtensorMap& mv, cudaStream_t s);
 
+// Packed causal prefill with grouped heads: sequences are the tokens
+// cu[b] .. cu[b + 1] - 1 of [N, heads, d] tensors, tokens qs, ks, vs elements apart
+// (mem and out contiguous).
+struct PackedArgs {
+  const void *q, *k, *v, *mem;
+  const float* w_count;
+  const int* cu;
+  void* out;
+  float *n_eff, *conf;  // conf may be null
+  long long qs, ks, vs;
+  int N, B, Hq, Hkv, d;
+  polar_consts_t c;
+  int* status;
+};
+// maps: q, k, v, out as [token, head, channel] with 128-row boxes.
+cudaError_t launch_packed_tc(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s);
+cudaError_t launch_packed_f32(const PackedArgs& a, cudaStream_t s);
+
 // Split kernel over the 4-bit cache (pages of polar_cache_q4.cuh).
 cudaError_t launch_decode_q4(const PagedArgs& a, int dtype, cudaStream_t s);
 
@@ -246,6 +264,10 @@ int* status_word();  // device address of the current device's status word, or n
 // 3-D map over a [BH, T, d] bf16 tensor with a {64, rows, 1} box and 128-byte
 // swizzle; out-of-range rows read as zeros.
 bool make_map(CUtensorMap* map, const void* base, int BH, int T, int d, int rows = 128);
+// 3-D map over a [N, heads, d] bf16 tensor, tokens `stride` elements apart, with
+// a {64, box_heads, box_tokens} box and 128-byte swizzle.
+bool make_map_tokens(CUtensorMap* map, const void* base, int N, int heads, int d, long long stride,
+                     int box_heads, int box_tokens);
 
 // Bounded-wait self test (one thread, a barrier nothing completes).
 cudaError_t launch_selftest_wait(long long limit_cycles, int* status, cudaStream_t s);

@@ -133,6 +133,7 @@ def lib() -> ctypes.CDLL:
             L.polar_pages_workspace_bytes.argtypes = [ci]
             L.polar_pages_workspace_bytes.restype = cs
             L.polar_rope.argtypes = [vp] * 6 + [cl] * 4 + [ci] * 8 + [cf, vp]
+            L.polar_attn_fwd_packed.argtypes = [vp] * 9 + [cl] * 3 + [ci] * 6 + [cp, vp]
             L.polar_cache_append_q4.argtypes = [vp] * 5 + [cl] * 2 + [ci] * 6 + [vp]
             L.polar_cache_read_q4.argtypes = [vp] * 5 + [ci] * 6 + [vp]
             L.polar_attn_decode_paged_q4.argtypes = [vp] * 10 + [ci] * 9 + [cp, ci, vp, cs, vp]
@@ -147,7 +148,7 @@ def lib() -> ctypes.CDLL:
                       "polar_attn_default_consts", "polar_linear_fwd", "polar_linear_step",
                       "polar_linear_bwd", "polar_attn_decode_paged_weights",
                       "polar_cache_evict", "polar_pages_extend", "polar_pages_release",
-                      "polar_rope", "polar_cache_append_q4", "polar_cache_read_q4",
+                      "polar_rope", "polar_attn_fwd_packed", "polar_cache_append_q4", "polar_cache_read_q4",
                       "polar_attn_decode_paged_q4", "polar_attn_decode_paged_q4_num_splits"):
                 getattr(L, f).restype = ci
             _lib = L
@@ -937,6 +938,45 @@ def rope(q, k, positions, inv_freq, scale=1.0, interleaved=False, inverse=False,
           _in(inv_freq, "inv_freq", torch.float64, (half,), dev), qop, kop, qs, ks, qos, kos, N, Hq,
           Hkv, d, 2 * half, code, 1 if interleaved else 0, 1 if inverse else 0, float(scale))
     return q_out, k_out
+
+
+@_on_stream
+def fwd_packed(q, k, v, mem, w_count, cu_seqlens, out=None, n_eff=None, conf=None, consts=None,
+               want_conf=False):
+    """Causal prefill of packed sequences with grouped heads: q, mem [N, Hq, d],
+    k, v [N, Hkv, d] (bf16 or fp32; tokens of q, k, v may be apart, as parts of
+    one projection's output are); w_count [Hq, d] fp32; cu_seqlens [B + 1] int32 on
+    the device: sequence b is the tokens cu_seqlens[b] to cu_seqlens[b + 1].
+    Returns (out [N, Hq, d], n_eff [N, Hq], conf or None); rows outside the
+    sequences are left as they are."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    if q.dim() != 3 or _need(k, "k").dim() != 3 or _need(cu_seqlens, "cu_seqlens").dim() != 1:
+        raise ValueError("q must be [N, Hq, d], k and v [N, Hkv, d], cu_seqlens [B + 1]")
+    N, Hq, d = shape = q.shape
+    Hkv, B = k.shape[1], cu_seqlens.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    dt, dev, f32 = q.dtype, q.get_device(), torch.float32
+    code = _dtype_code(q)
+    if out is None:
+        out = torch.empty(shape, device=q.device, dtype=dt)
+    if n_eff is None:
+        n_eff = torch.empty((N, Hq), device=q.device, dtype=f32)
+    if conf is None and want_conf:
+        conf = torch.empty((N, Hq), device=q.device, dtype=f32)
+    qp, qs = _row_in(q, "q", dt, shape, dev)
+    kp, ks = _row_in(k, "k", dt, (N, Hkv, d), dev)
+    vp, vs = _row_in(v, "v", dt, (N, Hkv, d), dev)
+    c = _DEFAULT_CONSTS if consts is None else consts
+    _call(dev, "polar_attn_fwd_packed", lib().polar_attn_fwd_packed, qp, kp, vp,
+          _in(_need(mem, "mem"), "mem", dt, shape, dev),
+          _in(_need(w_count, "w_count"), "w_count", f32, (Hq, d), dev),
+          _in(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev),
+          _in(out, "out", dt, shape, dev), _in(n_eff, "n_eff", f32, (N, Hq), dev),
+          _in(conf, "conf", f32, (N, Hq), dev), qs, ks, vs, N, B, Hq, Hkv, d, code,
+          ctypes.byref(c))
+    return out, n_eff, conf
 
 
 def _pages_q4(k_pages, v_pages, dev=None):
