@@ -552,7 +552,8 @@ int polar_rope(const void* q, const void* k, const int* positions, const double*
  * that holds an infinity or NaN may make other rows of its sequence's 128-token
  * tile non-finite, earlier ones included; other sequences it does not reach.
  * Offsets outside [0, N] or descending are cut and record status 3 in
- * polar_attn_device_status.  Memory beyond inputs and outputs: none.  Precision
+ * polar_attn_device_status (rows that two sequences then share hold either's
+ * results).  Memory beyond inputs and outputs: none.  Precision
  * as polar_attn_fwd.  An output that overlaps another tensor of the call is
  * refused.
  */

@@ -66,6 +66,12 @@ __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 
+// One pair, in one order of roundings wherever it is computed.
+__device__ __forceinline__ void turn(float xa, float xb, float c, float s, float& ya, float& yb) {
+  ya = fmaf(xa, c, -__fmul_rn(xb, s));
+  yb = fmaf(xb, c, __fmul_rn(xa, s));
+}
+
 // kVec: 16-byte accesses (8 bf16 or 4 fp32 channels a thread); without, one
 // pair or one channel a thread, for parts of a head and strides that are not
 // multiples of that.
@@ -132,12 +138,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
               // pair i: channels 2 i and 2 i + 1 of the two vectors in a row
               const float xa = i < V / 2 ? x0[u][2 * i % V] : x1[u][2 * i % V];
               const float xb = i < V / 2 ? x0[u][(2 * i + 1) % V] : x1[u][(2 * i + 1) % V];
-              const float ya = xa * cs[i] - xb * sn[i], yb = xb * cs[i] + xa * sn[i];
-              if (i < V / 2) y0[2 * i % V] = ya, y0[(2 * i + 1) % V] = yb;
-              else y1[2 * i % V] = ya, y1[(2 * i + 1) % V] = yb;
+              float(&y)[V] = i < V / 2 ? y0 : y1;
+              turn(xa, xb, cs[i], sn[i], y[2 * i % V], y[(2 * i + 1) % V]);
             } else {
-              y0[i] = x0[u][i] * cs[i] - x1[u][i] * sn[i];
-              y1[i] = x1[u][i] * cs[i] + x0[u][i] * sn[i];
+              turn(x0[u][i], x1[u][i], cs[i], sn[i], y0[i], y1[i]);
             }
           }
           store16(dst(r0 + u) + off0, y0, (const T*)nullptr);
@@ -147,8 +151,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   } else {
     for (int r = row0; r < row1; ++r) {
       const float x0 = as_float(src(r)[off0]), x1 = as_float(src(r)[off1]);
-      put(dst(r) + off0, x0 * cs[0] - x1 * sn[0]);
-      put(dst(r) + off1, x1 * cs[0] + x0 * sn[0]);
+      float y0, y1;
+      turn(x0, x1, cs[0], sn[0], y0, y1);
+      put(dst(r) + off0, y0);
+      put(dst(r) + off1, y1);
     }
   }
 }
