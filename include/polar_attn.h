@@ -596,21 +596,25 @@ int polar_cache_read_q4(const void* k_pages, const void* v_pages, const int* slo
 /*
  * polar_attn_decode_paged over a 4-bit cache: k_pages and v_pages as above,
  * dtype the type of q, mem and out, other arguments and results as there, but
- * a length past max_seq_len is cut to max_seq_len itself.  bf16 q: the weights
- * times V's scales are rounded to bf16, sums are fp32.  fp32 q: q and those
- * weights are taken to 24 bits.  Rows whose scales are in [2^-50, 2^50] and q
- * below 2^60 keep that precision.
+ * a length past max_seq_len is cut to max_seq_len itself (which bounds, and need
+ * not be near, the lengths: the rows of all sequences are spread evenly over
+ * num_runs CTAs, 0: as many as run at once).  bf16 q: the weights times V's
+ * scales are rounded to bf16, sums are fp32.  fp32 q: q and those weights are
+ * taken to 24 bits.  Rows whose scales are in [2^-30, 2^50] and q below 2^60 keep
+ * that precision.  A row that holds a NaN makes its own sequence's results of
+ * its KV head NaN.  workspace: polar_attn_decode_paged_q4_workspace_bytes(...)
+ * bytes, device, 16-byte aligned; two calls that may overlap need one each.
  */
 int polar_attn_decode_paged_q4(const void* q, const void* k_pages, const void* v_pages,
                                const int* block_table, const int* seq_lens, const void* mem,
                                const float* w_count, void* out, float* n_eff, float* conf, int B,
                                int Hq, int Hkv, int d, int page_size, int num_pages,
                                int max_pages, int max_seq_len, int dtype, const polar_consts_t* c,
-                               int num_splits, void* workspace, size_t workspace_bytes,
+                               int num_runs, void* workspace, size_t workspace_bytes,
                                void* stream);
-int polar_attn_decode_paged_q4_num_splits(int B, int Hkv, int max_seq_len, int d);
+int polar_attn_decode_paged_q4_num_runs(int B, int Hkv, int max_seq_len, int dtype);
 size_t polar_attn_decode_paged_q4_workspace_bytes(int B, int Hq, int Hkv, int max_seq_len, int d,
-                                                  int num_splits);
+                                                  int dtype, int num_runs);
 
 /* Size of the library-owned device array used by
  * polar_attn_decode_static_scratch (8 MiB per GPU that loads the library). */

@@ -228,9 +228,6 @@ struct PackedArgs {
 cudaError_t launch_packed_tc(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s);
 cudaError_t launch_packed_f32(const PackedArgs& a, cudaStream_t s);
 
-// Split kernel over the 4-bit cache (pages of polar_cache_q4.cuh).
-cudaError_t launch_decode_q4(const PagedArgs& a, int dtype, cudaStream_t s);
-
 // Heads per group in the multi-wave CTA orders of the tensor-core kernels
 // (each group's streamed operands kept in L2): the largest divisor of BH
 // whose heads' per_head_bytes fit a third of the current device's L2 (a

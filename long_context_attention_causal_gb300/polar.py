@@ -137,8 +137,8 @@ def lib() -> ctypes.CDLL:
             L.polar_cache_append_q4.argtypes = [vp] * 5 + [cl] * 2 + [ci] * 6 + [vp]
             L.polar_cache_read_q4.argtypes = [vp] * 5 + [ci] * 6 + [vp]
             L.polar_attn_decode_paged_q4.argtypes = [vp] * 10 + [ci] * 9 + [cp, ci, vp, cs, vp]
-            L.polar_attn_decode_paged_q4_num_splits.argtypes = [ci] * 4
-            L.polar_attn_decode_paged_q4_workspace_bytes.argtypes = [ci] * 6
+            L.polar_attn_decode_paged_q4_num_runs.argtypes = [ci] * 4
+            L.polar_attn_decode_paged_q4_workspace_bytes.argtypes = [ci] * 7
             L.polar_attn_decode_paged_q4_workspace_bytes.restype = cs
             L.polar_attn_last_error.argtypes = []
             L.polar_attn_last_error.restype = ctypes.c_char_p
@@ -149,7 +149,7 @@ def lib() -> ctypes.CDLL:
                       "polar_linear_bwd", "polar_attn_decode_paged_weights",
                       "polar_cache_evict", "polar_pages_extend", "polar_pages_release",
                       "polar_rope", "polar_attn_fwd_packed", "polar_cache_append_q4", "polar_cache_read_q4",
-                      "polar_attn_decode_paged_q4", "polar_attn_decode_paged_q4_num_splits"):
+                      "polar_attn_decode_paged_q4", "polar_attn_decode_paged_q4_num_runs"):
                 getattr(L, f).restype = ci
             _lib = L
     return _lib
@@ -1037,27 +1037,33 @@ def cache_read_q4(k_pages, v_pages, slots, k=None, v=None, dtype=torch.bfloat16)
     return k, v
 
 
-def decode_paged_q4_workspace_bytes(B, Hq, Hkv, max_seq_len, d, num_splits=0) -> int:
-    return int(lib().polar_attn_decode_paged_q4_workspace_bytes(B, Hq, Hkv, max_seq_len, d,
-                                                                num_splits))
+def decode_paged_q4_workspace_bytes(B, Hq, Hkv, max_seq_len, d, dtype=torch.bfloat16,
+                                    num_runs=0) -> int:
+    code = 1 if dtype == torch.bfloat16 else 0
+    return int(lib().polar_attn_decode_paged_q4_workspace_bytes(B, Hq, Hkv, max_seq_len, d, code,
+                                                                num_runs))
 
 
-def decode_paged_q4_num_splits(B, Hkv, max_seq_len, d) -> int:
-    return int(lib().polar_attn_decode_paged_q4_num_splits(B, Hkv, max_seq_len, d))
+def decode_paged_q4_num_runs(B, Hkv, max_seq_len, dtype=torch.bfloat16) -> int:
+    code = 1 if dtype == torch.bfloat16 else 0
+    return int(lib().polar_attn_decode_paged_q4_num_runs(B, Hkv, max_seq_len, code))
 
 
 @_on_stream
 def decode_paged_q4(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, max_seq_len=None,
-                    num_splits=0, workspace=None, out=None, n_eff=None, conf=None, consts=None,
+                    num_runs=0, workspace=None, out=None, n_eff=None, conf=None, consts=None,
                     want_conf=False):
     """decode_paged against a 4-bit cache (k_pages, v_pages uint8 as
-    cache_append_q4 fills them); other arguments and results as there."""
+    cache_append_q4 fills them); other arguments and results as there.  num_runs:
+    CTAs that the rows of all sequences are spread over (0: as many as run at
+    once)."""
     for name, t in (("q", q), ("block_table", block_table)):
         _dev(_need(t, name), name)
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("q must be [B, Hq, d], block_table [B, max_pages]")
     B, Hq, d = shape = q.shape
     dt, dev, f32, i32 = q.dtype, q.get_device(), torch.float32, torch.int32
+    code = _dtype_code(q)
     kpg, vpg, num_pages, Hkv, page, cache_d = _pages_q4(k_pages, v_pages, dev)
     if cache_d != d:
         raise ValueError(f"the cache holds rows of {cache_d} channels, q of {d}")
@@ -1071,7 +1077,7 @@ def decode_paged_q4(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, ma
     if conf is None and want_conf:
         conf = torch.empty((B, Hq), device=q.device, dtype=f32)
     need = _bytes("polar_attn_decode_paged_q4_workspace_bytes", dev, B, Hq, Hkv, int(max_seq_len),
-                  d, int(num_splits))
+                  d, code, int(num_runs))
     ws, size, _ = _scratch(workspace, need, dev)
     c = _DEFAULT_CONSTS if consts is None else consts
     _call(dev, "polar_attn_decode_paged_q4", lib().polar_attn_decode_paged_q4, q.data_ptr(), kpg,
@@ -1081,7 +1087,7 @@ def decode_paged_q4(q, k_pages, v_pages, block_table, seq_lens, mem, w_count, ma
           _in(_need(w_count, "w_count"), "w_count", f32, (Hq, d), dev),
           _in(out, "out", dt, shape, dev), _in(n_eff, "n_eff", f32, (B, Hq), dev),
           _in(conf, "conf", f32, (B, Hq), dev), B, Hq, Hkv, d, page, num_pages, max_pages,
-          int(max_seq_len), _dtype_code(q), ctypes.byref(c), int(num_splits), ws, size)
+          int(max_seq_len), code, ctypes.byref(c), int(num_runs), ws, size)
     return out, n_eff, conf
 
 

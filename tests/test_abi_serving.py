@@ -160,20 +160,20 @@ def test_append_valid_calls_reach_the_device(L, valid):
 
 
 def decode(L, p=None, B=2, Hq=4, Hkv=2, d=64, page=16, pool=8, cols=4, top=50, dtype=1, c=None,
-           splits=0, ws=A[11], wsb=BIG):
+           runs=0, ws=A[11], wsb=BIG):
     a = dict(enumerate(A))
     a.update(p or {})
     return L.polar_attn_decode_paged_q4(*[a[i] for i in range(10)], B, Hq, Hkv, d, page, pool, cols,
-                                        top, dtype, c, splits, ws, wsb, NULL)
+                                        top, dtype, c, runs, ws, wsb, NULL)
 
 
 def test_decode_q4_refusals(L):
     import long_context_attention_causal_gb300 as pa
-    assert decode(L, B=-1) == 1 and decode(L, splits=-1) == 1 and decode(L, pool=0) == 1
+    assert decode(L, B=-1) == 1 and decode(L, runs=-1) == 1 and decode(L, pool=0) == 1
     assert decode(L, top=0) == 1 and decode(L, top=65) == 1 and decode(L, cols=0) == 1
     assert decode(L, Hq=6) == 2 and decode(L, Hq=3) == 2 and decode(L, Hq=32) == 2
     assert decode(L, d=96) == 2 and decode(L, dtype=2) == 2 and decode(L, page=4) == 2
-    assert decode(L, page=48) == 2 and decode(L, pool=1 << 28) == 2 and decode(L, splits=70000) == 2
+    assert decode(L, page=48) == 2 and decode(L, pool=1 << 28) == 2 and decode(L, runs=(1 << 20) + 1) == 2
     assert decode(L, B=0) == 0
     bad = pa.Consts(math.log(2048.0), -1.0, 1.0, 1e-6, 1)
     assert decode(L, c=ctypes.byref(bad)) == 1
@@ -189,11 +189,15 @@ def test_decode_q4_refusals(L):
 
 def test_decode_q4_workspace(L, valid):
     n = L.polar_attn_decode_paged_q4_workspace_bytes
-    assert n(2, 4, 2, 50, 64, 3) == 2 * 4 * 3 * 68 * 4
-    assert n(2, 6, 2, 50, 64, 0) == 0 and n(2, 4, 2, 0, 64, 0) == 0 and n(2, 4, 2, 50, 64, -1) == 0
-    s = L.polar_attn_decode_paged_q4_num_splits(2, 2, 5000, 64)
-    assert s >= 1 and n(2, 4, 2, 5000, 64, 0) == 2 * 4 * s * 68 * 4
-    assert L.polar_attn_decode_paged_q4_num_splits(2, 2, 0, 64) == 0
+    assert n(2, 4, 2, 50, 64, 1, 3) == (3 + 4) * 2 * 68 * 4 + 4 * 8
+    assert n(2, 6, 2, 50, 64, 1, 0) == 0 and n(2, 4, 2, 0, 64, 1, 0) == 0
+    assert n(2, 4, 2, 50, 64, 1, -1) == 0 and n(2, 4, 2, 50, 64, 2, 0) == 0
+    runs = L.polar_attn_decode_paged_q4_num_runs
+    for dtype in (0, 1):
+        s = runs(2, 2, 5000, dtype)
+        assert s >= 1 and n(2, 4, 2, 5000, 64, dtype, 0) == (s + 4) * 2 * 68 * 4 + 4 * 8
+    assert runs(1, 2, 300, 1) == 6 and runs(0, 2, 300, 1) == 1   # a stage is 128 keys
+    assert runs(2, 2, 0, 1) == 0 and runs(2, 2, 50, 5) == 0
     assert decode(L) == valid
 
 

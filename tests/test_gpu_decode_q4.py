@@ -63,13 +63,13 @@ def check(args, values, got, dtype, rows=None):
     (16, 2, [777, 128, 129, 127], 64, 64), (4, 2, [1500, 1], 128, 128), (8, 8, [4000, 33], 128, 256),
     (32, 4, [1100, 1024, 1], 64, 1024), (6, 3, [513, 2500], 128, 32)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("splits", [0, 1, 5])
-def test_decode(Hq, Hkv, lens, d, page, dtype, splits):
+@pytest.mark.parametrize("runs", [0, 1, 5, 700])
+def test_decode(Hq, Hkv, lens, d, page, dtype, runs):
     import long_context_attention_causal_gb300 as pa
     args, values = case(len(lens), Hq, Hkv, lens, d, page, dtype, 7 + d + len(lens))
-    got = pa.decode_paged_q4(*args, max_seq_len=max(lens), num_splits=splits, want_conf=True)
+    got = pa.decode_paged_q4(*args, max_seq_len=max(lens), num_runs=runs, want_conf=True)
     check(args, values, got, dtype)
-    again = pa.decode_paged_q4(*args, max_seq_len=max(lens), num_splits=splits, want_conf=True)
+    again = pa.decode_paged_q4(*args, max_seq_len=max(lens), num_runs=runs, want_conf=True)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
     assert pa.device_status() == 0
 
@@ -90,7 +90,7 @@ def test_growing_and_peaked_logits(dtype):
         pa.cache_append_q4(k, v, slots, args[1], args[2])
         k, v = pa.cache_read_q4(args[1], args[2], slots, dtype=torch.float32)
         values[b] = (k.transpose(0, 1), v.transpose(0, 1))
-    got = pa.decode_paged_q4(*args, max_seq_len=1300, num_splits=2, want_conf=True)
+    got = pa.decode_paged_q4(*args, max_seq_len=1300, num_runs=5, want_conf=True)
     check(args, values, got, dtype)
 
 
@@ -126,6 +126,12 @@ def test_nan_row_reaches_its_sequence_only():
     slot = (args[3][1, 3] * 16 + 5).view(1)
     bad = torch.full((1, 2, 64), float("nan"), device=dev())
     pa.cache_append_q4(bad, bad, slot, args[1], args[2])
+    got = pa.decode_paged_q4(*args, max_seq_len=150, want_conf=True)
+    check(args, values, got, "bf16", rows=[0, 2])
+    assert got[0][1].isnan().all()
+    # the only key of a sequence
+    args[4][1] = 1
+    pa.cache_append_q4(bad, bad, args[3][1, :1] * 16, args[1], args[2])
     got = pa.decode_paged_q4(*args, max_seq_len=150, want_conf=True)
     check(args, values, got, "bf16", rows=[0, 2])
     assert got[0][1].isnan().all()
