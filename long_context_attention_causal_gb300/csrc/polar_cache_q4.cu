@@ -54,10 +54,8 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// Slot of token t: the page and its row, or false (negative: no slot; past
-// the pool: recorded).
-__device__ __forceinline__ bool place(const Q4Args& a, long long t, long long& page, int& row) {
-  const int slot = __ldg(a.slots + t);
+// Page and row of a slot, or false (negative: none; past the pool: recorded).
+__device__ __forceinline__ bool place(const Q4Args& a, int slot, int& page, int& row) {
   page = slot >> a.shift;
   row = slot & ((1 << a.shift) - 1);
   if (slot < 0) return false;
@@ -68,84 +66,137 @@ __device__ __forceinline__ bool place(const Q4Args& a, long long t, long long& p
   return true;
 }
 
+// The word of codes of x[0..7] for a scale s in the range where 1 / s and the
+// borders below keep their bits.  |x| (1 / s) + 2^23, rounded down, holds m = floor
+// (|x| / s), or a neighbour where |x| / s is near an integer; either way |n| is m
+// or m + 1, and the border between them, (m + 1/2) s, is exact in fp32 (8 bits by
+// 4).  A tie goes to the even one: as integers, the bits of |x| plus m's parity
+// are compared with the border's.
+__device__ __forceinline__ uint32_t q4_word(const float (&x)[8], float s) {
+  constexpr float kTwo23 = 8388608.0f;
+  constexpr uint32_t kBits = 0x4B000000u;  // of 2^23
+  const float inv = 1.0f / s, h = 0.5f * s;
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int at = q4_at(i & 3) + 16 * (i >> 2), sign = 15 - 4 * (i & 3) + 16 * (i >> 2);
+    const uint32_t bits = __float_as_uint(x[i]), size = bits & 0x7FFFFFFFu;
+    const float t = __fmaf_rz(__uint_as_float(size), inv, kTwo23);
+    const uint32_t tb = __float_as_uint(t);
+    const uint32_t border = __float_as_uint(fmaf(t - kTwo23, s, h));
+    word += (tb - kBits) << at;
+    if (size + (tb & 1u) > border) word += 1u << at;
+    word |= (bits & 0x80000000u) >> (31 - sign);
+  }
+  return word;
+}
+
+// The same for any scale s > 0, in fp64 (near the subnormal range).
+__device__ __noinline__ uint32_t q4_word_small(float x0, float x1, float x2, float x3, float x4,
+                                               float x5, float x6, float x7, float s) {
+  const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t n = (uint32_t)fmin(rint(fabs((double)x[i]) / (double)s), 7.0);
+    word |= n << (q4_at(i & 3) + 16 * (i >> 2));
+    word |= (__float_as_uint(x[i]) & 0x80000000u) >> (16 + 4 * (i & 3) - 16 * (i >> 2));
+  }
+  return word;
+}
+
+// Rows of k (blockIdx.y 0) and v (1), (token, head) by (token, head), W threads a
+// row and kBatch rows a thread, whose loads are in flight together.
+constexpr int kBatch = 2;
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const Q4Args a) {
   constexpr int W = D / 8;  // words (threads) of a row
+  constexpr int R = kThreads / W;
   const bool is_v = blockIdx.y != 0;
-  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long th = id / W;  // (token, head)
-  const int w = (int)(id % W);
-  const bool in = th < (long long)a.N * a.Hkv;  // the same for a group's threads
-  long long page = 0;
-  int row = 0;
-  const long long token = in ? th / a.Hkv : 0;
-  const int head = in ? (int)(th - token * a.Hkv) : 0;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (in)
-    load8(static_cast<const T*>(is_v ? a.rows[1] : a.rows[0]) +
-              token * (is_v ? a.stride[1] : a.stride[0]) + head * D + 8 * w, x);
-  const bool ok = in && place(a, token, page, row);
-  uint32_t top = 0;
+  const int w = threadIdx.x % W;
+  const uint32_t rows = (uint32_t)a.N * (uint32_t)a.Hkv;
+  const T* src = static_cast<const T*>(is_v ? a.rows[1] : a.rows[0]) + 8 * w;
+  const long long stride = is_v ? a.stride[1] : a.stride[0];
+  float x[kBatch][8];
+  int slot[kBatch], head[kBatch];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const bool finite = top < 0x7F800000u;
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
-  const float s = __bfloat162float(sb);
-  uint32_t code = 0;
-  if (finite && s > 1e-30f) {
-    const float inv = 1.0f / s;
+  for (int u = 0; u < kBatch; ++u) {
+    const uint32_t id = (blockIdx.x * kBatch + u) * R + threadIdx.x / W;
+    const uint32_t token = id / (uint32_t)a.Hkv;
+    head[u] = (int)(id - token * (uint32_t)a.Hkv);
+    slot[u] = -1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) code |= q4_code(q4_round(x[i], s, inv), i & 3) << (16 * (i >> 2));
-  } else if (finite && s > 0.f) {
-    // near the subnormal range 1 / s and the remainder lose bits
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double n = fmin(fmax(rint((double)x[i] / (double)s), -7.0), 7.0);
-      code |= q4_code((int)n, i & 3) << (16 * (i >> 2));
+    for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
+    if (id < rows) {  // the same for a group's threads
+      load8(src + (long long)token * stride + head[u] * D, x[u]);
+      slot[u] = __ldg(a.slots + token);
     }
   }
-  if (!ok) return;
-  uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head, a.Hkv, a.shift, D);
-  reinterpret_cast<uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)] = code;
-  if ((w & 3) == 0) {
-    uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
-    const uint16_t bits = finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FFF;
-    reinterpret_cast<uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] = bits;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[u][i]) & 0x7FFFFFFFu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const bool finite = top < 0x7F800000u;
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
+    const float s = __bfloat162float(sb);
+    uint32_t code = 0;
+    if (finite && s > 1e-30f) code = q4_word(x[u], s);
+    else if (finite && s > 0.f)
+      code = q4_word_small(x[u][0], x[u][1], x[u][2], x[u][3], x[u][4], x[u][5], x[u][6], x[u][7], s);
+    int page, row;
+    if (!place(a, slot[u], page, row)) continue;
+    uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head[u], a.Hkv, a.shift, D);
+    reinterpret_cast<uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)] = code;
+    if ((w & 3) == 0) {
+      uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
+      const uint16_t bits = finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FFF;
+      reinterpret_cast<uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] = bits;
+    }
   }
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Args a) {
   constexpr int W = D / 8;
+  constexpr int R = kThreads / W;
   const bool is_v = blockIdx.y != 0;
-  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long th = id / W;
-  const int w = (int)(id % W);
-  if (th >= (long long)a.N * a.Hkv) return;
-  const long long token = th / a.Hkv;
-  const int head = (int)(th - token * a.Hkv);
-  long long page;
-  int row;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (place(a, token, page, row)) {
-    const uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head, a.Hkv, a.shift, D);
-    const uint32_t code =
-        reinterpret_cast<const uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)];
-    const uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
-    const float s = __uint_as_float(
-        (uint32_t)reinterpret_cast<const uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] << 16);
+  const int w = threadIdx.x % W;
+  const uint32_t rows = (uint32_t)a.N * (uint32_t)a.Hkv;
+  const uint8_t* pages = is_v ? a.pages[1] : a.pages[0];
+  uint32_t code[kBatch], scale[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = s * (float)q4_value(code >> (16 * (i >> 2)), i & 3);
+  for (int u = 0; u < kBatch; ++u) {
+    const uint32_t id = (blockIdx.x * kBatch + u) * R + threadIdx.x / W;
+    code[u] = scale[u] = 0;
+    int page, row;
+    if (id < rows && place(a, __ldg(a.slots + id / (uint32_t)a.Hkv), page, row)) {
+      const uint8_t* block =
+          pages + q4_block(page, (int)(id % (uint32_t)a.Hkv), a.Hkv, a.shift, D);
+      code[u] = reinterpret_cast<const uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)];
+      const uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
+      scale[u] = reinterpret_cast<const uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2];
+    }
   }
-  store8(static_cast<T*>(is_v ? a.out[1] : a.out[0]) + (token * a.Hkv + head) * D + 8 * w, x);
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const uint32_t id = (blockIdx.x * kBatch + u) * R + threadIdx.x / W;
+    if (id >= rows) break;
+    const float s = __uint_as_float(scale[u] << 16);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = s * (float)q4_value(code[u] >> (16 * (i >> 2)), i & 3);
+    store8(static_cast<T*>(is_v ? a.out[1] : a.out[0]) + (size_t)id * D + 8 * w, x);
+  }
 }
 
 template <bool kRead>
 cudaError_t launch(const Q4Args& a, int d, int dtype, cudaStream_t s) {
-  const long long threads = (long long)a.N * a.Hkv * (d / 8);
-  const dim3 grid((unsigned)((threads + kThreads - 1) / kThreads), 2);
+  const long long rows = (long long)a.N * a.Hkv, per = (long long)kBatch * (kThreads / (d / 8));
+  const dim3 grid((unsigned)((rows + per - 1) / per), 2);
 #define POLAR_Q4(D, T)                                       \
   if (kRead) q4_read_kernel<D, T><<<grid, kThreads, 0, s>>>(a); \
   else q4_append_kernel<D, T><<<grid, kThreads, 0, s>>>(a)
@@ -167,7 +218,7 @@ int check(const Q4Args& a, int d, int page_size, int dtype, int* shift) {
   if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
     return POLAR_ERR_UNSUPPORTED;
   if ((long long)a.num_pages * page_size > INT_MAX || a.Hkv > 4096 ||
-      (long long)a.N * a.Hkv > (long long)INT_MAX * 8)
+      (long long)a.N * a.Hkv > INT_MAX)
     return POLAR_ERR_UNSUPPORTED;
   *shift = 0;
   while ((1 << *shift) < page_size) ++*shift;

@@ -31,27 +31,12 @@ __device__ __forceinline__ size_t q4_block(long long page, int head, int Hkv, in
 // Place of word w (channels 8 w .. 8 w + 7) in its row.
 __device__ __forceinline__ int q4_place(int w, int d) { return (w & 3) * (d / 32) + (w >> 2); }
 
-// Sign and size of channel j (0..3) in its 16 bits.
-__device__ __forceinline__ uint32_t q4_code(int n, int j) {
-  const uint32_t size = (uint32_t)(n < 0 ? -n : n);
-  const int at = j == 0 ? 4 : j == 1 ? 0 : j == 2 ? 12 : 8;
-  return (size << at) | (n < 0 ? 0x8000u >> (4 * j) : 0u);
-}
-__device__ __forceinline__ int q4_value(uint32_t piece, int j) {
-  const int at = j == 0 ? 4 : j == 1 ? 0 : j == 2 ? 12 : 8;
-  const int size = (int)(piece >> at) & 7;
-  return (piece & (0x8000u >> (4 * j))) ? -size : size;
-}
+// Bit of |n| of channel j (0..3) in its 16 bits; its sign is bit 15 - 4 j.
+__host__ __device__ constexpr int q4_at(int j) { return j == 0 ? 4 : j == 1 ? 0 : j == 2 ? 12 : 8; }
 
-// n of x for a scale s > 0 (exact: the nearest integer to x / s, ties to even).
-// x * inv is within 2^-22 of x / s, so m is that integer or, near a border, its
-// neighbour; the remainder x - m s is exact there and decides.
-__device__ __forceinline__ int q4_round(float x, float s, float inv) {
-  const float m = rintf(x * inv);
-  const float r = fmaf(-m, s, x), h = 0.5f * s;
-  int n = (int)m;
-  if (fabsf(r) > h || (fabsf(r) == h && (n & 1))) n += r > 0.f ? 1 : -1;
-  return n;
+__device__ __forceinline__ int q4_value(uint32_t piece, int j) {
+  const int size = (int)(piece >> q4_at(j)) & 7;
+  return (piece & (0x8000u >> (4 * j))) ? -size : size;
 }
 
 }  // namespace polar

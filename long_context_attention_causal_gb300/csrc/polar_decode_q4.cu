@@ -595,8 +595,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 template <int D, int kParts, typename T>
 __global__ void __launch_bounds__(D* kParts) polar_decode_q4_combine_kernel(const Q4DecodeParams p) {
   constexpr int R = D + 4;
-  __shared__ float4 head[kParts];  // m, l, Q2 of a group's records
-  __shared__ float acc[kParts][D];
   const int G = p.Hq / p.Hkv, b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
   const int x = threadIdx.x % D, part = threadIdx.x / D;
   bool bad = false;
@@ -611,35 +609,62 @@ __global__ void __launch_bounds__(D* kParts) polar_decode_q4_combine_kernel(cons
   const float* rec = p.records + ((size_t)s.x * G + h % G) * R;
   const size_t step = (size_t)G * R;
   const int n = s.y - s.x + 1;
-  // a group's own maximum and sums; every thread of it keeps them
   float M = -INFINITY, a = 0.f, L = 0.f, Q = 0.f;
+  if constexpr (kParts == 1) {
+    // a few records: every thread reads the heads of all
 #pragma unroll 4
-  for (int i = part; i < n; i += kParts) M = fmaxf(M, rec[i * step]);
+    for (int i = 0; i < n; ++i) M = fmaxf(M, rec[i * step]);
 #pragma unroll 4
-  for (int i = part; i < n; i += kParts) {
-    const float4 r = *reinterpret_cast<const float4*>(rec + i * step);
-    const float v = rec[i * step + 4 + x];
-    // a segment without visible keys weighs 0
-    const float e = r.x == -INFINITY ? 0.f : expf(r.x - M);
-    a = fmaf(e, v, a);
-    L = fmaf(e, r.y, L);
-    Q = fmaf(e * e, r.z, Q);  // squared correction factor
-  }
-  if constexpr (kParts > 1) {
-    if (x == 0) head[part] = make_float4(M, L, Q, 0.f);
+    for (int i = 0; i < n; ++i) {
+      const float4 r = *reinterpret_cast<const float4*>(rec + i * step);
+      const float v = rec[i * step + 4 + x];
+      // a segment without visible keys weighs 0
+      const float e = r.x == -INFINITY ? 0.f : expf(r.x - M);
+      a = fmaf(e, v, a);
+      L = fmaf(e, r.y, L);
+      Q = fmaf(e * e, r.z, Q);  // squared correction factor
+    }
+  } else {
+    // many: their weights once, in shared memory, then a group's share of acc
+    constexpr int N = D * kParts;
+    __shared__ float weight[N], red[3][N / 32];
+    __shared__ float acc[kParts][D];
+    auto over_block = [&](float v, int k, auto join) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+      if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = v;
+    };
+    auto larger = [](float u, float v) { return fmaxf(u, v); };
+    auto sum = [](float u, float v) { return u + v; };
+    for (int i = threadIdx.x; i < n; i += N) M = fmaxf(M, rec[i * step]);
+    over_block(M, 0, larger);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N / 32; ++i) M = fmaxf(M, red[0][i]);
+    for (int i0 = 0; i0 < n; i0 += N) {
+      const int m = min(N, n - i0);
+      __syncthreads();  // the last weights are read
+      if ((int)threadIdx.x < m) {
+        const float4 r = *reinterpret_cast<const float4*>(rec + (i0 + threadIdx.x) * step);
+        const float e = r.x == -INFINITY ? 0.f : expf(r.x - M);
+        weight[threadIdx.x] = e;
+        L = fmaf(e, r.y, L);
+        Q = fmaf(e * e, r.z, Q);
+      }
+      __syncthreads();
+#pragma unroll 8
+      for (int i = part; i < m; i += kParts) a = fmaf(weight[i], rec[(i0 + i) * step + 4 + x], a);
+    }
+    over_block(L, 1, sum);
+    over_block(Q, 2, sum);
     acc[part][x] = a;
     __syncthreads();
     if (part != 0) return;
-    for (int i = 1; i < kParts; ++i) M = fmaxf(M, head[i].x);
     a = L = Q = 0.f;
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-      const float4 r = head[i];
-      const float e = r.x == -INFINITY ? 0.f : expf(r.x - M);
-      a = fmaf(e, acc[i][x], a);
-      L = fmaf(e, r.y, L);
-      Q = fmaf(e * e, r.z, Q);
-    }
+    for (int i = 0; i < kParts; ++i) a += acc[i][x];
+#pragma unroll
+    for (int i = 0; i < N / 32; ++i) L += red[1][i], Q += red[2][i];
   }
   float acc_sq = a * a, q_sq = qx * qx;
 #pragma unroll

@@ -6,10 +6,11 @@
 //   need_b = ceil((len_b + new_b) / P) - ceil(len_b / P)
 // pages; it gets them from the top of a stack of free pages, in the order of
 // the sequences, if its own and all earlier needs fit what the stack holds.
-// Both sums over b are scans.  The work is a few bytes a sequence and a token
-// and is bound by launch and load latency, so a small call is one launch of
-// one block, which scans and then fills; a large one adds a grid that fills
-// (a programmatic launch, its tokens found by a search in the offsets).
+// Both sums over b are scans, made together.  The work is a few bytes a sequence
+// and a token and is bound by launch and load latency, so a small call is one
+// launch of one block, which scans and then fills, its offsets in shared memory;
+// a large one adds a grid that fills (a programmatic launch; a token's sequence
+// is found by a search in the offsets).
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -22,8 +23,9 @@ namespace polar {
 
 namespace {
 
-constexpr int kScan = 1024;  // threads of the scan
+constexpr int kScan = 1024;  // threads of the scan, at most
 constexpr int kFill = 256;
+constexpr int kHeld = 2048;  // sequences whose offsets fit shared memory
 
 struct PagesArgs {
   int* table;        // [B, max_pages]
@@ -40,26 +42,28 @@ struct PagesArgs {
   int* status;
 };
 
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+struct Two {
+  long long x, y;
+};
+
+// Inclusive scans of x and y over the block, `total` their last values.
+__device__ __forceinline__ Two block_scan(Two v, Two* part, Two& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const long long x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+    if (lane >= o) v.x += x, v.y += y;
   }
-  return v;
-}
-
-// Inclusive scan over the block, `total` its last value.
-__device__ __forceinline__ long long block_scan(long long v, long long* part, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long own = warp_scan(v, lane);
   __syncthreads();  // the previous scan's reads of part are over
-  if (lane == 31) part[warp] = own;
+  if (lane == 31) part[warp] = v;
   __syncthreads();
-  if (warp == 0) part[lane] = warp_scan(part[lane], lane);
-  __syncthreads();
-  total = part[31];
-  return own + (warp ? part[warp - 1] : 0);
+  total = Two{0, 0};
+  Two before{0, 0};
+  for (int w = 0; w < warps; ++w) {
+    if (w == warp) before = total;
+    total.x += part[w].x, total.y += part[w].y;
+  }
+  return Two{before.x + v.x, before.y + v.y};
 }
 
 __device__ __forceinline__ void flag(const PagesArgs& a) { atomicExch(a.status, 3); }
@@ -76,13 +80,15 @@ __device__ __forceinline__ int find(int B, int i, F start) {
   return lo;
 }
 
-__device__ __forceinline__ void fill_token(const PagesArgs& a, int t, int total) {
+// cu, plan: the arguments' arrays, or copies of them in shared memory
+__device__ __forceinline__ void fill_token(const PagesArgs& a, const int* cu, const int2* plans,
+                                           int t, int total) {
   int slot = -1, pos = 0;
   if (t < total) {
-    const int b = find(a.B, t, [&](int x) { return a.cu[x]; });
-    const int2 plan = a.plan[b];
+    const int b = find(a.B, t, [&](int x) { return cu[x]; });
+    const int2 plan = plans[b];
     if (plan.x >= 0) {
-      pos = plan.x + t - a.cu[b];
+      pos = plan.x + t - cu[b];
       const int page = pos >> a.shift, mask = (1 << a.shift) - 1;
       const int held = (plan.x + mask) >> a.shift;  // pages before this call
       int id;
@@ -104,21 +110,23 @@ __device__ __forceinline__ void fill_token(const PagesArgs& a, int t, int total)
   a.slots[t] = slot;
 }
 
-__device__ __forceinline__ void fill_freed(const PagesArgs& a, int i) {
-  const int b = find(a.B, i, [&](int x) { return a.plan[x].y; });
-  const int2 plan = a.plan[b];
-  const int at = a.plan[a.B].y + i;
+__device__ __forceinline__ void fill_freed(const PagesArgs& a, const int2* plans, int top, int i) {
+  const int b = find(a.B, i, [&](int x) { return plans[x].y; });
+  const int2 plan = plans[b];
   int id = a.table[(size_t)b * a.max_pages + plan.x + i - plan.y];
   if (id < 0 || id >= a.num_pages) {
     flag(a);
     id = -1;
   }
-  if (at < a.capacity) a.free_pages[at] = id;
+  if (top + i < a.capacity) a.free_pages[top + i] = id;
 }
 
+// kAlone: the block fills too (its sequences fit kHeld)
 template <bool kExtend, bool kAlone>
 __global__ void __launch_bounds__(kScan) pages_scan_kernel(const PagesArgs a) {
-  __shared__ long long part[32];
+  __shared__ Two part[32];
+  __shared__ int cu_held[kAlone && kExtend ? kHeld : 1];
+  __shared__ int2 plan_held[kAlone ? kHeld : 1];
   if (!kAlone) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int mask = (1 << a.shift) - 1;
   int count = *a.count;
@@ -126,9 +134,11 @@ __global__ void __launch_bounds__(kScan) pages_scan_kernel(const PagesArgs a) {
     if (threadIdx.x == 0) flag(a);
     count = count < 0 ? 0 : a.capacity;
   }
-  long long tokens = 0, pages = 0, taken = 0;  // sums over the sequences so far
+  auto pages_of = [&](long long rows) { return (rows + mask) >> a.shift; };
+  Two run{0, 0};        // extend: tokens, pages; release: -, pages of the sequences so far
+  long long taken = 0;  // pages of this thread's sequences that got them
   if (kExtend && threadIdx.x == 0) a.cu[0] = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kScan) {
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
     const int b = b0 + (int)threadIdx.x;
     const bool in = b < a.B;
     int len = in ? a.lens[b] : 0, next = in ? a.next[b] : 0;
@@ -138,78 +148,112 @@ __global__ void __launch_bounds__(kScan) pages_scan_kernel(const PagesArgs a) {
       flag(a);
       next = kExtend ? 0 : len;  // such a sequence is left as it is
     }
-    long long total;
+    Two total;
     if (kExtend) {
-      const long long end = tokens + block_scan(next, part, total);
-      const bool fits = !bad && (long long)len + next <= most && end <= a.tokens;
-      if (!bad && !fits) flag(a);
-      if (in) a.cu[b + 1] = (int)min(end, (long long)a.tokens);
-      tokens += total;
-      const long long need = fits ? ((len + (long long)next + mask) >> a.shift) -
-                                        (((long long)len + mask) >> a.shift)
-                                  : 0;
-      const long long upto = pages + block_scan(need, part, total);
-      const bool ok = fits && (need == 0 || upto <= count);
-      pages += total;
-      if (in) {
-        a.plan[b] = make_int2(ok ? len : -1, (int)(count - 1 - (upto - need)));
-        a.lens_out[b] = ok ? len + next : len;
+      const bool room = !bad && (long long)len + next <= most;
+      long long need = room ? pages_of((long long)len + next) - pages_of(len) : 0;
+      Two upto = block_scan(Two{next, need}, part, total);
+      upto.x += run.x;
+      bool fits = room && upto.x <= a.tokens;
+      if (run.x + total.x > a.tokens) {
+        // sequences past max_tokens need no pages: their sums once more
+        if (!fits) need = 0;
+        Two again;
+        upto.y = block_scan(Two{0, need}, part, again).y;
+        total.y = again.y;
       }
-      block_scan(ok ? need : 0, part, total);
-      taken += total;
-    } else {
-      const long long keep = ((long long)next + mask) >> a.shift;
-      const long long give = bad ? 0 : (((long long)len + mask) >> a.shift) - keep;
-      const long long upto = pages + block_scan(give, part, total);
-      pages += total;
+      upto.y += run.y;
+      if (!bad && !fits) flag(a);
+      const bool ok = fits && (need == 0 || upto.y <= count);
+      if (ok) taken += need;
       if (in) {
-        a.plan[b] = make_int2((int)keep, (int)(upto - give));
+        const int end = (int)min(upto.x, (long long)a.tokens);
+        const int2 plan = make_int2(ok ? len : -1, (int)(count - 1 - (upto.y - need)));
+        a.cu[b + 1] = end;
+        a.lens_out[b] = ok ? len + next : len;
+        if (kAlone) {
+          plan_held[b] = plan;
+          if (b + 1 < a.B) cu_held[b + 1] = end;
+          if (b == 0) cu_held[0] = 0;
+        } else {
+          a.plan[b] = plan;
+        }
+      }
+    } else {
+      const long long keep = pages_of(next), give = bad ? 0 : pages_of(len) - keep;
+      const long long upto = run.y + block_scan(Two{0, give}, part, total).y;
+      if (in) {
+        const int2 plan = make_int2((int)keep, (int)(upto - give));
         a.lens_out[b] = next;
+        if (kAlone) plan_held[b] = plan;
+        else a.plan[b] = plan;
       }
     }
+    run.x += total.x, run.y += total.y;
   }
-  const int fill = kExtend ? (int)min(tokens, (long long)a.tokens) : (int)pages;
+  if (kExtend) {
+    Two total;
+    block_scan(Two{0, taken}, part, total);
+    taken = total.y;
+  }
+  const int fill = kExtend ? (int)min(run.x, (long long)a.tokens) : (int)run.y;
   if (threadIdx.x == 0) {
-    a.plan[a.B] = make_int2(fill, count);
-    if (!kExtend && count + pages > a.capacity) flag(a);
-    *a.count_out = kExtend ? (int)(count - taken)
-                           : (int)min(count + pages, (long long)a.capacity);
+    if (!kAlone) a.plan[a.B] = make_int2(fill, count);
+    if (!kExtend && count + run.y > a.capacity) flag(a);
+    *a.count_out =
+        kExtend ? (int)(count - taken) : (int)min(count + run.y, (long long)a.capacity);
   }
   if (kAlone) {
-    __syncthreads();  // the block's own plan and offsets
+    __syncthreads();  // plans and offsets
     if (kExtend) {
-      for (int t = threadIdx.x; t < a.tokens; t += kScan) fill_token(a, t, fill);
+      for (int t = threadIdx.x; t < a.tokens; t += blockDim.x)
+        fill_token(a, cu_held, plan_held, t, fill);
     } else {
-      for (int i = threadIdx.x; i < fill; i += kScan) fill_freed(a, i);
+      for (int i = threadIdx.x; i < fill; i += blockDim.x) fill_freed(a, plan_held, count, i);
     }
   }
 }
 
 template <bool kExtend>
 __global__ void __launch_bounds__(kFill) pages_fill_kernel(const PagesArgs a) {
+  __shared__ int cu_held[kExtend ? kHeld : 1];
+  __shared__ int2 plan_held[kHeld];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int total = a.plan[a.B].x;
-  const int end = kExtend ? a.tokens : total;
+  const int2 all = a.plan[a.B];
+  const int total = all.x, end = kExtend ? a.tokens : total;
+  const bool held = a.B <= kHeld;
+  if (held) {
+    for (int b = threadIdx.x; b < a.B; b += kFill) {
+      plan_held[b] = a.plan[b];
+      if (kExtend) cu_held[b] = a.cu[b];
+    }
+    __syncthreads();
+  }
+  const int2* plan = held ? plan_held : a.plan;
+  const int* cu = held && kExtend ? cu_held : a.cu;
   const long long step = (long long)gridDim.x * kFill;
   for (long long i = (long long)blockIdx.x * kFill + threadIdx.x; i < end; i += step) {
-    if (kExtend) fill_token(a, (int)i, total);
-    else fill_freed(a, (int)i);
+    if (kExtend) fill_token(a, cu, plan, (int)i, total);
+    else fill_freed(a, plan, all.y, (int)i);
   }
 }
 
 template <bool kExtend>
 cudaError_t launch(const PagesArgs& a, long long items, int sms, cudaStream_t s) {
-  // One block fills about 1000 items a microsecond; a second launch costs
-  // less from a few thousand on.
-  if (items <= 4096) {
-    pages_scan_kernel<kExtend, true><<<1, kScan, 0, s>>>(a);
+  // One block fills some thousand items in the time of a second launch (and
+  // releases are a few of the entries that `items` allows for).
+  const bool alone = a.B <= kHeld && items <= (kExtend ? 4096 : 16384);
+  const long long width = alone ? std::max((long long)a.B, std::min(items, (long long)kScan)) : a.B;
+  const int threads = (int)std::min((width + 31) / 32 * 32, (long long)kScan);
+  if (alone) {
+    pages_scan_kernel<kExtend, true><<<1, threads, 0, s>>>(a);
     return cudaGetLastError();
   }
-  pages_scan_kernel<kExtend, false><<<1, kScan, 0, s>>>(a);
+  pages_scan_kernel<kExtend, false><<<1, threads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min((items + kFill - 1) / kFill, 8LL * sms));
+  cfg.gridDim = dim3((unsigned)std::min((items + kFill - 1) / kFill, 6LL * sms));
   cfg.blockDim = dim3(kFill);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
