@@ -66,6 +66,15 @@ __device__ __forceinline__ bool place(const Q4Args& a, int slot, int& page, int&
   return true;
 }
 
+// Nearest bf16 (ties to even) to top / 7, top in the normal range, as its bits: the
+// upper half of the bits of top (1 / 7) is it or its neighbour below or above, and
+// seven times the border between two neighbours is exact in fp32 (9 bits by 3).
+__device__ __forceinline__ uint32_t q4_scale(float top) {
+  const uint32_t low = __float_as_uint(top * (1.0f / 7.0f)) >> 16;
+  const uint32_t border = __float_as_uint(__uint_as_float(low << 16 | 0x8000u) * 7.0f);
+  return low + (__float_as_uint(top) + (low & 1u) > border ? 1u : 0u);
+}
+
 // The word of codes of x[0..7] for a scale s in the range where 1 / s and the
 // borders below keep their bits.  |x| (1 / s) + 2^23, rounded down, holds m = floor
 // (|x| / s), or a neighbour where |x| / s is near an integer; either way |n| is m
@@ -75,18 +84,26 @@ __device__ __forceinline__ bool place(const Q4Args& a, int slot, int& page, int&
 __device__ __forceinline__ uint32_t q4_word(const float (&x)[8], float s) {
   constexpr float kTwo23 = 8388608.0f;
   constexpr uint32_t kBits = 0x4B000000u;  // of 2^23
-  const float inv = 1.0f / s, h = 0.5f * s;
-  uint32_t word = 0;
+  const float h = 0.5f * s;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  uint32_t word = 0, excess = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int at = q4_at(i & 3) + 16 * (i >> 2), sign = 15 - 4 * (i & 3) + 16 * (i >> 2);
-    const uint32_t bits = __float_as_uint(x[i]), size = bits & 0x7FFFFFFFu;
+    const int at = q4_at(i & 3) + 16 * (i >> 2);
+    const uint32_t size = __float_as_uint(x[i]) & 0x7FFFFFFFu;
     const float t = __fmaf_rz(__uint_as_float(size), inv, kTwo23);
     const uint32_t tb = __float_as_uint(t);
     const uint32_t border = __float_as_uint(fmaf(t - kTwo23, s, h));
-    word += (tb - kBits) << at;
+    word += tb << at;
+    excess += kBits << at;
     if (size + (tb & 1u) > border) word += 1u << at;
-    word |= (bits & 0x80000000u) >> (31 - sign);
+  }
+  word -= excess;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int sign = 15 - 4 * (i & 3) + 16 * (i >> 2);
+    word |= (__float_as_uint(x[i]) >> (31 - sign)) & (1u << sign);
   }
   return word;
 }
@@ -106,11 +123,12 @@ __device__ __noinline__ uint32_t q4_word_small(float x0, float x1, float x2, flo
 }
 
 // Rows of k (blockIdx.y 0) and v (1), (token, head) by (token, head), W threads a
-// row and kBatch rows a thread, whose loads are in flight together.
-constexpr int kBatch = 2;
+// row and a batch of rows a thread, whose loads are in flight together.
+constexpr int kAppendBatch = 1, kReadBatch = 2;
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) q4_append_kernel(const Q4Args a) {
+__global__ void __launch_bounds__(kThreads, 6) q4_append_kernel(const Q4Args a) {
+  constexpr int kBatch = kAppendBatch;
   constexpr int W = D / 8;  // words (threads) of a row
   constexpr int R = kThreads / W;
   const bool is_v = blockIdx.y != 0;
@@ -140,27 +158,33 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const Q4Args a) {
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[u][i]) & 0x7FFFFFFFu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const bool finite = top < 0x7F800000u;
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
-    const float s = __bfloat162float(sb);
-    uint32_t code = 0;
-    if (finite && s > 1e-30f) code = q4_word(x[u], s);
-    else if (finite && s > 0.f)
-      code = q4_word_small(x[u][0], x[u][1], x[u][2], x[u][3], x[u][4], x[u][5], x[u][6], x[u][7], s);
+    uint32_t scale = 0, code = 0;
+    if (top >= 0x7F800000u) {
+      scale = 0x7FFF;  // an infinity or NaN: the group reads as NaN
+    } else if (top > 0x10000000u) {  // 2^-95
+      scale = q4_scale(__uint_as_float(top));
+      code = q4_word(x[u], __uint_as_float(scale << 16));
+    } else if (top > 0) {
+      const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
+      scale = __bfloat16_as_ushort(sb);
+      if (scale > 0)
+        code = q4_word_small(x[u][0], x[u][1], x[u][2], x[u][3], x[u][4], x[u][5], x[u][6], x[u][7],
+                             __bfloat162float(sb));
+    }
     int page, row;
     if (!place(a, slot[u], page, row)) continue;
     uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head[u], a.Hkv, a.shift, D);
     reinterpret_cast<uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)] = code;
     if ((w & 3) == 0) {
       uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
-      const uint16_t bits = finite ? __bfloat16_as_ushort(sb) : (uint16_t)0x7FFF;
-      reinterpret_cast<uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] = bits;
+      reinterpret_cast<uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] = (uint16_t)scale;
     }
   }
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Args a) {
+  constexpr int kBatch = kReadBatch;
   constexpr int W = D / 8;
   constexpr int R = kThreads / W;
   const bool is_v = blockIdx.y != 0;
@@ -195,7 +219,8 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Args a) {
 
 template <bool kRead>
 cudaError_t launch(const Q4Args& a, int d, int dtype, cudaStream_t s) {
-  const long long rows = (long long)a.N * a.Hkv, per = (long long)kBatch * (kThreads / (d / 8));
+  const long long rows = (long long)a.N * a.Hkv;
+  const long long per = (long long)(kRead ? kReadBatch : kAppendBatch) * (kThreads / (d / 8));
   const dim3 grid((unsigned)((rows + per - 1) / per), 2);
 #define POLAR_Q4(D, T)                                       \
   if (kRead) q4_read_kernel<D, T><<<grid, kThreads, 0, s>>>(a); \

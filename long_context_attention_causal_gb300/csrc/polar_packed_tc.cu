@@ -197,147 +197,153 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int keep = tile.len - (nkmax - 1) * kBN;
   const bool dirty = nkmax > 0 && keep < kBN;
 
+  // Registers: the softmax warpgroups take 216 a thread, the other keeps 72
+  // (together the 384 x 168 that the block was launched with).
   if (hkv < 0) {
     // more CTAs than tiles: only TMEM to give back
-  } else if (warp == kWarpTMA) {
-    // ------------------------------------------------------ TMA producer --
-    if (lane == 0) {
-      tma_prefetch_desc(&map_q);
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-    }
-    __syncwarp();
-    const int base = tile.start;
-    int nact = 0;
-    for (int t = 0; t < kNQ; ++t) nact += nkv[t] > 0;
-    mbar_arrive_expect_tx_warp(&bars->q_full, nact * L::kTileBytes);
-    for (int t = 0; t < kNQ; ++t) {
-      if (nkv[t] == 0) continue;
-      for (int hh = 0; hh < D / 64; ++hh)
-        tma_load_3d_warp(smem + L::kQOff + t * L::kTileBytes + hh * L::kHalfBytes, &map_q,
-                         &bars->q_full, 64 * hh, hkv * G, base + tok0[t]);
-    }
-    mbar_arrive_expect_tx_warp(&bars->k0_full, L::kTileBytes);
-    for (int hh = 0; hh < D / 64; ++hh)
-      tma_load_3d_warp(smem + L::kKOff + hh * L::kHalfBytes, &map_k, &bars->k0_full, 64 * hh, hkv,
-                       base);
-    // step j: V_j into V stage j % NS, K_{j+1} into K stage (j + 1) % NS; both
-    // were last used by step j - NS (for j = NS - 1 the K stage held K_0)
-    int issued = 0;
-    bool ok = true;
-    for (int j = 0; j < nkmax && ok; ++j) {
-      const int s = j % NS, sk = (j + 1) % NS;
-      const bool k_next = j + 1 < nkmax;
-      if (j == NS - 1) ok = mbar_wait_warp(&bars->k0_empty, 0, abort_flag, p.status);
-      if (ok && j >= NS)
-        ok = mbar_wait_warp(&bars->step_done[s], (uint32_t)(j / NS - 1) & 1, abort_flag, p.status);
-      if (!ok) break;
-      const bool own = dirty && !k_next;  // the tile that needs zeroing
-      uint64_t* v_bar = own ? &bars->v_last : &bars->kv_full[s];
-      if (own) mbar_arrive_expect_tx_warp(&bars->v_last, L::kTileBytes);
-      mbar_arrive_expect_tx_warp(&bars->kv_full[s],
-                                 ((own ? 0 : 1) + (k_next ? 1 : 0)) * L::kTileBytes);
-      for (int hh = 0; hh < D / 64; ++hh)
-        tma_load_3d_warp(smem + L::kVOff + s * L::kTileBytes + hh * L::kHalfBytes, &map_v, v_bar,
-                         64 * hh, hkv, base + kBN * j);
-      if (k_next)
-        for (int hh = 0; hh < D / 64; ++hh)
-          tma_load_3d_warp(smem + L::kKOff + sk * L::kTileBytes + hh * L::kHalfBytes, &map_k,
-                           &bars->kv_full[s], 64 * hh, hkv, base + kBN * (j + 1));
-      issued = j + 1;
-    }
-    if (!ok) {
-      // aborted: let the copies already issued land before the CTA exits
-      volatile int never = 0;
-      const long long lim = kWaitLimitCycles / 4;
-      for (int j = issued - 1; j >= 0 && j >= issued - NS; --j)
-        mbar_wait(&bars->kv_full[j % NS], (uint32_t)(j / NS) & 1, &never, p.status, lim);
-      if (dirty && issued == nkmax) mbar_wait(&bars->v_last, 0, &never, p.status, lim);
-      mbar_wait(&bars->k0_full, 0, &never, p.status, lim);
-      mbar_wait(&bars->q_full, 0, &never, p.status, lim);
-      __syncwarp();
-    }
-  } else if (warp == kWarpMMA) {
-    // ------------------------------------------------------- MMA issuer --
-    // The whole warp runs the loop, one elected lane issues (polar_device.cuh).
-    constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kBN, 0, 0);
-    constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, D, 0, 1);
-    const uint64_t desc_q = smem_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
-    const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
-    // V: MN-major, LBO = distance between the two 64-column atoms (d = 128)
-    const uint64_t desc_v =
-        smem_desc_sw128(smem_u32(smem + L::kVOff), D == 128 ? L::kHalfBytes : 0, 1024);
-    bool ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.status);
-    bool any_issued = false;
-    auto issue_s = [&](int t, int s) {
-      const uint64_t a0 = desc_q + (uint64_t)((t * L::kTileBytes) >> 4);
-      const uint64_t b0 = desc_k + (uint64_t)((s * L::kTileBytes) >> 4);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = (uint64_t)((kk >> 2) * (L::kHalfBytes >> 4) + (kk & 3) * 2);
-        umma_ss_warp(tmem + 256 * t, a0 + off, b0 + off, kIdescS, kk > 0);
+  } else if (warp >= 4 * kNQ) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kWarpTMA) {
+      // ------------------------------------------------------ TMA producer --
+      if (lane == 0) {
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
       }
-      umma_commit_warp(&bars->s_full[t]);
-    };
-    auto issue_pv = [&](int t, int s, int j) {
-      const uint64_t b0 = desc_v + (uint64_t)((s * L::kTileBytes) >> 4);
-      const uint32_t o_tm = tmem + 256 * t + 128, p_tm = tmem + 256 * t;
-      umma_ts_warp(o_tm, p_tm, b0, kIdescPV, j > 0 ? 1u : 0u);
+      __syncwarp();
+      const int base = tile.start;
+      int nact = 0;
+      for (int t = 0; t < kNQ; ++t) nact += nkv[t] > 0;
+      mbar_arrive_expect_tx_warp(&bars->q_full, nact * L::kTileBytes);
+      for (int t = 0; t < kNQ; ++t) {
+        if (nkv[t] == 0) continue;
+        for (int hh = 0; hh < D / 64; ++hh)
+          tma_load_3d_warp(smem + L::kQOff + t * L::kTileBytes + hh * L::kHalfBytes, &map_q,
+                           &bars->q_full, 64 * hh, hkv * G, base + tok0[t]);
+      }
+      mbar_arrive_expect_tx_warp(&bars->k0_full, L::kTileBytes);
+      for (int hh = 0; hh < D / 64; ++hh)
+        tma_load_3d_warp(smem + L::kKOff + hh * L::kHalfBytes, &map_k, &bars->k0_full, 64 * hh, hkv,
+                         base);
+      // step j: V_j into V stage j % NS, K_{j+1} into K stage (j + 1) % NS; both
+      // were last used by step j - NS (for j = NS - 1 the K stage held K_0)
+      int issued = 0;
+      bool ok = true;
+      for (int j = 0; j < nkmax && ok; ++j) {
+        const int s = j % NS, sk = (j + 1) % NS;
+        const bool k_next = j + 1 < nkmax;
+        if (j == NS - 1) ok = mbar_wait_warp(&bars->k0_empty, 0, abort_flag, p.status);
+        if (ok && j >= NS)
+          ok = mbar_wait_warp(&bars->step_done[s], (uint32_t)(j / NS - 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        const bool own = dirty && !k_next;  // the tile that needs zeroing
+        uint64_t* v_bar = own ? &bars->v_last : &bars->kv_full[s];
+        if (own) mbar_arrive_expect_tx_warp(&bars->v_last, L::kTileBytes);
+        mbar_arrive_expect_tx_warp(&bars->kv_full[s],
+                                   ((own ? 0 : 1) + (k_next ? 1 : 0)) * L::kTileBytes);
+        for (int hh = 0; hh < D / 64; ++hh)
+          tma_load_3d_warp(smem + L::kVOff + s * L::kTileBytes + hh * L::kHalfBytes, &map_v, v_bar,
+                           64 * hh, hkv, base + kBN * j);
+        if (k_next)
+          for (int hh = 0; hh < D / 64; ++hh)
+            tma_load_3d_warp(smem + L::kKOff + sk * L::kTileBytes + hh * L::kHalfBytes, &map_k,
+                             &bars->kv_full[s], 64 * hh, hkv, base + kBN * (j + 1));
+        issued = j + 1;
+      }
+      if (!ok) {
+        // aborted: let the copies already issued land before the CTA exits
+        volatile int never = 0;
+        const long long lim = kWaitLimitCycles / 4;
+        for (int j = issued - 1; j >= 0 && j >= issued - NS; --j)
+          mbar_wait(&bars->kv_full[j % NS], (uint32_t)(j / NS) & 1, &never, p.status, lim);
+        if (dirty && issued == nkmax) mbar_wait(&bars->v_last, 0, &never, p.status, lim);
+        mbar_wait(&bars->k0_full, 0, &never, p.status, lim);
+        mbar_wait(&bars->q_full, 0, &never, p.status, lim);
+        __syncwarp();
+      }
+    } else if (warp == kWarpMMA) {
+      // ------------------------------------------------------- MMA issuer --
+      // The whole warp runs the loop, one elected lane issues (polar_device.cuh).
+      constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kBN, 0, 0);
+      constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, D, 0, 1);
+      const uint64_t desc_q = smem_desc_sw128(smem_u32(smem + L::kQOff), 16, 1024);
+      const uint64_t desc_k = smem_desc_sw128(smem_u32(smem + L::kKOff), 16, 1024);
+      // V: MN-major, LBO = distance between the two 64-column atoms (d = 128)
+      const uint64_t desc_v =
+          smem_desc_sw128(smem_u32(smem + L::kVOff), D == 128 ? L::kHalfBytes : 0, 1024);
+      bool ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.status);
+      bool any_issued = false;
+      auto issue_s = [&](int t, int s) {
+        const uint64_t a0 = desc_q + (uint64_t)((t * L::kTileBytes) >> 4);
+        const uint64_t b0 = desc_k + (uint64_t)((s * L::kTileBytes) >> 4);
 #pragma unroll
-      for (int kk = 1; kk < kBN / 16; ++kk)
-        umma_ts_warp(o_tm, p_tm + kk * 8, b0 + (uint64_t)(kk * (2048 >> 4)), kIdescPV, 1u);
-    };
-    if (ok) ok = mbar_wait_warp(&bars->k0_full, 0, abort_flag, p.status);
-    if (ok) {
-      tc_fence_after();
-      for (int t = 0; t < kNQ; ++t)
-        if (nkv[t] > 0) issue_s(t, 0);
-      umma_commit_warp(&bars->k0_empty);
-      any_issued = true;
-    }
-    for (int j = 0; j < nkmax && ok; ++j) {
-      const int s = j % NS, jn = j + 1, sn = jn % NS;
-      ok = mbar_wait_warp(&bars->kv_full[s], (uint32_t)(j / NS) & 1, abort_flag, p.status);
-      if (ok && dirty && jn == nkmax) ok = mbar_wait_warp(&bars->v_clean, 0, abort_flag, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      for (int t = 0; t < kNQ && ok; ++t) {
-        if (j >= nkv[t]) continue;
-        ok = mbar_wait_warp(&bars->p_full[t], (uint32_t)j & 1, abort_flag, p.status);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)((kk >> 2) * (L::kHalfBytes >> 4) + (kk & 3) * 2);
+          umma_ss_warp(tmem + 256 * t, a0 + off, b0 + off, kIdescS, kk > 0);
+        }
+        umma_commit_warp(&bars->s_full[t]);
+      };
+      auto issue_pv = [&](int t, int s, int j) {
+        const uint64_t b0 = desc_v + (uint64_t)((s * L::kTileBytes) >> 4);
+        const uint32_t o_tm = tmem + 256 * t + 128, p_tm = tmem + 256 * t;
+        umma_ts_warp(o_tm, p_tm, b0, kIdescPV, j > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 1; kk < kBN / 16; ++kk)
+          umma_ts_warp(o_tm, p_tm + kk * 8, b0 + (uint64_t)(kk * (2048 >> 4)), kIdescPV, 1u);
+      };
+      if (ok) ok = mbar_wait_warp(&bars->k0_full, 0, abort_flag, p.status);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < kNQ; ++t)
+          if (nkv[t] > 0) issue_s(t, 0);
+        umma_commit_warp(&bars->k0_empty);
+        any_issued = true;
+      }
+      for (int j = 0; j < nkmax && ok; ++j) {
+        const int s = j % NS, jn = j + 1, sn = jn % NS;
+        ok = mbar_wait_warp(&bars->kv_full[s], (uint32_t)(j / NS) & 1, abort_flag, p.status);
+        if (ok && dirty && jn == nkmax) ok = mbar_wait_warp(&bars->v_clean, 0, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        issue_pv(t, s, j);
-        if (j == nkv[t] - 1) umma_commit_warp(&bars->o_final[t]);
-        if (jn < nkv[t]) issue_s(t, sn);
+        for (int t = 0; t < kNQ && ok; ++t) {
+          if (j >= nkv[t]) continue;
+          ok = mbar_wait_warp(&bars->p_full[t], (uint32_t)j & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(t, s, j);
+          if (j == nkv[t] - 1) umma_commit_warp(&bars->o_final[t]);
+          if (jn < nkv[t]) issue_s(t, sn);
+        }
+        if (!ok) break;
+        umma_commit_warp(&bars->step_done[s]);
       }
-      if (!ok) break;
-      umma_commit_warp(&bars->step_done[s]);
-    }
-    if (!ok && any_issued) {
-      // aborted: wait for the MMAs in flight before TMEM is released
-      volatile int never = 0;
-      umma_commit_warp(&bars->drain);
-      __syncwarp();
-      mbar_wait(&bars->drain, 0, &never, p.status, kWaitLimitCycles / 4);
-      __syncwarp();
-    }
-  } else if (warp >= kWarpZero) {
-    // ---------------------------------------------- rows past the sequence --
-    if (dirty) {
-      const bool ok = mbar_wait_warp(&bars->v_last, 0, abort_flag, p.status);
-      if (ok) {
-        uint8_t* v = smem + L::kVOff + ((nkmax - 1) % NS) * L::kTileBytes;
-        for (int i = keep * 8 + (warp - kWarpZero) * 32 + lane; i < kBN * 8; i += 64)
-#pragma unroll
-          for (int hh = 0; hh < D / 64; ++hh)
-            *reinterpret_cast<uint4*>(v + hh * L::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
+      if (!ok && any_issued) {
+        // aborted: wait for the MMAs in flight before TMEM is released
+        volatile int never = 0;
+        umma_commit_warp(&bars->drain);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->v_clean);
+        mbar_wait(&bars->drain, 0, &never, p.status, kWaitLimitCycles / 4);
+        __syncwarp();
+      }
+    } else {
+      // ---------------------------------------------- rows past the sequence --
+      if (dirty) {
+        const bool ok = mbar_wait_warp(&bars->v_last, 0, abort_flag, p.status);
+        if (ok) {
+          uint8_t* v = smem + L::kVOff + ((nkmax - 1) % NS) * L::kTileBytes;
+          for (int i = keep * 8 + (warp - kWarpZero) * 32 + lane; i < kBN * 8; i += 64)
+#pragma unroll
+            for (int hh = 0; hh < D / 64; ++hh)
+              *reinterpret_cast<uint4*>(v + hh * L::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->v_clean);
+        }
       }
     }
   } else if ((warp < 4 ? nkv[0] : nkv[1]) > 0) {
     // ------------------------------------------------- softmax + epilogue --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = warp >> 2;  // row tile of this warpgroup
     const int tk0 = t ? tok0[1] : tok0[0], tokens = t ? cnt[1] : cnt[0];
     const int steps = t ? nkv[1] : nkv[0];
