@@ -223,6 +223,7 @@ struct PackedArgs {
   int N, B, Hq, Hkv, d;
   polar_consts_t c;
   int* status;
+  int sms;
 };
 // maps: q, k, v, out as [token, head, channel] with 128-row boxes.
 cudaError_t launch_packed_tc(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s);

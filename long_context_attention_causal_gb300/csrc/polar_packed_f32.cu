@@ -334,10 +334,11 @@ extern "C" int polar_attn_fwd_packed(const void* q, const void* k, const void* v
         if (&other != &o && meet(o, other)) return POLAR_ERR_INVALID;
     }
   }
-  const int st = check_device(nullptr);
+  int sms = 0;
+  const int st = check_device(&sms);
   if (st != POLAR_OK) return st;
   PackedArgs a{q, k, v, mem, w_count, cu_seqlens, out, n_eff, conf, q_stride, k_stride, v_stride,
-               N, B, Hq, Hkv, d, cc, status_word()};
+               N, B, Hq, Hkv, d, cc, status_word(), sms};
   if (!a.status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == POLAR_F32) return cuda_status("packed prefill (fp32) launch", launch_packed_f32(a, s));

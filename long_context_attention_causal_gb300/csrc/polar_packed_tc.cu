@@ -9,21 +9,27 @@
 // the diagonal (a CTA's rows span 256 / G tokens), and short prompts fill tiles
 // with heads.
 //
-//   * a CTA owns two row tiles of one (sequence, KV head) and streams the keys
-//     0 .. its last token through a ring of K and V stages filled by TMA (3-D
-//     maps [token, head, channel]; a query box is {64 channels, G heads, 128 / G
-//     tokens}, which is the tile's row order);
+//   * a CTA takes two row tiles of one (sequence, KV head) at a time and streams
+//     the keys 0 .. their last token through a ring of K and V stages filled by
+//     TMA (3-D maps [token, head, channel]; a query box is {64 channels, G heads,
+//     128 / G tokens}, which is the tile's row order);
 //   * S_t = Q_t K_j^T into TMEM, softmax by one warpgroup a tile (thread = row =
 //     TMEM lane), P (bf16) over S, O_t += P_t V_j with A from TMEM;
+//   * CTAs stay (one a SM) and go from pair to pair (next_share), the ring and its barriers
+//     with them: with a CTA for each pair about 9 us of launch, search, first
+//     loads and last stores stood beside each pair's products (16 x 1024 tokens,
+//     d = 64: 15 us a CTA for 4.5 key tiles).  The next pair's first K tile
+//     follows the last V tile, its Q comes once the last scores are there, and
+//     its first scores are computed during the epilogue;
 //   * the last key tile of a sequence may hold the next sequence's rows: their
-//     scores are masked by causality, but 0 * NaN is not 0, so two spare warps
-//     zero those rows of V before the product reads them;
+//     scores are masked by causality, but 0 * NaN is not 0, so a spare warp
+//     zeroes those rows of V before the product reads them;
 //   * a tile whose rows are all tokens of the sequence is stored by TMA, one
 //     that the sequence ends in by its valid rows.
 //
 // Warp roles (384 threads): warps 0-3 softmax of tile 0, 4-7 of tile 1, warp 8
-// TMA producer, 9 MMA issuer and TMEM owner, 10-11 zero V rows.  TMEM as in
-// polar_prefill_tc.cu.
+// TMA producer, 9 MMA issuer and TMEM owner, 10 finds the pairs (polar_packed.cuh),
+// 11 zeroes V rows.  TMEM as in polar_prefill_tc.cu.
 #include <algorithm>
 
 #include "polar_device.cuh"
@@ -41,7 +47,9 @@ constexpr int kNSMax = 4;
 constexpr int kThreads = 384;
 constexpr int kWarpTMA = 8;
 constexpr int kWarpMMA = 9;
-constexpr int kWarpZero = 10;  // and 11
+constexpr int kWarpNext = 10;
+// warp 11 zeroes rows of V
+constexpr int kReaders = 11;  // warps that read a pair: all but kWarpNext
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -58,27 +66,73 @@ struct Layout {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kNQ * kTileBytes;
   static constexpr int kVOff = kKOff + kNSK * kTileBytes;
-  static constexpr int kBarOff = kVOff + kNSV * kTileBytes;
-  static constexpr int kSmemBytes = kBarOff + 256 + 1024;  // + align slack
+  static constexpr int kStageOff = kVOff + kNSV * kTileBytes;  // 64 output columns a tile
+  static constexpr int kBarOff = kStageOff + kNQ * kHalfBytes;
+  static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // + align slack
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(kSmemBytes > 232448 / 2, "one CTA per SM (512 TMEM columns)");
   static_assert(kNSK == kNSV, "K and V stages are released together");
 };
 
-// Barriers as in the padded prefill: step j consumes V_j and K_{j+1}.  v_last and
-// v_clean: the landing of the sequence's last V tile where rows of it must be
-// zeroed (in place of its kv_full bytes), and that they are.
+// Steps (key tiles) are counted through all pairs of the CTA: step g consumes V_g
+// and K_{g+1}, which may be the next pair's first.  kv_full: those two landed;
+// step_done: step g's products are done; k0_*: K_0, before the first step.
+// v_raw, v_clean: the landing of a V tile of which rows must be zeroed (in place of
+// its kv_full bytes), and that they are, per V stage.  tile_*: a pair is written
+// down, read by all warps, the next one is wanted.  share_full: an answer to
+// next_share.
 struct Bars {
-  uint64_t q_full;
+  uint64_t q_full[kNQ], q_empty[kNQ];
   uint64_t k0_full, k0_empty;
   uint64_t kv_full[kNSMax], step_done[kNSMax];
   uint64_t s_full[kNQ], p_full[kNQ], o_final[kNQ];
-  uint64_t v_last, v_clean;
+  uint64_t v_raw[kNSMax], v_clean[kNSMax];
+  uint64_t tile_full[2], tile_empty[2], tile_wanted;
+  uint64_t share_full;
   uint64_t drain;
+  PackedTile tile[2];
+  uint4 share;  // 16-byte aligned: the answer to a request for another CTA's share
   uint32_t tmem_base;
   int abort_flag;
-  PackedTile tile;
 };
+static_assert(sizeof(Bars) <= 512, "barriers");
+
+// A pair of row tiles: tokens tok0[t] .. tok0[t] + cnt[t] - 1 of the sequence are
+// tile t's.  They lie within one key tile, the tile's last (TT divides 128).
+template <int TT>
+struct Pair {
+  int head, start;
+  int tok0[kNQ], cnt[kNQ], nkv[kNQ], steps;
+  int keep;    // rows of the last V tile that are the sequence's
+  bool dirty;  // not all of them
+  __device__ __forceinline__ explicit Pair(const PackedTile& t) : head(t.head), start(t.start) {
+    steps = 0;
+#pragma unroll
+    for (int i = 0; i < kNQ; ++i) {
+      tok0[i] = (t.index * kNQ + i) * TT;
+      cnt[i] = head < 0 ? 0 : min(max(t.len - tok0[i], 0), TT);
+      nkv[i] = cnt[i] > 0 ? tok0[i] / kBN + 1 : 0;
+      steps = max(steps, nkv[i]);
+    }
+    keep = t.len - (steps - 1) * kBN;
+    dirty = steps > 0 && keep < kBN;
+  }
+};
+
+// The n-th pair of the CTA, by a converged warp; head -1 behind the last one, and
+// where a wait ran out (*ok false then).
+template <int TT>
+__device__ __forceinline__ Pair<TT> read_pair(Bars* bars, int n, int* status, bool* ok) {
+  volatile int* abort_flag = &bars->abort_flag;
+  PackedTile t{-1, 0, 0, 0};
+  *ok = *ok && mbar_wait_warp(&bars->tile_full[n & 1], (uint32_t)(n >> 1) & 1, abort_flag, status);
+  if (*ok) {
+    t = bars->tile[n & 1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->tile_empty[n & 1]);
+  }
+  return Pair<TT>(t);
+}
 
 struct PackedTcParams {
   const __nv_bfloat16* mem;
@@ -120,17 +174,47 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
-// Commit this thread's TMA stores and wait until they have read their
-// shared-memory source (the buffer may be released after this returns).
-__device__ __forceinline__ void tma_store_commit_wait_read() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy (TMA) reads of them.
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Takes over the share of a CTA of this grid that has not started (cluster launch
+// control): its blockIdx.x, or -1 if all have.  By a converged warp; a request
+// after one that failed is not allowed.
+__device__ __forceinline__ int next_share(Bars* bars, int n, int* status, bool* ok) {
+  if ((threadIdx.x & 31) == 0) {
+    mbar_arrive_expect_tx(&bars->share_full, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(smem_u32(&bars->share)),
+        "r"(smem_u32(&bars->share_full))
+        : "memory");
+  }
+  __syncwarp();
+  // (not given up on an abort: the answer is on its way into this CTA's memory)
+  volatile int never = 0;
+  if (!__all_sync(0xffffffffu,
+                  mbar_wait(&bars->share_full, (uint32_t)n & 1, &never, status))) {
+    bars->abort_flag = 1;
+    *ok = false;
+    return -1;
+  }
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(&bars->share))
+      : "memory");
+  fence_proxy_async_smem();  // read before the next answer is written over it
+  __syncwarp();
+  return got ? (int)x : -1;
 }
 
 template <int D, int G>
@@ -151,28 +235,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 32 * kWarpTMA) {
-    mbar_init(&bars->q_full, 1);
     mbar_init(&bars->k0_full, 1);
     mbar_init(&bars->k0_empty, 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bars->kv_full[s], 1);
       mbar_init(&bars->step_done[s], 1);
+      mbar_init(&bars->v_raw[s], 1);
+      mbar_init(&bars->v_clean[s], 1);
     }
     for (int t = 0; t < kNQ; ++t) {
+      mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->q_empty[t], kBM / 32);  // lane 0 of each softmax warp
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], kBM / 32);  // lane 0 of each softmax warp
+      mbar_init(&bars->p_full[t], kBM / 32);
       mbar_init(&bars->o_final[t], 1);
     }
-    mbar_init(&bars->v_last, 1);
-    mbar_init(&bars->v_clean, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->tile_full[i], 1);
+      mbar_init(&bars->tile_empty[i], kReaders);
+    }
+    mbar_init(&bars->tile_wanted, 1);
+    mbar_init(&bars->share_full, 1);
     mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
     fence_barrier_init();
-  }
-  if (warp == 0) {
-    const PackedTile tile = packed_tile(p.cu, p.B, p.N, p.Hkv, p.head_group, kNQ * TT,
-                                        (long long)blockIdx.x, p.status);
-    if (lane == 0) bars->tile = tile;
   }
   if (warp == kWarpMMA) tmem_alloc(&bars->tmem_base, kTmemCols);
   tc_fence_before();
@@ -180,89 +266,126 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
-  const PackedTile tile = bars->tile;
-  const int hkv = tile.head;
-  // tile t: tokens tok0[t] .. tok0[t] + cnt[t] - 1 of the sequence.  A tile's
-  // tokens lie within one key tile (TT divides 128), its last.
-  int tok0[kNQ], cnt[kNQ], nkv[kNQ];
-  int nkmax = 0;
-#pragma unroll
-  for (int t = 0; t < kNQ; ++t) {
-    tok0[t] = (tile.index * kNQ + t) * TT;
-    cnt[t] = hkv < 0 ? 0 : min(max(tile.len - tok0[t], 0), TT);
-    nkv[t] = cnt[t] > 0 ? tok0[t] / kBN + 1 : 0;
-    nkmax = max(nkmax, nkv[t]);
-  }
-  // rows of the last V tile that are not the sequence's
-  const int keep = tile.len - (nkmax - 1) * kBN;
-  const bool dirty = nkmax > 0 && keep < kBN;
 
-  // Registers: the softmax warpgroups take 216 a thread, the other keeps 72
+  // Registers: the softmax warpgroups take 200 a thread, the other keeps 104
   // (together the 384 x 168 that the block was launched with).
-  if (hkv < 0) {
-    // more CTAs than tiles: only TMEM to give back
-  } else if (warp >= 4 * kNQ) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == kWarpTMA) {
-      // ------------------------------------------------------ TMA producer --
+  if (warp >= 4 * kNQ) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    bool ok = true;
+    if (warp == kWarpNext) {
+      // ------------------------------------------------------- the pairs --
+      // CTA i's share: the ranks i, then back and forth over the grid's CTAs.  A
+      // CTA that is through takes the next share that no CTA has started on, so
+      // shares go out in order, longest first, to whoever is free.
+      int n = 0, asked = 0, share = (int)blockIdx.x;
+      while (ok && share >= 0) {
+        for (long long k = 0; ok; ++k) {
+          const long long rank =
+              k * gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - share : share);
+          if (n >= 1)  // not earlier: the next share goes to who is nearly through
+            ok = mbar_wait_warp(&bars->tile_wanted, (uint32_t)(n - 1) & 1, abort_flag, p.status);
+          if (ok && n >= 2)
+            ok = mbar_wait_warp(&bars->tile_empty[n & 1], (uint32_t)((n >> 1) - 1) & 1, abort_flag,
+                                p.status);
+          if (!ok) break;
+          const PackedTile tile = packed_tile(p.cu, p.B, p.N, p.Hkv, p.head_group, kNQ * TT, rank,
+                                              p.status);
+          if (tile.head < 0) break;
+          if (lane == 0) {
+            bars->tile[n & 1] = tile;
+            mbar_arrive(&bars->tile_full[n & 1]);
+          }
+          __syncwarp();
+          ++n;
+        }
+        if (ok) share = next_share(bars, asked++, p.status, &ok);
+      }
+      if (ok && lane == 0) {
+        // behind the last (the waits above have passed for this n)
+        bars->tile[n & 1] = PackedTile{-1, 0, 0, 0};
+        mbar_arrive(&bars->tile_full[n & 1]);
+      }
+      __syncwarp();
+    } else if (warp == kWarpTMA) {
+      // ---------------------------------------------------- TMA producer --
       if (lane == 0) {
         tma_prefetch_desc(&map_q);
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
       }
       __syncwarp();
-      const int base = tile.start;
-      int nact = 0;
-      for (int t = 0; t < kNQ; ++t) nact += nkv[t] > 0;
-      mbar_arrive_expect_tx_warp(&bars->q_full, nact * L::kTileBytes);
-      for (int t = 0; t < kNQ; ++t) {
-        if (nkv[t] == 0) continue;
+      auto load_kv = [&](const CUtensorMap* map, int off, int stage, uint64_t* bar,
+                         const Pair<TT>& a, int j) {
         for (int hh = 0; hh < D / 64; ++hh)
-          tma_load_3d_warp(smem + L::kQOff + t * L::kTileBytes + hh * L::kHalfBytes, &map_q,
-                           &bars->q_full, 64 * hh, hkv * G, base + tok0[t]);
-      }
-      mbar_arrive_expect_tx_warp(&bars->k0_full, L::kTileBytes);
-      for (int hh = 0; hh < D / 64; ++hh)
-        tma_load_3d_warp(smem + L::kKOff + hh * L::kHalfBytes, &map_k, &bars->k0_full, 64 * hh, hkv,
-                         base);
-      // step j: V_j into V stage j % NS, K_{j+1} into K stage (j + 1) % NS; both
-      // were last used by step j - NS (for j = NS - 1 the K stage held K_0)
-      int issued = 0;
-      bool ok = true;
-      for (int j = 0; j < nkmax && ok; ++j) {
-        const int s = j % NS, sk = (j + 1) % NS;
-        const bool k_next = j + 1 < nkmax;
-        if (j == NS - 1) ok = mbar_wait_warp(&bars->k0_empty, 0, abort_flag, p.status);
-        if (ok && j >= NS)
-          ok = mbar_wait_warp(&bars->step_done[s], (uint32_t)(j / NS - 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        const bool own = dirty && !k_next;  // the tile that needs zeroing
-        uint64_t* v_bar = own ? &bars->v_last : &bars->kv_full[s];
-        if (own) mbar_arrive_expect_tx_warp(&bars->v_last, L::kTileBytes);
-        mbar_arrive_expect_tx_warp(&bars->kv_full[s],
-                                   ((own ? 0 : 1) + (k_next ? 1 : 0)) * L::kTileBytes);
-        for (int hh = 0; hh < D / 64; ++hh)
-          tma_load_3d_warp(smem + L::kVOff + s * L::kTileBytes + hh * L::kHalfBytes, &map_v, v_bar,
-                           64 * hh, hkv, base + kBN * j);
-        if (k_next)
+          tma_load_3d_warp(smem + off + stage * L::kTileBytes + hh * L::kHalfBytes, map, bar,
+                           64 * hh, a.head, a.start + kBN * j);
+      };
+      int g = 0, nq[kNQ] = {0, 0};
+      uint32_t raw = 0;  // V stages with a zeroing load in flight or behind
+      Pair<TT> cur = read_pair<TT>(bars, 0, p.status, &ok);
+      for (int n = 0; ok && cur.head >= 0; ++n) {
+#pragma unroll
+        for (int t = 0; t < kNQ; ++t) {
+          if (cur.nkv[t] == 0 || !ok) continue;
+          if (nq[t] > 0)
+            ok = mbar_wait_warp(&bars->q_empty[t], (uint32_t)(nq[t] - 1) & 1, abort_flag, p.status);
+          if (!ok) continue;
+          mbar_arrive_expect_tx_warp(&bars->q_full[t], L::kTileBytes);
           for (int hh = 0; hh < D / 64; ++hh)
-            tma_load_3d_warp(smem + L::kKOff + sk * L::kTileBytes + hh * L::kHalfBytes, &map_k,
-                             &bars->kv_full[s], 64 * hh, hkv, base + kBN * (j + 1));
-        issued = j + 1;
+            tma_load_3d_warp(smem + L::kQOff + t * L::kTileBytes + hh * L::kHalfBytes, &map_q,
+                             &bars->q_full[t], 64 * hh, cur.head * G, cur.start + cur.tok0[t]);
+          ++nq[t];
+        }
+        if (!ok) break;
+        if (n == 0) {
+          mbar_arrive_expect_tx_warp(&bars->k0_full, L::kTileBytes);
+          load_kv(&map_k, L::kKOff, 0, &bars->k0_full, cur, 0);
+        }
+        Pair<TT> next(PackedTile{-1, 0, 0, 0});
+        for (int j = 0; j < cur.steps; ++j) {
+          const int s = g % NS;
+          // V stage s and K stage (g + 1) % NS were last used by step g - NS (for g =
+          // NS - 1 the K stage held K_0)
+          if (g == NS - 1) ok = mbar_wait_warp(&bars->k0_empty, 0, abort_flag, p.status);
+          if (ok && g >= NS)
+            ok = mbar_wait_warp(&bars->step_done[s], (uint32_t)(g / NS - 1) & 1, abort_flag,
+                                p.status);
+          const bool last = j + 1 == cur.steps;
+          // (four steps take longer than the answer does)
+          if (j == max(cur.steps - 4, 0) && lane == 0) mbar_arrive(&bars->tile_wanted);
+          if (last) next = read_pair<TT>(bars, n + 1, p.status, &ok);
+          if (!ok) break;
+          const bool own = cur.dirty && last;  // the tile that needs zeroing
+          const bool k_next = !last || next.head >= 0;
+          if (own) mbar_arrive_expect_tx_warp(&bars->v_raw[s], L::kTileBytes);
+          mbar_arrive_expect_tx_warp(&bars->kv_full[s],
+                                     ((own ? 0 : 1) + (k_next ? 1 : 0)) * L::kTileBytes);
+          load_kv(&map_v, L::kVOff, s, own ? &bars->v_raw[s] : &bars->kv_full[s], cur, j);
+          if (k_next)
+            load_kv(&map_k, L::kKOff, (g + 1) % NS, &bars->kv_full[s], last ? next : cur,
+                    last ? 0 : j + 1);
+          if (own) raw ^= 1u << s;
+          ++g;
+        }
+        if (!ok) break;
+        cur = next;
       }
       if (!ok) {
         // aborted: let the copies already issued land before the CTA exits
         volatile int never = 0;
         const long long lim = kWaitLimitCycles / 4;
-        for (int j = issued - 1; j >= 0 && j >= issued - NS; --j)
-          mbar_wait(&bars->kv_full[j % NS], (uint32_t)(j / NS) & 1, &never, p.status, lim);
-        if (dirty && issued == nkmax) mbar_wait(&bars->v_last, 0, &never, p.status, lim);
-        mbar_wait(&bars->k0_full, 0, &never, p.status, lim);
-        mbar_wait(&bars->q_full, 0, &never, p.status, lim);
+        for (int i = g - 1; i >= 0 && i >= g - NS; --i)
+          mbar_wait(&bars->kv_full[i % NS], (uint32_t)(i / NS) & 1, &never, p.status, lim);
+        for (int s = 0; s < NS; ++s)
+          if (raw >> s & 1) mbar_wait(&bars->v_raw[s], 0, &never, p.status, lim);
+          else mbar_wait(&bars->v_raw[s], 1, &never, p.status, lim);
+        if (nq[0] + nq[1] > 0 && g >= 0) mbar_wait(&bars->k0_full, 0, &never, p.status, lim);
+        for (int t = 0; t < kNQ; ++t)
+          if (nq[t] > 0) mbar_wait(&bars->q_full[t], (uint32_t)(nq[t] - 1) & 1, &never, p.status, lim);
         __syncwarp();
       }
     } else if (warp == kWarpMMA) {
-      // ------------------------------------------------------- MMA issuer --
+      // ----------------------------------------------------- MMA issuer --
       // The whole warp runs the loop, one elected lane issues (polar_device.cuh).
       constexpr uint32_t kIdescS = idesc_bf16_f32(kBM, kBN, 0, 0);
       constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, D, 0, 1);
@@ -271,8 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V: MN-major, LBO = distance between the two 64-column atoms (d = 128)
       const uint64_t desc_v =
           smem_desc_sw128(smem_u32(smem + L::kVOff), D == 128 ? L::kHalfBytes : 0, 1024);
-      bool ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.status);
-      bool any_issued = false;
       auto issue_s = [&](int t, int s) {
         const uint64_t a0 = desc_q + (uint64_t)((t * L::kTileBytes) >> 4);
         const uint64_t b0 = desc_k + (uint64_t)((s * L::kTileBytes) >> 4);
@@ -291,31 +412,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 1; kk < kBN / 16; ++kk)
           umma_ts_warp(o_tm, p_tm + kk * 8, b0 + (uint64_t)(kk * (2048 >> 4)), kIdescPV, 1u);
       };
-      if (ok) ok = mbar_wait_warp(&bars->k0_full, 0, abort_flag, p.status);
-      if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < kNQ; ++t)
-          if (nkv[t] > 0) issue_s(t, 0);
-        umma_commit_warp(&bars->k0_empty);
-        any_issued = true;
+      int g = 0, nq[kNQ] = {0, 0}, np[kNQ] = {0, 0};
+      uint32_t clean = 0;  // phase of each stage's v_clean
+      bool any_issued = false;
+      // the first scores of a pair: its Q has landed, K stage s holds its first keys
+      auto first_scores = [&](const Pair<TT>& a, int s) {
+#pragma unroll
+        for (int t = 0; t < kNQ; ++t) {
+          if (a.nkv[t] == 0 || !ok) continue;
+          ok = mbar_wait_warp(&bars->q_full[t], (uint32_t)nq[t] & 1, abort_flag, p.status);
+          if (!ok) continue;
+          ++nq[t];
+          tc_fence_after();
+          issue_s(t, s);
+          any_issued = true;
+        }
+      };
+      Pair<TT> cur = read_pair<TT>(bars, 0, p.status, &ok);
+      if (ok && cur.head >= 0) {
+        ok = mbar_wait_warp(&bars->k0_full, 0, abort_flag, p.status);
+        if (ok) first_scores(cur, 0);
+        if (ok) umma_commit_warp(&bars->k0_empty);
       }
-      for (int j = 0; j < nkmax && ok; ++j) {
-        const int s = j % NS, jn = j + 1, sn = jn % NS;
-        ok = mbar_wait_warp(&bars->kv_full[s], (uint32_t)(j / NS) & 1, abort_flag, p.status);
-        if (ok && dirty && jn == nkmax) ok = mbar_wait_warp(&bars->v_clean, 0, abort_flag, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        for (int t = 0; t < kNQ && ok; ++t) {
-          if (j >= nkv[t]) continue;
-          ok = mbar_wait_warp(&bars->p_full[t], (uint32_t)j & 1, abort_flag, p.status);
+      for (int n = 0; ok && cur.head >= 0; ++n) {
+        Pair<TT> next(PackedTile{-1, 0, 0, 0});
+        for (int j = 0; j < cur.steps; ++j, ++g) {
+          const int s = g % NS, sn = (g + 1) % NS;
+          const bool last = j + 1 == cur.steps;
+          ok = mbar_wait_warp(&bars->kv_full[s], (uint32_t)(g / NS) & 1, abort_flag, p.status);
+          if (ok && last && cur.dirty) {
+            ok = mbar_wait_warp(&bars->v_clean[s], clean >> s & 1, abort_flag, p.status);
+            clean ^= 1u << s;
+          }
           if (!ok) break;
           tc_fence_after();
-          issue_pv(t, s, j);
-          if (j == nkv[t] - 1) umma_commit_warp(&bars->o_final[t]);
-          if (jn < nkv[t]) issue_s(t, sn);
+#pragma unroll
+          for (int t = 0; t < kNQ; ++t) {
+            if (j >= cur.nkv[t] || !ok) continue;
+            ok = mbar_wait_warp(&bars->p_full[t], (uint32_t)np[t] & 1, abort_flag, p.status);
+            if (!ok) continue;
+            ++np[t];
+            tc_fence_after();
+            issue_pv(t, s, j);
+            if (j == cur.nkv[t] - 1) umma_commit_warp(&bars->o_final[t]);
+            if (j + 1 < cur.nkv[t]) issue_s(t, sn);
+          }
+          if (!ok) break;
+          if (last) {
+            next = read_pair<TT>(bars, n + 1, p.status, &ok);
+            if (ok && next.head >= 0) first_scores(next, sn);
+            if (!ok) break;
+          }
+          umma_commit_warp(&bars->step_done[s]);
         }
         if (!ok) break;
-        umma_commit_warp(&bars->step_done[s]);
+        cur = next;
       }
       if (!ok && any_issued) {
         // aborted: wait for the MMAs in flight before TMEM is released
@@ -326,153 +477,174 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     } else {
-      // ---------------------------------------------- rows past the sequence --
-      if (dirty) {
-        const bool ok = mbar_wait_warp(&bars->v_last, 0, abort_flag, p.status);
-        if (ok) {
-          uint8_t* v = smem + L::kVOff + ((nkmax - 1) % NS) * L::kTileBytes;
-          for (int i = keep * 8 + (warp - kWarpZero) * 32 + lane; i < kBN * 8; i += 64)
+      // -------------------------------------------- rows past the sequence --
+      int g = 0;
+      uint32_t raw = 0;  // phase of each stage's v_raw
+      for (int n = 0; ok; ++n) {
+        const Pair<TT> cur = read_pair<TT>(bars, n, p.status, &ok);
+        if (!ok || cur.head < 0) break;
+        g += cur.steps;
+        if (!cur.dirty) continue;
+        const int s = (g - 1) % NS;
+        ok = mbar_wait_warp(&bars->v_raw[s], raw >> s & 1, abort_flag, p.status);
+        if (!ok) break;
+        raw ^= 1u << s;
+        uint8_t* v = smem + L::kVOff + s * L::kTileBytes;
+        for (int i = cur.keep * 8 + lane; i < kBN * 8; i += 32)
 #pragma unroll
-            for (int hh = 0; hh < D / 64; ++hh)
-              *reinterpret_cast<uint4*>(v + hh * L::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->v_clean);
-        }
+          for (int hh = 0; hh < D / 64; ++hh)
+            *reinterpret_cast<uint4*>(v + hh * L::kHalfBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->v_clean[s]);
       }
     }
-  } else if ((warp < 4 ? nkv[0] : nkv[1]) > 0) {
+  } else {
     // ------------------------------------------------- softmax + epilogue --
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int t = warp >> 2;  // row tile of this warpgroup
-    const int tk0 = t ? tok0[1] : tok0[0], tokens = t ? cnt[1] : cnt[0];
-    const int steps = t ? nkv[1] : nkv[0];
     const int r = threadIdx.x & 127;
-    const int token = tk0 + r / G;  // of the sequence
-    const int head = hkv * G + r % G;
-    const bool valid = r / G < tokens;
-    const size_t at = (size_t)(tile.start + token) * p.Hq + head;  // row of the outputs
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + 256 * t;
     const uint32_t o_tm = s_tm + 128;
-    bool ok = mbar_wait_warp(&bars->q_full, 0, abort_flag, p.status);
-    // |q|^2 of this row: the swizzle permutes 16-byte chunks inside the row's
-    // 128-byte line (chunk c ^ (r & 7) in round c: no bank conflicts)
-    float q_sq = 0.f;
-    if (ok) {
-      for (int hh = 0; hh < D / 64; ++hh) {
-        const uint4* line = reinterpret_cast<const uint4*>(smem + L::kQOff + t * L::kTileBytes +
-                                                           hh * L::kHalfBytes + r * 128);
+    uint8_t* stage = smem + L::kStageOff + t * L::kHalfBytes;
+    int ns = 0, no = 0;  // scores, outputs of this tile so far
+    bool ok = true;
+    for (int n = 0;; ++n) {
+      // every warp of the group goes on, or none: the meetings below stay whole
+      const Pair<TT> cur = read_pair<TT>(bars, n, p.status, &ok);
+      ok = tile_bar_and(t, ok);
+      if (!ok || cur.head < 0) break;
+      const int tk0 = t ? cur.tok0[1] : cur.tok0[0], tokens = t ? cur.cnt[1] : cur.cnt[0];
+      const int steps = t ? cur.nkv[1] : cur.nkv[0];
+      if (steps == 0) continue;
+      const int token = tk0 + r / G;  // of the sequence
+      const int head = cur.head * G + r % G;
+      const bool valid = r / G < tokens;
+      const size_t at = (size_t)(cur.start + token) * p.Hq + head;  // row of the outputs
+      ok = mbar_wait_warp(&bars->q_full[t], (uint32_t)no & 1, abort_flag, p.status);
+      // |q|^2 of this row: the swizzle permutes 16-byte chunks inside the row's
+      // 128-byte line (chunk c ^ (r & 7) in round c: no bank conflicts)
+      float q_sq = 0.f;
+      if (ok) {
+        for (int hh = 0; hh < D / 64; ++hh) {
+          const uint4* line = reinterpret_cast<const uint4*>(smem + L::kQOff + t * L::kTileBytes +
+                                                             hh * L::kHalfBytes + r * 128);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 u = line[c ^ (r & 7)];
-          const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+          for (int c = 0; c < 8; ++c) {
+            const uint4 u = line[c ^ (r & 7)];
+            const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float lo = __uint_as_float(w4[e] << 16);
-            const float hi = __uint_as_float(w4[e] & 0xFFFF0000u);
-            q_sq = fmaf(lo, lo, q_sq);
-            q_sq = fmaf(hi, hi, q_sq);
+            for (int e = 0; e < 4; ++e) {
+              const float lo = __uint_as_float(w4[e] << 16);
+              const float hi = __uint_as_float(w4[e] & 0xFFFF0000u);
+              q_sq = fmaf(lo, lo, q_sq);
+              q_sq = fmaf(hi, hi, q_sq);
+            }
           }
         }
       }
-    }
-    const float n = (float)(token + 1);
-    const float scale2 = polar_tau(n, p.c.log_t0) * kLog2e * rsqrtf((float)D);  // log2 units
-    const int last_col = token - (steps - 1) * kBN;  // last visible key of the last tile
-    float m_ref = -INFINITY, l = 0.f, q2 = 0.f;
-    for (int j = 0; j < steps && ok; ++j) {
-      ok = mbar_wait_warp(&bars->s_full[t], (uint32_t)j & 1, abort_flag, p.status);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sv[4][32];
+      const float nk = (float)(token + 1);
+      const float scale2 = polar_tau(nk, p.c.log_t0) * kLog2e * rsqrtf((float)D);  // log2 units
+      const int last_col = token - (steps - 1) * kBN;  // last visible key of the last tile
+      float m_ref = -INFINITY, l = 0.f, q2 = 0.f;
+      for (int j = 0; j < steps && ok; ++j) {
+        ok = mbar_wait_warp(&bars->s_full[t], (uint32_t)ns & 1, abort_flag, p.status);
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        uint32_t sv[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, sv[c]);
-      tmem_ld_wait();
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, sv[c]);
+        tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
-      if (j == steps - 1) {
+        for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
+        if (j == steps - 1) {
+          // the last scores are there: Q is read, the next pair's may come
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->q_empty[t]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e > last_col) sv[c][e] = __float_as_uint(-INFINITY);
+        }
+        // row max: three-input max, two chains
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * c + e > last_col) sv[c][e] = __float_as_uint(-INFINITY);
-      }
-      // row max: three-input max, two chains
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          mx0 = fmax3(mx0, __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
-          mx1 = fmax3(mx1, __uint_as_float(sv[c][e + 2]), __uint_as_float(sv[c][e + 3]));
-        }
-      const float mt = fmaxf(mx0, mx1) * scale2;
-      // tcgen05.ld/st are warp-collective: the rescale decision is taken per
-      // warp; rows that do not need it use a factor of 1
-      const bool need = mt > m_ref + kRescaleThreshold;
-      if (__any_sync(0xffffffffu, need)) {
-        const float alpha = need ? ex2_approx(m_ref - mt) : 1.0f;  // 0 on tile 0
-        l *= alpha;
-        q2 *= alpha * alpha;  // squared correction factor
-        if (j > 0) {
-          // S_j was issued after P V of the earlier tiles: they are complete
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld32(o_tm + 32 * c, ov);
-            tmem_ld_wait();
-            reg_fence32(ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st32(o_tm + 32 * c, ov);
+          for (int e = 0; e < 32; e += 4) {
+            mx0 = fmax3(mx0, __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+            mx1 = fmax3(mx1, __uint_as_float(sv[c][e + 2]), __uint_as_float(sv[c][e + 3]));
           }
+        const float mt = fmaxf(mx0, mx1) * scale2;
+        // tcgen05.ld/st are warp-collective: the rescale decision is taken per
+        // warp; rows that do not need it use a factor of 1
+        const bool need = mt > m_ref + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? ex2_approx(m_ref - mt) : 1.0f;  // 0 on tile 0
+          l *= alpha;
+          q2 *= alpha * alpha;  // squared correction factor
+          if (j > 0) {
+            // S_j was issued after P V of the earlier tiles: they are complete
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld32(o_tm + 32 * c, ov);
+              tmem_ld_wait();
+              reg_fence32(ov);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st32(o_tm + 32 * c, ov);
+            }
+          }
+          if (need) m_ref = mt;
         }
-        if (need) m_ref = mt;
-      }
-      // P over S in place: keys 2c', 2c'+1 -> TMEM column c' (bf16x2)
-      const float2 sc2 = make_float2(scale2, scale2);
-      const float2 nm2 = make_float2(-m_ref, -m_ref);
-      float2 la = make_float2(0.f, 0.f), lb = la, qa = la, qb = la;
+        // P over S in place: keys 2c', 2c'+1 -> TMEM column c' (bf16x2)
+        const float2 sc2 = make_float2(scale2, scale2);
+        const float2 nm2 = make_float2(-m_ref, -m_ref);
+        float2 la = make_float2(0.f, 0.f), lb = la, qa = la, qb = la;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float2 x0 = ffma2(make_float2(__uint_as_float(sv[c][e]),
-                                              __uint_as_float(sv[c][e + 1])), sc2, nm2);
-          const float2 x1 = ffma2(make_float2(__uint_as_float(sv[c][e + 2]),
-                                              __uint_as_float(sv[c][e + 3])), sc2, nm2);
-          const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-          const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-          la = fadd2(la, p0);
-          lb = fadd2(lb, p1);
-          qa = ffma2(p0, p0, qa);
-          qb = ffma2(p1, p1, qb);
-          pk[e / 2] = pack_bf16x2(p0.x, p0.y);
-          pk[e / 2 + 1] = pack_bf16x2(p1.x, p1.y);
+          for (int e = 0; e < 32; e += 4) {
+            const float2 x0 = ffma2(make_float2(__uint_as_float(sv[c][e]),
+                                                __uint_as_float(sv[c][e + 1])), sc2, nm2);
+            const float2 x1 = ffma2(make_float2(__uint_as_float(sv[c][e + 2]),
+                                                __uint_as_float(sv[c][e + 3])), sc2, nm2);
+            const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+            const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+            la = fadd2(la, p0);
+            lb = fadd2(lb, p1);
+            qa = ffma2(p0, p0, qa);
+            qb = ffma2(p1, p1, qb);
+            pk[e / 2] = pack_bf16x2(p0.x, p0.y);
+            pk[e / 2 + 1] = pack_bf16x2(p1.x, p1.y);
+          }
+          tmem_st16(s_tm + 16 * c, pk);
         }
-        tmem_st16(s_tm + 16 * c, pk);
+        l += (la.x + la.y) + (lb.x + lb.y);
+        q2 += (qa.x + qa.y) + (qb.x + qb.y);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
-      l += (la.x + la.y) + (lb.x + lb.y);
-      q2 += (qa.x + qa.y) + (qb.x + qb.y);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_full[t]);
-    }
-    // the row's memory stream, loaded while the last products finish
-    uint4 mrow[D / 8];
-    {
-      const uint4* mp = reinterpret_cast<const uint4*>(p.mem + at * D);
+      // the row's memory stream, loaded while the last products finish
+      uint4 mrow[D / 8];
+      {
+        const uint4* mp = reinterpret_cast<const uint4*>(p.mem + at * D);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        mrow[i] = ok && valid ? __ldg(mp + i) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (ok) ok = mbar_wait_warp(&bars->o_final[t], 0, abort_flag, p.status);
-    uint8_t* stage = smem + L::kQOff + t * L::kTileBytes;
-    if (ok) {
+        for (int i = 0; i < D / 8; ++i)
+          mrow[i] = ok && valid ? __ldg(mp + i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (ok) ok = mbar_wait_warp(&bars->o_final[t], (uint32_t)no & 1, abort_flag, p.status);
+      ok = tile_bar_and(t, ok);
+      if (!ok) break;
+      ++no;
       tc_fence_after();
       float acc_sq = 0.f;
 #pragma unroll 1
@@ -487,68 +659,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc_sq = fmaf(a, a, acc_sq);
         }
       }
-      const RowResult res = polar_finish(m_ref * kLn2, l, q2, acc_sq, q_sq, n, D, p.c);
+      const RowResult res = polar_finish(m_ref * kLn2, l, q2, acc_sq, q_sq, nk, D, p.c);
       const float* wv = p.w_count + (size_t)head * D;
-      // The output tile is staged in this tile's Q buffer (its last reader, the
-      // final S product, is done) in the map's 128-byte-swizzle layout: 16-byte
-      // chunk ch of row r at r * 128 + ((ch ^ (r & 7)) << 4).
+      // The output is staged 64 columns at a time in the map's 128-byte-swizzle
+      // layout: 16-byte chunk ch of row r at r * 128 + ((ch ^ (r & 7)) << 4).
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t ov[32];
-        tmem_ld32(o_tm + 32 * c, ov);
-        tmem_ld_wait();
-        reg_fence32(ov);
-        const float4* wp = reinterpret_cast<const float4*>(wv + 32 * c);
-        uint8_t* line = stage + (c >> 1) * L::kHalfBytes + r * 128;
+      for (int hh = 0; hh < D / 64; ++hh) {
+        // the stage's last reader (a TMA store of thread 0's, or the group) is done
+        if (r == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        tile_bar_and(t, true);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint4 mu = mrow[4 * c + g];
-          const float4 w0 = __ldg(wp + 2 * g), w1 = __ldg(wp + 2 * g + 1);
-          const float wf[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-          const uint32_t mw[4] = {mu.x, mu.y, mu.z, mu.w};
-          uint32_t o4[4];
+        for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(o_tm + 32 * c, ov);
+          tmem_ld_wait();
+          reg_fence32(ov);
+          const float4* wp = reinterpret_cast<const float4*>(wv + 32 * c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float m0 = __uint_as_float(mw[e] << 16);
-            const float m1 = __uint_as_float(mw[e] & 0xFFFF0000u);
-            const float a0 = __uint_as_float(ov[8 * g + 2 * e]);
-            const float a1 = __uint_as_float(ov[8 * g + 2 * e + 1]);
-            o4[e] = pack_bf16x2(fmaf(a0, res.scale_u, fmaf(res.count, wf[2 * e], m0)),
-                                fmaf(a1, res.scale_u, fmaf(res.count, wf[2 * e + 1], m1)));
+          for (int g = 0; g < 4; ++g) {
+            const uint4 mu = mrow[4 * c + g];
+            const float4 w0 = __ldg(wp + 2 * g), w1 = __ldg(wp + 2 * g + 1);
+            const float wf[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            const uint32_t mw[4] = {mu.x, mu.y, mu.z, mu.w};
+            uint32_t o4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float m0 = __uint_as_float(mw[e] << 16);
+              const float m1 = __uint_as_float(mw[e] & 0xFFFF0000u);
+              const float a0 = __uint_as_float(ov[8 * g + 2 * e]);
+              const float a1 = __uint_as_float(ov[8 * g + 2 * e + 1]);
+              o4[e] = pack_bf16x2(fmaf(a0, res.scale_u, fmaf(res.count, wf[2 * e], m0)),
+                                  fmaf(a1, res.scale_u, fmaf(res.count, wf[2 * e + 1], m1)));
+            }
+            const int ch = (c & 1) * 4 + g;
+            *reinterpret_cast<uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4)) =
+                make_uint4(o4[0], o4[1], o4[2], o4[3]);
           }
-          const int ch = (c & 1) * 4 + g;
-          *reinterpret_cast<uint4*>(line + ((ch ^ (r & 7)) << 4)) =
-              make_uint4(o4[0], o4[1], o4[2], o4[3]);
+        }
+        fence_proxy_async_smem();
+        tile_bar_and(t, true);
+        if (tokens == TT) {
+          if (r == 0) {
+            tma_store_3d(&map_o, stage, 64 * hh, cur.head * G, cur.start + tk0);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {
+          // rows past the sequence are another's: 16 bytes a thread, valid rows
+          const size_t row0 = (size_t)(cur.start + tk0) * p.Hq + (size_t)cur.head * G;
+          for (int i = r; i < tokens * G * 8; i += 128) {
+            const int row = i >> 3, ch = i & 7;
+            const uint4 x =
+                *reinterpret_cast<const uint4*>(stage + row * 128 + ((ch ^ (row & 7)) << 4));
+            __nv_bfloat16* dst =
+                p.out + (row0 + (size_t)(row / G) * p.Hq + row % G) * D + 64 * hh + 8 * ch;
+            *reinterpret_cast<uint4*>(dst) = x;
+          }
         }
       }
-      fence_proxy_async_smem();
       if (valid) {
         p.n_eff[at] = res.n_eff;
         if (p.conf) p.conf[at] = res.conf;
       }
     }
-    // the staged tile is complete once every warp of the group is
-    if (tile_bar_and(t, ok)) {
-      if (tokens == TT) {
-        if (r == 0) {
-          for (int hh = 0; hh < D / 64; ++hh)
-            tma_store_3d(&map_o, stage + hh * L::kHalfBytes, 64 * hh, hkv * G,
-                         tile.start + tk0);
-          tma_store_commit_wait_read();
-        }
-      } else {
-        // rows past the sequence are another's: 16 bytes a thread, valid rows
-        constexpr int C = D / 8;
-        const size_t row0 = (size_t)(tile.start + tk0) * p.Hq + (size_t)hkv * G;
-        for (int i = r; i < tokens * G * C; i += 128) {
-          const int row = i / C, ch = i % C;
-          const uint4 x = *reinterpret_cast<const uint4*>(
-              stage + (ch >> 3) * L::kHalfBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-          __nv_bfloat16* dst = p.out + (row0 + (size_t)(row / G) * p.Hq + row % G) * D + 8 * ch;
-          *reinterpret_cast<uint4*>(dst) = x;
-        }
-      }
-    }
+    if (r == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -576,17 +749,19 @@ cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) 
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
   // KV heads whose K and V (of all tokens) fit a third of L2
-  static_assert(sizeof(Bars) <= 256, "barriers");
   p.head_group = l2_head_group(a.Hkv, 4.0 * (double)a.N * D);
   p.c = a.c;
   auto kern = polar_packed_tc_kernel<D, G>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
-  // as many CTAs as the sequences can have tiles: each ends in at most one
-  // partial tile
-  const long long tiles = std::min((long long)a.N / kTokens + a.B, (long long)a.N);
-  kern<<<(unsigned)(tiles * a.Hkv), kThreads, L::kSmemBytes, s>>>(m[0], m[1], m[2], m[3], p);
+  // Shares: as many as the sequences can have pairs of tiles (each ends in at most
+  // one partial pair), but where short sequences make that a loose bound, eight a
+  // SM: a share that turns out empty still costs a request.
+  const long long whole = (long long)a.N / kTokens * a.Hkv;
+  const long long pairs = std::min((long long)a.N / kTokens + a.B, (long long)a.N) * a.Hkv;
+  const unsigned ctas = (unsigned)std::min(pairs, std::max(whole, 8LL * a.sms));
+  kern<<<ctas, kThreads, L::kSmemBytes, s>>>(m[0], m[1], m[2], m[3], p);
   return cudaGetLastError();
 }
 
