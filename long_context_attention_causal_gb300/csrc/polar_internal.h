@@ -225,7 +225,7 @@ struct PackedArgs {
   int* status;
   int sms;
 };
-// maps: q, k, v, out as [token, head, channel] with 128-row boxes.
+// maps: q, k, v as [token, head, channel] with 128-row boxes.
 cudaError_t launch_packed_tc(const PackedArgs& a, const CUtensorMap* maps, cudaStream_t s);
 cudaError_t launch_packed_f32(const PackedArgs& a, cudaStream_t s);
 

@@ -342,11 +342,10 @@ extern "C" int polar_attn_fwd_packed(const void* q, const void* k, const void* v
   if (!a.status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == POLAR_F32) return cuda_status("packed prefill (fp32) launch", launch_packed_f32(a, s));
-  CUtensorMap maps[4];
+  CUtensorMap maps[3];
   if (!make_map_tokens(&maps[0], q, N, Hq, d, q_stride, G, 128 / G) ||
       !make_map_tokens(&maps[1], k, N, Hkv, d, k_stride, 1, 128) ||
-      !make_map_tokens(&maps[2], v, N, Hkv, d, v_stride, 1, 128) ||
-      !make_map_tokens(&maps[3], out, N, Hq, d, qw, G, 128 / G))
+      !make_map_tokens(&maps[2], v, N, Hkv, d, v_stride, 1, 128))
     return POLAR_ERR_CUDA;
   return cuda_status("packed prefill (tcgen05) launch", launch_packed_tc(a, maps, s));
 }

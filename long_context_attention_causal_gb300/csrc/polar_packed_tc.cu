@@ -24,12 +24,16 @@
 //   * the last key tile of a sequence may hold the next sequence's rows: their
 //     scores are masked by causality, but 0 * NaN is not 0, so a spare warp
 //     zeroes those rows of V before the product reads them;
-//   * a tile whose rows are all tokens of the sequence is stored by TMA, one
-//     that the sequence ends in by its valid rows.
+//   * in the epilogue every warp works alone, and its 32 rows pass through 4 KB of
+//     shared memory, so that eight lanes read a part of a row of the memory stream
+//     and write one of the output together (warps that met for TMA stores of whole
+//     tiles: 11500 clocks a pair from the last product on, of 20800 for two key
+//     tiles).
 //
 // Warp roles (384 threads): warps 0-3 softmax of tile 0, 4-7 of tile 1, warp 8
 // TMA producer, 9 MMA issuer and TMEM owner, 10 finds the pairs (polar_packed.cuh),
-// 11 zeroes V rows.  TMEM as in polar_prefill_tc.cu.
+// 11 zeroes V rows
+// and has the memory stream brought into L2.  TMEM as in polar_prefill_tc.cu.
 #include <algorithm>
 
 #include "polar_device.cuh"
@@ -66,7 +70,7 @@ struct Layout {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + kNQ * kTileBytes;
   static constexpr int kVOff = kKOff + kNSK * kTileBytes;
-  static constexpr int kStageOff = kVOff + kNSV * kTileBytes;  // 64 output columns a tile
+  static constexpr int kStageOff = kVOff + kNSV * kTileBytes;  // 32 columns of the output rows
   static constexpr int kBarOff = kStageOff + kNQ * kHalfBytes;
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // + align slack
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -146,34 +150,6 @@ struct PackedTcParams {
   polar_consts_t c;
 };
 
-// The 128 threads of query tile t's softmax warpgroup meet at named barrier
-// 1 + t; returns true iff `ok` holds in every one of them.  Every thread of
-// the warpgroup reaches it, whatever its own `ok`, so an aborted warp cannot
-// leave the others waiting.
-__device__ __forceinline__ bool tile_bar_and(int t, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred pi, po;\n\t"
-      "setp.ne.u32 pi, %2, 0;\n\t"
-      "bar.red.and.pred po, %1, 128, pi;\n\t"
-      "selp.u32 %0, 1, 0, po;\n\t}"
-      : "=r"(r)
-      : "r"(1 + t), "r"((uint32_t)ok)
-      : "memory");
-  return r != 0;
-}
-
-// TMA tile store shared -> global (bulk-group completion); rows past the
-// tensor's extent are not written.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x,
-                                             int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy (TMA) reads of them.
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -217,15 +193,41 @@ __device__ __forceinline__ int next_share(Bars* bars, int n, int* status, bool* 
   return got ? (int)x : -1;
 }
 
+// A lane's pieces of its warp's rows of the memory stream: 16 bytes of each 64
+// columns, or 8 of each 32.
+template <int D, bool kByRow>
+struct MemRows;
+template <int D>
+struct MemRows<D, true> {
+  static constexpr int kParts = D / 64, kCols = 8;
+  uint4 v[kParts][8];
+  __device__ __forceinline__ void load(int c, int i, const __nv_bfloat16* src, bool there) {
+    v[c][i] = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * c)) : make_uint4(0, 0, 0, 0);
+  }
+};
+template <int D>
+struct MemRows<D, false> {
+  static constexpr int kParts = D / 32, kCols = 4;
+  uint2 v[kParts][8];
+  __device__ __forceinline__ void load(int c, int i, const __nv_bfloat16* src, bool there) {
+    v[c][i] = there ? __ldg(reinterpret_cast<const uint2*>(src + 32 * c)) : make_uint2(0, 0);
+  }
+};
+
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1)
     polar_packed_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k,
-                           const __grid_constant__ CUtensorMap map_v,
-                           const __grid_constant__ CUtensorMap map_o, const PackedTcParams p) {
+                           const __grid_constant__ CUtensorMap map_v, const PackedTcParams p) {
   using L = Layout<D>;
   constexpr int NS = L::kNSK;
   constexpr int TT = kBM / G;  // tokens of a tile
+  // The epilogue: by rows, whose threads read their head's count direction (a line
+  // an instruction for each head of the warp), or by pieces of rows, whose lanes
+  // know one head or two but whose directions pass through shared memory in fp32.
+  // Measured, rows / pieces: G = 8, 24 prompts up to 2900 tokens, 360 / 320 us; G =
+  // 4, 64 up to 500, 90 / 86; G = 1, 200 up to 190, d = 64, 84 / 91.
+  constexpr bool kByRow = G <= 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -477,12 +479,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     } else {
-      // -------------------------------------------- rows past the sequence --
+      // ------------------------- rows past the sequence, and the memory stream --
       int g = 0;
       uint32_t raw = 0;  // phase of each stage's v_raw
       for (int n = 0; ok; ++n) {
         const Pair<TT> cur = read_pair<TT>(bars, n, p.status, &ok);
         if (!ok || cur.head < 0) break;
+        // the pair's memory stream into L2: a token's heads are one piece
+        const int tokens = cur.cnt[0] + cur.cnt[1];
+        const __nv_bfloat16* mem =
+            p.mem + ((size_t)(cur.start + cur.tok0[0]) * p.Hq + (size_t)cur.head * G) * D;
+        for (int i = lane; i < tokens; i += 32)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(mem +
+                                                                          (size_t)i * p.Hq * D),
+                       "n"(G * D * 2)
+                       : "memory");
         g += cur.steps;
         if (!cur.dirty) continue;
         const int s = (g - 1) % NS;
@@ -507,13 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_base + 256 * t;
     const uint32_t o_tm = s_tm + 128;
-    uint8_t* stage = smem + L::kStageOff + t * L::kHalfBytes;
+    uint8_t* stage = smem + L::kStageOff + t * L::kHalfBytes;  // 32 columns of the rows
     int ns = 0, no = 0;  // scores, outputs of this tile so far
     bool ok = true;
     for (int n = 0;; ++n) {
-      // every warp of the group goes on, or none: the meetings below stay whole
       const Pair<TT> cur = read_pair<TT>(bars, n, p.status, &ok);
-      ok = tile_bar_and(t, ok);
       if (!ok || cur.head < 0) break;
       const int tk0 = t ? cur.tok0[1] : cur.tok0[0], tokens = t ? cur.cnt[1] : cur.cnt[0];
       const int steps = t ? cur.nkv[1] : cur.nkv[0];
@@ -633,86 +642,146 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
-      // the row's memory stream, loaded while the last products finish
-      uint4 mrow[D / 8];
-      {
-        const uint4* mp = reinterpret_cast<const uint4*>(p.mem + at * D);
+      // The memory stream of the warp's 32 rows, while the last products finish (loads
+      // between the stores below waited for those: 13000 clocks a pair at d = 128).
+      // Eight lanes read, and below write, a part of a row together: row 4 i + lane /
+      // 8 of the warp (a row a thread took 32 lines an instruction).
+      const size_t tile_at = ((size_t)(cur.start + tk0) * p.Hq + (size_t)cur.head * G) * D;
+      const int row0 = (r & 96) + (lane >> 3);
+      auto row_at = [&](int i) {  // elements from the tile's first
+        const int row = row0 + 4 * i;
+        return tile_at + (size_t)(((row / G) * p.Hq + row % G) * D);
+      };
+      MemRows<D, kByRow> mem;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          mrow[i] = ok && valid ? __ldg(mp + i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 8; ++i) {
+        const bool there = ok && (row0 + 4 * i) / G < tokens;
+        const __nv_bfloat16* src = p.mem + (there ? row_at(i) : 0) + MemRows<D, kByRow>::kCols * (lane & 7);
+#pragma unroll
+        for (int c = 0; c < MemRows<D, kByRow>::kParts; ++c) mem.load(c, i, src, there);
       }
       if (ok) ok = mbar_wait_warp(&bars->o_final[t], (uint32_t)no & 1, abort_flag, p.status);
-      ok = tile_bar_and(t, ok);
       if (!ok) break;
       ++no;
       tc_fence_after();
       float acc_sq = 0.f;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t ov[32];
-        tmem_ld32(o_tm + 32 * c, ov);
-        tmem_ld_wait();
-        reg_fence32(ov);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float a = __uint_as_float(ov[e]);
-          acc_sq = fmaf(a, a, acc_sq);
+      for (int c = 0; c < D / 32; c += 2) {
+        uint32_t ov[2][32];
+        tmem_ld32(o_tm + 32 * c, ov[0]);
+        tmem_ld32(o_tm + 32 * c + 32, ov[1]);
+        tmem_ld_wait();
+        reg_fence32(ov[0]);
+        reg_fence32(ov[1]);
+        float2 sa = make_float2(0.f, 0.f), sb = sa;
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x0 = make_float2(__uint_as_float(ov[0][e]), __uint_as_float(ov[0][e + 1]));
+          const float2 x1 = make_float2(__uint_as_float(ov[1][e]), __uint_as_float(ov[1][e + 1]));
+          sa = ffma2(x0, x0, sa);
+          sb = ffma2(x1, x1, sb);
         }
+        acc_sq += (sa.x + sa.y) + (sb.x + sb.y);
       }
       const RowResult res = polar_finish(m_ref * kLn2, l, q2, acc_sq, q_sq, nk, D, p.c);
-      const float* wv = p.w_count + (size_t)head * D;
-      // The output is staged 64 columns at a time in the map's 128-byte-swizzle
-      // layout: 16-byte chunk ch of row r at r * 128 + ((ch ^ (r & 7)) << 4).
+      // Through the warp's 4 KB: 16-byte chunk ch of row r at r * 128 + ((ch ^ (r & 7))
+      // << 4), no bank conflicts by rows, nor by eighths of a row.
+      if constexpr (kByRow) {
+        // 64 columns at a time: the memory stream to the rows' threads, outputs back
+        const float* wv = p.w_count + (size_t)head * D;
 #pragma unroll
-      for (int hh = 0; hh < D / 64; ++hh) {
-        // the stage's last reader (a TMA store of thread 0's, or the group) is done
-        if (r == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        tile_bar_and(t, true);
+        for (int hh = 0; hh < D / 64; ++hh) {
+          __syncwarp();  // the last outputs are read
 #pragma unroll
-        for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
-          uint32_t ov[32];
-          tmem_ld32(o_tm + 32 * c, ov);
-          tmem_ld_wait();
-          reg_fence32(ov);
-          const float4* wp = reinterpret_cast<const float4*>(wv + 32 * c);
+          for (int i = 0; i < 8; ++i) {
+            const int row = row0 + 4 * i;
+            *reinterpret_cast<uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) =
+                mem.v[hh][i];
+          }
+          __syncwarp();
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint4 mu = mrow[4 * c + g];
-            const float4 w0 = __ldg(wp + 2 * g), w1 = __ldg(wp + 2 * g + 1);
-            const float wf[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            const uint32_t mw[4] = {mu.x, mu.y, mu.z, mu.w};
-            uint32_t o4[4];
+          for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(o_tm + 32 * c, ov);
+            // (what else a chunk needs is on its way before the wait)
+            const float4* wp = reinterpret_cast<const float4*>(wv + 32 * c);
+            float4 w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float m0 = __uint_as_float(mw[e] << 16);
-              const float m1 = __uint_as_float(mw[e] & 0xFFFF0000u);
-              const float a0 = __uint_as_float(ov[8 * g + 2 * e]);
-              const float a1 = __uint_as_float(ov[8 * g + 2 * e + 1]);
-              o4[e] = pack_bf16x2(fmaf(a0, res.scale_u, fmaf(res.count, wf[2 * e], m0)),
-                                  fmaf(a1, res.scale_u, fmaf(res.count, wf[2 * e + 1], m1)));
+            for (int g = 0; g < 8; ++g) w[g] = __ldg(wp + g);
+            tmem_ld_wait();
+            reg_fence32(ov);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint4* cell = reinterpret_cast<uint4*>(stage + r * 128 +
+                                                     ((((c & 1) * 4 + g) ^ (r & 7)) << 4));
+              const uint4 mu = *cell;
+              const float wf[8] = {w[2 * g].x,     w[2 * g].y,     w[2 * g].z,     w[2 * g].w,
+                                   w[2 * g + 1].x, w[2 * g + 1].y, w[2 * g + 1].z, w[2 * g + 1].w};
+              const uint32_t mw[4] = {mu.x, mu.y, mu.z, mu.w};
+              uint32_t o4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float m0 = __uint_as_float(mw[e] << 16);
+                const float m1 = __uint_as_float(mw[e] & 0xFFFF0000u);
+                const float a0 = __uint_as_float(ov[8 * g + 2 * e]);
+                const float a1 = __uint_as_float(ov[8 * g + 2 * e + 1]);
+                o4[e] = pack_bf16x2(fmaf(a0, res.scale_u, fmaf(res.count, wf[2 * e], m0)),
+                                    fmaf(a1, res.scale_u, fmaf(res.count, wf[2 * e + 1], m1)));
+              }
+              *cell = make_uint4(o4[0], o4[1], o4[2], o4[3]);
             }
-            const int ch = (c & 1) * 4 + g;
-            *reinterpret_cast<uint4*>(stage + r * 128 + ((ch ^ (r & 7)) << 4)) =
-                make_uint4(o4[0], o4[1], o4[2], o4[3]);
+          }
+          __syncwarp();
+          // rows past the sequence are another's, or no one's
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = row0 + 4 * i;
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + row * 128 +
+                                                            (((lane & 7) ^ (row & 7)) << 4));
+            if (row / G < tokens)
+              *reinterpret_cast<uint4*>(p.out + row_at(i) + 64 * hh + 8 * (lane & 7)) = y;
           }
         }
-        fence_proxy_async_smem();
-        tile_bar_and(t, true);
-        if (tokens == TT) {
-          if (r == 0) {
-            tma_store_3d(&map_o, stage, 64 * hh, cur.head * G, cur.start + tk0);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
-        } else {
-          // rows past the sequence are another's: 16 bytes a thread, valid rows
-          const size_t row0 = (size_t)(cur.start + tk0) * p.Hq + (size_t)cur.head * G;
-          for (int i = r; i < tokens * G * 8; i += 128) {
-            const int row = i >> 3, ch = i & 7;
-            const uint4 x =
-                *reinterpret_cast<const uint4*>(stage + row * 128 + ((ch ^ (row & 7)) << 4));
-            __nv_bfloat16* dst =
-                p.out + (row0 + (size_t)(row / G) * p.Hq + row % G) * D + 64 * hh + 8 * ch;
-            *reinterpret_cast<uint4*>(dst) = x;
+      } else {
+        // 32 columns at a time: directions to the lanes that hold the memory stream.
+        // A lane's rows belong to one head, or two where G = 8.
+        constexpr int kHeads = G == 8 ? 2 : 1;
+        const float* wv = p.w_count + ((size_t)cur.head * G + (lane >> 3)) * D + 4 * (lane & 7);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(o_tm + 32 * c, ov);
+          float4 w[kHeads];
+#pragma unroll
+          for (int i = 0; i < kHeads; ++i)
+            w[i] = __ldg(reinterpret_cast<const float4*>(wv + (size_t)(4 * i) * D + 32 * c));
+          tmem_ld_wait();
+          reg_fence32(ov);
+          __syncwarp();  // the last columns are read
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            *reinterpret_cast<float4*>(stage + r * 128 + ((g ^ (r & 7)) << 4)) =
+                make_float4(__uint_as_float(ov[4 * g]) * res.scale_u,
+                            __uint_as_float(ov[4 * g + 1]) * res.scale_u,
+                            __uint_as_float(ov[4 * g + 2]) * res.scale_u,
+                            __uint_as_float(ov[4 * g + 3]) * res.scale_u);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = row0 + 4 * i;
+            const float count = __shfl_sync(0xffffffffu, res.count, 4 * i + (lane >> 3));
+            const float4 u = *reinterpret_cast<const float4*>(stage + row * 128 +
+                                                              (((lane & 7) ^ (row & 7)) << 4));
+            const float4 wf = w[i % kHeads];
+            const uint2 m = mem.v[c][i];
+            const uint2 y = make_uint2(
+                pack_bf16x2(u.x + fmaf(count, wf.x, __uint_as_float(m.x << 16)),
+                            u.y + fmaf(count, wf.y, __uint_as_float(m.x & 0xFFFF0000u))),
+                pack_bf16x2(u.z + fmaf(count, wf.z, __uint_as_float(m.y << 16)),
+                            u.w + fmaf(count, wf.w, __uint_as_float(m.y & 0xFFFF0000u))));
+            // rows past the sequence are another's, or no one's
+            if (row / G < tokens)
+              *reinterpret_cast<uint2*>(p.out + row_at(i) + 32 * c + 4 * (lane & 7)) = y;
           }
         }
       }
@@ -721,7 +790,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.conf) p.conf[at] = res.conf;
       }
     }
-    if (r == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -761,7 +829,7 @@ cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) 
   const long long whole = (long long)a.N / kTokens * a.Hkv;
   const long long pairs = std::min((long long)a.N / kTokens + a.B, (long long)a.N) * a.Hkv;
   const unsigned ctas = (unsigned)std::min(pairs, std::max(whole, 8LL * a.sms));
-  kern<<<ctas, kThreads, L::kSmemBytes, s>>>(m[0], m[1], m[2], m[3], p);
+  kern<<<ctas, kThreads, L::kSmemBytes, s>>>(m[0], m[1], m[2], p);
   return cudaGetLastError();
 }
 
