@@ -326,6 +326,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t raw = 0;  // V stages with a zeroing load in flight or behind
       Pair<TT> cur = read_pair<TT>(bars, 0, p.status, &ok);
       for (int n = 0; ok && cur.head >= 0; ++n) {
+        // the next pair is asked for when four steps, which take longer than the
+        // answer does, are left to load; at once in a shorter pair, whose Q waits
+        // for the last one's scores below
+        if (cur.steps <= 4 && lane == 0) mbar_arrive(&bars->tile_wanted);
 #pragma unroll
         for (int t = 0; t < kNQ; ++t) {
           if (cur.nkv[t] == 0 || !ok) continue;
@@ -353,8 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_warp(&bars->step_done[s], (uint32_t)(g / NS - 1) & 1, abort_flag,
                                 p.status);
           const bool last = j + 1 == cur.steps;
-          // (four steps take longer than the answer does)
-          if (j == max(cur.steps - 4, 0) && lane == 0) mbar_arrive(&bars->tile_wanted);
+          if (j > 0 && j == cur.steps - 4 && lane == 0) mbar_arrive(&bars->tile_wanted);
           if (last) next = read_pair<TT>(bars, n + 1, p.status, &ok);
           if (!ok) break;
           const bool own = cur.dirty && last;  // the tile that needs zeroing
