@@ -451,7 +451,7 @@ def _own(st):
         return {"k": k, "v": v}
     out, n_eff, conf = pa.decode_paged_q4(
         st["q"], st["k_pages"], st["v_pages"], st["table"], st["lens"], st["mem"], st["w_count"],
-        max_seq_len=case["T"], want_conf=True)
+        max_seq_len=max(_lengths(case)), want_conf=True)
     return {"out": out, "n_eff": n_eff, "conf": conf}
 
 
