@@ -1,10 +1,10 @@
 // Rows of k and v into a paged 4-bit cache, and back.  (No counterpart on the
 // pages; layout and rounding: polar_cache_q4.cuh.)
 //
-// Bound by DRAM: the rows are read once and 9 bits are written for each 32.
-// Eight channels, one word of codes, are a thread's; the four threads of a
-// scale's group share its maximum by two shuffles (of the bits of |x|, whose
-// order as integers is that of the numbers, with infinity and NaN above).
+// The rows are read once and 9 bits are written for each 32 (bf16: 16) of a value,
+// so DRAM is the floor; the append's arithmetic, about a dozen instructions a
+// channel, takes longer.  A scale's maximum is that of the bits of |x|, whose order
+// as integers is that of the numbers, with infinity and NaN above.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -122,63 +122,66 @@ __device__ __noinline__ uint32_t q4_word_small(float x0, float x1, float x2, flo
   return word;
 }
 
-// Rows of k (blockIdx.y 0) and v (1), (token, head) by (token, head), W threads a
-// row and a batch of rows a thread, whose loads are in flight together.
-constexpr int kAppendBatch = 1, kReadBatch = 2;
+// Both kernels: rows of k (blockIdx.y 0) and v (1), (token, head) by (token, head),
+// W threads a row; the read with two rows a thread, whose loads are in flight
+// together.
+constexpr int kReadBatch = 2;
 
+// Two words a thread, so that what a row costs beside its codes (place, scale,
+// addresses) is spread over 16 channels; two threads share a scale.
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 6) q4_append_kernel(const Q4Args a) {
-  constexpr int kBatch = kAppendBatch;
-  constexpr int W = D / 8;  // words (threads) of a row
-  constexpr int R = kThreads / W;
+__global__ void __launch_bounds__(kThreads, 5) q4_append_kernel(const Q4Args a) {
+  constexpr int W = D / 16;  // threads of a row
   const bool is_v = blockIdx.y != 0;
   const int w = threadIdx.x % W;
   const uint32_t rows = (uint32_t)a.N * (uint32_t)a.Hkv;
-  const T* src = static_cast<const T*>(is_v ? a.rows[1] : a.rows[0]) + 8 * w;
-  const long long stride = is_v ? a.stride[1] : a.stride[0];
-  float x[kBatch][8];
-  int slot[kBatch], head[kBatch];
+  const uint32_t id = blockIdx.x * (kThreads / W) + threadIdx.x / W;
+  const uint32_t token = id / (uint32_t)a.Hkv;
+  const int head = (int)(id - token * (uint32_t)a.Hkv);
+  float x[2][8];
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    const uint32_t id = (blockIdx.x * kBatch + u) * R + threadIdx.x / W;
-    const uint32_t token = id / (uint32_t)a.Hkv;
-    head[u] = (int)(id - token * (uint32_t)a.Hkv);
-    slot[u] = -1;
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-    if (id < rows) {  // the same for a group's threads
-      load8(src + (long long)token * stride + head[u] * D, x[u]);
-      slot[u] = __ldg(a.slots + token);
-    }
+    for (int i = 0; i < 8; ++i) x[h][i] = 0.f;
+  int slot = -1;
+  if (id < rows) {  // the same for a group's threads
+    const T* src = static_cast<const T*>(is_v ? a.rows[1] : a.rows[0]) +
+                   (long long)token * (is_v ? a.stride[1] : a.stride[0]) + head * D + 16 * w;
+    load8(src, x[0]);
+    load8(src + 8, x[1]);
+    slot = __ldg(a.slots + token);
   }
+  uint32_t top = 0;
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    uint32_t top = 0;
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[u][i]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    uint32_t scale = 0, code = 0;
-    if (top >= 0x7F800000u) {
-      scale = 0x7FFF;  // an infinity or NaN: the group reads as NaN
-    } else if (top > 0x10000000u) {  // 2^-95
-      scale = q4_scale(__uint_as_float(top));
-      code = q4_word(x[u], __uint_as_float(scale << 16));
-    } else if (top > 0) {
-      const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
-      scale = __bfloat16_as_ushort(sb);
-      if (scale > 0)
-        code = q4_word_small(x[u][0], x[u][1], x[u][2], x[u][3], x[u][4], x[u][5], x[u][6], x[u][7],
-                             __bfloat162float(sb));
-    }
-    int page, row;
-    if (!place(a, slot[u], page, row)) continue;
-    uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head[u], a.Hkv, a.shift, D);
-    reinterpret_cast<uint32_t*>(block + (size_t)row * (D / 2))[q4_place(w, D)] = code;
-    if ((w & 3) == 0) {
-      uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
-      reinterpret_cast<uint16_t*>(scales + (size_t)row * (D / 16))[w >> 2] = (uint16_t)scale;
-    }
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[h][i]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  uint32_t scale = 0, code[2] = {0, 0};
+  if (top >= 0x7F800000u) {
+    scale = 0x7FFF;  // an infinity or NaN: the group reads as NaN
+  } else if (top > 0x10000000u) {  // 2^-95
+    scale = q4_scale(__uint_as_float(top));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) code[h] = q4_word(x[h], __uint_as_float(scale << 16));
+  } else if (top > 0) {
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
+    scale = __bfloat16_as_ushort(sb);
+    if (scale > 0)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        code[h] = q4_word_small(x[h][0], x[h][1], x[h][2], x[h][3], x[h][4], x[h][5], x[h][6],
+                                x[h][7], __bfloat162float(sb));
+  }
+  int page, row;
+  if (!place(a, slot, page, row)) return;
+  uint8_t* block = (is_v ? a.pages[1] : a.pages[0]) + q4_block(page, head, a.Hkv, a.shift, D);
+  uint32_t* codes = reinterpret_cast<uint32_t*>(block + (size_t)row * (D / 2));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) codes[q4_place(2 * w + h, D)] = code[h];
+  if ((w & 1) == 0) {
+    uint8_t* scales = block + ((size_t)(D / 2) << a.shift);
+    reinterpret_cast<uint16_t*>(scales + (size_t)row * (D / 16))[w >> 1] = (uint16_t)scale;
   }
 }
 
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Args a) {
 template <bool kRead>
 cudaError_t launch(const Q4Args& a, int d, int dtype, cudaStream_t s) {
   const long long rows = (long long)a.N * a.Hkv;
-  const long long per = (long long)(kRead ? kReadBatch : kAppendBatch) * (kThreads / (d / 8));
+  const long long per = kRead ? (long long)kReadBatch * (kThreads / (d / 8)) : kThreads / (d / 16);
   const dim3 grid((unsigned)((rows + per - 1) / per), 2);
 #define POLAR_Q4(D, T)                                       \
   if (kRead) q4_read_kernel<D, T><<<grid, kThreads, 0, s>>>(a); \

@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
   load_k(0);
   load_v(0);
 
-  float scale[4], m[4], l[4], q2[4], acc[4][4 * CX];
+  float scale[4], m[4], l[4], q2[4];
+  float2 acc[4][2 * CX];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int token = tok0 + (4 * y + i) / G;
@@ -135,13 +136,18 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
     m[i] = -INFINITY;
     l[i] = q2[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4 * CX; ++e) acc[i][e] = 0.f;
+    for (int e = 0; e < 2 * CX; ++e) acc[i][e] = make_float2(0.f, 0.f);
   }
   for (int j0 = 0; j0 < keys; j0 += kKeys) {
     cp_async_wait<1>();  // K (V may still be on its way)
     __syncthreads();
-    float s[4][4] = {};
-#pragma unroll 4
+    // (packed pairs: the sums of even and odd channels)
+    float2 s2[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s2[i][u] = make_float2(0.f, 0.f);
+#pragma unroll 2
     for (int ch = 0; ch < C; ++ch) {
       float4 qv[4], kv[4];
 #pragma unroll
@@ -153,12 +159,15 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          s[i][u] = fmaf(qv[i].x, kv[u].x, s[i][u]);
-          s[i][u] = fmaf(qv[i].y, kv[u].y, s[i][u]);
-          s[i][u] = fmaf(qv[i].z, kv[u].z, s[i][u]);
-          s[i][u] = fmaf(qv[i].w, kv[u].w, s[i][u]);
+          s2[i][u] = ffma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[u].x, kv[u].y), s2[i][u]);
+          s2[i][u] = ffma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[u].z, kv[u].w), s2[i][u]);
         }
     }
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s[i][u] = s2[i][u].x + s2[i][u].y;
     __syncthreads();  // K is read
     if (j0 + kKeys < keys) load_k(j0 + kKeys);
     else cp_async_commit();
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
       q2[i] = q2[i] * alpha * alpha + pq;  // squared correction factor
       m[i] = mn;
 #pragma unroll
-      for (int e = 0; e < 4 * CX; ++e) acc[i][e] *= alpha;
+      for (int e = 0; e < 2 * CX; ++e) acc[i][e].x *= alpha, acc[i][e].y *= alpha;
     }
     cp_async_wait<1>();  // V (the next K may still be on its way)
     __syncthreads();
@@ -205,10 +214,9 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
           const float4 vv = *reinterpret_cast<const float4*>(&sm.v[4 * k4 + u][4 * x + 64 * cx]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            acc[i][4 * cx] = fmaf(pv[i][u], vv.x, acc[i][4 * cx]);
-            acc[i][4 * cx + 1] = fmaf(pv[i][u], vv.y, acc[i][4 * cx + 1]);
-            acc[i][4 * cx + 2] = fmaf(pv[i][u], vv.z, acc[i][4 * cx + 2]);
-            acc[i][4 * cx + 3] = fmaf(pv[i][u], vv.w, acc[i][4 * cx + 3]);
+            const float2 pp = make_float2(pv[i][u], pv[i][u]);
+            acc[i][2 * cx] = ffma2(pp, make_float2(vv.x, vv.y), acc[i][2 * cx]);
+            acc[i][2 * cx + 1] = ffma2(pp, make_float2(vv.z, vv.w), acc[i][2 * cx + 1]);
           }
         }
     }
@@ -223,7 +231,8 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
     const int row = 4 * y + i, token = tok0 + row / G, head = tile.head * G + row % G;
     float a2 = 0.f, qq = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4 * CX; ++e) a2 = fmaf(acc[i][e], acc[i][e], a2);
+    for (int e = 0; e < 2 * CX; ++e)
+      a2 = fmaf(acc[i][e].x, acc[i][e].x, fmaf(acc[i][e].y, acc[i][e].y, a2));
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) qq = fmaf(sm.q[row][x + 16 * e], sm.q[row][x + 16 * e], qq);
     a2 = row_sum(a2);
@@ -239,10 +248,10 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
       const float4 mv = __ldg(reinterpret_cast<const float4*>(p.mem + at * D + ch));
       const float4 wv = __ldg(reinterpret_cast<const float4*>(p.w_count + (size_t)head * D + ch));
       *reinterpret_cast<float4*>(p.out + at * D + ch) =
-          make_float4(fmaf(acc[i][4 * cx], res.scale_u, fmaf(res.count, wv.x, mv.x)),
-                      fmaf(acc[i][4 * cx + 1], res.scale_u, fmaf(res.count, wv.y, mv.y)),
-                      fmaf(acc[i][4 * cx + 2], res.scale_u, fmaf(res.count, wv.z, mv.z)),
-                      fmaf(acc[i][4 * cx + 3], res.scale_u, fmaf(res.count, wv.w, mv.w)));
+          make_float4(fmaf(acc[i][2 * cx].x, res.scale_u, fmaf(res.count, wv.x, mv.x)),
+                      fmaf(acc[i][2 * cx].y, res.scale_u, fmaf(res.count, wv.y, mv.y)),
+                      fmaf(acc[i][2 * cx + 1].x, res.scale_u, fmaf(res.count, wv.z, mv.z)),
+                      fmaf(acc[i][2 * cx + 1].y, res.scale_u, fmaf(res.count, wv.w, mv.w)));
     }
     if (x == 0) {
       p.n_eff[at] = res.n_eff;
