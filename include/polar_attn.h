@@ -551,11 +551,11 @@ int polar_rope(const void* q, const void* k, const int* positions, const double*
  * from cu_seqlens[B] on are neither read into a result nor written.  A token
  * that holds an infinity or NaN may make other rows of its sequence's 128-token
  * tile non-finite, earlier ones included; other sequences it does not reach.
- * Offsets outside [0, N] or descending are cut and record status 3 in
- * polar_attn_device_status (rows that two sequences then share hold either's
- * results).  Memory beyond inputs and outputs: none.  Precision
- * as polar_attn_fwd.  An output that overlaps another tensor of the call is
- * refused.
+ * Offsets outside [0, N] are cut; one below the offset before it ends the list
+ * (its sequence and those after it are not computed); both record status 3 in
+ * polar_attn_device_status.  B up to 2^18.  Memory beyond inputs and outputs:
+ * none.  Precision as polar_attn_fwd.  An output that overlaps another tensor of
+ * the call is refused.
  */
 int polar_attn_fwd_packed(const void* q, const void* k, const void* v, const void* mem,
                           const float* w_count, const int* cu_seqlens, void* out, float* n_eff,

@@ -10,7 +10,9 @@
 // the 16 threads of a row share its maximum and sums by shuffles, P goes
 // through shared memory, and the thread adds the tile's values to 4 rows x D / 16
 // channels.  K of the next tile is copied (cp.async) while P V runs, V while the
-// next scores do.  Bound by the FP32 pipes.
+// next scores do.  Bound by the FP32 pipes: 4 prompts of up to 1500 tokens, 8 query on
+// 2 KV heads, d = 128, 290 us (29 TFLOP/s; with single instead of packed
+// multiply-adds 327).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -28,6 +30,7 @@ namespace {
 constexpr int kRows = 64;
 constexpr int kKeys = 64;
 constexpr int kThreads = 256;
+constexpr int kTurns = 32;
 
 template <int D>
 struct Smem {
@@ -35,7 +38,7 @@ struct Smem {
   // reads at once lie in different banks
   float q[kRows][D], k[kKeys][D], v[kKeys][D];
   float p[kRows][kKeys];
-  PackedTile tile;
+  PackedTile tiles[kTurns];
 };
 
 // Place of piece ch of a row: neighbouring keys, and rows 4 apart, differ.
@@ -49,6 +52,7 @@ struct PackedF32Params {
   int* status;
   long long qs, ks, vs;
   int N, B, Hq, Hkv, head_group;
+  int turns;  // tiles found at a time: 1 (and one a CTA) or kTurns
   polar_consts_t c;
 };
 
@@ -84,179 +88,189 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
   const int tid = threadIdx.x, x = tid & 15, y = tid >> 4;
-  if (tid < 32) {
-    const PackedTile t = packed_tile(p.cu, p.B, p.N, p.Hkv, p.head_group, TT, (long long)blockIdx.x,
-                                     p.status);
-    if (tid == 0) sm.tile = t;
-  }
-  __syncthreads();
-  const PackedTile tile = sm.tile;
-  if (tile.head < 0) return;
-  const int tok0 = tile.index * TT, cnt = min(tile.len - tok0, TT);
-  const int keys = tok0 + cnt;  // keys of the tile's last row
-  const size_t first = (size_t)tile.start;
-
-  auto load_k = [&](int j0) {
-    for (int i = tid; i < kKeys * C; i += kThreads) {
-      const int key = i / C, ch = i % C;
-      if (j0 + key < keys)
-        cp_async16(&sm.k[key][key_piece(key, ch)],
-                   p.k + (first + j0 + key) * (size_t)p.ks + tile.head * D + 4 * ch);
-    }
-    cp_async_commit();
-  };
-  auto load_v = [&](int j0) {
-    for (int i = tid; i < kKeys * C; i += kThreads) {
-      const int key = i / C, ch = i % C;
-      if (j0 + key < keys)
-        cp_async16(&sm.v[key][4 * ch],
-                   p.v + (first + j0 + key) * (size_t)p.vs + tile.head * D + 4 * ch);
-      else  // weighted by 0, and so a number
-        *reinterpret_cast<float4*>(&sm.v[key][4 * ch]) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    cp_async_commit();
-  };
-  for (int i = tid; i < kRows * C; i += kThreads) {
-    const int row = i / C, ch = i % C;
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row / G < cnt)
-      u = __ldg(reinterpret_cast<const float4*>(p.q + (first + tok0 + row / G) * (size_t)p.qs +
-                                                (tile.head * G + row % G) * D) + ch);
-    *reinterpret_cast<float4*>(&sm.q[row][row_piece(row, ch)]) = u;
-  }
-  load_k(0);
-  load_v(0);
-
-  float scale[4], m[4], l[4], q2[4];
-  float2 acc[4][2 * CX];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int token = tok0 + (4 * y + i) / G;
-    scale[i] = polar_tau((float)(token + 1), p.c.log_t0) * rsqrtf((float)D);
-    m[i] = -INFINITY;
-    l[i] = q2[i] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2 * CX; ++e) acc[i][e] = make_float2(0.f, 0.f);
-  }
-  for (int j0 = 0; j0 < keys; j0 += kKeys) {
-    cp_async_wait<1>();  // K (V may still be on its way)
-    __syncthreads();
-    // (packed pairs: the sums of even and odd channels)
-    float2 s2[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) s2[i][u] = make_float2(0.f, 0.f);
-#pragma unroll 2
-    for (int ch = 0; ch < C; ++ch) {
-      float4 qv[4], kv[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        qv[i] = *reinterpret_cast<const float4*>(&sm.q[4 * y + i][row_piece(4 * y, ch)]);
-        kv[i] = *reinterpret_cast<const float4*>(&sm.k[x + 16 * i][key_piece(x, ch)]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          s2[i][u] = ffma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[u].x, kv[u].y), s2[i][u]);
-          s2[i][u] = ffma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[u].z, kv[u].w), s2[i][u]);
+  for (int k = 0;; ++k) {
+    if (k % p.turns == 0) {
+      __syncthreads();  // the last list is read
+      if (tid < 32) {
+        PackedTiles tiles(p.cu, p.B, p.N, p.Hkv, p.head_group, TT, p.status);
+        for (int i = k; i < k + p.turns; ++i) {
+          const PackedTile t = tiles.find((long long)i * gridDim.x +
+                                          ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+          if (tid == 0) sm.tiles[i - k] = t;
         }
+      }
     }
-    float s[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) s[i][u] = s2[i][u].x + s2[i][u].y;
-    __syncthreads();  // K is read
-    if (j0 + kKeys < keys) load_k(j0 + kKeys);
-    else cp_async_commit();
+    __syncthreads();
+    const PackedTile tile = sm.tiles[k % p.turns];
+    if (tile.head < 0) return;
+    const int tok0 = tile.index * TT, cnt = min(tile.len - tok0, TT);
+    const int keys = tok0 + cnt;  // keys of the tile's last row
+    const size_t first = (size_t)tile.start;
+
+    auto load_k = [&](int j0) {
+      for (int i = tid; i < kKeys * C; i += kThreads) {
+        const int key = i / C, ch = i % C;
+        if (j0 + key < keys)
+          cp_async16(&sm.k[key][key_piece(key, ch)],
+                     p.k + (first + j0 + key) * (size_t)p.ks + tile.head * D + 4 * ch);
+      }
+      cp_async_commit();
+    };
+    auto load_v = [&](int j0) {
+      for (int i = tid; i < kKeys * C; i += kThreads) {
+        const int key = i / C, ch = i % C;
+        if (j0 + key < keys)
+          cp_async16(&sm.v[key][4 * ch],
+                     p.v + (first + j0 + key) * (size_t)p.vs + tile.head * D + 4 * ch);
+        else  // weighted by 0, and so a number
+          *reinterpret_cast<float4*>(&sm.v[key][4 * ch]) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      cp_async_commit();
+    };
+    for (int i = tid; i < kRows * C; i += kThreads) {
+      const int row = i / C, ch = i % C;
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row / G < cnt)
+        u = __ldg(reinterpret_cast<const float4*>(p.q + (first + tok0 + row / G) * (size_t)p.qs +
+                                                  (tile.head * G + row % G) * D) + ch);
+      *reinterpret_cast<float4*>(&sm.q[row][row_piece(row, ch)]) = u;
+    }
+    load_k(0);
+    load_v(0);
+
+    float scale[4], m[4], l[4], q2[4];
+    float2 acc[4][2 * CX];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int token = tok0 + (4 * y + i) / G;
-      float mt = -INFINITY;
+      scale[i] = polar_tau((float)(token + 1), p.c.log_t0) * rsqrtf((float)D);
+      m[i] = -INFINITY;
+      l[i] = q2[i] = 0.f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        s[i][u] = j0 + x + 16 * u <= token && j0 + x + 16 * u < keys ? s[i][u] * scale[i]
-                                                                       : -INFINITY;
-        mt = fmaxf(mt, s[i][u]);
-      }
-      const float mn = fmaxf(m[i], row_max(mt));
-      const float alpha = m[i] == mn ? 1.f : expf(m[i] - mn);  // 0 while m = -inf
-      float ps = 0.f, pq = 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float w = s[i][u] == -INFINITY ? 0.f : expf(s[i][u] - mn);
-        ps += w;
-        pq = fmaf(w, w, pq);
-        sm.p[4 * y + i][row_piece(4 * y, (x >> 2) + 4 * u) + (x & 3)] = w;
-      }
-      l[i] = l[i] * alpha + ps;
-      q2[i] = q2[i] * alpha * alpha + pq;  // squared correction factor
-      m[i] = mn;
-#pragma unroll
-      for (int e = 0; e < 2 * CX; ++e) acc[i][e].x *= alpha, acc[i][e].y *= alpha;
+      for (int e = 0; e < 2 * CX; ++e) acc[i][e] = make_float2(0.f, 0.f);
     }
-    cp_async_wait<1>();  // V (the next K may still be on its way)
-    __syncthreads();
+    for (int j0 = 0; j0 < keys; j0 += kKeys) {
+      cp_async_wait<1>();  // K (V may still be on its way)
+      __syncthreads();
+      // (packed pairs: the sums of even and odd channels)
+      float2 s2[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s2[i][u] = make_float2(0.f, 0.f);
 #pragma unroll 2
-    for (int k4 = 0; k4 < kKeys / 4; ++k4) {
-      float pv[4][4];
+      for (int ch = 0; ch < C; ++ch) {
+        float4 qv[4], kv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          qv[i] = *reinterpret_cast<const float4*>(&sm.q[4 * y + i][row_piece(4 * y, ch)]);
+          kv[i] = *reinterpret_cast<const float4*>(&sm.k[x + 16 * i][key_piece(x, ch)]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float2& a = s2[i][u];
+            a = ffma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[u].x, kv[u].y), a);
+            a = ffma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[u].z, kv[u].w), a);
+          }
+      }
+      float s[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[i][u] = s2[i][u].x + s2[i][u].y;
+      __syncthreads();  // K is read
+      if (j0 + kKeys < keys) load_k(j0 + kKeys);
+      else cp_async_commit();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 u = *reinterpret_cast<const float4*>(&sm.p[4 * y + i][row_piece(4 * y, k4)]);
-        pv[i][0] = u.x, pv[i][1] = u.y, pv[i][2] = u.z, pv[i][3] = u.w;
-      }
+        const int token = tok0 + (4 * y + i) / G;
+        float mt = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int cx = 0; cx < CX; ++cx) {
-          const float4 vv = *reinterpret_cast<const float4*>(&sm.v[4 * k4 + u][4 * x + 64 * cx]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 pp = make_float2(pv[i][u], pv[i][u]);
-            acc[i][2 * cx] = ffma2(pp, make_float2(vv.x, vv.y), acc[i][2 * cx]);
-            acc[i][2 * cx + 1] = ffma2(pp, make_float2(vv.z, vv.w), acc[i][2 * cx + 1]);
-          }
+        for (int u = 0; u < 4; ++u) {
+          s[i][u] = j0 + x + 16 * u <= token && j0 + x + 16 * u < keys ? s[i][u] * scale[i]
+                                                                         : -INFINITY;
+          mt = fmaxf(mt, s[i][u]);
         }
+        const float mn = fmaxf(m[i], row_max(mt));
+        const float alpha = m[i] == mn ? 1.f : expf(m[i] - mn);  // 0 while m = -inf
+        float ps = 0.f, pq = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float w = s[i][u] == -INFINITY ? 0.f : expf(s[i][u] - mn);
+          ps += w;
+          pq = fmaf(w, w, pq);
+          sm.p[4 * y + i][row_piece(4 * y, (x >> 2) + 4 * u) + (x & 3)] = w;
+        }
+        l[i] = l[i] * alpha + ps;
+        q2[i] = q2[i] * alpha * alpha + pq;  // squared correction factor
+        m[i] = mn;
+#pragma unroll
+        for (int e = 0; e < 2 * CX; ++e) acc[i][e].x *= alpha, acc[i][e].y *= alpha;
+      }
+      cp_async_wait<1>();  // V (the next K may still be on its way)
+      __syncthreads();
+#pragma unroll 2
+      for (int k4 = 0; k4 < kKeys / 4; ++k4) {
+        float pv[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 u = *reinterpret_cast<const float4*>(&sm.p[4 * y + i][row_piece(4 * y, k4)]);
+          pv[i][0] = u.x, pv[i][1] = u.y, pv[i][2] = u.z, pv[i][3] = u.w;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int cx = 0; cx < CX; ++cx) {
+            const float4 vv = *reinterpret_cast<const float4*>(&sm.v[4 * k4 + u][4 * x + 64 * cx]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 pp = make_float2(pv[i][u], pv[i][u]);
+              acc[i][2 * cx] = ffma2(pp, make_float2(vv.x, vv.y), acc[i][2 * cx]);
+              acc[i][2 * cx + 1] = ffma2(pp, make_float2(vv.z, vv.w), acc[i][2 * cx + 1]);
+            }
+          }
+      }
+      __syncthreads();  // V and P are read
+      if (j0 + kKeys < keys) load_v(j0 + kKeys);
+      else cp_async_commit();
     }
-    __syncthreads();  // V and P are read
-    if (j0 + kKeys < keys) load_v(j0 + kKeys);
-    else cp_async_commit();
-  }
-  cp_async_wait<0>();
-  // (the pieces' order does not matter to a sum over a row)
+    cp_async_wait<0>();
+    // (the pieces' order does not matter to a sum over a row)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 4 * y + i, token = tok0 + row / G, head = tile.head * G + row % G;
-    float a2 = 0.f, qq = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * y + i, token = tok0 + row / G, head = tile.head * G + row % G;
+      float a2 = 0.f, qq = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2 * CX; ++e)
-      a2 = fmaf(acc[i][e].x, acc[i][e].x, fmaf(acc[i][e].y, acc[i][e].y, a2));
+      for (int e = 0; e < 2 * CX; ++e)
+        a2 = fmaf(acc[i][e].x, acc[i][e].x, fmaf(acc[i][e].y, acc[i][e].y, a2));
 #pragma unroll
-    for (int e = 0; e < D / 16; ++e) qq = fmaf(sm.q[row][x + 16 * e], sm.q[row][x + 16 * e], qq);
-    a2 = row_sum(a2);
-    qq = row_sum(qq);
-    const float ls = row_sum(l[i]), qs = row_sum(q2[i]);
-    if (row / G >= cnt) continue;
-    const RowResult res =
-        polar_finish(m[i], ls, qs, a2, qq, (float)(token + 1), D, p.c);
-    const size_t at = (first + token) * p.Hq + head;
+      for (int e = 0; e < D / 16; ++e) qq = fmaf(sm.q[row][x + 16 * e], sm.q[row][x + 16 * e], qq);
+      a2 = row_sum(a2);
+      qq = row_sum(qq);
+      const float ls = row_sum(l[i]), qs = row_sum(q2[i]);
+      if (row / G >= cnt) continue;
+      const RowResult res =
+          polar_finish(m[i], ls, qs, a2, qq, (float)(token + 1), D, p.c);
+      const size_t at = (first + token) * p.Hq + head;
 #pragma unroll
-    for (int cx = 0; cx < CX; ++cx) {
-      const int ch = 4 * x + 64 * cx;
-      const float4 mv = __ldg(reinterpret_cast<const float4*>(p.mem + at * D + ch));
-      const float4 wv = __ldg(reinterpret_cast<const float4*>(p.w_count + (size_t)head * D + ch));
-      *reinterpret_cast<float4*>(p.out + at * D + ch) =
-          make_float4(fmaf(acc[i][2 * cx].x, res.scale_u, fmaf(res.count, wv.x, mv.x)),
-                      fmaf(acc[i][2 * cx].y, res.scale_u, fmaf(res.count, wv.y, mv.y)),
-                      fmaf(acc[i][2 * cx + 1].x, res.scale_u, fmaf(res.count, wv.z, mv.z)),
-                      fmaf(acc[i][2 * cx + 1].y, res.scale_u, fmaf(res.count, wv.w, mv.w)));
+      for (int cx = 0; cx < CX; ++cx) {
+        const int ch = 4 * x + 64 * cx;
+        const float4 mv = __ldg(reinterpret_cast<const float4*>(p.mem + at * D + ch));
+        const float4 wv = __ldg(reinterpret_cast<const float4*>(p.w_count + (size_t)head * D + ch));
+        *reinterpret_cast<float4*>(p.out + at * D + ch) =
+            make_float4(fmaf(acc[i][2 * cx].x, res.scale_u, fmaf(res.count, wv.x, mv.x)),
+                        fmaf(acc[i][2 * cx].y, res.scale_u, fmaf(res.count, wv.y, mv.y)),
+                        fmaf(acc[i][2 * cx + 1].x, res.scale_u, fmaf(res.count, wv.z, mv.z)),
+                        fmaf(acc[i][2 * cx + 1].y, res.scale_u, fmaf(res.count, wv.w, mv.w)));
+      }
+      if (x == 0) {
+        p.n_eff[at] = res.n_eff;
+        if (p.conf) p.conf[at] = res.conf;
+      }
     }
-    if (x == 0) {
-      p.n_eff[at] = res.n_eff;
-      if (p.conf) p.conf[at] = res.conf;
-    }
+    if (p.turns == 1) return;
   }
 }
 
@@ -266,14 +280,22 @@ cudaError_t launch_g(const PackedArgs& a, cudaStream_t s) {
   PackedF32Params p{static_cast<const float*>(a.q), static_cast<const float*>(a.k),
                     static_cast<const float*>(a.v), static_cast<const float*>(a.mem), a.w_count,
                     static_cast<float*>(a.out), a.n_eff, a.conf, a.cu, a.status, a.qs, a.ks, a.vs,
-                    a.N, a.B, a.Hq, a.Hkv, l2_head_group(a.Hkv, 8.0 * (double)a.N * D), a.c};
+                    a.N, a.B, a.Hq, a.Hkv, l2_head_group(a.Hkv, 8.0 * (double)a.N * D), 1, a.c};
   auto kern = polar_packed_f32_kernel<D, G>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)sizeof(Smem<D>));
   static_assert(2 * (sizeof(Smem<D>) + 1024) <= 233472, "two CTAs a SM");
   if (e != cudaSuccess) return e;
-  const long long tiles = std::min((long long)a.N / kTokens + a.B, (long long)a.N);
-  kern<<<(unsigned)(tiles * a.Hkv), kThreads, sizeof(Smem<D>), s>>>(p);
+  const long long tiles = std::min((long long)a.N / kTokens + a.B, (long long)a.N) * a.Hkv;
+  long long ctas = tiles;
+  // Finding a tile costs what the sequences are many: past those that a warp keeps in
+  // registers CTAs stay and find many tiles at a time.  65536 sequences of 16
+  // tokens, 8 query on 2 KV heads, d = 64: 520 ms with a CTA a tile, 26 so.
+  if (a.B > PackedTiles::kFew) {
+    p.turns = kTurns;
+    ctas = std::min(tiles, 8LL * a.sms);
+  }
+  kern<<<(unsigned)ctas, kThreads, sizeof(Smem<D>), s>>>(p);
   return cudaGetLastError();
 }
 
@@ -325,7 +347,7 @@ extern "C" int polar_attn_fwd_packed(const void* q, const void* k, const void* v
     return POLAR_ERR_MISALIGNED;
   // a tensor map's strides stay below 2^40 bytes, a grid below 2^31 CTAs
   const long long most = 1LL << 37;
-  if (q_stride > most || k_stride > most || v_stride > most || N > (1 << 30) || B > (1 << 24) ||
+  if (q_stride > most || k_stride > most || v_stride > most || N > (1 << 30) || B > (1 << 18) ||
       (long long)N + B > INT_MAX / 2 || (((long long)N * G) / 64 + B + 1) * Hkv > INT_MAX)
     return POLAR_ERR_UNSUPPORTED;
   {
@@ -350,7 +372,8 @@ extern "C" int polar_attn_fwd_packed(const void* q, const void* k, const void* v
                N, B, Hq, Hkv, d, cc, status_word(), sms};
   if (!a.status) return cuda_status("cudaGetSymbolAddress", cudaGetLastError());
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == POLAR_F32) return cuda_status("packed prefill (fp32) launch", launch_packed_f32(a, s));
+  if (dtype == POLAR_F32)
+    return cuda_status("packed prefill (fp32) launch", launch_packed_f32(a, s));
   CUtensorMap maps[3];
   if (!make_map_tokens(&maps[0], q, N, Hq, d, q_stride, G, 128 / G) ||
       !make_map_tokens(&maps[1], k, N, Hkv, d, k_stride, 1, 128) ||

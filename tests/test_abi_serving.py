@@ -73,6 +73,7 @@ def test_pages_extend_refusals(L):
 
 
 def test_pages_valid_calls_reach_the_device(L, valid):
+    assert extend(L, {3: NULL}, cap=0) == valid
     assert extend(L) == valid and extend(L, {5: A[1], 6: A[4]}) == valid
     assert extend(L, {8: NULL, 9: NULL}, tokens=0) == valid
     assert release(L) == valid and release(L, {5: A[1], 6: A[4]}) == valid
@@ -220,7 +221,7 @@ def test_packed_refusals(L):
         assert packed(L, {i: odd(i, 2)}) == 3, i
     assert packed(L, qs=255) == 1 and packed(L, ks=64) == 1 and packed(L, vs=0) == 1
     assert packed(L, qs=260) == 3 and packed(L, ks=129) == 3 and packed(L, qs=1 << 38) == 2
-    assert packed(L, N=0) == 0 and packed(L, B=0) == 0
+    assert packed(L, N=0) == 0 and packed(L, B=0) == 0 and packed(L, B=(1 << 18) + 1) == 2
     for i, j in ((6, 0), (6, 1), (6, 2), (6, 3), (6, 4), (6, 5), (7, 8), (7, 6), (8, 0)):
         assert packed(L, {i: A[j]}) == 1, (i, j)
 

@@ -228,3 +228,49 @@ def test_streams_capture_and_refusals():
         pa.fwd_packed(*args, n_eff=torch.empty(3, device=dev()))
     with pytest.raises(ValueError):
         pa.fwd_packed(q, k, v, mem, w, cu[:0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [8300, 33000])
+def test_thousands_of_sequences(B, dtype):
+    """Short and empty sequences with some long ones far apart among them."""
+    import long_context_attention_causal_gb300 as pa
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 4, (B,), generator=g).tolist()
+    far = list(range(5, B, B // 9)) + [B - 1]
+    for i, b in enumerate(far):
+        lens[b] = 300 + 170 * i
+    args = case(lens, 4, 2, 64, dtype, B, tail=3)
+    got = run(args)
+    check(args, got, dtype, seqs=far + list(range(0, B, B // 50)))
+    assert (got[1][:sum(lens)] != 77.0).all() and pa.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_descending_offsets_end_the_list(dtype):
+    """Sequences that would overlap are not computed, however many they are."""
+    import long_context_attention_causal_gb300 as pa
+    args = case([50, 0, 60, 40], 4, 2, 64, dtype, 33)
+    want = run(args)
+    for tail in ([109, 150], [0, 150] * 40000, [-1, 150], [50, 60, 70, 150] * 10):
+        bad = args[:5] + [torch.tensor([0, 50, 50, 110] + tail, dtype=torch.int32, device=dev())]
+        got = run(bad)
+        assert pa.device_status(reset=True) == 3
+        for a, b in zip(got, want):
+            assert torch.equal(a[:110], b[:110]) and (a[110:] == 77.0).all()
+
+
+def test_very_long_sequence():
+    """200000 tokens: the last rows of the prompt."""
+    import long_context_attention_causal_gb300 as pa
+    from serving_ref import polar_ref
+    n, m = 200000, 60
+    args = case([n], 4, 1, 64, "bf16", 43)
+    got = run(args)
+    t = lambda x: x.transpose(0, 1)  # noqa: E731
+    o, ne, c = polar_ref(t(args[0][n - m:]), t(args[1]).expand(4, -1, -1),
+                         t(args[2]).expand(4, -1, -1), n - m, args[4], t(args[3][n - m:]))
+    assert (t(got[0][n - m:]).double() - o).abs().max() <= TOL["bf16"]["out"]
+    assert (t(got[1][n - m:]).double() / ne - 1).abs().max() <= TOL["f32"]["neff"]
+    assert (t(got[2][n - m:]).double() - c).abs().max() <= TOL["f32"]["conf"]
+    assert pa.device_status() == 0
