@@ -497,7 +497,8 @@ size_t polar_cache_evict_workspace_bytes(int B, int Hkv, int max_seq_len, int ke
  * keep_lens out of bounds is left as it is; each records status 3.
  * page_size: a power of two in [8, 1024]; num_pages * page_size and max_pages *
  * page_size below 2^31.  workspace: polar_pages_workspace_bytes(B) bytes,
- * 16-byte aligned.  Written arrays must not overlap others of the call.
+ * 16-byte aligned.  Written arrays must not overlap others of the call.  B = 0
+ * writes nothing.
  */
 int polar_pages_extend(int* block_table, const int* seq_lens, const int* new_tokens,
                        const int* free_pages, const int* free_count, int* lens_out,

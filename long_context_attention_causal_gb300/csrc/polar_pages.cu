@@ -281,7 +281,8 @@ int check(const PagesArgs& a, int page_size, const void* workspace, size_t works
   *shift = 0;
   while ((1 << *shift) < page_size) ++*shift;
   if (a.B == 0) return POLAR_OK;
-  if (!a.table || !a.lens || !a.next || !a.free_pages || !a.count || !a.lens_out || !a.count_out)
+  if (!a.table || !a.lens || !a.next || (a.capacity && !a.free_pages) || !a.count || !a.lens_out ||
+      !a.count_out)
     return POLAR_ERR_INVALID;
   if (!aligned4(a.table) || !aligned4(a.lens) || !aligned4(a.next) || !aligned4(a.free_pages) ||
       !aligned4(a.count) || !aligned4(a.lens_out) || !aligned4(a.count_out) || !aligned4(a.cu) ||

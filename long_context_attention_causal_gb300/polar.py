@@ -839,12 +839,17 @@ def pages_extend(block_table, seq_lens, new_tokens, free_pages, free_count, page
     if n < 0:
         raise ValueError("max_tokens must not be negative")
     if cu_seqlens is None:
-        cu_seqlens = (torch.zeros if B == 0 else torch.empty)((B + 1,), device=block_table.device,
-                                                              dtype=i32)
+        cu_seqlens = torch.empty((B + 1,), device=block_table.device, dtype=i32)
     if positions is None:
         positions = torch.empty((n,), device=block_table.device, dtype=i32)
     if slots is None:
         slots = torch.empty((n,), device=block_table.device, dtype=i32)
+    if B == 0:  # the call writes nothing
+        _in(cu_seqlens, "cu_seqlens", i32, (1,), dev), cu_seqlens.zero_()
+        _in(positions, "positions", i32, (n,), dev), positions.zero_()
+        _in(slots, "slots", i32, (n,), dev), slots.fill_(-1)
+        if count_out is not None:
+            count_out.copy_(free_count)
     _call(dev, "polar_pages_extend", lib().polar_pages_extend, *ptrs,
           _in(cu_seqlens, "cu_seqlens", i32, (B + 1,), dev),
           _in(positions, "positions", i32, (n,), dev), _in(slots, "slots", i32, (n,), dev), B,
@@ -861,6 +866,8 @@ def pages_release(block_table, seq_lens, keep_lens, free_pages, free_count, page
     dev, ptrs, B, max_pages, pool, cap, ws, size, _ = _pages(
         block_table, seq_lens, keep_lens, "keep_lens", free_pages, free_count, lens_out, count_out,
         num_pages, workspace)
+    if B == 0 and count_out is not None:
+        count_out.copy_(free_count)
     _call(dev, "polar_pages_release", lib().polar_pages_release, *ptrs, B, max_pages,
           int(page_size), pool, cap, ws, size)
     return (seq_lens if lens_out is None else lens_out,

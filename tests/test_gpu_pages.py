@@ -218,3 +218,23 @@ def test_binding_refusals():
     with pytest.raises(TypeError):
         pa.pages_release(T, L, None, F, C, 8)
     assert T.tolist() == [[0, 1]] and L.tolist() == [3] and C.tolist() == [2]
+
+
+def test_no_sequences_and_no_stack():
+    """Without sequences every token is one without a row; a stack of no pages
+    serves tokens that need none."""
+    import long_context_attention_causal_gb300 as pa
+    none = torch.empty((0, 4), dtype=I32, device=dev())
+    z = torch.empty((0,), dtype=I32, device=dev())
+    count, left = t32([2]), t32([9])
+    cu, pos, slots = pa.pages_extend(none, z, z, t32([1, 2]), count, 8, 3, count_out=left)
+    assert cu.tolist() == [0] and pos.tolist() == [0] * 3 and slots.tolist() == [-1] * 3
+    assert left.tolist() == [2]
+    left = t32([9])
+    pa.pages_release(none, z, z, t32([1, 2]), count, 8, count_out=left)
+    assert left.tolist() == [2]
+    lens = t32([5, 8])
+    cu, pos, slots = pa.pages_extend(t32([[3, 7], [1, 7]]), lens, t32([2, 1]), z, t32([0]), 8, 4,
+                                     num_pages=8)
+    assert lens.tolist() == [7, 8] and slots.tolist() == [29, 30, -1, -1]
+    assert cu.tolist() == [0, 2, 3] and pa.device_status() == 0
