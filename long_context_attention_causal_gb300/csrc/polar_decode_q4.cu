@@ -231,7 +231,7 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&s)[D / 32]
   }
 }
 
-// Term t of x's expansion in bf16 (x = t0 + t1 + t2 up to 2^-24 x).
+// The first term of x's expansion in bf16 (x = t0 + t1 + t2 up to 2^-24 x).
 __device__ __forceinline__ float bf16_round(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
@@ -605,7 +605,9 @@ __global__ void __launch_bounds__(D* kParts) polar_decode_q4_combine_kernel(cons
   const float wx = p.w_count[(size_t)h * D + x];
   // the records are written by the grid before (programmatic launch)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int2 s = keys > 0 ? p.spans[b * p.Hkv + h / G] : make_int2(0, -1);
+  int2 s = keys > 0 ? p.spans[b * p.Hkv + h / G] : make_int2(0, -1);
+  // (a run that gave up, recorded, leaves what the workspace held)
+  if (s.x < 0 || s.y >= p.runs + p.B * p.Hkv) s = make_int2(0, -1);
   const float* rec = p.records + ((size_t)s.x * G + h % G) * R;
   const size_t step = (size_t)G * R;
   const int n = s.y - s.x + 1;

@@ -206,3 +206,14 @@ def test_refusals():
     with pytest.raises(pa.PolarError):
         pa.decode_paged_q4(*args, max_seq_len=20,
                            workspace=torch.empty(16, device=dev(), dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_long_sequence(dtype):
+    """400000 rows of one head, spread over all runs and joined from their records."""
+    import long_context_attention_causal_gb300 as pa
+    n = 400001
+    args, values = case(1, 4, 1, [n], 64, 256, dtype, 61)
+    got = pa.decode_paged_q4(*args, max_seq_len=n, want_conf=True)
+    check(args, values, got, dtype)
+    assert pa.device_status() == 0
