@@ -9,18 +9,19 @@
 // the diagonal (a CTA's rows span 256 / G tokens), and short prompts fill tiles
 // with heads.
 //
-//   * a CTA takes two row tiles of one (sequence, KV head) at a time and streams
-//     the keys 0 .. their last token through a ring of K and V stages filled by
-//     TMA (3-D maps [token, head, channel]; a query box is {64 channels, G heads,
-//     128 / G tokens}, which is the tile's row order);
+//   * a CTA takes two row tiles of one (sequence, KV head) at a time (NQ; one where
+//     sequences are short: launch_g) and streams the keys 0 .. their last token
+//     through a ring of K and V stages filled by TMA (3-D maps [token, head,
+//     channel]; a query box is {64 channels, G heads, 128 / G tokens}, which is the
+//     tile's row order);
 //   * S_t = Q_t K_j^T into TMEM, softmax by one warpgroup a tile (thread = row =
 //     TMEM lane), P (bf16) over S, O_t += P_t V_j with A from TMEM;
-//   * CTAs stay (one a SM) and go from pair to pair (next_share), the ring and its
-//     barriers with them: with a CTA for each pair about 9 us of launch, search, first
-//     loads and last stores stood beside each pair's products (16 x 1024 tokens,
-//     d = 64: 15 us a CTA for 4.5 key tiles).  The next pair's first K tile
-//     follows the last V tile, its Q comes once the last scores are there, and
-//     its first scores are computed during the epilogue;
+//   * CTAs stay (one a SM, or two of one tile) and go from pair to pair (next_share),
+//     the ring and its barriers with them: with a CTA for each pair about 9 us of
+//     launch, search, first loads and last stores stood beside each pair's products
+//     (16 x 1024 tokens, d = 64: 15 us a CTA for 4.5 key tiles).  The next pair's
+//     first K tile follows the last V tile, its Q comes when the last scores and
+//     |q|^2 are there, and its first scores are computed during the epilogue;
 //   * the last key tile of a sequence may hold the next sequence's rows: their
 //     scores are masked by causality, but 0 * NaN is not 0, so a spare warp
 //     zeroes those rows of V before the product reads them;
@@ -32,14 +33,14 @@
 //
 // Warp roles (384 threads): warps 0-3 softmax of tile 0, 4-7 of tile 1, warp 8
 // TMA producer, 9 MMA issuer and TMEM owner, 10 finds the pairs (polar_packed.cuh),
-// 11 zeroes V rows and has the memory stream brought into L2.  TMEM as in
-// polar_prefill_tc.cu.
+// 11 zeroes V rows and has the memory stream brought into L2; with one tile, 256
+// threads and the last four from warp 4 on.  TMEM as in polar_prefill_tc.cu.
 //
 // Bound by the chain of a step (scores, softmax, products), 1.4 to 1.54 us for two
 // tiles, and by a pair's first and last steps where prompts are short.  Measured:
 // two prompts of 16384 tokens, 16 query on 4 KV heads, d = 128, 1405-1490 us
 // (1476-1565 TFLOP/s); 24 prompts of 1 to 2900 tokens, 16 on 2 heads, 305-320 us;
-// 200 of 1 to 190, 8 heads, d = 64, 82-90 us.
+// 200 of 1 to 190, 8 heads, d = 64, 69 us.
 #include <algorithm>
 
 #include "polar_device.cuh"
@@ -52,35 +53,31 @@ namespace {
 
 constexpr int kBM = 128;  // rows per tile
 constexpr int kBN = 128;  // keys per tile
-constexpr int kNQ = 2;    // row tiles per CTA
 constexpr int kNSMax = 4;
-constexpr int kThreads = 384;
-constexpr int kWarpTMA = 8;
-constexpr int kWarpMMA = 9;
-constexpr int kWarpNext = 10;
-// warp 11 zeroes rows of V
-constexpr int kReaders = 11;  // warps that read a pair: all but kWarpNext
-constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-template <int D>
+// NQ: row tiles of a CTA.
+template <int D, int NQ>
 struct Layout {
-  // Ring depths: 2 K + 2 V stages at d = 128, 4 + 4 at d = 64.  Shared memory stays above
-  // half of the SM's, so one CTA per SM holds the 512 TMEM columns.
-  static constexpr int kNSK = D == 128 ? 2 : 4;
+  static constexpr int kThreads = 128 * (NQ + 1);
+  static constexpr uint32_t kTmemCols = 256 * NQ;
+  // Ring depths: 2 K + 2 V stages, 4 + 4 where there is room.  Shared memory allows as
+  // many CTAs a SM as share its 512 TMEM columns.
+  static constexpr int kNSK = D == 64 && NQ == 2 ? 4 : 2;
   static constexpr int kNSV = kNSK;
   static constexpr int kTileBytes = kBM * D * 2;  // 128 x D bf16
   static constexpr int kHalfBytes = kBM * 128;    // one 64-column swizzle atom
   static constexpr int kQOff = 0;
-  static constexpr int kKOff = kQOff + kNQ * kTileBytes;
+  static constexpr int kKOff = kQOff + NQ * kTileBytes;
   static constexpr int kVOff = kKOff + kNSK * kTileBytes;
   static constexpr int kStageOff = kVOff + kNSV * kTileBytes;  // 32 columns of the output rows
-  static constexpr int kBarOff = kStageOff + kNQ * kHalfBytes;
+  static constexpr int kBarOff = kStageOff + NQ * kHalfBytes;
   static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // + align slack
-  static_assert(kSmemBytes <= 232448, "shared memory");
-  static_assert(kSmemBytes > 232448 / 2, "one CTA per SM (512 TMEM columns)");
+  static constexpr int kCtas = 2 / NQ;  // a SM
+  static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory");
+  static_assert((kCtas + 1) * (kSmemBytes + 1024) > 233472, "TMEM columns");
   static_assert(kNSK == kNSV, "K and V stages are released together");
 };
 
@@ -92,10 +89,10 @@ struct Layout {
 // down, read by all warps, the next one is wanted.  share_full: an answer to
 // next_share.
 struct Bars {
-  uint64_t q_full[kNQ], q_empty[kNQ];
+  uint64_t q_full[2], q_empty[2];  // a row tile each
   uint64_t k0_full, k0_empty;
   uint64_t kv_full[kNSMax], step_done[kNSMax];
-  uint64_t s_full[kNQ], p_full[kNQ], o_final[kNQ];
+  uint64_t s_full[2], p_full[2], o_final[2];
   uint64_t v_raw[kNSMax], v_clean[kNSMax];
   uint64_t tile_full[2], tile_empty[2], tile_wanted;
   uint64_t share_full;
@@ -109,17 +106,17 @@ static_assert(sizeof(Bars) <= 512, "barriers");
 
 // A pair of row tiles: tokens tok0[t] .. tok0[t] + cnt[t] - 1 of the sequence are
 // tile t's.  They lie within one key tile, the tile's last (TT divides 128).
-template <int TT>
+template <int TT, int NQ>
 struct Pair {
   int head, start;
-  int tok0[kNQ], cnt[kNQ], nkv[kNQ], steps;
+  int tok0[NQ], cnt[NQ], nkv[NQ], steps;
   int keep;    // rows of the last V tile that are the sequence's
   bool dirty;  // not all of them
   __device__ __forceinline__ explicit Pair(const PackedTile& t) : head(t.head), start(t.start) {
     steps = 0;
 #pragma unroll
-    for (int i = 0; i < kNQ; ++i) {
-      tok0[i] = (t.index * kNQ + i) * TT;
+    for (int i = 0; i < NQ; ++i) {
+      tok0[i] = (t.index * NQ + i) * TT;
       cnt[i] = head < 0 ? 0 : min(max(t.len - tok0[i], 0), TT);
       nkv[i] = cnt[i] > 0 ? tok0[i] / kBN + 1 : 0;
       steps = max(steps, nkv[i]);
@@ -131,8 +128,8 @@ struct Pair {
 
 // The n-th pair of the CTA, by a converged warp; head -1 behind the last one, and
 // where a wait ran out (*ok false then).
-template <int TT>
-__device__ __forceinline__ Pair<TT> read_pair(Bars* bars, int n, int* status, bool* ok) {
+template <int TT, int NQ>
+__device__ __forceinline__ Pair<TT, NQ> read_pair(Bars* bars, int n, int* status, bool* ok) {
   volatile int* abort_flag = &bars->abort_flag;
   PackedTile t{-1, 0, 0, 0};
   *ok = *ok && mbar_wait_warp(&bars->tile_full[n & 1], (uint32_t)(n >> 1) & 1, abort_flag, status);
@@ -141,7 +138,7 @@ __device__ __forceinline__ Pair<TT> read_pair(Bars* bars, int n, int* status, bo
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->tile_empty[n & 1]);
   }
-  return Pair<TT>(t);
+  return Pair<TT, NQ>(t);
 }
 
 struct PackedTcParams {
@@ -220,13 +217,15 @@ struct MemRows<D, false> {
   }
 };
 
-template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int G, int NQ>
+__global__ void __launch_bounds__(Layout<D, NQ>::kThreads, Layout<D, NQ>::kCtas)
     polar_packed_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_k,
                            const __grid_constant__ CUtensorMap map_v, const PackedTcParams p) {
-  using L = Layout<D>;
+  using L = Layout<D, NQ>;
   constexpr int NS = L::kNSK;
+  constexpr int kWarpTMA = 4 * NQ, kWarpMMA = kWarpTMA + 1, kWarpNext = kWarpTMA + 2;
+  constexpr int kReaders = 4 * NQ + 3;  // warps that read a pair: all but kWarpNext
   constexpr int TT = kBM / G;  // tokens of a tile
   // The epilogue: by rows, whose threads read their head's count direction (a line
   // an instruction for each head of the warp), or by pieces of rows, whose lanes
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->v_raw[s], 1);
       mbar_init(&bars->v_clean[s], 1);
     }
-    for (int t = 0; t < kNQ; ++t) {
+    for (int t = 0; t < NQ; ++t) {
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], kBM / 32);  // lane 0 of each softmax warp
       mbar_init(&bars->s_full[t], 1);
@@ -268,17 +267,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars->abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpMMA) tmem_alloc(&bars->tmem_base, kTmemCols);
+  if (warp == kWarpMMA) tmem_alloc(&bars->tmem_base, L::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
 
-  // Registers: the softmax warpgroups take 200 a thread, the other keeps 104
-  // (together the 384 x 168 that the block was launched with).
-  if (warp >= 4 * kNQ) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  // Registers: the softmax warpgroups take 200 a thread, the other keeps 104 (together
+  // the 384 x 168 that the block was launched with); with one tile 176 and 80 (256 x
+  // 128).
+  if (warp >= 4 * NQ) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NQ == 2 ? 104 : 80));
     bool ok = true;
     if (warp == kWarpNext) {
       // ------------------------------------------------------- the pairs --
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // CTA that is through takes the next share that no CTA has started on, so
       // shares go out in order, longest first, to whoever is free.
       int n = 0, asked = 0, share = (int)blockIdx.x;
-      PackedTiles tiles(p.cu, p.B, p.N, p.Hkv, p.head_group, kNQ * TT, p.status);
+      PackedTiles tiles(p.cu, p.B, p.N, p.Hkv, p.head_group, NQ * TT, p.status);
       while (ok && share >= 0) {
         for (long long k = 0; ok; ++k) {
           const long long rank =
@@ -323,21 +323,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       auto load_kv = [&](const CUtensorMap* map, int off, int stage, uint64_t* bar,
-                         const Pair<TT>& a, int j) {
+                         const Pair<TT, NQ>& a, int j) {
         for (int hh = 0; hh < D / 64; ++hh)
           tma_load_3d_warp(smem + off + stage * L::kTileBytes + hh * L::kHalfBytes, map, bar,
                            64 * hh, a.head, a.start + kBN * j);
       };
-      int g = 0, nq[kNQ] = {0, 0};
+      int g = 0, nq[NQ] = {};
       uint32_t raw = 0;  // V stages with a zeroing load in flight or behind
-      Pair<TT> cur = read_pair<TT>(bars, 0, p.status, &ok);
+      Pair<TT, NQ> cur = read_pair<TT, NQ>(bars, 0, p.status, &ok);
       for (int n = 0; ok && cur.head >= 0; ++n) {
         // the next pair is asked for when four steps, which take longer than the
         // answer does, are left to load; at once in a shorter pair, whose Q waits
         // for the last one's scores below
         if (cur.steps <= 4 && lane == 0) mbar_arrive(&bars->tile_wanted);
 #pragma unroll
-        for (int t = 0; t < kNQ; ++t) {
+        for (int t = 0; t < NQ; ++t) {
           if (cur.nkv[t] == 0 || !ok) continue;
           if (nq[t] > 0)
             ok = mbar_wait_warp(&bars->q_empty[t], (uint32_t)(nq[t] - 1) & 1, abort_flag, p.status);
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx_warp(&bars->k0_full, L::kTileBytes);
           load_kv(&map_k, L::kKOff, 0, &bars->k0_full, cur, 0);
         }
-        Pair<TT> next(PackedTile{-1, 0, 0, 0});
+        Pair<TT, NQ> next(PackedTile{-1, 0, 0, 0});
         for (int j = 0; j < cur.steps; ++j) {
           const int s = g % NS;
           // V stage s and K stage (g + 1) % NS were last used by step g - NS (for g =
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 p.status);
           const bool last = j + 1 == cur.steps;
           if (j > 0 && j == cur.steps - 4 && lane == 0) mbar_arrive(&bars->tile_wanted);
-          if (last) next = read_pair<TT>(bars, n + 1, p.status, &ok);
+          if (last) next = read_pair<TT, NQ>(bars, n + 1, p.status, &ok);
           if (!ok) break;
           const bool own = cur.dirty && last;  // the tile that needs zeroing
           const bool k_next = !last || next.head >= 0;
@@ -390,9 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < NS; ++s)
           if (raw >> s & 1) mbar_wait(&bars->v_raw[s], 0, &never, p.status, lim);
           else mbar_wait(&bars->v_raw[s], 1, &never, p.status, lim);
-        if (nq[0] + nq[1] > 0 && g >= 0) mbar_wait(&bars->k0_full, 0, &never, p.status, lim);
-        for (int t = 0; t < kNQ; ++t)
-          if (nq[t] > 0) mbar_wait(&bars->q_full[t], (uint32_t)(nq[t] - 1) & 1, &never, p.status, lim);
+        if (nq[0] + nq[NQ - 1] > 0 && g >= 0) mbar_wait(&bars->k0_full, 0, &never, p.status, lim);
+        for (int t = 0; t < NQ; ++t)
+          if (nq[t] > 0)
+            mbar_wait(&bars->q_full[t], (uint32_t)(nq[t] - 1) & 1, &never, p.status, lim);
         __syncwarp();
       }
     } else if (warp == kWarpMMA) {
@@ -423,13 +424,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 1; kk < kBN / 16; ++kk)
           umma_ts_warp(o_tm, p_tm + kk * 8, b0 + (uint64_t)(kk * (2048 >> 4)), kIdescPV, 1u);
       };
-      int g = 0, nq[kNQ] = {0, 0}, np[kNQ] = {0, 0};
+      int g = 0, nq[NQ] = {}, np[NQ] = {};
       uint32_t clean = 0;  // phase of each stage's v_clean
       bool any_issued = false;
       // the first scores of a pair: its Q has landed, K stage s holds its first keys
-      auto first_scores = [&](const Pair<TT>& a, int s) {
+      auto first_scores = [&](const Pair<TT, NQ>& a, int s) {
 #pragma unroll
-        for (int t = 0; t < kNQ; ++t) {
+        for (int t = 0; t < NQ; ++t) {
           if (a.nkv[t] == 0 || !ok) continue;
           ok = mbar_wait_warp(&bars->q_full[t], (uint32_t)nq[t] & 1, abort_flag, p.status);
           if (!ok) continue;
@@ -439,14 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           any_issued = true;
         }
       };
-      Pair<TT> cur = read_pair<TT>(bars, 0, p.status, &ok);
+      Pair<TT, NQ> cur = read_pair<TT, NQ>(bars, 0, p.status, &ok);
       if (ok && cur.head >= 0) {
         ok = mbar_wait_warp(&bars->k0_full, 0, abort_flag, p.status);
         if (ok) first_scores(cur, 0);
         if (ok) umma_commit_warp(&bars->k0_empty);
       }
       for (int n = 0; ok && cur.head >= 0; ++n) {
-        Pair<TT> next(PackedTile{-1, 0, 0, 0});
+        Pair<TT, NQ> next(PackedTile{-1, 0, 0, 0});
         for (int j = 0; j < cur.steps; ++j, ++g) {
           const int s = g % NS, sn = (g + 1) % NS;
           const bool last = j + 1 == cur.steps;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int t = 0; t < kNQ; ++t) {
+          for (int t = 0; t < NQ; ++t) {
             if (j >= cur.nkv[t] || !ok) continue;
             ok = mbar_wait_warp(&bars->p_full[t], (uint32_t)np[t] & 1, abort_flag, p.status);
             if (!ok) continue;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           if (last) {
-            next = read_pair<TT>(bars, n + 1, p.status, &ok);
+            next = read_pair<TT, NQ>(bars, n + 1, p.status, &ok);
             if (ok && next.head >= 0) first_scores(next, sn);
             if (!ok) break;
           }
@@ -492,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g = 0;
       uint32_t raw = 0;  // phase of each stage's v_raw
       for (int n = 0; ok; ++n) {
-        const Pair<TT> cur = read_pair<TT>(bars, n, p.status, &ok);
+        const Pair<TT, NQ> cur = read_pair<TT, NQ>(bars, n, p.status, &ok);
         if (!ok || cur.head < 0) break;
         // the pair's memory stream into L2: a token's heads are one piece
-        const int tokens = cur.cnt[0] + cur.cnt[1];
+        const int tokens = cur.cnt[0] + (NQ == 2 ? cur.cnt[NQ - 1] : 0);
         const __nv_bfloat16* mem =
             p.mem + ((size_t)(cur.start + cur.tok0[0]) * p.Hq + (size_t)cur.head * G) * D;
         for (int i = lane; i < tokens; i += 32)
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------- softmax + epilogue --
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NQ == 2 ? 200 : 176));
     const int t = warp >> 2;  // row tile of this warpgroup
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -531,37 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ns = 0, no = 0;  // scores, outputs of this tile so far
     bool ok = true;
     for (int n = 0;; ++n) {
-      const Pair<TT> cur = read_pair<TT>(bars, n, p.status, &ok);
+      const Pair<TT, NQ> cur = read_pair<TT, NQ>(bars, n, p.status, &ok);
       if (!ok || cur.head < 0) break;
-      const int tk0 = t ? cur.tok0[1] : cur.tok0[0], tokens = t ? cur.cnt[1] : cur.cnt[0];
-      const int steps = t ? cur.nkv[1] : cur.nkv[0];
+      const int tk0 = t ? cur.tok0[NQ - 1] : cur.tok0[0];
+      const int tokens = t ? cur.cnt[NQ - 1] : cur.cnt[0];
+      const int steps = t ? cur.nkv[NQ - 1] : cur.nkv[0];
       if (steps == 0) continue;
       const int token = tk0 + r / G;  // of the sequence
       const int head = cur.head * G + r % G;
       const bool valid = r / G < tokens;
       const size_t at = (size_t)(cur.start + token) * p.Hq + head;  // row of the outputs
-      ok = mbar_wait_warp(&bars->q_full[t], (uint32_t)no & 1, abort_flag, p.status);
-      // |q|^2 of this row: the swizzle permutes 16-byte chunks inside the row's
-      // 128-byte line (chunk c ^ (r & 7) in round c: no bank conflicts)
-      float q_sq = 0.f;
-      if (ok) {
-        for (int hh = 0; hh < D / 64; ++hh) {
-          const uint4* line = reinterpret_cast<const uint4*>(smem + L::kQOff + t * L::kTileBytes +
-                                                             hh * L::kHalfBytes + r * 128);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 u = line[c ^ (r & 7)];
-            const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float lo = __uint_as_float(w4[e] << 16);
-              const float hi = __uint_as_float(w4[e] & 0xFFFF0000u);
-              q_sq = fmaf(lo, lo, q_sq);
-              q_sq = fmaf(hi, hi, q_sq);
-            }
-          }
-        }
-      }
       const float nk = (float)(token + 1);
       const float scale2 = polar_tau(nk, p.c.log_t0) * kLog2e * rsqrtf((float)D);  // log2 units
       const int last_col = token - (steps - 1) * kBN;  // last visible key of the last tile
@@ -578,9 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
         if (j == steps - 1) {
-          // the last scores are there: Q is read, the next pair's may come
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->q_empty[t]);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -665,10 +642,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool there = ok && (row0 + 4 * i) / G < tokens;
-        const __nv_bfloat16* src = p.mem + (there ? row_at(i) : 0) + MemRows<D, kByRow>::kCols * (lane & 7);
+        const __nv_bfloat16* src = p.mem + (there ? row_at(i) : 0) + mem.kCols * (lane & 7);
 #pragma unroll
-        for (int c = 0; c < MemRows<D, kByRow>::kParts; ++c) mem.load(c, i, src, there);
+        for (int c = 0; c < mem.kParts; ++c) mem.load(c, i, src, there);
       }
+      if (ok) ok = mbar_wait_warp(&bars->q_full[t], (uint32_t)no & 1, abort_flag, p.status);
+      // |q|^2 of this row, likewise: the swizzle permutes 16-byte chunks inside the row's
+      // 128-byte line (chunk c ^ (r & 7) in round c: no bank conflicts)
+      float2 qa = make_float2(0.f, 0.f), qb = qa;
+      if (ok) {
+        for (int hh = 0; hh < D / 64; ++hh) {
+          const uint4* line = reinterpret_cast<const uint4*>(smem + L::kQOff + t * L::kTileBytes +
+                                                             hh * L::kHalfBytes + r * 128);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 u = line[c ^ (r & 7)];
+            const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 x = make_float2(__uint_as_float(w4[e] << 16),
+                                           __uint_as_float(w4[e] & 0xFFFF0000u));
+              if (e & 1) qb = ffma2(x, x, qb);
+              else qa = ffma2(x, x, qa);
+            }
+          }
+        }
+      }
+      const float q_sq = (qa.x + qa.y) + (qb.x + qb.y);
+      // Q is read, by the last scores' product too: the next pair's may come
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&bars->q_empty[t]);
       if (ok) ok = mbar_wait_warp(&bars->o_final[t], (uint32_t)no & 1, abort_flag, p.status);
       if (!ok) break;
       ++no;
@@ -805,14 +808,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kWarpMMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, L::kTmemCols);
   }
 }
 
-template <int D, int G>
-cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) {
-  using L = Layout<D>;
-  constexpr int kTokens = kNQ * kBM / G;
+template <int D, int G, int NQ>
+cudaError_t launch_n(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) {
+  using L = Layout<D, NQ>;
+  constexpr int kTokens = NQ * kBM / G;
   PackedTcParams p;
   p.mem = static_cast<const __nv_bfloat16*>(a.mem);
   p.w_count = a.w_count;
@@ -828,7 +831,7 @@ cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) 
   // KV heads whose K and V (of all tokens) fit a third of L2
   p.head_group = l2_head_group(a.Hkv, 4.0 * (double)a.N * D);
   p.c = a.c;
-  auto kern = polar_packed_tc_kernel<D, G>;
+  auto kern = polar_packed_tc_kernel<D, G, NQ>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -838,8 +841,22 @@ cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) 
   const long long whole = (long long)a.N / kTokens * a.Hkv;
   const long long pairs = std::min((long long)a.N / kTokens + a.B, (long long)a.N) * a.Hkv;
   const unsigned ctas = (unsigned)std::min(pairs, std::max(whole, 8LL * a.sms));
-  kern<<<ctas, kThreads, L::kSmemBytes, s>>>(m[0], m[1], m[2], p);
+  kern<<<ctas, L::kThreads, L::kSmemBytes, s>>>(m[0], m[1], m[2], p);
   return cudaGetLastError();
+}
+
+// Two row tiles a CTA, which share K and V, or one and two CTAs a SM (d = 64), whose
+// chains run side by side: a short prompt leaves the second tile of a pair empty.
+// One where a sequence has at most 192 of a pair's 256 rows on average.  Measured,
+// two / one, us: G = 1, prompts up to 30, 190, 500, 1000 tokens (15 to 500 on average),
+// 179 / 110, 87 / 69, 71 / 67, 68 / 73; G = 2, up to 60, 190, 300, 181 / 118, 106 /
+// 104, 94 / 106; G = 4, up to 30, 60, 120, 96 / 67, 101 / 93, 100 / 111; G = 8, up to
+// 30, 60, 59 / 60, 82 / 100.
+template <int D, int G>
+cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) {
+  if constexpr (D == 64)
+    if ((long long)a.N * G <= 192LL * a.B) return launch_n<D, G, 1>(a, m, s);
+  return launch_n<D, G, 2>(a, m, s);
 }
 
 template <int D>
