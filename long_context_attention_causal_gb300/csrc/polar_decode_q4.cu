@@ -58,6 +58,7 @@ constexpr float kTwo65 = 36893488147419103232.0f;
 // weights carry 2^40: squares of weights up to 2^8, summed over 2^30 keys, stay
 // below 2^127, and a weight of 1 keeps 24 bits beside a scale down to 2^-36
 constexpr float kShift = 40.0f;
+constexpr float kTwo40 = 1099511627776.0f;
 constexpr float kUnshift = 9.094947017729282e-13f;              // 2^-40
 constexpr float kUnshiftAcc = 618970019642690137449562112.0f;  // 2^(129 - 40)
 constexpr uint32_t kCodeMask = 0x80708070u;
@@ -317,15 +318,23 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
     }
     const float slack = kRescale / z.scale2;
     float a0 = 1.f, a1 = 1.f;  // 0 at the first keys
-    if (t0 > z.up0) a0 = ex2_approx((z.m0 - t0) * z.scale2), z.m0 = t0, z.up0 = t0 + slack;
-    if (t1 > z.up1) a1 = ex2_approx((z.m1 - t1) * z.scale2), z.m1 = t1, z.up1 = t1 + slack;
+    auto correction = [&](float m, float t) {
+      if constexpr (NT == 1) return ex2_approx((m - t) * z.scale2);
+      // of the rounded products, which the weights and the records are relative to
+      return ex2_approx(__fmul_rn(m, z.scale2) - __fmul_rn(t, z.scale2));
+    };
+    if (t0 > z.up0) a0 = correction(z.m0, t0), z.m0 = t0, z.up0 = t0 + slack;
+    if (t1 > z.up1) a1 = correction(z.m1, t1), z.m1 = t1, z.up1 = t1 + slack;
     z.l0 *= a0, z.l1 *= a1;
     z.s0 *= a0 * a0, z.s1 *= a1 * a1;  // squared correction factor
 #pragma unroll
     for (int i = 0; i < 2 * NG; ++i)
       z.o[i][0] *= a0, z.o[i][2] *= a0, z.o[i][1] *= a1, z.o[i][3] *= a1;
   }
-  const float n0 = fmaf(-z.m0, z.scale2, kShift), n1 = fmaf(-z.m1, z.scale2, kShift);
+  // fp32: the shift is in the values' scales, as the exponents here would lose five
+  // bits to it (the outputs' error was 6.4e-7 of their norm, and is 1.1e-7)
+  constexpr float kShiftW = NT == 1 ? kShift : 0.f;
+  const float n0 = fmaf(-z.m0, z.scale2, kShiftW), n1 = fmaf(-z.m1, z.scale2, kShiftW);
 #pragma unroll
   for (int h = 0; h < 2 * NS; ++h) {
     float w0 = ex2_approx(fmaf(x[2 * h], z.scale2, n0));
@@ -345,6 +354,10 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
     float va[NG], vb[NG];
     load_scales<D>(vc + scales + (base + rk) * (D / 16), va);
     load_scales<D>(vc + scales + (base + 8 + rk) * (D / 16), vb);
+    if constexpr (NT > 1) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) va[g] *= kTwo40, vb[g] *= kTwo40;
+    }
     if constexpr (!kWhole) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -563,10 +576,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     ok = compute_bar_and(ok);
     if (!ok) break;
     if (r == 0) {
+      constexpr float kDown = NT == 1 ? kUnshift : 1.f;
       sm.m[warp][2 * c] = z.m0 * z.scale2, sm.m[warp][2 * c + 1] = z.m1 * z.scale2;
-      sm.l[warp][2 * c] = z.l0 * kUnshift, sm.l[warp][2 * c + 1] = z.l1 * kUnshift;
-      sm.q2[warp][2 * c] = z.s0 * kUnshift * kUnshift;
-      sm.q2[warp][2 * c + 1] = z.s1 * kUnshift * kUnshift;
+      sm.l[warp][2 * c] = z.l0 * kDown, sm.l[warp][2 * c + 1] = z.l1 * kDown;
+      sm.q2[warp][2 * c] = z.s0 * kDown * kDown;
+      sm.q2[warp][2 * c + 1] = z.s1 * kDown * kDown;
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i)

@@ -128,3 +128,63 @@ def test_captured_decode_step():
             assert torch.equal(a, b)
     assert loop.lens.tolist() == [90] * B and torch.equal(loop.table, eager.table)
     assert pa.device_status() == 0
+
+
+def test_two_threads():
+    """Two host threads run the whole chain at once, each on a stream of its own
+    with tensors of its own, and get the bits of the same calls made alone."""
+    import threading
+
+    import long_context_attention_causal_gb300 as pa
+    B, Hq, Hkv, d, page, cols, pool = 7, 16, 2, 128, 32, 16, 120
+    inv_freq, _ = pa.rope_inv_freq(d)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev())  # noqa: E731
+    w = torch.randn((Hq, d), generator=torch.Generator(device=dev()).manual_seed(1), device=dev()) * 0.02
+
+    def chain(seed):
+        """Every output of some rounds of a prompt and a token for each request."""
+        g = torch.Generator(device=dev()).manual_seed(seed)
+        table = torch.full((B, cols), -1, dtype=torch.int32, device=dev())
+        lens, count = i32([0] * B), i32([pool])
+        free, cache = torch.arange(pool, dtype=torch.int32, device=dev()), pa.cache_q4(pool, Hkv, page, d)
+        got = []
+        for i in range(12):
+            new = [1] * B if i % 3 else [(37 * seed + 29 * i + 11 * b) % 90 for b in range(B)]
+            n = sum(new)
+            qkv = torch.randn((n, Hq + 2 * Hkv, d), generator=g, device=dev()).bfloat16()
+            mem = torch.randn((n, Hq, d), generator=g, device=dev()).bfloat16()
+            q, k, v = qkv.split([Hq, Hkv, Hkv], 1)
+            cu, pos, slots = pa.pages_extend(table, lens, i32(new), free, count, page, n)
+            q, k = pa.rope(q, k, pos, inv_freq)
+            pa.cache_append_q4(k, v, slots, *cache)
+            if i % 3:
+                got += pa.decode_paged_q4(q, *cache, table, lens, mem, w)[:2]
+            else:
+                got += pa.fwd_packed(q, k, v, mem, w, cu)[:2]
+            if i % 4 == 3:
+                pa.pages_release(table, lens, lens - lens % page, free, count, page)
+        return got + [lens, count, table]
+
+    alone = [chain(s) for s in (1, 2)]
+    torch.cuda.synchronize()
+    together, failed = [None, None], []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(5):
+                    together[i] = chain(i + 1)
+            stream.synchronize()
+        except BaseException as e:  # noqa: BLE001 (shown below)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for a, b in zip(alone, together):
+        assert len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+    assert pa.device_status() == 0
