@@ -29,11 +29,12 @@
 // from the lengths, which every CTA sums itself.
 // 160 threads: warps 0-3 compute, 32 keys of a stage each, with their own running
 // maxima, sums and O, joined in shared memory at a segment's end; warp 4 copies
-// (cp.async.bulk into a ring of stages; a whole page of 32 to 128 rows is one copy,
+// (cp.async.bulk into a ring of stages; a whole page of 16 to 128 rows is one copy,
 // other pieces are a copy of codes and one of scales), ahead of the segments' ends.
 // Measured: 32 sequences of 32768 rows, 16 query on 4 KV heads, d = 128, pages of 64:
 // 120 us, 5.05 TB/s (two copies a page: 125); the same copies without arithmetic 100.
-// d = 64, 8 heads, 16384 rows: 77 us (two copies 84).
+// d = 64, 8 heads, 16384 rows: 77 us (two copies 84).  32 of up to 20000 rows, pages
+// of 16: 53 us (two copies 63).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -66,7 +67,7 @@ constexpr uint32_t kCodeMask = 0x80708070u;
 template <int D>
 struct Q4Smem {
   // a stage's rows of K and V: codes and scales of each page, as in the pages, where
-  // pages of 32 to 128 rows are copied whole; else all codes, then all scales
+  // pages of 16 to 128 rows are copied whole; else all codes, then all scales
   uint8_t k[kStages][kSK * q4_row_bytes(D)], v[kStages][kSK * q4_row_bytes(D)];
   float join[kWarps][8][D];  // the warps' O
   uint32_t valid[kStages];   // a bit for each 8 keys of the stage
@@ -253,12 +254,14 @@ struct Q4State {
 };
 
 // The warp's 32 keys of a stage, their codes at kc and vc and their scales `scales`
-// bytes further, as two products of 16, so that their chains overlap.  kWhole: every key is visible
+// bytes further, as two products of 16 (the second's rows next_codes, next_scales
+// bytes further), so that their chains overlap.  kWhole: every key is visible
 // and on a page of the pool; else bit h of `octets` says so of the page of rows
 // 8 h .., and n keys are visible.
 template <int D, int NT, bool kWhole>
-__device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, int scales, int n,
-                                        uint32_t octets, Q4State<D, NT>& z) {
+__device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, int scales,
+                                        int next_codes, int next_scales, int n, uint32_t octets,
+                                        Q4State<D, NT>& z) {
   constexpr int NG = D / 32, NS = 2;
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   // row r of a product's 16 keys (8 and more: + 8) is the key (r / 2) + 4 (r % 2)
@@ -269,13 +272,13 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
   float x[4 * NS];
 #pragma unroll
   for (int u = 0; u < NS; ++u) {
-    const int base = 16 * u;
+    const uint8_t *codes = kc + u * next_codes, *scale = kc + scales + u * next_scales;
     uint32_t ka[NG], kb[NG];
     float sa[NG], sb[NG], y[4] = {0.f, 0.f, 0.f, 0.f};
-    load_words<D>(kc + (base + rk) * (D / 2) + c * (D / 8), ka);
-    load_words<D>(kc + (base + 8 + rk) * (D / 2) + c * (D / 8), kb);
-    load_scales<D>(kc + scales + (base + rk) * (D / 16), sa);
-    load_scales<D>(kc + scales + (base + 8 + rk) * (D / 16), sb);
+    load_words<D>(codes + rk * (D / 2) + c * (D / 8), ka);
+    load_words<D>(codes + (8 + rk) * (D / 2) + c * (D / 8), kb);
+    load_scales<D>(scale + rk * (D / 16), sa);
+    load_scales<D>(scale + (8 + rk) * (D / 16), sb);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       float acc[4];
@@ -350,10 +353,10 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
   const uint32_t sel_a = (r & 1) ? 0x7632u : 0x5410u, sel_b = (r & 1) ? 0x6723u : 0x4501u;
 #pragma unroll
   for (int u = 0; u < NS; ++u) {
-    const int base = 16 * u;
+    const uint8_t *codes = vc + u * next_codes, *scale = vc + scales + u * next_scales;
     float va[NG], vb[NG];
-    load_scales<D>(vc + scales + (base + rk) * (D / 16), va);
-    load_scales<D>(vc + scales + (base + 8 + rk) * (D / 16), vb);
+    load_scales<D>(scale + rk * (D / 16), va);
+    load_scales<D>(scale + (8 + rk) * (D / 16), vb);
     if constexpr (NT > 1) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) va[g] *= kTwo40, vb[g] *= kTwo40;
@@ -368,7 +371,7 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
     uint32_t y[4][NG];  // keys c, c + 4, c + 8, c + 12
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      load_words<D>(vc + (base + c + 4 * i) * (D / 2) + (r >> 1) * (D / 8), y[i]);
+      load_words<D>(codes + (c + 4 * i) * (D / 2) + (r >> 1) * (D / 8), y[i]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const uint32_t p01 = __byte_perm(y[0][g], y[1][g], sel_a);
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
   volatile int* abort_flag = &sm.abort_flag;
 
   const int page = 1 << p.shift;
-  const bool whole = page >= 32 && page <= kSK;  // pages are copied whole
+  const bool whole = page >= 16 && page <= kSK;  // pages are copied whole
 
   if (warp == kWarps) {
     // ------------------------------------------------------------- copies --
@@ -558,8 +561,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
       const uint32_t octets = (sm.valid[slot] >> (4 * warp)) & 15u;
       const uint8_t *kc = sm.k[slot] + codes_at, *vc = sm.v[slot] + codes_at;
       const int scales = scales_at - codes_at;
-      if (n >= 32 && octets == 15u) q4_keys<D, NT, true>(kc, vc, scales, n, octets, z);
-      else if (n > 0) q4_keys<D, NT, false>(kc, vc, scales, n, octets, z);
+      const int next_codes = page == 16 ? 16 * q4_row_bytes(D) : 16 * (D / 2);
+      const int next_scales = page == 16 ? 16 * q4_row_bytes(D) : 16 * (D / 16);
+      if (n >= 32 && octets == 15u)
+        q4_keys<D, NT, true>(kc, vc, scales, next_codes, next_scales, n, octets, z);
+      else if (n > 0)
+        q4_keys<D, NT, false>(kc, vc, scales, next_codes, next_scales, n, octets, z);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[slot]);
     }
@@ -628,7 +635,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 // One CTA a query head: D threads for the channels, times kParts groups that
 // share the records of its pair.
 template <int D, int kParts, typename T>
-__global__ void __launch_bounds__(D* kParts) polar_decode_q4_combine_kernel(const Q4DecodeParams p) {
+__global__ void __launch_bounds__(D* kParts)
+    polar_decode_q4_combine_kernel(const Q4DecodeParams p) {
   constexpr int R = D + 4;
   const int G = p.Hq / p.Hkv, b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
   const int x = threadIdx.x % D, part = threadIdx.x / D;
@@ -840,7 +848,8 @@ int polar_attn_decode_paged_q4(const void* q, const void* k_pages, const void* v
   const int st = check_device(&sms);
   if (st != POLAR_OK) return st;
   const int runs = num_runs > 0 ? num_runs : auto_runs(B, Hkv, max_seq_len, dtype, sms);
-  if (!workspace || workspace_bytes < scratch_bytes(B, Hq, Hkv, d, runs)) return POLAR_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < scratch_bytes(B, Hq, Hkv, d, runs))
+    return POLAR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return POLAR_ERR_MISALIGNED;
   Q4DecodeParams p{q, mem, w_count, out, n_eff, conf, static_cast<const uint8_t*>(k_pages),
                    static_cast<const uint8_t*>(v_pages), block_table, seq_lens,
