@@ -264,10 +264,12 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
                                         Q4State<D, NT>& z) {
   constexpr int NG = D / 32, NS = 2;
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  // row r of a product's 16 keys (8 and more: + 8) is the key (r / 2) + 4 (r % 2)
-  // of them, so that V's operand, whose columns 2 c and 2 c + 1 are the keys c and
-  // c + 4, reads neighbouring rows
-  const int rk = (r >> 1) + 4 * (r & 1);
+  // row r of a product's 16 keys (8 and more: + 8) is the key r / 2 of them for even
+  // r, 4 + (r / 2 ^ kTurn) for odd: V's operand, whose columns 2 c and 2 c + 1 are
+  // the keys c and 4 + (c ^ kTurn), reads neighbouring rows, and the lanes that read K
+  // together take rows of different banks
+  constexpr int kTurn = D == 128 ? 1 : 2;
+  const int rk = r & 1 ? 4 + ((r >> 1) ^ kTurn) : r >> 1;
   // ---- scores: x[2 h + i] of rows 8 h + r, heads 2 c + i
   float x[4 * NS];
 #pragma unroll
@@ -368,10 +370,11 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
         if (!in[2 * u + 1]) vb[g] = 0.f;
       }
     }
-    uint32_t y[4][NG];  // keys c, c + 4, c + 8, c + 12
+    uint32_t y[4][NG];  // keys c, 4 + (c ^ kTurn), and 8 more
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      load_words<D>(codes + (c + 4 * i) * (D / 2) + (r >> 1) * (D / 8), y[i]);
+      load_words<D>(codes + (4 * i + (i & 1 ? c ^ kTurn : c)) * (D / 2) + (r >> 1) * (D / 8),
+                    y[i]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const uint32_t p01 = __byte_perm(y[0][g], y[1][g], sel_a);
