@@ -274,3 +274,25 @@ def test_very_long_sequence():
     assert (t(got[1][n - m:]).double() / ne - 1).abs().max() <= TOL["f32"]["neff"]
     assert (t(got[2][n - m:]).double() - c).abs().max() <= TOL["f32"]["conf"]
     assert pa.device_status() == 0
+
+
+def test_beside_the_padded_prefill():
+    """Short prompts (two CTAs a SM) and padded batches on two streams at once:
+    both kernels hold tensor memory, and each gives the bits it gives alone."""
+    import long_context_attention_causal_gb300 as pa
+    args = case([(37 * i) % 120 + 1 for i in range(300)], 8, 8, 64, "bf16", 61)
+    g = torch.Generator(device=dev()).manual_seed(62)
+    pad = [torch.randn((2, 8, 700, 64), generator=g, device=dev()).bfloat16() for _ in range(4)]
+    want, wide = run(args), pa.fwd(*pad, args[4])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got, other = [], []
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            got.append(run(args))
+        with torch.cuda.stream(streams[1]):
+            other.append(pa.fwd(*pad, args[4]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for x in got for a, b in zip(x, want))
+    assert all(torch.equal(x[0], wide[0]) and torch.equal(x[1], wide[1]) for x in other)
+    assert pa.device_status() == 0
