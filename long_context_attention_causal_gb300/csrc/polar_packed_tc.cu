@@ -63,9 +63,10 @@ template <int D, int NQ>
 struct Layout {
   static constexpr int kThreads = 128 * (NQ + 1);
   static constexpr uint32_t kTmemCols = 256 * NQ;
-  // Ring depths: 2 K + 2 V stages, 4 + 4 where there is room.  Shared memory allows as
-  // many CTAs a SM as share its 512 TMEM columns.
-  static constexpr int kNSK = D == 64 && NQ == 2 ? 4 : 2;
+  // Ring depths: 2 K + 2 V stages, 4 + 4 where there is room, 1 + 1 where there is
+  // none (two CTAs fill each other's waits).  Shared memory allows as many CTAs a SM
+  // as share its 512 TMEM columns.
+  static constexpr int kNSK = NQ == 2 ? (D == 64 ? 4 : 2) : (D == 64 ? 2 : 1);
   static constexpr int kNSV = kNSK;
   static constexpr int kTileBytes = kBM * D * 2;  // 128 x D bf16
   static constexpr int kHalfBytes = kBM * 128;    // one 64-column swizzle atom
@@ -74,7 +75,8 @@ struct Layout {
   static constexpr int kVOff = kKOff + kNSK * kTileBytes;
   static constexpr int kStageOff = kVOff + kNSV * kTileBytes;  // 32 columns of the output rows
   static constexpr int kBarOff = kStageOff + NQ * kHalfBytes;
-  static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // + align slack
+  static constexpr int kSlack = D == 128 && NQ == 1 ? 0 : 1024;  // to align the base
+  static constexpr int kSmemBytes = kBarOff + 512 + kSlack;
   static constexpr int kCtas = 2 / NQ;  // a SM
   static_assert(kCtas * (kSmemBytes + 1024) <= 233472, "shared memory");
   static_assert((kCtas + 1) * (kSmemBytes + 1024) > 233472, "TMEM columns");
@@ -233,9 +235,13 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, Layout<D, NQ>::kCtas)
   // Measured, rows / pieces: G = 8, 24 prompts up to 2900 tokens, 360 / 320 us; G =
   // 4, 64 up to 500, 90 / 86; G = 1, 200 up to 190, d = 64, 84 / 91.
   constexpr bool kByRow = G <= 2;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+      (reinterpret_cast<uintptr_t>(smem_raw) + (L::kSlack ? 1023 : 0)) & ~uintptr_t(1023));
+  if (L::kSlack == 0 && smem != smem_raw) {  // not so: recorded, as a wait that ran out is
+    if (threadIdx.x == 0) atomicExch(p.status, kStatusWaitTimeout);
+    return;
+  }
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBarOff);
 
   const int warp = threadIdx.x >> 5;
@@ -845,17 +851,23 @@ cudaError_t launch_n(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) 
   return cudaGetLastError();
 }
 
-// Two row tiles a CTA, which share K and V, or one and two CTAs a SM (d = 64), whose
-// chains run side by side: a short prompt leaves the second tile of a pair empty.
-// One where a sequence has at most 192 of a pair's 256 rows on average.  Measured,
-// two / one, us: G = 1, prompts up to 30, 190, 500, 1000 tokens (15 to 500 on average),
-// 179 / 110, 87 / 69, 71 / 67, 68 / 73; G = 2, up to 60, 190, 300, 181 / 118, 106 /
-// 104, 94 / 106; G = 4, up to 30, 60, 120, 96 / 67, 101 / 93, 100 / 111; G = 8, up to
-// 30, 60, 59 / 60, 82 / 100.
+// Two row tiles a CTA, which share K and V, or one and two CTAs a SM, whose chains
+// run side by side: a short prompt leaves the second tile of a pair empty.  One where
+// a sequence has on average at most 192 of a pair's 256 rows, 100 at d = 128, whose
+// two rings have one stage each.  Measured, two / one, us, for prompts of random
+// lengths up to the one given (the mean is half of it):
+//   d = 64, G = 1:   30: 179 / 110, 190: 87 / 69, 500: 71 / 67, 1000: 68 / 73
+//           G = 2:   60: 181 / 118, 190: 106 / 104, 300: 94 / 106
+//           G = 4:   30: 96 / 67, 60: 101 / 93, 120: 100 / 111
+//           G = 8:   30: 59 / 60, 60: 82 / 100
+//   d = 128, G = 1:  30: 213 / 152, 120: 150 / 111, 190: 117 / 103, 300: 94 / 99
+//            G = 2:  60: 221 / 156, 120: 162 / 167
+//            G = 4:  30: 117 / 90, 60: 126 / 120, 120: 127 / 137
+//            G = 8:  30: 75 / 74, 60: 106 / 119
 template <int D, int G>
 cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) {
-  if constexpr (D == 64)
-    if ((long long)a.N * G <= 192LL * a.B) return launch_n<D, G, 1>(a, m, s);
+  const long long few = D == 64 ? 192 : 100;
+  if ((long long)a.N * G <= few * a.B) return launch_n<D, G, 1>(a, m, s);
   return launch_n<D, G, 2>(a, m, s);
 }
 
