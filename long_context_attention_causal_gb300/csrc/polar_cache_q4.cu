@@ -2,8 +2,11 @@
 // pages; layout and rounding: polar_cache_q4.cuh.)
 //
 // The rows are read once and 9 bits are written for each 32 (bf16: 16) of a value,
-// so DRAM is the floor; the append's arithmetic, about a dozen instructions a
-// channel, takes longer.  A scale's maximum is that of the bits of |x|, whose order
+// so DRAM is the floor; the append's arithmetic, 22 instructions a channel with what
+// a row costs, takes longer.  Measured: 32768 tokens of 4 heads, d = 128, bf16 in 29 us
+// (eight channels a thread 37), fp32 out 34 us, 4.5 TB/s (rows in the order of the
+// heads 37; 16 bytes a thread 35 to 39; CTAs that stay, with loads ahead, 35 to 43).
+// A scale's maximum is that of the bits of |x|, whose order
 // as integers is that of the numbers, with infinity and NaN above.
 #include <algorithm>
 #include <climits>
