@@ -551,7 +551,9 @@ int polar_rope(const void* q, const void* k, const int* positions, const double*
  * KV head h / (Hq / Hkv), Hq / Hkv 1, 2, 4 or 8.  Rows before cu_seqlens[0] and
  * from cu_seqlens[B] on are neither read into a result nor written.  A token
  * that holds an infinity or NaN may make other rows of its sequence's 128-token
- * tile non-finite, earlier ones included; other sequences it does not reach.
+ * tile non-finite, earlier ones included; other sequences it does not reach.  A
+ * NaN in a row of v, in one channel too, makes all of out of the rows that see it
+ * NaN, and leaves n_eff and conf.
  * Offsets outside [0, N] are cut; one below the offset before it ends the list
  * (its sequence and those after it are not computed); both record status 3 in
  * polar_attn_device_status.  B up to 2^18.  Memory beyond inputs and outputs:
@@ -602,8 +604,9 @@ int polar_cache_read_q4(const void* k_pages, const void* v_pages, const int* slo
  * num_runs CTAs, 0: as many as run at once).  bf16 q: the weights times V's
  * scales are rounded to bf16, sums are fp32.  fp32 q: q and those weights are
  * taken to 24 bits.  Rows whose scales are in [2^-30, 2^50] and q below 2^60 keep
- * that precision.  A row that holds a NaN makes its own sequence's results of
- * its KV head NaN.  workspace: polar_attn_decode_paged_q4_workspace_bytes(...)
+ * that precision.  A row of K that holds a NaN makes its own sequence's results of
+ * its KV head NaN, a row of V that does, in one group too, all of out (n_eff and
+ * conf follow K alone).  workspace: polar_attn_decode_paged_q4_workspace_bytes(...)
  * bytes, device, 16-byte aligned; two calls that may overlap need one each.
  */
 int polar_attn_decode_paged_q4(const void* q, const void* k_pages, const void* v_pages,

@@ -440,7 +440,9 @@ __device__ __forceinline__ RowResult polar_finish(float m_nat, float l, float q2
   float lse = m_nat + logf(l);
   r.conf = 1.0f / (1.0f + expf(b - lse));
   float a_norm = sqrtf(acc_sq) / l;  // |a|, a = acc / l
-  float den = fmaxf(a_norm, c.eps);
+  // (a norm that is no number stays one: fmaxf would give eps, and the row's other
+  // channels numbers up to 1 / eps too large)
+  float den = a_norm <= c.eps ? c.eps : a_norm;
   r.scale_u = 1.0f / (l * den);
   r.count = r.conf * tanhf(logf(r.n_eff) / c.kappa);
   return r;
