@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
         const int key = i / C, ch = i % C;
         if (j0 + key < keys)
           cp_async16(&sm.k[key][key_piece(key, ch)],
-                     p.k + (first + j0 + key) * (size_t)p.ks + tile.head * D + 4 * ch);
+                     p.k + (first + j0 + key) * (size_t)p.ks + (size_t)tile.head * D + 4 * ch);
       }
       cp_async_commit();
     };
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
         const int key = i / C, ch = i % C;
         if (j0 + key < keys)
           cp_async16(&sm.v[key][4 * ch],
-                     p.v + (first + j0 + key) * (size_t)p.vs + tile.head * D + 4 * ch);
+                     p.v + (first + j0 + key) * (size_t)p.vs + (size_t)tile.head * D + 4 * ch);
         else  // weighted by 0, and so a number
           *reinterpret_cast<float4*>(&sm.v[key][4 * ch]) = make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2) polar_packed_f32_kernel(const Pac
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
       if (row / G < cnt)
         u = __ldg(reinterpret_cast<const float4*>(p.q + (first + tok0 + row / G) * (size_t)p.qs +
-                                                  (tile.head * G + row % G) * D) + ch);
+                                                  ((size_t)tile.head * G + row % G) * D) + ch);
       *reinterpret_cast<float4*>(&sm.q[row][row_piece(row, ch)]) = u;
     }
     load_k(0);

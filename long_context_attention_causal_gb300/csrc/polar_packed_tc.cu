@@ -641,8 +641,8 @@ __global__ void __launch_bounds__(Layout<D, NQ>::kThreads, Layout<D, NQ>::kCtas)
       const size_t tile_at = ((size_t)(cur.start + tk0) * p.Hq + (size_t)cur.head * G) * D;
       const int row0 = (r & 96) + (lane >> 3);
       auto row_at = [&](int i) {  // elements from the tile's first
-        const int row = row0 + 4 * i;
-        return tile_at + (size_t)(((row / G) * p.Hq + row % G) * D);
+        const uint32_t row = (uint32_t)(row0 + 4 * i);  // (128 tokens of all heads pass 2^31)
+        return tile_at + ((size_t)(row / G) * (uint32_t)p.Hq + row % G) * D;
       };
       MemRows<D, kByRow> mem;
 #pragma unroll
