@@ -89,7 +89,7 @@ __device__ __forceinline__ void fill_token(const PagesArgs& a, const int* cu, co
     const int b = find(a.B, t, [&](int x) { return cu[x]; });
     const int2 plan = plans[b];
     if (plan.x >= 0) {
-      pos = plan.x + t - cu[b];
+      pos = plan.x + (t - cu[b]);
       const int page = pos >> a.shift, mask = (1 << a.shift) - 1;
       const int held = (plan.x + mask) >> a.shift;  // pages before this call
       int id;
@@ -119,7 +119,8 @@ __device__ __forceinline__ void fill_freed(const PagesArgs& a, const int2* plans
     flag(a);
     id = -1;
   }
-  if (top + i < a.capacity) a.free_pages[top + i] = id;
+  const long long at = (long long)top + i;  // (both near 2^31 at most)
+  if (at < a.capacity) a.free_pages[at] = id;
 }
 
 // kAlone: the block fills too (its sequences fit kHeld)
