@@ -253,7 +253,7 @@ cudaError_t launch(const PagesArgs& a, long long items, int sms, cudaStream_t s)
   }
   pages_scan_kernel<kExtend, false><<<1, threads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || items == 0) return e;  // (no tokens: nothing to fill)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min((items + kFill - 1) / kFill, 6LL * sms));
   cfg.blockDim = dim3(kFill);

@@ -1,12 +1,32 @@
-"""Pages given back to stacks whose heights pass 2^31 with them."""
+"""Page calls of many sequences without tokens, and of stacks whose heights pass
+2^31 with what is given back."""
 import pytest
 import torch
 
 from gpu_util import dev
 from serving_ref import release_ref
-from test_gpu_pages import pool_state, t32
+from test_gpu_pages import pool_state, run_extend, t32
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B", [1, 2048, 2049, 5000])
+@pytest.mark.parametrize("late", [False, True])
+def test_no_tokens(B, late):
+    """max_tokens 0: the table, lengths and stack stay; `late`: sequences that
+    ask for tokens all the same are past max_tokens, which is recorded."""
+    import long_context_attention_causal_gb300 as pa
+    lens = [(7 * b) % 40 for b in range(B)]
+    table, free, pool = pool_state(B, 6, 8, lens, 9, B)
+    new = [0] * B
+    if late:
+        new[B // 2] = 3
+    want = run_extend(table, lens, new, free, 9, 8, 0, pool)
+    assert want[1] == lens and want[2] == 9 and want[3] == [0] * (B + 1)
+    assert pa.device_status(reset=True) == (3 if late else 0)
+    # and what is asked of the stream afterwards runs as ever
+    run_extend(table, lens, [1] * B, free, 9, 8, B, pool)
+    assert pa.device_status(reset=True) == 0
 
 
 def test_stack_past_2_31():
