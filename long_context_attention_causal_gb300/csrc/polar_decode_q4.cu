@@ -729,7 +729,12 @@ __global__ void __launch_bounds__(D* kParts)
 #pragma unroll
     for (int i = 0; i < N / 32; ++i) L += red[1][i], Q += red[2][i];
   }
-  float acc_sq = a * a, q_sq = qx * qx;
+  // |acc|^2 in units of the power of two below L, which changes no bit (128 channels of
+  // 2^52 overflowed from L = 363 on, and the direction was lost)
+  const float unit =
+      __uint_as_float(0x7F000000u - (__float_as_uint(L) & 0x7F800000u));  // 2^-floor(log2 L)
+  const float au = a * unit;
+  float acc_sq = au * au, q_sq = qx * qx;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
     acc_sq += __shfl_xor_sync(0xffffffffu, acc_sq, o);
@@ -753,7 +758,8 @@ __global__ void __launch_bounds__(D* kParts)
     }
     return;
   }
-  const RowResult res = polar_finish(M, L, Q, acc_sq, q_sq, (float)keys, D, p.c);
+  const RowResult res =
+      polar_finish_norm(M, L, Q, sqrtf(acc_sq) / (L * unit), q_sq, (float)keys, D, p.c);
   out[row] = (T)fmaf(a, res.scale_u, fmaf(res.count, wx, mx));
   if (x == 0) {
     p.n_eff[blockIdx.x] = res.n_eff;

@@ -419,11 +419,11 @@ struct RowResult {
 // Epilogue of one row from its final streaming state.
 //   m_nat : reference logit (natural units of s = tau q.k / sqrt(d))
 //   l, q2 : sum exp(s - m), sum exp(2 (s - m)) over the row's keys
-//   acc_sq: |acc|^2, acc = sum exp(s - m) v
+//   a_norm: |a|, a = acc / l, acc = sum exp(s - m) v
 //   q_sq  : |q|^2;  n: visible keys
-__device__ __forceinline__ RowResult polar_finish(float m_nat, float l, float q2,
-                                                  float acc_sq, float q_sq, float n,
-                                                  int d, const polar_consts_t& c) {
+__device__ __forceinline__ RowResult polar_finish_norm(float m_nat, float l, float q2,
+                                                       float a_norm, float q_sq, float n,
+                                                       int d, const polar_consts_t& c) {
   RowResult r;
   float tau = polar_tau(n, c.log_t0);
   r.n_eff = (l * l) / q2;
@@ -439,13 +439,19 @@ __device__ __forceinline__ RowResult polar_finish(float m_nat, float l, float q2
   }
   float lse = m_nat + logf(l);
   r.conf = 1.0f / (1.0f + expf(b - lse));
-  float a_norm = sqrtf(acc_sq) / l;  // |a|, a = acc / l
   // (a norm that is no number stays one: fmaxf would give eps, and the row's other
   // channels numbers up to 1 / eps too large)
   float den = a_norm <= c.eps ? c.eps : a_norm;
   r.scale_u = 1.0f / (l * den);
   r.count = r.conf * tanhf(logf(r.n_eff) / c.kappa);
   return r;
+}
+
+// The same from acc_sq = |acc|^2.
+__device__ __forceinline__ RowResult polar_finish(float m_nat, float l, float q2,
+                                                  float acc_sq, float q_sq, float n,
+                                                  int d, const polar_consts_t& c) {
+  return polar_finish_norm(m_nat, l, q2, sqrtf(acc_sq) / l, q_sq, n, d, c);
 }
 
 }  // namespace polar
