@@ -68,3 +68,40 @@ def test_scales_of_keys(power, dtype):
     got = pa.decode_paged_q4(q / by, *pages_of(k * by, v, 32), mem, w)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert pa.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weights_keep_fp32(dtype):
+    """n_eff of one key of weight 1 beside 1023 of one weight w = 2^-6 to 2^-8, whose
+    scores are exact: q and k have one channel each, d = 64 and no temperature.
+    With S = 1023 w and R = 1023 w^2, an error e of w moves n_eff by 2 e (S / (1 + S) -
+    R / (1 + R)), below 1.8 e.  e: the exponent, below 8, is rounded to half of
+    2^-21, ln 2 times that (rms 1 / sqrt(3) of it) 1e-7; ex2 2.4e-7; log2(e) in the
+    scale 0.7e-7; a sum of 1023 equal numbers 1.5e-7 rms.  In all below 2^-20 rms (with
+    exponents near 40, half of 2^-18, it is 1.3e-6)."""
+    import long_context_attention_causal_gb300 as pa
+    B, Hq, d, n, page = 64, 8, 64, 1024, 64
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    scale = ((1.0 + torch.arange(B, device=dev()) / 512.0).bfloat16()).float()
+    k = torch.zeros((B, n, 1, d), device=dev())
+    k[:, :, 0, 3] = -7.0 * scale[:, None]
+    k[:, 500, 0, 3] *= -1.0
+    v = torch.ones((B * n, 1, d), device=dev())
+    kp, vp = pa.cache_q4(B * n // page, 1, page, d)
+    slots = torch.arange(B * n, dtype=torch.int32, device=dev())
+    pa.cache_append_q4(k.view(B * n, 1, d), v, slots, kp, vp)
+    back, _ = pa.cache_read_q4(kp, vp, slots, dtype=torch.float32)
+    assert torch.equal(back, k.view(B * n, 1, d))
+    q = torch.zeros((B, Hq, d), device=dev(), dtype=dt)
+    q[..., 3] = (2.4 + 0.05 * torch.arange(Hq, device=dev())).bfloat16().to(dt)
+    table = torch.arange(B * n // page, dtype=torch.int32, device=dev()).view(B, -1)
+    lens = torch.full((B,), n, dtype=torch.int32, device=dev())
+    got = pa.decode_paged_q4(q, kp, vp, table, lens, torch.zeros_like(q),
+                             torch.zeros((Hq, d), device=dev()))
+    x = -14.0 * q[..., 3].double() * scale.double()[:, None] / 8.0
+    weight = torch.exp(x)
+    assert (weight > 2.0 ** -8).all() and (weight < 2.0 ** -5.5).all()
+    want = (1 + (n - 1) * weight) ** 2 / (1 + (n - 1) * weight ** 2)
+    far = (got[1].double() / want - 1).square().mean().sqrt()
+    assert far <= 2.0 ** -20
+    assert pa.device_status() == 0
