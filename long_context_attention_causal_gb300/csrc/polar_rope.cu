@@ -6,10 +6,12 @@
 // with (a, b) = (i, i + r/2) (halves) or (2 i, 2 i + 1) (interleaved); the
 // inverse, whose angle is negative, is the gradient, as s R^T is.
 // A far position's angle in fp32 would be off by tenths of a radian, so the
-// angle is kept in turns, as a 64-bit fraction: f_i / (2 pi) * 2^64 rounded to
-// an integer once a block, times the position, modulo 2^64 (whole turns drop
-// out).  Its upper 32 bits are rounded to fp32 for one sincospi of an argument
-// in [-1, 1].
+// angle is kept in turns, as a 64-bit fraction: f_i / (2 pi) * 2^64 cut to an
+// integer once a block, times the position, modulo 2^64 (whole turns drop out).
+// Its upper 24 bits, h, are an fp32 number exactly, for one sincospi in [-1, 1); the
+// next 16 are an angle e below 2^-21 beside it,
+//   cos(h + e) = cos h - e sin h,   sin(h + e) = sin h + e cos h   (up to e^2 / 2).
+// (Upper bits rounded to fp32 had left up to 2^-26 of a turn.)
 // Bound by DRAM: q and k are read and written once.  A thread owns 16 bytes of
 // the pairs of one token, whose sines it computes once, and walks over heads;
 // with few tokens the heads are spread over threads instead.  Measured: 32768 tokens
@@ -111,10 +113,12 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const unsigned long long t = p * turns[unit * V + i];
-    const float x = (float)(int)(t >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
-    sincospif(x, &sn[i], &cs[i]);
-    cs[i] *= a.scale;
-    sn[i] *= kInverse ? -a.scale : a.scale;
+    const float x = (float)((int)(t >> 32) >> 8) * 1.1920928955078125e-7f;  // 2^-23: half turns
+    const float e = (float)(int)((t >> 24) & 0xFFFFu) * 5.714523747137342e-12f;  // 2 pi 2^-40
+    float s, c;
+    sincospif(x, &s, &c);
+    cs[i] = fmaf(-e, s, c) * a.scale;
+    sn[i] = fmaf(e, c, s) * (kInverse ? -a.scale : a.scale);
   }
   const int off0 = kInterleaved ? 2 * unit * V : unit * V;
   const int off1 = kInterleaved ? off0 + V : off0 + a.rot / 2;
