@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kRowsPerCta * 32)
   const float Tt = tanhf(-logf(Q2) / c.kappa);
   const float count = cf * Tt;
   // direction gradient
-  const bool big = an > c.eps;
+  const bool big = !(an <= c.eps);  // (true of NaN, which stays in the gradient)
   float ug = 0.f;
 #pragma unroll
   for (int x = 0; x < D / 32; ++x) ug = fmaf(a[x] / (big ? an : c.eps), g[x], ug);

@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(128)
     ug = wsum(ug);
     gw = wsum(gw);
     qsq = wsum(qsq);
-    const bool big = st.y > c.eps;
+    const bool big = !(st.y <= c.eps);  // (true of NaN, which stays in the gradient)
     const float den = big ? st.y : c.eps;  // a = den * u
     const float inv = 1.0f / den;
     float dd = 0.f;

@@ -185,7 +185,7 @@ __device__ __forceinline__ void bwd_row_epilogue(const TcParams& p, uint32_t o_t
   const float cf = 1.0f / (1.0f + expf(sig_per_q * qn * f - lse));
   const float tt = tanhf(-logf(q2n) / p.c.kappa);
   const float count = cf * tt;
-  const bool big = an > p.c.eps;
+  const bool big = !(an <= p.c.eps);  // (true of NaN, which stays in the gradient)
   const float inv = 1.0f / (big ? an : p.c.eps);
   const float su = inv / l;  // u = acc * su
   const size_t roff = ((size_t)bh * p.T + (size_t)(valid ? row : 0)) * D;

@@ -79,3 +79,32 @@ def test_padded_prefill_and_decode(dtype, d):
     assert torch.equal(got[0][0], clean[0][0]) and torch.equal(got[0][1, :2], clean[0][1, :2])
     assert torch.equal(got[1], clean[1]) and torch.equal(got[2], clean[2])
     assert pa.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "bf16 statistics"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients(dtype, d):
+    """The rows that see the NaN have no gradient of a direction: every row of
+    the head's dv (all are seen by one of them) and theirs of dq hold NaN alone,
+    not the gradient of a direction of norm eps.  Other heads keep their bits."""
+    import long_context_attention_causal_gb300 as pa
+    dt = DT[dtype.split()[0]]
+    g = torch.Generator(device=dev()).manual_seed(9)
+    q, k, v, mem, dout = (torch.randn((2, 2, 300, d), generator=g, device=dev()).to(dt)
+                          for _ in range(5))
+    w = torch.randn((2, d), generator=g, device=dev()) * 0.02
+    bad = v.clone()
+    bad[1, 0, 201, 7] = math.nan
+
+    def grads(v):
+        if dtype == dtype.split()[0]:
+            return pa.bwd(q, k, v, w, dout)
+        return pa.bwd_stats(q, k, v, mem, w, *pa.fwd_stats(q, k, v, mem, w), dout)
+
+    clean, got = grads(v), grads(bad)
+    assert got[2][1, 0].isnan().all() and got[0][1, 0, 201:].isnan().all()
+    assert got[1][1, 0, :202].isnan().all()
+    for a, b in zip(got[:3], clean[:3]):
+        assert torch.isfinite(b).all()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1, 1], b[1, 1])
+    assert pa.device_status() == 0
