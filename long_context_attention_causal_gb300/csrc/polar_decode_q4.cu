@@ -20,6 +20,9 @@
 //   O^T (16 channels x 8 heads) += V codes^T (A, 16 channels x 16 keys) . P'^T (B)
 // P' comes from S's registers by movmatrix.  fp32 queries are split into three
 // bf16 terms, whose sum is q, and so are the weights: three products each.
+// The eight columns are the query heads of a KV head; with four of them half of the
+// maxima, exponentials, sums and weights, with one seven eighths, are of zero rows,
+// and cost what others do.
 //
 // Work: the stages (128 keys) of all (sequence, KV head) pairs in one row are
 // cut into equal runs, a run a CTA, all resident at once: sequences of different
@@ -32,9 +35,9 @@
 // (cp.async.bulk into a ring of stages; a whole page of 16 to 128 rows is one copy,
 // other pieces are a copy of codes and one of scales), ahead of the segments' ends.
 // Measured: 32 sequences of 32768 rows, 16 query on 4 KV heads, d = 128, pages of 64:
-// 119 us, 5.1 TB/s (two copies a page: 124); the same copies without arithmetic 100.
-// d = 64, 8 heads, 16384 rows: 77 us (two copies 84).  32 of up to 20000 rows, pages
-// of 16: 51 us (two copies 61).  Records are joined eight at a time, heads and sums
+// 118 us, 5.1 TB/s (two copies a page: 5 more); the same copies without arithmetic 100.
+// d = 64, 8 heads, 16384 rows: 76 us (two copies 7 more).  32 of up to 20000 rows, pages
+// of 16: 50 us (two copies 10 more).  Records are joined eight at a time, heads and sums
 // loaded together (maxima first, then the sums: 1.2 to 2 us more).
 #include <algorithm>
 #include <climits>
@@ -396,6 +399,8 @@ __device__ __forceinline__ void q4_keys(const uint8_t* kc, const uint8_t* vc, in
           for (int i = 0; i < 4; ++i) e[i] -= bf16_round(e[i]);
       }
       if constexpr (NT == 1) {
+        // (the tensor cores' own fp32 sums: cut to about 1e-6 over 81355 keys, far below
+        // the weights' 2^-9)
         mma16816(z.o[2 * g], f0, bl[0], bh[0]);
         mma16816(z.o[2 * g + 1], f1, bl[0], bh[0]);
       } else {

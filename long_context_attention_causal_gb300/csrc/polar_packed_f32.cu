@@ -2,17 +2,19 @@
 // FP32 pipes, and the entry point of both types.
 //
 // "ATMA", §2.1 and §2.2 (online participation ratio, squared correction
-// factors); tiles as in polar_packed.cuh.  fp32 inputs rule out the bf16 tensor
-// cores, so the two products run as register-tiled matrix products: a CTA of
-// 256 threads owns 64 rows (64 / G tokens of a group's G heads) and walks over
+// factors); tiles as in polar_packed.cuh.  One bf16 term of an fp32 input is not
+// enough for the tensor cores (three of each are, as in the decode over the 4-bit
+// cache, at six products for one; not built here): the two products run as
+// register-tiled matrix products: a CTA of 256 threads owns 64 rows (64 / G tokens of a group's G heads) and walks over
 // keys 64 at a time.  Thread (y, x) of a 16 x 16 grid scores rows 4 y .. 4 y + 3
 // against keys x, x + 16, x + 32, x + 48 (64 products for 8 reads of 16 bytes),
 // the 16 threads of a row share its maximum and sums by shuffles, P goes
 // through shared memory, and the thread adds the tile's values to 4 rows x D / 16
 // channels.  K of the next tile is copied (cp.async) while P V runs, V while the
-// next scores do.  Bound by the FP32 pipes: 4 prompts of up to 1500 tokens, 8 query on
-// 2 KV heads, d = 128, 290 us (29 TFLOP/s; with single instead of packed
-// multiply-adds 327).
+// next scores do.  Bound by a tile's chain, its four block barriers with two CTAs a
+// SM, not by a pipe: FMA 34 % (packed), LSU 28 %, 1.9 instructions a clock.  4
+// prompts of up to 1500 tokens, 8 query on 2 KV heads, d = 128, 287 us (29 TFLOP/s;
+// with single instead of packed multiply-adds 327).
 #include <algorithm>
 #include <climits>
 #include <cmath>

@@ -38,8 +38,8 @@
 //
 // Bound by the chain of a step (scores, softmax, products), 1.4 to 1.54 us for two
 // tiles, and by a pair's first and last steps where prompts are short.  Measured:
-// two prompts of 16384 tokens, 16 query on 4 KV heads, d = 128, 1405-1490 us
-// (1476-1565 TFLOP/s); 24 prompts of 1 to 2900 tokens, 16 on 2 heads, 305-320 us;
+// two prompts of 16384 tokens, 16 query on 4 KV heads, d = 128, 1400-1510 us
+// (1456-1570 TFLOP/s); 24 prompts of 1 to 2900 tokens, 16 on 2 heads, 305-330 us;
 // 200 of 1 to 190, 8 heads, d = 64, 69 us.
 #include <algorithm>
 
@@ -864,6 +864,14 @@ cudaError_t launch_n(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) 
 //            G = 2:  60: 221 / 156, 120: 162 / 167
 //            G = 4:  30: 117 / 90, 60: 126 / 120, 120: 127 / 137
 //            G = 8:  30: 75 / 74, 60: 106 / 119
+// The lengths are on the device, so the rule knows their mean alone, with empty
+// sequences and rows outside of them counted: a long prompt among many short ones may
+// get the width that is slower for it.  Two / one, 8 heads unless said:
+//   16384 tokens and 500 up to 30:    d = 64: 567 / 574,   d = 128: 634 / 723
+//   8192 and 300 up to 60:            d = 64: 193 / 196,   d = 128: 273 / 294
+//   two of 4000 and 200 up to 60:     d = 64: 116 / 108,   d = 128: 149 / 168
+//   4000, 500 up to 60, 300 empty, 16 on 4 heads:  147 / 171,      179 / 213
+// (all of them one tile by the rule)
 template <int D, int G>
 cudaError_t launch_g(const PackedArgs& a, const CUtensorMap* m, cudaStream_t s) {
   const long long few = D == 64 ? 192 : 100;
